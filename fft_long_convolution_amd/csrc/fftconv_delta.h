@@ -1,0 +1,98 @@
+// Internal declarations of the token-mixer operators that stand next to the
+// long convolution: norms of queries and keys with the position rotation
+// (fftconv_qknorm.hip) and the gated delta rule (fftconv_delta.hip,
+// fftconv_delta_bwd.hip).  Host checks and the C ABI: fftconv_delta_host.cpp.
+// Not part of the public ABI.
+#pragma once
+
+#include "fftconv_internal.h"
+
+namespace fftconv {
+
+// ------------------------------------------------------------- q/k norms
+
+struct QkNormParams {
+    long long tokens;         // B * T
+    long long T;
+    int Hq, Hk, D, R;         // R: rotated elements of a head
+    int interleaved;
+    int parts;                // threads groups a token's heads are dealt to
+    float c, eps;             // r = rsqrt(c sum x^2 + eps)
+    long long P;              // rows of the tables
+    long long qs[3], ks[3];   // element strides (batch, token, head) of q, k
+    const void* q;
+    const void* k;
+    const float* wq;          // [D] or null
+    const float* wk;
+    const float* cs;          // [P][R/2]
+    const float* sn;
+    const long long* pos;     // [B][T]
+    void* qo;                 // forward: outputs, [B][T][H][D]
+    void* ko;
+    const void* dqo;          // backward: gradients of the outputs
+    const void* dko;
+    void* dq;
+    void* dk;
+    float* part;              // backward: [blocks][2][D] weight-gradient sums
+    float* dwq;
+    float* dwk;
+    int blocks;
+};
+hipError_t launch_qknorm_fwd(int io, const QkNormParams& p, hipStream_t s);
+hipError_t launch_qknorm_bwd(int io, const QkNormParams& p, hipStream_t s);
+int qknorm_bwd_blocks(long long tokens);
+
+// ------------------------------------------------------- gated delta rule
+
+struct DeltaStepParams {
+    int N, Hk, Hv, Dk, Dv;
+    float scale;
+    long long pool;
+    long long qs[2], ks[2], vs[2];   // element strides (request, head)
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;                  // [N][Hv]
+    const float* beta;
+    float* state;                    // [pool][Hv][Dk][Dv]
+    const long long* slots;          // [N] or null
+    void* o;                         // [N][Hv][Dv]
+};
+hipError_t launch_delta_step(int io, const DeltaStepParams& p, hipStream_t s);
+
+// Sequences in chunks of kChunk tokens.  Equal lengths: sequence i is batch
+// row i, its chunks are slots i * nch ...  Packed: sequence i is the tokens
+// cu[i] .. cu[i+1] of the one batch row, its chunks are slots
+// cu[i] / kChunk + i ..., which never reach those of sequence i + 1.
+constexpr int kChunk = 64;
+constexpr int kTriTiles = 6;               // 16 x 32 tiles of a 64 x 64 triangle
+constexpr int kTriFloats = kTriTiles * 512;
+// decays of a chunk: e^G [64], e^(Gc-G) [64], beta [64], e^Gc
+constexpr int kDecFloats = 196;
+
+struct DeltaParams {
+    int Hk, Hv, group, Dk, Dv;
+    float scale;
+    long long T;
+    long long qs[3], ks[3], vs[3];   // element strides (batch, token, head)
+    const long long* cu;             // [nseq + 1] or null
+    long long nseq, nch, slots;
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;                  // [B][T][Hv]
+    const float* beta;
+    const float* init;               // [nseq][Hv][Dk][Dv] or null
+    void* o;                         // [B][T][Hv][Dv]
+    float* fin;                      // [nseq][Hv][Dk][Dv] or null
+    float* tri;                      // [slots][Hv] (I + A)^-1, operand order
+    float* pm;                       // [slots][Hv] decayed scores, operand order
+    float* dec;                      // [slots][Hv][kDecFloats]
+    float* states;                   // [slots][Hv][Dk][Dv] or null: each
+                                     // chunk's first state, for the backward
+    float* us;                       // [slots][Hv][kChunk][Dv] or null: U
+};
+hipError_t launch_delta_prep(int io, const DeltaParams& p, hipStream_t s);
+hipError_t launch_delta_scan(int io, const DeltaParams& p, hipStream_t s);
+
+}  // namespace fftconv

@@ -1,0 +1,434 @@
+// Host side of the token-mixer operators: argument checks, buffer layouts and
+// the C ABI declared in include/fftconv.h.
+#include <stdint.h>
+
+#include "../../include/fftconv.h"
+#include "fftconv_delta.h"
+
+using namespace fftconv;
+
+namespace {
+
+constexpr size_t kMaxCount = 0x7fffffff;      // of any one dimension
+constexpr size_t kMaxElems = (size_t)1 << 46; // of any one tensor
+constexpr size_t kMaxGrid = 0xfffff0;         // workgroups of 256 threads of a launch
+
+// a byte range of the caller's memory
+struct Range {
+    const void* p;
+    size_t n;
+};
+
+bool meet(const Range& a, const Range& b) {
+    if (!a.p || !b.p || !a.n || !b.n) return false;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x < y + b.n && y < x + a.n;
+}
+// no output may meet an input or another output
+template <size_t NO, size_t NI>
+bool outputs_clear(const Range (&out)[NO], const Range (&in)[NI]) {
+    for (size_t i = 0; i < NO; ++i) {
+        for (size_t j = 0; j < NI; ++j)
+            if (meet(out[i], in[j])) return false;
+        for (size_t j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return false;
+    }
+    return true;
+}
+// a missing pointer or one that is not 16-byte aligned
+fftconv_status check_ptr(const void* p, size_t bytes, bool needed = true) {
+    if (!p) return needed && bytes ? FFTCONV_ERR_INVALID_ARG : FFTCONV_OK;
+    return ((uintptr_t)p & 15) ? FFTCONV_ERR_ALIGNMENT : FFTCONV_OK;
+}
+
+bool dtype_ok(fftconv_dtype t) {
+    return t == FFTCONV_F32 || t == FFTCONV_F16 || t == FFTCONV_BF16;
+}
+size_t elem(fftconv_dtype t) { return t == FFTCONV_F32 ? 4 : 2; }
+
+// a * b * c * d, false beyond kMaxElems
+bool product(size_t a, size_t b, size_t c, size_t d, size_t* out) {
+    size_t r = 1;
+    const size_t f[4] = {a, b, c, d};
+    for (size_t x : f)
+        if (x == 0) { *out = 0; return true; }
+    for (size_t x : f) {
+        if (x > kMaxElems / r) return false;
+        r *= x;
+    }
+    *out = r;
+    return true;
+}
+
+// Bytes a strided [B][T][H][D] tensor spans, or an error.
+fftconv_status span_bytes(size_t B, size_t T, size_t H, size_t D, const long long st[3],
+                          fftconv_dtype t, size_t* bytes) {
+    *bytes = 0;
+    const long long step = (long long)(16 / elem(t));
+    const size_t n[3] = {B, T, H};
+    size_t last = 0;
+    if (!B || !T || !H || !D) return FFTCONV_OK;
+    for (int i = 0; i < 3; ++i) {
+        if (st[i] < 0 || (size_t)st[i] > kMaxElems) return FFTCONV_ERR_INVALID_ARG;
+        if (n[i] > 1 && st[i] % step) return FFTCONV_ERR_ALIGNMENT;
+        if (n[i] > 1 && (size_t)st[i] > kMaxElems / (n[i] - 1)) return FFTCONV_ERR_INVALID_ARG;
+        last += (n[i] - 1) * (size_t)st[i];
+    }
+    if (last > kMaxElems) return FFTCONV_ERR_INVALID_ARG;
+    *bytes = (last + D) * elem(t);
+    return FFTCONV_OK;
+}
+
+#define CHECK(expr)                                      \
+    do {                                                 \
+        const fftconv_status status_ = (expr);           \
+        if (status_ != FFTCONV_OK) return status_;       \
+    } while (0)
+
+fftconv_status launched(hipError_t e) { return e == hipSuccess ? FFTCONV_OK : FFTCONV_ERR_HIP; }
+
+// ------------------------------------------------------------- q/k norms
+
+fftconv_status qknorm_sizes(const fftconv_qknorm_desc* d) {
+    if (!d) return FFTCONV_ERR_INVALID_ARG;
+    if (!dtype_ok(d->dtype)) return FFTCONV_ERR_UNSUPPORTED;
+    if (d->norm != FFTCONV_NORM_RMS && d->norm != FFTCONV_NORM_L2) return FFTCONV_ERR_INVALID_ARG;
+    if (!(d->eps >= 0.f)) return FFTCONV_ERR_INVALID_ARG;
+    if (d->D == 0 || d->D % 8 || d->D > 256) return FFTCONV_ERR_UNSUPPORTED;
+    if (d->rotary_dim > d->D) return FFTCONV_ERR_INVALID_ARG;
+    if (d->rotary_dim % (d->interleaved ? 8 : 16)) return FFTCONV_ERR_UNSUPPORTED;
+    if (d->B > kMaxCount || d->T > kMaxCount || d->Hq > 65536 || d->Hk > 65536)
+        return FFTCONV_ERR_UNSUPPORTED;
+    size_t n;
+    if (!product(d->B, d->T, d->Hq + d->Hk, d->D, &n)) return FFTCONV_ERR_UNSUPPORTED;
+    if (d->table_rows > kMaxCount) return FFTCONV_ERR_UNSUPPORTED;
+    return FFTCONV_OK;
+}
+
+struct QkNormArgs {
+    const void *q, *k;
+    const float *wq, *wk, *cos, *sin;
+    const long long* pos;
+};
+
+// Checks what both directions read and fills the kernels' parameters.
+fftconv_status qknorm_inputs(const fftconv_qknorm_desc* d, const QkNormArgs& a, QkNormParams& p,
+                             Range (&in)[7]) {
+    CHECK(qknorm_sizes(d));
+    size_t qb, kb;
+    CHECK(span_bytes(d->B, d->T, d->Hq, d->D, d->q_stride, d->dtype, &qb));
+    CHECK(span_bytes(d->B, d->T, d->Hk, d->D, d->k_stride, d->dtype, &kb));
+    const size_t tokens = d->B * d->T, work = tokens * (d->Hq + d->Hk);
+    const size_t table = work && d->rotary_dim ? d->table_rows * (d->rotary_dim / 2) * 4 : 0;
+    const size_t posb = work && d->rotary_dim ? tokens * 8 : 0;
+    CHECK(check_ptr(a.q, qb));
+    CHECK(check_ptr(a.k, kb));
+    CHECK(check_ptr(a.wq, 0, false));
+    CHECK(check_ptr(a.wk, 0, false));
+    if (posb && (!a.cos || !a.sin || !a.pos) && d->table_rows) return FFTCONV_ERR_INVALID_ARG;
+    if (posb && !a.pos) return FFTCONV_ERR_INVALID_ARG;
+    CHECK(check_ptr(a.cos, table));
+    CHECK(check_ptr(a.sin, table));
+    if ((uintptr_t)a.pos & 7) return FFTCONV_ERR_ALIGNMENT;
+    in[0] = {a.q, qb};
+    in[1] = {a.k, kb};
+    in[2] = {a.wq, d->D * 4};
+    in[3] = {a.wk, d->D * 4};
+    in[4] = {a.cos, table};
+    in[5] = {a.sin, table};
+    in[6] = {a.pos, posb};
+    p = QkNormParams();
+    p.tokens = (long long)tokens;
+    p.T = (long long)d->T;
+    p.Hq = (int)d->Hq;
+    p.Hk = (int)d->Hk;
+    p.D = (int)d->D;
+    p.R = (int)d->rotary_dim;
+    p.interleaved = d->interleaved != 0;
+    p.c = d->norm == FFTCONV_NORM_RMS ? 1.f / (float)d->D : 1.f;
+    p.eps = d->eps;
+    p.P = (long long)d->table_rows;
+    for (int i = 0; i < 3; ++i) {
+        p.qs[i] = d->q_stride[i];
+        p.ks[i] = d->k_stride[i];
+    }
+    p.q = a.q;
+    p.k = a.k;
+    p.wq = a.wq;
+    p.wk = a.wk;
+    p.cs = a.cos;
+    p.sn = a.sin;
+    p.pos = a.pos;
+    // Heads of a token are dealt to several groups of lanes while there are
+    // too few tokens to fill the card (some 16 groups for each SIMD).
+    const size_t H = d->Hq + d->Hk, want = 16384;
+    size_t parts = tokens ? (want + tokens - 1) / tokens : 1;
+    if (parts > H) parts = H;
+    p.parts = (int)(parts ? parts : 1);
+    if (tokens * (size_t)p.parts / 8 > kMaxGrid) return FFTCONV_ERR_UNSUPPORTED;
+    return FFTCONV_OK;
+}
+
+// ------------------------------------------------------- gated delta rule
+
+fftconv_status delta_sizes(const fftconv_delta_desc* d) {
+    if (!d) return FFTCONV_ERR_INVALID_ARG;
+    if (!dtype_ok(d->dtype)) return FFTCONV_ERR_UNSUPPORTED;
+    if (!d->Dk || d->Dk % 8 || d->Dk > 128 || !d->Dv || d->Dv % 8 || d->Dv > 1024)
+        return FFTCONV_ERR_UNSUPPORTED;
+    if (!d->Hk || d->Hv % d->Hk || !d->Hv) return FFTCONV_ERR_INVALID_ARG;
+    if (d->Hv > 65536 || d->B > kMaxCount || d->T > kMaxCount - 64 || d->sequences > kMaxCount)
+        return FFTCONV_ERR_UNSUPPORTED;
+    if (d->sequences && d->B != 1) return FFTCONV_ERR_INVALID_ARG;
+    size_t n;
+    if (!product(d->B, d->T, d->Hv, d->Dv, &n) || !product(d->B, d->T, d->Hk, d->Dk, &n))
+        return FFTCONV_ERR_UNSUPPORTED;
+    const size_t rows = d->sequences ? d->sequences : d->B;
+    if (!product(rows, d->Hv, d->Dk, d->Dv, &n)) return FFTCONV_ERR_UNSUPPORTED;
+    return FFTCONV_OK;
+}
+
+size_t delta_slots(const fftconv_delta_desc* d) {
+    const size_t per = (d->T + kChunk - 1) / kChunk;
+    return d->sequences ? per + d->sequences : d->B * per;
+}
+
+// Where the buffers of a call stand in a block of memory, in floats.
+struct DeltaLayout {
+    size_t tri, pm, dec, states, us, all;
+};
+bool delta_layout(const fftconv_delta_desc* d, bool saved, DeltaLayout* l) {
+    size_t n, x, y;
+    if (!product(delta_slots(d), d->Hv, 1, 1, &n) || n > kMaxGrid) return false;
+    if (!product(n, d->Dk, d->Dv, 1, &x) || !product(n, kChunk, d->Dv, 1, &y)) return false;
+    l->tri = 0;
+    l->pm = n * kTriFloats;
+    l->dec = l->pm + n * kTriFloats;
+    l->states = l->dec + n * kDecFloats;
+    l->us = l->states + (saved ? x : 0);
+    l->all = l->us + (saved ? y : 0);
+    return true;
+}
+
+struct DeltaArgs {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const long long* cu;
+    const float* init;
+};
+
+// Checks what both directions read and fills the kernels' parameters.
+fftconv_status delta_inputs(const fftconv_delta_desc* d, const DeltaArgs& a, DeltaParams& p,
+                            Range (&in)[7]) {
+    CHECK(delta_sizes(d));
+    size_t qb, kb, vb;
+    CHECK(span_bytes(d->B, d->T, d->Hk, d->Dk, d->q_stride, d->dtype, &qb));
+    CHECK(span_bytes(d->B, d->T, d->Hk, d->Dk, d->k_stride, d->dtype, &kb));
+    CHECK(span_bytes(d->B, d->T, d->Hv, d->Dv, d->v_stride, d->dtype, &vb));
+    const size_t gates = d->B * d->T * d->Hv * 4;
+    const size_t rows = d->sequences ? d->sequences : d->B;
+    const size_t state = rows * d->Hv * d->Dk * d->Dv * 4;
+    CHECK(check_ptr(a.q, qb));
+    CHECK(check_ptr(a.k, kb));
+    CHECK(check_ptr(a.v, vb));
+    CHECK(check_ptr(a.g, gates));
+    CHECK(check_ptr(a.beta, gates));
+    CHECK(check_ptr(a.init, state, false));
+    if (d->sequences ? !a.cu : a.cu != nullptr) return FFTCONV_ERR_INVALID_ARG;
+    if ((uintptr_t)a.cu & 7) return FFTCONV_ERR_ALIGNMENT;
+    in[0] = {a.q, qb};
+    in[1] = {a.k, kb};
+    in[2] = {a.v, vb};
+    in[3] = {a.g, gates};
+    in[4] = {a.beta, gates};
+    in[5] = {a.init, state};
+    in[6] = {a.cu, a.cu ? (d->sequences + 1) * 8 : 0};
+    p = DeltaParams();
+    p.Hk = (int)d->Hk;
+    p.Hv = (int)d->Hv;
+    p.group = (int)(d->Hv / d->Hk);
+    p.Dk = (int)d->Dk;
+    p.Dv = (int)d->Dv;
+    p.scale = d->scale;
+    p.T = (long long)d->T;
+    for (int i = 0; i < 3; ++i) {
+        p.qs[i] = d->q_stride[i];
+        p.ks[i] = d->k_stride[i];
+        p.vs[i] = d->v_stride[i];
+    }
+    p.cu = a.cu;
+    p.nseq = (long long)rows;
+    p.nch = (long long)((d->T + kChunk - 1) / kChunk);
+    p.slots = (long long)delta_slots(d);
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.g = a.g;
+    p.beta = a.beta;
+    p.init = a.init;
+    if (rows * d->Hv * ((d->Dv + 15) / 16) > kMaxGrid) return FFTCONV_ERR_UNSUPPORTED;
+    return FFTCONV_OK;
+}
+
+void delta_place(const DeltaLayout& l, void* block, bool saved, DeltaParams& p) {
+    float* f = (float*)block;
+    p.tri = f + l.tri;
+    p.pm = f + l.pm;
+    p.dec = f + l.dec;
+    p.states = saved ? f + l.states : nullptr;
+    p.us = saved ? f + l.us : nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+fftconv_status fftconv_qknorm_forward(const fftconv_qknorm_desc* d, const void* q, const void* k,
+                                      const float* q_weight, const float* k_weight,
+                                      const float* cos, const float* sin,
+                                      const long long* positions, void* q_out, void* k_out,
+                                      void* stream) {
+    QkNormParams p;
+    Range in[7];
+    CHECK(qknorm_inputs(d, {q, k, q_weight, k_weight, cos, sin, positions}, p, in));
+    const size_t qn = d->B * d->T * d->Hq * d->D * elem(d->dtype);
+    const size_t kn = d->B * d->T * d->Hk * d->D * elem(d->dtype);
+    CHECK(check_ptr(q_out, qn));
+    CHECK(check_ptr(k_out, kn));
+    const Range out[] = {{q_out, qn}, {k_out, kn}};
+    if (!outputs_clear(out, in)) return FFTCONV_ERR_INVALID_ARG;
+    if (!(qn + kn)) return FFTCONV_OK;
+    p.qo = q_out;
+    p.ko = k_out;
+    return launched(launch_qknorm_fwd(d->dtype, p, (hipStream_t)stream));
+}
+
+size_t fftconv_qknorm_workspace_bytes(const fftconv_qknorm_desc* d) {
+    if (qknorm_sizes(d) != FFTCONV_OK) return 0;
+    return (size_t)qknorm_bwd_blocks((long long)(d->B * d->T)) * 2 * d->D * 4;
+}
+
+fftconv_status fftconv_qknorm_backward(const fftconv_qknorm_desc* d, const void* q, const void* k,
+                                       const float* q_weight, const float* k_weight,
+                                       const float* cos, const float* sin,
+                                       const long long* positions, const void* dq_out,
+                                       const void* dk_out, void* dq, void* dk, float* dq_weight,
+                                       float* dk_weight, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+    QkNormParams p;
+    Range in[7];
+    CHECK(qknorm_inputs(d, {q, k, q_weight, k_weight, cos, sin, positions}, p, in));
+    const size_t qn = d->B * d->T * d->Hq * d->D * elem(d->dtype);
+    const size_t kn = d->B * d->T * d->Hk * d->D * elem(d->dtype);
+    CHECK(check_ptr(dq_out, qn));
+    CHECK(check_ptr(dk_out, kn));
+    CHECK(check_ptr(dq, qn));
+    CHECK(check_ptr(dk, kn));
+    CHECK(check_ptr(dq_weight, 0, false));
+    CHECK(check_ptr(dk_weight, 0, false));
+    const size_t need = dq_weight || dk_weight ? fftconv_qknorm_workspace_bytes(d) : 0;
+    if (need) {
+        if (!workspace || workspace_bytes < need) return FFTCONV_ERR_WORKSPACE;
+        if ((uintptr_t)workspace & 15) return FFTCONV_ERR_ALIGNMENT;
+    }
+    const Range more[] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6], {dq_out, qn},
+                          {dk_out, kn}};
+    const Range out[] = {{dq, qn}, {dk, kn}, {dq_weight, d->D * 4}, {dk_weight, d->D * 4},
+                         {workspace, need}};
+    if (!outputs_clear(out, more)) return FFTCONV_ERR_INVALID_ARG;
+    if (!(qn + kn) && !need) return FFTCONV_OK;
+    p.dqo = dq_out;
+    p.dko = dk_out;
+    p.dq = dq;
+    p.dk = dk;
+    p.part = need ? (float*)workspace : nullptr;
+    p.dwq = dq_weight;
+    p.dwk = dk_weight;
+    p.blocks = qknorm_bwd_blocks(p.tokens);
+    return launched(launch_qknorm_bwd(d->dtype, p, (hipStream_t)stream));
+}
+
+size_t fftconv_delta_workspace_bytes(const fftconv_delta_desc* d) {
+    DeltaLayout l;
+    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, false, &l)) return 0;
+    return l.all * 4;
+}
+
+size_t fftconv_delta_saved_bytes(const fftconv_delta_desc* d) {
+    DeltaLayout l;
+    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, true, &l)) return 0;
+    return l.all * 4;
+}
+
+fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q, const void* k,
+                                     const void* v, const float* g, const float* beta,
+                                     const long long* cu_seqlens, const float* initial_state,
+                                     void* o, float* final_state, void* saved, size_t saved_bytes,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+    DeltaParams p;
+    Range in[7];
+    CHECK(delta_inputs(d, {q, k, v, g, beta, cu_seqlens, initial_state}, p, in));
+    DeltaLayout l;
+    if (!delta_layout(d, saved != nullptr, &l)) return FFTCONV_ERR_UNSUPPORTED;
+    const size_t on = d->B * d->T * d->Hv * d->Dv * elem(d->dtype);
+    const size_t state = (size_t)p.nseq * d->Hv * d->Dk * d->Dv * 4;
+    CHECK(check_ptr(o, on));
+    CHECK(check_ptr(final_state, state, false));
+    void* block = saved ? saved : workspace;
+    if (l.all * 4 && (!block || (saved ? saved_bytes : workspace_bytes) < l.all * 4))
+        return FFTCONV_ERR_WORKSPACE;
+    if ((uintptr_t)block & 15) return FFTCONV_ERR_ALIGNMENT;
+    const Range out[] = {{o, on}, {final_state, state}, {block, l.all * 4}};
+    if (!outputs_clear(out, in)) return FFTCONV_ERR_INVALID_ARG;
+    if (!p.nseq) return FFTCONV_OK;
+    p.o = o;
+    p.fin = final_state;
+    delta_place(l, block, saved != nullptr, p);
+    hipStream_t s = (hipStream_t)stream;
+    if (d->B * d->T) CHECK(launched(launch_delta_prep(d->dtype, p, s)));
+    return launched(launch_delta_scan(d->dtype, p, s));
+}
+
+fftconv_status fftconv_delta_step(const fftconv_delta_desc* d, const void* q, const void* k,
+                                  const void* v, const float* g, const float* beta, float* state,
+                                  size_t pool, const long long* slots, void* o, void* stream) {
+    DeltaParams c;
+    Range in[7];
+    if (d && (d->T != 1 || d->sequences)) return FFTCONV_ERR_INVALID_ARG;
+    CHECK(delta_inputs(d, {q, k, v, g, beta, nullptr, nullptr}, c, in));
+    size_t n;
+    if (pool > kMaxCount || !product(pool, d->Hv, d->Dk, d->Dv, &n))
+        return FFTCONV_ERR_UNSUPPORTED;
+    const size_t on = d->B * d->Hv * d->Dv * elem(d->dtype);
+    if (!d->B) return FFTCONV_OK;
+    CHECK(check_ptr(state, n * 4));
+    CHECK(check_ptr(o, on));
+    if ((uintptr_t)slots & 7) return FFTCONV_ERR_ALIGNMENT;
+    if (!slots && pool < d->B) return FFTCONV_ERR_INVALID_ARG;
+    in[6] = {slots, slots ? d->B * 8 : 0};
+    const Range out[] = {{o, on}, {state, n * 4}};
+    if (!outputs_clear(out, in)) return FFTCONV_ERR_INVALID_ARG;
+    if (d->B * d->Hv * ((d->Dv + 31) / 32) > kMaxGrid) return FFTCONV_ERR_UNSUPPORTED;
+    DeltaStepParams p = DeltaStepParams();
+    p.N = (int)d->B;
+    p.Hk = c.Hk;
+    p.Hv = c.Hv;
+    p.Dk = c.Dk;
+    p.Dv = c.Dv;
+    p.scale = c.scale;
+    p.pool = (long long)pool;
+    p.qs[0] = c.qs[0]; p.qs[1] = c.qs[2];
+    p.ks[0] = c.ks[0]; p.ks[1] = c.ks[2];
+    p.vs[0] = c.vs[0]; p.vs[1] = c.vs[2];
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.g = g;
+    p.beta = beta;
+    p.state = state;
+    p.slots = slots;
+    p.o = o;
+    return launched(launch_delta_step(d->dtype, p, (hipStream_t)stream));
+}
+
+}  // extern "C"

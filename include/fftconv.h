@@ -400,6 +400,138 @@ fftconv_status fftconv_backward(fftconv_plan_t plan, const void *u,
                                 void *workspace, size_t workspace_bytes,
                                 void *stream);
 
+/* ------------------------------------------------------------------------
+ * Token mixers beside the long convolution.  Hybrid models put layers of the
+ * gated delta rule (a linear recurrence over a matrix-valued state for each
+ * head) next to long-convolution layers; the calls below are that rule over
+ * whole sequences and for single tokens, and the norms and position rotation
+ * of its queries and keys.  They need no plan: a descriptor holds the sizes.
+ *
+ * Conventions beyond those at the head of this file:
+ *  - Strides are in elements; the last dimension is contiguous.  Strides are
+ *    not negative and keep 16-byte alignment (multiples of 8 elements at 16
+ *    bits, of 4 at 32), else FFTCONV_ERR_ALIGNMENT.
+ *  - Outputs are contiguous and overlap no input, no other output and no
+ *    workspace (FFTCONV_ERR_INVALID_ARG).
+ *  - A size of zero is a valid call with empty tensors; pointers to empty
+ *    tensors may be NULL.
+ * ------------------------------------------------------------------------ */
+
+typedef enum fftconv_norm_kind {
+    FFTCONV_NORM_RMS = 0,     /* r = (sum x^2 / D + eps)^(-1/2)             */
+    FFTCONV_NORM_L2 = 1       /* r = (sum x^2 + eps)^(-1/2)                 */
+} fftconv_norm_kind;
+
+/* Sizes of fftconv_qknorm_forward / _backward. */
+typedef struct fftconv_qknorm_desc {
+    fftconv_dtype dtype;      /* of q, k, their outputs and gradients       */
+    size_t B, T, Hq, Hk, D;   /* q [B][T][Hq][D], k [B][T][Hk][D];
+                                 D a multiple of 8, at most 256             */
+    size_t rotary_dim;        /* R: the first R elements of each head are
+                                 rotated; 0 none, else R <= D and a multiple
+                                 of 16 (pairs i, i + R/2) or of 8 (pairs
+                                 2i, 2i+1)                                  */
+    int interleaved;          /* pairs 2i, 2i+1 instead of i, i + R/2       */
+    fftconv_norm_kind norm;
+    float eps;
+    size_t table_rows;        /* P: rows of cos and sin                     */
+    long long q_stride[3];    /* batch, token, head                         */
+    long long k_stride[3];
+} fftconv_qknorm_desc;
+
+/* Norms of queries and keys for each head, with the position rotation in the
+ * same pass:
+ *     n = w x r (r as in fftconv_norm_kind),
+ *     (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin)
+ * for the pairs (a, b) of the first R elements, y = n for the others.
+ *  q_weight, k_weight: device, fp32 [D], or NULL for w = 1.
+ *  cos, sin: device, fp32 [P][R/2]; positions: device, int64 [B][T], the
+ *     row of the tables for each token (all three unused when R = 0).  The
+ *     rotated elements of a token whose position is not in [0, P) are NaN.
+ *  q_out [B][T][Hq][D], k_out [B][T][Hk][D].
+ * Arithmetic is fp32 with one rounding to the outputs' type. */
+fftconv_status fftconv_qknorm_forward(const fftconv_qknorm_desc *desc, const void *q,
+                                      const void *k, const float *q_weight,
+                                      const float *k_weight, const float *cos,
+                                      const float *sin, const long long *positions,
+                                      void *q_out, void *k_out, void *stream);
+
+/* Bytes of the workspace of fftconv_qknorm_backward (0 where no weight
+ * gradient is asked for does not matter: it is only used for those). */
+size_t fftconv_qknorm_workspace_bytes(const fftconv_qknorm_desc *desc);
+
+/* Gradients of fftconv_qknorm_forward with respect to q, k (dq, dk,
+ * contiguous) and the weights (dq_weight, dk_weight: fp32 [D], each NULL to
+ * skip it), from the gradients of its outputs (dq_out, dk_out: contiguous).
+ * The weight sums run in a fixed order: equal inputs give equal bits. */
+fftconv_status fftconv_qknorm_backward(const fftconv_qknorm_desc *desc, const void *q,
+                                       const void *k, const float *q_weight,
+                                       const float *k_weight, const float *cos,
+                                       const float *sin, const long long *positions,
+                                       const void *dq_out, const void *dk_out, void *dq,
+                                       void *dk, float *dq_weight, float *dk_weight,
+                                       void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/* Sizes of the gated delta rule's calls. */
+typedef struct fftconv_delta_desc {
+    fftconv_dtype dtype;      /* of q, k, v, o and their gradients          */
+    size_t B, T;              /* batch rows and tokens of a row             */
+    size_t Hk, Hv;            /* heads of q and k, and of v: Hv a multiple of
+                                 Hk; value head h reads head h / (Hv/Hk)    */
+    size_t Dk, Dv;            /* head sizes, multiples of 8; Dk <= 128,
+                                 Dv <= 1024                                 */
+    size_t sequences;         /* 0: each batch row is a sequence.  n > 0: B
+                                 = 1 and the row packs n sequences whose
+                                 bounds are in cu_seqlens                   */
+    float scale;              /* of the outputs, e.g. Dk^(-1/2)             */
+    long long q_stride[3];    /* batch, token, head                         */
+    long long k_stride[3];
+    long long v_stride[3];
+} fftconv_delta_desc;
+
+/* The gated delta rule over sequences.  For each value head, from a state S
+ * [Dk][Dv], every token does
+ *     S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  o = scale S^T q.
+ *  q, k [B][T][Hk][Dk], v [B][T][Hv][Dv]: strided, plan of the descriptor.
+ *  g (log decay), beta (write strength): fp32 [B][T][Hv], contiguous.  g may
+ *     be -inf (the state is dropped).  The rule is stable for beta |k|^2 <= 2
+ *     and g <= 0: keys of norm one (FFTCONV_NORM_L2).
+ *  cu_seqlens: device, int64 [sequences + 1], ascending from 0 to T
+ *     (sequences may be empty); NULL when sequences = 0.  Bounds outside
+ *     [0, T] or out of order are clamped on the device.
+ *  initial_state: fp32 [rows][Hv][Dk][Dv], rows = sequences or B; NULL for 0.
+ *  o [B][T][Hv][Dv].  Tokens that no sequence holds are not written.
+ *  final_state: fp32, as initial_state; NULL to skip it.
+ *  saved: fftconv_delta_saved_bytes(desc) bytes that fftconv_delta_backward
+ *     will read (16-B aligned), or NULL in inference.
+ *  workspace: fftconv_delta_workspace_bytes(desc) bytes; unused (may be NULL)
+ *     when saved is given.
+ * States, gates and sums are fp32 or wider whatever the I/O type; fp32
+ * operands of the matrix products are split so that 24 bits take part. */
+fftconv_status fftconv_delta_forward(const fftconv_delta_desc *desc, const void *q,
+                                     const void *k, const void *v, const float *g,
+                                     const float *beta, const long long *cu_seqlens,
+                                     const float *initial_state, void *o,
+                                     float *final_state, void *saved, size_t saved_bytes,
+                                     void *workspace, size_t workspace_bytes,
+                                     void *stream);
+size_t fftconv_delta_workspace_bytes(const fftconv_delta_desc *desc);
+size_t fftconv_delta_saved_bytes(const fftconv_delta_desc *desc);
+
+/* One token for each of desc->B requests (T must be 1) against a pool of
+ * states that is updated in place.
+ *  q, k, v, g, beta: as above with T = 1.
+ *  state: fp32 [pool][Hv][Dk][Dv]; slots: device, int64 [B], the state of
+ *     each request (NULL: request i has state i).  A request whose slot is
+ *     outside [0, pool), such as -1 for padding, changes no state and its o
+ *     is 0.  Two requests of a call must not share a slot.
+ *  o [B][Hv][Dv]. */
+fftconv_status fftconv_delta_step(const fftconv_delta_desc *desc, const void *q,
+                                  const void *k, const void *v, const float *g,
+                                  const float *beta, float *state, size_t pool,
+                                  const long long *slots, void *o, void *stream);
+
 /* Static, human-readable text for a status code. */
 const char *fftconv_status_string(fftconv_status status);
 
