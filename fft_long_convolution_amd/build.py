@@ -21,7 +21,8 @@ SOURCES = [os.path.join(HERE, "csrc", "fftconv_host.cpp"),
            os.path.join(HERE, "csrc", "fftconv_scratch.hip"),
            os.path.join(HERE, "csrc", "fftconv_delta_host.cpp"),
            os.path.join(HERE, "csrc", "fftconv_qknorm.hip"),
-           os.path.join(HERE, "csrc", "fftconv_delta.hip")]
+           os.path.join(HERE, "csrc", "fftconv_delta.hip"),
+           os.path.join(HERE, "csrc", "fftconv_delta_bwd.hip")]
 # per-source extra flags: the inner multi-pass kernel schedules best with the
 # max-ILP strategy (measured; the other kernels are slower with it)
 EXTRA = {"fftconv_inner.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]}

@@ -88,10 +88,28 @@ struct DeltaParams {
     float* tri;                      // [slots][Hv] (I + A)^-1, operand order
     float* pm;                       // [slots][Hv] decayed scores, operand order
     float* dec;                      // [slots][Hv][kDecFloats]
+    float* trit;                     // the transposes of tri and pm, or null
+    float* pmt;
     float* states;                   // [slots][Hv][Dk][Dv] or null: each
                                      // chunk's first state, for the backward
     float* us;                       // [slots][Hv][kChunk][Dv] or null: U
 };
+struct DeltaGradParams {
+    DeltaParams f;                   // inputs, dec, trit, pmt, states, us
+    const void* dout;                // [B][T][Hv][Dv]
+    const float* dfin;               // [nseq][Hv][Dk][Dv] or null
+    float* dstates;                  // [slots][Hv][Dk][Dv]: gradient of each
+                                     // chunk's last state
+    float* dys;                      // [slots][Hv][kChunk][Dv]: T^T dU
+    void* dq;                        // [B][T][Hk][Dk]
+    void* dk;
+    void* dv;                        // [B][T][Hv][Dv]
+    float* dg;                       // [B][T][Hv]
+    float* dbeta;
+    float* dinit;                    // [nseq][Hv][Dk][Dv] or null
+};
+hipError_t launch_delta_rscan(int io, const DeltaGradParams& p, hipStream_t s);
+hipError_t launch_delta_grads(int io, const DeltaGradParams& p, hipStream_t s);
 hipError_t launch_delta_prep(int io, const DeltaParams& p, hipStream_t s);
 hipError_t launch_delta_scan(int io, const DeltaParams& p, hipStream_t s);
 

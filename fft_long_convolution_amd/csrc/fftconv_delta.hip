@@ -15,17 +15,10 @@
 //   S1 = e^Gc S0 + K^T (e^(Gc-G) o U)
 // T and P need no state: delta_prep_kernel makes them for all chunks at
 // once.  delta_scan_kernel then walks over a sequence's chunks.
-//
-// Sums of log decays are formed in fp64, so e^(G_i - G_j) is right to fp32
-// however much the chunk has decayed before; log decays below -1e4 count as
-// -1e4 (their factor is 0 in fp32 either way), so a reset (g = -inf) does not
-// meet itself as inf - inf.
 #include "fftconv_delta_dev.h"
 
 namespace fftconv {
 namespace {
-
-constexpr float kLowestDecay = -1e4f;
 
 // ------------------------------------------------------------ one token
 
@@ -110,8 +103,6 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
 
 // ------------------------------------- what a chunk needs before its state
 
-constexpr int kLd = 68;   // floats between rows of the 64 x 64 matrices in LDS
-
 __device__ __forceinline__ dfloat4 mma_f32(float a, float b, dfloat4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
@@ -190,6 +181,19 @@ __device__ __forceinline__ void store_tri(const float (*t)[kLd], float* dst) {
     }
 }
 
+// The same triangle's transpose, an upper one: tile (m, kb), kb >= m / 2.
+__device__ __forceinline__ void store_tri_transposed(const float (*t)[kLd], float* dst) {
+    for (int i = threadIdx.x; i < kTriTiles * 64; i += blockDim.x) {
+        const int tile = i >> 6, l = i & 63;
+        const int m = tile < 4 ? tile >> 1 : tile - 2;
+        const int kb = tile < 4 ? tile & 1 : 1;
+        const int col = tile_row(m, l & 15), row = 32 * kb + 8 * (l >> 4);
+        float4* d = (float4*)(dst + (long long)i * 8);
+        d[0] = make_float4(t[row][col], t[row + 1][col], t[row + 2][col], t[row + 3][col]);
+        d[1] = make_float4(t[row + 4][col], t[row + 5][col], t[row + 6][col], t[row + 7][col]);
+    }
+}
+
 // One workgroup per chunk and value head.
 template <int IO, int DK>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
@@ -212,15 +216,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     const int c = lane & 15, g4 = lane >> 4;
     if (wave == 0) {
         const long long gi = (sp.b * p.T + tok + lane) * p.Hv + h;
-        float gv = lane < n ? p.g[gi] : 0.f;
+        const float gv = lane < n ? p.g[gi] : 0.f;
         const float bv = lane < n ? p.beta[gi] : 0.f;
-        gv = gv < kLowestDecay ? kLowestDecay : gv;   // keeps NaN
-        double s = gv;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const double o = __shfl_up(s, m);
-            if (lane >= m) s += o;
-        }
+        const double s = decay_sum(gv);
         G[lane] = s;
         bet[lane] = bv;
         const double last = __shfl(s, 63);
@@ -267,69 +265,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
         }
     __syncthreads();
     store_tri(P, p.pm + id * kTriFloats);
+    if (p.pmt) store_tri_transposed(P, p.pmt + id * kTriFloats);
     __syncthreads();
     invert_unit_lower(A, P);
     store_tri(P, p.tri + id * kTriFloats);
+    if (p.trit) store_tri_transposed(P, p.trit + id * kTriFloats);
 }
 
 // ------------------------------------------------- the walk over the chunks
-
-// Fills the A operands of `rows` x DK from 64 tokens of a head: tile (m, kb),
-// lane (g, c) holds [token tile_row(m, c)][32 kb + 8 g + i].
-template <int IO, int DK>
-__device__ __forceinline__ void fill_rows(uint4* dst, const void* src, long long base,
-                                          long long stride, int n, int Dk) {
-    constexpr int NA = IoTerms<IO>::n, KB = DK / 32;
-    for (int i = threadIdx.x; i < 4 * KB * 64; i += 256) {
-        const int tile = i >> 6, l = i & 63;
-        const int m = tile / KB, kb = tile - m * KB;
-        const int row = tile_row(m, l & 15), e = 32 * kb + 8 * (l >> 4);
-        uint4 t[NA];
-        load_terms<IO>(src, base + row * stride + e, row < n && e < Dk, t);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) dst[a * 4 * KB * 64 + i] = t[a];
-    }
-}
-// The same tokens' transpose: tile (t, tb), lane (g, c) holds
-// [element tile_row(t, c)][token 32 tb + 8 g + i].
-template <int IO, int DK>
-__device__ __forceinline__ void fill_cols(uint4* dst, const void* src, long long base,
-                                          long long stride, int n, int Dk) {
-    constexpr int NA = IoTerms<IO>::n;
-    for (int i = threadIdx.x; i < 8 * (DK / 8); i += 256) {
-        // eight tokens x eight elements
-        const int tg = i & 7, ec = i >> 3;
-        uint4 t[8][NA];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            load_terms<IO>(src, base + (8 * tg + j) * stride + 8 * ec,
-                           8 * tg + j < n && 8 * ec < Dk, t[j]);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-            uint4 r[8], col[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = t[j][a];
-            transpose8(r, col);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // element 8 ec + j: tile and row that stand for it
-                const int tile = 2 * (ec >> 2) + (j >> 2), row = 4 * (ec & 3) + (j & 3);
-                dst[((a * (DK / 16) + tile) * 2 + (tg >> 2)) * 64 + 16 * (tg & 3) + row] = col[j];
-            }
-        }
-    }
-}
-template <int N>
-__device__ __forceinline__ void fill_tri(uint4* dst, const float* src) {
-    for (int i = threadIdx.x; i < kTriTiles * 64; i += 256) {
-        const float4 a = *(const float4*)(src + i * 8), b = *(const float4*)(src + i * 8 + 4);
-        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint4 t[N];
-        split8<N>(x, t);
-#pragma unroll
-        for (int j = 0; j < N; ++j) dst[j * kTriTiles * 64 + i] = t[j];
-    }
-}
 
 template <int IO, int DK>
 struct ScanLds {

@@ -37,6 +37,11 @@ __device__ __forceinline__ constexpr int tri_tile(int m, int kb) {
     return m < 2 ? m : 2 + 2 * (m - 2) + kb;
 }
 
+// tile (m, kb) of an upper triangle, kb >= m / 2
+__device__ __forceinline__ constexpr int upper_tile(int m, int kb) {
+    return m < 2 ? 2 * m + kb : 2 + m;
+}
+
 struct Span {
     long long b, t0, slot0;
     int len;
@@ -175,6 +180,80 @@ __device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
         }
         c[j] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+}
+
+// Fills the A operands of 64 tokens x DK of a head in LDS: tile (m, kb),
+// lane (g, c) holds [token tile_row(m, c)][32 kb + 8 g + i].
+template <int IO, int DK>
+__device__ __forceinline__ void fill_rows(uint4* dst, const void* src, long long base,
+                                          long long stride, int n, int Dk) {
+    constexpr int NA = IoTerms<IO>::n, KB = DK / 32;
+    for (int i = threadIdx.x; i < 4 * KB * 64; i += 256) {
+        const int tile = i >> 6, l = i & 63;
+        const int m = tile / KB, kb = tile - m * KB;
+        const int row = tile_row(m, l & 15), e = 32 * kb + 8 * (l >> 4);
+        uint4 t[NA];
+        load_terms<IO>(src, base + row * stride + e, row < n && e < Dk, t);
+#pragma unroll
+        for (int a = 0; a < NA; ++a) dst[a * 4 * KB * 64 + i] = t[a];
+    }
+}
+// The same tokens' transpose: tile (t, tb), lane (g, c) holds
+// [element tile_row(t, c)][token 32 tb + 8 g + i].
+template <int IO, int DK>
+__device__ __forceinline__ void fill_cols(uint4* dst, const void* src, long long base,
+                                          long long stride, int n, int Dk) {
+    constexpr int NA = IoTerms<IO>::n;
+    for (int i = threadIdx.x; i < 8 * (DK / 8); i += 256) {
+        // eight tokens x eight elements
+        const int tg = i & 7, ec = i >> 3;
+        uint4 t[8][NA];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            load_terms<IO>(src, base + (8 * tg + j) * stride + 8 * ec,
+                           8 * tg + j < n && 8 * ec < Dk, t[j]);
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+            uint4 r[8], col[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = t[j][a];
+            transpose8(r, col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // element 8 ec + j: tile and row that stand for it
+                const int tile = 2 * (ec >> 2) + (j >> 2), row = 4 * (ec & 3) + (j & 3);
+                dst[((a * (DK / 16) + tile) * 2 + (tg >> 2)) * 64 + 16 * (tg & 3) + row] = col[j];
+            }
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void fill_tri(uint4* dst, const float* src) {
+    for (int i = threadIdx.x; i < kTriTiles * 64; i += 256) {
+        const float4 a = *(const float4*)(src + i * 8), b = *(const float4*)(src + i * 8 + 4);
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint4 t[N];
+        split8<N>(x, t);
+#pragma unroll
+        for (int j = 0; j < N; ++j) dst[j * kTriTiles * 64 + i] = t[j];
+    }
+}
+
+constexpr int kLd = 68;   // floats between rows of the 64 x 64 matrices in LDS
+
+// Sum of the log decays up to the lane's token.  Sums are fp64, so
+// e^(G_i - G_j) is right to fp32 however much the chunk has decayed before;
+// decays below -1e4 count as -1e4 (their factor is 0 in fp32 either way), so
+// a reset (g = -inf) does not meet itself as inf - inf.  NaN stays NaN.
+__device__ __forceinline__ double decay_sum(float g) {
+    const int lane = threadIdx.x & 63;
+    double s = g < -1e4f ? -1e4f : g;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const double o = __shfl_up(s, m);
+        if (lane >= m) s += o;
+    }
+    return s;
 }
 
 // Workgroups are dealt round robin over the 8 XCDs; this gives each XCD a

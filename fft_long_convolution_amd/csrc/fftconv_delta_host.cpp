@@ -195,7 +195,7 @@ size_t delta_slots(const fftconv_delta_desc* d) {
 
 // Where the buffers of a call stand in a block of memory, in floats.
 struct DeltaLayout {
-    size_t tri, pm, dec, states, us, all;
+    size_t tri, pm, dec, trit, pmt, states, us, all;
 };
 bool delta_layout(const fftconv_delta_desc* d, bool saved, DeltaLayout* l) {
     size_t n, x, y;
@@ -204,7 +204,9 @@ bool delta_layout(const fftconv_delta_desc* d, bool saved, DeltaLayout* l) {
     l->tri = 0;
     l->pm = n * kTriFloats;
     l->dec = l->pm + n * kTriFloats;
-    l->states = l->dec + n * kDecFloats;
+    l->trit = l->dec + n * kDecFloats;
+    l->pmt = l->trit + (saved ? n * kTriFloats : 0);
+    l->states = l->pmt + (saved ? n * kTriFloats : 0);
     l->us = l->states + (saved ? x : 0);
     l->all = l->us + (saved ? y : 0);
     return true;
@@ -275,6 +277,8 @@ void delta_place(const DeltaLayout& l, void* block, bool saved, DeltaParams& p) 
     p.tri = f + l.tri;
     p.pm = f + l.pm;
     p.dec = f + l.dec;
+    p.trit = saved ? f + l.trit : nullptr;
+    p.pmt = saved ? f + l.pmt : nullptr;
     p.states = saved ? f + l.states : nullptr;
     p.us = saved ? f + l.us : nullptr;
 }
@@ -387,6 +391,63 @@ fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q,
     hipStream_t s = (hipStream_t)stream;
     if (d->B * d->T) CHECK(launched(launch_delta_prep(d->dtype, p, s)));
     return launched(launch_delta_scan(d->dtype, p, s));
+}
+
+size_t fftconv_delta_backward_workspace_bytes(const fftconv_delta_desc* d) {
+    DeltaLayout l;
+    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, true, &l)) return 0;
+    return (l.all - l.states) * 4;      // as many as the saved states and U
+}
+
+fftconv_status fftconv_delta_backward(const fftconv_delta_desc* d, const void* q, const void* k,
+                                      const void* v, const float* g, const float* beta,
+                                      const long long* cu_seqlens, const void* saved,
+                                      size_t saved_bytes, const void* d_o,
+                                      const float* d_final_state, void* dq, void* dk, void* dv,
+                                      float* dg, float* dbeta, float* d_initial_state,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+    DeltaGradParams p = DeltaGradParams();
+    Range in[7];
+    CHECK(delta_inputs(d, {q, k, v, g, beta, cu_seqlens, nullptr}, p.f, in));
+    DeltaLayout l;
+    if (!delta_layout(d, true, &l)) return FFTCONV_ERR_UNSUPPORTED;
+    const size_t n = d->B * d->T, e = elem(d->dtype);
+    const size_t on = n * d->Hv * d->Dv * e, kn = n * d->Hk * d->Dk * e, gn = n * d->Hv * 4;
+    const size_t state = (size_t)p.f.nseq * d->Hv * d->Dk * d->Dv * 4;
+    CHECK(check_ptr(d_o, on));
+    CHECK(check_ptr(d_final_state, state, false));
+    CHECK(check_ptr(dq, kn));
+    CHECK(check_ptr(dk, kn));
+    CHECK(check_ptr(dv, on));
+    CHECK(check_ptr(dg, gn));
+    CHECK(check_ptr(dbeta, gn));
+    CHECK(check_ptr(d_initial_state, state, false));
+    CHECK(check_ptr(saved, l.all * 4));
+    if (saved_bytes < l.all * 4) return FFTCONV_ERR_INVALID_ARG;
+    const size_t need = (l.all - l.states) * 4;
+    if (need && (!workspace || workspace_bytes < need)) return FFTCONV_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 15) return FFTCONV_ERR_ALIGNMENT;
+    in[5] = {saved, l.all * 4};
+    const Range more[] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6], {d_o, on},
+                          {d_final_state, state}};
+    const Range out[] = {{dq, kn}, {dk, kn}, {dv, on}, {dg, gn}, {dbeta, gn},
+                         {d_initial_state, state}, {workspace, need}};
+    if (!outputs_clear(out, more)) return FFTCONV_ERR_INVALID_ARG;
+    if (!p.f.nseq) return FFTCONV_OK;
+    delta_place(l, (void*)saved, true, p.f);     // only read here
+    p.dout = d_o;
+    p.dfin = d_final_state;
+    p.dstates = (float*)workspace;
+    p.dys = (float*)workspace + (l.us - l.states);
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.dg = dg;
+    p.dbeta = dbeta;
+    p.dinit = d_initial_state;
+    hipStream_t s = (hipStream_t)stream;
+    CHECK(launched(launch_delta_rscan(d->dtype, p, s)));
+    return n ? launched(launch_delta_grads(d->dtype, p, s)) : FFTCONV_OK;
 }
 
 fftconv_status fftconv_delta_step(const fftconv_delta_desc* d, const void* q, const void* k,

@@ -61,6 +61,8 @@ def lib() -> ctypes.CDLL:
                 ("fftconv_delta_forward", i, [dd] + [vp] * 10 + [sz, vp, sz, vp]),
                 ("fftconv_delta_workspace_bytes", sz, [dd]),
                 ("fftconv_delta_saved_bytes", sz, [dd]),
+                ("fftconv_delta_backward", i, [dd] + [vp] * 7 + [sz] + [vp] * 9 + [sz, vp]),
+                ("fftconv_delta_backward_workspace_bytes", sz, [dd]),
                 ("fftconv_delta_step", i, [dd] + [vp] * 6 + [sz, vp, vp, vp])):
             fn = getattr(L, name)
             fn.restype, fn.argtypes = res, args
@@ -139,7 +141,7 @@ class _Op:
     def _space(nbytes, given, device, name):
         """A workspace of at least nbytes: the caller's or a new one."""
         if given is None:
-            return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
         if given.device != device or not given.is_contiguous():
             raise ValueError("%s must be contiguous on %s" % (name, device))
         return given
@@ -322,6 +324,32 @@ class GatedDelta(_Op):
                             args[0], "saved")
         o, state = self._forward(args, out, final_state, saved, None, stream)
         return o, state, saved
+
+    def backward(self, q, k, v, g, beta, d_out, saved, d_final_state=None, initial_state=None,
+                 cu_seqlens=None, workspace=None, stream=None):
+        """Gradients of forward_train, for the same inputs and what it saved:
+        d_out = dL/do, d_final_state = dL/d(final state) (None: 0).  Returns
+        (dq, dk, dv, dg, dbeta, d_initial_state); the last is None where there
+        is no initial_state."""
+        dev, desc, state, ins = self._inputs(q, k, v, g, beta, initial_state, cu_seqlens)
+        q, k, v, g, beta, cu, init = ins
+        _check(d_out, "d_out", v.shape, self._dt, dev)
+        d_out = _dense(d_out)
+        if d_final_state is not None:
+            _check(d_final_state, "d_final_state", state, torch.float32, dev)
+            d_final_state = _dense(d_final_state)
+        if saved.device != dev or not saved.is_contiguous():
+            raise ValueError("saved must be what forward_train returned")
+        ref = ctypes.byref(desc)
+        ws = self._space(self._lib.fftconv_delta_backward_workspace_bytes(ref), workspace, dev,
+                         "workspace")
+        new = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v, g, beta)]
+        new.append(None if init is None else torch.empty(state, dtype=torch.float32, device=dev))
+        self._call("fftconv_delta_backward", dev, stream,
+                   (*ins, saved, d_out, d_final_state, ws, *new), ref, *map(_ptr, ins[:6]),
+                   _ptr(saved), self._bytes(saved), _ptr(d_out), _ptr(d_final_state),
+                   *map(_ptr, new), _ptr(ws), self._bytes(ws))
+        return tuple(new)
 
     def step(self, q, k, v, g, beta, state, slots=None, out=None, stream=None):
         """One token for each of N requests: q, k [N, Hk, D_k], v [N, Hv, D_v],

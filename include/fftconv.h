@@ -519,6 +519,23 @@ fftconv_status fftconv_delta_forward(const fftconv_delta_desc *desc, const void 
 size_t fftconv_delta_workspace_bytes(const fftconv_delta_desc *desc);
 size_t fftconv_delta_saved_bytes(const fftconv_delta_desc *desc);
 
+/* Gradients of fftconv_delta_forward.
+ *  q .. cu_seqlens: as given to the forward call; saved: what it saved.
+ *  d_o [B][T][Hv][Dv], contiguous; d_final_state: as final_state, or NULL
+ *     for 0.
+ *  dq, dk [B][T][Hk][Dk] (summed over the value heads that share the head,
+ *     in a fixed order), dv [B][T][Hv][Dv], dg, dbeta fp32 [B][T][Hv];
+ *     d_initial_state: as initial_state, or NULL to skip it.
+ *  workspace: fftconv_delta_backward_workspace_bytes(desc) bytes. */
+fftconv_status fftconv_delta_backward(const fftconv_delta_desc *desc, const void *q,
+                                      const void *k, const void *v, const float *g,
+                                      const float *beta, const long long *cu_seqlens,
+                                      const void *saved, size_t saved_bytes, const void *d_o,
+                                      const float *d_final_state, void *dq, void *dk, void *dv,
+                                      float *dg, float *dbeta, float *d_initial_state,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+size_t fftconv_delta_backward_workspace_bytes(const fftconv_delta_desc *desc);
+
 /* One token for each of desc->B requests (T must be 1) against a pool of
  * states that is updated in place.
  *  q, k, v, g, beta: as above with T = 1.

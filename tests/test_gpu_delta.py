@@ -224,3 +224,131 @@ def test_refusals():
         assert e.value.status == 2
     with pytest.raises(ValueError):
         op.step(q[:, 0], k[:, 0], v[:, 0], g[:, 0], beta[:, 0], S.transpose(2, 3))
+
+
+# ------------------------------------------------------------- gradients
+
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dinit")
+
+
+def run_backward(ins, cu, dtype, Dk, Dv, do, dS):
+    op = rule(Dk, Dv, dtype)
+    a = gpu(*ins[:5])
+    kw = dict(initial_state=gpu(ins[5])[0], cu_seqlens=None if cu is None else cu.cuda())
+    o, S, saved = op.forward_train(*a, **kw)
+    o2, S2 = op.forward(*a, **kw)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    return op.backward(*a, do.cuda(), saved, d_final_state=gpu(dS)[0], **kw)
+
+
+def check_backward(ins, cu, dtype, Dk, Dv, with_final=True):
+    gen = torch.Generator().manual_seed(77)
+    do = torch.randn(ins[2].shape, generator=gen).to(DT[dtype])
+    rows = ins[0].shape[0] if cu is None else len(cu) - 1
+    dS = torch.randn(rows, ins[2].shape[2], Dk, Dv, generator=gen) if with_final else None
+    got = run_backward(ins, cu, dtype, Dk, Dv, do, dS)
+    again = run_backward(ins, cu, dtype, Dk, Dv, do, dS)
+    leaf = [None if x is None else x.requires_grad_() for x in double(*ins)]
+    o, S = delta(*leaf, cu, Dk ** -0.5)
+    loss = (o * do.double()).sum() + (0 if dS is None else (S * dS.double()).sum())
+    want = torch.autograd.grad(loss, [x for x in leaf if x is not None])
+    assert (got[5] is None) == (ins[5] is None)
+    for i, (n, w) in enumerate(zip(NAMES, want)):
+        assert got[i].dtype == ins[i].dtype
+        assert torch.equal(got[i], again[i]), n
+        t = TOL[dtype if i < 3 else "f32"]
+        assert rel(got[i], w) <= t, (n, rel(got[i], w))
+
+
+@pytest.mark.parametrize("init", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_backward(shape, dtype, init):
+    ins = delta_inputs(sum(shape) + 1, *shape, dtype, init=init)
+    check_backward(ins, None, dtype, shape[4], shape[5], with_final=init)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bounds", [[0, 1], [0, 0, 5, 5, 6, 70, 70], [0, 64, 128, 129, 300],
+                                    [0, 10, 10, 10, 11, 12, 13, 14, 80]], ids=str)
+def test_backward_packed(bounds, dtype):
+    cu = torch.tensor(bounds)
+    ins = delta_inputs(len(bounds), 1, bounds[-1], 1, 2, 64, 64, dtype, rows=len(bounds) - 1)
+    check_backward(ins, cu, dtype, 64, 64)
+
+
+def test_backward_resets_and_silent_tokens():
+    ins = list(delta_inputs(6, 1, 150, 1, 2, 64, 64, "f32"))
+    g, beta = ins[3].clone(), ins[4].clone()
+    g[0, 10] = -200.0
+    g[0, 63, 0] = -1e30
+    g[0, 100:103] = -1e4
+    beta[0, 20:90] = 0
+    ins[3], ins[4] = g, beta
+    check_backward(ins, None, "f32", 64, 64)
+    # -inf: the factor is 0 and so is its gradient; the 64-bit form would
+    # multiply 0 by inf, so its log decay there is a large finite one
+    got = []
+    for low in (-math.inf, -1e30):
+        g[0, 10] = low
+        ins[3] = g
+        got.append(run_backward(ins, None, "f32", 64, 64, torch.ones_like(ins[2]), None))
+    for a, b in zip(*got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+    assert (got[0][3][0, 10] == 0).all()
+
+
+def test_backward_of_empty_sequences():
+    op = rule(64, 64, "bf16")
+    q, k, v, g, beta, S = gpu(*delta_inputs(3, 1, 0, 1, 2, 64, 64, "bf16", rows=2))
+    cu = torch.zeros(3, dtype=torch.int64, device="cuda")
+    o, F, saved = op.forward_train(q, k, v, g, beta, initial_state=S, cu_seqlens=cu)
+    assert torch.equal(F, S)
+    d = op.backward(q, k, v, g, beta, o, saved, d_final_state=2 * S, initial_state=S,
+                    cu_seqlens=cu)
+    assert torch.equal(d[5], 2 * S)
+
+
+def test_gradient_against_differences():
+    # fp32 kernels: central differences of the library's own forward.  With
+    # h = 2^-6 the third derivative leaves about h^2 / 6 = 4e-5 of a value of
+    # order one, and rounding 1e-6 * |loss| / h = 6e-5 |loss|; |loss| < 10.
+    ins = gpu(*delta_inputs(12, 1, 70, 1, 2, 16, 16, "f32"))
+    op = rule(16, 16, "f32")
+    gen = torch.Generator().manual_seed(5)
+    do = (0.1 * torch.randn(ins[2].shape, generator=gen)).cuda()
+    dS = (0.1 * torch.randn(ins[5].shape, generator=gen)).cuda()
+
+    def loss(a):
+        o, S = op.forward(*a[:5], initial_state=a[5])
+        return ((o.double() * do).sum() + (S.double() * dS).sum()).item()
+
+    o, S, saved = op.forward_train(*ins[:5], initial_state=ins[5])
+    d = op.backward(*ins[:5], do, saved, d_final_state=dS, initial_state=ins[5])
+    h = 2.0 ** -6
+    for i, x in enumerate(ins):
+        for j in torch.randint(0, x.numel(), (8,), generator=gen).tolist():
+            up, down = list(ins), list(ins)
+            for a, s in ((up, h), (down, -h)):
+                a[i] = x.clone()
+                a[i].view(-1)[j] += s
+            diff = (loss(up) - loss(down)) / (2 * h)
+            assert abs(diff - d[i].reshape(-1)[j].item()) <= 2e-3, NAMES[i]
+
+
+def test_backward_refusals():
+    from fft_long_convolution_amd.fftconv import FFTConvError
+    q, k, v, g, beta, S = gpu(*delta_inputs(3, 1, 4, 2, 4, 64, 64, "bf16"))
+    op = rule(64, 64, "bf16")
+    o, F, saved = op.forward_train(q, k, v, g, beta)
+    with pytest.raises(ValueError):
+        op.backward(q, k, v, g, beta, o.float(), saved)
+    with pytest.raises(ValueError):
+        op.backward(q, k, v, g, beta, o, saved, d_final_state=F[:, :2])
+    with pytest.raises(FFTConvError) as e:
+        op.backward(q, k, v, g, beta, o, saved[:-16])
+    assert e.value.status == 1
+    with pytest.raises(FFTConvError) as e:
+        op.backward(q, k, v, g, beta, o, saved,
+                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 4
