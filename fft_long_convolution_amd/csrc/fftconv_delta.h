@@ -66,9 +66,11 @@ hipError_t launch_delta_step(int io, const DeltaStepParams& p, hipStream_t s);
 // cu[i] / kChunk + i ..., which never reach those of sequence i + 1.
 constexpr int kChunk = 64;
 constexpr int kTriTiles = 6;               // 16 x 32 tiles of a 64 x 64 triangle
-constexpr int kTriFloats = kTriTiles * 512;
-// decays of a chunk: e^G [64], e^(Gc-G) [64], beta [64], e^Gc
-constexpr int kDecFloats = 196;
+// What a chunk and value head needs besides its tokens, in matrix-operand
+// order, one uint4 a lane: (I + A)^-1 in three bf16 terms, the decays (e^G,
+// e^(Gc-G), beta, e^Gc, 64 floats each), the decayed scores P.
+int delta_pack_uint4(int io);              // of the forward pack
+int delta_back_pack_uint4();               // of its transposes
 
 struct DeltaParams {
     int Hk, Hv, group, Dk, Dv;
@@ -85,17 +87,20 @@ struct DeltaParams {
     const float* init;               // [nseq][Hv][Dk][Dv] or null
     void* o;                         // [B][T][Hv][Dv]
     float* fin;                      // [nseq][Hv][Dk][Dv] or null
-    float* tri;                      // [slots][Hv] (I + A)^-1, operand order
-    float* pm;                       // [slots][Hv] decayed scores, operand order
-    float* dec;                      // [slots][Hv][kDecFloats]
-    float* trit;                     // the transposes of tri and pm, or null
-    float* pmt;
+    uint4* pack;                     // [slots][Hv] packs
+    uint4* bpack;                    // the transposes' packs, or null
+    // sequences longer than seg_chunks chunks are cut into segments, numbered
+    // like the slots of chunks, where seg_m is given
+    long long segs;
+    int seg_chunks;
+    float* seg_n;                    // [segs][Hv][Dk][Dv]
+    float* seg_m;                    // [segs][Hv][Dk][Dk]
     float* states;                   // [slots][Hv][Dk][Dv] or null: each
                                      // chunk's first state, for the backward
     float* us;                       // [slots][Hv][kChunk][Dv] or null: U
 };
 struct DeltaGradParams {
-    DeltaParams f;                   // inputs, dec, trit, pmt, states, us
+    DeltaParams f;                   // inputs, bpack, states, us
     const void* dout;                // [B][T][Hv][Dv]
     const float* dfin;               // [nseq][Hv][Dk][Dv] or null
     float* dstates;                  // [slots][Hv][Dk][Dv]: gradient of each

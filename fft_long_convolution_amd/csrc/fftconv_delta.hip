@@ -167,42 +167,51 @@ __device__ void invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
     __syncthreads();
 }
 
-// Writes a lower triangle from LDS in operand order: tile (m, kb), lane
-// (g, c), element i holds [tile_row(m, c)][32 kb + 8 g + i].
-__device__ __forceinline__ void store_tri(const float (*t)[kLd], float* dst) {
+// Writes a lower triangle from LDS as N terms in operand order: tile (m, kb),
+// lane (g, c), element i holds [tile_row(m, c)][32 kb + 8 g + i].
+template <int N>
+__device__ __forceinline__ void store_tri(const float (*t)[kLd], uint4* dst) {
     for (int i = threadIdx.x; i < kTriTiles * 64; i += blockDim.x) {
         const int tile = i >> 6, l = i & 63;
         const int m = tile < 2 ? tile : 2 + ((tile - 2) >> 1);
         const int kb = tile < 2 ? 0 : (tile - 2) & 1;
         const float* s = &t[tile_row(m, l & 15)][32 * kb + 8 * (l >> 4)];
-        float4* d = (float4*)(dst + (long long)i * 8);
-        d[0] = *(const float4*)s;
-        d[1] = *(const float4*)(s + 4);
+        const float4 a = *(const float4*)s, b = *(const float4*)(s + 4);
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint4 w[N];
+        split8<N>(x, w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) dst[j * kTriTiles * 64 + i] = w[j];
     }
 }
-
 // The same triangle's transpose, an upper one: tile (m, kb), kb >= m / 2.
-__device__ __forceinline__ void store_tri_transposed(const float (*t)[kLd], float* dst) {
+template <int N>
+__device__ __forceinline__ void store_tri_transposed(const float (*t)[kLd], uint4* dst) {
     for (int i = threadIdx.x; i < kTriTiles * 64; i += blockDim.x) {
         const int tile = i >> 6, l = i & 63;
         const int m = tile < 4 ? tile >> 1 : tile - 2;
         const int kb = tile < 4 ? tile & 1 : 1;
         const int col = tile_row(m, l & 15), row = 32 * kb + 8 * (l >> 4);
-        float4* d = (float4*)(dst + (long long)i * 8);
-        d[0] = make_float4(t[row][col], t[row + 1][col], t[row + 2][col], t[row + 3][col]);
-        d[1] = make_float4(t[row + 4][col], t[row + 5][col], t[row + 6][col], t[row + 7][col]);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = t[row + j][col];
+        uint4 w[N];
+        split8<N>(x, w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) dst[j * kTriTiles * 64 + i] = w[j];
     }
 }
 
 // One workgroup per chunk and value head.
 template <int IO, int DK>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
+    typedef Operand<IO> Op;
     constexpr int NA = IoTerms<IO>::n, KB = DK / 32;
     const long long id = xcd_unit(blockIdx.x, p.slots * p.Hv);
     if (id >= p.slots * p.Hv) return;
     const long long slot = id / p.Hv;
     const int h = (int)(id - slot * p.Hv);
-    const long long seq = seq_of(p, slot);
+    const long long seq = seq_of(p, slot, 1);
     const Span sp = span_of(p, seq);
     const long long at = (slot - sp.slot0) * kChunk;
     if (at < 0 || at >= sp.len) return;      // a slot between two sequences
@@ -222,11 +231,15 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
         G[lane] = s;
         bet[lane] = bv;
         const double last = __shfl(s, 63);
-        float* dec = p.dec + id * kDecFloats;
-        dec[lane] = expf((float)s);
-        dec[64 + lane] = expf((float)(last - s));
-        dec[128 + lane] = bv;
-        if (lane == 0) dec[192] = expf((float)last);
+        const float eg = expf((float)s), ee = expf((float)(last - s)), ec = expf((float)last);
+        for (uint4* d : {p.pack + id * Op::kPack, p.bpack ? p.bpack + id * kBackPack : nullptr})
+            if (d) {
+                float* dec = (float*)(d + 3 * kTriTiles * 64);
+                dec[lane] = eg;
+                dec[64 + lane] = ee;
+                dec[128 + lane] = bv;
+                dec[192 + lane] = ec;
+            }
     }
     // scores of the 16 rows of the wave against the columns up to them
     const int hk = h / p.group;
@@ -264,92 +277,134 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
             P[row][col] = row >= col ? p.scale * gam * qk[j][r] : 0.f;
         }
     __syncthreads();
-    store_tri(P, p.pm + id * kTriFloats);
-    if (p.pmt) store_tri_transposed(P, p.pmt + id * kTriFloats);
+    uint4* pack = p.pack + id * Op::kPack;
+    uint4* back = p.bpack ? p.bpack + id * kBackPack : nullptr;
+    constexpr int kP = (3 * kTriTiles + 1) * 64;
+    store_tri<Op::NP>(P, pack + kP);
+    if (back) store_tri_transposed<3>(P, back + kP);
     __syncthreads();
     invert_unit_lower(A, P);
-    store_tri(P, p.tri + id * kTriFloats);
-    if (p.trit) store_tri_transposed(P, p.trit + id * kTriFloats);
+    store_tri<3>(P, pack);
+    if (back) store_tri_transposed<3>(P, back);
 }
 
 // ------------------------------------------------- the walk over the chunks
 
-template <int IO, int DK>
+// LDS of the walk, in uint4.  16-bit keys are loaded one chunk ahead into a
+// second buffer; fp32 keys, three times as large, have no room for one.
+template <int IO, int DK, bool FULL>
 struct ScanLds {
-    static constexpr int NA = IoTerms<IO>::n;
-    static constexpr int NP = IO == IO_F32 ? 3 : 2;   // terms of P and of U in P U
-    // fp32 operands fill the LDS: the transposed keys take the place of the
-    // keys once those are used
-    static constexpr bool kShare = NA == 3;
-    static constexpr int kRows = NA * 4 * (DK / 32) * 64;     // uint4
-    static constexpr int kK = 0, kQ = kRows, kT = kShare ? 0 : 2 * kRows;
-    static constexpr int kTri = kShare ? 2 * kRows : 3 * kRows;
-    static constexpr int kP = kTri + 3 * kTriTiles * 64;
-    static constexpr int kDec = kP + NP * kTriTiles * 64;
-    static constexpr int kBytes = (kDec + kDecFloats / 4) * 16;
+    static constexpr int NA = Operand<IO>::NA;
+    static constexpr int kRows = NA * 4 * (DK / 32) * 64;
+    static constexpr int kBufs = NA == 1 ? 2 : 1;
+    static constexpr int kK = 0, kQ = kBufs * kRows;
+    static constexpr int kPack = kQ + (FULL ? kRows : 0);
+    static constexpr int kTri = kPack, kDec = kTri + 3 * kTriTiles * 64, kP = kDec + 64;
+    static constexpr int kTail = FULL ? Operand<IO>::NP * kTriTiles * 64 : 0;
+    static constexpr int kBytes = (kP + kTail) * 16;
 };
 
 // A wave owns 16 columns of the state: its accumulators hold S (Dk x 16), and
 // every product of the chunk, K S, T X, P U, K^T U, takes the last one's
 // accumulators as its B operand, so the chain of a chunk has no exchange and
 // no barrier of its own.  The four waves of a workgroup share the operands
-// that do not depend on the state (K, Q, K^T, T, P) through LDS.
-template <int IO, int DK>
-__global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
-    typedef ScanLds<IO, DK> L;
-    constexpr int NA = L::NA, KB = DK / 32, ST = DK / 16, NP = L::NP;
+// that do not depend on the state (K, Q, T, P) through LDS, K^T being K read
+// transposed.  K of the next chunk is on its way during the whole chunk, the
+// rest from the last use of the present ones on.
+//
+// FULL: outputs and final state.  Otherwise a segment's effect on the state
+// alone: its last state from the first (the first segment of a sequence) or
+// from 0, and, in columns of their own, the matrix its first state is
+// multiplied with (the last state from the identity, without v).
+template <int IO, int DK, bool FULL>
+__global__ __launch_bounds__(256, Operand<IO>::NA == 1 ? 2 : 1)
+void delta_scan_kernel(DeltaParams p) {
+    typedef ScanLds<IO, DK, FULL> L;
+    typedef Operand<IO> Op;
+    constexpr int NA = Op::NA, KB = DK / 32, ST = DK / 16, NP = Op::NP, NB = Op::NB;
     extern __shared__ uint4 lds[];
     const float* dec = (const float*)(lds + L::kDec);
-    const int cols = (p.Dv + 63) / 64;
-    const long long units = p.nseq * p.Hv * cols;
+    const int vcols = (p.Dv + 63) / 64, cols = vcols + (FULL ? 0 : (p.Dk + 63) / 64);
+    const long long units = p.segs * p.Hv * cols;
     long long id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
-    const int cb = (int)(id % cols);
+    int cb = (int)(id % cols);
     id /= cols;
     const int h = (int)(id % p.Hv);
-    const long long seq = id / p.Hv;
+    const long long seg = id / p.Hv;
+    const long long seq = seq_of(p, seg, p.seg_chunks);
     const Span sp = span_of(p, seq);
+    const int chunks = (sp.len + kChunk - 1) / kChunk;
+    const int sn = (int)(seg - seg_of(p, sp, seq));      // segment of the sequence
+    const int first = sn * p.seg_chunks;
+    const int last = first + p.seg_chunks < chunks ? first + p.seg_chunks : chunks;
+    if (sn != 0 && first >= chunks) return;              // no such segment
+    if (!FULL && (last == chunks || (sn == 0 && cb >= vcols))) return;
+    const bool matrix = !FULL && cb >= vcols;
+    if (matrix) cb -= vcols;
+
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
+    const int slot = 16 * g + (c ^ (4 * g));             // of a row operand
     const int col = cb * 64 + wave * 16 + c;
-    const bool cok = col < p.Dv;
+    const int width = matrix ? p.Dk : p.Dv;
+    const bool cok = col < width;
     const int hk = h / p.group;
-    const long long sbase = (seq * p.Hv + h) * p.Dk * (long long)p.Dv + col;
+    const long long state = p.Dk * (long long)p.Dv;
     dfloat4 S[ST];
+    {
+        const float* s = nullptr;
+        if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col : nullptr;
+        else if (FULL) s = p.seg_n + ((seg - 1) * p.Hv + h) * state + col;
 #pragma unroll
-    for (int t = 0; t < ST; ++t)
+        for (int t = 0; t < ST; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = tile_row(t, 4 * g + r);
-            S[t][r] = p.init && cok && row < p.Dk ? p.init[sbase + (long long)row * p.Dv] : 0.f;
-        }
-    const int chunks = (sp.len + kChunk - 1) / kChunk;
-    for (int ch = 0; ch < chunks; ++ch) {
-        const long long tok = sp.t0 + (long long)ch * kChunk;
-        const int left = sp.len - ch * kChunk, n = left < kChunk ? left : kChunk;
-        const long long ci = (sp.slot0 + ch) * p.Hv + h;
-        const long long kbase = sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2];
-        const long long qbase = sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2];
-        fill_rows<IO, DK>(lds + L::kK, p.k, kbase, p.ks[1], n, p.Dk);
-        fill_rows<IO, DK>(lds + L::kQ, p.q, qbase, p.qs[1], n, p.Dk);
-        if (!L::kShare) fill_cols<IO, DK>(lds + L::kT, p.k, kbase, p.ks[1], n, p.Dk);
-        fill_tri<3>(lds + L::kTri, p.tri + ci * kTriFloats);
-        fill_tri<NP>(lds + L::kP, p.pm + ci * kTriFloats);
-        if (threadIdx.x < kDecFloats / 4)
-            lds[L::kDec + threadIdx.x] = ((const uint4*)(p.dec + ci * kDecFloats))[threadIdx.x];
-        float v[4][4];
+            for (int r = 0; r < 4; ++r) {
+                const int row = tile_row(t, 4 * g + r);
+                S[t][r] = matrix ? (row == col ? 1.f : 0.f)
+                                 : (s && cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f);
+            }
+    }
+    const long long kbase = sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2];
+    const long long qbase = sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2];
+    const long long vbase = sp.b * p.vs[0] + sp.t0 * p.vs[1] + h * p.vs[2] + col;
+    const auto load_k = [&](int ch, int buf) {
+        fill_rows<IO, DK>(lds + L::kK + buf * L::kRows, p.k, kbase + ch * (kChunk * p.ks[1]),
+                          p.ks[1], sp.len - ch * kChunk, p.Dk);
+    };
+    const auto load_rest = [&](int ch) {
+        if (FULL)
+            fill_rows<IO, DK>(lds + L::kQ, p.q, qbase + ch * (kChunk * p.qs[1]), p.qs[1],
+                              sp.len - ch * kChunk, p.Dk);
+        copy_lds(lds + L::kPack, p.pack + ((sp.slot0 + ch) * p.Hv + h) * Op::kPack,
+                 3 * kTriTiles + 1 + (FULL ? NP * kTriTiles : 0));
+    };
+    float v[4][4];
+    const auto load_v = [&](int ch) {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = tile_row(m, 4 * g + r);
-                v[m][r] = cok && row < n
-                              ? io_load<IO>(p.v, sp.b * p.vs[0] + (tok + row) * p.vs[1] +
-                                                     h * p.vs[2] + col)
-                              : 0.f;
+                const int row = ch * kChunk + tile_row(m, 4 * g + r);
+                v[m][r] = !matrix && cok && row < sp.len
+                              ? io_load<IO>(p.v, vbase + row * p.vs[1]) : 0.f;
             }
-        if (p.states && cok) {
-            float* d = p.states + ci * p.Dk * (long long)p.Dv + col;
+    };
+    if (first < last) {
+        load_k(first, 0);
+        load_rest(first);
+        load_v(first);
+    }
+    wait_loads();
+    __syncthreads();
+    int buf = 0;
+    for (int ch = first; ch < last; ++ch) {
+        const long long ci = (sp.slot0 + ch) * p.Hv + h;
+        const bool more = ch + 1 < last;
+        if (L::kBufs == 2 && more) load_k(ch + 1, buf ^ 1);
+        const uint4* Kl = lds + L::kK + buf * L::kRows;
+        if (FULL && p.states && cok) {
+            float* d = p.states + ci * state + col;
 #pragma unroll
             for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -358,24 +413,27 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
                     if (row < p.Dk) d[(long long)row * p.Dv] = S[t][r];
                 }
         }
-        __syncthreads();
         // K S and Q S
         dfloat4 X[4], O[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) X[m] = O[m] = dfloat4{0, 0, 0, 0};
+        const ColScale sc = Op::template scale_of<ST>(S);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            uint4 st[3];
-            split_acc<3>(S[2 * kb], S[2 * kb + 1], st);
+            uint4 st[NB];
+            Op::split(S[2 * kb], S[2 * kb + 1], sc, st);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 uint4 a[NA];
 #pragma unroll
-                for (int i = 0; i < NA; ++i) a[i] = lds[L::kK + ((i * 4 + m) * KB + kb) * 64 + lane];
-                X[m] = mma_terms<3>(a, st, X[m]);
+                for (int i = 0; i < NA; ++i) a[i] = Kl[((i * 4 + m) * KB + kb) * 64 + slot];
+                X[m] = Op::mma(a, st, X[m]);
+                if (FULL) {
 #pragma unroll
-                for (int i = 0; i < NA; ++i) a[i] = lds[L::kQ + ((i * 4 + m) * KB + kb) * 64 + lane];
-                O[m] = mma_terms<NP>(a, st, O[m]);
+                    for (int i = 0; i < NA; ++i)
+                        a[i] = lds[L::kQ + ((i * 4 + m) * KB + kb) * 64 + slot];
+                    O[m] = Op::mma_out(a, st, O[m]);
+                }
             }
         }
         // X = beta o (V - e^G o K S);  O = scale e^G o Q S
@@ -386,8 +444,8 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
             const float ev[4] = {e.x, e.y, e.z, e.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                X[m][r] = bv[r] * (v[m][r] - ev[r] * X[m][r]);
-                O[m][r] = p.scale * ev[r] * O[m][r];
+                X[m][r] = bv[r] * (v[m][r] - ev[r] * (X[m][r] * sc.back));
+                if (FULL) O[m][r] = p.scale * ev[r] * (O[m][r] * sc.back);
             }
         }
         // U = T X
@@ -407,80 +465,167 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
                 U[m] = mma_terms<3>(a, xt, U[m]);
             }
         }
-        if (p.us && cok) {
-            float* d = p.us + ci * kChunk * p.Dv + col;
+        if (FULL) {
+            if (p.us && cok) {
+                float* d = p.us + ci * kChunk * p.Dv + col;
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+                for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = tile_row(m, 4 * g + r);
-                    d[(long long)row * p.Dv] = U[m][r];
-                }
-        }
-        // O += P U
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            uint4 ut[NP];
-            split_acc<NP>(U[2 * kb], U[2 * kb + 1], ut);
-#pragma unroll
-            for (int m = 2 * kb; m < 4; ++m) {
-                uint4 a[NP];
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    a[i] = lds[L::kP + (i * kTriTiles + tri_tile(m, kb)) * 64 + lane];
-                O[m] = mma_terms<NP>(a, ut, O[m]);
+                    for (int r = 0; r < 4; ++r)
+                        d[(long long)tile_row(m, 4 * g + r) * p.Dv] = U[m][r];
             }
-        }
-        if (cok)
+            // O += P U
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int kb = 0; kb < 2; ++kb) {
+                uint4 ut[NP];
+                split_acc<NP>(U[2 * kb], U[2 * kb + 1], ut);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = tile_row(m, 4 * g + r);
-                    if (row < n)
-                        io_store<IO>(p.o, ((sp.b * p.T + tok + row) * p.Hv + h) * p.Dv + col,
-                                     O[m][r]);
+                for (int m = 2 * kb; m < 4; ++m) {
+                    uint4 a[NP];
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        a[i] = lds[L::kP + (i * kTriTiles + tri_tile(m, kb)) * 64 + lane];
+                    O[m] = mma_terms<NP>(a, ut, O[m]);
                 }
-        if (L::kShare) {
-            __syncthreads();
-            fill_cols<IO, DK>(lds + L::kT, p.k, kbase, p.ks[1], n, p.Dk);
-            __syncthreads();
+            }
+            if (cok)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = ch * kChunk + tile_row(m, 4 * g + r);
+                        if (row < sp.len)
+                            io_store<IO>(p.o, ((sp.b * p.T + sp.t0 + row) * p.Hv + h) * p.Dv + col,
+                                         O[m][r]);
+                    }
         }
-        // S = e^Gc S + K^T (e^(Gc-G) o U)
+        // e^(Gc-G) o U
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float4 e = *(const float4*)(dec + 64 + tile_row(m, 4 * g));
+            U[m][0] *= e.x;
+            U[m][1] *= e.y;
+            U[m][2] *= e.z;
+            U[m][3] *= e.w;
+        }
         const float ec = dec[192];
-#pragma unroll
-        for (int t = 0; t < ST; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[t][r] *= ec;
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-            const int row = 32 * tb + 8 * g;
-            const float4 e0 = *(const float4*)(dec + 64 + row);
-            const float4 e1 = *(const float4*)(dec + 68 + row);
-            const float x[8] = {e0.x * U[2 * tb][0],     e0.y * U[2 * tb][1],
-                                e0.z * U[2 * tb][2],     e0.w * U[2 * tb][3],
-                                e1.x * U[2 * tb + 1][0], e1.y * U[2 * tb + 1][1],
-                                e1.z * U[2 * tb + 1][2], e1.w * U[2 * tb + 1][3]};
-            uint4 ut[3];
-            split8<3>(x, ut);
-#pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                uint4 a[NA];
-#pragma unroll
-                for (int i = 0; i < NA; ++i) a[i] = lds[L::kT + ((i * ST + t) * 2 + tb) * 64 + lane];
-                S[t] = mma_terms<3>(a, ut, S[t]);
-            }
+        __syncthreads();          // Q, T, P and the decays are used up
+        if (more) {
+            load_rest(ch + 1);
+            load_v(ch + 1);
         }
+        // S = e^Gc S + K^T U
+        const ColScale su = Op::template scale_of<4>(U);
+        uint4 ut[2][NB];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) Op::split(U[2 * tb], U[2 * tb + 1], su, ut[tb]);
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+            dfloat4 a = {0, 0, 0, 0};
+            if (!Op::kScaled)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a[r] = ec * S[t][r];
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                uint4 x[NA];
+#pragma unroll
+                for (int i = 0; i < NA; ++i) x[i] = read_cols<DK>(Kl + i * 4 * KB * 64, t, tb);
+                a = Op::mma(x, ut[tb], a);
+            }
+            if (Op::kScaled)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a[r] = ec * S[t][r] + su.back * a[r];
+            S[t] = a;
+        }
+        if (L::kBufs == 1) {
+            __syncthreads();
+            if (more) load_k(ch + 1, 0);
+        } else {
+            buf ^= 1;
+        }
+        wait_loads();
         __syncthreads();
     }
-    if (p.fin && cok)
+    if (!cok) return;
+    float* d = nullptr;
+    if (FULL) d = p.fin && last == chunks ? p.fin + (seq * p.Hv + h) * state : nullptr;
+    else if (matrix) d = p.seg_m + (seg * p.Hv + h) * p.Dk * (long long)p.Dk;
+    else d = p.seg_n + (seg * p.Hv + h) * state;
+    if (!d) return;
+#pragma unroll
+    for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = tile_row(t, 4 * g + r);
+            if (row < p.Dk) d[(long long)row * width + col] = S[t][r];
+        }
+}
+
+// Joins the segments of a sequence: with N the last state of a segment from 0
+// and M the matrix of the segment, the state after it is M S + N.  Leaves in
+// place of N the state after each segment but the last.  A wave takes 16
+// columns, as in the walk.
+template <int DK>
+__global__ __launch_bounds__(64) void delta_join_kernel(DeltaParams p) {
+    constexpr int KB = DK / 32, ST = DK / 16;
+    const int cols = (p.Dv + 15) / 16;
+    long long id = blockIdx.x;
+    const int cb = (int)(id % cols);
+    id /= cols;
+    const int h = (int)(id % p.Hv);
+    const long long seq = id / p.Hv;
+    const Span sp = span_of(p, seq);
+    const int chunks = (sp.len + kChunk - 1) / kChunk;
+    const int n = (chunks + p.seg_chunks - 1) / p.seg_chunks;   // segments
+    if (n < 3) return;           // the first segment's state is already whole
+    const int lane = threadIdx.x, c = lane & 15, g = lane >> 4;
+    const int col = cb * 16 + c;
+    const bool cok = col < p.Dv;
+    const long long state = p.Dk * (long long)p.Dv, square = p.Dk * (long long)p.Dk;
+    const long long seg0 = seg_of(p, sp, seq);
+    dfloat4 S[ST];
+    const auto at = [&](long long seg) { return p.seg_n + (seg * p.Hv + h) * state + col; };
+    const float* s = at(seg0);
+#pragma unroll
+    for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = tile_row(t, 4 * g + r);
+            S[t][r] = cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f;
+        }
+    for (int i = 1; i + 1 < n; ++i) {
+        const float* M = p.seg_m + ((seg0 + i) * p.Hv + h) * square;
+        float* d = at(seg0 + i);
+        dfloat4 R[ST];
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = tile_row(t, 4 * g + r);
-                if (row < p.Dk) p.fin[sbase + (long long)row * p.Dv] = S[t][r];
+                R[t][r] = cok && row < p.Dk ? d[(long long)row * p.Dv] : 0.f;
             }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            uint4 b[3];
+            split_acc<3>(S[2 * kb], S[2 * kb + 1], b);
+#pragma unroll
+            for (int t = 0; t < ST; ++t) {
+                const int row = tile_row(t, c), e = 32 * kb + 8 * g;
+                uint4 a[3];
+                load_terms<IO_F32>(M, row * (long long)p.Dk + e, row < p.Dk && e < p.Dk, a);
+                R[t] = mma_terms<3>(a, b, R[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+            S[t] = R[t];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = tile_row(t, 4 * g + r);
+                if (cok && row < p.Dk) d[(long long)row * p.Dv] = R[t][r];
+            }
+        }
+    }
 }
 
 template <int IO>
@@ -493,16 +638,30 @@ hipError_t step_io(const DeltaStepParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int IO, int DK>
-hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
-    const int bytes = ScanLds<IO, DK>::kBytes;
-    const hipError_t e = hipFuncSetAttribute((const void*)delta_scan_kernel<IO, DK>,
+template <int IO, int DK, bool FULL>
+hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
+    const int bytes = ScanLds<IO, DK, FULL>::kBytes;
+    const hipError_t e = hipFuncSetAttribute((const void*)delta_scan_kernel<IO, DK, FULL>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const long long units = p.nseq * p.Hv * ((p.Dv + 63) / 64);
-    hipLaunchKernelGGL((delta_scan_kernel<IO, DK>), dim3((unsigned)xcd_blocks(units)), dim3(256),
-                       bytes, s, p);
+    const int cols = (p.Dv + 63) / 64 + (FULL ? 0 : (p.Dk + 63) / 64);
+    const long long units = p.segs * p.Hv * cols;
+    hipLaunchKernelGGL((delta_scan_kernel<IO, DK, FULL>), dim3((unsigned)xcd_blocks(units)),
+                       dim3(256), bytes, s, p);
     return hipGetLastError();
+}
+
+template <int IO, int DK>
+hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
+    if (p.seg_m) {
+        hipError_t e = scan_launch<IO, DK, false>(p, s);
+        if (e != hipSuccess) return e;
+        const long long joins = p.nseq * p.Hv * ((p.Dv + 15) / 16);
+        hipLaunchKernelGGL((delta_join_kernel<DK>), dim3((unsigned)joins), dim3(64), 0, s, p);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return scan_launch<IO, DK, true>(p, s);
 }
 
 template <int IO>
@@ -516,6 +675,11 @@ hipError_t prep_io(const DeltaParams& p, hipStream_t s) {
 }
 
 }  // namespace
+
+int delta_pack_uint4(int io) {
+    return io == IO_F32 ? Operand<IO_F32>::kPack : Operand<IO_BF16>::kPack;
+}
+int delta_back_pack_uint4() { return kBackPack; }
 
 hipError_t launch_delta_step(int io, const DeltaStepParams& p, hipStream_t s) {
     switch (io) {

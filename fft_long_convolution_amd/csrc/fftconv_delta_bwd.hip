@@ -21,25 +21,21 @@ namespace {
 
 template <int IO, int DK>
 struct RscanLds {
-    static constexpr int NA = IoTerms<IO>::n;
-    // fp32 operands fill the LDS: the transposed queries take the place of
-    // the keys, the transposed keys that of the queries
-    static constexpr bool kShare = NA == 3;
-    static constexpr int kRows = NA * 4 * (DK / 32) * 64;
-    static constexpr int kK = 0, kKt = kShare ? 0 : kRows, kQt = kShare ? kRows : 2 * kRows;
-    static constexpr int kTri = kShare ? 2 * kRows : 3 * kRows;
-    static constexpr int kP = kTri + 3 * kTriTiles * 64;
-    static constexpr int kDec = kP + 3 * kTriTiles * 64;
-    static constexpr int kBytes = (kDec + kDecFloats / 4) * 16;
+    static constexpr int kRows = Operand<IO>::NA * 4 * (DK / 32) * 64;     // uint4
+    static constexpr int kK = 0, kQ = kRows, kPack = 2 * kRows;
+    static constexpr int kTri = kPack, kDec = kTri + 3 * kTriTiles * 64, kP = kDec + 64;
+    static constexpr int kBytes = (kPack + kBackPack) * 16;
 };
 
 // The mirror of the forward walk: a wave owns 16 columns of D and goes
 // through K D, T^T dU and the two transposed products without an exchange.
 template <int IO, int DK>
-__global__ __launch_bounds__(256) void delta_rscan_kernel(DeltaGradParams gp) {
+__global__ __launch_bounds__(256, Operand<IO>::NA == 1 ? 2 : 1)
+void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
+    typedef Operand<IO> Op;
     const DeltaParams& p = gp.f;
-    constexpr int NA = L::NA, KB = DK / 32, ST = DK / 16;
+    constexpr int NA = Op::NA, NB = Op::NB, KB = DK / 32, ST = DK / 16, NO = IoTerms<IO>::n;
     extern __shared__ uint4 lds[];
     const float* dec = (const float*)(lds + L::kDec);
     const int cols = (p.Dv + 63) / 64;
@@ -53,10 +49,12 @@ __global__ __launch_bounds__(256) void delta_rscan_kernel(DeltaGradParams gp) {
     const Span sp = span_of(p, seq);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
+    const int slot = 16 * g + (c ^ (4 * g));             // of a row operand
     const int col = cb * 64 + wave * 16 + c;
     const bool cok = col < p.Dv;
     const int hk = h / p.group;
-    const long long sbase = (seq * p.Hv + h) * p.Dk * (long long)p.Dv + col;
+    const long long state = p.Dk * (long long)p.Dv;
+    const long long sbase = (seq * p.Hv + h) * state + col;
     dfloat4 D[ST];
 #pragma unroll
     for (int t = 0; t < ST; ++t)
@@ -66,31 +64,44 @@ __global__ __launch_bounds__(256) void delta_rscan_kernel(DeltaGradParams gp) {
             D[t][r] = gp.dfin && cok && row < p.Dk ? gp.dfin[sbase + (long long)row * p.Dv] : 0.f;
         }
     const int chunks = (sp.len + kChunk - 1) / kChunk;
-    for (int ch = chunks - 1; ch >= 0; --ch) {
-        const long long tok = sp.t0 + (long long)ch * kChunk;
-        const int left = sp.len - ch * kChunk, n = left < kChunk ? left : kChunk;
-        const long long ci = (sp.slot0 + ch) * p.Hv + h;
-        const long long kbase = sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2];
-        const long long qbase = sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2];
-        fill_rows<IO, DK>(lds + L::kK, p.k, kbase, p.ks[1], n, p.Dk);
-        fill_cols<IO, DK>(lds + L::kQt, p.q, qbase, p.qs[1], n, p.Dk);
-        if (!L::kShare) fill_cols<IO, DK>(lds + L::kKt, p.k, kbase, p.ks[1], n, p.Dk);
-        fill_tri<3>(lds + L::kTri, p.trit + ci * kTriFloats);
-        fill_tri<3>(lds + L::kP, p.pmt + ci * kTriFloats);
-        if (threadIdx.x < kDecFloats / 4)
-            lds[L::kDec + threadIdx.x] = ((const uint4*)(p.dec + ci * kDecFloats))[threadIdx.x];
-        const long long obase = ((sp.b * p.T + tok) * p.Hv + h) * p.Dv + col;
-        dfloat4 dO[4];
+    const long long kbase = sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2];
+    const long long qbase = sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2];
+    const long long obase = ((sp.b * p.T + sp.t0) * p.Hv + h) * p.Dv + col;
+    const long long ostride = (long long)p.Hv * p.Dv;
+    const auto load_rows = [&](int ch) {
+        fill_rows<IO, DK>(lds + L::kK, p.k, kbase + ch * (kChunk * p.ks[1]), p.ks[1],
+                          sp.len - ch * kChunk, p.Dk);
+        fill_rows<IO, DK>(lds + L::kQ, p.q, qbase + ch * (kChunk * p.qs[1]), p.qs[1],
+                          sp.len - ch * kChunk, p.Dk);
+    };
+    const auto load_pack = [&](int ch) {
+        copy_lds(lds + L::kPack, p.bpack + ((sp.slot0 + ch) * p.Hv + h) * kBackPack,
+                 kBackPack / 64);
+    };
+    dfloat4 dN[4];                       // dO of the next chunk
+    const auto load_do = [&](int ch) {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = tile_row(m, 4 * g + r);
-                dO[m][r] = cok && row < n
-                               ? io_load<IO>(gp.dout, obase + (long long)row * p.Hv * p.Dv) : 0.f;
+                const int row = ch * kChunk + tile_row(m, 4 * g + r);
+                dN[m][r] = cok && row < sp.len ? io_load<IO>(gp.dout, obase + row * ostride) : 0.f;
             }
+    };
+    if (chunks > 0) {
+        load_rows(chunks - 1);
+        load_pack(chunks - 1);
+        load_do(chunks - 1);
+    }
+    wait_loads();
+    __syncthreads();
+    for (int ch = chunks - 1; ch >= 0; --ch) {
+        const long long ci = (sp.slot0 + ch) * p.Hv + h;
+        dfloat4 dO[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) dO[m] = dN[m];
         if (cok) {
-            float* d = gp.dstates + ci * p.Dk * (long long)p.Dv + col;
+            float* d = gp.dstates + ci * state + col;
 #pragma unroll
             for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -99,35 +110,38 @@ __global__ __launch_bounds__(256) void delta_rscan_kernel(DeltaGradParams gp) {
                     if (row < p.Dk) d[(long long)row * p.Dv] = D[t][r];
                 }
         }
-        __syncthreads();
         // dU = e^(Gc-G) o K D + P^T dO
         dfloat4 dU[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dU[m] = dfloat4{0, 0, 0, 0};
+        {
+            const ColScale sc = Op::template scale_of<ST>(D);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            uint4 dt[3];
-            split_acc<3>(D[2 * kb], D[2 * kb + 1], dt);
+            for (int kb = 0; kb < KB; ++kb) {
+                uint4 dt[NB];
+                Op::split(D[2 * kb], D[2 * kb + 1], sc, dt);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    uint4 a[NA];
+#pragma unroll
+                    for (int i = 0; i < NA; ++i)
+                        a[i] = lds[L::kK + ((i * 4 + m) * KB + kb) * 64 + slot];
+                    dU[m] = Op::mma(a, dt, dU[m]);
+                }
+            }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                uint4 a[NA];
-#pragma unroll
-                for (int i = 0; i < NA; ++i) a[i] = lds[L::kK + ((i * 4 + m) * KB + kb) * 64 + lane];
-                dU[m] = mma_terms<3>(a, dt, dU[m]);
+                const float4 e = *(const float4*)(dec + 64 + tile_row(m, 4 * g));
+                dU[m][0] *= e.x * sc.back;
+                dU[m][1] *= e.y * sc.back;
+                dU[m][2] *= e.z * sc.back;
+                dU[m][3] *= e.w * sc.back;
             }
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const float4 e = *(const float4*)(dec + 64 + tile_row(m, 4 * g));
-            dU[m][0] *= e.x;
-            dU[m][1] *= e.y;
-            dU[m][2] *= e.z;
-            dU[m][3] *= e.w;
-        }
-#pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            uint4 ot[NA];
-            split_acc<NA>(dO[2 * kb], dO[2 * kb + 1], ot);
+            uint4 ot[NO];
+            split_acc<NO>(dO[2 * kb], dO[2 * kb + 1], ot);
 #pragma unroll
             for (int m = 0; m < 2 * kb + 2; ++m) {
                 uint4 a[3];
@@ -165,40 +179,53 @@ __global__ __launch_bounds__(256) void delta_rscan_kernel(DeltaGradParams gp) {
             for (int r = 0; r < 4; ++r) {
                 if (cok) yd[(long long)(r0 + r) * p.Dv] = dY[m][r];
                 const float dx = bv[r] * dY[m][r];
-                if (cok && r0 + r < n)
-                    io_store<IO>(gp.dv, obase + (long long)(r0 + r) * p.Hv * p.Dv, dx);
+                const int row = ch * kChunk + r0 + r;
+                if (cok && row < sp.len) io_store<IO>(gp.dv, obase + row * ostride, dx);
                 dY[m][r] = -ev[r] * dx;
                 dO[m][r] *= p.scale * ev[r];
             }
         }
-        if (L::kShare) {
-            __syncthreads();
-            fill_cols<IO, DK>(lds + L::kKt, p.k, kbase, p.ks[1], n, p.Dk);
-            __syncthreads();
-        }
         const float ec = dec[192];
-#pragma unroll
-        for (int t = 0; t < ST; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) D[t][r] *= ec;
+        __syncthreads();              // T, P and the decays are used up
+        if (ch > 0) {
+            load_pack(ch - 1);
+            load_do(ch - 1);
+        }
+        const ColScale sy = Op::template scale_of<4>(dY), so = Op::template scale_of<4>(dO);
+        uint4 yt[2][NB], ot[2][NB];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            uint4 yt[3], ot[3];
-            split_acc<3>(dY[2 * tb], dY[2 * tb + 1], yt);
-            split_acc<3>(dO[2 * tb], dO[2 * tb + 1], ot);
-#pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                uint4 a[NA];
-#pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    a[i] = lds[L::kKt + ((i * ST + t) * 2 + tb) * 64 + lane];
-                D[t] = mma_terms<3>(a, yt, D[t]);
-#pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    a[i] = lds[L::kQt + ((i * ST + t) * 2 + tb) * 64 + lane];
-                D[t] = mma_terms<3>(a, ot, D[t]);
-            }
+            Op::split(dY[2 * tb], dY[2 * tb + 1], sy, yt[tb]);
+            Op::split(dO[2 * tb], dO[2 * tb + 1], so, ot[tb]);
         }
+#pragma unroll
+        for (int t = 0; t < ST; ++t) {
+            dfloat4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+            if (!Op::kScaled)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a[r] = ec * D[t][r];
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                uint4 x[NA];
+#pragma unroll
+                for (int i = 0; i < NA; ++i)
+                    x[i] = read_cols<DK>(lds + L::kK + i * 4 * KB * 64, t, tb);
+                a = Op::mma(x, yt[tb], a);
+#pragma unroll
+                for (int i = 0; i < NA; ++i)
+                    x[i] = read_cols<DK>(lds + L::kQ + i * 4 * KB * 64, t, tb);
+                b = Op::mma(x, ot[tb], b);
+            }
+            if (Op::kScaled)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    D[t][r] = ec * D[t][r] + (sy.back * a[r] + so.back * b[r]);
+            else
+                D[t] = a + b;
+        }
+        __syncthreads();
+        if (ch > 0) load_rows(ch - 1);
+        wait_loads();
         __syncthreads();
     }
     if (gp.dinit && cok)
@@ -213,44 +240,46 @@ __global__ __launch_bounds__(256) void delta_rscan_kernel(DeltaGradParams gp) {
 
 // ------------------------------------------------ the gradients of a chunk
 
-// LDS of delta_grads_kernel.  The slices of S0, D and U (32 columns, three
-// terms) and the transposed keys and queries are never live together.
+// LDS of delta_grads_kernel, in uint4.  The slices of S0, D and U (32
+// columns, three terms) are used up before the keys, queries and the 64 x 64
+// matrices take their place.
 template <int IO, int DK>
 struct GradsLds {
-    static constexpr int NA = IoTerms<IO>::n;
     static constexpr int ST = DK / 16;
-    static constexpr int kS = 0, kD = 3 * ST * 64, kU = 2 * kD;   // uint4
-    static constexpr int kSlices = kU + 3 * 4 * 64;
-    static constexpr int kKt = 0, kQt = NA * ST * 2 * 64, kCols = 2 * kQt;
-    static constexpr int kBig = kSlices > kCols ? kSlices : kCols;
-    static constexpr int kW = kBig, kF = kW + kChunk * kLd / 4;
-    static constexpr int kBytes = (kF + kChunk * kLd / 4) * 16;
+    static constexpr int kS = 0, kD = 3 * ST * 64, kU = 2 * kD, kSlices = kU + 3 * 4 * 64;
+    static constexpr int kRows = Operand<IO>::NA * 4 * (DK / 32) * 64;
+    static constexpr int kK = 0, kQ = kRows, kW = 2 * kRows, kF = kW + kChunk * kLd / 4;
+    static constexpr int kTail = kF + kChunk * kLd / 4;
+    static constexpr int kBytes = (kSlices > kTail ? kSlices : kTail) * 16;
 };
 
-// eight consecutive fp32 values as three terms
-__device__ __forceinline__ void load_f32_terms(const float* p, bool ok, uint4 (&t)[3]) {
-    load_terms<IO_F32>(p, 0, ok, t);
+// Sum over the four groups of 16 lanes.
+__device__ __forceinline__ float sum_groups(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
 }
 
-// One workgroup per chunk and key head; a wave owns 16 tokens.  The value
-// heads that share the key head follow one another and their parts of dQ and
-// dK are summed in registers, in a fixed order.
+// One workgroup per chunk and key head; a wave owns 16 tokens as the columns
+// of its products, R^T = S0 dO^T and so on, so a lane has one token: what
+// belongs to it (decays, row sums) is a scalar of the lane, and sums over a
+// head's elements are sums in the lane and over four groups.  The value heads
+// that share the key head follow one another, and their parts of dQ and dK
+// are summed in registers, in a fixed order.
 template <int IO, int DK>
 __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
     typedef GradsLds<IO, DK> L;
+    typedef Operand<IO> Op;
     const DeltaParams& p = gp.f;
-    constexpr int NA = L::NA, KB = DK / 32, ST = L::ST;
-    constexpr int NW = NA == 3 ? 3 : 2;      // terms of W and E
+    constexpr int NA = Op::NA, NB = Op::NB, NO = IoTerms<IO>::n, KB = DK / 32, ST = L::ST;
     extern __shared__ uint4 lds[];
     __shared__ double G[kChunk];
-    __shared__ float bet[kChunk], colsum[4][kChunk], rowG[kChunk], rowB[kChunk];
-    __shared__ float rowV[kChunk], red[4], red3[4];
+    __shared__ float bet[kChunk], colsum[4][kChunk], rowG[kChunk], rowB[kChunk], red[4], red3[4];
     const long long units = p.slots * p.Hk;
     const long long id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
     const long long slot = id / p.Hk;
     const int hk = (int)(id - slot * p.Hk);
-    const long long seq = seq_of(p, slot);
+    const long long seq = seq_of(p, slot, 1);
     const Span sp = span_of(p, seq);
     const long long at = (slot - sp.slot0) * kChunk;
     if (at < 0 || at >= sp.len) return;
@@ -260,29 +289,30 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
     const int c = lane & 15, g = lane >> 4;
     const long long kbase = sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2];
     const long long qbase = sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2];
-    const int arow = 16 * wave + c;          // the lane's token in A operands
-    float (*W)[kLd] = (float (*)[kLd])(lds + L::kW);
-    float (*F)[kLd] = (float (*)[kLd])(lds + L::kF);
+    const int mine = 16 * wave + c;          // the lane's token
+    const int jtiles = wave < 2 ? 2 : 4;     // tiles of tokens up to the wave's
+    float (*W)[kLd] = (float (*)[kLd])(lds + L::kW);   // [j][i]: W_ij
+    float (*F)[kLd] = (float (*)[kLd])(lds + L::kF);   // E + E^T
 
-    // scores of the wave's tokens against those up to them
+    // q.k and k.k of the lane's token with those of tile j
     dfloat4 kk[4], qk[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) kk[j] = qk[j] = dfloat4{0, 0, 0, 0};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
         const int e = 32 * kb + 8 * g;
-        uint4 ka[NA], qa[NA];
-        const bool ok = arow < n && e < p.Dk;
-        load_terms<IO>(p.k, kbase + arow * p.ks[1] + e, ok, ka);
-        load_terms<IO>(p.q, qbase + arow * p.qs[1] + e, ok, qa);
+        uint4 kb_[NO], qb_[NO];
+        const bool ok = mine < n && e < p.Dk;
+        load_terms<IO>(p.k, kbase + mine * p.ks[1] + e, ok, kb_);
+        load_terms<IO>(p.q, qbase + mine * p.qs[1] + e, ok, qb_);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (j <= wave) {
-                uint4 b[NA];
-                const int col = 16 * j + c;
-                load_terms<IO>(p.k, kbase + col * p.ks[1] + e, col < n && e < p.Dk, b);
-                kk[j] = mma_terms<3>(ka, b, kk[j]);
-                qk[j] = mma_terms<3>(qa, b, qk[j]);
+            if (j < jtiles) {
+                uint4 a[NO];
+                const int row = tile_row(j, c);
+                load_terms<IO>(p.k, kbase + row * p.ks[1] + e, row < n && e < p.Dk, a);
+                kk[j] = mma_terms<3>(a, kb_, kk[j]);
+                qk[j] = mma_terms<3>(a, qb_, qk[j]);
             }
     }
     dfloat4 dQ[ST], dK[ST];
@@ -311,15 +341,16 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
         for (int d0 = 0; d0 < p.Dv; d0 += 32) {
             const int e = d0 + 8 * g;
             __syncthreads();
-            // B operands: tile t, lane (g, c) holds [16 t + c][d0 + 8 g + i]
+            // A operands: tile t, lane (g, c) holds [tile_row(t, c)][d0 + 8 g + i]
+#pragma unroll
             for (int i = threadIdx.x; i < ST * 64; i += 256) {
-                const int row = 16 * (i >> 6) + (i & 15), el = d0 + 8 * ((i >> 4) & 3);
+                const int row = tile_row(i >> 6, i & 15), el = d0 + 8 * ((i >> 4) & 3);
                 const bool ok = row < p.Dk && el < p.Dv;
                 const float* s = S0 + (long long)row * p.Dv + el;
                 const float* d = D + (long long)row * p.Dv + el;
                 uint4 ts[3], td[3];
-                load_f32_terms(s, ok, ts);
-                load_f32_terms(d, ok, td);
+                load_terms<IO_F32>(s, 0, ok, ts);
+                load_terms<IO_F32>(d, 0, ok, td);
                 if (ok)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sd += s[j] * d[j];
@@ -331,135 +362,122 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
             }
             {
                 const int i = threadIdx.x;
-                const int row = 16 * (i >> 6) + (i & 15), el = d0 + 8 * ((i >> 4) & 3);
+                const int row = tile_row(i >> 6, i & 15), el = d0 + 8 * ((i >> 4) & 3);
                 uint4 tu[3];
-                load_f32_terms(U + (long long)row * p.Dv + el, el < p.Dv, tu);
+                load_terms<IO_F32>(U, (long long)row * p.Dv + el, el < p.Dv, tu);
 #pragma unroll
                 for (int j = 0; j < 3; ++j) lds[L::kU + j * 256 + i] = tu[j];
             }
-            // A operands of the wave's tokens
-            uint4 oa[NA], ya[3], ua[3];
-            load_terms<IO>(gp.dout, ((sp.b * p.T + tok + arow) * p.Hv + h) * p.Dv + e,
-                           arow < n && e < p.Dv, oa);
-            const float* yp = Y + (long long)arow * p.Dv + e;
-            load_f32_terms(yp, e < p.Dv, ya);
-            load_f32_terms(U + (long long)arow * p.Dv + e, e < p.Dv, ua);
-            if (arow < n && e < p.Dv) {
-                const long long vi = sp.b * p.vs[0] + (tok + arow) * p.vs[1] + h * p.vs[2] + e;
+            // B operands: columns of the wave's tokens
+            uint4 ob[NO], yb[3], ub[3];
+            const bool ok = mine < n && e < p.Dv;
+            load_terms<IO>(gp.dout, ((sp.b * p.T + tok + mine) * p.Hv + h) * p.Dv + e, ok, ob);
+            const float* yp = Y + (long long)mine * p.Dv + e;
+            load_terms<IO_F32>(yp, 0, e < p.Dv, yb);
+            load_terms<IO_F32>(U, (long long)mine * p.Dv + e, e < p.Dv, ub);
+            if (ok) {
+                const long long vi = sp.b * p.vs[0] + (tok + mine) * p.vs[1] + h * p.vs[2] + e;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) yv += yp[j] * io_load<IO>(p.v, vi + j);
             }
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < ST; ++t) {
-                uint4 b[3];
+                uint4 a[3];
 #pragma unroll
-                for (int j = 0; j < 3; ++j) b[j] = lds[L::kS + (j * ST + t) * 64 + lane];
-                R1[t] = mma_terms<3>(oa, b, R1[t]);
-                R2[t] = mma_terms<3>(ya, b, R2[t]);
+                for (int j = 0; j < 3; ++j) a[j] = lds[L::kS + (j * ST + t) * 64 + lane];
+                R1[t] = mma_terms<3>(a, ob, R1[t]);
+                R2[t] = mma_terms<3>(a, yb, R2[t]);
 #pragma unroll
-                for (int j = 0; j < 3; ++j) b[j] = lds[L::kD + (j * ST + t) * 64 + lane];
-                R3[t] = mma_terms<3>(ua, b, R3[t]);
+                for (int j = 0; j < 3; ++j) a[j] = lds[L::kD + (j * ST + t) * 64 + lane];
+                R3[t] = mma_terms<3>(a, ub, R3[t]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j <= wave) {
-                    uint4 b[3];
+                if (j < jtiles) {
+                    uint4 a[3];
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) b[i] = lds[L::kU + i * 256 + j * 64 + lane];
-                    Dp[j] = mma_terms<3>(oa, b, Dp[j]);
-                    Dy[j] = mma_terms<3>(ya, b, Dy[j]);
+                    for (int i = 0; i < 3; ++i) a[i] = lds[L::kU + i * 256 + j * 64 + lane];
+                    Dp[j] = mma_terms<3>(a, ob, Dp[j]);
+                    Dy[j] = mma_terms<3>(a, yb, Dy[j]);
                 }
         }
         __syncthreads();
-        // transposed keys and queries take the slices' place
-        fill_cols<IO, DK>(lds + L::kKt, p.k, kbase, p.ks[1], n, p.Dk);
-        fill_cols<IO, DK>(lds + L::kQt, p.q, qbase, p.qs[1], n, p.Dk);
-        // <S0, D>, and dY.V of the lane's token
+        // keys and queries take the slices' place
+        fill_rows<IO, DK>(lds + L::kK, p.k, kbase, p.ks[1], n, p.Dk);
+        fill_rows<IO, DK>(lds + L::kQ, p.q, qbase, p.qs[1], n, p.Dk);
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) sd += __shfl_xor(sd, m);
-        if (lane == 0) red[wave] = sd;
+        yv = sum_groups(yv);
+        const double last = G[kChunk - 1], Gi = G[mine];
+        const float eg = expf((float)Gi), ee = expf((float)(last - Gi)), b = bet[mine];
+        // sums over the elements of a head
+        float s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-        for (int m = 16; m < 64; m <<= 1) yv += __shfl_xor(yv, m);
-        if (g == 0) rowV[arow] = yv;
-        const double last = G[kChunk - 1];
-        // sums over the elements of a head: rows 16 wave + 4 g + r
-        float a1[4], a2[4], a3[4];
+        for (int t = 0; t < ST; ++t) {
+            const int el = tile_row(t, 4 * g);
+            const bool ok = mine < n && el < p.Dk;
+            float qv[4], kv[4];
+            load4<IO>(p.q, qbase + mine * p.qs[1] + el, ok, qv);
+            load4<IO>(p.k, kbase + mine * p.ks[1] + el, ok, kv);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 16 * wave + 4 * g + r;
-            const double Gr = G[row];
-            const float eg = expf((float)Gr), ee = expf((float)(last - Gr)), b = bet[row];
-            float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                const int el = 16 * t + c;
-                const bool ok = row < n && el < p.Dk;
-                const float qv = ok ? io_load<IO>(p.q, qbase + row * p.qs[1] + el) : 0.f;
-                const float kv = ok ? io_load<IO>(p.k, kbase + row * p.ks[1] + el) : 0.f;
-                s1 += qv * R1[t][r];
-                s2 += kv * R2[t][r];
-                s3 += kv * R3[t][r];
+            for (int r = 0; r < 4; ++r) {
+                s1 += qv[r] * R1[t][r];
+                s2 += kv[r] * R2[t][r];
+                s3 += kv[r] * R3[t][r];
                 dQ[t][r] += p.scale * eg * R1[t][r];
                 dK[t][r] += ee * R3[t][r] - b * eg * R2[t][r];
             }
-#pragma unroll
-            for (int m = 1; m < 16; m <<= 1) {
-                s1 += __shfl_xor(s1, m);
-                s2 += __shfl_xor(s2, m);
-                s3 += __shfl_xor(s3, m);
-            }
-            a1[r] = p.scale * eg * s1;
-            a2[r] = eg * s2;
-            a3[r] = ee * s3;
         }
-        // the 64 x 64 part
-        float cs[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 16 * wave + 4 * g + r;
-            const double Gr = G[row];
-            const float b = bet[row];
-            float sg = 0.f, sb = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = 16 * j + c;
-                float w = 0.f, f = 0.f;
-                if (row >= col) {
-                    const float gam = expf((float)(Gr - G[col]));
-                    w = p.scale * gam * Dp[j][r];
-                    const float x = row > col ? gam * Dy[j][r] : 0.f;
-                    f = -b * x;
-                    const float t = w * qk[j][r] + f * kk[j][r];
-                    sg += t;
-                    cs[j] += t;
-                    sb -= x * kk[j][r];
-                    if (row > col) F[col][row] = f;
-                }
-                if (row >= col) F[row][col] = f;
-                W[row][col] = w;
-            }
-#pragma unroll
-            for (int m = 1; m < 16; m <<= 1) {
-                sg += __shfl_xor(sg, m);
-                sb += __shfl_xor(sb, m);
-            }
-            if (c == 0) {
-                rowG[row] = sg + a1[r] - b * a2[r] - a3[r];
-                rowB[row] = sb - a2[r];
-            }
-        }
+        s1 = p.scale * eg * sum_groups(s1);
+        s2 = eg * sum_groups(s2);
+        s3 = ee * sum_groups(s3);
+        // the 64 x 64 part: the lane's token is i, tile j's row 4 g + r is j
+        float sg = 0.f, sb = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const int j0 = tile_row(j, 4 * g);
+            float cs[4];
 #pragma unroll
-            for (int m = 16; m < 64; m <<= 1) cs[j] += __shfl_xor(cs[j], m);
-            if (g == 0) colsum[wave][16 * j + c] = cs[j];
+            for (int r = 0; r < 4; ++r) {
+                float w = 0.f, f = 0.f, t = 0.f;
+                if (j < jtiles && mine >= j0 + r) {
+                    const float gam = expf((float)(Gi - G[j0 + r]));
+                    w = p.scale * gam * Dp[j][r];
+                    const float x = mine > j0 + r ? gam * Dy[j][r] : 0.f;
+                    f = -b * x;
+                    t = w * qk[j][r] + f * kk[j][r];
+                    sg += t;
+                    sb -= x * kk[j][r];
+                    F[mine][j0 + r] = f;
+                    if (mine > j0 + r) F[j0 + r][mine] = f;
+                }
+                W[j0 + r][mine] = w;
+                Dp[j][r] = w;                 // the lane's row of W
+                cs[r] = t;
+            }
+            // sums over the wave's tokens
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1) cs[r] += __shfl_xor(cs[r], m);
+                if (c == 0) colsum[wave][j0 + r] = cs[r];
+            }
         }
-        // the chunk's last decay: sum of a3 over all tokens
-        float s3 = c == 0 ? a3[0] + a3[1] + a3[2] + a3[3] : 0.f;
+        sg = sum_groups(sg);
+        sb = sum_groups(sb);
+        if (g == 0) {
+            rowG[mine] = sg + s1 - b * s2 - s3;
+            rowB[mine] = yv + sb - s2;
+        }
+        // the chunk's last decay
 #pragma unroll
-        for (int m = 16; m < 64; m <<= 1) s3 += __shfl_xor(s3, m);
-        if (lane == 0) red3[wave] = s3;
+        for (int m = 1; m < 16; m <<= 1) s3 += __shfl_xor(s3, m);
+        if (lane == 0) {
+            red[wave] = sd;
+            red3[wave] = s3;
+        }
+        wait_loads();
         __syncthreads();
         if (wave == 0) {
             double x = (double)rowG[lane] - (colsum[0][lane] + colsum[1][lane] +
@@ -478,54 +496,56 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
                 // a factor of 0 has the gradient 0, which the difference of
                 // sums above meets only up to their rounding
                 gp.dg[gi] = expf(p.g[gi]) == 0.f ? 0.f : (float)x;
-                gp.dbeta[gi] = rowV[lane] + rowB[lane];
+                gp.dbeta[gi] = rowB[lane];
             }
         }
-        // dQ += W K, dK += W^T Q + F K
+        // dQ^T += K^T W^T, dK^T += Q^T W + K^T F
+        dfloat4 wt[4], ft[4];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            const int e = 32 * kb + 8 * g;
-            float x[8];
-            uint4 wa[NW], wt[NW], fa[NW];
+        for (int m = 0; m < 4; ++m) {
+            wt[m] = *(const dfloat4*)&W[mine][tile_row(m, 4 * g)];
+            ft[m] = *(const dfloat4*)&F[mine][tile_row(m, 4 * g)];
+        }
+        const ColScale sw = Op::template scale_of<4>(Dp), st = Op::template scale_of<4>(wt),
+                       sf = Op::template scale_of<4>(ft);
+        uint4 wb[2][NB], tb_[2][NB], fb[2][NB];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = W[arow][e + i];
-            split8<NW>(x, wa);
+        for (int tb = 0; tb < 2; ++tb) {
+            Op::split(Dp[2 * tb], Dp[2 * tb + 1], sw, wb[tb]);
+            Op::split(wt[2 * tb], wt[2 * tb + 1], st, tb_[tb]);
+            Op::split(ft[2 * tb], ft[2 * tb + 1], sf, fb[tb]);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = W[e + i][arow];
-            split8<NW>(x, wt);
+        for (int t = 0; t < ST; ++t) {
+            dfloat4 a = {0, 0, 0, 0}, x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = F[arow][e + i];
-            split8<NW>(x, fa);
+            for (int tb = 0; tb < 2; ++tb) {
+                uint4 kt[NA], qt[NA];
 #pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                // the lane's column of tile t is element 16 t + c
-                const int el = 16 * t + c;
-                const int tile = 2 * (el >> 5) + ((el >> 2) & 1);
-                const int row = 4 * ((el >> 3) & 3) + (el & 3);
-                uint4 b[NA];
+                for (int i = 0; i < NA; ++i) {
+                    kt[i] = read_cols<DK>(lds + L::kK + i * 4 * KB * 64, t, tb);
+                    qt[i] = read_cols<DK>(lds + L::kQ + i * 4 * KB * 64, t, tb);
+                }
+                a = Op::mma_out(kt, wb[tb], a);
+                x = Op::mma_out(qt, tb_[tb], x);
+                y = Op::mma_out(kt, fb[tb], y);
+            }
 #pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    b[i] = lds[L::kKt + ((i * ST + tile) * 2 + kb) * 64 + 16 * g + row];
-                dQ[t] = mma_terms<NW>(wa, b, dQ[t]);
-                dK[t] = mma_terms<NW>(fa, b, dK[t]);
-#pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    b[i] = lds[L::kQt + ((i * ST + tile) * 2 + kb) * 64 + 16 * g + row];
-                dK[t] = mma_terms<NW>(wt, b, dK[t]);
+            for (int r = 0; r < 4; ++r) {
+                dQ[t][r] += sw.back * a[r];
+                dK[t][r] += st.back * x[r] + sf.back * y[r];
             }
         }
     }
+    if (mine >= n) return;
+    const long long o = ((sp.b * p.T + tok + mine) * p.Hk + hk) * p.Dk;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int row = 16 * wave + 4 * g + r;
-        if (row >= n) continue;
-        const long long o = ((sp.b * p.T + tok + row) * p.Hk + hk) * p.Dk;
-#pragma unroll
-        for (int t = 0; t < ST; ++t)
-            if (16 * t + c < p.Dk) {
-                io_store<IO>(gp.dq, o + 16 * t + c, dQ[t][r]);
-                io_store<IO>(gp.dk, o + 16 * t + c, dK[t][r]);
-            }
+    for (int t = 0; t < ST; ++t) {
+        const int el = tile_row(t, 4 * g);
+        if (el < p.Dk) {
+            store4<IO>(gp.dq, o + el, dQ[t]);
+            store4<IO>(gp.dk, o + el, dK[t]);
+        }
     }
 }
 

@@ -66,15 +66,26 @@ __device__ __forceinline__ Span span_of(const DeltaParams& p, long long i) {
     }
     return s;
 }
-// the sequence whose chunk a slot is (its span may end before the slot)
-__device__ __forceinline__ long long seq_of(const DeltaParams& p, long long slot) {
-    if (!p.cu) return slot / p.nch;
+// index of the first segment (of L chunks; L = 1: chunk) of a sequence
+__device__ __forceinline__ long long seg_first(long long t0, long long i, long long nch, long long L,
+                                               bool packed) {
+    return packed ? t0 / (kChunk * L) + i : i * (nch ? (nch + L - 1) / L : 1);
+}
+__device__ __forceinline__ long long seg_of(const DeltaParams& p, const Span& s, long long i) {
+    return seg_first(s.t0, i, p.nch, p.seg_chunks, p.cu != nullptr);
+}
+// the sequence whose segment (of L chunks) number `seg` is; its span may end
+// before the segment
+__device__ __forceinline__ long long seq_of(const DeltaParams& p, long long seg, long long L) {
+    if (!p.cu) {
+        return seg / (p.nch ? (p.nch + L - 1) / L : 1);
+    }
     long long lo = 0, hi = p.nseq - 1;
     while (lo < hi) {
         const long long mid = (lo + hi + 1) / 2;
         long long a = p.cu[mid];
         a = a < 0 ? 0 : a > p.T ? p.T : a;
-        if (a / kChunk + mid <= slot) lo = mid; else hi = mid - 1;
+        if (a / (kChunk * L) + mid <= seg) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
@@ -90,6 +101,42 @@ __device__ __forceinline__ void io_store(void* p, long long i, float x) {
     if constexpr (IO == IO_F32) ((float*)p)[i] = x;
     else if constexpr (IO == IO_F16) ((_Float16*)p)[i] = (_Float16)x;
     else ((__bf16*)p)[i] = (__bf16)x;
+}
+
+// four consecutive elements (the place a multiple of four)
+template <int IO>
+__device__ __forceinline__ void load4(const void* p, long long i, bool ok, float (&x)[4]) {
+    if constexpr (IO == IO_F32) {
+        const float4 a = ok ? *(const float4*)((const float*)p + i) : make_float4(0, 0, 0, 0);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    } else {
+        const uint2 a = ok ? *(const uint2*)((const uint16_t*)p + i) : make_uint2(0, 0);
+        const uint32_t u[2] = {a.x, a.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (IO == IO_BF16) {
+                x[2 * j] = __uint_as_float(u[j] << 16);
+                x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+            } else {
+                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+                const h2 h = __builtin_bit_cast(h2, u[j]);
+                x[2 * j] = (float)h.x;
+                x[2 * j + 1] = (float)h.y;
+            }
+        }
+    }
+}
+template <int IO>
+__device__ __forceinline__ void store4(void* p, long long i, dfloat4 x) {
+    if constexpr (IO == IO_F32) {
+        *(float4*)((float*)p + i) = make_float4(x[0], x[1], x[2], x[3]);
+    } else if constexpr (IO == IO_BF16) {
+        __bf16 h[4] = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+        *(uint2*)((uint16_t*)p + i) = __builtin_bit_cast(uint2, h);
+    } else {
+        _Float16 h[4] = {(_Float16)x[0], (_Float16)x[1], (_Float16)x[2], (_Float16)x[3]};
+        *(uint2*)((uint16_t*)p + i) = __builtin_bit_cast(uint2, h);
+    }
 }
 
 // the upper halves of a and b, a in the low one
@@ -165,79 +212,142 @@ __device__ __forceinline__ void load_terms(const void* p, long long i, bool ok,
     }
 }
 
-// The 8 x 8 transpose of 16-bit elements held as rows of eight.
-__device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&c)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t ra[4] = {r[2 * i].x, r[2 * i].y, r[2 * i].z, r[2 * i].w};
-            const uint32_t rb[4] = {r[2 * i + 1].x, r[2 * i + 1].y, r[2 * i + 1].z,
-                                    r[2 * i + 1].w};
-            w[i] = __builtin_amdgcn_perm(rb[j >> 1], ra[j >> 1],
-                                         (j & 1) ? 0x07060302u : 0x05040100u);
-        }
-        c[j] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+// Where lanes without an element read from.
+static __device__ __align__(16) uint32_t kNothing[4] = {0, 0, 0, 0};
+
+// 16 bytes a lane from global memory to LDS, to consecutive places from `dst`
+// (the same for the wave) on, without passing through registers.
+__device__ __forceinline__ void dma16(uint4* dst, const void* src) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                     (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+// The wave's loads, those to LDS among them, are done.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// `kb` KiB from global memory to LDS by the four waves.
+__device__ __forceinline__ void copy_lds(uint4* dst, const uint4* src, int kb) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    for (int i = wave; i < kb; i += 4) dma16(dst + i * 64, src + i * 64 + lane);
 }
 
-// Fills the A operands of 64 tokens x DK of a head in LDS: tile (m, kb),
-// lane (g, c) holds [token tile_row(m, c)][32 kb + 8 g + i].
+// Fills the A operands of 64 tokens x DK of a head in LDS.  Tile (m, kb),
+// place 16 g + (c ^ 4 g) holds [token tile_row(m, c)][32 kb + 8 g + i], i < 8;
+// the exclusive or spreads the four groups over the banks for the transposed
+// reads.  Tokens from n on and elements from Dk on are 0.
 template <int IO, int DK>
 __device__ __forceinline__ void fill_rows(uint4* dst, const void* src, long long base,
                                           long long stride, int n, int Dk) {
-    constexpr int NA = IoTerms<IO>::n, KB = DK / 32;
-    for (int i = threadIdx.x; i < 4 * KB * 64; i += 256) {
-        const int tile = i >> 6, l = i & 63;
-        const int m = tile / KB, kb = tile - m * KB;
-        const int row = tile_row(m, l & 15), e = 32 * kb + 8 * (l >> 4);
-        uint4 t[NA];
-        load_terms<IO>(src, base + row * stride + e, row < n && e < Dk, t);
+    constexpr int KB = DK / 32, kTiles = 4 * KB;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int g = lane >> 4, c = (lane & 15) ^ (4 * g);
 #pragma unroll
-        for (int a = 0; a < NA; ++a) dst[a * 4 * KB * 64 + i] = t[a];
-    }
-}
-// The same tokens' transpose: tile (t, tb), lane (g, c) holds
-// [element tile_row(t, c)][token 32 tb + 8 g + i].
-template <int IO, int DK>
-__device__ __forceinline__ void fill_cols(uint4* dst, const void* src, long long base,
-                                          long long stride, int n, int Dk) {
-    constexpr int NA = IoTerms<IO>::n;
-    for (int i = threadIdx.x; i < 8 * (DK / 8); i += 256) {
-        // eight tokens x eight elements
-        const int tg = i & 7, ec = i >> 3;
-        uint4 t[8][NA];
+    for (int j = 0; j < KB; ++j) {
+        const int tile = 4 * j + wave, m = tile / KB, kb = tile - m * KB;
+        const int row = tile_row(m, c), e = 32 * kb + 8 * g;
+        const bool ok = row < n && e < Dk;
+        if constexpr (IO != IO_F32) {
+            dma16(dst + tile * 64,
+                  ok ? (const void*)((const uint16_t*)src + base + row * stride + e)
+                     : (const void*)kNothing);
+        } else {
+            uint4 t[3];
+            load_terms<IO>(src, base + row * stride + e, ok, t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            load_terms<IO>(src, base + (8 * tg + j) * stride + 8 * ec,
-                           8 * tg + j < n && 8 * ec < Dk, t[j]);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-            uint4 r[8], col[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = t[j][a];
-            transpose8(r, col);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // element 8 ec + j: tile and row that stand for it
-                const int tile = 2 * (ec >> 2) + (j >> 2), row = 4 * (ec & 3) + (j & 3);
-                dst[((a * (DK / 16) + tile) * 2 + (tg >> 2)) * 64 + 16 * (tg & 3) + row] = col[j];
-            }
+            for (int a = 0; a < 3; ++a) dst[a * kTiles * 64 + tile * 64 + lane] = t[a];
         }
     }
 }
-template <int N>
-__device__ __forceinline__ void fill_tri(uint4* dst, const float* src) {
-    for (int i = threadIdx.x; i < kTriTiles * 64; i += 256) {
-        const float4 a = *(const float4*)(src + i * 8), b = *(const float4*)(src + i * 8 + 4);
-        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint4 t[N];
-        split8<N>(x, t);
+// The transposed operand from rows so filled: tile (t, tb), the lane's
+// [element tile_row(t, c)][token 32 tb + 8 g + i], i < 8.  Each transposed
+// read takes four tokens x 16 elements for 16 lanes.
+template <int DK>
+__device__ __forceinline__ uint4 read_cols(const uint4* rows, int t, int tb) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    constexpr int KB = DK / 32;
+    const int lane = threadIdx.x & 63, g = lane >> 4, j = lane & 15;
+    const int a = j & 3, c = 4 * g + (j >> 2);
+    uint2 r[2];
 #pragma unroll
-        for (int j = 0; j < N; ++j) dst[j * kTriTiles * 64 + i] = t[j];
+    for (int half = 0; half < 2; ++half) {
+        const uint4* s = rows + ((2 * tb + half) * KB + (t >> 1)) * 64 + 16 * a + (c ^ (4 * a));
+        const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4*)((const char*)s + 8 * (t & 1)));
+        r[half] = __builtin_bit_cast(uint2, x);
     }
+    return make_uint4(r[0].x, r[0].y, r[1].x, r[1].y);
 }
+
+// Products of an operand of the I/O type with an fp32 one.
+//   bf16: exact in one term, times three bf16 terms;
+//   fp32: three terms, times three (the six products above 2^-24);
+//   f16: exact in one f16 term, times two f16 terms, 22 bits.  f16 has little
+//     range, so each column of the fp32 operand is first multiplied with the
+//     power of two that takes its largest value to 2^14; a column stays in
+//     one lane of each group of 16 from operand to result.
+struct ColScale { float to, back; };
+template <int IO>
+struct Operand {
+    static constexpr int NA = IO == IO_F32 ? 3 : 1, NB = IO == IO_F16 ? 2 : 3;
+    static constexpr bool kScaled = IO == IO_F16;
+    // terms of P and U in the outputs' P U: 16 bits are enough for a 16-bit
+    // output, whose rounding is 2^-9 or 2^-12 of it
+    static constexpr int NP = IO == IO_F32 ? 3 : 2;
+    // uint4 of a chunk's pack: T (three terms), decays, P
+    static constexpr int kPack = (3 * kTriTiles + 1 + NP * kTriTiles) * 64;
+
+    template <int N>
+    static __device__ __forceinline__ ColScale scale_of(const dfloat4 (&x)[N]) {
+        if constexpr (!kScaled) return {1.f, 1.f};
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a = fmaxf(a, fabsf(x[i][r]));
+        a = fmaxf(a, __shfl_xor(a, 16));
+        a = fmaxf(a, __shfl_xor(a, 32));
+        // exponents where both factors are normal numbers
+        int e = (int)(__float_as_uint(a) >> 23);
+        e = e < 28 ? 28 : e > 240 ? 240 : e;
+        return {__uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23),
+                __uint_as_float((uint32_t)(e - 14) << 23)};
+    }
+    static __device__ __forceinline__ void split(dfloat4 lo, dfloat4 hi, const ColScale& s,
+                                                 uint4 (&t)[NB]) {
+        if constexpr (kScaled) {
+            typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+            h8 a, b;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = (i < 4 ? lo[i & 3] : hi[i & 3]) * s.to;
+                a[i] = (_Float16)x;
+                b[i] = (_Float16)(x - (float)a[i]);
+            }
+            t[0] = __builtin_bit_cast(uint4, a);
+            t[1] = __builtin_bit_cast(uint4, b);
+        } else {
+            split_acc<NB>(lo, hi, t);
+        }
+    }
+    static __device__ __forceinline__ dfloat4 mma(const uint4 (&a)[NA], const uint4 (&b)[NB],
+                                                  dfloat4 c) {
+        if constexpr (kScaled) return mma_h(a[0], b[0], mma_h(a[0], b[1], c));
+        else return mma_terms<3>(a, b, c);
+    }
+    // where a 16-bit output is all that follows, 16 bits of b
+    static __device__ __forceinline__ dfloat4 mma_out(const uint4 (&a)[NA], const uint4 (&b)[NB],
+                                                      dfloat4 c) {
+        if constexpr (kScaled) return mma(a, b, c);
+        else return mma_terms<NP>(a, b, c);
+    }
+    static __device__ __forceinline__ dfloat4 mma_h(uint4 a, uint4 b, dfloat4 c) {
+        typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a),
+                                                      __builtin_bit_cast(h8, b), c, 0, 0, 0);
+    }
+};
+// uint4 of a chunk's pack for the backward: T^T and P^T (three terms each)
+// around the decays
+constexpr int kBackPack = (6 * kTriTiles + 1) * 64;
 
 constexpr int kLd = 68;   // floats between rows of the 64 x 64 matrices in LDS
 

@@ -193,22 +193,46 @@ size_t delta_slots(const fftconv_delta_desc* d) {
     return d->sequences ? per + d->sequences : d->B * per;
 }
 
-// Where the buffers of a call stand in a block of memory, in floats.
+// Chunks of a segment: sequences are cut where there are too few heads and
+// columns to give every CU two workgroups, into segments of at least
+// kSegChunks, so that the cut (each segment's effect on the state, some 1.4
+// times the walk itself, and the join) costs less than it wins.
+constexpr size_t kSegChunks = 16, kSegUnits = 512;
+size_t delta_seg_chunks(const fftconv_delta_desc* d) {
+    const size_t nch = (d->T + kChunk - 1) / kChunk;
+    const size_t cols = (d->Dv + 63) / 64, rows = d->sequences ? d->sequences : d->B;
+    const size_t whole = nch + 1;           // one segment a sequence
+    if (rows * d->Hv * cols * 2 >= kSegUnits) return whole;
+    size_t per = (delta_slots(d) * d->Hv * cols + kSegUnits - 1) / kSegUnits;
+    if (per < kSegChunks) per = kSegChunks;
+    return nch > 2 * per ? per : whole;
+}
+size_t delta_segs(const fftconv_delta_desc* d, size_t per) {
+    const size_t nch = (d->T + kChunk - 1) / kChunk;
+    if (d->sequences) return d->T / (kChunk * per) + d->sequences;
+    return d->B * (nch ? (nch + per - 1) / per : 1);
+}
+
+// Bytes of the buffers of a call, each a multiple of 16.
 struct DeltaLayout {
-    size_t tri, pm, dec, trit, pmt, states, us, all;
+    size_t pack, seg_n, seg_m;      // forward workspace
+    size_t bpack, states, us;       // saved
+    size_t workspace() const { return pack + seg_n + seg_m; }
+    size_t saved() const { return bpack + states + us; }
 };
-bool delta_layout(const fftconv_delta_desc* d, bool saved, DeltaLayout* l) {
-    size_t n, x, y;
+bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
+    size_t n, x, y, per = delta_seg_chunks(d), m;
     if (!product(delta_slots(d), d->Hv, 1, 1, &n) || n > kMaxGrid) return false;
     if (!product(n, d->Dk, d->Dv, 1, &x) || !product(n, kChunk, d->Dv, 1, &y)) return false;
-    l->tri = 0;
-    l->pm = n * kTriFloats;
-    l->dec = l->pm + n * kTriFloats;
-    l->trit = l->dec + n * kDecFloats;
-    l->pmt = l->trit + (saved ? n * kTriFloats : 0);
-    l->states = l->pmt + (saved ? n * kTriFloats : 0);
-    l->us = l->states + (saved ? x : 0);
-    l->all = l->us + (saved ? y : 0);
+    const bool cut = per <= (d->T + kChunk - 1) / kChunk;
+    const size_t segs = delta_segs(d, per);
+    if (!product(segs, d->Hv, (d->Dv + d->Dk + 15) / 16, 1, &m) || m > kMaxGrid) return false;
+    l->pack = n * (size_t)delta_pack_uint4(d->dtype) * 16;
+    l->seg_n = cut ? segs * d->Hv * d->Dk * d->Dv * 4 : 0;
+    l->seg_m = cut ? segs * d->Hv * d->Dk * d->Dk * 4 : 0;
+    l->bpack = n * (size_t)delta_back_pack_uint4() * 16;
+    l->states = x * 4;
+    l->us = y * 4;
     return true;
 }
 
@@ -272,15 +296,11 @@ fftconv_status delta_inputs(const fftconv_delta_desc* d, const DeltaArgs& a, Del
     return FFTCONV_OK;
 }
 
-void delta_place(const DeltaLayout& l, void* block, bool saved, DeltaParams& p) {
-    float* f = (float*)block;
-    p.tri = f + l.tri;
-    p.pm = f + l.pm;
-    p.dec = f + l.dec;
-    p.trit = saved ? f + l.trit : nullptr;
-    p.pmt = saved ? f + l.pmt : nullptr;
-    p.states = saved ? f + l.states : nullptr;
-    p.us = saved ? f + l.us : nullptr;
+void delta_place_saved(const DeltaLayout& l, void* saved, DeltaParams& p) {
+    char* f = (char*)saved;
+    p.bpack = (uint4*)f;
+    p.states = (float*)(f + l.bpack);
+    p.us = (float*)(f + l.bpack + l.states);
 }
 
 }  // namespace
@@ -354,14 +374,14 @@ fftconv_status fftconv_qknorm_backward(const fftconv_qknorm_desc* d, const void*
 
 size_t fftconv_delta_workspace_bytes(const fftconv_delta_desc* d) {
     DeltaLayout l;
-    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, false, &l)) return 0;
-    return l.all * 4;
+    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, &l)) return 0;
+    return l.workspace();
 }
 
 size_t fftconv_delta_saved_bytes(const fftconv_delta_desc* d) {
     DeltaLayout l;
-    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, true, &l)) return 0;
-    return l.all * 4;
+    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, &l)) return 0;
+    return l.saved();
 }
 
 fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q, const void* k,
@@ -373,21 +393,29 @@ fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q,
     Range in[7];
     CHECK(delta_inputs(d, {q, k, v, g, beta, cu_seqlens, initial_state}, p, in));
     DeltaLayout l;
-    if (!delta_layout(d, saved != nullptr, &l)) return FFTCONV_ERR_UNSUPPORTED;
+    if (!delta_layout(d, &l)) return FFTCONV_ERR_UNSUPPORTED;
     const size_t on = d->B * d->T * d->Hv * d->Dv * elem(d->dtype);
     const size_t state = (size_t)p.nseq * d->Hv * d->Dk * d->Dv * 4;
+    const size_t need = l.workspace(), keep = saved ? l.saved() : 0;
     CHECK(check_ptr(o, on));
     CHECK(check_ptr(final_state, state, false));
-    void* block = saved ? saved : workspace;
-    if (l.all * 4 && (!block || (saved ? saved_bytes : workspace_bytes) < l.all * 4))
-        return FFTCONV_ERR_WORKSPACE;
-    if ((uintptr_t)block & 15) return FFTCONV_ERR_ALIGNMENT;
-    const Range out[] = {{o, on}, {final_state, state}, {block, l.all * 4}};
+    CHECK(check_ptr(saved, keep, false));
+    if (saved_bytes < keep) return FFTCONV_ERR_INVALID_ARG;
+    if (need && (!workspace || workspace_bytes < need)) return FFTCONV_ERR_WORKSPACE;
+    if ((uintptr_t)workspace & 15) return FFTCONV_ERR_ALIGNMENT;
+    const Range out[] = {{o, on}, {final_state, state}, {saved, keep}, {workspace, need}};
     if (!outputs_clear(out, in)) return FFTCONV_ERR_INVALID_ARG;
     if (!p.nseq) return FFTCONV_OK;
     p.o = o;
     p.fin = final_state;
-    delta_place(l, block, saved != nullptr, p);
+    p.pack = (uint4*)workspace;
+    if (keep) delta_place_saved(l, saved, p);
+    p.seg_chunks = (int)delta_seg_chunks(d);
+    p.segs = (long long)delta_segs(d, (size_t)p.seg_chunks);
+    if (l.seg_m) {
+        p.seg_n = (float*)((char*)workspace + l.pack);
+        p.seg_m = (float*)((char*)workspace + l.pack + l.seg_n);
+    }
     hipStream_t s = (hipStream_t)stream;
     if (d->B * d->T) CHECK(launched(launch_delta_prep(d->dtype, p, s)));
     return launched(launch_delta_scan(d->dtype, p, s));
@@ -395,8 +423,8 @@ fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q,
 
 size_t fftconv_delta_backward_workspace_bytes(const fftconv_delta_desc* d) {
     DeltaLayout l;
-    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, true, &l)) return 0;
-    return (l.all - l.states) * 4;      // as many as the saved states and U
+    if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, &l)) return 0;
+    return l.states + l.us;
 }
 
 fftconv_status fftconv_delta_backward(const fftconv_delta_desc* d, const void* q, const void* k,
@@ -410,7 +438,7 @@ fftconv_status fftconv_delta_backward(const fftconv_delta_desc* d, const void* q
     Range in[7];
     CHECK(delta_inputs(d, {q, k, v, g, beta, cu_seqlens, nullptr}, p.f, in));
     DeltaLayout l;
-    if (!delta_layout(d, true, &l)) return FFTCONV_ERR_UNSUPPORTED;
+    if (!delta_layout(d, &l)) return FFTCONV_ERR_UNSUPPORTED;
     const size_t n = d->B * d->T, e = elem(d->dtype);
     const size_t on = n * d->Hv * d->Dv * e, kn = n * d->Hk * d->Dk * e, gn = n * d->Hv * 4;
     const size_t state = (size_t)p.f.nseq * d->Hv * d->Dk * d->Dv * 4;
@@ -422,23 +450,23 @@ fftconv_status fftconv_delta_backward(const fftconv_delta_desc* d, const void* q
     CHECK(check_ptr(dg, gn));
     CHECK(check_ptr(dbeta, gn));
     CHECK(check_ptr(d_initial_state, state, false));
-    CHECK(check_ptr(saved, l.all * 4));
-    if (saved_bytes < l.all * 4) return FFTCONV_ERR_INVALID_ARG;
-    const size_t need = (l.all - l.states) * 4;
+    CHECK(check_ptr(saved, l.saved()));
+    if (saved_bytes < l.saved()) return FFTCONV_ERR_INVALID_ARG;
+    const size_t need = l.states + l.us;
     if (need && (!workspace || workspace_bytes < need)) return FFTCONV_ERR_WORKSPACE;
     if ((uintptr_t)workspace & 15) return FFTCONV_ERR_ALIGNMENT;
-    in[5] = {saved, l.all * 4};
+    in[5] = {saved, l.saved()};
     const Range more[] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6], {d_o, on},
                           {d_final_state, state}};
     const Range out[] = {{dq, kn}, {dk, kn}, {dv, on}, {dg, gn}, {dbeta, gn},
                          {d_initial_state, state}, {workspace, need}};
     if (!outputs_clear(out, more)) return FFTCONV_ERR_INVALID_ARG;
     if (!p.f.nseq) return FFTCONV_OK;
-    delta_place(l, (void*)saved, true, p.f);     // only read here
+    delta_place_saved(l, (void*)saved, p.f);     // only read here
     p.dout = d_o;
     p.dfin = d_final_state;
     p.dstates = (float*)workspace;
-    p.dys = (float*)workspace + (l.us - l.states);
+    p.dys = (float*)((char*)workspace + l.states);
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;

@@ -298,10 +298,8 @@ class GatedDelta(_Op):
             if not final_state.is_contiguous():
                 raise ValueError("final_state must be contiguous")
         ref = ctypes.byref(desc)
-        ws = None
-        if saved is None:
-            ws = self._space(self._lib.fftconv_delta_workspace_bytes(ref), workspace, dev,
-                             "workspace")
+        ws = self._space(self._lib.fftconv_delta_workspace_bytes(ref), workspace, dev,
+                         "workspace")
         self._call("fftconv_delta_forward", dev, stream, ins + (out, final_state, saved, ws), ref,
                    *map(_ptr, ins), _ptr(out), _ptr(final_state), _ptr(saved),
                    self._bytes(saved), _ptr(ws), self._bytes(ws))
@@ -316,13 +314,13 @@ class GatedDelta(_Op):
                              final_state, None, workspace, stream)
 
     def forward_train(self, q, k, v, g, beta, initial_state=None, cu_seqlens=None, out=None,
-                      final_state=None, saved=None, stream=None):
+                      final_state=None, saved=None, workspace=None, stream=None):
         """As forward, and what backward needs besides the inputs (an opaque
         tensor of bytes): returns (o, final_state, saved)."""
         args = self._inputs(q, k, v, g, beta, initial_state, cu_seqlens)
         saved = self._space(self._lib.fftconv_delta_saved_bytes(ctypes.byref(args[1])), saved,
                             args[0], "saved")
-        o, state = self._forward(args, out, final_state, saved, None, stream)
+        o, state = self._forward(args, out, final_state, saved, workspace, stream)
         return o, state, saved
 
     def backward(self, q, k, v, g, beta, d_out, saved, d_final_state=None, initial_state=None,

@@ -505,8 +505,7 @@ typedef struct fftconv_delta_desc {
  *  final_state: fp32, as initial_state; NULL to skip it.
  *  saved: fftconv_delta_saved_bytes(desc) bytes that fftconv_delta_backward
  *     will read (16-B aligned), or NULL in inference.
- *  workspace: fftconv_delta_workspace_bytes(desc) bytes; unused (may be NULL)
- *     when saved is given.
+ *  workspace: fftconv_delta_workspace_bytes(desc) bytes.
  * States, gates and sums are fp32 or wider whatever the I/O type; fp32
  * operands of the matrix products are split so that 24 bits take part. */
 fftconv_status fftconv_delta_forward(const fftconv_delta_desc *desc, const void *q,
