@@ -16,6 +16,7 @@
 // T and P need no state: delta_prep_kernel makes them for all chunks at
 // once.  delta_scan_kernel then walks over a sequence's chunks.
 #include "fftconv_delta_dev.h"
+#include <stdlib.h>
 
 namespace fftconv {
 namespace {
@@ -45,19 +46,23 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
             io_store<IO>(p.o, (n * p.Hv + h) * p.Dv + tile * 32 + threadIdx.x, 0.f);
         return;
     }
-    float* S = p.state + (slot * p.Hv + h) * p.Dk * (long long)p.Dv + col;
+    const long long at = (slot * p.Hv + h) * p.Dk * (long long)p.Dv + col;
+    float* S = p.state + at;
     const int hk = h / (p.Hv / p.Hk);
     float4 s[R];
     float k[R], q[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const bool ok = row0 + i < p.Dk;
-        s[i] = cok && ok ? *(const float4*)(S + (long long)(row0 + i) * p.Dv)
-                         : make_float4(0, 0, 0, 0);
-        k[i] = ok ? io_load<IO>(p.k, n * p.ks[0] + hk * p.ks[1] + row0 + i) : 0.f;
-        q[i] = ok ? io_load<IO>(p.q, n * p.qs[0] + hk * p.qs[1] + row0 + i) : 0.f;
+        float x[4];
+        load4<IO_F32>(p.state, at + (long long)(row0 + i) * p.Dv, cok && ok, x);
+        s[i] = make_float4(x[0], x[1], x[2], x[3]);
+        k[i] = io_load_if<IO>(p.k, n * p.ks[0] + hk * p.ks[1] + row0 + i, ok);
+        q[i] = io_load_if<IO>(p.q, n * p.qs[0] + hk * p.qs[1] + row0 + i, ok);
     }
     const float a = expf(p.g[n * p.Hv + h]), beta = p.beta[n * p.Hv + h];
+    float v[4];
+    load4<IO>(p.v, n * p.vs[0] + h * p.vs[1] + col, cok, v);
     // sums over the rows: S^T k, S^T q (four columns each) and q.k
     float r[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
@@ -87,7 +92,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
     float u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        u[j] = beta * (io_load<IO>(p.v, n * p.vs[0] + h * p.vs[1] + col + j) - a * r[j]);
+        u[j] = beta * (v[j] - a * r[j]);
     if (row0 == 0)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -290,41 +295,41 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
 
 // ------------------------------------------------- the walk over the chunks
 
-// LDS of the walk, in uint4.  16-bit keys are loaded one chunk ahead into a
-// second buffer; fp32 keys, three times as large, have no room for one.
+// LDS of the walk, in uint4.  16-bit operands of the next chunk are put into a
+// second buffer while the present one is worked on; fp32 ones, three times as
+// large, have no room for one.
 template <int IO, int DK, bool FULL>
 struct ScanLds {
     static constexpr int NA = Operand<IO>::NA;
     static constexpr int kRows = NA * 4 * (DK / 32) * 64;
+    static constexpr int kPackKb = 3 * kTriTiles + 1 + (FULL ? Operand<IO>::NP * kTriTiles : 0);
+    static constexpr int kK = 0, kQ = kRows, kTri = kQ + (FULL ? kRows : 0);
+    static constexpr int kDec = kTri + 3 * kTriTiles * 64, kP = kDec + 64;
+    static constexpr int kSize = kTri + kPackKb * 64;
     static constexpr int kBufs = NA == 1 ? 2 : 1;
-    static constexpr int kK = 0, kQ = kBufs * kRows;
-    static constexpr int kPack = kQ + (FULL ? kRows : 0);
-    static constexpr int kTri = kPack, kDec = kTri + 3 * kTriTiles * 64, kP = kDec + 64;
-    static constexpr int kTail = FULL ? Operand<IO>::NP * kTriTiles * 64 : 0;
-    static constexpr int kBytes = (kP + kTail) * 16;
+    static constexpr int kBytes = kBufs * kSize * 16;
 };
 
-// A wave owns 16 columns of the state: its accumulators hold S (Dk x 16), and
-// every product of the chunk, K S, T X, P U, K^T U, takes the last one's
-// accumulators as its B operand, so the chain of a chunk has no exchange and
-// no barrier of its own.  The four waves of a workgroup share the operands
-// that do not depend on the state (K, Q, T, P) through LDS, K^T being K read
-// transposed.  K of the next chunk is on its way during the whole chunk, the
-// rest from the last use of the present ones on.
+// A wave owns NT times 16 columns of the state: its accumulators hold S (Dk x
+// 16 each), and every product of the chunk, K S, T X, P U, K^T U, takes the
+// last one's accumulators as its B operand, so the chain of a chunk has no
+// exchange and no barrier of its own.  The four waves of a workgroup share
+// the operands that do not depend on the state (K, Q, T, P) through LDS, K^T
+// being K read transposed.
 //
 // FULL: outputs and final state.  Otherwise a segment's effect on the state
 // alone: its last state from the first (the first segment of a sequence) or
 // from 0, and, in columns of their own, the matrix its first state is
 // multiplied with (the last state from the identity, without v).
-template <int IO, int DK, bool FULL>
-__global__ __launch_bounds__(256, Operand<IO>::NA == 1 ? 2 : 1)
-void delta_scan_kernel(DeltaParams p) {
+template <int IO, int DK, int NT, bool FULL>
+__global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
     typedef ScanLds<IO, DK, FULL> L;
     typedef Operand<IO> Op;
     constexpr int NA = Op::NA, KB = DK / 32, ST = DK / 16, NP = Op::NP, NB = Op::NB;
+    constexpr int kCols = 64 * NT;
     extern __shared__ uint4 lds[];
-    const float* dec = (const float*)(lds + L::kDec);
-    const int vcols = (p.Dv + 63) / 64, cols = vcols + (FULL ? 0 : (p.Dk + 63) / 64);
+    const int vcols = (p.Dv + kCols - 1) / kCols;
+    const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
     const long long units = p.segs * p.Hv * cols;
     long long id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
@@ -336,9 +341,10 @@ void delta_scan_kernel(DeltaParams p) {
     const Span sp = span_of(p, seq);
     const int chunks = (sp.len + kChunk - 1) / kChunk;
     const int sn = (int)(seg - seg_of(p, sp, seq));      // segment of the sequence
-    const int first = sn * p.seg_chunks;
-    const int last = first + p.seg_chunks < chunks ? first + p.seg_chunks : chunks;
-    if (sn != 0 && first >= chunks) return;              // no such segment
+    const long long first_ = (long long)sn * p.seg_chunks;
+    if (sn != 0 && first_ >= chunks) return;             // no such segment
+    const int first = (int)first_;
+    const int last = chunks - first > p.seg_chunks ? first + p.seg_chunks : chunks;
     if (!FULL && (last == chunks || (sn == 0 && cb >= vcols))) return;
     const bool matrix = !FULL && cb >= vcols;
     if (matrix) cb -= vcols;
@@ -346,94 +352,116 @@ void delta_scan_kernel(DeltaParams p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int slot = 16 * g + (c ^ (4 * g));             // of a row operand
-    const int col = cb * 64 + wave * 16 + c;
+    const int col0 = cb * kCols + wave * 16 * NT + c;    // and 16 further each
     const int width = matrix ? p.Dk : p.Dv;
-    const bool cok = col < width;
+    bool cok[NT];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) cok[u] = col0 + 16 * u < width;
     const int hk = h / p.group;
     const long long state = p.Dk * (long long)p.Dv;
-    dfloat4 S[ST];
+    dfloat4 S[NT][ST];
     {
         const float* s = nullptr;
-        if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col : nullptr;
-        else if (FULL) s = p.seg_n + ((seg - 1) * p.Hv + h) * state + col;
+        if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col0 : nullptr;
+        else if (FULL) s = p.seg_n + ((seg - 1) * p.Hv + h) * state + col0;
 #pragma unroll
-        for (int t = 0; t < ST; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = tile_row(t, 4 * g + r);
-                S[t][r] = matrix ? (row == col ? 1.f : 0.f)
-                                 : (s && cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f);
-            }
-    }
-    const long long kbase = sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2];
-    const long long qbase = sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2];
-    const long long vbase = sp.b * p.vs[0] + sp.t0 * p.vs[1] + h * p.vs[2] + col;
-    const auto load_k = [&](int ch, int buf) {
-        fill_rows<IO, DK>(lds + L::kK + buf * L::kRows, p.k, kbase + ch * (kChunk * p.ks[1]),
-                          p.ks[1], sp.len - ch * kChunk, p.Dk);
-    };
-    const auto load_rest = [&](int ch) {
-        if (FULL)
-            fill_rows<IO, DK>(lds + L::kQ, p.q, qbase + ch * (kChunk * p.qs[1]), p.qs[1],
-                              sp.len - ch * kChunk, p.Dk);
-        copy_lds(lds + L::kPack, p.pack + ((sp.slot0 + ch) * p.Hv + h) * Op::kPack,
-                 3 * kTriTiles + 1 + (FULL ? NP * kTriTiles : 0));
-    };
-    float v[4][4];
-    const auto load_v = [&](int ch) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = ch * kChunk + tile_row(m, 4 * g + r);
-                v[m][r] = !matrix && cok && row < sp.len
-                              ? io_load<IO>(p.v, vbase + row * p.vs[1]) : 0.f;
-            }
-    };
-    if (first < last) {
-        load_k(first, 0);
-        load_rest(first);
-        load_v(first);
-    }
-    wait_loads();
-    __syncthreads();
-    int buf = 0;
-    for (int ch = first; ch < last; ++ch) {
-        const long long ci = (sp.slot0 + ch) * p.Hv + h;
-        const bool more = ch + 1 < last;
-        if (L::kBufs == 2 && more) load_k(ch + 1, buf ^ 1);
-        const uint4* Kl = lds + L::kK + buf * L::kRows;
-        if (FULL && p.states && cok) {
-            float* d = p.states + ci * state + col;
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = tile_row(t, 4 * g + r);
-                    if (row < p.Dk) d[(long long)row * p.Dv] = S[t][r];
+                    S[u][t][r] = matrix ? (row == col0 + 16 * u ? 1.f : 0.f)
+                                        : (s && cok[u] && row < p.Dk
+                                               ? s[(long long)row * p.Dv + 16 * u] : 0.f);
                 }
-        }
-        // K S and Q S
-        dfloat4 X[4], O[4];
+    }
+    const long long kbase = sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2];
+    const long long qbase = sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2];
+    const long long vbase = sp.b * p.vs[0] + sp.t0 * p.vs[1] + h * p.vs[2] + col0;
+    const long long ostride = (long long)p.Hv * p.Dv;
+    const long long obase = ((sp.b * p.T + sp.t0) * p.Hv + h) * p.Dv + col0;
+
+    RowTiles<IO, DK> rk, rq;
+    Block<L::kPackKb> rp;
+    float v[NT][4][4];
+    const auto load = [&](int ch) __attribute__((always_inline)) {
+        const int n = sp.len - ch * kChunk;
+        rk.load(p.k, kbase + ch * (kChunk * p.ks[1]), p.ks[1], n, p.Dk);
+        if (FULL) rq.load(p.q, qbase + ch * (kChunk * p.qs[1]), p.qs[1], n, p.Dk);
+        rp.load(p.pack + ((sp.slot0 + ch) * p.Hv + h) * Op::kPack);
+    };
+    const auto store = [&](uint4* d) __attribute__((always_inline)) {
+        rk.store(d + L::kK);
+        if (FULL) rq.store(d + L::kQ);
+        rp.store(d + L::kTri);
+    };
+    const auto load_v = [&](int ch) __attribute__((always_inline)) {
+        const int n = sp.len - ch * kChunk - 8 * g;
+        const long long at = vbase + (ch * kChunk + 8 * g) * p.vs[1];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) X[m] = O[m] = dfloat4{0, 0, 0, 0};
-        const ColScale sc = Op::template scale_of<ST>(S);
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = tile_base(m) + r;
+                    v[u][m][r] = io_load_if<IO>(p.v, at + row * p.vs[1] + 16 * u,
+                                                !matrix && cok[u] && row < n);
+                }
+    };
+    if (first < last) {
+        load(first);
+        load_v(first);
+        store(lds);
+    }
+    __syncthreads();
+    uint4* now = lds;
+    uint4* next = lds + (L::kBufs == 2 ? L::kSize : 0);
+    for (int ch = first; ch < last; ++ch) {
+        const long long ci = (sp.slot0 + ch) * p.Hv + h;
+        const int n = sp.len - ch * kChunk - 8 * g;      // of the group's tokens
+        const int ahead = ch + 1 < last ? ch + 1 : ch;
+        load(ahead);
+        const float* dec = (const float*)(now + L::kDec);
+        if (FULL && p.states)
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                float* d = p.states + ci * state + (long long)(8 * g) * p.Dv + col0 + 16 * u;
+                if (cok[u])
+#pragma unroll
+                    for (int t = 0; t < ST; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int row = tile_base(t) + r;
+                            if (8 * g + row < p.Dk) d[(long long)row * p.Dv] = S[u][t][r];
+                        }
+            }
+        // K S and Q S
+        dfloat4 X[NT][4], O[NT][4];
+        ColScale sc[NT];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) X[u][m] = O[u][m] = dfloat4{0, 0, 0, 0};
+            sc[u] = Op::template scale_of<ST>(S[u]);
+        }
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            uint4 st[NB];
-            Op::split(S[2 * kb], S[2 * kb + 1], sc, st);
+            uint4 a[4][NA], q[4][NA];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                uint4 a[NA];
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-                for (int i = 0; i < NA; ++i) a[i] = Kl[((i * 4 + m) * KB + kb) * 64 + slot];
-                X[m] = Op::mma(a, st, X[m]);
-                if (FULL) {
-#pragma unroll
-                    for (int i = 0; i < NA; ++i)
-                        a[i] = lds[L::kQ + ((i * 4 + m) * KB + kb) * 64 + slot];
-                    O[m] = Op::mma_out(a, st, O[m]);
+                for (int i = 0; i < NA; ++i) {
+                    a[m][i] = now[L::kK + ((i * 4 + m) * KB + kb) * 64 + slot];
+                    if (FULL) q[m][i] = now[L::kQ + ((i * 4 + m) * KB + kb) * 64 + slot];
                 }
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                uint4 st[NB];
+                Op::split(S[u][2 * kb], S[u][2 * kb + 1], sc[u], st);
+                Op::mma_all(a, st, X[u]);
+                if (FULL) Op::mma_all_out(q, st, O[u]);
             }
         }
         // X = beta o (V - e^G o K S);  O = scale e^G o Q S
@@ -443,122 +471,168 @@ void delta_scan_kernel(DeltaParams p) {
             const float4 e = *(const float4*)(dec + row), b = *(const float4*)(dec + 128 + row);
             const float ev[4] = {e.x, e.y, e.z, e.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                X[m][r] = bv[r] * (v[m][r] - ev[r] * (X[m][r] * sc.back));
-                if (FULL) O[m][r] = p.scale * ev[r] * (O[m][r] * sc.back);
-            }
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    X[u][m][r] = bv[r] * (v[u][m][r] - ev[r] * (X[u][m][r] * sc[u].back));
+                    if (FULL) O[u][m][r] = p.scale * ev[r] * (O[u][m][r] * sc[u].back);
+                }
         }
+        load_v(ahead);
         // U = T X
-        dfloat4 U[4];
+        dfloat4 U[NT][4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) U[m] = dfloat4{0, 0, 0, 0};
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            uint4 xt[3];
-            split_acc<3>(X[2 * kb], X[2 * kb + 1], xt);
+            for (int m = 0; m < 4; ++m) U[u][m] = dfloat4{0, 0, 0, 0};
 #pragma unroll
-            for (int m = 2 * kb; m < 4; ++m) {
-                uint4 a[3];
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    a[i] = lds[L::kTri + (i * kTriTiles + tri_tile(m, kb)) * 64 + lane];
-                U[m] = mma_terms<3>(a, xt, U[m]);
-            }
-        }
-        if (FULL) {
-            if (p.us && cok) {
-                float* d = p.us + ci * kChunk * p.Dv + col;
+            for (int m0 = 2 * kb; m0 < 4; m0 += 2) {
+                uint4 a[2][3];
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        d[(long long)tile_row(m, 4 * g + r) * p.Dv] = U[m][r];
-            }
-            // O += P U
+                    for (int i = 0; i < 3; ++i)
+                        a[m][i] = now[L::kTri + (i * kTriTiles + tri_tile(m0 + m, kb)) * 64 + lane];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                uint4 ut[NP];
-                split_acc<NP>(U[2 * kb], U[2 * kb + 1], ut);
-#pragma unroll
-                for (int m = 2 * kb; m < 4; ++m) {
-                    uint4 a[NP];
-#pragma unroll
-                    for (int i = 0; i < NP; ++i)
-                        a[i] = lds[L::kP + (i * kTriTiles + tri_tile(m, kb)) * 64 + lane];
-                    O[m] = mma_terms<NP>(a, ut, O[m]);
+                for (int u = 0; u < NT; ++u) {
+                    uint4 xt[3];
+                    split_acc<3>(X[u][2 * kb], X[u][2 * kb + 1], xt);
+                    mma_tiles<3>(a, xt, *(dfloat4 (*)[2])&U[u][m0]);
                 }
             }
-            if (cok)
+        if (FULL) {
+            if (p.us)
 #pragma unroll
-                for (int m = 0; m < 4; ++m)
+                for (int u = 0; u < NT; ++u) {
+                    float* d = p.us + (ci * kChunk + 8 * g) * p.Dv + col0 + 16 * u;
+                    if (cok[u])
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = ch * kChunk + tile_row(m, 4 * g + r);
-                        if (row < sp.len)
-                            io_store<IO>(p.o, ((sp.b * p.T + sp.t0 + row) * p.Hv + h) * p.Dv + col,
-                                         O[m][r]);
+                        for (int m = 0; m < 4; ++m)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                d[(long long)(tile_base(m) + r) * p.Dv] = U[u][m][r];
+                }
+            // O += P U
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int m0 = 2 * kb; m0 < 4; m0 += 2) {
+                    uint4 a[2][NP];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int i = 0; i < NP; ++i)
+                            a[m][i] =
+                                now[L::kP + (i * kTriTiles + tri_tile(m0 + m, kb)) * 64 + lane];
+#pragma unroll
+                    for (int u = 0; u < NT; ++u) {
+                        uint4 ut[NP];
+                        split_acc<NP>(U[u][2 * kb], U[u][2 * kb + 1], ut);
+                        mma_tiles<NP>(a, ut, *(dfloat4 (*)[2])&O[u][m0]);
                     }
+                }
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                const long long at = obase + (ch * kChunk + 8 * g) * ostride + 16 * u;
+                if (!cok[u]) continue;
+                if (sp.len - ch * kChunk >= kChunk) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            io_store<IO>(p.o, at + (tile_base(m) + r) * ostride, O[u][m][r]);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (tile_base(m) + r < n)
+                                io_store<IO>(p.o, at + (tile_base(m) + r) * ostride, O[u][m][r]);
+                }
+            }
         }
         // e^(Gc-G) o U
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float4 e = *(const float4*)(dec + 64 + tile_row(m, 4 * g));
-            U[m][0] *= e.x;
-            U[m][1] *= e.y;
-            U[m][2] *= e.z;
-            U[m][3] *= e.w;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                U[u][m][0] *= e.x;
+                U[u][m][1] *= e.y;
+                U[u][m][2] *= e.z;
+                U[u][m][3] *= e.w;
+            }
         }
         const float ec = dec[192];
-        __syncthreads();          // Q, T, P and the decays are used up
-        if (more) {
-            load_rest(ch + 1);
-            load_v(ch + 1);
-        }
+        if (L::kBufs == 2) store(next);
         // S = e^Gc S + K^T U
-        const ColScale su = Op::template scale_of<4>(U);
-        uint4 ut[2][NB];
+        ColScale su[NT];
+        uint4 ut[NT][2][NB];
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) Op::split(U[2 * tb], U[2 * tb + 1], su, ut[tb]);
+        for (int u = 0; u < NT; ++u) {
+            su[u] = Op::template scale_of<4>(U[u]);
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            dfloat4 a = {0, 0, 0, 0};
-            if (!Op::kScaled)
+            for (int tb = 0; tb < 2; ++tb)
+                Op::split(U[u][2 * tb], U[u][2 * tb + 1], su[u], ut[u][tb]);
+        }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) a[r] = ec * S[t][r];
+        for (int t0 = 0; t0 < ST; t0 += 4) {
+            dfloat4 a[NT][4];
+#pragma unroll
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        a[u][t][r] = Op::kScaled ? 0.f : ec * S[u][t0 + t][r];
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
-                uint4 x[NA];
+                uint4 x[4][NA];
 #pragma unroll
-                for (int i = 0; i < NA; ++i) x[i] = read_cols<DK>(Kl + i * 4 * KB * 64, t, tb);
-                a = Op::mma(x, ut[tb], a);
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < NA; ++i)
+                        x[t][i] = read_cols<DK>(now + L::kK + i * 4 * KB * 64, t0 + t, tb);
+#pragma unroll
+                for (int u = 0; u < NT; ++u) Op::mma_all(x, ut[u][tb], a[u]);
             }
-            if (Op::kScaled)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) a[r] = ec * S[t][r] + su.back * a[r];
-            S[t] = a;
+            for (int u = 0; u < NT; ++u)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        S[u][t0 + t][r] = Op::kScaled
+                                              ? ec * S[u][t0 + t][r] + su[u].back * a[u][t][r]
+                                              : a[u][t][r];
         }
-        if (L::kBufs == 1) {
-            __syncthreads();
-            if (more) load_k(ch + 1, 0);
-        } else {
-            buf ^= 1;
-        }
-        wait_loads();
         __syncthreads();
+        if (L::kBufs == 2) {
+            uint4* x = now;
+            now = next;
+            next = x;
+        } else {
+            store(lds);
+            __syncthreads();
+        }
     }
-    if (!cok) return;
     float* d = nullptr;
     if (FULL) d = p.fin && last == chunks ? p.fin + (seq * p.Hv + h) * state : nullptr;
     else if (matrix) d = p.seg_m + (seg * p.Hv + h) * p.Dk * (long long)p.Dk;
     else d = p.seg_n + (seg * p.Hv + h) * state;
     if (!d) return;
 #pragma unroll
-    for (int t = 0; t < ST; ++t)
+    for (int u = 0; u < NT; ++u)
+        if (cok[u])
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = tile_row(t, 4 * g + r);
-            if (row < p.Dk) d[(long long)row * width + col] = S[t][r];
-        }
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = tile_row(t, 4 * g + r);
+                    if (row < p.Dk) d[(long long)row * width + col0 + 16 * u] = S[u][t][r];
+                }
 }
 
 // Joins the segments of a sequence: with N the last state of a segment from 0
@@ -584,7 +658,7 @@ __global__ __launch_bounds__(64) void delta_join_kernel(DeltaParams p) {
     const long long state = p.Dk * (long long)p.Dv, square = p.Dk * (long long)p.Dk;
     const long long seg0 = seg_of(p, sp, seq);
     dfloat4 S[ST];
-    const auto at = [&](long long seg) { return p.seg_n + (seg * p.Hv + h) * state + col; };
+    const auto at = [&](long long seg) __attribute__((always_inline)) { return p.seg_n + (seg * p.Hv + h) * state + col; };
     const float* s = at(seg0);
 #pragma unroll
     for (int t = 0; t < ST; ++t)
@@ -602,7 +676,8 @@ __global__ __launch_bounds__(64) void delta_join_kernel(DeltaParams p) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = tile_row(t, 4 * g + r);
-                R[t][r] = cok && row < p.Dk ? d[(long long)row * p.Dv] : 0.f;
+                R[t][r] = io_load_if<IO_F32>(p.seg_n, d - p.seg_n + (long long)row * p.Dv,
+                                             cok && row < p.Dk);
             }
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
@@ -638,30 +713,36 @@ hipError_t step_io(const DeltaStepParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int IO, int DK, bool FULL>
+template <int IO, int DK, int NT, bool FULL>
 hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
     const int bytes = ScanLds<IO, DK, FULL>::kBytes;
-    const hipError_t e = hipFuncSetAttribute((const void*)delta_scan_kernel<IO, DK, FULL>,
+    const hipError_t e = hipFuncSetAttribute((const void*)delta_scan_kernel<IO, DK, NT, FULL>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int cols = (p.Dv + 63) / 64 + (FULL ? 0 : (p.Dk + 63) / 64);
+    const int width = 64 * NT;
+    const int cols = (p.Dv + width - 1) / width + (FULL ? 0 : (p.Dk + width - 1) / width);
     const long long units = p.segs * p.Hv * cols;
-    hipLaunchKernelGGL((delta_scan_kernel<IO, DK, FULL>), dim3((unsigned)xcd_blocks(units)),
+    hipLaunchKernelGGL((delta_scan_kernel<IO, DK, NT, FULL>), dim3((unsigned)xcd_blocks(units)),
                        dim3(256), bytes, s, p);
     return hipGetLastError();
 }
 
-template <int IO, int DK>
-hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
+template <int IO, int DK, int NT>
+hipError_t scan_nt(const DeltaParams& p, hipStream_t s) {
     if (p.seg_m) {
-        hipError_t e = scan_launch<IO, DK, false>(p, s);
+        hipError_t e = scan_launch<IO, DK, NT, false>(p, s);
         if (e != hipSuccess) return e;
         const long long joins = p.nseq * p.Hv * ((p.Dv + 15) / 16);
         hipLaunchKernelGGL((delta_join_kernel<DK>), dim3((unsigned)joins), dim3(64), 0, s, p);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return scan_launch<IO, DK, true>(p, s);
+    return scan_launch<IO, DK, NT, true>(p, s);
+}
+template <int IO, int DK>
+hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
+    if (getenv("NT2")) return scan_nt<IO, DK, 2>(p, s);
+    return scan_nt<IO, DK, 1>(p, s);
 }
 
 template <int IO>

@@ -30,8 +30,7 @@ struct RscanLds {
 // The mirror of the forward walk: a wave owns 16 columns of D and goes
 // through K D, T^T dU and the two transposed products without an exchange.
 template <int IO, int DK>
-__global__ __launch_bounds__(256, Operand<IO>::NA == 1 ? 2 : 1)
-void delta_rscan_kernel(DeltaGradParams gp) {
+__global__ __launch_bounds__(256) void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
     typedef Operand<IO> Op;
     const DeltaParams& p = gp.f;
@@ -68,38 +67,42 @@ void delta_rscan_kernel(DeltaGradParams gp) {
     const long long qbase = sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2];
     const long long obase = ((sp.b * p.T + sp.t0) * p.Hv + h) * p.Dv + col;
     const long long ostride = (long long)p.Hv * p.Dv;
-    const auto load_rows = [&](int ch) {
-        fill_rows<IO, DK>(lds + L::kK, p.k, kbase + ch * (kChunk * p.ks[1]), p.ks[1],
-                          sp.len - ch * kChunk, p.Dk);
-        fill_rows<IO, DK>(lds + L::kQ, p.q, qbase + ch * (kChunk * p.qs[1]), p.qs[1],
-                          sp.len - ch * kChunk, p.Dk);
+    RowTiles<IO, DK> rk, rq;
+    Block<kBackPack / 64> rp;
+    const auto load = [&](int ch) __attribute__((always_inline)) {
+        const int n = sp.len - ch * kChunk;
+        rk.load(p.k, kbase + ch * (kChunk * p.ks[1]), p.ks[1], n, p.Dk);
+        rq.load(p.q, qbase + ch * (kChunk * p.qs[1]), p.qs[1], n, p.Dk);
+        rp.load(p.bpack + ((sp.slot0 + ch) * p.Hv + h) * kBackPack);
     };
-    const auto load_pack = [&](int ch) {
-        copy_lds(lds + L::kPack, p.bpack + ((sp.slot0 + ch) * p.Hv + h) * kBackPack,
-                 kBackPack / 64);
+    const auto store = [&](uint4* d) __attribute__((always_inline)) {
+        rk.store(d + L::kK);
+        rq.store(d + L::kQ);
+        rp.store(d + L::kPack);
     };
     dfloat4 dN[4];                       // dO of the next chunk
-    const auto load_do = [&](int ch) {
+    const auto load_do = [&](int ch) __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = ch * kChunk + tile_row(m, 4 * g + r);
-                dN[m][r] = cok && row < sp.len ? io_load<IO>(gp.dout, obase + row * ostride) : 0.f;
+                dN[m][r] = io_load_if<IO>(gp.dout, obase + row * ostride, cok && row < sp.len);
             }
     };
     if (chunks > 0) {
-        load_rows(chunks - 1);
-        load_pack(chunks - 1);
+        load(chunks - 1);
         load_do(chunks - 1);
+        store(lds);
     }
-    wait_loads();
     __syncthreads();
     for (int ch = chunks - 1; ch >= 0; --ch) {
         const long long ci = (sp.slot0 + ch) * p.Hv + h;
         dfloat4 dO[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dO[m] = dN[m];
+        const int ahead = ch > 0 ? ch - 1 : 0;
+        load(ahead);
         if (cok) {
             float* d = gp.dstates + ci * state + col;
 #pragma unroll
@@ -186,11 +189,7 @@ void delta_rscan_kernel(DeltaGradParams gp) {
             }
         }
         const float ec = dec[192];
-        __syncthreads();              // T, P and the decays are used up
-        if (ch > 0) {
-            load_pack(ch - 1);
-            load_do(ch - 1);
-        }
+        load_do(ahead);
         const ColScale sy = Op::template scale_of<4>(dY), so = Op::template scale_of<4>(dO);
         uint4 yt[2][NB], ot[2][NB];
 #pragma unroll
@@ -224,8 +223,7 @@ void delta_rscan_kernel(DeltaGradParams gp) {
                 D[t] = a + b;
         }
         __syncthreads();
-        if (ch > 0) load_rows(ch - 1);
-        wait_loads();
+        store(lds);
         __syncthreads();
     }
     if (gp.dinit && cok)
@@ -346,14 +344,15 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
             for (int i = threadIdx.x; i < ST * 64; i += 256) {
                 const int row = tile_row(i >> 6, i & 15), el = d0 + 8 * ((i >> 4) & 3);
                 const bool ok = row < p.Dk && el < p.Dv;
-                const float* s = S0 + (long long)row * p.Dv + el;
-                const float* d = D + (long long)row * p.Dv + el;
+                const long long at = ok ? (long long)row * p.Dv + el : 0;
+                float s[8], d[8];
+                load8<IO_F32>(S0, at, ok, s);
+                load8<IO_F32>(D, at, ok, d);
                 uint4 ts[3], td[3];
-                load_terms<IO_F32>(s, 0, ok, ts);
-                load_terms<IO_F32>(d, 0, ok, td);
-                if (ok)
+                split8<3>(s, ts);
+                split8<3>(d, td);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sd += s[j] * d[j];
+                for (int j = 0; j < 8; ++j) sd += s[j] * d[j];
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
                     lds[L::kS + j * ST * 64 + i] = ts[j];
@@ -372,14 +371,13 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
             uint4 ob[NO], yb[3], ub[3];
             const bool ok = mine < n && e < p.Dv;
             load_terms<IO>(gp.dout, ((sp.b * p.T + tok + mine) * p.Hv + h) * p.Dv + e, ok, ob);
-            const float* yp = Y + (long long)mine * p.Dv + e;
-            load_terms<IO_F32>(yp, 0, e < p.Dv, yb);
+            float y[8], v[8];
+            load8<IO_F32>(Y, (long long)mine * p.Dv + e, e < p.Dv, y);
+            load8<IO>(p.v, sp.b * p.vs[0] + (tok + mine) * p.vs[1] + h * p.vs[2] + e, ok, v);
             load_terms<IO_F32>(U, (long long)mine * p.Dv + e, e < p.Dv, ub);
-            if (ok) {
-                const long long vi = sp.b * p.vs[0] + (tok + mine) * p.vs[1] + h * p.vs[2] + e;
+            split8<3>(y, yb);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) yv += yp[j] * io_load<IO>(p.v, vi + j);
-            }
+            for (int j = 0; j < 8; ++j) yv += y[j] * v[j];
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < ST; ++t) {
@@ -404,8 +402,13 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
         }
         __syncthreads();
         // keys and queries take the slices' place
-        fill_rows<IO, DK>(lds + L::kK, p.k, kbase, p.ks[1], n, p.Dk);
-        fill_rows<IO, DK>(lds + L::kQ, p.q, qbase, p.qs[1], n, p.Dk);
+        {
+            RowTiles<IO, DK> rk, rq;
+            rk.load(p.k, kbase, p.ks[1], n, p.Dk);
+            rq.load(p.q, qbase, p.qs[1], n, p.Dk);
+            rk.store(lds + L::kK);
+            rq.store(lds + L::kQ);
+        }
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) sd += __shfl_xor(sd, m);
         yv = sum_groups(yv);
@@ -477,7 +480,6 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaGradParams gp) {
             red[wave] = sd;
             red3[wave] = s3;
         }
-        wait_loads();
         __syncthreads();
         if (wave == 0) {
             double x = (double)rowG[lane] - (colsum[0][lane] + colsum[1][lane] +

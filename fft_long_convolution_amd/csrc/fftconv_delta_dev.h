@@ -42,6 +42,9 @@ __device__ __forceinline__ constexpr int upper_tile(int m, int kb) {
     return m < 2 ? 2 * m + kb : 2 + m;
 }
 
+// tile_row(m, 4 g + r) = 8 g + tile_base(m) + r
+__device__ __forceinline__ constexpr int tile_base(int m) { return 32 * (m >> 1) + 4 * (m & 1); }
+
 struct Span {
     long long b, t0, slot0;
     int len;
@@ -107,11 +110,12 @@ __device__ __forceinline__ void io_store(void* p, long long i, float x) {
 template <int IO>
 __device__ __forceinline__ void load4(const void* p, long long i, bool ok, float (&x)[4]) {
     if constexpr (IO == IO_F32) {
-        const float4 a = ok ? *(const float4*)((const float*)p + i) : make_float4(0, 0, 0, 0);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        const float4 a = *(const float4*)((const float*)p + (ok ? i : 0));
+        x[0] = ok ? a.x : 0.f; x[1] = ok ? a.y : 0.f;
+        x[2] = ok ? a.z : 0.f; x[3] = ok ? a.w : 0.f;
     } else {
-        const uint2 a = ok ? *(const uint2*)((const uint16_t*)p + i) : make_uint2(0, 0);
-        const uint32_t u[2] = {a.x, a.y};
+        const uint2 a = *(const uint2*)((const uint16_t*)p + (ok ? i : 0));
+        const uint32_t u[2] = {ok ? a.x : 0, ok ? a.y : 0};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if constexpr (IO == IO_BF16) {
@@ -185,78 +189,146 @@ __device__ __forceinline__ dfloat4 mma_terms(const uint4 (&a)[NA], const uint4 (
     return c;
 }
 
-// eight consecutive elements of the I/O type as NA bf16 terms
+// c[m] += a[m] b for M tiles: the same products, but consecutive instructions
+// go to different accumulators
+template <int LIM, int M, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(const uint4 (&a)[M][NA], const uint4 (&b)[NB],
+                                          dfloat4 (&c)[M]) {
+#pragma unroll
+    for (int w = LIM - 1; w >= 0; --w)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = w - i;
+            if (j >= 0 && j < NB)
+#pragma unroll
+                for (int m = 0; m < M; ++m) c[m] = mma(a[m][i], b[j], c[m]);
+        }
+}
+
+// Loads under a condition read the tensor's first elements where it does not
+// hold and drop them: a load inside a branch would have to arrive before the
+// branch ends, one latency after the other.
+__device__ __forceinline__ uint4 keep(bool ok, uint4 x) {
+    return make_uint4(ok ? x.x : 0, ok ? x.y : 0, ok ? x.z : 0, ok ? x.w : 0);
+}
+template <int IO>
+__device__ __forceinline__ float io_load_if(const void* p, long long i, bool ok) {
+    const float x = io_load<IO>(p, ok ? i : 0);
+    return ok ? x : 0.f;
+}
+
+// eight consecutive elements
+template <int IO>
+__device__ __forceinline__ void load8(const void* p, long long i, bool ok, float (&x)[8]) {
+    if constexpr (IO == IO_F32) {
+        const uint4* s = (const uint4*)((const float*)p + (ok ? i : 0));
+        const uint4 a = keep(ok, s[0]), b = keep(ok, s[1]);
+        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
+    } else {
+        const uint4 a = keep(ok, *(const uint4*)((const uint16_t*)p + (ok ? i : 0)));
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (IO == IO_BF16) {
+                x[2 * j] = __uint_as_float(u[j] << 16);
+                x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+            } else {
+                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+                const h2 h = __builtin_bit_cast(h2, u[j]);
+                x[2 * j] = (float)h.x;
+                x[2 * j + 1] = (float)h.y;
+            }
+        }
+    }
+}
+// the same as bf16 terms
 template <int IO>
 __device__ __forceinline__ void load_terms(const void* p, long long i, bool ok,
                                            uint4 (&t)[IoTerms<IO>::n]) {
     if constexpr (IO == IO_BF16) {
-        t[0] = ok ? *(const uint4*)((const uint16_t*)p + i) : make_uint4(0, 0, 0, 0);
+        t[0] = keep(ok, *(const uint4*)((const uint16_t*)p + (ok ? i : 0)));
     } else {
         float x[8];
-        if constexpr (IO == IO_F16) {
-            typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-            const uint4 r = ok ? *(const uint4*)((const uint16_t*)p + i) : make_uint4(0, 0, 0, 0);
-            const h8 h = __builtin_bit_cast(h8, r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = (float)h[j];
-        } else {
-            float4 a = make_float4(0, 0, 0, 0), b = a;
-            if (ok) {
-                a = *(const float4*)((const float*)p + i);
-                b = *(const float4*)((const float*)p + i + 4);
-            }
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        }
+        load8<IO>(p, i, ok, x);
         split8<IoTerms<IO>::n>(x, t);
     }
 }
 
-// Where lanes without an element read from.
-static __device__ __align__(16) uint32_t kNothing[4] = {0, 0, 0, 0};
-
-// 16 bytes a lane from global memory to LDS, to consecutive places from `dst`
-// (the same for the wave) on, without passing through registers.
-__device__ __forceinline__ void dma16(uint4* dst, const void* src) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-}
-// The wave's loads, those to LDS among them, are done.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// `kb` KiB from global memory to LDS by the four waves.
-__device__ __forceinline__ void copy_lds(uint4* dst, const uint4* src, int kb) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    for (int i = wave; i < kb; i += 4) dma16(dst + i * 64, src + i * 64 + lane);
-}
-
-// Fills the A operands of 64 tokens x DK of a head in LDS.  Tile (m, kb),
-// place 16 g + (c ^ 4 g) holds [token tile_row(m, c)][32 kb + 8 g + i], i < 8;
-// the exclusive or spreads the four groups over the banks for the transposed
-// reads.  Tokens from n on and elements from Dk on are 0.
+// Operands go from global memory to LDS through registers: the loads of the
+// next chunk are in flight while the present one is worked on.  (Loads
+// straight to LDS were tried: the compiler lets no later LDS read pass them,
+// as they might write what it reads, and each chunk waited for its own
+// prefetch.)
+//
+// The A operands of 64 tokens x DK of a head.  In LDS, tile (m, kb), place
+// 16 g + (c ^ 4 g) holds [token tile_row(m, c)][32 kb + 8 g + i], i < 8; the
+// exclusive or spreads the four groups over the banks for the transposed
+// reads.  Tokens from n on and elements from Dk on are 0.  Four waves.
 template <int IO, int DK>
-__device__ __forceinline__ void fill_rows(uint4* dst, const void* src, long long base,
-                                          long long stride, int n, int Dk) {
-    constexpr int KB = DK / 32, kTiles = 4 * KB;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int g = lane >> 4, c = (lane & 15) ^ (4 * g);
+struct RowTiles {
+    static constexpr int KB = DK / 32, kTiles = 4 * KB;
+    static constexpr int kWords = IO == IO_F32 ? 2 : 1;
+    uint4 r[KB][kWords];
+    __device__ __forceinline__ void load(const void* src, long long base, long long stride, int n,
+                                         int Dk) {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int g = lane >> 4, c = (lane & 15) ^ (4 * g);
 #pragma unroll
-    for (int j = 0; j < KB; ++j) {
-        const int tile = 4 * j + wave, m = tile / KB, kb = tile - m * KB;
-        const int row = tile_row(m, c), e = 32 * kb + 8 * g;
-        const bool ok = row < n && e < Dk;
-        if constexpr (IO != IO_F32) {
-            dma16(dst + tile * 64,
-                  ok ? (const void*)((const uint16_t*)src + base + row * stride + e)
-                     : (const void*)kNothing);
-        } else {
-            uint4 t[3];
-            load_terms<IO>(src, base + row * stride + e, ok, t);
+        for (int j = 0; j < KB; ++j) {
+            const int tile = 4 * j + wave, m = tile / KB, kb = tile - m * KB;
+            const int row = tile_row(m, c), e = 32 * kb + 8 * g;
+            const bool ok = row < n && e < Dk;
+            const long long i = ok ? base + row * stride + e : 0;
+            const uint4* s = IO == IO_F32 ? (const uint4*)((const float*)src + i)
+                                          : (const uint4*)((const uint16_t*)src + i);
 #pragma unroll
-            for (int a = 0; a < 3; ++a) dst[a * kTiles * 64 + tile * 64 + lane] = t[a];
+            for (int w = 0; w < kWords; ++w) r[j][w] = keep(ok, s[w]);
         }
     }
-}
+    __device__ __forceinline__ void store(uint4* dst) const {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const int at = (4 * j + wave) * 64 + lane;
+            if constexpr (IO == IO_F32) {
+                const uint4 a = r[j][0], b = r[j][1];
+                const float x[8] = {__uint_as_float(a.x), __uint_as_float(a.y),
+                                    __uint_as_float(a.z), __uint_as_float(a.w),
+                                    __uint_as_float(b.x), __uint_as_float(b.y),
+                                    __uint_as_float(b.z), __uint_as_float(b.w)};
+                uint4 t[3];
+                split8<3>(x, t);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) dst[i * kTiles * 64 + at] = t[i];
+            } else {
+                dst[at] = r[j][0];
+            }
+        }
+    }
+};
+// N KiB of consecutive memory.  Four waves; those without a last piece of
+// their own move the last one too, with the same values.  (In clang's own
+// vector type: copies of HIP's, a struct, end up in scratch memory here.)
+template <int N>
+struct Block {
+    typedef uint32_t v4 __attribute__((ext_vector_type(4)));
+    static constexpr int kMine = (N + 3) / 4;
+    v4 r[kMine];
+    static __device__ __forceinline__ int place(int j) {
+        const int i = 4 * j + (threadIdx.x >> 6);
+        return (i < N ? i : N - 1) * 64 + (threadIdx.x & 63);
+    }
+    __device__ __forceinline__ void load(const uint4* src) {
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) r[j] = ((const v4*)src)[place(j)];
+    }
+    __device__ __forceinline__ void store(uint4* dst) const {
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) ((v4*)dst)[place(j)] = r[j];
+    }
+};
 // The transposed operand from rows so filled: tile (t, tb), the lane's
 // [element tile_row(t, c)][token 32 tb + 8 g + i], i < 8.  Each transposed
 // read takes four tokens x 16 elements for 16 lanes.
@@ -332,6 +404,24 @@ struct Operand {
                                                   dfloat4 c) {
         if constexpr (kScaled) return mma_h(a[0], b[0], mma_h(a[0], b[1], c));
         else return mma_terms<3>(a, b, c);
+    }
+    template <int M>
+    static __device__ __forceinline__ void mma_all(const uint4 (&a)[M][NA], const uint4 (&b)[NB],
+                                                   dfloat4 (&c)[M]) {
+        if constexpr (kScaled) {
+#pragma unroll
+            for (int i = 1; i >= 0; --i)
+#pragma unroll
+                for (int m = 0; m < M; ++m) c[m] = mma_h(a[m][0], b[i], c[m]);
+        } else {
+            mma_tiles<3>(a, b, c);
+        }
+    }
+    template <int M>
+    static __device__ __forceinline__ void mma_all_out(const uint4 (&a)[M][NA],
+                                                       const uint4 (&b)[NB], dfloat4 (&c)[M]) {
+        if constexpr (kScaled) mma_all(a, b, c);
+        else mma_tiles<NP>(a, b, c);
     }
     // where a 16-bit output is all that follows, 16 bits of b
     static __device__ __forceinline__ dfloat4 mma_out(const uint4 (&a)[NA], const uint4 (&b)[NB],
