@@ -16,7 +16,6 @@
 // T and P need no state: delta_prep_kernel makes them for all chunks at
 // once.  delta_scan_kernel then walks over a sequence's chunks.
 #include "fftconv_delta_dev.h"
-#include <stdlib.h>
 
 namespace fftconv {
 namespace {
@@ -207,11 +206,17 @@ __device__ __forceinline__ void store_tri_transposed(const float (*t)[kLd], uint
     }
 }
 
+template <int IO, int DK>
+struct PrepLds {
+    static constexpr int kRows = Operand<IO>::NA * 4 * (DK / 32) * 64;   // uint4
+    static constexpr int kMat = kChunk * kLd / 4;
+    static constexpr int kBytes = 32 * (kRows > kMat ? kRows : kMat);
+};
 // One workgroup per chunk and value head.
 template <int IO, int DK>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     typedef Operand<IO> Op;
-    constexpr int NA = IoTerms<IO>::n, KB = DK / 32;
+    constexpr int NA = Op::NA, KB = DK / 32;
     const long long id = xcd_unit(blockIdx.x, p.slots * p.Hv);
     if (id >= p.slots * p.Hv) return;
     const long long slot = id / p.Hv;
@@ -223,52 +228,67 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     const int n = (int)(sp.len - at < kChunk ? sp.len - at : kChunk);
     const long long tok = sp.t0 + at;
 
-    __shared__ __align__(16) float A[kChunk][kLd], P[kChunk][kLd];
+    // keys and queries first, then the 64 x 64 matrices
+    extern __shared__ uint4 lds[];
+    float (*A)[kLd] = (float (*)[kLd])lds;
+    float (*P)[kLd] = A + kChunk;
     __shared__ double G[kChunk];
     __shared__ float bet[kChunk];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = lane & 15, g4 = lane >> 4;
-    if (wave == 0) {
-        const long long gi = (sp.b * p.T + tok + lane) * p.Hv + h;
-        const float gv = lane < n ? p.g[gi] : 0.f;
-        const float bv = lane < n ? p.beta[gi] : 0.f;
-        const double s = decay_sum(gv);
-        G[lane] = s;
-        bet[lane] = bv;
-        const double last = __shfl(s, 63);
-        const float eg = expf((float)s), ee = expf((float)(last - s)), ec = expf((float)last);
-        for (uint4* d : {p.pack + id * Op::kPack, p.bpack ? p.bpack + id * kBackPack : nullptr})
-            if (d) {
-                float* dec = (float*)(d + 3 * kTriTiles * 64);
-                dec[lane] = eg;
-                dec[64 + lane] = ee;
-                dec[128 + lane] = bv;
-                dec[192 + lane] = ec;
-            }
-    }
-    // scores of the 16 rows of the wave against the columns up to them
+    const int c = lane & 15, g4 = lane >> 4, rslot = 16 * g4 + (c ^ (4 * g4));
     const int hk = h / p.group;
-    const long long kbase = sp.b * p.ks[0] + hk * p.ks[2];
-    const long long qbase = sp.b * p.qs[0] + hk * p.qs[2];
+    {
+        RowTiles<IO, DK, 4> rk, rq;
+        rk.load(tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2], p.ks[1]), 0, n,
+                p.Dk);
+        rq.load(tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2], p.qs[1]), 0, n,
+                p.Dk);
+        if (wave == 0) {
+            const long long gi = (sp.b * p.T + tok + (lane < n ? lane : 0)) * p.Hv + h;
+            float gv = p.g[gi], bv = p.beta[gi];
+            gv = lane < n ? gv : 0.f;
+            bv = lane < n ? bv : 0.f;
+            const double s = decay_sum(gv);
+            G[lane] = s;
+            bet[lane] = bv;
+            const double last = __shfl(s, 63);
+            const float eg = expf((float)s), ee = expf((float)(last - s)),
+                        ec = expf((float)last);
+            for (uint4* d : {p.pack + id * Op::kPack, p.bpack ? p.bpack + id * kBackPack : nullptr})
+                if (d) {
+                    float* dec = (float*)(d + 3 * kTriTiles * 64);
+                    dec[lane] = eg;
+                    dec[64 + lane] = ee;
+                    dec[128 + lane] = bv;
+                    dec[192 + lane] = ec;
+                }
+        }
+        rk.store(lds);
+        rq.store(lds + PrepLds<IO, DK>::kRows);
+    }
+    __syncthreads();
+    // scores of the wave's tokens, tile_row(wave, .), against those of the
+    // tiles up to it
     dfloat4 kk[4], qk[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) kk[j] = qk[j] = dfloat4{0, 0, 0, 0};
+    const int jtiles = wave < 2 ? 2 : 4;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-        const int e = 32 * kb + 8 * g4;
         uint4 ka[NA], qa[NA];
-        const int row = 16 * wave + c;
-        const bool ok = row < n && e < p.Dk;
-        load_terms<IO>(p.k, kbase + (tok + row) * p.ks[1] + e, ok, ka);
-        load_terms<IO>(p.q, qbase + (tok + row) * p.qs[1] + e, ok, qa);
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            ka[i] = lds[((i * 4 + wave) * KB + kb) * 64 + rslot];
+            qa[i] = lds[PrepLds<IO, DK>::kRows + ((i * 4 + wave) * KB + kb) * 64 + rslot];
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (j <= wave) {
+            if (j < jtiles) {
                 uint4 b[NA];
-                const int col = 16 * j + c;
-                load_terms<IO>(p.k, kbase + (tok + col) * p.ks[1] + e, col < n && e < p.Dk, b);
-                kk[j] = mma_terms<3>(ka, b, kk[j]);
-                qk[j] = mma_terms<3>(qa, b, qk[j]);
+#pragma unroll
+                for (int i = 0; i < NA; ++i) b[i] = lds[((i * 4 + j) * KB + kb) * 64 + rslot];
+                kk[j] = Op::mma_io(ka, b, kk[j]);
+                qk[j] = Op::mma_io(qa, b, qk[j]);
             }
     }
     __syncthreads();
@@ -276,7 +296,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int row = 16 * wave + 4 * g4 + r, col = 16 * j + c;
+            const int row = tile_row(wave, 4 * g4 + r), col = tile_row(j, c);
             const float gam = row >= col ? expf((float)(G[row] - G[col])) : 0.f;
             A[row][col] = row > col ? bet[row] * gam * kk[j][r] : 0.f;
             P[row][col] = row >= col ? p.scale * gam * qk[j][r] : 0.f;
@@ -310,23 +330,26 @@ struct ScanLds {
     static constexpr int kBytes = kBufs * kSize * 16;
 };
 
-// A wave owns NT times 16 columns of the state: its accumulators hold S (Dk x
-// 16 each), and every product of the chunk, K S, T X, P U, K^T U, takes the
-// last one's accumulators as its B operand, so the chain of a chunk has no
-// exchange and no barrier of its own.  The four waves of a workgroup share
-// the operands that do not depend on the state (K, Q, T, P) through LDS, K^T
-// being K read transposed.
-//
-// FULL: outputs and final state.  Otherwise a segment's effect on the state
-// alone: its last state from the first (the first segment of a sequence) or
-// from 0, and, in columns of their own, the matrix its first state is
-// multiplied with (the last state from the identity, without v).
-template <int IO, int DK, int NT, bool FULL>
-__global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
+// What a walk does.  kEffect: a segment's effect on the state alone: its last
+// state from the first (the first segment of a sequence) or from 0, and, in
+// columns of their own, the matrix its first state is multiplied with (the
+// last state from the identity, without v).  kOutputs: outputs and final
+// state; kSaving: and what the backward pass reads.
+enum ScanMode { kEffect, kOutputs, kSaving };
+
+// A wave owns 16 columns of the state: its accumulators hold S (Dk x 16), and
+// every product of the chunk, K S, T X, P U, K^T U, takes the last one's
+// accumulators as its B operand, so the chain of a chunk has no exchange and
+// no barrier of its own.  The W waves of a workgroup share the operands that
+// do not depend on the state (K, Q, T, P) through LDS, K^T being K read
+// transposed.
+template <int IO, int DK, int W, int MODE>
+__global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
+    constexpr bool FULL = MODE != kEffect;
     typedef ScanLds<IO, DK, FULL> L;
     typedef Operand<IO> Op;
     constexpr int NA = Op::NA, KB = DK / 32, ST = DK / 16, NP = Op::NP, NB = Op::NB;
-    constexpr int kCols = 64 * NT;
+    constexpr int kCols = 16 * W, kB = IO == IO_F32 ? 4 : 2;
     extern __shared__ uint4 lds[];
     const int vcols = (p.Dv + kCols - 1) / kCols;
     const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
@@ -352,44 +375,45 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int slot = 16 * g + (c ^ (4 * g));             // of a row operand
-    const int col0 = cb * kCols + wave * 16 * NT + c;    // and 16 further each
+    const int col = cb * kCols + wave * 16 + c;
     const int width = matrix ? p.Dk : p.Dv;
-    bool cok[NT];
-#pragma unroll
-    for (int u = 0; u < NT; ++u) cok[u] = col0 + 16 * u < width;
+    const bool cok = col < width;
+    const int colv = cok ? col : 0;                      // to read from
     const int hk = h / p.group;
     const long long state = p.Dk * (long long)p.Dv;
-    dfloat4 S[NT][ST];
+    dfloat4 S[ST];
     {
         const float* s = nullptr;
-        if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col0 : nullptr;
-        else if (FULL) s = p.seg_n + ((seg - 1) * p.Hv + h) * state + col0;
+        if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col : nullptr;
+        else if (FULL) s = p.seg_n + ((seg - 1) * p.Hv + h) * state + col;
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
+        for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int t = 0; t < ST; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = tile_row(t, 4 * g + r);
-                    S[u][t][r] = matrix ? (row == col0 + 16 * u ? 1.f : 0.f)
-                                        : (s && cok[u] && row < p.Dk
-                                               ? s[(long long)row * p.Dv + 16 * u] : 0.f);
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int row = tile_row(t, 4 * g + r);
+                S[t][r] = matrix ? (row == col ? 1.f : 0.f)
+                                 : (s && cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f);
+            }
     }
-    const long long kbase = sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2];
-    const long long qbase = sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2];
-    const long long vbase = sp.b * p.vs[0] + sp.t0 * p.vs[1] + h * p.vs[2] + col0;
-    const long long ostride = (long long)p.Hv * p.Dv;
-    const long long obase = ((sp.b * p.T + sp.t0) * p.Hv + h) * p.Dv + col0;
+    const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2], p.ks[1]);
+    const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2], p.qs[1]);
+    const Tokens tv = tokens_of<IO>(p.v, sp.b * p.vs[0] + sp.t0 * p.vs[1] + h * p.vs[2], p.vs[1]);
+    const Tokens to = tokens_of<IO>(p.o, (sp.b * p.T + sp.t0) * p.Hv * p.Dv + h * p.Dv,
+                                    (long long)p.Hv * p.Dv);
+    const uint32_t vlane = (uint32_t)(8 * g) * (uint32_t)tv.bytes + colv * kB;
+    const uint32_t olane = (uint32_t)(8 * g) * (uint32_t)to.bytes + col * kB;
+    const uint32_t slane = (uint32_t)(8 * g * p.Dv + col) * 4;
+    const uint4* pack = p.pack + (sp.slot0 * p.Hv + h) * Op::kPack;
+    const long long pack_step = (long long)p.Hv * Op::kPack;
 
-    RowTiles<IO, DK> rk, rq;
-    Block<L::kPackKb> rp;
-    float v[NT][4][4];
+    RowTiles<IO, DK, W> rk, rq;
+    Block<L::kPackKb, W> rp;
+    dfloat4 v[4];
     const auto load = [&](int ch) __attribute__((always_inline)) {
         const int n = sp.len - ch * kChunk;
-        rk.load(p.k, kbase + ch * (kChunk * p.ks[1]), p.ks[1], n, p.Dk);
-        if (FULL) rq.load(p.q, qbase + ch * (kChunk * p.qs[1]), p.qs[1], n, p.Dk);
-        rp.load(p.pack + ((sp.slot0 + ch) * p.Hv + h) * Op::kPack);
+        rk.load(tk, ch * kChunk, n, p.Dk);
+        if (FULL) rq.load(tq, ch * kChunk, n, p.Dk);
+        rp.load(pack + ch * pack_step);
     };
     const auto store = [&](uint4* d) __attribute__((always_inline)) {
         rk.store(d + L::kK);
@@ -397,19 +421,10 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
         rp.store(d + L::kTri);
     };
     const auto load_v = [&](int ch) __attribute__((always_inline)) {
-        const int n = sp.len - ch * kChunk - 8 * g;
-        const long long at = vbase + (ch * kChunk + 8 * g) * p.vs[1];
-#pragma unroll
-        for (int u = 0; u < NT; ++u)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = tile_base(m) + r;
-                    v[u][m][r] = io_load_if<IO>(p.v, at + row * p.vs[1] + 16 * u,
-                                                !matrix && cok[u] && row < n);
-                }
+        if (!matrix) load_column<IO>(tv, ch * kChunk, vlane, sp.len - ch * kChunk, v);
     };
+#pragma unroll
+    for (int m = 0; m < 4; ++m) v[m] = dfloat4{0, 0, 0, 0};
     if (first < last) {
         load(first);
         load_v(first);
@@ -420,32 +435,17 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
     uint4* next = lds + (L::kBufs == 2 ? L::kSize : 0);
     for (int ch = first; ch < last; ++ch) {
         const long long ci = (sp.slot0 + ch) * p.Hv + h;
-        const int n = sp.len - ch * kChunk - 8 * g;      // of the group's tokens
+        const int n = sp.len - ch * kChunk;
         const int ahead = ch + 1 < last ? ch + 1 : ch;
         load(ahead);
         const float* dec = (const float*)(now + L::kDec);
-        if (FULL && p.states)
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                float* d = p.states + ci * state + (long long)(8 * g) * p.Dv + col0 + 16 * u;
-                if (cok[u])
-#pragma unroll
-                    for (int t = 0; t < ST; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int row = tile_base(t) + r;
-                            if (8 * g + row < p.Dk) d[(long long)row * p.Dv] = S[u][t][r];
-                        }
-            }
+        if (MODE == kSaving && cok)
+            store_state<ST>((char*)(p.states + ci * state), p.Dv * 4, slane, p.Dk, S);
         // K S and Q S
-        dfloat4 X[NT][4], O[NT][4];
-        ColScale sc[NT];
+        dfloat4 X[4], O[4];
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) X[u][m] = O[u][m] = dfloat4{0, 0, 0, 0};
-            sc[u] = Op::template scale_of<ST>(S[u]);
-        }
+        for (int m = 0; m < 4; ++m) X[m] = O[m] = dfloat4{0, 0, 0, 0};
+        const ColScale sc = Op::template scale_of<ST>(S);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             uint4 a[4][NA], q[4][NA];
@@ -456,13 +456,10 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
                     a[m][i] = now[L::kK + ((i * 4 + m) * KB + kb) * 64 + slot];
                     if (FULL) q[m][i] = now[L::kQ + ((i * 4 + m) * KB + kb) * 64 + slot];
                 }
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                uint4 st[NB];
-                Op::split(S[u][2 * kb], S[u][2 * kb + 1], sc[u], st);
-                Op::mma_all(a, st, X[u]);
-                if (FULL) Op::mma_all_out(q, st, O[u]);
-            }
+            uint4 st[NB];
+            Op::split(S[2 * kb], S[2 * kb + 1], sc, st);
+            Op::mma_all(a, st, X);
+            if (FULL) Op::mma_all_out(q, st, O);
         }
         // X = beta o (V - e^G o K S);  O = scale e^G o Q S
 #pragma unroll
@@ -471,22 +468,21 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
             const float4 e = *(const float4*)(dec + row), b = *(const float4*)(dec + 128 + row);
             const float ev[4] = {e.x, e.y, e.z, e.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    X[u][m][r] = bv[r] * (v[u][m][r] - ev[r] * (X[u][m][r] * sc[u].back));
-                    if (FULL) O[u][m][r] = p.scale * ev[r] * (O[u][m][r] * sc[u].back);
-                }
+            for (int r = 0; r < 4; ++r) {
+                const float es = ev[r] * sc.back;
+                X[m][r] = bv[r] * fmaf(-es, X[m][r], v[m][r]);
+                if (FULL) O[m][r] = p.scale * es * O[m][r];
+            }
         }
         load_v(ahead);
         // U = T X
-        dfloat4 U[NT][4];
+        dfloat4 U[4];
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
+        for (int m = 0; m < 4; ++m) U[m] = dfloat4{0, 0, 0, 0};
 #pragma unroll
-            for (int m = 0; m < 4; ++m) U[u][m] = dfloat4{0, 0, 0, 0};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb) {
+            uint4 xt[3];
+            split_acc<3>(X[2 * kb], X[2 * kb + 1], xt);
 #pragma unroll
             for (int m0 = 2 * kb; m0 < 4; m0 += 2) {
                 uint4 a[2][3];
@@ -495,28 +491,18 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
 #pragma unroll
                     for (int i = 0; i < 3; ++i)
                         a[m][i] = now[L::kTri + (i * kTriTiles + tri_tile(m0 + m, kb)) * 64 + lane];
-#pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    uint4 xt[3];
-                    split_acc<3>(X[u][2 * kb], X[u][2 * kb + 1], xt);
-                    mma_tiles<3>(a, xt, *(dfloat4 (*)[2])&U[u][m0]);
-                }
+                mma_tiles<3>(a, xt, *(dfloat4 (*)[2])&U[m0]);
             }
+        }
         if (FULL) {
-            if (p.us)
-#pragma unroll
-                for (int u = 0; u < NT; ++u) {
-                    float* d = p.us + (ci * kChunk + 8 * g) * p.Dv + col0 + 16 * u;
-                    if (cok[u])
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                d[(long long)(tile_base(m) + r) * p.Dv] = U[u][m][r];
-                }
+            if (MODE == kSaving && cok)
+                store_column<IO_F32>((char*)(p.us + ci * kChunk * p.Dv), p.Dv * 4, slane, kChunk,
+                                     U);
             // O += P U
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+            for (int kb = 0; kb < 2; ++kb) {
+                uint4 ut[NP];
+                split_acc<NP>(U[2 * kb], U[2 * kb + 1], ut);
 #pragma unroll
                 for (int m0 = 2 * kb; m0 < 4; m0 += 2) {
                     uint4 a[2][NP];
@@ -526,67 +512,34 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
                         for (int i = 0; i < NP; ++i)
                             a[m][i] =
                                 now[L::kP + (i * kTriTiles + tri_tile(m0 + m, kb)) * 64 + lane];
-#pragma unroll
-                    for (int u = 0; u < NT; ++u) {
-                        uint4 ut[NP];
-                        split_acc<NP>(U[u][2 * kb], U[u][2 * kb + 1], ut);
-                        mma_tiles<NP>(a, ut, *(dfloat4 (*)[2])&O[u][m0]);
-                    }
-                }
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const long long at = obase + (ch * kChunk + 8 * g) * ostride + 16 * u;
-                if (!cok[u]) continue;
-                if (sp.len - ch * kChunk >= kChunk) {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            io_store<IO>(p.o, at + (tile_base(m) + r) * ostride, O[u][m][r]);
-                } else {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (tile_base(m) + r < n)
-                                io_store<IO>(p.o, at + (tile_base(m) + r) * ostride, O[u][m][r]);
+                    mma_tiles<NP>(a, ut, *(dfloat4 (*)[2])&O[m0]);
                 }
             }
+            if (cok) store_column<IO>((char*)to.at(ch * kChunk), to.bytes, olane, n, O);
         }
         // e^(Gc-G) o U
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const float4 e = *(const float4*)(dec + 64 + tile_row(m, 4 * g));
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                U[u][m][0] *= e.x;
-                U[u][m][1] *= e.y;
-                U[u][m][2] *= e.z;
-                U[u][m][3] *= e.w;
-            }
+            U[m][0] *= e.x;
+            U[m][1] *= e.y;
+            U[m][2] *= e.z;
+            U[m][3] *= e.w;
         }
         const float ec = dec[192];
         if (L::kBufs == 2) store(next);
         // S = e^Gc S + K^T U
-        ColScale su[NT];
-        uint4 ut[NT][2][NB];
+        const ColScale su = Op::template scale_of<4>(U);
+        uint4 ut[2][NB];
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            su[u] = Op::template scale_of<4>(U[u]);
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb)
-                Op::split(U[u][2 * tb], U[u][2 * tb + 1], su[u], ut[u][tb]);
-        }
+        for (int tb = 0; tb < 2; ++tb) Op::split(U[2 * tb], U[2 * tb + 1], su, ut[tb]);
 #pragma unroll
         for (int t0 = 0; t0 < ST; t0 += 4) {
-            dfloat4 a[NT][4];
+            dfloat4 a[4];
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        a[u][t][r] = Op::kScaled ? 0.f : ec * S[u][t0 + t][r];
+                for (int r = 0; r < 4; ++r) a[t][r] = Op::kScaled ? 0.f : ec * S[t0 + t][r];
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
                 uint4 x[4][NA];
@@ -595,18 +548,14 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
 #pragma unroll
                     for (int i = 0; i < NA; ++i)
                         x[t][i] = read_cols<DK>(now + L::kK + i * 4 * KB * 64, t0 + t, tb);
-#pragma unroll
-                for (int u = 0; u < NT; ++u) Op::mma_all(x, ut[u][tb], a[u]);
+                Op::mma_all(x, ut[tb], a);
             }
 #pragma unroll
-            for (int u = 0; u < NT; ++u)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        S[u][t0 + t][r] = Op::kScaled
-                                              ? ec * S[u][t0 + t][r] + su[u].back * a[u][t][r]
-                                              : a[u][t][r];
+                for (int r = 0; r < 4; ++r)
+                    S[t0 + t][r] =
+                        Op::kScaled ? fmaf(su.back, a[t][r], ec * S[t0 + t][r]) : a[t][r];
         }
         __syncthreads();
         if (L::kBufs == 2) {
@@ -618,31 +567,31 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaParams p) {
             __syncthreads();
         }
     }
+    if (!cok) return;
     float* d = nullptr;
     if (FULL) d = p.fin && last == chunks ? p.fin + (seq * p.Hv + h) * state : nullptr;
     else if (matrix) d = p.seg_m + (seg * p.Hv + h) * p.Dk * (long long)p.Dk;
     else d = p.seg_n + (seg * p.Hv + h) * state;
-    if (!d) return;
-#pragma unroll
-    for (int u = 0; u < NT; ++u)
-        if (cok[u])
-#pragma unroll
-            for (int t = 0; t < ST; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = tile_row(t, 4 * g + r);
-                    if (row < p.Dk) d[(long long)row * width + col0 + 16 * u] = S[u][t][r];
-                }
+    if (d) store_state<ST>((char*)d, width * 4, (uint32_t)(8 * g * width + col) * 4, p.Dk, S);
 }
 
 // Joins the segments of a sequence: with N the last state of a segment from 0
 // and M the matrix of the segment, the state after it is M S + N.  Leaves in
-// place of N the state after each segment but the last.  A wave takes 16
-// columns, as in the walk.
+// place of N the state after each segment but the last.  The eight waves of a
+// workgroup take 16 columns each, as in the walk, and share M through LDS, the
+// next one's loads in flight.
 template <int DK>
-__global__ __launch_bounds__(64) void delta_join_kernel(DeltaParams p) {
+struct JoinLds {
+    static constexpr int kHalves = DK / 64;             // 64 rows of M each
+    static constexpr int kRows = 3 * 4 * (DK / 32) * 64;
+    static constexpr int kBytes = kHalves * kRows * 16;
+};
+template <int DK>
+__global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
+    typedef JoinLds<DK> L;
     constexpr int KB = DK / 32, ST = DK / 16;
-    const int cols = (p.Dv + 15) / 16;
+    extern __shared__ uint4 lds[];
+    const int cols = (p.Dv + 127) / 128;
     long long id = blockIdx.x;
     const int cb = (int)(id % cols);
     id /= cols;
@@ -652,54 +601,66 @@ __global__ __launch_bounds__(64) void delta_join_kernel(DeltaParams p) {
     const int chunks = (sp.len + kChunk - 1) / kChunk;
     const int n = (chunks + p.seg_chunks - 1) / p.seg_chunks;   // segments
     if (n < 3) return;           // the first segment's state is already whole
-    const int lane = threadIdx.x, c = lane & 15, g = lane >> 4;
-    const int col = cb * 16 + c;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = lane & 15, g = lane >> 4, slot = 16 * g + (c ^ (4 * g));
+    const int col = cb * 128 + wave * 16 + c;
     const bool cok = col < p.Dv;
     const long long state = p.Dk * (long long)p.Dv, square = p.Dk * (long long)p.Dk;
     const long long seg0 = seg_of(p, sp, seq);
-    dfloat4 S[ST];
-    const auto at = [&](long long seg) __attribute__((always_inline)) { return p.seg_n + (seg * p.Hv + h) * state + col; };
-    const float* s = at(seg0);
-#pragma unroll
-    for (int t = 0; t < ST; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = tile_row(t, 4 * g + r);
-            S[t][r] = cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f;
-        }
-    for (int i = 1; i + 1 < n; ++i) {
-        const float* M = p.seg_m + ((seg0 + i) * p.Hv + h) * square;
-        float* d = at(seg0 + i);
-        dfloat4 R[ST];
+    const uint32_t slane = (uint32_t)(8 * g * p.Dv + col) * 4;
+    dfloat4 S[ST], R[ST];
+    RowTiles<IO_F32, DK, 8> rm[L::kHalves];
+    const auto load = [&](int i, dfloat4 (&x)[ST]) __attribute__((always_inline)) {
+        const long long at = ((seg0 + i) * p.Hv + h) * state;
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = tile_row(t, 4 * g + r);
-                R[t][r] = io_load_if<IO_F32>(p.seg_n, d - p.seg_n + (long long)row * p.Dv,
+                x[t][r] = io_load_if<IO_F32>(p.seg_n, at + (long long)row * p.Dv + col,
                                              cok && row < p.Dk);
             }
+    };
+    const auto load_m = [&](int i) __attribute__((always_inline)) {
+        const Tokens m = tokens_of<IO_F32>(p.seg_m, ((seg0 + i) * p.Hv + h) * square, p.Dk);
+#pragma unroll
+        for (int j = 0; j < L::kHalves; ++j) {
+            const int rows = p.Dk - 64 * j;
+            rm[j].load(m, rows > 0 ? 64 * j : 0, rows > 0 ? rows : 0, p.Dk);
+        }
+    };
+    load(0, S);
+    load_m(1);
+    load(1, R);
+    for (int i = 1; i + 1 < n; ++i) {
+#pragma unroll
+        for (int j = 0; j < L::kHalves; ++j) rm[j].store(lds + j * L::kRows);
+        __syncthreads();
+        const int ahead = i + 2 < n ? i + 1 : i;
+        load_m(ahead);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             uint4 b[3];
             split_acc<3>(S[2 * kb], S[2 * kb + 1], b);
 #pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                const int row = tile_row(t, c), e = 32 * kb + 8 * g;
-                uint4 a[3];
-                load_terms<IO_F32>(M, row * (long long)p.Dk + e, row < p.Dk && e < p.Dk, a);
-                R[t] = mma_terms<3>(a, b, R[t]);
+            for (int t0 = 0; t0 < ST; t0 += 2) {
+                uint4 a[2][3];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        a[t][j] = lds[((t0 + t) >> 2) * L::kRows +
+                                      ((j * 4 + ((t0 + t) & 3)) * KB + kb) * 64 + slot];
+                mma_tiles<3>(a, b, *(dfloat4 (*)[2])&R[t0]);
             }
         }
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            S[t] = R[t];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = tile_row(t, 4 * g + r);
-                if (cok && row < p.Dk) d[(long long)row * p.Dv] = R[t][r];
-            }
-        }
+        for (int t = 0; t < ST; ++t) S[t] = R[t];
+        if (cok)
+            store_state<ST>((char*)(p.seg_n + ((seg0 + i) * p.Hv + h) * state), p.Dv * 4, slane,
+                            p.Dk, S);
+        load(ahead, R);
+        __syncthreads();
     }
 }
 
@@ -713,45 +674,51 @@ hipError_t step_io(const DeltaStepParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int IO, int DK, int NT, bool FULL>
+template <int IO, int DK, int W, int MODE>
 hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
-    const int bytes = ScanLds<IO, DK, FULL>::kBytes;
-    const hipError_t e = hipFuncSetAttribute((const void*)delta_scan_kernel<IO, DK, NT, FULL>,
+    const int bytes = ScanLds<IO, DK, MODE != kEffect>::kBytes;
+    const hipError_t e = hipFuncSetAttribute((const void*)delta_scan_kernel<IO, DK, W, MODE>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int width = 64 * NT;
-    const int cols = (p.Dv + width - 1) / width + (FULL ? 0 : (p.Dk + width - 1) / width);
+    const int width = 16 * W;
+    const int cols = (p.Dv + width - 1) / width +
+                     (MODE == kEffect ? (p.Dk + width - 1) / width : 0);
     const long long units = p.segs * p.Hv * cols;
-    hipLaunchKernelGGL((delta_scan_kernel<IO, DK, NT, FULL>), dim3((unsigned)xcd_blocks(units)),
-                       dim3(256), bytes, s, p);
+    hipLaunchKernelGGL((delta_scan_kernel<IO, DK, W, MODE>), dim3((unsigned)xcd_blocks(units)),
+                       dim3(64 * W), bytes, s, p);
     return hipGetLastError();
 }
 
-template <int IO, int DK, int NT>
-hipError_t scan_nt(const DeltaParams& p, hipStream_t s) {
+template <int IO, int DK, int W>
+hipError_t scan_w(const DeltaParams& p, hipStream_t s) {
     if (p.seg_m) {
-        hipError_t e = scan_launch<IO, DK, NT, false>(p, s);
+        hipError_t e = scan_launch<IO, DK, W, kEffect>(p, s);
         if (e != hipSuccess) return e;
-        const long long joins = p.nseq * p.Hv * ((p.Dv + 15) / 16);
-        hipLaunchKernelGGL((delta_join_kernel<DK>), dim3((unsigned)joins), dim3(64), 0, s, p);
+        const int lds = JoinLds<DK>::kBytes;
+        e = hipFuncSetAttribute((const void*)delta_join_kernel<DK>,
+                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        const long long joins = p.nseq * p.Hv * ((p.Dv + 127) / 128);
+        hipLaunchKernelGGL((delta_join_kernel<DK>), dim3((unsigned)joins), dim3(512), lds, s, p);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return scan_launch<IO, DK, NT, true>(p, s);
+    return p.states ? scan_launch<IO, DK, W, kSaving>(p, s)
+                    : scan_launch<IO, DK, W, kOutputs>(p, s);
 }
 template <int IO, int DK>
 hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
-    if (getenv("NT2")) return scan_nt<IO, DK, 2>(p, s);
-    return scan_nt<IO, DK, 1>(p, s);
+    return p.Dv <= 64 ? scan_w<IO, DK, 4>(p, s) : scan_w<IO, DK, 8>(p, s);
 }
 
-template <int IO>
+template <int IO, int DK>
 hipError_t prep_io(const DeltaParams& p, hipStream_t s) {
-    const dim3 grid((unsigned)xcd_blocks(p.slots * p.Hv));
-    if (p.Dk <= 64)
-        hipLaunchKernelGGL((delta_prep_kernel<IO, 64>), grid, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((delta_prep_kernel<IO, 128>), grid, dim3(256), 0, s, p);
+    const int bytes = PrepLds<IO, DK>::kBytes;
+    const hipError_t e = hipFuncSetAttribute((const void*)delta_prep_kernel<IO, DK>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((delta_prep_kernel<IO, DK>), dim3((unsigned)xcd_blocks(p.slots * p.Hv)),
+                       dim3(256), bytes, s, p);
     return hipGetLastError();
 }
 
@@ -771,10 +738,11 @@ hipError_t launch_delta_step(int io, const DeltaStepParams& p, hipStream_t s) {
 }
 
 hipError_t launch_delta_prep(int io, const DeltaParams& p, hipStream_t s) {
+    const bool d64 = p.Dk <= 64;
     switch (io) {
-    case IO_F32: return prep_io<IO_F32>(p, s);
-    case IO_F16: return prep_io<IO_F16>(p, s);
-    default: return prep_io<IO_BF16>(p, s);
+    case IO_F32: return d64 ? prep_io<IO_F32, 64>(p, s) : prep_io<IO_F32, 128>(p, s);
+    case IO_F16: return d64 ? prep_io<IO_F16, 64>(p, s) : prep_io<IO_F16, 128>(p, s);
+    default: return d64 ? prep_io<IO_BF16, 64>(p, s) : prep_io<IO_BF16, 128>(p, s);
     }
 }
 

@@ -25,6 +25,9 @@ namespace fftconv {
 
 typedef __bf16 dbf8 __attribute__((ext_vector_type(8)));
 typedef float dfloat4 __attribute__((ext_vector_type(4)));
+// Registers that hold loads in flight are of clang's own vector type: copies
+// of HIP's, a struct, end up in scratch memory here.
+typedef uint32_t du4 __attribute__((ext_vector_type(4)));
 
 template <int IO>
 struct IoTerms { static constexpr int n = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3; };
@@ -217,31 +220,39 @@ __device__ __forceinline__ float io_load_if(const void* p, long long i, bool ok)
     return ok ? x : 0.f;
 }
 
-// eight consecutive elements
+// eight elements from their bits (two vectors of an fp32 type, else one)
 template <int IO>
-__device__ __forceinline__ void load8(const void* p, long long i, bool ok, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const du4* r, float (&x)[8]) {
     if constexpr (IO == IO_F32) {
-        const uint4* s = (const uint4*)((const float*)p + (ok ? i : 0));
-        const uint4 a = keep(ok, s[0]), b = keep(ok, s[1]);
-        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
+        for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(r[j >> 2][j & 3]);
     } else {
-        const uint4 a = keep(ok, *(const uint4*)((const uint16_t*)p + (ok ? i : 0)));
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const uint32_t u = r[0][j];
             if constexpr (IO == IO_BF16) {
-                x[2 * j] = __uint_as_float(u[j] << 16);
-                x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+                x[2 * j] = __uint_as_float(u << 16);
+                x[2 * j + 1] = __uint_as_float(u & 0xffff0000u);
             } else {
                 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-                const h2 h = __builtin_bit_cast(h2, u[j]);
+                const h2 h = __builtin_bit_cast(h2, u);
                 x[2 * j] = (float)h.x;
                 x[2 * j + 1] = (float)h.y;
             }
         }
     }
+}
+// eight consecutive elements
+template <int IO>
+__device__ __forceinline__ void load8(const void* p, long long i, bool ok, float (&x)[8]) {
+    constexpr int kB = IO == IO_F32 ? 4 : 2;
+    const du4* s = (const du4*)((const char*)p + (ok ? i : 0) * kB);
+    du4 r[2];
+    r[0] = s[0];
+    if (IO == IO_F32) r[1] = s[1];
+    unpack8<IO>(r, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = ok ? x[j] : 0.f;
 }
 // the same as bf16 terms
 template <int IO>
@@ -256,79 +267,173 @@ __device__ __forceinline__ void load_terms(const void* p, long long i, bool ok,
     }
 }
 
+// The tokens of one head: a base for the whole workgroup and byte offsets of
+// the lanes below 2^32 (the host keeps token strides below 2^24 elements), so
+// that addresses cost a lane one 32-bit register.
+struct Tokens {
+    const char* base;        // first token of the sequence
+    long long bytes;         // between tokens
+    __device__ __forceinline__ const char* at(long long token) const {
+        return base + token * bytes;
+    }
+};
+template <int IO>
+__device__ __forceinline__ Tokens tokens_of(const void* p, long long first, long long stride) {
+    constexpr int kB = IO == IO_F32 ? 4 : 2;
+    return {(const char*)p + first * kB, stride * kB};
+}
+
 // Operands go from global memory to LDS through registers: the loads of the
 // next chunk are in flight while the present one is worked on.  (Loads
 // straight to LDS were tried: the compiler lets no later LDS read pass them,
 // as they might write what it reads, and each chunk waited for its own
 // prefetch.)
-//
-// The A operands of 64 tokens x DK of a head.  In LDS, tile (m, kb), place
-// 16 g + (c ^ 4 g) holds [token tile_row(m, c)][32 kb + 8 g + i], i < 8; the
-// exclusive or spreads the four groups over the banks for the transposed
-// reads.  Tokens from n on and elements from Dk on are 0.  Four waves.
-template <int IO, int DK>
+
+// The A operands of 64 tokens x DK of a head, by W waves.  In LDS, tile
+// (m, kb), place 16 g + (c ^ 4 g) holds [token tile_row(m, c)][32 kb + 8 g +
+// i], i < 8; the exclusive or spreads the four groups over the banks for the
+// transposed reads.  Tokens from n on and elements from Dk on are 0.
+template <int IO, int DK, int W>
 struct RowTiles {
     static constexpr int KB = DK / 32, kTiles = 4 * KB;
+    static constexpr int kMine = (kTiles + W - 1) / W;
     static constexpr int kWords = IO == IO_F32 ? 2 : 1;
-    uint4 r[KB][kWords];
-    __device__ __forceinline__ void load(const void* src, long long base, long long stride, int n,
-                                         int Dk) {
+    static constexpr int kB = IO == IO_F32 ? 4 : 2;
+    du4 r[kMine][kWords];
+    __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int Dk) {
         const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
         const int g = lane >> 4, c = (lane & 15) ^ (4 * g);
+        const char* s = x.at(token);
+        const uint32_t stride = (uint32_t)x.bytes;
+        const bool whole = n >= kChunk && Dk == DK;
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-            const int tile = 4 * j + wave, m = tile / KB, kb = tile - m * KB;
-            const int row = tile_row(m, c), e = 32 * kb + 8 * g;
-            const bool ok = row < n && e < Dk;
-            const long long i = ok ? base + row * stride + e : 0;
-            const uint4* s = IO == IO_F32 ? (const uint4*)((const float*)src + i)
-                                          : (const uint4*)((const uint16_t*)src + i);
+        for (int j = 0; j < kMine; ++j) {
+            const int tile = W * j + wave, m = tile / KB, kb = tile % KB;
+            const uint32_t row = tile_row(m, c), e = 32 * kb + 8 * g;
+            const bool ok = whole || ((int)row < n && (int)e < Dk);
+            const uint32_t at = ok ? row * stride + e * kB : 0;
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) r[j][w] = keep(ok, s[w]);
+            for (int w = 0; w < kWords; ++w) {
+                r[j][w] = *(const du4*)(s + at + 16 * w);
+            }
+        }
+        if (!whole) {
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                const int tile = W * j + wave, m = tile / KB, kb = tile % KB;
+                const bool ok = tile_row(m, c) < n && 32 * kb + 8 * g < Dk;
+#pragma unroll
+                for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[j][w][i] = ok ? r[j][w][i] : 0;
+            }
         }
     }
     __device__ __forceinline__ void store(uint4* dst) const {
         const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-            const int at = (4 * j + wave) * 64 + lane;
+        for (int j = 0; j < kMine; ++j) {
+            const int at = (W * j + wave) * 64 + lane;
+            if (kTiles % W && W * j + wave >= kTiles) continue;
             if constexpr (IO == IO_F32) {
-                const uint4 a = r[j][0], b = r[j][1];
-                const float x[8] = {__uint_as_float(a.x), __uint_as_float(a.y),
-                                    __uint_as_float(a.z), __uint_as_float(a.w),
-                                    __uint_as_float(b.x), __uint_as_float(b.y),
-                                    __uint_as_float(b.z), __uint_as_float(b.w)};
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[j][i >> 2][i & 3]);
                 uint4 t[3];
                 split8<3>(x, t);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) dst[i * kTiles * 64 + at] = t[i];
             } else {
-                dst[at] = r[j][0];
+                ((du4*)dst)[at] = r[j][0];
             }
         }
     }
 };
-// N KiB of consecutive memory.  Four waves; those without a last piece of
-// their own move the last one too, with the same values.  (In clang's own
-// vector type: copies of HIP's, a struct, end up in scratch memory here.)
-template <int N>
+// N KiB of consecutive memory, by W waves; those without a last piece of
+// their own move the last one too, with the same values.
+template <int N, int W>
 struct Block {
-    typedef uint32_t v4 __attribute__((ext_vector_type(4)));
-    static constexpr int kMine = (N + 3) / 4;
-    v4 r[kMine];
+    static constexpr int kMine = (N + W - 1) / W;
+    du4 r[kMine];
     static __device__ __forceinline__ int place(int j) {
-        const int i = 4 * j + (threadIdx.x >> 6);
+        const int i = W * j + (threadIdx.x >> 6);
         return (i < N ? i : N - 1) * 64 + (threadIdx.x & 63);
     }
     __device__ __forceinline__ void load(const uint4* src) {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) r[j] = ((const v4*)src)[place(j)];
+        for (int j = 0; j < kMine; ++j) r[j] = ((const du4*)src)[place(j)];
     }
     __device__ __forceinline__ void store(uint4* dst) const {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) ((v4*)dst)[place(j)] = r[j];
+        for (int j = 0; j < kMine; ++j) ((du4*)dst)[place(j)] = r[j];
     }
 };
+// Elements [8 g + tile_base(m) + r] of one column of 64 tokens, as a lane's
+// accumulators have them; `lane`: byte offset of the column and the group's
+// first token.  Tokens from n on read the last one: nothing that is made of
+// them is kept.
+template <int IO>
+__device__ __forceinline__ void load_column(const Tokens& x, long long token, uint32_t lane, int n,
+                                            dfloat4 (&v)[4]) {
+    const char* s = x.at(token);
+    if (n >= kChunk) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[m][r] = io_load<IO>(s + (tile_base(m) + r) * x.bytes + lane, 0);
+    } else {
+        const int g = (threadIdx.x >> 4) & 3;
+        const uint32_t col = lane - 8 * g * (uint32_t)x.bytes;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 8 * g + tile_base(m) + r;
+                v[m][r] = io_load<IO>(s + (row < n ? row : n - 1) * (uint32_t)x.bytes + col, 0);
+            }
+    }
+}
+template <int IO>
+__device__ __forceinline__ void store_column(char* s, long long bytes, uint32_t lane, int n,
+                                             const dfloat4 (&v)[4]) {
+    if (n >= kChunk) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                io_store<IO>(s + (tile_base(m) + r) * bytes + lane, 0, v[m][r]);
+    } else {
+        const int left = n - 8 * ((threadIdx.x >> 4) & 3);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (tile_base(m) + r < left)
+                    io_store<IO>(s + (tile_base(m) + r) * bytes + lane, 0, v[m][r]);
+    }
+}
+// A column of an fp32 matrix of 16 ST rows (rows of `bytes`): rows from Dk on
+// are left out.
+template <int ST>
+__device__ __forceinline__ void store_state(char* s, uint32_t bytes, uint32_t lane, int Dk,
+                                            const dfloat4 (&S)[ST]) {
+    if (Dk == 16 * ST) {
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *(float*)(s + (tile_base(t) + r) * bytes + lane) = S[t][r];
+    } else {
+        const int left = Dk - 8 * ((threadIdx.x >> 4) & 3);
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (tile_base(t) + r < left)
+                    *(float*)(s + (tile_base(t) + r) * bytes + lane) = S[t][r];
+    }
+}
 // The transposed operand from rows so filled: tile (t, tb), the lane's
 // [element tile_row(t, c)][token 32 tb + 8 g + i], i < 8.  Each transposed
 // read takes four tokens x 16 elements for 16 lanes.
@@ -347,6 +452,34 @@ __device__ __forceinline__ uint4 read_cols(const uint4* rows, int t, int tb) {
         r[half] = __builtin_bit_cast(uint2, x);
     }
     return make_uint4(r[0].x, r[0].y, r[1].x, r[1].y);
+}
+
+// Four consecutive elements (el a multiple of four) of token tile_row(m, c)
+// from rows filled by RowTiles.
+template <int IO, int DK>
+__device__ __forceinline__ void row4(const uint4* rows, int m, int c, int el, float (&x)[4]) {
+    constexpr int KB = DK / 32, NA = IO == IO_F32 ? 3 : 1;
+    const int g = (el >> 3) & 3;
+    const int at = (m * KB + (el >> 5)) * 64 + 16 * g + (c ^ (4 * g));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = 0.f;
+#pragma unroll
+    for (int a = NA - 1; a >= 0; --a) {
+        const uint2 r = ((const uint2*)(rows + a * 4 * KB * 64 + at))[(el >> 2) & 1];
+        const uint32_t u[2] = {r.x, r.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (IO == IO_F16) {
+                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+                const h2 h = __builtin_bit_cast(h2, u[j]);
+                x[2 * j] = (float)h.x;
+                x[2 * j + 1] = (float)h.y;
+            } else {
+                x[2 * j] += __uint_as_float(u[j] << 16);
+                x[2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
+            }
+        }
+    }
 }
 
 // Products of an operand of the I/O type with an fp32 one.
@@ -422,6 +555,12 @@ struct Operand {
                                                        const uint4 (&b)[NB], dfloat4 (&c)[M]) {
         if constexpr (kScaled) mma_all(a, b, c);
         else mma_tiles<NP>(a, b, c);
+    }
+    // both operands of the I/O type
+    static __device__ __forceinline__ dfloat4 mma_io(const uint4 (&a)[NA], const uint4 (&b)[NA],
+                                                     dfloat4 c) {
+        if constexpr (kScaled) return mma_h(a[0], b[0], c);
+        else return mma_terms<3>(a, b, c);
     }
     // where a 16-bit output is all that follows, 16 bits of b
     static __device__ __forceinline__ dfloat4 mma_out(const uint4 (&a)[NA], const uint4 (&b)[NB],

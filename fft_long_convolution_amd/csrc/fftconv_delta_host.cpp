@@ -13,6 +13,8 @@ constexpr size_t kMaxCount = 0x7fffffff;      // of any one dimension
 constexpr size_t kMaxElems = (size_t)1 << 46; // of any one tensor
 constexpr size_t kMaxGrid = 0xfffff0;         // workgroups of 256 threads of a launch
 
+constexpr size_t kMaxTokenStride = (size_t)1 << 24;  // elements, gated delta rule
+
 // a byte range of the caller's memory
 struct Range {
     const void* p;
@@ -251,6 +253,12 @@ fftconv_status delta_inputs(const fftconv_delta_desc* d, const DeltaArgs& a, Del
     CHECK(span_bytes(d->B, d->T, d->Hk, d->Dk, d->q_stride, d->dtype, &qb));
     CHECK(span_bytes(d->B, d->T, d->Hk, d->Dk, d->k_stride, d->dtype, &kb));
     CHECK(span_bytes(d->B, d->T, d->Hv, d->Dv, d->v_stride, d->dtype, &vb));
+    // the kernels' byte offsets within 64 tokens are 32-bit numbers
+    const size_t far = kMaxTokenStride;
+    if (d->T > 1 && ((size_t)d->q_stride[1] >= far || (size_t)d->k_stride[1] >= far ||
+                     (size_t)d->v_stride[1] >= far))
+        return FFTCONV_ERR_UNSUPPORTED;
+    if (d->Hv * d->Dv >= far) return FFTCONV_ERR_UNSUPPORTED;
     const size_t gates = d->B * d->T * d->Hv * 4;
     const size_t rows = d->sequences ? d->sequences : d->B;
     const size_t state = rows * d->Hv * d->Dk * d->Dv * 4;

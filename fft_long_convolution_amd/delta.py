@@ -277,7 +277,8 @@ class GatedDelta(_Op):
         if initial_state is not None:
             _check(initial_state, "initial_state", state, torch.float32, dev)
             initial_state = _dense(initial_state)
-        q, k, v = (_strided(x, self._step) for x in (q, k, v))
+        q, k, v = (_strided(x if x.stride(1) < 1 << 24 else x.contiguous(), self._step)
+                   for x in (q, k, v))
         desc = DeltaDesc(DTYPES[self.dtype], B, T, Hk, Hv, self.D_k, self.D_v, n, self.scale,
                          _LL3(*q.stride()[:3]), _LL3(*k.stride()[:3]), _LL3(*v.stride()[:3]))
         return dev, desc, state, (q, k, v, _dense(g), _dense(beta), cu_seqlens, initial_state)

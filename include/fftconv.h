@@ -485,8 +485,8 @@ typedef struct fftconv_delta_desc {
                                  = 1 and the row packs n sequences whose
                                  bounds are in cu_seqlens                   */
     float scale;              /* of the outputs, e.g. Dk^(-1/2)             */
-    long long q_stride[3];    /* batch, token, head                         */
-    long long k_stride[3];
+    long long q_stride[3];    /* batch, token, head; token strides (and      */
+    long long k_stride[3];    /* Hv Dv) below 2^24                           */
     long long v_stride[3];
 } fftconv_delta_desc;
 
