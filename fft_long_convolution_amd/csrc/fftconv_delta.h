@@ -95,17 +95,17 @@ struct DeltaParams {
     int seg_chunks;
     float* seg_n;                    // [segs][Hv][Dk][Dv]
     float* seg_m;                    // [segs][Hv][Dk][Dk]
-    float* states;                   // [slots][Hv][Dk][Dv] or null: each
-                                     // chunk's first state, for the backward
-    float* us;                       // [slots][Hv][kChunk][Dv] or null: U
+    // for the backward, or null: each chunk's first state and U, [slots][Hv]
+    // matrices in the layout of saved_floats()
+    float* states;
+    float* us;
 };
 struct DeltaGradParams {
     DeltaParams f;                   // inputs, bpack, states, us
     const void* dout;                // [B][T][Hv][Dv]
     const float* dfin;               // [nseq][Hv][Dk][Dv] or null
-    float* dstates;                  // [slots][Hv][Dk][Dv]: gradient of each
-                                     // chunk's last state
-    float* dys;                      // [slots][Hv][kChunk][Dv]: T^T dU
+    float* dstates;                  // [slots][Hv] saved matrices: gradient of
+    float* dys;                      // each chunk's last state, T^T dU
     void* dq;                        // [B][T][Hk][Dk]
     void* dk;
     void* dv;                        // [B][T][Hv][Dv]

@@ -172,25 +172,27 @@ __device__ void invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
 }
 
 // Writes a lower triangle from LDS as N terms in operand order: tile (m, kb),
-// lane (g, c), element i holds [tile_row(m, c)][32 kb + 8 g + i].
+// lane (g, c), element i holds [tile_row(m, c)][32 kb + 8 g + i].  Rows are
+// multiplied with their scale.
 template <int N>
-__device__ __forceinline__ void store_tri(const float (*t)[kLd], uint4* dst) {
+__device__ __forceinline__ void store_tri(const float (*t)[kLd], const float* scale, uint4* dst) {
     for (int i = threadIdx.x; i < kTriTiles * 64; i += blockDim.x) {
         const int tile = i >> 6, l = i & 63;
         const int m = tile < 2 ? tile : 2 + ((tile - 2) >> 1);
         const int kb = tile < 2 ? 0 : (tile - 2) & 1;
-        const float* s = &t[tile_row(m, l & 15)][32 * kb + 8 * (l >> 4)];
+        const int row = tile_row(m, l & 15);
+        const float* s = &t[row][32 * kb + 8 * (l >> 4)];
         const float4 a = *(const float4*)s, b = *(const float4*)(s + 4);
         const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         uint4 w[N];
-        split8<N>(x, w);
+        split8h<N>(x, scale[row], w);
 #pragma unroll
-        for (int j = 0; j < N; ++j) dst[j * kTriTiles * 64 + i] = w[j];
+        for (int j = 0; j < N; ++j) dst[j * kTerm + i] = w[j];
     }
 }
 // The same triangle's transpose, an upper one: tile (m, kb), kb >= m / 2.
-template <int N>
-__device__ __forceinline__ void store_tri_transposed(const float (*t)[kLd], uint4* dst) {
+__device__ __forceinline__ void store_tri_transposed(const float (*t)[kLd], const float* scale,
+                                                     uint4* dst) {
     for (int i = threadIdx.x; i < kTriTiles * 64; i += blockDim.x) {
         const int tile = i >> 6, l = i & 63;
         const int m = tile < 4 ? tile >> 1 : tile - 2;
@@ -199,24 +201,25 @@ __device__ __forceinline__ void store_tri_transposed(const float (*t)[kLd], uint
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = t[row + j][col];
-        uint4 w[N];
-        split8<N>(x, w);
+        uint4 w[2];
+        split8h<2>(x, scale[col], w);
 #pragma unroll
-        for (int j = 0; j < N; ++j) dst[j * kTriTiles * 64 + i] = w[j];
+        for (int j = 0; j < 2; ++j) dst[j * kTerm + i] = w[j];
     }
 }
 
 template <int IO, int DK>
 struct PrepLds {
-    static constexpr int kRows = Operand<IO>::NA * 4 * (DK / 32) * 64;   // uint4
+    static constexpr int NT = IO == IO_F32 ? 3 : 1;                 // plain terms
+    static constexpr int kRows = NT * 4 * (DK / 32) * 64;           // uint4
     static constexpr int kMat = kChunk * kLd / 4;
     static constexpr int kBytes = 32 * (kRows > kMat ? kRows : kMat);
 };
 // One workgroup per chunk and value head.
 template <int IO, int DK>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
-    typedef Operand<IO> Op;
-    constexpr int NA = Op::NA, KB = DK / 32;
+    typedef PrepLds<IO, DK> L;
+    constexpr int NT = L::NT, KB = DK / 32, NO = Io<IO>::NO;
     const long long id = xcd_unit(blockIdx.x, p.slots * p.Hv);
     if (id >= p.slots * p.Hv) return;
     const long long slot = id / p.Hv;
@@ -233,40 +236,31 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     float (*A)[kLd] = (float (*)[kLd])lds;
     float (*P)[kLd] = A + kChunk;
     __shared__ double G[kChunk];
-    __shared__ float bet[kChunk];
+    __shared__ float bet[kChunk], rowp[kChunk], colp[kChunk];
+    __shared__ uint32_t big[4][kChunk];      // largest of K, Q, columns of P, T
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g4 = lane >> 4, rslot = 16 * g4 + (c ^ (4 * g4));
     const int hk = h / p.group;
-    {
-        RowTiles<IO, DK, 4> rk, rq;
-        rk.load(tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2], p.ks[1]), 0, n,
-                p.Dk);
-        rq.load(tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2], p.qs[1]), 0, n,
-                p.Dk);
-        if (wave == 0) {
-            const long long gi = (sp.b * p.T + tok + (lane < n ? lane : 0)) * p.Hv + h;
-            float gv = p.g[gi], bv = p.beta[gi];
-            gv = lane < n ? gv : 0.f;
-            bv = lane < n ? bv : 0.f;
-            const double s = decay_sum(gv);
-            G[lane] = s;
-            bet[lane] = bv;
-            const double last = __shfl(s, 63);
-            const float eg = expf((float)s), ee = expf((float)(last - s)),
-                        ec = expf((float)last);
-            for (uint4* d : {p.pack + id * Op::kPack, p.bpack ? p.bpack + id * kBackPack : nullptr})
-                if (d) {
-                    float* dec = (float*)(d + 3 * kTriTiles * 64);
-                    dec[lane] = eg;
-                    dec[64 + lane] = ee;
-                    dec[128 + lane] = bv;
-                    dec[192 + lane] = ec;
-                }
-        }
-        rk.store(lds);
-        rq.store(lds + PrepLds<IO, DK>::kRows);
+    big[wave][lane] = 0;
+    RowTiles<IO, DK, 4> rk, rq;
+    rk.load(tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2], p.ks[1]), 0, n, p.Dk);
+    rq.load(tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2], p.qs[1]), 0, n, p.Dk);
+    double mine = 0, last = 0;               // sums of log decays
+    if (wave == 0) {
+        const long long gi = (sp.b * p.T + tok + (lane < n ? lane : 0)) * p.Hv + h;
+        const float gv = p.g[gi], bv = p.beta[gi];
+        mine = decay_sum(lane < n ? gv : 0.f);
+        last = __shfl(mine, 63);
+        G[lane] = mine;
+        bet[lane] = lane < n ? bv : 0.f;
     }
+    rk.store_plain(lds);
+    rq.store_plain(lds + L::kRows);
     __syncthreads();
+    if (IO != IO_F16) {
+        rk.max_rows(big[0]);
+        rq.max_rows(big[1]);
+    }
     // scores of the wave's tokens, tile_row(wave, .), against those of the
     // tiles up to it
     dfloat4 kk[4], qk[4];
@@ -275,58 +269,130 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     const int jtiles = wave < 2 ? 2 : 4;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-        uint4 ka[NA], qa[NA];
+        uint4 a[2][NT];
 #pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            ka[i] = lds[((i * 4 + wave) * KB + kb) * 64 + rslot];
-            qa[i] = lds[PrepLds<IO, DK>::kRows + ((i * 4 + wave) * KB + kb) * 64 + rslot];
+        for (int i = 0; i < NT; ++i) {
+            a[0][i] = lds[((i * 4 + wave) * KB + kb) * 64 + rslot];
+            a[1][i] = lds[L::kRows + ((i * 4 + wave) * KB + kb) * 64 + rslot];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (j < jtiles) {
-                uint4 b[NA];
+                uint4 b[NT];
 #pragma unroll
-                for (int i = 0; i < NA; ++i) b[i] = lds[((i * 4 + j) * KB + kb) * 64 + rslot];
-                kk[j] = Op::mma_io(ka, b, kk[j]);
-                qk[j] = Op::mma_io(qa, b, qk[j]);
+                for (int i = 0; i < NT; ++i) b[i] = lds[((i * 4 + j) * KB + kb) * 64 + rslot];
+                dfloat4 x[2] = {kk[j], qk[j]};
+                if constexpr (IO == IO_F16) mma_tiles(a, b, x);
+                else mma_bf_tiles(a, b, x);
+                kk[j] = x[0];
+                qk[j] = x[1];
             }
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+        const int col = tile_row(j, c);
+        float big_p = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int row = tile_row(wave, 4 * g4 + r), col = tile_row(j, c);
+            const int row = tile_row(wave, 4 * g4 + r);
             const float gam = row >= col ? expf((float)(G[row] - G[col])) : 0.f;
+            const float pv = row >= col ? p.scale * gam * qk[j][r] : 0.f;
             A[row][col] = row > col ? bet[row] * gam * kk[j][r] : 0.f;
-            P[row][col] = row >= col ? p.scale * gam * qk[j][r] : 0.f;
+            P[row][col] = pv;
+            big_p = fmaxf(big_p, fabsf(pv));
         }
+        if (p.bpack && j < jtiles) {
+            big_p = max_groups(big_p);
+            if (g4 == 0) atomicMax(&big[2][col], __float_as_uint(big_p));
+        }
+    }
+    // rows of P: largest over the wave's tiles, 16 lanes a row
+    float back_row[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = tile_row(wave, 4 * g4 + r);
+        float a = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a = fmaxf(a, fabsf(P[row][tile_row(j, c)]));
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) a = fmaxf(a, __shfl_xor(a, m));
+        const Scale s = scale_to(a);
+        back_row[r] = s.back;
+        if (c == 0) rowp[row] = s.to;
+    }
     __syncthreads();
-    uint4* pack = p.pack + id * Op::kPack;
+    uint4* pack = p.pack + id * pack_uint4<IO>();
     uint4* back = p.bpack ? p.bpack + id * kBackPack : nullptr;
-    constexpr int kP = (3 * kTriTiles + 1) * 64;
-    store_tri<Op::NP>(P, pack + kP);
-    if (back) store_tri_transposed<3>(P, back + kP);
+    if (wave == 0) {
+        const Scale one = {1.f, 1.f};
+        const Scale sk = IO == IO_F16 ? one : scale_to(__uint_as_float(big[0][lane]));
+        const Scale sq = IO == IO_F16 ? one : scale_to(__uint_as_float(big[1][lane]));
+        const Scale sc = scale_to(__uint_as_float(big[2][lane]));
+        colp[lane] = sc.to;
+        const float eg = expf((float)mine), ee = expf((float)(last - mine));
+        for (uint4* d : {pack, back})
+            if (d) {
+                float* f = (float*)(d + kDec);
+                f[kDecayK + lane] = eg * sk.back;
+                f[kDecayQ + lane] = p.scale * eg * sq.back;
+                f[kEndK + lane] = ee * sk.back;
+                f[kBeta + lane] = bet[lane];
+                f[kScaleK + lane] = sk.to;
+                f[kScaleQ + lane] = sq.to;
+                if (lane == 0) f[kDecayAll] = expf((float)last);
+            }
+        if (back) ((float*)(back + kDec))[kBackP + lane] = sc.back;
+    }
+    if (c == 0)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            ((float*)(pack + kDec))[kBackP + tile_row(wave, 4 * g4 + r)] = back_row[r];
+    store_tri<NO>(P, rowp, pack + kPm);
+    if (back) {
+        __syncthreads();
+        store_tri_transposed(P, colp, back + kPm);
+    }
     __syncthreads();
     invert_unit_lower(A, P);
-    store_tri<3>(P, pack);
-    if (back) store_tri_transposed<3>(P, back);
+    // one scale for T
+    {
+        float a = 0.f;
+        for (int i = threadIdx.x; i < kChunk * kChunk; i += 256)
+            a = fmaxf(a, fabsf(P[i >> 6][i & 63]));
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) a = fmaxf(a, __shfl_xor(a, m));
+        if (lane == 0) big[3][wave] = __float_as_uint(a);
+    }
+    __syncthreads();
+    {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a = fmaxf(a, __uint_as_float(big[3][i]));
+        const Scale s = scale_to(a);
+        if (threadIdx.x < 64) rowp[threadIdx.x] = s.to;
+        if (threadIdx.x == 0) {
+            ((float*)(pack + kDec))[kBackT] = s.back;
+            if (back) ((float*)(back + kDec))[kBackT] = s.back;
+        }
+    }
+    __syncthreads();
+    store_tri<2>(P, rowp, pack);
+    if (back) store_tri_transposed(P, rowp, back);
 }
 
 // ------------------------------------------------- the walk over the chunks
 
-// LDS of the walk, in uint4.  16-bit operands of the next chunk are put into a
-// second buffer while the present one is worked on; fp32 ones, three times as
-// large, have no room for one.
+// LDS of the walk, in uint4.  Operands of the next chunk are put into a second
+// buffer while the present one is worked on, if they are of 16 bits; there is
+// no room for two of fp32's.
 template <int IO, int DK, bool FULL>
 struct ScanLds {
-    static constexpr int NA = Operand<IO>::NA;
-    static constexpr int kRows = NA * 4 * (DK / 32) * 64;
-    static constexpr int kPackKb = 3 * kTriTiles + 1 + (FULL ? Operand<IO>::NP * kTriTiles : 0);
-    static constexpr int kK = 0, kQ = kRows, kTri = kQ + (FULL ? kRows : 0);
-    static constexpr int kDec = kTri + 3 * kTriTiles * 64, kP = kDec + 64;
-    static constexpr int kSize = kTri + kPackKb * 64;
-    static constexpr int kBufs = NA == 1 ? 2 : 1;
+    static constexpr int kRows = Io<IO>::NA * 4 * (DK / 32) * 64;
+    static constexpr int kPackU4 = FULL ? pack_uint4<IO>() : kPm;
+    static constexpr int kK = 0, kQ = kRows, kPack = kQ + (FULL ? kRows : 0);
+    static constexpr int kSize = kPack + kPackU4;
+    static constexpr int kBufs = IO == IO_F32 ? 1 : 2;
     static constexpr int kBytes = kBufs * kSize * 16;
 };
 
@@ -347,9 +413,8 @@ template <int IO, int DK, int W, int MODE>
 __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
     constexpr bool FULL = MODE != kEffect;
     typedef ScanLds<IO, DK, FULL> L;
-    typedef Operand<IO> Op;
-    constexpr int NA = Op::NA, KB = DK / 32, ST = DK / 16, NP = Op::NP, NB = Op::NB;
-    constexpr int kCols = 16 * W, kB = IO == IO_F32 ? 4 : 2;
+    constexpr int NA = Io<IO>::NA, NO = Io<IO>::NO, KB = DK / 32, ST = DK / 16;
+    constexpr int kCols = 16 * W, kB = Io<IO>::kB;
     extern __shared__ uint4 lds[];
     const int vcols = (p.Dv + kCols - 1) / kCols;
     const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
@@ -402,23 +467,24 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
                                     (long long)p.Hv * p.Dv);
     const uint32_t vlane = (uint32_t)(8 * g) * (uint32_t)tv.bytes + colv * kB;
     const uint32_t olane = (uint32_t)(8 * g) * (uint32_t)to.bytes + col * kB;
-    const uint32_t slane = (uint32_t)(8 * g * p.Dv + col) * 4;
-    const uint4* pack = p.pack + (sp.slot0 * p.Hv + h) * Op::kPack;
-    const long long pack_step = (long long)p.Hv * Op::kPack;
+    const uint4* pack = p.pack + (sp.slot0 * p.Hv + h) * pack_uint4<IO>();
+    const long long pack_step = (long long)p.Hv * pack_uint4<IO>();
 
     RowTiles<IO, DK, W> rk, rq;
-    Block<L::kPackKb, W> rp;
+    Block<L::kPackU4 / 64, W> rp;
     dfloat4 v[4];
     const auto load = [&](int ch) __attribute__((always_inline)) {
         const int n = sp.len - ch * kChunk;
-        rk.load(tk, ch * kChunk, n, p.Dk);
-        if (FULL) rq.load(tq, ch * kChunk, n, p.Dk);
-        rp.load(pack + ch * pack_step);
+        const uint4* next_pack = pack + ch * pack_step;
+        const float* f = (const float*)(next_pack + kDec);
+        rk.load(tk, ch * kChunk, n, p.Dk, f + kScaleK);
+        if (FULL) rq.load(tq, ch * kChunk, n, p.Dk, f + kScaleQ);
+        rp.load(next_pack);
     };
     const auto store = [&](uint4* d) __attribute__((always_inline)) {
         rk.store(d + L::kK);
         if (FULL) rq.store(d + L::kQ);
-        rp.store(d + L::kTri);
+        rp.store(d + L::kPack);
     };
     const auto load_v = [&](int ch) __attribute__((always_inline)) {
         if (!matrix) load_column<IO>(tv, ch * kChunk, vlane, sp.len - ch * kChunk, v);
@@ -438,14 +504,15 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
         const int n = sp.len - ch * kChunk;
         const int ahead = ch + 1 < last ? ch + 1 : ch;
         load(ahead);
-        const float* dec = (const float*)(now + L::kDec);
-        if (MODE == kSaving && cok)
-            store_state<ST>((char*)(p.states + ci * state), p.Dv * 4, slane, p.Dk, S);
+        const float* fac = (const float*)(now + L::kPack + kDec);
+        const uint4* tri = now + L::kPack;
+        const float big_s = max_column(S);
+        const Scale ss = scale_to(big_s);
+        if (MODE == kSaving && cok) save_columns<KB>(p.states, ci, p.Dv, col, S, big_s);
         // K S and Q S
         dfloat4 X[4], O[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) X[m] = O[m] = dfloat4{0, 0, 0, 0};
-        const ColScale sc = Op::template scale_of<ST>(S);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             uint4 a[4][NA], q[4][NA];
@@ -456,90 +523,105 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
                     a[m][i] = now[L::kK + ((i * 4 + m) * KB + kb) * 64 + slot];
                     if (FULL) q[m][i] = now[L::kQ + ((i * 4 + m) * KB + kb) * 64 + slot];
                 }
-            uint4 st[NB];
-            Op::split(S[2 * kb], S[2 * kb + 1], sc, st);
-            Op::mma_all(a, st, X);
-            if (FULL) Op::mma_all_out(q, st, O);
+            uint4 st[2];
+            split_acc<2>(S[2 * kb], S[2 * kb + 1], ss.to, st);
+            mma_tiles(a, st, X);
+            if (FULL) mma_tiles(q, leading<NO>(st), O);
         }
         // X = beta o (V - e^G o K S);  O = scale e^G o Q S
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const int row = tile_row(m, 4 * g);
-            const float4 e = *(const float4*)(dec + row), b = *(const float4*)(dec + 128 + row);
+            const float4 e = *(const float4*)(fac + kDecayK + row);
+            const float4 b = *(const float4*)(fac + kBeta + row);
+            const float4 f = *(const float4*)(fac + kDecayQ + row);
             const float ev[4] = {e.x, e.y, e.z, e.w}, bv[4] = {b.x, b.y, b.z, b.w};
+            const float fv[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float es = ev[r] * sc.back;
-                X[m][r] = bv[r] * fmaf(-es, X[m][r], v[m][r]);
-                if (FULL) O[m][r] = p.scale * es * O[m][r];
+                X[m][r] = bv[r] * fmaf(-(ev[r] * ss.back), X[m][r], v[m][r]);
+                if (FULL) O[m][r] = (fv[r] * ss.back) * O[m][r];
             }
         }
         load_v(ahead);
         // U = T X
         dfloat4 U[4];
+        const Scale sx = scale_to(max_column(X));
 #pragma unroll
         for (int m = 0; m < 4; ++m) U[m] = dfloat4{0, 0, 0, 0};
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            uint4 xt[3];
-            split_acc<3>(X[2 * kb], X[2 * kb + 1], xt);
+            uint4 xt[2];
+            split_acc<2>(X[2 * kb], X[2 * kb + 1], sx.to, xt);
 #pragma unroll
             for (int m0 = 2 * kb; m0 < 4; m0 += 2) {
-                uint4 a[2][3];
+                uint4 a[2][2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        a[m][i] = now[L::kTri + (i * kTriTiles + tri_tile(m0 + m, kb)) * 64 + lane];
-                mma_tiles<3>(a, xt, *(dfloat4 (*)[2])&U[m0]);
+                    for (int i = 0; i < 2; ++i)
+                        a[m][i] = tri[i * kTerm + tri_tile(m0 + m, kb) * 64 + lane];
+                mma_tiles(a, xt, *(dfloat4 (*)[2])&U[m0]);
             }
         }
+        {
+            const float back = sx.back * fac[kBackT];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) U[m] *= back;
+        }
         if (FULL) {
-            if (MODE == kSaving && cok)
-                store_column<IO_F32>((char*)(p.us + ci * kChunk * p.Dv), p.Dv * 4, slane, kChunk,
-                                     U);
+            const float big_u = max_column(U);
+            if (MODE == kSaving && cok) save_columns<2>(p.us, ci, p.Dv, col, U, big_u);
             // O += P U
+            const Scale su = scale_to(big_u);
+            dfloat4 PU[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) PU[m] = dfloat4{0, 0, 0, 0};
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                uint4 ut[NP];
-                split_acc<NP>(U[2 * kb], U[2 * kb + 1], ut);
+                uint4 ut[NO];
+                split_acc<NO>(U[2 * kb], U[2 * kb + 1], su.to, ut);
 #pragma unroll
                 for (int m0 = 2 * kb; m0 < 4; m0 += 2) {
-                    uint4 a[2][NP];
+                    uint4 a[2][NO];
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int i = 0; i < NP; ++i)
-                            a[m][i] =
-                                now[L::kP + (i * kTriTiles + tri_tile(m0 + m, kb)) * 64 + lane];
-                    mma_tiles<NP>(a, ut, *(dfloat4 (*)[2])&O[m0]);
+                        for (int i = 0; i < NO; ++i)
+                            a[m][i] = tri[kPm + i * kTerm + tri_tile(m0 + m, kb) * 64 + lane];
+                    mma_tiles(a, ut, *(dfloat4 (*)[2])&PU[m0]);
                 }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float4 e = *(const float4*)(fac + kBackP + tile_row(m, 4 * g));
+                const float ev[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) O[m][r] = fmaf(ev[r] * su.back, PU[m][r], O[m][r]);
             }
             if (cok) store_column<IO>((char*)to.at(ch * kChunk), to.bytes, olane, n, O);
         }
         // e^(Gc-G) o U
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const float4 e = *(const float4*)(dec + 64 + tile_row(m, 4 * g));
+            const float4 e = *(const float4*)(fac + kEndK + tile_row(m, 4 * g));
             U[m][0] *= e.x;
             U[m][1] *= e.y;
             U[m][2] *= e.z;
             U[m][3] *= e.w;
         }
-        const float ec = dec[192];
+        const float ec = fac[kDecayAll];
         if (L::kBufs == 2) store(next);
         // S = e^Gc S + K^T U
-        const ColScale su = Op::template scale_of<4>(U);
-        uint4 ut[2][NB];
+        const Scale se = scale_to(max_column(U));
+        uint4 ut[2][2];
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) Op::split(U[2 * tb], U[2 * tb + 1], su, ut[tb]);
+        for (int tb = 0; tb < 2; ++tb) split_acc<2>(U[2 * tb], U[2 * tb + 1], se.to, ut[tb]);
 #pragma unroll
         for (int t0 = 0; t0 < ST; t0 += 4) {
             dfloat4 a[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) a[t][r] = Op::kScaled ? 0.f : ec * S[t0 + t][r];
+            for (int t = 0; t < 4; ++t) a[t] = dfloat4{0, 0, 0, 0};
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
                 uint4 x[4][NA];
@@ -548,14 +630,13 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
 #pragma unroll
                     for (int i = 0; i < NA; ++i)
                         x[t][i] = read_cols<DK>(now + L::kK + i * 4 * KB * 64, t0 + t, tb);
-                Op::mma_all(x, ut[tb], a);
+                mma_tiles(x, ut[tb], a);
             }
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[t0 + t][r] =
-                        Op::kScaled ? fmaf(su.back, a[t][r], ec * S[t0 + t][r]) : a[t][r];
+                    S[t0 + t][r] = fmaf(se.back, a[t][r], ec * S[t0 + t][r]);
         }
         __syncthreads();
         if (L::kBufs == 2) {
@@ -634,14 +715,16 @@ __global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
     load(1, R);
     for (int i = 1; i + 1 < n; ++i) {
 #pragma unroll
-        for (int j = 0; j < L::kHalves; ++j) rm[j].store(lds + j * L::kRows);
+        for (int j = 0; j < L::kHalves; ++j) rm[j].store_plain(lds + j * L::kRows);
         __syncthreads();
         const int ahead = i + 2 < n ? i + 1 : i;
         load_m(ahead);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             uint4 b[3];
-            split_acc<3>(S[2 * kb], S[2 * kb + 1], b);
+            const dfloat4 lo = S[2 * kb], hi = S[2 * kb + 1];
+            const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            split8<3>(x, b);
 #pragma unroll
             for (int t0 = 0; t0 < ST; t0 += 2) {
                 uint4 a[2][3];
@@ -651,7 +734,7 @@ __global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
                     for (int j = 0; j < 3; ++j)
                         a[t][j] = lds[((t0 + t) >> 2) * L::kRows +
                                       ((j * 4 + ((t0 + t) & 3)) * KB + kb) * 64 + slot];
-                mma_tiles<3>(a, b, *(dfloat4 (*)[2])&R[t0]);
+                mma_bf_tiles(a, b, *(dfloat4 (*)[2])&R[t0]);
             }
         }
 #pragma unroll
@@ -725,7 +808,8 @@ hipError_t prep_io(const DeltaParams& p, hipStream_t s) {
 }  // namespace
 
 int delta_pack_uint4(int io) {
-    return io == IO_F32 ? Operand<IO_F32>::kPack : Operand<IO_BF16>::kPack;
+    return io == IO_F32 ? pack_uint4<IO_F32>()
+           : io == IO_F16 ? pack_uint4<IO_F16>() : pack_uint4<IO_BF16>();
 }
 int delta_back_pack_uint4() { return kBackPack; }
 

@@ -21,11 +21,9 @@ namespace {
 
 template <int IO, int DK>
 struct RscanLds {
-    static constexpr int kRows = Operand<IO>::NA * 4 * (DK / 32) * 64;     // uint4
-    static constexpr int kK = 0, kQ = kRows, kPack = 2 * kRows;
-    static constexpr int kTri = kPack, kDec = kTri + 3 * kTriTiles * 64, kP = kDec + 64;
-    static constexpr int kSize = kPack + kBackPack;
-    static constexpr int kBufs = Operand<IO>::NA == 1 ? 2 : 1;
+    static constexpr int kRows = Io<IO>::NA * 4 * (DK / 32) * 64;     // uint4
+    static constexpr int kK = 0, kQ = kRows, kPack = 2 * kRows, kSize = kPack + kBackPack;
+    static constexpr int kBufs = IO == IO_F32 ? 1 : 2;
     static constexpr int kBytes = kBufs * kSize * 16;
 };
 
@@ -34,11 +32,9 @@ struct RscanLds {
 template <int IO, int DK, int W>
 __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
-    typedef Operand<IO> Op;
     const DeltaParams& p = gp.f;
-    constexpr int NA = Op::NA, NB = Op::NB, KB = DK / 32, ST = DK / 16, NO = IoTerms<IO>::n;
+    constexpr int NA = Io<IO>::NA, KB = DK / 32, ST = DK / 16, kB = Io<IO>::kB, kCols = 16 * W;
     extern __shared__ uint4 lds[];
-    constexpr int kCols = 16 * W, kB = IO == IO_F32 ? 4 : 2;
     const int cols = (p.Dv + kCols - 1) / kCols;
     const long long units = p.nseq * p.Hv * cols;
     long long id = xcd_unit(blockIdx.x, units);
@@ -53,9 +49,9 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
     const int slot = 16 * g + (c ^ (4 * g));             // of a row operand
     const int col = cb * kCols + wave * 16 + c;
     const bool cok = col < p.Dv;
+    const int colv = cok ? col : 0;                      // to read from
     const int hk = h / p.group;
     const long long state = p.Dk * (long long)p.Dv;
-    const int colv = cok ? col : 0;                      // to read from
     const long long sbase = (seq * p.Hv + h) * state + col;
     dfloat4 D[ST];
 #pragma unroll
@@ -72,16 +68,17 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
     const Tokens to = tokens_of<IO>(gp.dout, ofirst, (long long)p.Hv * p.Dv);
     const Tokens tv = tokens_of<IO>(gp.dv, ofirst, (long long)p.Hv * p.Dv);
     const uint32_t olane = (uint32_t)(8 * g) * (uint32_t)to.bytes + colv * kB;
-    const uint32_t slane = (uint32_t)(8 * g * p.Dv + col) * 4;
     const uint4* pack = p.bpack + (sp.slot0 * p.Hv + h) * kBackPack;
     const long long pack_step = (long long)p.Hv * kBackPack;
     RowTiles<IO, DK, W> rk, rq;
     Block<kBackPack / 64, W> rp;
     const auto load = [&](int ch) __attribute__((always_inline)) {
         const int n = sp.len - ch * kChunk;
-        rk.load(tk, ch * kChunk, n, p.Dk);
-        rq.load(tq, ch * kChunk, n, p.Dk);
-        rp.load(pack + ch * pack_step);
+        const uint4* next_pack = pack + ch * pack_step;
+        const float* f = (const float*)(next_pack + kDec);
+        rk.load(tk, ch * kChunk, n, p.Dk, f + kScaleK);
+        rq.load(tq, ch * kChunk, n, p.Dk, f + kScaleQ);
+        rp.load(next_pack);
     };
     const auto store = [&](uint4* d) __attribute__((always_inline)) {
         rk.store(d + L::kK);
@@ -104,77 +101,87 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
     uint4* next = lds + (L::kBufs == 2 ? L::kSize : 0);
     for (int ch = chunks - 1; ch >= 0; --ch) {
         const long long ci = (sp.slot0 + ch) * p.Hv + h;
-        const float* dec = (const float*)(now + L::kDec);
+        const float* fac = (const float*)(now + L::kPack + kDec);
+        const uint4* tri = now + L::kPack;
         dfloat4 dO[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dO[m] = dN[m];
         const int ahead = ch > 0 ? ch - 1 : 0;
         load(ahead);
-        if (cok) store_state<ST>((char*)(gp.dstates + ci * state), p.Dv * 4, slane, p.Dk, D);
+        const float big_d = max_column(D);
+        if (cok) save_columns<KB>(gp.dstates, ci, p.Dv, col, D, big_d);
         // dU = e^(Gc-G) o K D + P^T dO
-        dfloat4 dU[4];
+        dfloat4 dU[4], PO[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) dU[m] = dfloat4{0, 0, 0, 0};
-        {
-            const ColScale sc = Op::template scale_of<ST>(D);
+        for (int m = 0; m < 4; ++m) dU[m] = PO[m] = dfloat4{0, 0, 0, 0};
+        const Scale sd = scale_to(big_d), so = scale_to(max_column(dO));
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                uint4 dt[NB];
-                Op::split(D[2 * kb], D[2 * kb + 1], sc, dt);
+        for (int kb = 0; kb < KB; ++kb) {
+            uint4 dt[2], a[4][NA];
+            split_acc<2>(D[2 * kb], D[2 * kb + 1], sd.to, dt);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    uint4 a[NA];
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-                    for (int i = 0; i < NA; ++i)
-                        a[i] = now[L::kK + ((i * 4 + m) * KB + kb) * 64 + slot];
-                    dU[m] = Op::mma(a, dt, dU[m]);
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float4 e = *(const float4*)(dec + 64 + tile_row(m, 4 * g));
-                dU[m][0] *= e.x * sc.back;
-                dU[m][1] *= e.y * sc.back;
-                dU[m][2] *= e.z * sc.back;
-                dU[m][3] *= e.w * sc.back;
-            }
+                for (int i = 0; i < NA; ++i) a[m][i] = now[L::kK + ((i * 4 + m) * KB + kb) * 64 + slot];
+            mma_tiles(a, dt, dU);
         }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            uint4 ot[NO];
-            split_acc<NO>(dO[2 * kb], dO[2 * kb + 1], ot);
+            uint4 ot[NA];
+            split_acc<NA>(dO[2 * kb], dO[2 * kb + 1], so.to, ot);
 #pragma unroll
-            for (int m = 0; m < 2 * kb + 2; ++m) {
-                uint4 a[3];
+            for (int m0 = 0; m0 < 2 * kb + 2; m0 += 2) {
+                uint4 a[2][2];
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    a[i] = now[L::kP + (i * kTriTiles + upper_tile(m, kb)) * 64 + lane];
-                dU[m] = mma_terms<3>(a, ot, dU[m]);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        a[m][i] = tri[kPm + i * kTerm + upper_tile(m0 + m, kb) * 64 + lane];
+                mma_tiles(a, ot, *(dfloat4 (*)[2])&PO[m0]);
             }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float4 e = *(const float4*)(fac + kEndK + tile_row(m, 4 * g));
+            const float4 f = *(const float4*)(fac + kBackP + tile_row(m, 4 * g));
+            const float ev[4] = {e.x, e.y, e.z, e.w}, fv[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                dU[m][r] = fmaf(fv[r] * so.back, PO[m][r], (ev[r] * sd.back) * dU[m][r]);
         }
         // dY = T^T dU
         dfloat4 dY[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dY[m] = dfloat4{0, 0, 0, 0};
+        {
+            const Scale su = scale_to(max_column(dU));
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            uint4 ut[3];
-            split_acc<3>(dU[2 * kb], dU[2 * kb + 1], ut);
+            for (int kb = 0; kb < 2; ++kb) {
+                uint4 ut[2];
+                split_acc<2>(dU[2 * kb], dU[2 * kb + 1], su.to, ut);
 #pragma unroll
-            for (int m = 0; m < 2 * kb + 2; ++m) {
-                uint4 a[3];
+                for (int m0 = 0; m0 < 2 * kb + 2; m0 += 2) {
+                    uint4 a[2][2];
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    a[i] = now[L::kTri + (i * kTriTiles + upper_tile(m, kb)) * 64 + lane];
-                dY[m] = mma_terms<3>(a, ut, dY[m]);
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            a[m][i] = tri[i * kTerm + upper_tile(m0 + m, kb) * 64 + lane];
+                    mma_tiles(a, ut, *(dfloat4 (*)[2])&dY[m0]);
+                }
             }
+            const float back = su.back * fac[kBackT];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) dY[m] *= back;
         }
-        if (cok)
-            store_column<IO_F32>((char*)(gp.dys + ci * kChunk * p.Dv), p.Dv * 4, slane, kChunk, dY);
+        {
+            const float big_y = max_column(dY);
+            if (cok) save_columns<2>(gp.dys, ci, p.Dv, col, dY, big_y);
+        }
         // dV = beta o dY; what goes back to the state through K and Q
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const float4 b = *(const float4*)(dec + 128 + tile_row(m, 4 * g));
+            const float4 b = *(const float4*)(fac + kBeta + tile_row(m, 4 * g));
             dY[m][0] *= b.x;
             dY[m][1] *= b.y;
             dY[m][2] *= b.z;
@@ -184,48 +191,49 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
             store_column<IO>((char*)tv.at(ch * kChunk), tv.bytes, olane, sp.len - ch * kChunk, dY);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            const float4 e = *(const float4*)(dec + tile_row(m, 4 * g));
-            const float ev[4] = {e.x, e.y, e.z, e.w};
+            const float4 e = *(const float4*)(fac + kDecayK + tile_row(m, 4 * g));
+            const float4 f = *(const float4*)(fac + kDecayQ + tile_row(m, 4 * g));
+            const float ev[4] = {e.x, e.y, e.z, e.w}, fv[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 dY[m][r] *= -ev[r];
-                dO[m][r] *= p.scale * ev[r];
+                dO[m][r] *= fv[r];
             }
         }
-        const float ec = dec[192];
+        const float ec = fac[kDecayAll];
         if (L::kBufs == 2) store(next);
         load_do(ahead);
-        const ColScale sy = Op::template scale_of<4>(dY), so = Op::template scale_of<4>(dO);
-        uint4 yt[2][NB], ot[2][NB];
+        const Scale sy = scale_to(max_column(dY)), sq = scale_to(max_column(dO));
+        uint4 yt[2][2], ot[2][2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            Op::split(dY[2 * tb], dY[2 * tb + 1], sy, yt[tb]);
-            Op::split(dO[2 * tb], dO[2 * tb + 1], so, ot[tb]);
+            split_acc<2>(dY[2 * tb], dY[2 * tb + 1], sy.to, yt[tb]);
+            split_acc<2>(dO[2 * tb], dO[2 * tb + 1], sq.to, ot[tb]);
         }
 #pragma unroll
-        for (int t = 0; t < ST; ++t) {
-            dfloat4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-            if (!Op::kScaled)
+        for (int t0 = 0; t0 < ST; t0 += 2) {
+            dfloat4 a[2], b[2];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) a[r] = ec * D[t][r];
+            for (int t = 0; t < 2; ++t) a[t] = b[t] = dfloat4{0, 0, 0, 0};
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
-                uint4 x[NA];
+                uint4 x[2][NA], z[2][NA];
 #pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    x[i] = read_cols<DK>(now + L::kK + i * 4 * KB * 64, t, tb);
-                a = Op::mma(x, yt[tb], a);
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < NA; ++i)
-                    x[i] = read_cols<DK>(now + L::kQ + i * 4 * KB * 64, t, tb);
-                b = Op::mma(x, ot[tb], b);
+                    for (int i = 0; i < NA; ++i) {
+                        x[t][i] = read_cols<DK>(now + L::kK + i * 4 * KB * 64, t0 + t, tb);
+                        z[t][i] = read_cols<DK>(now + L::kQ + i * 4 * KB * 64, t0 + t, tb);
+                    }
+                mma_tiles(x, yt[tb], a);
+                mma_tiles(z, ot[tb], b);
             }
-            if (Op::kScaled)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    D[t][r] = fmaf(sy.back, a[r], fmaf(so.back, b[r], ec * D[t][r]));
-            else
-                D[t] = a + b;
+                    D[t0 + t][r] =
+                        fmaf(sy.back, a[t][r], fmaf(sq.back, b[t][r], ec * D[t0 + t][r]));
         }
         __syncthreads();
         if (L::kBufs == 2) {
@@ -238,24 +246,28 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
         }
     }
     if (gp.dinit && cok)
-        store_state<ST>((char*)(gp.dinit + (seq * p.Hv + h) * state), p.Dv * 4, slane, p.Dk, D);
+        store_state<ST>((char*)(gp.dinit + (seq * p.Hv + h) * state), p.Dv * 4,
+                        (uint32_t)(8 * g * p.Dv + col) * 4, p.Dk, D);
 }
 
 // ------------------------------------------------ the gradients of a chunk
 
-// LDS of delta_grads_kernel, in uint4.  The slices of S0, D, U and dY (32
-// columns, three terms; two buffers) are used up before the keys, queries and
-// the 64 x 64 matrices take their place.
+// LDS of delta_grads_kernel, in uint4: the chunk's keys and queries, then
+// slices (32 columns, two terms) of S0, D, U and dY, which the 64 x 64
+// matrices replace.
 template <int IO, int DK>
 struct GradsLds {
-    static constexpr int ST = DK / 16;
-    static constexpr int kS = 0, kD = 3 * ST * 64, kU = 2 * kD, kY = kU + 3 * 4 * 64;
-    static constexpr int kSlice = kY + 3 * 4 * 64;
-    static constexpr int kRows = Operand<IO>::NA * 4 * (DK / 32) * 64;
+    static constexpr int ST = DK / 16, KB = DK / 32;
+    static constexpr int kRows = Io<IO>::NA * 4 * KB * 64;
+    static constexpr int kK = 0, kQ = kRows, kSlices = 2 * kRows;
+    static constexpr int kSTerm = 2 * KB * 64, kUTerm = 4 * 64;      // one term of a slice
+    static constexpr int kS = 0, kD = 2 * kSTerm, kU = 2 * kD, kY = kU + 2 * kUTerm;
+    static constexpr int kSlice = kY + 2 * kUTerm;
+    static constexpr int kBufs = IO == IO_F32 ? 1 : 2;
     static constexpr int kMat = kChunk * kLd / 4;
-    static constexpr int kK = 0, kQ = kRows, kW = 2 * kRows, kWt = kW + kMat, kF = kWt + kMat;
-    static constexpr int kTail = kF + kMat;
-    static constexpr int kBytes = (2 * kSlice > kTail ? 2 * kSlice : kTail) * 16;
+    static constexpr int kW = kSlices, kWt = kW + kMat, kF = kWt + kMat;
+    static constexpr int kTail = kBufs * kSlice > 3 * kMat ? kBufs * kSlice : 3 * kMat;
+    static constexpr int kBytes = (kSlices + kTail) * 16;
 };
 
 // Sum over the four groups of 16 lanes.
@@ -265,31 +277,50 @@ __device__ __forceinline__ float sum_groups(float x) {
 }
 
 // What a thread has in flight of a slice: eight elements of S0 and D, of U
-// (waves 0..3) or dY and V (4..7) and of its wave's token's dO.
+// (waves 0..3) or dY (4..7), and eight of its wave's token's dO and V in two
+// pieces of four.
+template <int IO>
 struct SliceRegs {
-    du4 s[2], d[2], u[2], v[2], o[2];
+    typedef uint32_t piece __attribute__((ext_vector_type(IO == IO_F32 ? 4 : 2)));
+    du4 s[2], d[2], u[2];
+    piece o[2], v[2];
 };
+template <int IO, typename P>
+__device__ __forceinline__ void unpack_pieces(const P (&x)[2], bool ok0, bool ok1, float (&y)[8]) {
+    du4 r[2];
+    if constexpr (IO == IO_F32) {
+        r[0] = x[0];
+        r[1] = x[1];
+    } else {
+        r[0] = du4{x[0][0], x[0][1], x[1][0], x[1][1]};
+    }
+    unpack8<IO>(r, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (i < 4 ? ok0 : ok1) ? y[i] : 0.f;
+}
 
 // One workgroup of eight waves per chunk and key head.  A wave owns 16 tokens
 // (tile w % 4) as the columns of its products, R^T = S0 dO^T and so on, and
 // half of their rows (w / 4): half of a head's elements, and of the other
 // tokens in the 64 x 64 part.  So a lane has one token: what belongs to it
 // (decays, row sums) is a scalar of the lane, and sums over a head's elements
-// are sums in the lane and over four groups.  The value heads that share the
-// key head follow one another, and their parts of dQ and dK are summed in
-// registers, in a fixed order.
+// are sums in the lane and over four groups.  S0, D, U and dY come as the
+// walks saved them, eight rows of a column together, and are read transposed:
+// position i of the lane's eight columns is d0 + 16 (i/4) + 4 g + i%4.  They
+// and dO have one scale each.  The value heads that share the key head follow
+// one another, and their parts of dQ and dK are summed in registers, in a
+// fixed order.
 template <int IO, int DK>
 __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
     typedef GradsLds<IO, DK> L;
-    typedef Operand<IO> Op;
     const DeltaParams& p = gp.f;
-    constexpr int NA = Op::NA, NB = Op::NB, NO = IoTerms<IO>::n, KB = DK / 32, ST = L::ST;
+    constexpr int NA = Io<IO>::NA, NO = Io<IO>::NO, KB = DK / 32, ST = L::ST, kB = Io<IO>::kB;
     constexpr int HT = ST / 2;               // a wave's tiles of a head's elements
-    constexpr int kB = IO == IO_F32 ? 4 : 2;
     extern __shared__ uint4 lds[];
     __shared__ double G[kChunk];
     __shared__ float bet[kChunk], colsum[4][kChunk], rowG[2][kChunk], rowB[2][kChunk];
-    __shared__ float red[8], red3[8];
+    __shared__ float backK[kChunk], backQ[kChunk];
+    __shared__ float red[8], red3[8], big[8], bigO[8];
     const long long units = p.slots * p.Hk;
     const long long id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
@@ -308,183 +339,244 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
     const int mine = tile_row(tile, c);              // the lane's token
     const int have = mine < n ? mine : n - 1;        // one to read from
     const bool jwork = half <= tile >> 1;            // tokens up to the wave's
-    const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2], p.ks[1]);
-    const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2], p.qs[1]);
-    float (*W)[kLd] = (float (*)[kLd])(lds + L::kW);     // [i][j]: W_ij
-    float (*Wt)[kLd] = (float (*)[kLd])(lds + L::kWt);   // [j][i]: W_ij
-    float (*F)[kLd] = (float (*)[kLd])(lds + L::kF);     // E + E^T
+    float (*W)[kLd] = (float (*)[kLd])(lds + L::kW);     // [i][j]: W_ij / rk_j
+    float (*Wt)[kLd] = (float (*)[kLd])(lds + L::kWt);   // [j][i]: W_ij / rq_i
+    float (*F)[kLd] = (float (*)[kLd])(lds + L::kF);     // [i][j]: (E + E^T)_ij / rk_j
+    {
+        const float* f = (const float*)(p.bpack + (slot * p.Hv + hk * p.group) * kBackPack + kDec);
+        const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2],
+                                        p.ks[1]);
+        const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2],
+                                        p.qs[1]);
+        RowTiles<IO, DK, 8> rk, rq;
+        rk.load(tk, 0, n, p.Dk, f + kScaleK);
+        rq.load(tq, 0, n, p.Dk, f + kScaleQ);
+        if (threadIdx.x < kChunk) {
+            backK[threadIdx.x] = 1.f / f[kScaleK + threadIdx.x];
+            backQ[threadIdx.x] = 1.f / f[kScaleQ + threadIdx.x];
+        }
+        rk.store(lds + L::kK);
+        rq.store(lds + L::kQ);
+    }
 
     dfloat4 dQ[HT], dK[HT];
 #pragma unroll
     for (int t = 0; t < HT; ++t) dQ[t] = dK[t] = dfloat4{0, 0, 0, 0};
+    const int padded = (p.Dv + 15) / 16 * 16;
 
     for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
         const long long ci = slot * p.Hv + h;
-        if (wave == 0) {
+        const float* S0 = p.states + ci * saved_floats(DK, p.Dv);
+        const float* D = gp.dstates + ci * saved_floats(DK, p.Dv);
+        const float* U = p.us + ci * saved_floats(kChunk, p.Dv);
+        const float* Y = gp.dys + ci * saved_floats(kChunk, p.Dv);
+        const char* dO = (const char*)gp.dout +
+                         ((sp.b * p.T + tok + have) * p.Hv + h) * (long long)p.Dv * kB;
+        const char* V = (const char*)p.v +
+                        (sp.b * p.vs[0] + (tok + have) * p.vs[1] + h * p.vs[2]) * kB;
+        // the thread's place among the eights of a slice
+        const int su_ = threadIdx.x, uu = threadIdx.x & 255;
+        const int s_tile = su_ / (KB * 64), s_in = su_ % (KB * 64);
+        const int u_tile = uu >> 7, u_in = uu & 127;
+        const float* UY = half == 0 ? U : Y;
+        // its column within 16: places hold c ^ 4 g
+        const int pc = c ^ (4 * g);
+        const auto load = [&](SliceRegs<IO>& x, int d0) __attribute__((always_inline)) {
+            const int ds = d0 + 16 * s_tile < padded ? d0 + 16 * s_tile : 0;
+            const int du = d0 + 16 * u_tile < padded ? d0 + 16 * u_tile : 0;
+            const du4* s = (const du4*)(S0 + (long long)ds * DK + s_in * 8);
+            const du4* d = (const du4*)(D + (long long)ds * DK + s_in * 8);
+            const du4* u = (const du4*)(UY + (long long)du * kChunk + u_in * 8);
+            typedef typename SliceRegs<IO>::piece piece;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (s_tile < 2) {
+                    x.s[j] = s[j];
+                    x.d[j] = d[j];
+                }
+                x.u[j] = u[j];
+                const int e = d0 + 16 * j + 4 * g < p.Dv ? d0 + 16 * j + 4 * g : 0;
+                x.o[j] = *(const piece*)(dO + e * kB);
+                x.v[j] = *(const piece*)(V + e * kB);
+            }
+        };
+        SliceRegs<IO> x;
+        load(x, 0);
+        // scales: largest of S0, D, U, dY over their columns (waves 0..3), and
+        // of dO
+        if (wave < 4) {
+            const float* m = wave == 0 ? S0 + (long long)DK * padded
+                             : wave == 1 ? D + (long long)DK * padded
+                             : wave == 2 ? U + (long long)kChunk * padded
+                                         : Y + (long long)kChunk * padded;
+            float a = 0.f;
+            for (int i = lane; i < p.Dv; i += 64) a = fmaxf(a, m[i]);
+#pragma unroll
+            for (int j = 1; j < 64; j <<= 1) a = fmaxf(a, __shfl_xor(a, j));
+            if (lane == 0) big[wave] = a;
+        } else {
             const long long gi = (sp.b * p.T + tok + (lane < n ? lane : 0)) * p.Hv + h;
-            const float gv = p.g[gi], bv = p.beta[gi];
-            G[lane] = decay_sum(lane < n ? gv : 0.f);
-            bet[lane] = lane < n ? bv : 0.f;
+            if (wave == 4) {
+                const float gv = p.g[gi], bv = p.beta[gi];
+                G[lane] = decay_sum(lane < n ? gv : 0.f);
+                bet[lane] = lane < n ? bv : 0.f;
+            }
         }
+        {
+            const char* base = (const char*)gp.dout + ((sp.b * p.T + tok) * p.Hv + h) *
+                                                          (long long)p.Dv * kB;
+            const int per = p.Dv / 8;
+            float a = 0.f;
+            for (int i = threadIdx.x; i < n * per; i += 512) {
+                const int row = i / per, e = (i - row * per) * 8;
+                float v[8];
+                load8<IO>(base, (long long)row * p.Hv * p.Dv + e, true, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
+            }
+#pragma unroll
+            for (int j = 1; j < 64; j <<= 1) a = fmaxf(a, __shfl_xor(a, j));
+            if (lane == 0) bigO[wave] = a;
+        }
+        __syncthreads();             // and the last head's matrices are used up
+        const Scale sS = scale_to(big[0]), sD = scale_to(big[1]), sU = scale_to(big[2]),
+                    sY = scale_to(big[3]);
+        float big_o = bigO[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) big_o = fmaxf(big_o, bigO[j]);
+        const Scale sO = scale_to(big_o);
+
+        float sd = 0.f, yv = 0.f;
+        const auto store = [&](const SliceRegs<IO>& x, int d0, uint4* to) __attribute__((always_inline)) {
+            if (s_tile < 2) {
+                const bool ok = d0 + 16 * s_tile + pc < p.Dv;
+                float s[8], d[8];
+                uint4 ts[2], td[2];
+                unpack8<IO_F32>(x.s, s);
+                unpack8<IO_F32>(x.d, d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    s[j] = ok ? s[j] : 0.f;
+                    d[j] = ok ? d[j] : 0.f;
+                    sd += s[j] * d[j];
+                }
+                split8h<2>(s, sS.to, ts);
+                split8h<2>(d, sD.to, td);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    to[L::kS + j * L::kSTerm + su_] = ts[j];
+                    to[L::kD + j * L::kSTerm + su_] = td[j];
+                }
+            }
+            float u[8];
+            uint4 tu[2];
+            unpack8<IO_F32>(x.u, u);
+            const bool ok = d0 + 16 * u_tile + pc < p.Dv;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = ok ? u[j] : 0.f;
+            split8h<2>(u, half == 0 ? sU.to : sY.to, tu);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                to[(half == 0 ? L::kU : L::kY) + j * L::kUTerm + uu] = tu[j];
+        };
+        store(x, 0, lds + L::kSlices);
+        __syncthreads();
         // products over the columns of the state, 32 at a time
         dfloat4 R1[HT], R2[HT], R3[HT], Dp[2], Dy[2];
 #pragma unroll
         for (int t = 0; t < HT; ++t) R1[t] = R2[t] = R3[t] = dfloat4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 2; ++j) Dp[j] = Dy[j] = dfloat4{0, 0, 0, 0};
-        float sd = 0.f, yv = 0.f;
-        const float* S0 = p.states + ci * p.Dk * (long long)p.Dv;
-        const float* D = gp.dstates + ci * p.Dk * (long long)p.Dv;
-        const float* U = p.us + ci * kChunk * (long long)p.Dv;
-        const float* Y = gp.dys + ci * kChunk * (long long)p.Dv;
-        const char* dO = (const char*)gp.dout +
-                         (((sp.b * p.T + tok + have) * p.Hv + h) * (long long)p.Dv) * kB;
-        const long long vat = sp.b * p.vs[0] + (tok + have) * p.vs[1] + h * p.vs[2];
-        // operands: tile t, lane (g, c) holds [tile_row(t, c)][d0 + 8 g + i];
-        // the thread's are those of tile `wave` of S0 and D, of tile `tile` of
-        // U or dY
-        const int arow = tile_row(wave, c);
-        const float* UY = half == 0 ? U : Y;
-        const auto load = [&](SliceRegs& x, int d0) __attribute__((always_inline)) {
-            const int e = d0 + 8 * g < p.Dv ? d0 + 8 * g : 0;
-            const long long sa = (long long)(arow < p.Dk ? arow : 0) * p.Dv + e;
-            const du4* s = (const du4*)(S0 + sa);
-            const du4* d = (const du4*)(D + sa);
-            const du4* u = (const du4*)(UY + (long long)mine * p.Dv + e);
-            const du4* v = (const du4*)((const char*)p.v + (vat + e) * kB);
-            const du4* o = (const du4*)(dO + e * kB);
+        for (int d0 = 0, b = 0; d0 < p.Dv; d0 += 32) {
+            const uint4* now = lds + L::kSlices + b * L::kSlice;
+            // B operands: columns of the wave's tokens
+            uint4 ob[NA], yb[2], ub[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                x.s[j] = s[j];
-                x.d[j] = d[j];
-                x.u[j] = u[j];
+                ub[j] = read_cols<64>(now + L::kU + j * L::kUTerm, tile, 0);
+                yb[j] = read_cols<64>(now + L::kY + j * L::kUTerm, tile, 0);
             }
-            x.v[0] = v[0];
-            x.o[0] = o[0];
-            if (IO == IO_F32) {
-                x.v[1] = v[1];
-                x.o[1] = o[1];
-            }
-        };
-        const auto store = [&](const SliceRegs& x, int d0, uint4* to) __attribute__((always_inline)) {
-            const bool ok = d0 + 8 * g < p.Dv;
-            if (wave < ST) {
-                const bool in = ok && arow < p.Dk;
-                float s[8], d[8];
-                uint4 ts[3], td[3];
-                unpack8<IO_F32>(x.s, s);
-                unpack8<IO_F32>(x.d, d);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s[j] = in ? s[j] : 0.f;
-                    d[j] = in ? d[j] : 0.f;
-                    sd += s[j] * d[j];
-                }
-                split8<3>(s, ts);
-                split8<3>(d, td);
-#pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    to[L::kS + j * ST * 64 + threadIdx.x] = ts[j];
-                    to[L::kD + j * ST * 64 + threadIdx.x] = td[j];
-                }
-            }
-            float u[8], v[8];
-            uint4 tu[3];
-            unpack8<IO_F32>(x.u, u);
-            unpack8<IO>(x.v, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                u[j] = ok ? u[j] : 0.f;
-                yv += half == 1 && ok && mine < n ? u[j] * v[j] : 0.f;
-            }
-            split8<3>(u, tu);
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-                to[(half == 0 ? L::kU : L::kY) + j * 256 + tile * 64 + lane] = tu[j];
-        };
-        SliceRegs x;
-        load(x, 0);
-        __syncthreads();             // the last head's matrices are used up
-        store(x, 0, lds);
-        __syncthreads();
-        for (int d0 = 0, b = 0; d0 < p.Dv; d0 += 32, b ^= 1) {
-            const uint4* now = lds + b * L::kSlice;
-            const bool ok = d0 + 8 * g < p.Dv;
-            // B operands: columns of the wave's tokens
-            uint4 ob[NO], yb[3], ub[3];
-            if constexpr (IO == IO_BF16) {
-                ob[0] = keep(ok && mine < n, __builtin_bit_cast(uint4, x.o[0]));
-            } else {
+            {
+                const bool ok0 = mine < n && d0 + 4 * g < p.Dv;
+                const bool ok1 = mine < n && d0 + 16 + 4 * g < p.Dv;
                 float o[8];
-                unpack8<IO>(x.o, o);
+                unpack_pieces<IO>(x.o, ok0, ok1, o);
+                split8h<NA>(o, sO.to, ob);
+                if (half == 1) {
+                    float v[8];
+                    unpack_pieces<IO>(x.v, ok0, ok1, v);
+                    const dh8 y0 = __builtin_bit_cast(dh8, yb[0]),
+                              y1 = __builtin_bit_cast(dh8, yb[1]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = ok && mine < n ? o[j] : 0.f;
-                split8<NO>(o, ob);
-            }
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                ub[j] = now[L::kU + j * 256 + tile * 64 + lane];
-                yb[j] = now[L::kY + j * 256 + tile * 64 + lane];
+                    for (int j = 0; j < 8; ++j) yv += ((float)y0[j] + (float)y1[j]) * v[j];
+                }
             }
             load(x, d0 + 32 < p.Dv ? d0 + 32 : 0);
 #pragma unroll
-            for (int t = 0; t < HT; ++t) {
-                uint4 a[3], d[3];
+            for (int t0 = 0; t0 < HT; t0 += 2) {
+                uint4 a[2][2], d[2][2];
 #pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    a[j] = now[L::kS + (j * ST + half * HT + t) * 64 + lane];
-                    d[j] = now[L::kD + (j * ST + half * HT + t) * 64 + lane];
-                }
-                R1[t] = mma_terms<3>(a, ob, R1[t]);
-                R2[t] = mma_terms<3>(a, yb, R2[t]);
-                R3[t] = mma_terms<3>(d, ub, R3[t]);
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        a[t][j] = read_cols<DK>(now + L::kS + j * L::kSTerm, half * HT + t0 + t, 0);
+                        d[t][j] = read_cols<DK>(now + L::kD + j * L::kSTerm, half * HT + t0 + t, 0);
+                    }
+                mma_tiles(a, ob, *(dfloat4 (*)[2])&R1[t0]);
+                mma_tiles(a, yb, *(dfloat4 (*)[2])&R2[t0]);
+                mma_tiles(d, ub, *(dfloat4 (*)[2])&R3[t0]);
             }
-            if (jwork)
+            if (jwork) {
+                uint4 a[2][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint4 a[3];
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        a[i] = now[L::kU + i * 256 + (2 * half + j) * 64 + lane];
-                    Dp[j] = mma_terms<3>(a, ob, Dp[j]);
-                    Dy[j] = mma_terms<3>(a, yb, Dy[j]);
-                }
-            if (d0 + 32 < p.Dv) store(x, d0 + 32, lds + (b ^ 1) * L::kSlice);
-            __syncthreads();
+                    for (int i = 0; i < 2; ++i)
+                        a[j][i] = read_cols<64>(now + L::kU + i * L::kUTerm, 2 * half + j, 0);
+                mma_tiles(a, ob, Dp);
+                mma_tiles(a, yb, Dy);
+            }
+            if (L::kBufs == 2) {
+                b ^= 1;
+                if (d0 + 32 < p.Dv) store(x, d0 + 32, lds + L::kSlices + b * L::kSlice);
+                __syncthreads();
+            } else {
+                __syncthreads();
+                if (d0 + 32 < p.Dv) store(x, d0 + 32, lds + L::kSlices);
+                __syncthreads();
+            }
         }
-        // keys and queries take the slices' place
-        {
-            RowTiles<IO, DK, 8> rk, rq;
-            rk.load(tk, 0, n, p.Dk);
-            rq.load(tq, 0, n, p.Dk);
-            rk.store(lds + L::kK);
-            rq.store(lds + L::kQ);
-        }
-        __syncthreads();
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) sd += __shfl_xor(sd, m);
+        yv *= sY.back;
         const double last = G[kChunk - 1], Gi = G[mine];
         const float eg = expf((float)Gi), ee = expf((float)(last - Gi)), b = bet[mine];
+        const float bk = backK[mine], bq = backQ[mine];
         // sums over the wave's elements of the head
         float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        {
+            const float f1 = p.scale * eg * (sS.back * sO.back), f2 = eg * (sS.back * sY.back),
+                        f3 = ee * (sD.back * sU.back);
 #pragma unroll
-        for (int t = 0; t < HT; ++t) {
-            // four elements of the token's key and query, from LDS
-            float qv[4], kv[4];
-            row4<IO, DK>(lds + L::kQ, tile, c, tile_row(half * HT + t, 4 * g), qv);
-            row4<IO, DK>(lds + L::kK, tile, c, tile_row(half * HT + t, 4 * g), kv);
+            for (int t = 0; t < HT; ++t) {
+                // four elements of the token's key and query
+                float qv[4], kv[4];
+                row4<NA, DK>(lds + L::kQ, tile, c, tile_row(half * HT + t, 4 * g), qv);
+                row4<NA, DK>(lds + L::kK, tile, c, tile_row(half * HT + t, 4 * g), kv);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                s1 += qv[r] * R1[t][r];
-                s2 += kv[r] * R2[t][r];
-                s3 += kv[r] * R3[t][r];
-                dQ[t][r] += p.scale * eg * R1[t][r];
-                dK[t][r] += ee * R3[t][r] - b * eg * R2[t][r];
+                for (int r = 0; r < 4; ++r) {
+                    const float r1 = f1 * R1[t][r], r2 = f2 * R2[t][r], r3 = f3 * R3[t][r];
+                    s1 += qv[r] * r1;
+                    s2 += kv[r] * r2;
+                    s3 += kv[r] * r3;
+                    dQ[t][r] += r1;
+                    dK[t][r] += r3 - b * r2;
+                }
             }
         }
-        s1 = p.scale * eg * s1;
-        s2 = eg * s2;
-        s3 = ee * s3;
+        s1 *= bq;
+        s2 *= bk;
+        s3 *= bk;
         // the 64 x 64 part: the lane's token is i, tile j's row 4 g + r is j
         float sg = 0.f, sb = yv;
         if (jwork) {
@@ -493,22 +585,19 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
             for (int j = 0; j < 2; ++j) kk[j] = qk[j] = dfloat4{0, 0, 0, 0};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                uint4 ko[NA], qo[NA];
+                uint4 ko[NA], qo[NA], a[2][NA];
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
                     ko[i] = lds[L::kK + ((i * 4 + tile) * KB + kb) * 64 + rslot];
                     qo[i] = lds[L::kQ + ((i * 4 + tile) * KB + kb) * 64 + rslot];
-                }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint4 a[NA];
-#pragma unroll
-                    for (int i = 0; i < NA; ++i)
-                        a[i] = lds[L::kK + ((i * 4 + 2 * half + j) * KB + kb) * 64 + rslot];
-                    kk[j] = Op::mma_io(a, ko, kk[j]);
-                    qk[j] = Op::mma_io(a, qo, qk[j]);
+                    for (int j = 0; j < 2; ++j)
+                        a[j][i] = lds[L::kK + ((i * 4 + 2 * half + j) * KB + kb) * 64 + rslot];
                 }
+                mma_tiles(a, ko, kk);
+                mma_tiles(a, qo, qk);
             }
+            const float fp = p.scale * (sU.back * sO.back), fy = sU.back * sY.back;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int j0 = tile_row(2 * half + j, 4 * g);
@@ -516,20 +605,22 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
                 dfloat4 wr;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
+                    const float bj = backK[j0 + r];
                     float w = 0.f, f = 0.f, t = 0.f;
                     if (mine >= j0 + r) {
                         const float gam = expf((float)(Gi - G[j0 + r]));
-                        w = p.scale * gam * Dp[j][r];
-                        const float x = mine > j0 + r ? gam * Dy[j][r] : 0.f;
+                        const float kij = kk[j][r] * (bk * bj);
+                        w = gam * (fp * Dp[j][r]);
+                        const float x = mine > j0 + r ? gam * (fy * Dy[j][r]) : 0.f;
                         f = -b * x;
-                        t = w * qk[j][r] + f * kk[j][r];
+                        t = w * (qk[j][r] * (bq * bj)) + f * kij;
                         sg += t;
-                        sb -= x * kk[j][r];
-                        F[mine][j0 + r] = f;
-                        if (mine > j0 + r) F[j0 + r][mine] = f;
+                        sb -= x * kij;
+                        F[mine][j0 + r] = f * bj;
+                        if (mine > j0 + r) F[j0 + r][mine] = f * bk;
                     }
-                    wr[r] = w;
-                    Wt[j0 + r][mine] = w;
+                    wr[r] = w * bj;
+                    Wt[j0 + r][mine] = w * bq;
                     cs[r] = t;
                 }
                 *(dfloat4*)&W[mine][j0] = wr;
@@ -602,14 +693,14 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
             wt[m] = *(const dfloat4*)&Wt[mine][tile_row(m, 4 * g)];
             ft[m] = *(const dfloat4*)&F[mine][tile_row(m, 4 * g)];
         }
-        const ColScale sw = Op::template scale_of<4>(wr), st = Op::template scale_of<4>(wt),
-                       sf = Op::template scale_of<4>(ft);
-        uint4 wb[2][NB], tb_[2][NB], fb[2][NB];
+        const Scale sw = scale_to(max_column(wr)), st = scale_to(max_column(wt)),
+                    sf = scale_to(max_column(ft));
+        uint4 wb[2][NO], tb_[2][NO], fb[2][NO];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            Op::split(wr[2 * tb], wr[2 * tb + 1], sw, wb[tb]);
-            Op::split(wt[2 * tb], wt[2 * tb + 1], st, tb_[tb]);
-            Op::split(ft[2 * tb], ft[2 * tb + 1], sf, fb[tb]);
+            split_acc<NO>(wr[2 * tb], wr[2 * tb + 1], sw.to, wb[tb]);
+            split_acc<NO>(wt[2 * tb], wt[2 * tb + 1], st.to, tb_[tb]);
+            split_acc<NO>(ft[2 * tb], ft[2 * tb + 1], sf.to, fb[tb]);
         }
 #pragma unroll
         for (int t = 0; t < HT; ++t) {
@@ -622,9 +713,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
                     kt[i] = read_cols<DK>(lds + L::kK + i * 4 * KB * 64, half * HT + t, tb);
                     qt[i] = read_cols<DK>(lds + L::kQ + i * 4 * KB * 64, half * HT + t, tb);
                 }
-                a = Op::mma_out(kt, wb[tb], a);
-                x = Op::mma_out(qt, tb_[tb], x);
-                y = Op::mma_out(kt, fb[tb], y);
+                a = mma_prod(kt, wb[tb], a);
+                x = mma_prod(qt, tb_[tb], x);
+                y = mma_prod(kt, fb[tb], y);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -632,7 +723,8 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
                 dK[t][r] += st.back * x[r] + sf.back * y[r];
             }
         }
-        __syncthreads();
+        // the next head's slices take the matrices' place only after its
+        // scales, behind a barrier
     }
     if (mine >= n) return;
     const long long o = ((sp.b * p.T + tok + mine) * p.Hk + hk) * p.Dk;

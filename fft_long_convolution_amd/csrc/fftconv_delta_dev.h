@@ -1,16 +1,20 @@
 // Device helpers of the gated delta rule kernels: spans of sequences, loads
-// of the I/O types, products on the bf16 matrix cores at 24 bits.
+// of the I/O types, products on the 16-bit matrix cores at fp32 accuracy.
 //
 // Matrix products.  States, solutions and gradients have to keep fp32
 // accuracy over thousands of chunks, and gfx950's fp32 matrix rate is 1/16 of
-// its bf16 rate.  So an fp32 operand x is written as three bf16 terms,
-// x = h + m + l with h the leading 8 bits of x, m those of x - h and l those
-// of the rest (24 bits), and a product is the sum of the term products whose
-// weight is not below 2^-24 of the whole: with an operand that is exact in
-// bf16 three matrix instructions, with one of f16 (two terms) five, of fp32
-// six.
+// its 16-bit rate.  So an fp32 operand x is written as two f16 terms, h = f16(x)
+// and l = f16(x - h), 22 bits, and a product is the sum of the term products
+// but the smallest: two matrix instructions with an operand that is exact in
+// one term, three otherwise.  (Three bf16 terms, 24 bits, need three and six,
+// and twice the vector work.)  f16 has little range, so operands are scaled by
+// powers of two that take their largest value to 2^14: the fp32 one column by
+// column, a column staying in one lane of each group of 16 from operand to
+// result; the other one row by row, by factors that the chunk's preparation
+// folds into the decays the rows are multiplied with anyway.  What is 2^-16
+// of the largest value still has all its 22 bits.
 //
-// Operand order.  v_mfma_f32_16x16x32_bf16 takes from lane (g = l/16, c =
+// Operand order.  v_mfma_f32_16x16x32_f16 takes from lane (g = l/16, c =
 // l%16) A[row c][k = 8g + i] and B[k = 8g + i][col c], i < 8, and leaves
 // D[row 4g + r][col c], r < 4.  Rows of a 16-row tile m stand for index
 // tile_row(m, row) = 32 (m/2) + 8 (row/4) + 4 (m%2) + row%4 of the matrix, so
@@ -29,8 +33,14 @@ typedef float dfloat4 __attribute__((ext_vector_type(4)));
 // of HIP's, a struct, end up in scratch memory here.
 typedef uint32_t du4 __attribute__((ext_vector_type(4)));
 
+// Terms: NA of an operand of the I/O type (16-bit values are exact in one),
+// NO of P, S and U where only outputs follow.  One f16 term, off by 2^-12, is
+// enough for a bf16 output, rounded by 2^-9; the others take both.
 template <int IO>
-struct IoTerms { static constexpr int n = IO == IO_BF16 ? 1 : IO == IO_F16 ? 2 : 3; };
+struct Io {
+    static constexpr int NA = IO == IO_F32 ? 2 : 1, NO = IO == IO_BF16 ? 1 : 2;
+    static constexpr int kB = IO == IO_F32 ? 4 : 2;
+};
 
 __device__ __forceinline__ int tile_row(int m, int row) {
     return 32 * (m >> 1) + 8 * (row >> 2) + 4 * (m & 1) + (row & 3);
@@ -146,6 +156,11 @@ __device__ __forceinline__ void store4(void* p, long long i, dfloat4 x) {
     }
 }
 
+// ------------------------------------------------------------ bf16 terms
+// x = h + m + l, h the leading 8 bits of x, m those of x - h, l those of the
+// rest: 24 bits, and fp32's range without a scale.  For the products that
+// come before the scales are known, and the join of segments.
+
 // the upper halves of a and b, a in the low one
 __device__ __forceinline__ uint32_t hi_pair(float a, float b) {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
@@ -169,43 +184,116 @@ __device__ __forceinline__ void split8(const float (&x)[8], uint4 (&t)[N]) {
         }
     }
 }
-template <int N>
-__device__ __forceinline__ void split_acc(dfloat4 lo, dfloat4 hi, uint4 (&t)[N]) {
-    const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    split8<N>(x, t);
-}
-
-__device__ __forceinline__ dfloat4 mma(uint4 a, uint4 b, dfloat4 c) {
+__device__ __forceinline__ dfloat4 mma_bf(uint4 a, uint4 b, dfloat4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(dbf8, a),
                                                    __builtin_bit_cast(dbf8, b), c, 0, 0, 0);
 }
-// c += a b over the term products of weight above 2^-8 LIM, small ones first
-template <int LIM, int NA, int NB>
-__device__ __forceinline__ dfloat4 mma_terms(const uint4 (&a)[NA], const uint4 (&b)[NB], dfloat4 c) {
+// c[m] += a[m] b for M tiles over the bf16 term products of weight above
+// 2^-24, small ones first, consecutive instructions on different accumulators
+template <int M, int NA, int NB>
+__device__ __forceinline__ void mma_bf_tiles(const uint4 (&a)[M][NA], const uint4 (&b)[NB],
+                                             dfloat4 (&c)[M]) {
 #pragma unroll
-    for (int w = LIM - 1; w >= 0; --w)
-#pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            const int j = w - i;
-            if (j >= 0 && j < NB) c = mma(a[i], b[j], c);
-        }
-    return c;
-}
-
-// c[m] += a[m] b for M tiles: the same products, but consecutive instructions
-// go to different accumulators
-template <int LIM, int M, int NA, int NB>
-__device__ __forceinline__ void mma_tiles(const uint4 (&a)[M][NA], const uint4 (&b)[NB],
-                                          dfloat4 (&c)[M]) {
-#pragma unroll
-    for (int w = LIM - 1; w >= 0; --w)
+    for (int w = 2; w >= 0; --w)
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
             const int j = w - i;
             if (j >= 0 && j < NB)
 #pragma unroll
-                for (int m = 0; m < M; ++m) c[m] = mma(a[m][i], b[j], c[m]);
+                for (int m = 0; m < M; ++m) c[m] = mma_bf(a[m][i], b[j], c[m]);
         }
+}
+
+// ------------------------------------------------------------- f16 terms
+
+typedef _Float16 dh8 __attribute__((ext_vector_type(8)));
+typedef _Float16 dh2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ dfloat4 mma_h(uint4 a, uint4 b, dfloat4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(dh8, a),
+                                                  __builtin_bit_cast(dh8, b), c, 0, 0, 0);
+}
+// x[8] times s as N terms
+template <int N>
+__device__ __forceinline__ void split8h(const float (&x)[8], float s, uint4 (&t)[N]) {
+    uint32_t u[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i] * s, b = x[2 * i + 1] * s;
+        const dh2 h = {(_Float16)a, (_Float16)b};
+        u[0][i] = __builtin_bit_cast(uint32_t, h);
+        if (N == 2) {
+            const dh2 l = {(_Float16)(a - (float)h.x), (_Float16)(b - (float)h.y)};
+            u[1][i] = __builtin_bit_cast(uint32_t, l);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) t[n] = make_uint4(u[n][0], u[n][1], u[n][2], u[n][3]);
+}
+template <int N>
+__device__ __forceinline__ void split_acc(dfloat4 lo, dfloat4 hi, float s, uint4 (&t)[N]) {
+    const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    split8h<N>(x, s, t);
+}
+// c[m] += a[m] b for M tiles: all term products but low by low, small ones
+// first, consecutive instructions on different accumulators
+template <int M, int NA, int NB>
+__device__ __forceinline__ void mma_tiles(const uint4 (&a)[M][NA], const uint4 (&b)[NB],
+                                          dfloat4 (&c)[M]) {
+#pragma unroll
+    for (int w = 1; w >= 0; --w)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = w - i;
+            if (j >= 0 && j < NB)
+#pragma unroll
+                for (int m = 0; m < M; ++m) c[m] = mma_h(a[m][i], b[j], c[m]);
+        }
+}
+template <int NA, int NB>
+__device__ __forceinline__ dfloat4 mma_prod(const uint4 (&a)[NA], const uint4 (&b)[NB], dfloat4 c) {
+#pragma unroll
+    for (int w = 1; w >= 0; --w)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = w - i;
+            if (j >= 0 && j < NB) c = mma_h(a[i], b[j], c);
+        }
+    return c;
+}
+// the first N of the terms
+template <int N>
+__device__ __forceinline__ const uint4 (&leading(const uint4 (&t)[2]))[N] {
+    return *(const uint4 (*)[N])&t;
+}
+
+// A power of two and its inverse.  Both are normal numbers for every largest
+// value, 0, infinity and NaN (which stays what it is) among them.
+struct Scale { float to, back; };
+__device__ __forceinline__ Scale scale_to(float largest) {
+    int e = (int)(__float_as_uint(largest) >> 23) & 255;
+    e = e < 28 ? 28 : e > 240 ? 240 : e;
+    return {__uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23),
+            __uint_as_float((uint32_t)(e - 14) << 23)};
+}
+// the larger value of the lane and of the other groups of 16 at its place
+__device__ __forceinline__ float max_groups(float a) {
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(a), false,
+                                                    false);
+    a = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(a), false,
+                                                    false);
+    return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+// largest magnitude in the lane's column of N tiles
+template <int N>
+__device__ __forceinline__ float max_column(const dfloat4 (&x)[N]) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) a = fmaxf(fmaxf(a, fabsf(x[i][r])), fabsf(x[i][r + 1]));
+    return max_groups(a);
 }
 
 // Loads under a condition read the tensor's first elements where it does not
@@ -254,19 +342,6 @@ __device__ __forceinline__ void load8(const void* p, long long i, bool ok, float
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = ok ? x[j] : 0.f;
 }
-// the same as bf16 terms
-template <int IO>
-__device__ __forceinline__ void load_terms(const void* p, long long i, bool ok,
-                                           uint4 (&t)[IoTerms<IO>::n]) {
-    if constexpr (IO == IO_BF16) {
-        t[0] = keep(ok, *(const uint4*)((const uint16_t*)p + (ok ? i : 0)));
-    } else {
-        float x[8];
-        load8<IO>(p, i, ok, x);
-        split8<IoTerms<IO>::n>(x, t);
-    }
-}
-
 // The tokens of one head: a base for the whole workgroup and byte offsets of
 // the lanes below 2^32 (the host keeps token strides below 2^24 elements), so
 // that addresses cost a lane one 32-bit register.
@@ -300,10 +375,11 @@ struct RowTiles {
     static constexpr int kWords = IO == IO_F32 ? 2 : 1;
     static constexpr int kB = IO == IO_F32 ? 4 : 2;
     du4 r[kMine][kWords];
+    float s[kMine];
     __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int Dk) {
         const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
         const int g = lane >> 4, c = (lane & 15) ^ (4 * g);
-        const char* s = x.at(token);
+        const char* p = x.at(token);
         const uint32_t stride = (uint32_t)x.bytes;
         const bool whole = n >= kChunk && Dk == DK;
 #pragma unroll
@@ -314,7 +390,7 @@ struct RowTiles {
             const uint32_t at = ok ? row * stride + e * kB : 0;
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
-                r[j][w] = *(const du4*)(s + at + 16 * w);
+                r[j][w] = *(const du4*)(p + at + 16 * w);
             }
         }
         if (!whole) {
@@ -329,7 +405,41 @@ struct RowTiles {
             }
         }
     }
+    // and the rows' scales (f16 needs none)
+    __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int Dk,
+                                         const float* scales) {
+        load(x, token, n, Dk);
+        if (IO == IO_F16) return;
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int c = (lane & 15) ^ (4 * (lane >> 4));
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            const int tile = W * j + wave;
+            s[j] = scales[tile_row((kTiles % W ? tile % kTiles : tile) / KB, c)];
+        }
+    }
+    // as f16 terms, Io<IO>::NA of them
     __device__ __forceinline__ void store(uint4* dst) const {
+        constexpr int NA = Io<IO>::NA;
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            const int at = (W * j + wave) * 64 + lane;
+            if (kTiles % W && W * j + wave >= kTiles) continue;
+            if constexpr (IO == IO_F16) {
+                ((du4*)dst)[at] = r[j][0];
+            } else {
+                float x[8];
+                uint4 t[NA];
+                unpack8<IO>(r[j], x);
+                split8h<NA>(x, s[j], t);
+#pragma unroll
+                for (int i = 0; i < NA; ++i) dst[i * kTiles * 64 + at] = t[i];
+            }
+        }
+    }
+    // as they are, fp32 in three bf16 terms
+    __device__ __forceinline__ void store_plain(uint4* dst) const {
         const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
@@ -337,8 +447,7 @@ struct RowTiles {
             if (kTiles % W && W * j + wave >= kTiles) continue;
             if constexpr (IO == IO_F32) {
                 float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[j][i >> 2][i & 3]);
+                unpack8<IO>(r[j], x);
                 uint4 t[3];
                 split8<3>(x, t);
 #pragma unroll
@@ -346,6 +455,26 @@ struct RowTiles {
             } else {
                 ((du4*)dst)[at] = r[j][0];
             }
+        }
+    }
+    // largest magnitudes of the rows, joined into `largest` in LDS (the bits
+    // of a magnitude grow with it)
+    __device__ __forceinline__ void max_rows(uint32_t* largest) const {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int c = (lane & 15) ^ (4 * (lane >> 4));
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            const int tile = W * j + wave;
+            if (kTiles % W && tile >= kTiles) continue;
+            float x[8];
+            unpack8<IO>(r[j], x);
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = __float_as_uint(x[i]) & 0x7fffffffu;
+                a = a > u ? a : u;
+            }
+            atomicMax(&largest[tile_row(tile / KB, c)], a);
         }
     }
 };
@@ -434,6 +563,30 @@ __device__ __forceinline__ void store_state(char* s, uint32_t bytes, uint32_t la
                     *(float*)(s + (tile_base(t) + r) * bytes + lane) = S[t][r];
     }
 }
+// Saved matrices (states and their gradients, U, dY): rows x Dv of fp32 for a
+// chunk and head, rows a multiple of 32, columns padded to 16 (cols of them
+// in all), and the largest magnitude of each column behind them.  Sixteen
+// columns together: block kb, place 16 g + (c ^ 4 g) holds rows
+// 32 kb + 8 g + i, i < 8, of column c: a lane's accumulators in two 16-byte
+// stores, and what RowTiles puts into LDS for transposed reads.
+__host__ __device__ __forceinline__ long long saved_floats(int rows, int Dv) {
+    const int cols = (Dv + 15) / 16 * 16;
+    return (long long)(rows + 1) * cols;
+}
+template <int KB>
+__device__ __forceinline__ void save_columns(float* all, long long ci, int Dv, int col,
+                                             const dfloat4 (&x)[2 * KB], float largest) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    float* base = all + ci * saved_floats(32 * KB, Dv);
+    dfloat4* d = (dfloat4*)(base + (long long)(col - c) * (32 * KB)) + (16 * g + (c ^ (4 * g))) * 2;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+        d[kb * 128] = x[2 * kb];
+        d[kb * 128 + 1] = x[2 * kb + 1];
+    }
+    if (g == 0) base[(long long)(Dv + 15) / 16 * 16 * (32 * KB) + col] = largest;
+}
+
 // The transposed operand from rows so filled: tile (t, tb), the lane's
 // [element tile_row(t, c)][token 32 tb + 8 g + i], i < 8.  Each transposed
 // read takes four tokens x 16 elements for 16 lanes.
@@ -455,10 +608,10 @@ __device__ __forceinline__ uint4 read_cols(const uint4* rows, int t, int tb) {
 }
 
 // Four consecutive elements (el a multiple of four) of token tile_row(m, c)
-// from rows filled by RowTiles.
-template <int IO, int DK>
+// from rows stored by RowTiles in NA f16 terms.
+template <int NA, int DK>
 __device__ __forceinline__ void row4(const uint4* rows, int m, int c, int el, float (&x)[4]) {
-    constexpr int KB = DK / 32, NA = IO == IO_F32 ? 3 : 1;
+    constexpr int KB = DK / 32;
     const int g = (el >> 3) & 3;
     const int at = (m * KB + (el >> 5)) * 64 + 16 * g + (c ^ (4 * g));
 #pragma unroll
@@ -469,114 +622,33 @@ __device__ __forceinline__ void row4(const uint4* rows, int m, int c, int el, fl
         const uint32_t u[2] = {r.x, r.y};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            if constexpr (IO == IO_F16) {
-                typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-                const h2 h = __builtin_bit_cast(h2, u[j]);
-                x[2 * j] = (float)h.x;
-                x[2 * j + 1] = (float)h.y;
-            } else {
-                x[2 * j] += __uint_as_float(u[j] << 16);
-                x[2 * j + 1] += __uint_as_float(u[j] & 0xffff0000u);
-            }
+            const dh2 h = __builtin_bit_cast(dh2, u[j]);
+            x[2 * j] += (float)h.x;
+            x[2 * j + 1] += (float)h.y;
         }
     }
 }
 
-// Products of an operand of the I/O type with an fp32 one.
-//   bf16: exact in one term, times three bf16 terms;
-//   fp32: three terms, times three (the six products above 2^-24);
-//   f16: exact in one f16 term, times two f16 terms, 22 bits.  f16 has little
-//     range, so each column of the fp32 operand is first multiplied with the
-//     power of two that takes its largest value to 2^14; a column stays in
-//     one lane of each group of 16 from operand to result.
-struct ColScale { float to, back; };
+// A chunk's pack, in uint4: T (two terms), the factors below, P (NO terms).
+// For the backward pass: T^T, factors, P^T (two terms).
+constexpr int kTerm = kTriTiles * 64;             // one term of a triangle
+constexpr int kDec = 2 * kTerm, kDecU4 = 128, kPm = kDec + kDecU4;
 template <int IO>
-struct Operand {
-    static constexpr int NA = IO == IO_F32 ? 3 : 1, NB = IO == IO_F16 ? 2 : 3;
-    static constexpr bool kScaled = IO == IO_F16;
-    // terms of P and U in the outputs' P U: 16 bits are enough for a 16-bit
-    // output, whose rounding is 2^-9 or 2^-12 of it
-    static constexpr int NP = IO == IO_F32 ? 3 : 2;
-    // uint4 of a chunk's pack: T (three terms), decays, P
-    static constexpr int kPack = (3 * kTriTiles + 1 + NP * kTriTiles) * 64;
-
-    template <int N>
-    static __device__ __forceinline__ ColScale scale_of(const dfloat4 (&x)[N]) {
-        if constexpr (!kScaled) return {1.f, 1.f};
-        float a = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) a = fmaxf(a, fabsf(x[i][r]));
-        a = fmaxf(a, __shfl_xor(a, 16));
-        a = fmaxf(a, __shfl_xor(a, 32));
-        // exponents where both factors are normal numbers
-        int e = (int)(__float_as_uint(a) >> 23);
-        e = e < 28 ? 28 : e > 240 ? 240 : e;
-        return {__uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23),
-                __uint_as_float((uint32_t)(e - 14) << 23)};
-    }
-    static __device__ __forceinline__ void split(dfloat4 lo, dfloat4 hi, const ColScale& s,
-                                                 uint4 (&t)[NB]) {
-        if constexpr (kScaled) {
-            typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-            h8 a, b;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = (i < 4 ? lo[i & 3] : hi[i & 3]) * s.to;
-                a[i] = (_Float16)x;
-                b[i] = (_Float16)(x - (float)a[i]);
-            }
-            t[0] = __builtin_bit_cast(uint4, a);
-            t[1] = __builtin_bit_cast(uint4, b);
-        } else {
-            split_acc<NB>(lo, hi, t);
-        }
-    }
-    static __device__ __forceinline__ dfloat4 mma(const uint4 (&a)[NA], const uint4 (&b)[NB],
-                                                  dfloat4 c) {
-        if constexpr (kScaled) return mma_h(a[0], b[0], mma_h(a[0], b[1], c));
-        else return mma_terms<3>(a, b, c);
-    }
-    template <int M>
-    static __device__ __forceinline__ void mma_all(const uint4 (&a)[M][NA], const uint4 (&b)[NB],
-                                                   dfloat4 (&c)[M]) {
-        if constexpr (kScaled) {
-#pragma unroll
-            for (int i = 1; i >= 0; --i)
-#pragma unroll
-                for (int m = 0; m < M; ++m) c[m] = mma_h(a[m][0], b[i], c[m]);
-        } else {
-            mma_tiles<3>(a, b, c);
-        }
-    }
-    template <int M>
-    static __device__ __forceinline__ void mma_all_out(const uint4 (&a)[M][NA],
-                                                       const uint4 (&b)[NB], dfloat4 (&c)[M]) {
-        if constexpr (kScaled) mma_all(a, b, c);
-        else mma_tiles<NP>(a, b, c);
-    }
-    // both operands of the I/O type
-    static __device__ __forceinline__ dfloat4 mma_io(const uint4 (&a)[NA], const uint4 (&b)[NA],
-                                                     dfloat4 c) {
-        if constexpr (kScaled) return mma_h(a[0], b[0], c);
-        else return mma_terms<3>(a, b, c);
-    }
-    // where a 16-bit output is all that follows, 16 bits of b
-    static __device__ __forceinline__ dfloat4 mma_out(const uint4 (&a)[NA], const uint4 (&b)[NB],
-                                                      dfloat4 c) {
-        if constexpr (kScaled) return mma(a, b, c);
-        else return mma_terms<NP>(a, b, c);
-    }
-    static __device__ __forceinline__ dfloat4 mma_h(uint4 a, uint4 b, dfloat4 c) {
-        typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a),
-                                                      __builtin_bit_cast(h8, b), c, 0, 0, 0);
-    }
+constexpr int pack_uint4() { return kPm + Io<IO>::NO * kTerm; }
+constexpr int kBackPack = kPm + 2 * kTerm;
+// Factors of the chunk's tokens, 64 floats each.  With rk, rq the scales of
+// the rows of K and Q and G, beta as in the formulas:
+enum Factor {
+    kDecayK = 0,      // e^G / rk
+    kDecayQ = 64,     // scale e^G / rq
+    kEndK = 128,      // e^(Gc-G) / rk
+    kBeta = 192,
+    kBackP = 256,     // inverse scales of the rows of P (backward: of P^T)
+    kScaleK = 320,    // rk
+    kScaleQ = 384,    // rq
+    kDecayAll = 448,  // e^Gc
+    kBackT = 449,     // inverse scale of T
 };
-// uint4 of a chunk's pack for the backward: T^T and P^T (three terms each)
-// around the decays
-constexpr int kBackPack = (6 * kTriTiles + 1) * 64;
 
 constexpr int kLd = 68;   // floats between rows of the 64 x 64 matrices in LDS
 
