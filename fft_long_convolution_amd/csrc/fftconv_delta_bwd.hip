@@ -114,7 +114,8 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
         dfloat4 dU[4], PO[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dU[m] = PO[m] = dfloat4{0, 0, 0, 0};
-        const Scale sd = scale_to(big_d), so = scale_to(max_column(dO));
+        const float big_o = max_column(dO);
+        const Scale sd = scale_to(big_d), so = scale_to(big_o);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             uint4 dt[2], a[4][NA];
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
         }
         {
             const float big_y = max_column(dY);
-            if (cok) save_columns<2>(gp.dys, ci, p.Dv, col, dY, big_y);
+            if (cok) save_columns<2>(gp.dys, ci, p.Dv, col, dY, big_y, big_o);
         }
         // dV = beta o dY; what goes back to the state through K and Q
 #pragma unroll
@@ -252,22 +253,21 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
 
 // ------------------------------------------------ the gradients of a chunk
 
-// LDS of delta_grads_kernel, in uint4: the chunk's keys and queries, then
-// slices (32 columns, two terms) of S0, D, U and dY, which the 64 x 64
-// matrices replace.
+// LDS of delta_grads_kernel, in uint4: a slice (32 columns, two terms) of S0, D,
+// U and dY; after the last one, in its place, the chunk's keys and queries and
+// two 64 x 64 matrices.  Two workgroups fit a CU where keys and queries are of
+// 16 bits, and their waits and work overlap.
 template <int IO, int DK>
 struct GradsLds {
     static constexpr int ST = DK / 16, KB = DK / 32;
     static constexpr int kRows = Io<IO>::NA * 4 * KB * 64;
-    static constexpr int kK = 0, kQ = kRows, kSlices = 2 * kRows;
     static constexpr int kSTerm = 2 * KB * 64, kUTerm = 4 * 64;      // one term of a slice
     static constexpr int kS = 0, kD = 2 * kSTerm, kU = 2 * kD, kY = kU + 2 * kUTerm;
     static constexpr int kSlice = kY + 2 * kUTerm;
-    static constexpr int kBufs = IO == IO_F32 ? 1 : 2;
     static constexpr int kMat = kChunk * kLd / 4;
-    static constexpr int kW = kSlices, kWt = kW + kMat, kF = kWt + kMat;
-    static constexpr int kTail = kBufs * kSlice > 3 * kMat ? kBufs * kSlice : 3 * kMat;
-    static constexpr int kBytes = (kSlices + kTail) * 16;
+    static constexpr int kK = 0, kQ = kRows, kWt = 2 * kRows, kF = kWt + kMat;
+    static constexpr int kTail = kF + kMat;
+    static constexpr int kBytes = (kSlice > kTail ? kSlice : kTail) * 16;
 };
 
 // Sum over the four groups of 16 lanes.
@@ -276,13 +276,13 @@ __device__ __forceinline__ float sum_groups(float x) {
     return x + __shfl_xor(x, 32);
 }
 
-// What a thread has in flight of a slice: eight elements of S0 and D, of U
-// (waves 0..3) or dY (4..7), and eight of its wave's token's dO and V in two
-// pieces of four.
-template <int IO>
+// What a thread has in flight of a slice: eights of S0, D, U and dY, and eight
+// elements of its wave's token's dO and V in two pieces of four.
+template <int IO, int DK>
 struct SliceRegs {
     typedef uint32_t piece __attribute__((ext_vector_type(IO == IO_F32 ? 4 : 2)));
-    du4 s[2], d[2], u[2];
+    static constexpr int NS = DK / 64;
+    du4 s[NS][2], d[NS][2], u[2], y[2];
     piece o[2], v[2];
 };
 template <int IO, typename P>
@@ -299,28 +299,30 @@ __device__ __forceinline__ void unpack_pieces(const P (&x)[2], bool ok0, bool ok
     for (int i = 0; i < 8; ++i) y[i] = (i < 4 ? ok0 : ok1) ? y[i] : 0.f;
 }
 
-// One workgroup of eight waves per chunk and key head.  A wave owns 16 tokens
-// (tile w % 4) as the columns of its products, R^T = S0 dO^T and so on, and
-// half of their rows (w / 4): half of a head's elements, and of the other
-// tokens in the 64 x 64 part.  So a lane has one token: what belongs to it
-// (decays, row sums) is a scalar of the lane, and sums over a head's elements
-// are sums in the lane and over four groups.  S0, D, U and dY come as the
-// walks saved them, eight rows of a column together, and are read transposed:
-// position i of the lane's eight columns is d0 + 16 (i/4) + 4 g + i%4.  They
-// and dO have one scale each.  The value heads that share the key head follow
-// one another, and their parts of dQ and dK are summed in registers, in a
-// fixed order.
-template <int IO, int DK>
-__global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
+// One workgroup of four waves per chunk and key head.  A wave owns 16 tokens as
+// the columns of its products, R^T = S0 dO^T and so on.  So a lane has one
+// token: what belongs to it (decays, row sums) is a scalar of the lane, and
+// sums over a head's elements are sums in the lane and over four groups; W_ij
+// with the lane's token as i is in its registers as the B operand of W K.  S0,
+// D, U and dY come as the walks saved them, eight rows of a column together,
+// and are read transposed: position i of the lane's eight columns is
+// d0 + 16 (i/4) + 4 g + i%4.  They and dO have one scale each.  The value heads
+// that share the key head follow one another, and their parts of dQ and dK are
+// summed in registers, in a fixed order; with one (GROUP false) R1 and R3 become
+// dQ and dK.
+template <int IO, int DK, bool GROUP>
+__global__ __launch_bounds__(256, GROUP || IO == IO_F32 ? 1 : 2)
+void delta_grads_kernel(DeltaGradParams gp) {
     typedef GradsLds<IO, DK> L;
+    typedef SliceRegs<IO, DK> Regs;
     const DeltaParams& p = gp.f;
     constexpr int NA = Io<IO>::NA, NO = Io<IO>::NO, KB = DK / 32, ST = L::ST, kB = Io<IO>::kB;
-    constexpr int HT = ST / 2;               // a wave's tiles of a head's elements
+    constexpr int NS = Regs::NS, GT = GROUP ? ST : 1;
     extern __shared__ uint4 lds[];
     __shared__ double G[kChunk];
-    __shared__ float bet[kChunk], colsum[4][kChunk], rowG[2][kChunk], rowB[2][kChunk];
+    __shared__ float bet[kChunk], colsum[4][kChunk], rowG[kChunk], rowB[kChunk];
     __shared__ float backK[kChunk], backQ[kChunk];
-    __shared__ float red[8], red3[8], big[8], bigO[8];
+    __shared__ float red[4], red3[4], big[5];
     const long long units = p.slots * p.Hk;
     const long long id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
@@ -334,37 +336,24 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
     const long long tok = sp.t0 + at;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
-    const int tile = wave & 3, half = wave >> 2;
     const int rslot = 16 * g + (c ^ (4 * g));        // of a row operand
-    const int mine = tile_row(tile, c);              // the lane's token
+    const int mine = tile_row(wave, c);              // the lane's token
     const int have = mine < n ? mine : n - 1;        // one to read from
-    const bool jwork = half <= tile >> 1;            // tokens up to the wave's
-    float (*W)[kLd] = (float (*)[kLd])(lds + L::kW);     // [i][j]: W_ij / rk_j
+    const int jtiles = wave < 2 ? 2 : 4;             // tiles of tokens up to the wave's
     float (*Wt)[kLd] = (float (*)[kLd])(lds + L::kWt);   // [j][i]: W_ij / rq_i
     float (*F)[kLd] = (float (*)[kLd])(lds + L::kF);     // [i][j]: (E + E^T)_ij / rk_j
-    {
-        const float* f = (const float*)(p.bpack + (slot * p.Hv + hk * p.group) * kBackPack + kDec);
-        const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2],
-                                        p.ks[1]);
-        const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2],
-                                        p.qs[1]);
-        RowTiles<IO, DK, 8> rk, rq;
-        rk.load(tk, 0, n, p.Dk, f + kScaleK);
-        rq.load(tq, 0, n, p.Dk, f + kScaleQ);
-        if (threadIdx.x < kChunk) {
-            backK[threadIdx.x] = 1.f / f[kScaleK + threadIdx.x];
-            backQ[threadIdx.x] = 1.f / f[kScaleQ + threadIdx.x];
-        }
-        rk.store(lds + L::kK);
-        rq.store(lds + L::kQ);
-    }
+    const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2], p.ks[1]);
+    const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2], p.qs[1]);
+    const float* fac = (const float*)(p.bpack + (slot * p.Hv + hk * p.group) * kBackPack + kDec);
 
-    dfloat4 dQ[HT], dK[HT];
+    dfloat4 dQ[GT], dK[GT];
 #pragma unroll
-    for (int t = 0; t < HT; ++t) dQ[t] = dK[t] = dfloat4{0, 0, 0, 0};
+    for (int t = 0; t < GT; ++t) dQ[t] = dK[t] = dfloat4{0, 0, 0, 0};
     const int padded = (p.Dv + 15) / 16 * 16;
+    const int hn = GROUP ? p.group : 1;
 
-    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+    for (int hi = 0; hi < hn; ++hi) {
+        const int h = hk * p.group + hi;
         const long long ci = slot * p.Hv + h;
         const float* S0 = p.states + ci * saved_floats(DK, p.Dv);
         const float* D = gp.dstates + ci * saved_floats(DK, p.Dv);
@@ -374,86 +363,81 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
                          ((sp.b * p.T + tok + have) * p.Hv + h) * (long long)p.Dv * kB;
         const char* V = (const char*)p.v +
                         (sp.b * p.vs[0] + (tok + have) * p.vs[1] + h * p.vs[2]) * kB;
-        // the thread's place among the eights of a slice
-        const int su_ = threadIdx.x, uu = threadIdx.x & 255;
-        const int s_tile = su_ / (KB * 64), s_in = su_ % (KB * 64);
-        const int u_tile = uu >> 7, u_in = uu & 127;
-        const float* UY = half == 0 ? U : Y;
-        // its column within 16: places hold c ^ 4 g
-        const int pc = c ^ (4 * g);
-        const auto load = [&](SliceRegs<IO>& x, int d0) __attribute__((always_inline)) {
-            const int ds = d0 + 16 * s_tile < padded ? d0 + 16 * s_tile : 0;
+        // the thread's eights of a slice: of U and dY number threadIdx.x, of
+        // S0 and D that and 256 further
+        const int u_tile = threadIdx.x >> 7, u_in = threadIdx.x & 127;
+        const int pc = c ^ (4 * g);          // their column within 16
+        const auto load = [&](Regs& x, int d0) __attribute__((always_inline)) {
+            typedef typename Regs::piece piece;
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                const int i = threadIdx.x + 256 * k, t = i / (KB * 64), in = i % (KB * 64);
+                const int ds = d0 + 16 * t < padded ? d0 + 16 * t : 0;
+                const du4* s = (const du4*)(S0 + (long long)ds * DK + in * 8);
+                const du4* d = (const du4*)(D + (long long)ds * DK + in * 8);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x.s[k][j] = s[j];
+                    x.d[k][j] = d[j];
+                }
+            }
             const int du = d0 + 16 * u_tile < padded ? d0 + 16 * u_tile : 0;
-            const du4* s = (const du4*)(S0 + (long long)ds * DK + s_in * 8);
-            const du4* d = (const du4*)(D + (long long)ds * DK + s_in * 8);
-            const du4* u = (const du4*)(UY + (long long)du * kChunk + u_in * 8);
-            typedef typename SliceRegs<IO>::piece piece;
+            const du4* u = (const du4*)(U + (long long)du * kChunk + u_in * 8);
+            const du4* y = (const du4*)(Y + (long long)du * kChunk + u_in * 8);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (s_tile < 2) {
-                    x.s[j] = s[j];
-                    x.d[j] = d[j];
-                }
                 x.u[j] = u[j];
+                x.y[j] = y[j];
                 const int e = d0 + 16 * j + 4 * g < p.Dv ? d0 + 16 * j + 4 * g : 0;
                 x.o[j] = *(const piece*)(dO + e * kB);
                 x.v[j] = *(const piece*)(V + e * kB);
             }
         };
-        SliceRegs<IO> x;
+        Regs x;
         load(x, 0);
-        // scales: largest of S0, D, U, dY over their columns (waves 0..3), and
-        // of dO
-        if (wave < 4) {
+        // scales: largest of S0, D, U, dY and dO over their columns
+        {
             const float* m = wave == 0 ? S0 + (long long)DK * padded
                              : wave == 1 ? D + (long long)DK * padded
                              : wave == 2 ? U + (long long)kChunk * padded
                                          : Y + (long long)kChunk * padded;
-            float a = 0.f;
-            for (int i = lane; i < p.Dv; i += 64) a = fmaxf(a, m[i]);
+            float a = 0.f, o = 0.f;
+            for (int i = lane; i < p.Dv; i += 64) {
+                a = fmaxf(a, m[i]);
+                if (wave == 3) o = fmaxf(o, m[padded + i]);
+            }
 #pragma unroll
-            for (int j = 1; j < 64; j <<= 1) a = fmaxf(a, __shfl_xor(a, j));
-            if (lane == 0) big[wave] = a;
-        } else {
-            const long long gi = (sp.b * p.T + tok + (lane < n ? lane : 0)) * p.Hv + h;
-            if (wave == 4) {
-                const float gv = p.g[gi], bv = p.beta[gi];
-                G[lane] = decay_sum(lane < n ? gv : 0.f);
-                bet[lane] = lane < n ? bv : 0.f;
+            for (int j = 1; j < 64; j <<= 1) {
+                a = fmaxf(a, __shfl_xor(a, j));
+                o = fmaxf(o, __shfl_xor(o, j));
+            }
+            if (lane == 0) {
+                big[wave] = a;
+                if (wave == 3) big[4] = o;
             }
         }
-        {
-            const char* base = (const char*)gp.dout + ((sp.b * p.T + tok) * p.Hv + h) *
-                                                          (long long)p.Dv * kB;
-            const int per = p.Dv / 8;
-            float a = 0.f;
-            for (int i = threadIdx.x; i < n * per; i += 512) {
-                const int row = i / per, e = (i - row * per) * 8;
-                float v[8];
-                load8<IO>(base, (long long)row * p.Hv * p.Dv + e, true, v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
-            }
-#pragma unroll
-            for (int j = 1; j < 64; j <<= 1) a = fmaxf(a, __shfl_xor(a, j));
-            if (lane == 0) bigO[wave] = a;
+        if (wave == 0) {
+            const long long gi = (sp.b * p.T + tok + (lane < n ? lane : 0)) * p.Hv + h;
+            const float gv = p.g[gi], bv = p.beta[gi];
+            G[lane] = decay_sum(lane < n ? gv : 0.f);
+            bet[lane] = lane < n ? bv : 0.f;
+        } else if (wave == 1) {
+            backK[lane] = 1.f / fac[kScaleK + lane];
+            backQ[lane] = 1.f / fac[kScaleQ + lane];
         }
         __syncthreads();             // and the last head's matrices are used up
         const Scale sS = scale_to(big[0]), sD = scale_to(big[1]), sU = scale_to(big[2]),
-                    sY = scale_to(big[3]);
-        float big_o = bigO[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) big_o = fmaxf(big_o, bigO[j]);
-        const Scale sO = scale_to(big_o);
-
+                    sY = scale_to(big[3]), sO = scale_to(big[4]);
         float sd = 0.f, yv = 0.f;
-        const auto store = [&](const SliceRegs<IO>& x, int d0, uint4* to) __attribute__((always_inline)) {
-            if (s_tile < 2) {
-                const bool ok = d0 + 16 * s_tile + pc < p.Dv;
+        const auto store = [&](const Regs& x, int d0) __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                const int i = threadIdx.x + 256 * k, t = i / (KB * 64);
+                const bool ok = d0 + 16 * t + pc < p.Dv;
                 float s[8], d[8];
                 uint4 ts[2], td[2];
-                unpack8<IO_F32>(x.s, s);
-                unpack8<IO_F32>(x.d, d);
+                unpack8<IO_F32>(x.s[k], s);
+                unpack8<IO_F32>(x.d[k], d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     s[j] = ok ? s[j] : 0.f;
@@ -464,113 +448,120 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
                 split8h<2>(d, sD.to, td);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    to[L::kS + j * L::kSTerm + su_] = ts[j];
-                    to[L::kD + j * L::kSTerm + su_] = td[j];
+                    lds[L::kS + j * L::kSTerm + i] = ts[j];
+                    lds[L::kD + j * L::kSTerm + i] = td[j];
                 }
             }
-            float u[8];
-            uint4 tu[2];
+            float u[8], y[8];
+            uint4 tu[2], ty[2];
             unpack8<IO_F32>(x.u, u);
+            unpack8<IO_F32>(x.y, y);
             const bool ok = d0 + 16 * u_tile + pc < p.Dv;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = ok ? u[j] : 0.f;
-            split8h<2>(u, half == 0 ? sU.to : sY.to, tu);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                to[(half == 0 ? L::kU : L::kY) + j * L::kUTerm + uu] = tu[j];
-        };
-        store(x, 0, lds + L::kSlices);
-        __syncthreads();
-        // products over the columns of the state, 32 at a time
-        dfloat4 R1[HT], R2[HT], R3[HT], Dp[2], Dy[2];
-#pragma unroll
-        for (int t = 0; t < HT; ++t) R1[t] = R2[t] = R3[t] = dfloat4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) Dp[j] = Dy[j] = dfloat4{0, 0, 0, 0};
-        for (int d0 = 0, b = 0; d0 < p.Dv; d0 += 32) {
-            const uint4* now = lds + L::kSlices + b * L::kSlice;
-            // B operands: columns of the wave's tokens
-            uint4 ob[NA], yb[2], ub[2];
+            for (int j = 0; j < 8; ++j) {
+                u[j] = ok ? u[j] : 0.f;
+                y[j] = ok ? y[j] : 0.f;
+            }
+            split8h<2>(u, sU.to, tu);
+            split8h<2>(y, sY.to, ty);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                ub[j] = read_cols<64>(now + L::kU + j * L::kUTerm, tile, 0);
-                yb[j] = read_cols<64>(now + L::kY + j * L::kUTerm, tile, 0);
+                lds[L::kU + j * L::kUTerm + threadIdx.x] = tu[j];
+                lds[L::kY + j * L::kUTerm + threadIdx.x] = ty[j];
             }
+        };
+        // products over the columns of the state, 32 at a time
+        dfloat4 R1[ST], R2[ST], R3[ST], Dp[4], Dy[4];
+#pragma unroll
+        for (int t = 0; t < ST; ++t) R1[t] = R2[t] = R3[t] = dfloat4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) Dp[j] = Dy[j] = dfloat4{0, 0, 0, 0};
+        for (int d0 = 0; d0 < p.Dv; d0 += 32) {
+            store(x, d0);
+            // B operands: columns of the wave's tokens
+            uint4 ob[NA], yb[2], ub[2];
+            float v[8];
             {
                 const bool ok0 = mine < n && d0 + 4 * g < p.Dv;
                 const bool ok1 = mine < n && d0 + 16 + 4 * g < p.Dv;
                 float o[8];
                 unpack_pieces<IO>(x.o, ok0, ok1, o);
                 split8h<NA>(o, sO.to, ob);
-                if (half == 1) {
-                    float v[8];
-                    unpack_pieces<IO>(x.v, ok0, ok1, v);
-                    const dh8 y0 = __builtin_bit_cast(dh8, yb[0]),
-                              y1 = __builtin_bit_cast(dh8, yb[1]);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) yv += ((float)y0[j] + (float)y1[j]) * v[j];
-                }
+                unpack_pieces<IO>(x.v, ok0, ok1, v);
             }
-            load(x, d0 + 32 < p.Dv ? d0 + 32 : 0);
+            __syncthreads();
 #pragma unroll
-            for (int t0 = 0; t0 < HT; t0 += 2) {
+            for (int j = 0; j < 2; ++j) {
+                ub[j] = read_cols<64>(lds + L::kU + j * L::kUTerm, wave, 0);
+                yb[j] = read_cols<64>(lds + L::kY + j * L::kUTerm, wave, 0);
+            }
+            {
+                const dh8 y0 = __builtin_bit_cast(dh8, yb[0]), y1 = __builtin_bit_cast(dh8, yb[1]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) yv += ((float)y0[j] + (float)y1[j]) * v[j];
+            }
+#pragma unroll
+            for (int t0 = 0; t0 < ST; t0 += 2) {
                 uint4 a[2][2], d[2][2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        a[t][j] = read_cols<DK>(now + L::kS + j * L::kSTerm, half * HT + t0 + t, 0);
-                        d[t][j] = read_cols<DK>(now + L::kD + j * L::kSTerm, half * HT + t0 + t, 0);
+                        a[t][j] = read_cols<DK>(lds + L::kS + j * L::kSTerm, t0 + t, 0);
+                        d[t][j] = read_cols<DK>(lds + L::kD + j * L::kSTerm, t0 + t, 0);
                     }
                 mma_tiles(a, ob, *(dfloat4 (*)[2])&R1[t0]);
                 mma_tiles(a, yb, *(dfloat4 (*)[2])&R2[t0]);
                 mma_tiles(d, ub, *(dfloat4 (*)[2])&R3[t0]);
             }
-            if (jwork) {
-                uint4 a[2][2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+            for (int j0 = 0; j0 < 4; j0 += 2)
+                if (j0 < jtiles) {
+                    uint4 a[2][2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        a[j][i] = read_cols<64>(now + L::kU + i * L::kUTerm, 2 * half + j, 0);
-                mma_tiles(a, ob, Dp);
-                mma_tiles(a, yb, Dy);
-            }
-            if (L::kBufs == 2) {
-                b ^= 1;
-                if (d0 + 32 < p.Dv) store(x, d0 + 32, lds + L::kSlices + b * L::kSlice);
-                __syncthreads();
-            } else {
-                __syncthreads();
-                if (d0 + 32 < p.Dv) store(x, d0 + 32, lds + L::kSlices);
-                __syncthreads();
-            }
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            a[j][i] = read_cols<64>(lds + L::kU + i * L::kUTerm, j0 + j, 0);
+                    mma_tiles(a, ob, *(dfloat4 (*)[2])&Dp[j0]);
+                    mma_tiles(a, yb, *(dfloat4 (*)[2])&Dy[j0]);
+                }
+            load(x, d0 + 32 < p.Dv ? d0 + 32 : 0);
+            __syncthreads();
         }
+        {
+            RowTiles<IO, DK, 4> rk, rq;
+            rk.load(tk, 0, n, p.Dk, fac + kScaleK);
+            rq.load(tq, 0, n, p.Dk, fac + kScaleQ);
+            rk.store(lds + L::kK);
+            rq.store(lds + L::kQ);
+        }
+        __syncthreads();
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) sd += __shfl_xor(sd, m);
         yv *= sY.back;
         const double last = G[kChunk - 1], Gi = G[mine];
         const float eg = expf((float)Gi), ee = expf((float)(last - Gi)), b = bet[mine];
         const float bk = backK[mine], bq = backQ[mine];
-        // sums over the wave's elements of the head
+        // sums over the elements of a head
         float s1 = 0.f, s2 = 0.f, s3 = 0.f;
         {
             const float f1 = p.scale * eg * (sS.back * sO.back), f2 = eg * (sS.back * sY.back),
                         f3 = ee * (sD.back * sU.back);
 #pragma unroll
-            for (int t = 0; t < HT; ++t) {
+            for (int t = 0; t < ST; ++t) {
                 // four elements of the token's key and query
                 float qv[4], kv[4];
-                row4<NA, DK>(lds + L::kQ, tile, c, tile_row(half * HT + t, 4 * g), qv);
-                row4<NA, DK>(lds + L::kK, tile, c, tile_row(half * HT + t, 4 * g), kv);
+                row4<NA, DK>(lds + L::kQ, wave, c, tile_row(t, 4 * g), qv);
+                row4<NA, DK>(lds + L::kK, wave, c, tile_row(t, 4 * g), kv);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float r1 = f1 * R1[t][r], r2 = f2 * R2[t][r], r3 = f3 * R3[t][r];
                     s1 += qv[r] * r1;
                     s2 += kv[r] * r2;
                     s3 += kv[r] * r3;
-                    dQ[t][r] += r1;
-                    dK[t][r] += r3 - b * r2;
+                    R1[t][r] = r1;
+                    R3[t][r] = r3 - b * r2;
                 }
             }
         }
@@ -579,77 +570,70 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
         s3 *= bk;
         // the 64 x 64 part: the lane's token is i, tile j's row 4 g + r is j
         float sg = 0.f, sb = yv;
-        if (jwork) {
-            dfloat4 kk[2], qk[2];
+        {
+            dfloat4 kk[4], qk[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) kk[j] = qk[j] = dfloat4{0, 0, 0, 0};
+            for (int j = 0; j < 4; ++j) kk[j] = qk[j] = dfloat4{0, 0, 0, 0};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                uint4 ko[NA], qo[NA], a[2][NA];
+                uint4 ko[NA], qo[NA];
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
-                    ko[i] = lds[L::kK + ((i * 4 + tile) * KB + kb) * 64 + rslot];
-                    qo[i] = lds[L::kQ + ((i * 4 + tile) * KB + kb) * 64 + rslot];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        a[j][i] = lds[L::kK + ((i * 4 + 2 * half + j) * KB + kb) * 64 + rslot];
+                    ko[i] = lds[L::kK + ((i * 4 + wave) * KB + kb) * 64 + rslot];
+                    qo[i] = lds[L::kQ + ((i * 4 + wave) * KB + kb) * 64 + rslot];
                 }
-                mma_tiles(a, ko, kk);
-                mma_tiles(a, qo, qk);
+#pragma unroll
+                for (int j0 = 0; j0 < 4; j0 += 2)
+                    if (j0 < jtiles) {
+                        uint4 a[2][NA];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int i = 0; i < NA; ++i)
+                                a[j][i] = lds[L::kK + ((i * 4 + j0 + j) * KB + kb) * 64 + rslot];
+                        mma_tiles(a, ko, *(dfloat4 (*)[2])&kk[j0]);
+                        mma_tiles(a, qo, *(dfloat4 (*)[2])&qk[j0]);
+                    }
             }
             const float fp = p.scale * (sU.back * sO.back), fy = sU.back * sY.back;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int j0 = tile_row(2 * half + j, 4 * g);
+            for (int j = 0; j < 4; ++j) {
+                const int j0 = tile_row(j, 4 * g);
                 float cs[4];
-                dfloat4 wr;
+                const dfloat4 bj = *(const dfloat4*)&backK[j0];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float bj = backK[j0 + r];
                     float w = 0.f, f = 0.f, t = 0.f;
-                    if (mine >= j0 + r) {
+                    if (j < jtiles && mine >= j0 + r) {
                         const float gam = expf((float)(Gi - G[j0 + r]));
-                        const float kij = kk[j][r] * (bk * bj);
+                        const float kij = kk[j][r] * (bk * bj[r]);
                         w = gam * (fp * Dp[j][r]);
                         const float x = mine > j0 + r ? gam * (fy * Dy[j][r]) : 0.f;
                         f = -b * x;
-                        t = w * (qk[j][r] * (bq * bj)) + f * kij;
+                        t = w * (qk[j][r] * (bq * bj[r])) + f * kij;
                         sg += t;
                         sb -= x * kij;
-                        F[mine][j0 + r] = f * bj;
+                        F[mine][j0 + r] = f * bj[r];
                         if (mine > j0 + r) F[j0 + r][mine] = f * bk;
                     }
-                    wr[r] = w * bj;
+                    Dp[j][r] = w * bj[r];        // the lane's row of W
                     Wt[j0 + r][mine] = w * bq;
                     cs[r] = t;
                 }
-                *(dfloat4*)&W[mine][j0] = wr;
                 // sums over the wave's tokens
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
 #pragma unroll
                     for (int m = 1; m < 16; m <<= 1) cs[r] += __shfl_xor(cs[r], m);
-                    if (c == 0) colsum[tile][j0 + r] = cs[r];
-                }
-            }
-        } else {
-            // tokens after the wave's
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int j0 = tile_row(2 * half + j, 4 * g);
-                *(dfloat4*)&W[mine][j0] = dfloat4{0, 0, 0, 0};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    Wt[j0 + r][mine] = 0.f;
-                    if (c == 0) colsum[tile][j0 + r] = 0.f;
+                    if (c == 0) colsum[wave][j0 + r] = cs[r];
                 }
             }
         }
         const float rg = sum_groups(sg + s1 - b * s2 - s3), rb = sum_groups(sb - s2);
         s3 = sum_groups(s3);
         if (g == 0) {
-            rowG[half][mine] = rg;
-            rowB[half][mine] = rb;
+            rowG[mine] = rg;
+            rowB[mine] = rb;
         }
         // the chunk's last decay
 #pragma unroll
@@ -660,17 +644,11 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
         }
         __syncthreads();
         if (wave == 0) {
-            double x = ((double)rowG[0][lane] + rowG[1][lane]) -
-                       (colsum[0][lane] + colsum[1][lane] + colsum[2][lane] + colsum[3][lane]);
-            if (lane == 63) {
-                float s = 0.f, d = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s += red3[j];
-                    d += red[j];
-                }
-                x += s + expf((float)last) * d;
-            }
+            double x = (double)rowG[lane] - (colsum[0][lane] + colsum[1][lane] + colsum[2][lane] +
+                                             colsum[3][lane]);
+            if (lane == 63)
+                x += (red3[0] + red3[1] + red3[2] + red3[3]) +
+                     expf((float)last) * (red[0] + red[1] + red[2] + red[3]);
             // sums from the end
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
@@ -682,36 +660,35 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
                 // a factor of 0 has the gradient 0, which the difference of
                 // sums above meets only up to their rounding
                 gp.dg[gi] = expf(p.g[gi]) == 0.f ? 0.f : (float)x;
-                gp.dbeta[gi] = rowB[0][lane] + rowB[1][lane];
+                gp.dbeta[gi] = rowB[lane];
             }
         }
         // dQ^T += K^T W^T, dK^T += Q^T W + K^T F
-        dfloat4 wr[4], wt[4], ft[4];
+        dfloat4 wt[4], ft[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            wr[m] = *(const dfloat4*)&W[mine][tile_row(m, 4 * g)];
             wt[m] = *(const dfloat4*)&Wt[mine][tile_row(m, 4 * g)];
             ft[m] = *(const dfloat4*)&F[mine][tile_row(m, 4 * g)];
         }
-        const Scale sw = scale_to(max_column(wr)), st = scale_to(max_column(wt)),
+        const Scale sw = scale_to(max_column(Dp)), st = scale_to(max_column(wt)),
                     sf = scale_to(max_column(ft));
         uint4 wb[2][NO], tb_[2][NO], fb[2][NO];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            split_acc<NO>(wr[2 * tb], wr[2 * tb + 1], sw.to, wb[tb]);
+            split_acc<NO>(Dp[2 * tb], Dp[2 * tb + 1], sw.to, wb[tb]);
             split_acc<NO>(wt[2 * tb], wt[2 * tb + 1], st.to, tb_[tb]);
             split_acc<NO>(ft[2 * tb], ft[2 * tb + 1], sf.to, fb[tb]);
         }
 #pragma unroll
-        for (int t = 0; t < HT; ++t) {
+        for (int t = 0; t < ST; ++t) {
             dfloat4 a = {0, 0, 0, 0}, x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
                 uint4 kt[NA], qt[NA];
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
-                    kt[i] = read_cols<DK>(lds + L::kK + i * 4 * KB * 64, half * HT + t, tb);
-                    qt[i] = read_cols<DK>(lds + L::kQ + i * 4 * KB * 64, half * HT + t, tb);
+                    kt[i] = read_cols<DK>(lds + L::kK + i * 4 * KB * 64, t, tb);
+                    qt[i] = read_cols<DK>(lds + L::kQ + i * 4 * KB * 64, t, tb);
                 }
                 a = mma_prod(kt, wb[tb], a);
                 x = mma_prod(qt, tb_[tb], x);
@@ -719,22 +696,29 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaGradParams gp) {
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                dQ[t][r] += sw.back * a[r];
-                dK[t][r] += st.back * x[r] + sf.back * y[r];
+                R1[t][r] += sw.back * a[r];
+                R3[t][r] += st.back * x[r] + sf.back * y[r];
+            }
+            if (GROUP) {
+                dQ[t % GT] += R1[t];
+                dK[t % GT] += R3[t];
             }
         }
-        // the next head's slices take the matrices' place only after its
-        // scales, behind a barrier
-    }
-    if (mine >= n) return;
-    const long long o = ((sp.b * p.T + tok + mine) * p.Hk + hk) * p.Dk;
+        if (!GROUP || hi + 1 == hn) {
+            if (mine < n) {
+                const long long o = ((sp.b * p.T + tok + mine) * p.Hk + hk) * p.Dk;
 #pragma unroll
-    for (int t = 0; t < HT; ++t) {
-        const int el = tile_row(half * HT + t, 4 * g);
-        if (el < p.Dk) {
-            store4<IO>(gp.dq, o + el, dQ[t]);
-            store4<IO>(gp.dk, o + el, dK[t]);
+                for (int t = 0; t < ST; ++t) {
+                    const int el = tile_row(t, 4 * g);
+                    if (el < p.Dk) {
+                        store4<IO>(gp.dq, o + el, GROUP ? dQ[t % GT] : R1[t]);
+                        store4<IO>(gp.dk, o + el, GROUP ? dK[t % GT] : R3[t]);
+                    }
+                }
+            }
         }
+        // the next head's slices take the matrices' place only behind the
+        // barrier that follows its scales
     }
 }
 
@@ -754,15 +738,19 @@ hipError_t rscan_io(const DeltaGradParams& p, hipStream_t s) {
     return p.f.Dv <= 64 ? rscan_w<IO, DK, 4>(p, s) : rscan_w<IO, DK, 8>(p, s);
 }
 
-template <int IO, int DK>
-hipError_t grads_io(const DeltaGradParams& p, hipStream_t s) {
+template <int IO, int DK, bool GROUP>
+hipError_t grads_launch(const DeltaGradParams& p, hipStream_t s) {
     const int bytes = GradsLds<IO, DK>::kBytes;
-    const hipError_t e = hipFuncSetAttribute((const void*)delta_grads_kernel<IO, DK>,
+    const hipError_t e = hipFuncSetAttribute((const void*)delta_grads_kernel<IO, DK, GROUP>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((delta_grads_kernel<IO, DK>), dim3((unsigned)xcd_blocks(p.f.slots * p.f.Hk)),
-                       dim3(512), bytes, s, p);
+    hipLaunchKernelGGL((delta_grads_kernel<IO, DK, GROUP>),
+                       dim3((unsigned)xcd_blocks(p.f.slots * p.f.Hk)), dim3(256), bytes, s, p);
     return hipGetLastError();
+}
+template <int IO, int DK>
+hipError_t grads_io(const DeltaGradParams& p, hipStream_t s) {
+    return p.f.group == 1 ? grads_launch<IO, DK, false>(p, s) : grads_launch<IO, DK, true>(p, s);
 }
 
 }  // namespace

@@ -564,18 +564,19 @@ __device__ __forceinline__ void store_state(char* s, uint32_t bytes, uint32_t la
     }
 }
 // Saved matrices (states and their gradients, U, dY): rows x Dv of fp32 for a
-// chunk and head, rows a multiple of 32, columns padded to 16 (cols of them
-// in all), and the largest magnitude of each column behind them.  Sixteen
+// chunk and head, rows a multiple of 32, columns padded to 16, and
+// behind them the largest magnitude of each column (and, with dY, of dO's).  Sixteen
 // columns together: block kb, place 16 g + (c ^ 4 g) holds rows
 // 32 kb + 8 g + i, i < 8, of column c: a lane's accumulators in two 16-byte
 // stores, and what RowTiles puts into LDS for transposed reads.
 __host__ __device__ __forceinline__ long long saved_floats(int rows, int Dv) {
     const int cols = (Dv + 15) / 16 * 16;
-    return (long long)(rows + 1) * cols;
+    return (long long)(rows + 2) * cols;
 }
 template <int KB>
 __device__ __forceinline__ void save_columns(float* all, long long ci, int Dv, int col,
-                                             const dfloat4 (&x)[2 * KB], float largest) {
+                                             const dfloat4 (&x)[2 * KB], float largest,
+                                             float other = 0.f) {
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     float* base = all + ci * saved_floats(32 * KB, Dv);
     dfloat4* d = (dfloat4*)(base + (long long)(col - c) * (32 * KB)) + (16 * g + (c ^ (4 * g))) * 2;
@@ -584,7 +585,12 @@ __device__ __forceinline__ void save_columns(float* all, long long ci, int Dv, i
         d[kb * 128] = x[2 * kb];
         d[kb * 128 + 1] = x[2 * kb + 1];
     }
-    if (g == 0) base[(long long)(Dv + 15) / 16 * 16 * (32 * KB) + col] = largest;
+    if (g == 0) {
+        const int cols = (Dv + 15) / 16 * 16;
+        float* m = base + (long long)cols * (32 * KB) + col;
+        m[0] = largest;
+        m[cols] = other;
+    }
 }
 
 // The transposed operand from rows so filled: tile (t, tb), the lane's

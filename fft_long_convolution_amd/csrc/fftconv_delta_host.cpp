@@ -227,7 +227,7 @@ bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
     if (!product(delta_slots(d), d->Hv, 1, 1, &n) || n > kMaxGrid) return false;
     // saved matrices: rows for the largest magnitudes, columns padded to 16
     const size_t cols = (d->Dv + 15) / 16 * 16, rows = d->Dk <= 64 ? 64 : 128;
-    if (!product(n, rows + 1, cols, 1, &x) || !product(n, kChunk + 1, cols, 1, &y)) return false;
+    if (!product(n, rows + 2, cols, 1, &x) || !product(n, kChunk + 2, cols, 1, &y)) return false;
     const bool cut = per <= (d->T + kChunk - 1) / kChunk;
     const size_t segs = delta_segs(d, per);
     if (!product(segs, d->Hv, (d->Dv + d->Dk + 15) / 16, 1, &m) || m > kMaxGrid) return false;
