@@ -20,10 +20,11 @@ import ctypes
 
 import torch
 
-from .fftconv import DTYPES, FFTConvError, _torch_dtype
+from .fftconv import DTYPES, FFTConvError
 from .fftconv import lib as _base_lib
 
 NORMS = {"rms": 0, "l2": 1}
+TORCH_DTYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 
 _LL3 = ctypes.c_longlong * 3
 
@@ -84,11 +85,21 @@ def _check(t, name, shape, dtype, device):
         raise ValueError("%s must be on %s" % (name, device))
 
 
+def _out(t, name, shape, dtype, device):
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
 def _strided(t, step):
-    """t, or a copy of it where its strides or its address do not suit the
-    kernels' 16-byte accesses."""
+    """t, or a copy of it where its strides do not suit the kernels' 16-byte
+    accesses."""
     s = t.stride()
-    if t.numel() and (s[-1] != 1 and t.shape[-1] > 1 or t.data_ptr() & 15 or
+    if t.numel() and (s[-1] != 1 and t.shape[-1] > 1 or
                       any(x % step and n > 1 for x, n in zip(s[:-1], t.shape))):
         t = t.clone(memory_format=torch.contiguous_format)
     return t
@@ -100,14 +111,44 @@ def _dense(t):
     return t.clone() if t.data_ptr() & 15 else t
 
 
+def _layout(ts):
+    """What the checks of a call's tensors depend on."""
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device) for t in ts])
+
+
 class _Op:
+    # descriptors of calls that passed the checks, by the operator's settings
+    # and the sizes, strides, types and devices of the tensors
+    _known = {}
+
     def __init__(self, dtype):
         if dtype not in DTYPES:
             raise ValueError("dtype must be one of %s" % list(DTYPES))
         self.dtype = dtype
-        self._dt = _torch_dtype(dtype)
+        self._dt = TORCH_DTYPES[dtype]
         self._step = 4 if dtype == "f32" else 8
         self._lib = lib()
+
+    def _checked(self, kind, ts):
+        """The call's tensors in a layout the library takes, its descriptor
+        and what else follows from the sizes: from `kind` (a method that
+        checks and describes) where no such call was seen before.  Misaligned
+        tensors are copied."""
+        key = (kind, self._settings, _layout(ts))
+        found = self._known.get(key)
+        if found is None:
+            found, ts = getattr(self, kind)(*ts)
+            if len(self._known) >= 4096:
+                self._known.clear()
+            # tensors that had to be copied have another layout now
+            self._known[(kind, self._settings, _layout(ts))] = found
+        ptrs = [0 if t is None else t.data_ptr() for t in ts]
+        for i, x in enumerate(ptrs):
+            if x & 15 and (x & 7 or ts[i].dtype != torch.int64):
+                ts = list(ts)
+                ts[i] = ts[i].clone()
+                ptrs[i] = ts[i].data_ptr()
+        return found, ts, ptrs
 
     def _first(self, q, dims):
         if q.dim() != dims:
@@ -116,8 +157,8 @@ class _Op:
             raise ValueError("q must be a CUDA tensor")
         return q.device
 
-    def _call(self, name, device, stream, kept, *args):
-        """Run the entry point `name` on `stream` (default: the device's
+    def _call(self, fn, device, stream, kept, *args):
+        """Run the entry point `fn` on `stream` (default: the device's
         current one).  kept: tensors made for this call, which the allocator
         must not hand out before `stream` has passed it."""
         current = torch.cuda.current_stream(device)
@@ -130,12 +171,12 @@ class _Op:
                 if t is not None:
                     t.record_stream(stream)
         if torch.cuda.current_device() == device.index:
-            st = getattr(self._lib, name)(*args, stream.cuda_stream)
+            st = fn(*args, stream.cuda_stream)
         else:
             with torch.cuda.device(device):
-                st = getattr(self._lib, name)(*args, stream.cuda_stream)
+                st = fn(*args, stream.cuda_stream)
         if st != 0:
-            raise FFTConvError(st, name)
+            raise FFTConvError(st, fn.__name__)
 
     @staticmethod
     def _space(nbytes, given, device, name):
@@ -166,8 +207,9 @@ class QKNorm(_Op):
             raise ValueError("norm must be one of %s" % list(NORMS))
         self.D, self.rotary_dim, self.norm = D, rotary_dim, norm
         self.eps, self.interleaved = eps, interleaved
+        self._settings = (D, rotary_dim, norm, eps, interleaved, dtype)
 
-    def _inputs(self, q, k, q_weight, k_weight, cos, sin, positions):
+    def _describe(self, q, k, q_weight, k_weight, cos, sin, positions):
         dev = self._first(q, 4)
         B, T, Hq, D = q.shape
         if D != self.D:
@@ -188,16 +230,18 @@ class QKNorm(_Op):
             _check(cos, "cos", (rows, self.rotary_dim // 2), torch.float32, dev)
             _check(sin, "sin", (rows, self.rotary_dim // 2), torch.float32, dev)
             _check(positions, "positions", (B, T), torch.int64, dev)
-            cos, sin, positions = _dense(cos), _dense(sin), positions.contiguous()
+            cos, sin, positions = cos.contiguous(), sin.contiguous(), positions.contiguous()
         else:
             cos = sin = positions = None
         q, k = _strided(q, self._step), _strided(k, self._step)
-        q_weight = None if q_weight is None else _dense(q_weight)
-        k_weight = None if k_weight is None else _dense(k_weight)
+        q_weight = None if q_weight is None else q_weight.contiguous()
+        k_weight = None if k_weight is None else k_weight.contiguous()
         desc = QKNormDesc(DTYPES[self.dtype], B, T, Hq, Hk, D, self.rotary_dim,
                           1 if self.interleaved else 0, NORMS[self.norm], self.eps, rows,
                           _LL3(*q.stride()[:3]), _LL3(*k.stride()[:3]))
-        return dev, desc, (q, k, q_weight, k_weight, cos, sin, positions)
+        ref = ctypes.byref(desc)
+        need = self._lib.fftconv_qknorm_workspace_bytes(ref)
+        return (dev, ref, need), (q, k, q_weight, k_weight, cos, sin, positions)
 
     def forward(self, q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
                 out=None, stream=None):
@@ -205,39 +249,36 @@ class QKNorm(_Op):
         normed and rotated (q, k).  weights: fp32 [D] or None; cos, sin: fp32
         [P, rotary_dim/2]; positions: int64 [B, T], rows of the tables (a
         position outside them gives NaN).  out: a pair of tensors."""
-        dev, desc, ins = self._inputs(q, k, q_weight, k_weight, cos, sin, positions)
-        if out is None:
-            out = (torch.empty(q.shape, dtype=q.dtype, device=dev),
-                   torch.empty(k.shape, dtype=k.dtype, device=dev))
-        for name, o, x in (("out[0]", out[0], q), ("out[1]", out[1], k)):
-            _check(o, name, x.shape, self._dt, dev)
-            if not o.is_contiguous():
-                raise ValueError("%s must be contiguous" % name)
-        self._call("fftconv_qknorm_forward", dev, stream, ins + tuple(out), ctypes.byref(desc),
-                   *map(_ptr, ins), _ptr(out[0]), _ptr(out[1]))
-        return out[0], out[1]
+        (dev, ref, _), ins, ptrs = self._checked(
+            "_describe", (q, k, q_weight, k_weight, cos, sin, positions))
+        yq, yk = (None, None) if out is None else out
+        yq = _out(yq, "out[0]", q.shape, self._dt, dev)
+        yk = _out(yk, "out[1]", k.shape, self._dt, dev)
+        self._call(self._lib.fftconv_qknorm_forward, dev, stream, (*ins, yq, yk), ref, *ptrs,
+                   yq.data_ptr(), yk.data_ptr())
+        return yq, yk
 
     def backward(self, q, k, dq_out, dk_out, q_weight=None, k_weight=None, cos=None, sin=None,
                  positions=None, workspace=None, stream=None):
         """Gradients for dq_out, dk_out = dL/d(outputs of forward): returns
         (dq, dk, dq_weight, dk_weight), the last two fp32 [D] or None where
         there is no weight."""
-        dev, desc, ins = self._inputs(q, k, q_weight, k_weight, cos, sin, positions)
+        (dev, ref, need), ins, ptrs = self._checked(
+            "_describe", (q, k, q_weight, k_weight, cos, sin, positions))
         _check(dq_out, "dq_out", q.shape, self._dt, dev)
         _check(dk_out, "dk_out", k.shape, self._dt, dev)
         dq_out, dk_out = _dense(dq_out), _dense(dk_out)
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        dq = torch.empty(q.shape, dtype=self._dt, device=dev)
+        dk = torch.empty(k.shape, dtype=self._dt, device=dev)
         dwq = None if q_weight is None else torch.empty(self.D, dtype=torch.float32, device=dev)
         dwk = None if k_weight is None else torch.empty(self.D, dtype=torch.float32, device=dev)
-        need = 0
+        ws = None
         if dwq is not None or dwk is not None:
-            need = self._lib.fftconv_qknorm_workspace_bytes(ctypes.byref(desc))
-        ws = self._space(need, workspace, dev, "workspace")
-        self._call("fftconv_qknorm_backward", dev, stream,
-                   ins + (dq_out, dk_out, dq, dk, dwq, dwk, ws), ctypes.byref(desc),
-                   *map(_ptr, ins), _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq),
-                   _ptr(dwk), _ptr(ws), self._bytes(ws))
+            ws = self._space(need, workspace, dev, "workspace")
+        self._call(self._lib.fftconv_qknorm_backward, dev, stream,
+                   (*ins, dq_out, dk_out, dq, dk, dwq, dwk, ws), ref, *ptrs, _ptr(dq_out),
+                   _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws),
+                   self._bytes(ws))
         return dq, dk, dwq, dwk
 
 
@@ -254,8 +295,9 @@ class GatedDelta(_Op):
         super().__init__(dtype)
         self.D_k, self.D_v = D_k, D_v
         self.scale = D_k ** -0.5 if scale is None else float(scale)
+        self._settings = (D_k, D_v, dtype, self.scale)
 
-    def _inputs(self, q, k, v, g, beta, initial_state, cu_seqlens):
+    def _describe(self, q, k, v, g, beta, cu_seqlens, initial_state):
         dev = self._first(q, 4)
         B, T, Hk, _ = q.shape
         if v.dim() != 4:
@@ -276,53 +318,45 @@ class GatedDelta(_Op):
         state = (rows, Hv, self.D_k, self.D_v)
         if initial_state is not None:
             _check(initial_state, "initial_state", state, torch.float32, dev)
-            initial_state = _dense(initial_state)
+            initial_state = initial_state.contiguous()
         q, k, v = (_strided(x if x.stride(1) < 1 << 24 else x.contiguous(), self._step)
                    for x in (q, k, v))
         desc = DeltaDesc(DTYPES[self.dtype], B, T, Hk, Hv, self.D_k, self.D_v, n, self.scale,
                          _LL3(*q.stride()[:3]), _LL3(*k.stride()[:3]), _LL3(*v.stride()[:3]))
-        return dev, desc, state, (q, k, v, _dense(g), _dense(beta), cu_seqlens, initial_state)
-
-    def _forward(self, args, out, final_state, saved, workspace, stream):
-        dev, desc, state, ins = args
-        v = ins[2]
-        if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-        else:
-            _check(out, "out", v.shape, self._dt, dev)
-            if not out.is_contiguous():
-                raise ValueError("out must be contiguous")
-        if final_state is None:
-            final_state = torch.empty(state, dtype=torch.float32, device=dev)
-        else:
-            _check(final_state, "final_state", state, torch.float32, dev)
-            if not final_state.is_contiguous():
-                raise ValueError("final_state must be contiguous")
         ref = ctypes.byref(desc)
-        ws = self._space(self._lib.fftconv_delta_workspace_bytes(ref), workspace, dev,
-                         "workspace")
-        self._call("fftconv_delta_forward", dev, stream, ins + (out, final_state, saved, ws), ref,
-                   *map(_ptr, ins), _ptr(out), _ptr(final_state), _ptr(saved),
-                   self._bytes(saved), _ptr(ws), self._bytes(ws))
-        return out, final_state
+        L = self._lib
+        sizes = (L.fftconv_delta_workspace_bytes(ref), L.fftconv_delta_saved_bytes(ref),
+                 L.fftconv_delta_backward_workspace_bytes(ref))
+        return ((dev, ref, state, sizes),
+                (q, k, v, g.contiguous(), beta.contiguous(), cu_seqlens, initial_state))
+
+    def _forward(self, ins, out, final_state, saved, train, workspace, stream):
+        (dev, ref, state, sizes), ins, ptrs = self._checked("_describe", ins)
+        out = _out(out, "out", ins[2].shape, self._dt, dev)
+        final_state = _out(final_state, "final_state", state, torch.float32, dev)
+        ws = self._space(sizes[0], workspace, dev, "workspace")
+        if train:
+            saved = self._space(sizes[1], saved, dev, "saved")
+        self._call(self._lib.fftconv_delta_forward, dev, stream,
+                   (*ins, out, final_state, saved, ws), ref, *ptrs, out.data_ptr(),
+                   final_state.data_ptr(), _ptr(saved), self._bytes(saved), ws.data_ptr(),
+                   self._bytes(ws))
+        return out, final_state, saved
 
     def forward(self, q, k, v, g, beta, initial_state=None, cu_seqlens=None, out=None,
                 final_state=None, workspace=None, stream=None):
         """Outputs [B, T, Hv, D_v] and final states [rows, Hv, D_k, D_v].
         cu_seqlens: int64 [n + 1] with the bounds of n sequences packed in the
         one batch row (they may be empty); rows = n then, B otherwise."""
-        return self._forward(self._inputs(q, k, v, g, beta, initial_state, cu_seqlens), out,
-                             final_state, None, workspace, stream)
+        return self._forward((q, k, v, g, beta, cu_seqlens, initial_state), out, final_state,
+                             None, False, workspace, stream)[:2]
 
     def forward_train(self, q, k, v, g, beta, initial_state=None, cu_seqlens=None, out=None,
                       final_state=None, saved=None, workspace=None, stream=None):
         """As forward, and what backward needs besides the inputs (an opaque
         tensor of bytes): returns (o, final_state, saved)."""
-        args = self._inputs(q, k, v, g, beta, initial_state, cu_seqlens)
-        saved = self._space(self._lib.fftconv_delta_saved_bytes(ctypes.byref(args[1])), saved,
-                            args[0], "saved")
-        o, state = self._forward(args, out, final_state, saved, workspace, stream)
-        return o, state, saved
+        return self._forward((q, k, v, g, beta, cu_seqlens, initial_state), out, final_state,
+                             saved, True, workspace, stream)
 
     def backward(self, q, k, v, g, beta, d_out, saved, d_final_state=None, initial_state=None,
                  cu_seqlens=None, workspace=None, stream=None):
@@ -330,32 +364,26 @@ class GatedDelta(_Op):
         d_out = dL/do, d_final_state = dL/d(final state) (None: 0).  Returns
         (dq, dk, dv, dg, dbeta, d_initial_state); the last is None where there
         is no initial_state."""
-        dev, desc, state, ins = self._inputs(q, k, v, g, beta, initial_state, cu_seqlens)
-        q, k, v, g, beta, cu, init = ins
-        _check(d_out, "d_out", v.shape, self._dt, dev)
+        (dev, ref, state, sizes), ins, ptrs = self._checked(
+            "_describe", (q, k, v, g, beta, cu_seqlens, initial_state))
+        _check(d_out, "d_out", ins[2].shape, self._dt, dev)
         d_out = _dense(d_out)
         if d_final_state is not None:
             _check(d_final_state, "d_final_state", state, torch.float32, dev)
             d_final_state = _dense(d_final_state)
         if saved.device != dev or not saved.is_contiguous():
             raise ValueError("saved must be what forward_train returned")
-        ref = ctypes.byref(desc)
-        ws = self._space(self._lib.fftconv_delta_backward_workspace_bytes(ref), workspace, dev,
-                         "workspace")
-        new = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v, g, beta)]
-        new.append(None if init is None else torch.empty(state, dtype=torch.float32, device=dev))
-        self._call("fftconv_delta_backward", dev, stream,
-                   (*ins, saved, d_out, d_final_state, ws, *new), ref, *map(_ptr, ins[:6]),
-                   _ptr(saved), self._bytes(saved), _ptr(d_out), _ptr(d_final_state),
-                   *map(_ptr, new), _ptr(ws), self._bytes(ws))
+        ws = self._space(sizes[2], workspace, dev, "workspace")
+        new = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in ins[:5]]
+        new.append(None if initial_state is None
+                   else torch.empty(state, dtype=torch.float32, device=dev))
+        self._call(self._lib.fftconv_delta_backward, dev, stream,
+                   (*ins, saved, d_out, d_final_state, ws, *new), ref, *ptrs[:6], _ptr(saved),
+                   self._bytes(saved), _ptr(d_out), _ptr(d_final_state), *map(_ptr, new),
+                   _ptr(ws), self._bytes(ws))
         return tuple(new)
 
-    def step(self, q, k, v, g, beta, state, slots=None, out=None, stream=None):
-        """One token for each of N requests: q, k [N, Hk, D_k], v [N, Hv, D_v],
-        g, beta [N, Hv]; state [pool, Hv, D_k, D_v] fp32, updated in place;
-        slots int64 [N], the state of each request (default: request i has
-        state i; outside the pool, such as -1: no state, output 0; two
-        requests must not share one).  Returns o [N, Hv, D_v]."""
+    def _describe_step(self, q, k, v, g, beta, slots, state):
         dev = self._first(q, 3)
         N, Hk, _ = q.shape
         if v.dim() != 3 or state.dim() != 4:
@@ -373,18 +401,24 @@ class GatedDelta(_Op):
         if slots is not None:
             _check(slots, "slots", (N,), torch.int64, dev)
             slots = slots.contiguous()
-        if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-        else:
-            _check(out, "out", v.shape, self._dt, dev)
-            if not out.is_contiguous():
-                raise ValueError("out must be contiguous")
         q, k, v = (_strided(x, self._step) for x in (q, k, v))
-        g, beta = _dense(g), _dense(beta)
-        st = [(x.stride(0), 0, x.stride(1)) for x in (q, k, v)]
+        st = [_LL3(x.stride(0), 0, x.stride(1)) for x in (q, k, v)]
         desc = DeltaDesc(DTYPES[self.dtype], N, 1, Hk, Hv, self.D_k, self.D_v, 0, self.scale,
-                         _LL3(*st[0]), _LL3(*st[1]), _LL3(*st[2]))
-        self._call("fftconv_delta_step", dev, stream, (q, k, v, g, beta, state, slots, out),
-                   ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                   _ptr(state), pool, _ptr(slots), _ptr(out))
+                         *st)
+        return ((dev, ctypes.byref(desc), pool),
+                (q, k, v, g.contiguous(), beta.contiguous(), slots, state))
+
+    def step(self, q, k, v, g, beta, state, slots=None, out=None, stream=None):
+        """One token for each of N requests: q, k [N, Hk, D_k], v [N, Hv, D_v],
+        g, beta [N, Hv]; state [pool, Hv, D_k, D_v] fp32, updated in place;
+        slots int64 [N], the state of each request (default: request i has
+        state i; outside the pool, such as -1: no state, output 0; two
+        requests must not share one).  Returns o [N, Hv, D_v]."""
+        if state.data_ptr() & 15:
+            raise ValueError("state must be 16-byte aligned")
+        (dev, ref, pool), ins, ptrs = self._checked("_describe_step",
+                                                    (q, k, v, g, beta, slots, state))
+        out = _out(out, "out", v.shape, self._dt, dev)
+        self._call(self._lib.fftconv_delta_step, dev, stream, (*ins, out), ref, *ptrs[:5],
+                   ptrs[6], pool, ptrs[5], out.data_ptr())
         return out
