@@ -13,7 +13,8 @@
 // I/O type.
 //
 // The pass moves each element once in and once out and does some ten
-// operations on it, so HBM bounds it.  A lane holds 8 consecutive elements
+// operations on it, so HBM bounds it: 64 x 1024 tokens of 12 heads of 128 in
+// bf16, 403 MB, take 76 us (5.3 TB/s; a streaming copy reaches 6.0).  A lane holds 8 consecutive elements
 // (one 16-byte access at 16 bits, two at 32), the lanes of a head (D/8,
 // rounded up to a power of two) sum by shuffles, and a group of lanes walks
 // over heads of ONE token, so the token's cosines and sines are read once
@@ -26,20 +27,31 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;     // heads in flight in a group of lanes
 
+typedef uint32_t qu4 __attribute__((ext_vector_type(4)));
 template <int IO>
-struct Raw8 { uint4 v; };
+struct Raw8 { qu4 v; };
 template <>
-struct Raw8<IO_F32> { uint4 v, w; };
+struct Raw8<IO_F32> { qu4 v, w; };
 
-template <int IO>
+// NT: past the caches, for tensors that do not stay there anyway
+template <bool NT>
+__device__ __forceinline__ qu4 load16(const void* p) {
+    return NT ? __builtin_nontemporal_load((const qu4*)p) : *(const qu4*)p;
+}
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, qu4 x) {
+    if (NT) __builtin_nontemporal_store(x, (qu4*)p);
+    else *(qu4*)p = x;
+}
+
+template <int IO, bool NT>
 __device__ __forceinline__ Raw8<IO> load8(const void* p, long long i) {
     Raw8<IO> r;
     if constexpr (IO == IO_F32) {
-        const uint4* s = (const uint4*)((const float*)p + i);
-        r.v = s[0];
-        r.w = s[1];
+        r.v = load16<NT>((const float*)p + i);
+        r.w = load16<NT>((const float*)p + i + 4);
     } else {
-        r.v = *(const uint4*)((const uint16_t*)p + i);
+        r.v = load16<NT>((const uint16_t*)p + i);
     }
     return r;
 }
@@ -67,12 +79,14 @@ __device__ __forceinline__ void unpack8(const Raw8<IO>& r, float (&x)[8]) {
     }
 }
 
-template <int IO>
+template <int IO, bool NT>
 __device__ __forceinline__ void store8(void* p, long long i, const float (&x)[8]) {
     if constexpr (IO == IO_F32) {
-        float4* d = (float4*)((float*)p + i);
-        d[0] = make_float4(x[0], x[1], x[2], x[3]);
-        d[1] = make_float4(x[4], x[5], x[6], x[7]);
+        qu4 u[2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j >> 2][j & 3] = __float_as_uint(x[j]);
+        store16<NT>((float*)p + i, u[0]);
+        store16<NT>((float*)p + i + 4, u[1]);
     } else {
         uint32_t u[4];
 #pragma unroll
@@ -85,7 +99,7 @@ __device__ __forceinline__ void store8(void* p, long long i, const float (&x)[8]
                 u[j] = __builtin_bit_cast(uint32_t, h);
             }
         }
-        *(uint4*)((uint16_t*)p + i) = make_uint4(u[0], u[1], u[2], u[3]);
+        store16<NT>((uint16_t*)p + i, qu4{u[0], u[1], u[2], u[3]});
     }
 }
 
@@ -178,7 +192,7 @@ __device__ __forceinline__ void load_weight(const float* w, int c, bool have, fl
 // A group of LPR lanes takes (token, part): the heads part, part + parts, ...
 // of the token's Hq + Hk.  All lanes of a wave run the same trip counts, so
 // every shuffle has its partners; a lane without work holds zeros.
-template <int IO, int LPR>
+template <int IO, int LPR, bool NT>
 __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkNormParams p) {
     const int c = threadIdx.x & (LPR - 1);
     const long long unit = ((long long)blockIdx.x * kThreads + threadIdx.x) / LPR;
@@ -205,8 +219,8 @@ __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkNormParams p) {
             ok[j] = have && h < H;
             raw[j] = Raw8<IO>{};
             if (ok[j])
-                raw[j] = h < p.Hq ? load8<IO>(p.q, qb + h * p.qs[2])
-                                  : load8<IO>(p.k, kb + (h - p.Hq) * p.ks[2]);
+                raw[j] = h < p.Hq ? load8<IO, NT>(p.q, qb + h * p.qs[2])
+                                  : load8<IO, NT>(p.k, kb + (h - p.Hq) * p.ks[2]);
         }
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
@@ -224,14 +238,14 @@ __global__ __launch_bounds__(kThreads) void qknorm_fwd_kernel(QkNormParams p) {
             for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (isq ? wq[i] : wk[i]);
             turn8(p, t, x);
             if (ok[j]) {
-                if (isq) store8<IO>(p.qo, (token * p.Hq + h) * p.D + 8 * c, x);
-                else store8<IO>(p.ko, (token * p.Hk + (h - p.Hq)) * p.D + 8 * c, x);
+                if (isq) store8<IO, NT>(p.qo, (token * p.Hq + h) * p.D + 8 * c, x);
+                else store8<IO, NT>(p.ko, (token * p.Hk + (h - p.Hq)) * p.D + 8 * c, x);
             }
         }
     }
 }
 
-template <int IO, int LPR>
+template <int IO, int LPR, bool NT>
 __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkNormParams p) {
     const int c = threadIdx.x & (LPR - 1);
     const int H = p.Hq + p.Hk;
@@ -265,11 +279,11 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkNormParams p) {
                 rx[j] = rd[j] = Raw8<IO>{};
                 if (ok[j]) {
                     if (h < p.Hq) {
-                        rx[j] = load8<IO>(p.q, qb + h * p.qs[2]);
-                        rd[j] = load8<IO>(p.dqo, (token * p.Hq + h) * p.D + 8 * c);
+                        rx[j] = load8<IO, NT>(p.q, qb + h * p.qs[2]);
+                        rd[j] = load8<IO, NT>(p.dqo, (token * p.Hq + h) * p.D + 8 * c);
                     } else {
-                        rx[j] = load8<IO>(p.k, kb + (h - p.Hq) * p.ks[2]);
-                        rd[j] = load8<IO>(p.dko, (token * p.Hk + (h - p.Hq)) * p.D + 8 * c);
+                        rx[j] = load8<IO, NT>(p.k, kb + (h - p.Hq) * p.ks[2]);
+                        rd[j] = load8<IO, NT>(p.dko, (token * p.Hk + (h - p.Hq)) * p.D + 8 * c);
                     }
                 }
             }
@@ -299,8 +313,8 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkNormParams p) {
                         if (isq) gq[i] += xr; else gk[i] += xr;
                         x[i] = r * (m[i] * (isq ? wq[i] : wk[i])) - x[i] * e;
                     }
-                    if (isq) store8<IO>(p.dq, (token * p.Hq + h) * p.D + 8 * c, x);
-                    else store8<IO>(p.dk, (token * p.Hk + (h - p.Hq)) * p.D + 8 * c, x);
+                    if (isq) store8<IO, NT>(p.dq, (token * p.Hq + h) * p.D + 8 * c, x);
+                    else store8<IO, NT>(p.dk, (token * p.Hk + (h - p.Hq)) * p.D + 8 * c, x);
                 }
             }
         }
@@ -334,58 +348,84 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkNormParams p) {
     }
 }
 
-// Sums the blocks' weight gradients: one workgroup per 16 columns, 16
-// threads a column, in a fixed order.
+// Sums the blocks' weight gradients: a workgroup takes four columns, 64 threads
+// a column, in a fixed order.
 __global__ __launch_bounds__(256) void qknorm_dw_kernel(QkNormParams p) {
-    __shared__ float sums[16][17];
-    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
-    const int i = blockIdx.x * 16 + col;
+    __shared__ float sums[64][5];
+    const int col = threadIdx.x & 3, row = threadIdx.x >> 2;
+    const int i = blockIdx.x * 4 + col;          // 2 D is a multiple of four
     float a = 0.f;
-    if (i < 2 * p.D)
-        for (int b = row; b < p.blocks; b += 16) a += p.part[(long long)b * 2 * p.D + i];
+#pragma unroll 4
+    for (int b = row; b < p.blocks; b += 64) a += p.part[(long long)b * 2 * p.D + i];
     sums[row][col] = a;
     __syncthreads();
-    if (row == 0 && i < 2 * p.D) {
+    if (row < 8) {
+        a = 0.f;
 #pragma unroll
-        for (int j = 1; j < 16; ++j) a += sums[j][col];
+        for (int j = 0; j < 8; ++j) a += sums[8 * row + j][col];
+    }
+    __syncthreads();
+    if (row < 8) sums[row][col] = a;
+    __syncthreads();
+    if (row == 0) {
+#pragma unroll
+        for (int j = 1; j < 8; ++j) a += sums[j][col];
         float* d = i < p.D ? p.dwq : p.dwk;
         if (d) d[i < p.D ? i : i - p.D] = a;
     }
 }
 
-template <int IO>
-hipError_t fwd_io(const QkNormParams& p, hipStream_t s) {
+template <int IO, bool NT>
+hipError_t fwd_nt(const QkNormParams& p, hipStream_t s) {
     const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
     const long long units = p.tokens * p.parts;
     const long long per = kThreads / lanes;
     const dim3 grid((unsigned)((units + per - 1) / per));
     switch (lanes) {
-    case 8: hipLaunchKernelGGL((qknorm_fwd_kernel<IO, 8>), grid, kThreads, 0, s, p); break;
-    case 16: hipLaunchKernelGGL((qknorm_fwd_kernel<IO, 16>), grid, kThreads, 0, s, p); break;
-    default: hipLaunchKernelGGL((qknorm_fwd_kernel<IO, 32>), grid, kThreads, 0, s, p); break;
+    case 8: hipLaunchKernelGGL((qknorm_fwd_kernel<IO, 8, NT>), grid, kThreads, 0, s, p); break;
+    case 16: hipLaunchKernelGGL((qknorm_fwd_kernel<IO, 16, NT>), grid, kThreads, 0, s, p); break;
+    default: hipLaunchKernelGGL((qknorm_fwd_kernel<IO, 32, NT>), grid, kThreads, 0, s, p); break;
     }
     return hipGetLastError();
 }
 
-template <int IO>
-hipError_t bwd_io(const QkNormParams& p, hipStream_t s) {
+template <int IO, bool NT>
+hipError_t bwd_nt(const QkNormParams& p, hipStream_t s) {
     const int lanes = p.D <= 64 ? 8 : p.D <= 128 ? 16 : 32;
     const dim3 grid(p.blocks);
     switch (lanes) {
-    case 8: hipLaunchKernelGGL((qknorm_bwd_kernel<IO, 8>), grid, kThreads, 0, s, p); break;
-    case 16: hipLaunchKernelGGL((qknorm_bwd_kernel<IO, 16>), grid, kThreads, 0, s, p); break;
-    default: hipLaunchKernelGGL((qknorm_bwd_kernel<IO, 32>), grid, kThreads, 0, s, p); break;
+    case 8: hipLaunchKernelGGL((qknorm_bwd_kernel<IO, 8, NT>), grid, kThreads, 0, s, p); break;
+    case 16: hipLaunchKernelGGL((qknorm_bwd_kernel<IO, 16, NT>), grid, kThreads, 0, s, p); break;
+    default: hipLaunchKernelGGL((qknorm_bwd_kernel<IO, 32, NT>), grid, kThreads, 0, s, p); break;
     }
     return hipGetLastError();
+}
+
+// Whether q and k are so large that little of them is still in a cache (256 MB
+// in all, which the pass fills four or five times over) when they are read
+// again.  Past the caches, 200 MB: forward 82 -> 76 us, 268 MB: backward 173 ->
+// 152 us; but 23 MB: backward 22.5 -> 25 us.
+bool streams(int io, const QkNormParams& p) {
+    return p.tokens * (p.Hq + p.Hk) * p.D * (io == IO_F32 ? 4 : 2) > (64ll << 20);
+}
+template <int IO>
+hipError_t fwd_io(const QkNormParams& p, hipStream_t s) {
+    return streams(IO, p) ? fwd_nt<IO, true>(p, s) : fwd_nt<IO, false>(p, s);
+}
+template <int IO>
+hipError_t bwd_io(const QkNormParams& p, hipStream_t s) {
+    return streams(IO, p) ? bwd_nt<IO, true>(p, s) : bwd_nt<IO, false>(p, s);
 }
 
 }  // namespace
 
 // Workgroups of the backward pass: they keep their weight-gradient sums to
-// the end, so enough to fill the 256 CUs and no more.
+// the end, so as many as run at once, three on each of the 256 CUs (their
+// registers allow no more; 1024 leave a second round of a third: 168 us where
+// 768 take 152).
 int qknorm_bwd_blocks(long long tokens) {
     const long long n = (tokens + 3) / 4;
-    return (int)(n < 1 ? 1 : n > 2048 ? 2048 : n);
+    return (int)(n < 1 ? 1 : n > 768 ? 768 : n);
 }
 
 hipError_t launch_qknorm_fwd(int io, const QkNormParams& p, hipStream_t s) {
@@ -404,7 +444,7 @@ hipError_t launch_qknorm_bwd(int io, const QkNormParams& p, hipStream_t s) {
     default: e = bwd_io<IO_BF16>(p, s); break;
     }
     if (e != hipSuccess || !p.part) return e;
-    hipLaunchKernelGGL(qknorm_dw_kernel, dim3((2 * p.D + 15) / 16), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(qknorm_dw_kernel, dim3(2 * p.D / 4), dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
