@@ -29,7 +29,7 @@ namespace {
 template <int IO, int R>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
     const int tiles = (p.Dv + 31) / 32;
-    long long id = blockIdx.x;
+    unsigned id = blockIdx.x;
     const int tile = (int)(id % tiles);
     id /= tiles;
     const int h = (int)(id % p.Hv);
@@ -75,9 +75,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepParams p) {
         r[8] += q[i] * k[i];
     }
 #pragma unroll
-    for (int j = 0; j < 9; ++j)
-#pragma unroll
-        for (int m = 8; m < 64; m <<= 1) r[j] += __shfl_xor(r[j], m);
+    for (int j = 0; j < 9; ++j) r[j] = sum_groups(r[j] + row_ror<8>(r[j]));
     __shared__ float sums[4][8][9];
     if (lane < 8)
 #pragma unroll
@@ -129,10 +127,12 @@ __device__ void invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
             float x[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                float s = i == c ? 1.f : 0.f;
+                // four sums side by side: each step waits for the one before
+                float s[4] = {i == c ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int l = 0; l < i; ++l) s -= a[o + i][o + l] * x[l];
-                x[i] = s;
+                for (int l = 0; l < i; ++l)
+                    s[(i - 1 - l) & 3] = fmaf(-a[o + i][o + l], x[l], s[(i - 1 - l) & 3]);
+                x[i] = (s[3] + s[2]) + (s[1] + s[0]);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) t[o + i][o + c] = x[i];
@@ -220,13 +220,13 @@ template <int IO, int DK>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     typedef PrepLds<IO, DK> L;
     constexpr int NT = L::NT, KB = DK / 32, NO = Io<IO>::NO;
-    const long long id = xcd_unit(blockIdx.x, p.slots * p.Hv);
-    if (id >= p.slots * p.Hv) return;
-    const long long slot = id / p.Hv;
-    const int h = (int)(id - slot * p.Hv);
-    const long long seq = seq_of(p, slot, 1);
-    const Span sp = span_of(p, seq);
-    const long long at = (slot - sp.slot0) * kChunk;
+    const unsigned units = (unsigned)p.slots * p.Hv, u = xcd_unit(blockIdx.x, units);
+    if (u >= units) return;
+    const unsigned slot = u / p.Hv;
+    const int h = (int)(u - slot * p.Hv);
+    const long long id = u;
+    const Span sp = span_of(p, seq_of(p, slot, 1));
+    const long long at = ((long long)slot - sp.slot0) * kChunk;
     if (at < 0 || at >= sp.len) return;      // a slot between two sequences
     const int n = (int)(sp.len - at < kChunk ? sp.len - at : kChunk);
     const long long tok = sp.t0 + at;
@@ -290,34 +290,33 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int col = tile_row(j, c);
-        float big_p = 0.f;
+    for (int j = 0; j < 4; ++j)
+        if (j < jtiles) {
+            const int col = tile_row(j, c);
+            float big_p = 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = tile_row(wave, 4 * g4 + r);
-            const float gam = row >= col ? expf((float)(G[row] - G[col])) : 0.f;
-            const float pv = row >= col ? p.scale * gam * qk[j][r] : 0.f;
-            A[row][col] = row > col ? bet[row] * gam * kk[j][r] : 0.f;
-            P[row][col] = pv;
-            big_p = fmaxf(big_p, fabsf(pv));
+            for (int r = 0; r < 4; ++r) {
+                const int row = tile_row(wave, 4 * g4 + r);
+                const float gam = row >= col ? decay(G[row] - G[col]) : 0.f;
+                const float pv = row >= col ? p.scale * gam * qk[j][r] : 0.f;
+                A[row][col] = row > col ? bet[row] * gam * kk[j][r] : 0.f;
+                P[row][col] = pv;
+                qk[j][r] = fabsf(pv);
+                big_p = fmaxf(big_p, qk[j][r]);
+            }
+            if (p.bpack) {
+                big_p = max_groups(big_p);
+                if (g4 == 0) atomicMax(&big[2][col], __float_as_uint(big_p));
+            }
         }
-        if (p.bpack && j < jtiles) {
-            big_p = max_groups(big_p);
-            if (g4 == 0) atomicMax(&big[2][col], __float_as_uint(big_p));
-        }
-    }
     // rows of P: largest over the wave's tiles, 16 lanes a row
     float back_row[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int row = tile_row(wave, 4 * g4 + r);
-        float a = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a = fmaxf(a, fabsf(P[row][tile_row(j, c)]));
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) a = fmaxf(a, __shfl_xor(a, m));
-        const Scale s = scale_to(a);
+        float a = fmaxf(qk[0][r], qk[1][r]);
+        if (jtiles == 4) a = fmaxf(a, fmaxf(qk[2][r], qk[3][r]));
+        const Scale s = scale_to(max16(a));
         back_row[r] = s.back;
         if (c == 0) rowp[row] = s.to;
     }
@@ -330,7 +329,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
         const Scale sq = IO == IO_F16 ? one : scale_to(__uint_as_float(big[1][lane]));
         const Scale sc = scale_to(__uint_as_float(big[2][lane]));
         colp[lane] = sc.to;
-        const float eg = expf((float)mine), ee = expf((float)(last - mine));
+        const float eg = decay(mine), ee = decay(last - mine);
         for (uint4* d : {pack, back})
             if (d) {
                 float* f = (float*)(d + kDec);
@@ -340,7 +339,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
                 f[kBeta + lane] = bet[lane];
                 f[kScaleK + lane] = sk.to;
                 f[kScaleQ + lane] = sq.to;
-                if (lane == 0) f[kDecayAll] = expf((float)last);
+                if (lane == 0) f[kDecayAll] = decay(last);
             }
         if (back) ((float*)(back + kDec))[kBackP + lane] = sc.back;
     }
@@ -360,8 +359,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
         float a = 0.f;
         for (int i = threadIdx.x; i < kChunk * kChunk; i += 256)
             a = fmaxf(a, fabsf(P[i >> 6][i & 63]));
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) a = fmaxf(a, __shfl_xor(a, m));
+        a = max_groups(max16(a));
         if (lane == 0) big[3][wave] = __float_as_uint(a);
     }
     __syncthreads();
@@ -418,17 +416,18 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
     extern __shared__ uint4 lds[];
     const int vcols = (p.Dv + kCols - 1) / kCols;
     const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
-    const long long units = p.segs * p.Hv * cols;
-    long long id = xcd_unit(blockIdx.x, units);
+    const unsigned units = (unsigned)p.segs * p.Hv * cols;
+    unsigned id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
     int cb = (int)(id % cols);
     id /= cols;
     const int h = (int)(id % p.Hv);
     const long long seg = id / p.Hv;
-    const long long seq = seq_of(p, seg, p.seg_chunks);
+    const long long seq = seq_of(p, (unsigned)seg, p.seg_chunks);
     const Span sp = span_of(p, seq);
     const int chunks = (sp.len + kChunk - 1) / kChunk;
-    const int sn = (int)(seg - seg_of(p, sp, seq));      // segment of the sequence
+    // segment of the sequence
+    const int sn = (int)((unsigned)seg - seg_of(p, sp, (unsigned)seq, p.seg_chunks));
     const long long first_ = (long long)sn * p.seg_chunks;
     if (sn != 0 && first_ >= chunks) return;             // no such segment
     const int first = (int)first_;
@@ -673,7 +672,7 @@ __global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
     constexpr int KB = DK / 32, ST = DK / 16;
     extern __shared__ uint4 lds[];
     const int cols = (p.Dv + 127) / 128;
-    long long id = blockIdx.x;
+    unsigned id = blockIdx.x;
     const int cb = (int)(id % cols);
     id /= cols;
     const int h = (int)(id % p.Hv);
@@ -687,7 +686,7 @@ __global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
     const int col = cb * 128 + wave * 16 + c;
     const bool cok = col < p.Dv;
     const long long state = p.Dk * (long long)p.Dv, square = p.Dk * (long long)p.Dk;
-    const long long seg0 = seg_of(p, sp, seq);
+    const long long seg0 = seg_of(p, sp, (unsigned)seq, p.seg_chunks);
     const uint32_t slane = (uint32_t)(8 * g * p.Dv + col) * 4;
     dfloat4 S[ST], R[ST];
     RowTiles<IO_F32, DK, 8> rm[L::kHalves];

@@ -36,8 +36,8 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
     constexpr int NA = Io<IO>::NA, KB = DK / 32, ST = DK / 16, kB = Io<IO>::kB, kCols = 16 * W;
     extern __shared__ uint4 lds[];
     const int cols = (p.Dv + kCols - 1) / kCols;
-    const long long units = p.nseq * p.Hv * cols;
-    long long id = xcd_unit(blockIdx.x, units);
+    const unsigned units = (unsigned)p.nseq * p.Hv * cols;
+    unsigned id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
     const int cb = (int)(id % cols);
     id /= cols;
@@ -270,12 +270,6 @@ struct GradsLds {
     static constexpr int kBytes = (kSlice > kTail ? kSlice : kTail) * 16;
 };
 
-// Sum over the four groups of 16 lanes.
-__device__ __forceinline__ float sum_groups(float x) {
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
-}
-
 // What a thread has in flight of a slice: eights of S0, D, U and dY, and eight
 // elements of its wave's token's dO and V in two pieces of four.
 template <int IO, int DK>
@@ -323,13 +317,11 @@ void delta_grads_kernel(DeltaGradParams gp) {
     __shared__ float bet[kChunk], colsum[4][kChunk], rowG[kChunk], rowB[kChunk];
     __shared__ float backK[kChunk], backQ[kChunk];
     __shared__ float red[4], red3[4], big[5];
-    const long long units = p.slots * p.Hk;
-    const long long id = xcd_unit(blockIdx.x, units);
+    const unsigned units = (unsigned)p.slots * p.Hk, id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
     const long long slot = id / p.Hk;
-    const int hk = (int)(id - slot * p.Hk);
-    const long long seq = seq_of(p, slot, 1);
-    const Span sp = span_of(p, seq);
+    const int hk = (int)(id - (unsigned)slot * p.Hk);
+    const Span sp = span_of(p, seq_of(p, (unsigned)slot, 1));
     const long long at = (slot - sp.slot0) * kChunk;
     if (at < 0 || at >= sp.len) return;
     const int n = (int)(sp.len - at < kChunk ? sp.len - at : kChunk);
@@ -406,11 +398,8 @@ void delta_grads_kernel(DeltaGradParams gp) {
                 a = fmaxf(a, m[i]);
                 if (wave == 3) o = fmaxf(o, m[padded + i]);
             }
-#pragma unroll
-            for (int j = 1; j < 64; j <<= 1) {
-                a = fmaxf(a, __shfl_xor(a, j));
-                o = fmaxf(o, __shfl_xor(o, j));
-            }
+            a = max_groups(max16(a));
+            o = max_groups(max16(o));
             if (lane == 0) {
                 big[wave] = a;
                 if (wave == 3) big[4] = o;
@@ -537,11 +526,10 @@ void delta_grads_kernel(DeltaGradParams gp) {
             rq.store(lds + L::kQ);
         }
         __syncthreads();
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) sd += __shfl_xor(sd, m);
+        sd = sum_groups(sum16(sd));
         yv *= sY.back;
         const double last = G[kChunk - 1], Gi = G[mine];
-        const float eg = expf((float)Gi), ee = expf((float)(last - Gi)), b = bet[mine];
+        const float eg = decay(Gi), ee = decay(last - Gi), b = bet[mine];
         const float bk = backK[mine], bq = backQ[mine];
         // sums over the elements of a head
         float s1 = 0.f, s2 = 0.f, s3 = 0.f;
@@ -605,7 +593,7 @@ void delta_grads_kernel(DeltaGradParams gp) {
                 for (int r = 0; r < 4; ++r) {
                     float w = 0.f, f = 0.f, t = 0.f;
                     if (j < jtiles && mine >= j0 + r) {
-                        const float gam = expf((float)(Gi - G[j0 + r]));
+                        const float gam = decay(Gi - G[j0 + r]);
                         const float kij = kk[j][r] * (bk * bj[r]);
                         w = gam * (fp * Dp[j][r]);
                         const float x = mine > j0 + r ? gam * (fy * Dy[j][r]) : 0.f;
@@ -623,8 +611,7 @@ void delta_grads_kernel(DeltaGradParams gp) {
                 // sums over the wave's tokens
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-#pragma unroll
-                    for (int m = 1; m < 16; m <<= 1) cs[r] += __shfl_xor(cs[r], m);
+                    cs[r] = sum16(cs[r]);
                     if (c == 0) colsum[wave][j0 + r] = cs[r];
                 }
             }
@@ -636,8 +623,7 @@ void delta_grads_kernel(DeltaGradParams gp) {
             rowB[mine] = rb;
         }
         // the chunk's last decay
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) s3 += __shfl_xor(s3, m);
+        s3 = sum16(s3);
         if (lane == 0) {
             red[wave] = sd;
             red3[wave] = s3;
@@ -648,7 +634,7 @@ void delta_grads_kernel(DeltaGradParams gp) {
                                              colsum[3][lane]);
             if (lane == 63)
                 x += (red3[0] + red3[1] + red3[2] + red3[3]) +
-                     expf((float)last) * (red[0] + red[1] + red[2] + red[3]);
+                     decay(last) * (red[0] + red[1] + red[2] + red[3]);
             // sums from the end
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {

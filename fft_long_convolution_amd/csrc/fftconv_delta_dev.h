@@ -82,26 +82,25 @@ __device__ __forceinline__ Span span_of(const DeltaParams& p, long long i) {
     }
     return s;
 }
+// Units of work, slots, segments and tokens of a row are below 2^31, so their
+// divisions are of 32 bits.
 // index of the first segment (of L chunks; L = 1: chunk) of a sequence
-__device__ __forceinline__ long long seg_first(long long t0, long long i, long long nch, long long L,
-                                               bool packed) {
-    return packed ? t0 / (kChunk * L) + i : i * (nch ? (nch + L - 1) / L : 1);
-}
-__device__ __forceinline__ long long seg_of(const DeltaParams& p, const Span& s, long long i) {
-    return seg_first(s.t0, i, p.nch, p.seg_chunks, p.cu != nullptr);
+__device__ __forceinline__ unsigned seg_of(const DeltaParams& p, const Span& s, unsigned i,
+                                           unsigned L) {
+    const unsigned nch = (unsigned)p.nch;
+    return p.cu ? (unsigned)s.t0 / kChunk / L + i : i * (nch ? (nch + L - 1) / L : 1);
 }
 // the sequence whose segment (of L chunks) number `seg` is; its span may end
 // before the segment
-__device__ __forceinline__ long long seq_of(const DeltaParams& p, long long seg, long long L) {
-    if (!p.cu) {
-        return seg / (p.nch ? (p.nch + L - 1) / L : 1);
-    }
-    long long lo = 0, hi = p.nseq - 1;
+__device__ __forceinline__ unsigned seq_of(const DeltaParams& p, unsigned seg, unsigned L) {
+    const unsigned nch = (unsigned)p.nch;
+    if (!p.cu) return seg / (nch ? (nch + L - 1) / L : 1);
+    unsigned lo = 0, hi = (unsigned)p.nseq - 1;
     while (lo < hi) {
-        const long long mid = (lo + hi + 1) / 2;
+        const unsigned mid = lo + (hi - lo + 1) / 2;
         long long a = p.cu[mid];
         a = a < 0 ? 0 : a > p.T ? p.T : a;
-        if (a / (kChunk * L) + mid <= seg) lo = mid; else hi = mid - 1;
+        if ((unsigned)a / kChunk / L + mid <= seg) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
@@ -275,6 +274,33 @@ __device__ __forceinline__ Scale scale_to(float largest) {
     e = e < 28 ? 28 : e > 240 ? 240 : e;
     return {__uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23),
             __uint_as_float((uint32_t)(e - 14) << 23)};
+}
+// Reductions in the vector unit; a shuffle through LDS would take some 100
+// cycles a step.  All-reduce over the 16 lanes of a group, by rotations:
+template <int N>
+__device__ __forceinline__ float row_ror(float a) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(a), 0x120 + N, 15, 15, true));
+}
+__device__ __forceinline__ float max16(float a) {
+    a = fmaxf(a, row_ror<8>(a));
+    a = fmaxf(a, row_ror<4>(a));
+    a = fmaxf(a, row_ror<2>(a));
+    return fmaxf(a, row_ror<1>(a));
+}
+__device__ __forceinline__ float sum16(float a) {
+    a += row_ror<8>(a);
+    a += row_ror<4>(a);
+    a += row_ror<2>(a);
+    return a + row_ror<1>(a);
+}
+// over the four groups at the lane's place
+__device__ __forceinline__ float sum_groups(float a) {
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(a), false,
+                                                    false);
+    a = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(a), false,
+                                                    false);
+    return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
 // the larger value of the lane and of the other groups of 16 at its place
 __device__ __forceinline__ float max_groups(float a) {
@@ -658,27 +684,40 @@ enum Factor {
 
 constexpr int kLd = 68;   // floats between rows of the 64 x 64 matrices in LDS
 
-// Sum of the log decays up to the lane's token.  Sums are fp64, so
-// e^(G_i - G_j) is right to fp32 however much the chunk has decayed before;
+// x of the lane that is so many places before in the group of 16, or 0
+template <int DPP>
+__device__ __forceinline__ double shifted(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)u, DPP, 15, 15, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(u >> 32), DPP, 15, 15, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum of the log decays up to the lane's token, in units of log 2 (decay()
+// makes factors of them).  Sums are fp64, so e^(G_i - G_j) is right to fp32 however much the chunk has decayed before;
 // decays below -1e4 count as -1e4 (their factor is 0 in fp32 either way), so
 // a reset (g = -inf) does not meet itself as inf - inf.  NaN stays NaN.
 __device__ __forceinline__ double decay_sum(float g) {
-    const int lane = threadIdx.x & 63;
     double s = g < -1e4f ? -1e4f : g;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const double o = __shfl_up(s, m);
-        if (lane >= m) s += o;
-    }
-    return s;
+    // within each group of 16, then the groups before
+    s += shifted<0x111>(s);
+    s += shifted<0x112>(s);
+    s += shifted<0x114>(s);
+    s += shifted<0x118>(s);
+    const int lane = threadIdx.x & 63;
+    const double a = __shfl(s, 15), b = __shfl(s, 31), c = __shfl(s, 47);
+    if (lane >= 16) s += a;
+    if (lane >= 32) s += b;
+    if (lane >= 48) s += c;
+    return s * 1.4426950408889634074;
 }
+__device__ __forceinline__ float decay(double g) { return __builtin_amdgcn_exp2f((float)g); }
 
 // Workgroups are dealt round robin over the 8 XCDs; this gives each XCD a
 // run of consecutive units, so the units that share a head's rows share an
 // L2.  Returns n where there is no unit.
-__device__ __forceinline__ long long xcd_unit(long long block, long long n) {
-    const long long per = (n + 7) / 8;
-    const long long u = (block & 7) * per + (block >> 3);
+__device__ __forceinline__ unsigned xcd_unit(unsigned block, unsigned n) {
+    const unsigned per = (n + 7) / 8;
+    const unsigned u = (block & 7) * per + (block >> 3);
     return (block >> 3) < per && u < n ? u : n;
 }
 inline long long xcd_blocks(long long n) { return (n + 7) / 8 * 8; }
