@@ -112,17 +112,17 @@ __device__ __forceinline__ dfloat4 mma_f32(float a, float b, dfloat4 c) {
 // Turns the strict lower triangle a (64 x 64 in LDS) into t = (I + a)^-1 by
 // halves: 16 x 16 diagonal blocks by forward substitution (a lane a column),
 // then [T11 0; -T22 A21 T11 T22] for 32 and 64, on the fp32 matrix cores.
-// The four waves of the workgroup call it together.
-__device__ void invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
+// Above the diagonal t is 0 within 32 x 32 blocks and not written beyond.  The
+// four waves of the workgroup call it together; returns the largest magnitude
+// of what the lane made.
+__device__ float invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
+    float big = 1.f;                         // the diagonal
     {
-        // zero the blocks above the diagonal, invert those on it
         const int o = 16 * wave;
-        for (int i = lane; i < 16 * 64; i += 64) {
-            const int row = o + (i >> 6), col = i & 63;
-            if (col >= o + 16) t[row][col] = 0.f;
-        }
+        if (!(wave & 1))                     // the block to the right
+            *(float4*)&t[o + (lane >> 2)][o + 16 + 4 * (lane & 3)] = make_float4(0, 0, 0, 0);
         if (lane < 16) {
             float x[16];
 #pragma unroll
@@ -135,7 +135,10 @@ __device__ void invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
                 x[i] = (s[3] + s[2]) + (s[1] + s[0]);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) t[o + i][o + c] = x[i];
+            for (int i = 0; i < 16; ++i) {
+                t[o + i][o + c] = x[i];
+                big = fmaxf(big, fabsf(x[i]));
+            }
         }
     }
     __syncthreads();
@@ -149,7 +152,10 @@ __device__ void invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) r = mma_f32(t[o + 16 + c][o + 16 + 4 * g + s], m[s], r);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) t[o + 16 + 4 * g + s][o + c] = -r[s];
+        for (int s = 0; s < 4; ++s) {
+            t[o + 16 + 4 * g + s][o + c] = -r[s];
+            big = fmaxf(big, fabsf(r[s]));
+        }
     }
     __syncthreads();
     {
@@ -166,9 +172,12 @@ __device__ void invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
             for (int s = 0; s < 4; ++s)
                 r = mma_f32(t[row + c][32 + 16 * i + 4 * g + s], m[i][s], r);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) t[row + 4 * g + s][col + c] = -r[s];
+        for (int s = 0; s < 4; ++s) {
+            t[row + 4 * g + s][col + c] = -r[s];
+            big = fmaxf(big, fabsf(r[s]));
+        }
     }
-    __syncthreads();
+    return big;
 }
 
 // Writes a lower triangle from LDS as N terms in operand order: tile (m, kb),
@@ -353,20 +362,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
         store_tri_transposed(P, colp, back + kPm);
     }
     __syncthreads();
-    invert_unit_lower(A, P);
     // one scale for T
-    {
-        float a = 0.f;
-        for (int i = threadIdx.x; i < kChunk * kChunk; i += 256)
-            a = fmaxf(a, fabsf(P[i >> 6][i & 63]));
-        a = max_groups(max16(a));
-        if (lane == 0) big[3][wave] = __float_as_uint(a);
-    }
+    const float big_t = max_groups(max16(invert_unit_lower(A, P)));
+    if (lane == 0) big[3][wave] = __float_as_uint(big_t);
     __syncthreads();
     {
-        float a = 0.f;
+        float a = __uint_as_float(big[3][0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a = fmaxf(a, __uint_as_float(big[3][i]));
+        for (int i = 1; i < 4; ++i) a = fmaxf(a, __uint_as_float(big[3][i]));
         const Scale s = scale_to(a);
         if (threadIdx.x < 64) rowp[threadIdx.x] = s.to;
         if (threadIdx.x == 0) {
