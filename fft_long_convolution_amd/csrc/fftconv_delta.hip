@@ -409,9 +409,11 @@ enum ScanMode { kEffect, kOutputs, kSaving };
 // accumulators as its B operand, so the chain of a chunk has no exchange and
 // no barrier of its own.  The W waves of a workgroup share the operands that
 // do not depend on the state (K, Q, T, P) through LDS, K^T being K read
-// transposed.
+// transposed; four further waves bring the next chunk's, in step by a barrier a
+// chunk.  The chain is latency: a step's vector work, its products and their
+// operands wait for one another, and what else a wave did would add to it.
 template <int IO, int DK, int W, int MODE>
-__global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
+__global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaParams p) {
     constexpr bool FULL = MODE != kEffect;
     typedef ScanLds<IO, DK, FULL> L;
     constexpr int NA = Io<IO>::NA, NO = Io<IO>::NO, KB = DK / 32, ST = DK / 16;
@@ -472,40 +474,56 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
     const uint4* pack = p.pack + (sp.slot0 * p.Hv + h) * pack_uint4<IO>();
     const long long pack_step = (long long)p.Hv * pack_uint4<IO>();
 
-    RowTiles<IO, DK, W> rk, rq;
-    Block<L::kPackU4 / 64, W> rp;
+    if (__builtin_amdgcn_readfirstlane(wave) >= W) {
+        RowTiles<IO, DK, kLoaders> rk, rq;
+        Block<L::kPackU4 / 64, kLoaders> rp;
+        const auto load = [&](int ch) __attribute__((always_inline)) {
+            const int n = sp.len - ch * kChunk;
+            const uint4* next_pack = pack + ch * pack_step;
+            const float* f = (const float*)(next_pack + kDec);
+            rk.load(tk, ch * kChunk, n, p.Dk, f + kScaleK);
+            if (FULL) rq.load(tq, ch * kChunk, n, p.Dk, f + kScaleQ);
+            rp.load(next_pack);
+        };
+        const auto store = [&](uint4* d) __attribute__((always_inline)) {
+            rk.store(d + L::kK);
+            if (FULL) rq.store(d + L::kQ);
+            rp.store(d + L::kPack);
+        };
+        if (first < last) {
+            load(first);
+            store(lds);
+        }
+        __syncthreads();
+        for (int ch = first, buf = 0; ch < last; ++ch) {
+            load(ch + 1 < last ? ch + 1 : ch);
+            if (L::kBufs == 2) {
+                buf ^= 1;
+                store(lds + buf * L::kSize);
+                __syncthreads();
+            } else {
+                __syncthreads();
+                store(lds);
+                __syncthreads();
+            }
+        }
+        return;
+    }
+
     dfloat4 v[4];
-    const auto load = [&](int ch) __attribute__((always_inline)) {
-        const int n = sp.len - ch * kChunk;
-        const uint4* next_pack = pack + ch * pack_step;
-        const float* f = (const float*)(next_pack + kDec);
-        rk.load(tk, ch * kChunk, n, p.Dk, f + kScaleK);
-        if (FULL) rq.load(tq, ch * kChunk, n, p.Dk, f + kScaleQ);
-        rp.load(next_pack);
-    };
-    const auto store = [&](uint4* d) __attribute__((always_inline)) {
-        rk.store(d + L::kK);
-        if (FULL) rq.store(d + L::kQ);
-        rp.store(d + L::kPack);
-    };
     const auto load_v = [&](int ch) __attribute__((always_inline)) {
         if (!matrix) load_column<IO>(tv, ch * kChunk, vlane, sp.len - ch * kChunk, v);
     };
 #pragma unroll
     for (int m = 0; m < 4; ++m) v[m] = dfloat4{0, 0, 0, 0};
-    if (first < last) {
-        load(first);
-        load_v(first);
-        store(lds);
-    }
+    if (first < last) load_v(first);
     __syncthreads();
-    uint4* now = lds;
-    uint4* next = lds + (L::kBufs == 2 ? L::kSize : 0);
+    int buf = 0;
     for (int ch = first; ch < last; ++ch) {
         const long long ci = (sp.slot0 + ch) * p.Hv + h;
         const int n = sp.len - ch * kChunk;
         const int ahead = ch + 1 < last ? ch + 1 : ch;
-        load(ahead);
+        const uint4* now = lds + buf * L::kSize;
         const float* fac = (const float*)(now + L::kPack + kDec);
         const uint4* tri = now + L::kPack;
         const float big_s = max_column(S);
@@ -613,7 +631,6 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
             U[m][3] *= e.w;
         }
         const float ec = fac[kDecayAll];
-        if (L::kBufs == 2) store(next);
         // S = e^Gc S + K^T U
         const Scale se = scale_to(max_column(U));
         uint4 ut[2][2];
@@ -641,14 +658,8 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaParams p) {
                     S[t0 + t][r] = fmaf(se.back, a[t][r], ec * S[t0 + t][r]);
         }
         __syncthreads();
-        if (L::kBufs == 2) {
-            uint4* x = now;
-            now = next;
-            next = x;
-        } else {
-            store(lds);
-            __syncthreads();
-        }
+        if (L::kBufs == 2) buf ^= 1;
+        else __syncthreads();
     }
     if (!cok) return;
     float* d = nullptr;
@@ -770,7 +781,7 @@ hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
                      (MODE == kEffect ? (p.Dk + width - 1) / width : 0);
     const long long units = p.segs * p.Hv * cols;
     hipLaunchKernelGGL((delta_scan_kernel<IO, DK, W, MODE>), dim3((unsigned)xcd_blocks(units)),
-                       dim3(64 * W), bytes, s, p);
+                       dim3(64 * (W + kLoaders)), bytes, s, p);
     return hipGetLastError();
 }
 
@@ -793,7 +804,11 @@ hipError_t scan_w(const DeltaParams& p, hipStream_t s) {
 }
 template <int IO, int DK>
 hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
-    return p.Dv <= 64 ? scan_w<IO, DK, 4>(p, s) : scan_w<IO, DK, 8>(p, s);
+    // Eight waves for the chain take 128 columns at 6.2 us a chunk, four take 64 at
+    // 3.4: four while that leaves CUs idle otherwise (1 x 77 x 6 x 128 bf16:
+    // 12.7 us, with eight 15.9; 64 x 1024 x 6 x 128: 225 and 199).
+    return p.segs * p.Hv * ((p.Dv + 127) / 128) < 256 || p.Dv <= 64 ? scan_w<IO, DK, 4>(p, s)
+                                                                    : scan_w<IO, DK, 8>(p, s);
 }
 
 template <int IO, int DK>

@@ -30,7 +30,7 @@ struct RscanLds {
 // The mirror of the forward walk: a wave owns 16 columns of D and goes
 // through K D, T^T dU and the two transposed products without an exchange.
 template <int IO, int DK, int W>
-__global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp) {
+__global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
     const DeltaParams& p = gp.f;
     constexpr int NA = Io<IO>::NA, KB = DK / 32, ST = DK / 16, kB = Io<IO>::kB, kCols = 16 * W;
@@ -70,44 +70,59 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
     const uint32_t olane = (uint32_t)(8 * g) * (uint32_t)to.bytes + colv * kB;
     const uint4* pack = p.bpack + (sp.slot0 * p.Hv + h) * kBackPack;
     const long long pack_step = (long long)p.Hv * kBackPack;
-    RowTiles<IO, DK, W> rk, rq;
-    Block<kBackPack / 64, W> rp;
-    const auto load = [&](int ch) __attribute__((always_inline)) {
-        const int n = sp.len - ch * kChunk;
-        const uint4* next_pack = pack + ch * pack_step;
-        const float* f = (const float*)(next_pack + kDec);
-        rk.load(tk, ch * kChunk, n, p.Dk, f + kScaleK);
-        rq.load(tq, ch * kChunk, n, p.Dk, f + kScaleQ);
-        rp.load(next_pack);
-    };
-    const auto store = [&](uint4* d) __attribute__((always_inline)) {
-        rk.store(d + L::kK);
-        rq.store(d + L::kQ);
-        rp.store(d + L::kPack);
-    };
+    if (__builtin_amdgcn_readfirstlane(wave) >= W) {
+        RowTiles<IO, DK, kLoaders> rk, rq;
+        Block<kBackPack / 64, kLoaders> rp;
+        const auto load = [&](int ch) __attribute__((always_inline)) {
+            const int n = sp.len - ch * kChunk;
+            const uint4* next_pack = pack + ch * pack_step;
+            const float* f = (const float*)(next_pack + kDec);
+            rk.load(tk, ch * kChunk, n, p.Dk, f + kScaleK);
+            rq.load(tq, ch * kChunk, n, p.Dk, f + kScaleQ);
+            rp.load(next_pack);
+        };
+        const auto store = [&](uint4* d) __attribute__((always_inline)) {
+            rk.store(d + L::kK);
+            rq.store(d + L::kQ);
+            rp.store(d + L::kPack);
+        };
+        if (chunks > 0) {
+            load(chunks - 1);
+            store(lds);
+        }
+        __syncthreads();
+        for (int ch = chunks - 1, buf = 0; ch >= 0; --ch) {
+            load(ch > 0 ? ch - 1 : 0);
+            if (L::kBufs == 2) {
+                buf ^= 1;
+                store(lds + buf * L::kSize);
+                __syncthreads();
+            } else {
+                __syncthreads();
+                store(lds);
+                __syncthreads();
+            }
+        }
+        return;
+    }
     // dO of the next chunk.  The tokens from n on that repeat the last one
     // meet columns of P^T and rows of Q that are 0.
     dfloat4 dN[4];
     const auto load_do = [&](int ch) __attribute__((always_inline)) {
         load_column<IO>(to, ch * kChunk, olane, sp.len - ch * kChunk, dN);
     };
-    if (chunks > 0) {
-        load(chunks - 1);
-        load_do(chunks - 1);
-        store(lds);
-    }
+    if (chunks > 0) load_do(chunks - 1);
     __syncthreads();
-    uint4* now = lds;
-    uint4* next = lds + (L::kBufs == 2 ? L::kSize : 0);
+    int buf = 0;
     for (int ch = chunks - 1; ch >= 0; --ch) {
         const long long ci = (sp.slot0 + ch) * p.Hv + h;
+        const uint4* now = lds + buf * L::kSize;
         const float* fac = (const float*)(now + L::kPack + kDec);
         const uint4* tri = now + L::kPack;
         dfloat4 dO[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dO[m] = dN[m];
         const int ahead = ch > 0 ? ch - 1 : 0;
-        load(ahead);
         const float big_d = max_column(D);
         if (cok) save_columns<KB>(gp.dstates, ci, p.Dv, col, D, big_d);
         // dU = e^(Gc-G) o K D + P^T dO
@@ -202,7 +217,6 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
             }
         }
         const float ec = fac[kDecayAll];
-        if (L::kBufs == 2) store(next);
         load_do(ahead);
         const Scale sy = scale_to(max_column(dY)), sq = scale_to(max_column(dO));
         uint4 yt[2][2], ot[2][2];
@@ -237,14 +251,8 @@ __global__ __launch_bounds__(64 * W) void delta_rscan_kernel(DeltaGradParams gp)
                         fmaf(sy.back, a[t][r], fmaf(sq.back, b[t][r], ec * D[t0 + t][r]));
         }
         __syncthreads();
-        if (L::kBufs == 2) {
-            uint4* x = now;
-            now = next;
-            next = x;
-        } else {
-            store(lds);
-            __syncthreads();
-        }
+        if (L::kBufs == 2) buf ^= 1;
+        else __syncthreads();
     }
     if (gp.dinit && cok)
         store_state<ST>((char*)(gp.dinit + (seq * p.Hv + h) * state), p.Dv * 4,
@@ -716,12 +724,14 @@ hipError_t rscan_w(const DeltaGradParams& p, hipStream_t s) {
     if (e != hipSuccess) return e;
     const long long units = p.f.nseq * p.f.Hv * ((p.f.Dv + 16 * W - 1) / (16 * W));
     hipLaunchKernelGGL((delta_rscan_kernel<IO, DK, W>), dim3((unsigned)xcd_blocks(units)),
-                       dim3(64 * W), bytes, s, p);
+                       dim3(64 * (W + kLoaders)), bytes, s, p);
     return hipGetLastError();
 }
 template <int IO, int DK>
 hipError_t rscan_io(const DeltaGradParams& p, hipStream_t s) {
-    return p.f.Dv <= 64 ? rscan_w<IO, DK, 4>(p, s) : rscan_w<IO, DK, 8>(p, s);
+    // as the forward walk
+    return p.f.nseq * p.f.Hv * ((p.f.Dv + 127) / 128) < 256 || p.f.Dv <= 64
+               ? rscan_w<IO, DK, 4>(p, s) : rscan_w<IO, DK, 8>(p, s);
 }
 
 template <int IO, int DK, bool GROUP>

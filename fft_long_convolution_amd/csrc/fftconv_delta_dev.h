@@ -390,7 +390,8 @@ __device__ __forceinline__ Tokens tokens_of(const void* p, long long first, long
 // as they might write what it reads, and each chunk waited for its own
 // prefetch.)
 
-// The A operands of 64 tokens x DK of a head, by W waves.  In LDS, tile
+// The A operands of 64 tokens x DK of a head, by W waves (those whose number
+// modulo W is 0 .. W - 1).  In LDS, tile
 // (m, kb), place 16 g + (c ^ 4 g) holds [token tile_row(m, c)][32 kb + 8 g +
 // i], i < 8; the exclusive or spreads the four groups over the banks for the
 // transposed reads.  Tokens from n on and elements from Dk on are 0.
@@ -403,7 +404,7 @@ struct RowTiles {
     du4 r[kMine][kWords];
     float s[kMine];
     __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int Dk) {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int wave = (threadIdx.x >> 6) & (W - 1), lane = threadIdx.x & 63;
         const int g = lane >> 4, c = (lane & 15) ^ (4 * g);
         const char* p = x.at(token);
         const uint32_t stride = (uint32_t)x.bytes;
@@ -436,7 +437,7 @@ struct RowTiles {
                                          const float* scales) {
         load(x, token, n, Dk);
         if (IO == IO_F16) return;
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int wave = (threadIdx.x >> 6) & (W - 1), lane = threadIdx.x & 63;
         const int c = (lane & 15) ^ (4 * (lane >> 4));
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
@@ -447,7 +448,7 @@ struct RowTiles {
     // as f16 terms, Io<IO>::NA of them
     __device__ __forceinline__ void store(uint4* dst) const {
         constexpr int NA = Io<IO>::NA;
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int wave = (threadIdx.x >> 6) & (W - 1), lane = threadIdx.x & 63;
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
             const int at = (W * j + wave) * 64 + lane;
@@ -466,7 +467,7 @@ struct RowTiles {
     }
     // as they are, fp32 in three bf16 terms
     __device__ __forceinline__ void store_plain(uint4* dst) const {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int wave = (threadIdx.x >> 6) & (W - 1), lane = threadIdx.x & 63;
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
             const int at = (W * j + wave) * 64 + lane;
@@ -486,7 +487,7 @@ struct RowTiles {
     // largest magnitudes of the rows, joined into `largest` in LDS (the bits
     // of a magnitude grow with it)
     __device__ __forceinline__ void max_rows(uint32_t* largest) const {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int wave = (threadIdx.x >> 6) & (W - 1), lane = threadIdx.x & 63;
         const int c = (lane & 15) ^ (4 * (lane >> 4));
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
@@ -511,7 +512,7 @@ struct Block {
     static constexpr int kMine = (N + W - 1) / W;
     du4 r[kMine];
     static __device__ __forceinline__ int place(int j) {
-        const int i = W * j + (threadIdx.x >> 6);
+        const int i = W * j + ((threadIdx.x >> 6) & (W - 1));
         return (i < N ? i : N - 1) * 64 + (threadIdx.x & 63);
     }
     __device__ __forceinline__ void load(const uint4* src) {
@@ -682,6 +683,7 @@ enum Factor {
     kBackT = 449,     // inverse scale of T
 };
 
+constexpr int kLoaders = 4;   // waves of a walk that bring the operands
 constexpr int kLd = 68;   // floats between rows of the 64 x 64 matrices in LDS
 
 // x of the lane that is so many places before in the group of 16, or 0
