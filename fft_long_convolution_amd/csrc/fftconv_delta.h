@@ -72,6 +72,27 @@ constexpr int kTriTiles = 6;               // 16 x 32 tiles of a 64 x 64 triangl
 int delta_pack_uint4(int io);              // of the forward pack
 int delta_back_pack_uint4();               // of its transposes
 
+// Time of a walk for each chunk of its longest chain, in us, by the number of
+// workgroups that take 64 or 128 columns (four or eight waves for the chain),
+// measured at heads of 128 in bf16: alone on a card and with all 256 CUs taken.
+// A workgroup has a CU to itself, so more than 256 run in rounds; packed
+// sequences differ in length, and about half of a further round is hidden behind
+// the longest of them (46 sequences, 8 heads of 64, f16: 82 us with four waves
+// and 368 workgroups, 97 with eight and 184).  *waves: the better of four and
+// eight.
+inline double walk_us(double units64, double units128, bool effect, bool packed, int* waves) {
+    const double cus = 256.0;
+    const auto time = [&](double units, double alone, double full) {
+        const double load = units / cus;
+        const double rounds = load <= 1 ? 1 : packed ? 0.5 + 0.5 * load : (double)(long long)(load + 0.999999);
+        return rounds * (alone + (full - alone) * (load < 1 ? load : 1));
+    };
+    const double four = effect ? time(units64, 2.5, 3.25) : time(units64, 3.4, 4.7);
+    const double eight = effect ? time(units128, 3.6, 4.7) : time(units128, 4.7, 6.2);
+    if (waves) *waves = four <= eight ? 4 : 8;
+    return four <= eight ? four : eight;
+}
+
 struct DeltaParams {
     int Hk, Hv, group, Dk, Dv;
     float scale;

@@ -785,10 +785,20 @@ hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int IO, int DK, int W>
-hipError_t scan_w(const DeltaParams& p, hipStream_t s) {
+template <int IO, int DK, int MODE>
+hipError_t scan_mode(const DeltaParams& p, hipStream_t s) {
+    const auto units = [&](int width) {
+        return (double)p.segs * p.Hv *
+               ((p.Dv + width - 1) / width + (MODE == kEffect ? (p.Dk + width - 1) / width : 0));
+    };
+    int waves;
+    walk_us(units(64), units(128), MODE == kEffect, p.cu != nullptr, &waves);
+    return waves == 4 ? scan_launch<IO, DK, 4, MODE>(p, s) : scan_launch<IO, DK, 8, MODE>(p, s);
+}
+template <int IO, int DK>
+hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
     if (p.seg_m) {
-        hipError_t e = scan_launch<IO, DK, W, kEffect>(p, s);
+        hipError_t e = scan_mode<IO, DK, kEffect>(p, s);
         if (e != hipSuccess) return e;
         const int lds = JoinLds<DK>::kBytes;
         e = hipFuncSetAttribute((const void*)delta_join_kernel<DK>,
@@ -799,16 +809,7 @@ hipError_t scan_w(const DeltaParams& p, hipStream_t s) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return p.states ? scan_launch<IO, DK, W, kSaving>(p, s)
-                    : scan_launch<IO, DK, W, kOutputs>(p, s);
-}
-template <int IO, int DK>
-hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
-    // Eight waves for the chain take 128 columns at 6.2 us a chunk, four take 64 at
-    // 3.4: four while that leaves CUs idle otherwise (1 x 77 x 6 x 128 bf16:
-    // 12.7 us, with eight 15.9; 64 x 1024 x 6 x 128: 225 and 199).
-    return p.segs * p.Hv * ((p.Dv + 127) / 128) < 256 || p.Dv <= 64 ? scan_w<IO, DK, 4>(p, s)
-                                                                    : scan_w<IO, DK, 8>(p, s);
+    return p.states ? scan_mode<IO, DK, kSaving>(p, s) : scan_mode<IO, DK, kOutputs>(p, s);
 }
 
 template <int IO, int DK>

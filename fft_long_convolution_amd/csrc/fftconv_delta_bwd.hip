@@ -729,9 +729,11 @@ hipError_t rscan_w(const DeltaGradParams& p, hipStream_t s) {
 }
 template <int IO, int DK>
 hipError_t rscan_io(const DeltaGradParams& p, hipStream_t s) {
-    // as the forward walk
-    return p.f.nseq * p.f.Hv * ((p.f.Dv + 127) / 128) < 256 || p.f.Dv <= 64
-               ? rscan_w<IO, DK, 4>(p, s) : rscan_w<IO, DK, 8>(p, s);
+    const double heads = (double)p.f.nseq * p.f.Hv;
+    int waves;
+    walk_us(heads * ((p.f.Dv + 63) / 64), heads * ((p.f.Dv + 127) / 128), false,
+            p.f.cu != nullptr, &waves);
+    return waves == 4 ? rscan_w<IO, DK, 4>(p, s) : rscan_w<IO, DK, 8>(p, s);
 }
 
 template <int IO, int DK, bool GROUP>

@@ -195,19 +195,40 @@ size_t delta_slots(const fftconv_delta_desc* d) {
     return d->sequences ? per + d->sequences : d->B * per;
 }
 
-// Chunks of a segment: sequences are cut where there are too few heads and
-// columns to give every CU two workgroups, into segments of at least
-// kSegChunks, so that the cut (each segment's effect on the state, some 1.4
-// times the walk itself, and the join) costs less than it wins.
-constexpr size_t kSegChunks = 16, kSegUnits = 512;
+// Chunks of a segment.  A sequence is a chain of chunks; where the heads and
+// columns leave CUs idle, sequences are cut into segments that are walked side
+// by side: once for their effects on the state, and, after a join of some 7 us a
+// segment, for the outputs.  The number of segments is the one of least time
+// under walk_us(); one where that is least.  (4 x 32768 x 4 x 128 bf16: 16
+// segments, 0.70 ms, uncut 2.1; 1 x 4096 x 8 x 128: 6, 0.12 ms, uncut 0.26;
+// 16 x 8192 x 6 x 128: uncut 0.65, in three 0.91.)
 size_t delta_seg_chunks(const fftconv_delta_desc* d) {
     const size_t nch = (d->T + kChunk - 1) / kChunk;
-    const size_t cols = (d->Dv + 63) / 64, rows = d->sequences ? d->sequences : d->B;
+    const size_t rows = d->sequences ? d->sequences : d->B;
+    const size_t chunks = d->sequences ? nch : d->B * nch;
     const size_t whole = nch + 1;           // one segment a sequence
-    if (rows * d->Hv * cols * 2 >= kSegUnits) return whole;
-    size_t per = (delta_slots(d) * d->Hv * cols + kSegUnits - 1) / kSegUnits;
-    if (per < kSegChunks) per = kSegChunks;
-    return nch > 2 * per ? per : whole;
+    const size_t L = rows ? chunks / rows : 0;      // of a sequence, on average
+    if (L < 8) return whole;
+    const bool packed = d->sequences != 0;
+    const double heads = (double)rows * d->Hv;
+    const size_t v64 = (d->Dv + 63) / 64, v128 = (d->Dv + 127) / 128;
+    const size_t k64 = (d->Dk + 63) / 64, k128 = (d->Dk + 127) / 128;
+    double best = L * walk_us(heads * v64, heads * v128, false, packed, nullptr);
+    size_t per = whole;
+    for (size_t n = 3; n <= 64 && n * 2 <= L; ++n) {
+        const size_t p = (L + n - 1) / n;
+        if ((L + p - 1) / p != n) continue;
+        const double full = walk_us(heads * n * v64, heads * n * v128, false, packed, nullptr);
+        const double effect = walk_us(heads * ((n - 1) * v64 + (n - 2) * k64),
+                                      heads * ((n - 1) * v128 + (n - 2) * k128), true, packed,
+                                      nullptr);
+        const double t = p * (full + effect) + 7.0 * (n - 2) + 12.0;
+        if (t < best) {
+            best = t;
+            per = p;
+        }
+    }
+    return per;
 }
 size_t delta_segs(const fftconv_delta_desc* d, size_t per) {
     const size_t nch = (d->T + kChunk - 1) / kChunk;
