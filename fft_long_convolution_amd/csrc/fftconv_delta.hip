@@ -434,7 +434,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
     // segment of the sequence
     const int sn = (int)((unsigned)seg - seg_of(p, sp, (unsigned)seq, p.seg_chunks));
     const long long first_ = (long long)sn * p.seg_chunks;
-    if (sn != 0 && first_ >= chunks) return;             // no such segment
+    if (sn < 0 || (sn != 0 && first_ >= chunks)) return;   // no such segment
     const int first = (int)first_;
     const int last = chunks - first > p.seg_chunks ? first + p.seg_chunks : chunks;
     if (!FULL && (last == chunks || (sn == 0 && cb >= vcols))) return;
