@@ -85,10 +85,13 @@ def _check(t, name, shape, dtype, device):
         raise ValueError("%s must be on %s" % (name, device))
 
 
-def _out(t, name, shape, dtype, device):
-    """The caller's output tensor, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _like(t):
+    """A new contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _given(t, name, shape, dtype, device):
+    """The caller's output tensor, checked."""
     _check(t, name, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -161,20 +164,22 @@ class _Op:
         """Run the entry point `fn` on `stream` (default: the device's
         current one).  kept: tensors made for this call, which the allocator
         must not hand out before `stream` has passed it."""
-        current = torch.cuda.current_stream(device)
         if stream is None:
-            stream = current
-        elif stream != current:
-            # what was made here has to be ready there, and to live until then
-            stream.wait_stream(current)
-            for t in kept:
-                if t is not None:
-                    t.record_stream(stream)
+            # the handle alone: a Stream object takes 2 us to make
+            handle = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            handle, current = stream.cuda_stream, torch.cuda.current_stream(device)
+            if stream != current:
+                # what was made here has to be ready there, and to live until then
+                stream.wait_stream(current)
+                for t in kept:
+                    if t is not None:
+                        t.record_stream(stream)
         if torch.cuda.current_device() == device.index:
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
         else:
             with torch.cuda.device(device):
-                st = fn(*args, stream.cuda_stream)
+                st = fn(*args, handle)
         if st != 0:
             raise FFTConvError(st, fn.__name__)
 
@@ -252,8 +257,8 @@ class QKNorm(_Op):
         (dev, ref, _), ins, ptrs = self._checked(
             "_describe", (q, k, q_weight, k_weight, cos, sin, positions))
         yq, yk = (None, None) if out is None else out
-        yq = _out(yq, "out[0]", q.shape, self._dt, dev)
-        yk = _out(yk, "out[1]", k.shape, self._dt, dev)
+        yq = _like(q) if yq is None else _given(yq, "out[0]", q.shape, self._dt, dev)
+        yk = _like(k) if yk is None else _given(yk, "out[1]", k.shape, self._dt, dev)
         self._call(self._lib.fftconv_qknorm_forward, dev, stream, (*ins, yq, yk), ref, *ptrs,
                    yq.data_ptr(), yk.data_ptr())
         return yq, yk
@@ -268,10 +273,9 @@ class QKNorm(_Op):
         _check(dq_out, "dq_out", q.shape, self._dt, dev)
         _check(dk_out, "dk_out", k.shape, self._dt, dev)
         dq_out, dk_out = _dense(dq_out), _dense(dk_out)
-        dq = torch.empty(q.shape, dtype=self._dt, device=dev)
-        dk = torch.empty(k.shape, dtype=self._dt, device=dev)
-        dwq = None if q_weight is None else torch.empty(self.D, dtype=torch.float32, device=dev)
-        dwk = None if k_weight is None else torch.empty(self.D, dtype=torch.float32, device=dev)
+        dq, dk = _like(q), _like(k)
+        dwq = None if q_weight is None else _like(q_weight)
+        dwk = None if k_weight is None else _like(k_weight)
         ws = None
         if dwq is not None or dwk is not None:
             ws = self._space(need, workspace, dev, "workspace")
@@ -332,8 +336,12 @@ class GatedDelta(_Op):
 
     def _forward(self, ins, out, final_state, saved, train, workspace, stream):
         (dev, ref, state, sizes), ins, ptrs = self._checked("_describe", ins)
-        out = _out(out, "out", ins[2].shape, self._dt, dev)
-        final_state = _out(final_state, "final_state", state, torch.float32, dev)
+        v = ins[2]
+        out = _like(v) if out is None else _given(out, "out", v.shape, self._dt, dev)
+        if final_state is None:
+            final_state = torch.empty(state, dtype=torch.float32, device=dev)
+        else:
+            _given(final_state, "final_state", state, torch.float32, dev)
         ws = self._space(sizes[0], workspace, dev, "workspace")
         if train:
             saved = self._space(sizes[1], saved, dev, "saved")
@@ -374,9 +382,8 @@ class GatedDelta(_Op):
         if saved.device != dev or not saved.is_contiguous():
             raise ValueError("saved must be what forward_train returned")
         ws = self._space(sizes[2], workspace, dev, "workspace")
-        new = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in ins[:5]]
-        new.append(None if initial_state is None
-                   else torch.empty(state, dtype=torch.float32, device=dev))
+        new = [_like(x) for x in ins[:5]]
+        new.append(None if initial_state is None else _like(initial_state))
         self._call(self._lib.fftconv_delta_backward, dev, stream,
                    (*ins, saved, d_out, d_final_state, ws, *new), ref, *ptrs[:6], _ptr(saved),
                    self._bytes(saved), _ptr(d_out), _ptr(d_final_state), *map(_ptr, new),
@@ -418,7 +425,7 @@ class GatedDelta(_Op):
             raise ValueError("state must be 16-byte aligned")
         (dev, ref, pool), ins, ptrs = self._checked("_describe_step",
                                                     (q, k, v, g, beta, slots, state))
-        out = _out(out, "out", v.shape, self._dt, dev)
+        out = _like(v) if out is None else _given(out, "out", v.shape, self._dt, dev)
         self._call(self._lib.fftconv_delta_step, dev, stream, (*ins, out), ref, *ptrs[:5],
                    ptrs[6], pool, ptrs[5], out.data_ptr())
         return out
