@@ -121,8 +121,20 @@ struct DeltaParams {
     float* states;
     float* us;
 };
+// Waves for the chain of a walk over p's segments.  effect: of the one that
+// makes their effects on the state, with columns for the matrices too.
+inline int walk_waves(const DeltaParams& p, bool effect) {
+    const auto units = [&](int width) {
+        return (double)p.segs * p.Hv *
+               ((p.Dv + width - 1) / width + (effect ? (p.Dk + width - 1) / width : 0));
+    };
+    int waves;
+    walk_us(units(64), units(128), effect, p.cu != nullptr, &waves);
+    return waves;
+}
+
 struct DeltaGradParams {
-    DeltaParams f;                   // inputs, bpack, states, us
+    DeltaParams f;                   // inputs, bpack, states, us, segments
     const void* dout;                // [B][T][Hv][Dv]
     const float* dfin;               // [nseq][Hv][Dk][Dv] or null
     float* dstates;                  // [slots][Hv] saved matrices: gradient of
@@ -134,6 +146,8 @@ struct DeltaGradParams {
     float* dbeta;
     float* dinit;                    // [nseq][Hv][Dk][Dv] or null
 };
+// reverse: the segments' effects on the gradient of the state, from the last on
+hipError_t launch_delta_join(const DeltaParams& p, bool reverse, hipStream_t s);
 hipError_t launch_delta_rscan(int io, const DeltaGradParams& p, hipStream_t s);
 hipError_t launch_delta_grads(int io, const DeltaGradParams& p, hipStream_t s);
 hipError_t launch_delta_prep(int io, const DeltaParams& p, hipStream_t s);

@@ -671,7 +671,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
 
 // Joins the segments of a sequence: with N the last state of a segment from 0
 // and M the matrix of the segment, the state after it is M S + N.  Leaves in
-// place of N the state after each segment but the last.  The eight waves of a
+// place of N the state after each segment but the last (the backward walk's
+// segments go from the last on, all but the first).  The eight waves of a
 // workgroup take 16 columns each, as in the walk, and share M through LDS, the
 // next one's loads in flight.
 template <int DK>
@@ -681,7 +682,7 @@ struct JoinLds {
     static constexpr int kBytes = kHalves * kRows * 16;
 };
 template <int DK>
-__global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
+__global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p, bool reverse) {
     typedef JoinLds<DK> L;
     constexpr int KB = DK / 32, ST = DK / 16;
     extern __shared__ uint4 lds[];
@@ -694,18 +695,20 @@ __global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
     const Span sp = span_of(p, seq);
     const int chunks = (sp.len + kChunk - 1) / kChunk;
     const int n = (chunks + p.seg_chunks - 1) / p.seg_chunks;   // segments
-    if (n < 3) return;           // the first segment's state is already whole
+    if (n < 3) return;           // the first one's state is already whole
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4, slot = 16 * g + (c ^ (4 * g));
     const int col = cb * 128 + wave * 16 + c;
     const bool cok = col < p.Dv;
     const long long state = p.Dk * (long long)p.Dv, square = p.Dk * (long long)p.Dk;
     const long long seg0 = seg_of(p, sp, (unsigned)seq, p.seg_chunks);
+    // the i-th segment on the way
+    const auto seg = [&](int i) { return (seg0 + (reverse ? n - 1 - i : i)) * p.Hv + h; };
     const uint32_t slane = (uint32_t)(8 * g * p.Dv + col) * 4;
     dfloat4 S[ST], R[ST];
     RowTiles<IO_F32, DK, 8> rm[L::kHalves];
     const auto load = [&](int i, dfloat4 (&x)[ST]) __attribute__((always_inline)) {
-        const long long at = ((seg0 + i) * p.Hv + h) * state;
+        const long long at = seg(i) * state;
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -716,7 +719,7 @@ __global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
             }
     };
     const auto load_m = [&](int i) __attribute__((always_inline)) {
-        const Tokens m = tokens_of<IO_F32>(p.seg_m, ((seg0 + i) * p.Hv + h) * square, p.Dk);
+        const Tokens m = tokens_of<IO_F32>(p.seg_m, seg(i) * square, p.Dk);
 #pragma unroll
         for (int j = 0; j < L::kHalves; ++j) {
             const int rows = p.Dk - 64 * j;
@@ -753,8 +756,7 @@ __global__ __launch_bounds__(512) void delta_join_kernel(DeltaParams p) {
 #pragma unroll
         for (int t = 0; t < ST; ++t) S[t] = R[t];
         if (cok)
-            store_state<ST>((char*)(p.seg_n + ((seg0 + i) * p.Hv + h) * state), p.Dv * 4, slane,
-                            p.Dk, S);
+            store_state<ST>((char*)(p.seg_n + seg(i) * state), p.Dv * 4, slane, p.Dk, S);
         load(ahead, R);
         __syncthreads();
     }
@@ -787,29 +789,28 @@ hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
 
 template <int IO, int DK, int MODE>
 hipError_t scan_mode(const DeltaParams& p, hipStream_t s) {
-    const auto units = [&](int width) {
-        return (double)p.segs * p.Hv *
-               ((p.Dv + width - 1) / width + (MODE == kEffect ? (p.Dk + width - 1) / width : 0));
-    };
-    int waves;
-    walk_us(units(64), units(128), MODE == kEffect, p.cu != nullptr, &waves);
-    return waves == 4 ? scan_launch<IO, DK, 4, MODE>(p, s) : scan_launch<IO, DK, 8, MODE>(p, s);
+    return walk_waves(p, MODE == kEffect) == 4 ? scan_launch<IO, DK, 4, MODE>(p, s)
+                                               : scan_launch<IO, DK, 8, MODE>(p, s);
 }
 template <int IO, int DK>
 hipError_t scan_io(const DeltaParams& p, hipStream_t s) {
     if (p.seg_m) {
         hipError_t e = scan_mode<IO, DK, kEffect>(p, s);
-        if (e != hipSuccess) return e;
-        const int lds = JoinLds<DK>::kBytes;
-        e = hipFuncSetAttribute((const void*)delta_join_kernel<DK>,
-                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-        const long long joins = p.nseq * p.Hv * ((p.Dv + 127) / 128);
-        hipLaunchKernelGGL((delta_join_kernel<DK>), dim3((unsigned)joins), dim3(512), lds, s, p);
-        e = hipGetLastError();
+        if (e == hipSuccess) e = launch_delta_join(p, false, s);
         if (e != hipSuccess) return e;
     }
     return p.states ? scan_mode<IO, DK, kSaving>(p, s) : scan_mode<IO, DK, kOutputs>(p, s);
+}
+template <int DK>
+hipError_t join_launch(const DeltaParams& p, bool reverse, hipStream_t s) {
+    const int bytes = JoinLds<DK>::kBytes;
+    const hipError_t e = hipFuncSetAttribute((const void*)delta_join_kernel<DK>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    const long long joins = p.nseq * p.Hv * ((p.Dv + 127) / 128);
+    hipLaunchKernelGGL((delta_join_kernel<DK>), dim3((unsigned)joins), dim3(512), bytes, s, p,
+                       reverse);
+    return hipGetLastError();
 }
 
 template <int IO, int DK>
@@ -846,6 +847,10 @@ hipError_t launch_delta_prep(int io, const DeltaParams& p, hipStream_t s) {
     case IO_F16: return d64 ? prep_io<IO_F16, 64>(p, s) : prep_io<IO_F16, 128>(p, s);
     default: return d64 ? prep_io<IO_BF16, 64>(p, s) : prep_io<IO_BF16, 128>(p, s);
     }
+}
+
+hipError_t launch_delta_join(const DeltaParams& p, bool reverse, hipStream_t s) {
+    return p.Dk <= 64 ? join_launch<64>(p, reverse, s) : join_launch<128>(p, reverse, s);
 }
 
 hipError_t launch_delta_scan(int io, const DeltaParams& p, hipStream_t s) {

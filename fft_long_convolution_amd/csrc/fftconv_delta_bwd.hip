@@ -29,39 +29,60 @@ struct RscanLds {
 
 // The mirror of the forward walk: a wave owns 16 columns of D and goes
 // through K D, T^T dU and the two transposed products without an exchange.
-template <int IO, int DK, int W>
+// FULL false: a segment's effect on D alone, from the gradient of the final
+// state (the last segment of a sequence) or from 0, and in columns of their own
+// the matrix D is multiplied with (from the identity, without dO).
+template <int IO, int DK, int W, bool FULL>
 __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
     const DeltaParams& p = gp.f;
     constexpr int NA = Io<IO>::NA, KB = DK / 32, ST = DK / 16, kB = Io<IO>::kB, kCols = 16 * W;
     extern __shared__ uint4 lds[];
-    const int cols = (p.Dv + kCols - 1) / kCols;
-    const unsigned units = (unsigned)p.nseq * p.Hv * cols;
+    const int vcols = (p.Dv + kCols - 1) / kCols;
+    const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
+    const unsigned units = (unsigned)p.segs * p.Hv * cols;
     unsigned id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
-    const int cb = (int)(id % cols);
+    int cb = (int)(id % cols);
     id /= cols;
     const int h = (int)(id % p.Hv);
-    const long long seq = id / p.Hv;
+    const long long seg = id / p.Hv;
+    const long long seq = seq_of(p, (unsigned)seg, p.seg_chunks);
     const Span sp = span_of(p, seq);
+    const int chunks = (sp.len + kChunk - 1) / kChunk;
+    // segment of the sequence
+    const int sn = (int)((unsigned)seg - seg_of(p, sp, (unsigned)seq, p.seg_chunks));
+    const long long first_ = (long long)sn * p.seg_chunks;
+    if (sn < 0 || (sn != 0 && first_ >= chunks)) return;   // no such segment
+    const int first = (int)first_;
+    const int last = chunks - first > p.seg_chunks ? first + p.seg_chunks : chunks;
+    if (!FULL && (sn == 0 || (last == chunks && cb >= vcols))) return;
+    const bool matrix = !FULL && cb >= vcols;
+    if (matrix) cb -= vcols;
+
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int slot = 16 * g + (c ^ (4 * g));             // of a row operand
     const int col = cb * kCols + wave * 16 + c;
-    const bool cok = col < p.Dv;
+    const int width = matrix ? p.Dk : p.Dv;
+    const bool cok = col < width;
     const int colv = cok ? col : 0;                      // to read from
     const int hk = h / p.group;
     const long long state = p.Dk * (long long)p.Dv;
-    const long long sbase = (seq * p.Hv + h) * state + col;
     dfloat4 D[ST];
+    {
+        const float* s = nullptr;
+        if (last == chunks) s = gp.dfin ? gp.dfin + (seq * p.Hv + h) * state + col : nullptr;
+        else if (FULL) s = p.seg_n + ((seg + 1) * p.Hv + h) * state + col;
 #pragma unroll
-    for (int t = 0; t < ST; ++t)
+        for (int t = 0; t < ST; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = tile_row(t, 4 * g + r);
-            D[t][r] = gp.dfin && cok && row < p.Dk ? gp.dfin[sbase + (long long)row * p.Dv] : 0.f;
-        }
-    const int chunks = (sp.len + kChunk - 1) / kChunk;
+            for (int r = 0; r < 4; ++r) {
+                const int row = tile_row(t, 4 * g + r);
+                D[t][r] = matrix ? (row == col ? 1.f : 0.f)
+                                 : (s && cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f);
+            }
+    }
     const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2], p.ks[1]);
     const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2], p.qs[1]);
     const long long ofirst = (sp.b * p.T + sp.t0) * p.Hv * p.Dv + h * p.Dv;
@@ -86,13 +107,13 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
             rq.store(d + L::kQ);
             rp.store(d + L::kPack);
         };
-        if (chunks > 0) {
-            load(chunks - 1);
+        if (first < last) {
+            load(last - 1);
             store(lds);
         }
         __syncthreads();
-        for (int ch = chunks - 1, buf = 0; ch >= 0; --ch) {
-            load(ch > 0 ? ch - 1 : 0);
+        for (int ch = last - 1, buf = 0; ch >= first; --ch) {
+            load(ch > first ? ch - 1 : first);
             if (L::kBufs == 2) {
                 buf ^= 1;
                 store(lds + buf * L::kSize);
@@ -109,12 +130,14 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     // meet columns of P^T and rows of Q that are 0.
     dfloat4 dN[4];
     const auto load_do = [&](int ch) __attribute__((always_inline)) {
-        load_column<IO>(to, ch * kChunk, olane, sp.len - ch * kChunk, dN);
+        if (!matrix) load_column<IO>(to, ch * kChunk, olane, sp.len - ch * kChunk, dN);
     };
-    if (chunks > 0) load_do(chunks - 1);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) dN[m] = dfloat4{0, 0, 0, 0};
+    if (first < last) load_do(last - 1);
     __syncthreads();
     int buf = 0;
-    for (int ch = chunks - 1; ch >= 0; --ch) {
+    for (int ch = last - 1; ch >= first; --ch) {
         const long long ci = (sp.slot0 + ch) * p.Hv + h;
         const uint4* now = lds + buf * L::kSize;
         const float* fac = (const float*)(now + L::kPack + kDec);
@@ -122,9 +145,9 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
         dfloat4 dO[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dO[m] = dN[m];
-        const int ahead = ch > 0 ? ch - 1 : 0;
+        const int ahead = ch > first ? ch - 1 : first;
         const float big_d = max_column(D);
-        if (cok) save_columns<KB>(gp.dstates, ci, p.Dv, col, D, big_d);
+        if (FULL && cok) save_columns<KB>(gp.dstates, ci, p.Dv, col, D, big_d);
         // dU = e^(Gc-G) o K D + P^T dO
         dfloat4 dU[4], PO[4];
 #pragma unroll
@@ -190,7 +213,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
 #pragma unroll
             for (int m = 0; m < 4; ++m) dY[m] *= back;
         }
-        {
+        if (FULL) {
             const float big_y = max_column(dY);
             if (cok) save_columns<2>(gp.dys, ci, p.Dv, col, dY, big_y, big_o);
         }
@@ -203,7 +226,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
             dY[m][2] *= b.z;
             dY[m][3] *= b.w;
         }
-        if (cok)
+        if (FULL && cok)
             store_column<IO>((char*)tv.at(ch * kChunk), tv.bytes, olane, sp.len - ch * kChunk, dY);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -254,9 +277,12 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
         if (L::kBufs == 2) buf ^= 1;
         else __syncthreads();
     }
-    if (gp.dinit && cok)
-        store_state<ST>((char*)(gp.dinit + (seq * p.Hv + h) * state), p.Dv * 4,
-                        (uint32_t)(8 * g * p.Dv + col) * 4, p.Dk, D);
+    if (!cok) return;
+    float* d = nullptr;
+    if (FULL) d = gp.dinit && sn == 0 ? gp.dinit + (seq * p.Hv + h) * state : nullptr;
+    else if (matrix) d = p.seg_m + (seg * p.Hv + h) * p.Dk * (long long)p.Dk;
+    else d = p.seg_n + (seg * p.Hv + h) * state;
+    if (d) store_state<ST>((char*)d, width * 4, (uint32_t)(8 * g * width + col) * 4, p.Dk, D);
 }
 
 // ------------------------------------------------ the gradients of a chunk
@@ -716,24 +742,32 @@ void delta_grads_kernel(DeltaGradParams gp) {
     }
 }
 
-template <int IO, int DK, int W>
-hipError_t rscan_w(const DeltaGradParams& p, hipStream_t s) {
+template <int IO, int DK, int W, bool FULL>
+hipError_t rscan_launch(const DeltaGradParams& p, hipStream_t s) {
     const int bytes = RscanLds<IO, DK>::kBytes;
-    const hipError_t e = hipFuncSetAttribute((const void*)delta_rscan_kernel<IO, DK, W>,
+    const hipError_t e = hipFuncSetAttribute((const void*)delta_rscan_kernel<IO, DK, W, FULL>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const long long units = p.f.nseq * p.f.Hv * ((p.f.Dv + 16 * W - 1) / (16 * W));
-    hipLaunchKernelGGL((delta_rscan_kernel<IO, DK, W>), dim3((unsigned)xcd_blocks(units)),
+    const int width = 16 * W;
+    const int cols = (p.f.Dv + width - 1) / width + (FULL ? 0 : (p.f.Dk + width - 1) / width);
+    const long long units = p.f.segs * p.f.Hv * cols;
+    hipLaunchKernelGGL((delta_rscan_kernel<IO, DK, W, FULL>), dim3((unsigned)xcd_blocks(units)),
                        dim3(64 * (W + kLoaders)), bytes, s, p);
     return hipGetLastError();
 }
+template <int IO, int DK, bool FULL>
+hipError_t rscan_mode(const DeltaGradParams& p, hipStream_t s) {
+    return walk_waves(p.f, !FULL) == 4 ? rscan_launch<IO, DK, 4, FULL>(p, s)
+                                       : rscan_launch<IO, DK, 8, FULL>(p, s);
+}
 template <int IO, int DK>
 hipError_t rscan_io(const DeltaGradParams& p, hipStream_t s) {
-    const double heads = (double)p.f.nseq * p.f.Hv;
-    int waves;
-    walk_us(heads * ((p.f.Dv + 63) / 64), heads * ((p.f.Dv + 127) / 128), false,
-            p.f.cu != nullptr, &waves);
-    return waves == 4 ? rscan_w<IO, DK, 4>(p, s) : rscan_w<IO, DK, 8>(p, s);
+    if (p.f.seg_m) {
+        hipError_t e = rscan_mode<IO, DK, false>(p, s);
+        if (e == hipSuccess) e = launch_delta_join(p.f, true, s);
+        if (e != hipSuccess) return e;
+    }
+    return rscan_mode<IO, DK, true>(p, s);
 }
 
 template <int IO, int DK, bool GROUP>

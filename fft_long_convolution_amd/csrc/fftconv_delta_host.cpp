@@ -242,6 +242,8 @@ struct DeltaLayout {
     size_t bpack, states, us;       // saved
     size_t workspace() const { return pack + seg_n + seg_m; }
     size_t saved() const { return bpack + states + us; }
+    // dstates, dys and the segments
+    size_t backward() const { return states + us + seg_n + seg_m; }
 };
 bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
     size_t n, x, y, per = delta_seg_chunks(d), m;
@@ -327,6 +329,15 @@ fftconv_status delta_inputs(const fftconv_delta_desc* d, const DeltaArgs& a, Del
     return FFTCONV_OK;
 }
 
+void delta_place_segments(const fftconv_delta_desc* d, const DeltaLayout& l, char* at,
+                          DeltaParams& p) {
+    p.seg_chunks = (int)delta_seg_chunks(d);
+    p.segs = (long long)delta_segs(d, (size_t)p.seg_chunks);
+    if (l.seg_m) {
+        p.seg_n = (float*)at;
+        p.seg_m = (float*)(at + l.seg_n);
+    }
+}
 void delta_place_saved(const DeltaLayout& l, void* saved, DeltaParams& p) {
     char* f = (char*)saved;
     p.bpack = (uint4*)f;
@@ -441,12 +452,7 @@ fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q,
     p.fin = final_state;
     p.pack = (uint4*)workspace;
     if (keep) delta_place_saved(l, saved, p);
-    p.seg_chunks = (int)delta_seg_chunks(d);
-    p.segs = (long long)delta_segs(d, (size_t)p.seg_chunks);
-    if (l.seg_m) {
-        p.seg_n = (float*)((char*)workspace + l.pack);
-        p.seg_m = (float*)((char*)workspace + l.pack + l.seg_n);
-    }
+    delta_place_segments(d, l, (char*)workspace + l.pack, p);
     hipStream_t s = (hipStream_t)stream;
     if (d->B * d->T) CHECK(launched(launch_delta_prep(d->dtype, p, s)));
     return launched(launch_delta_scan(d->dtype, p, s));
@@ -455,7 +461,7 @@ fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q,
 size_t fftconv_delta_backward_workspace_bytes(const fftconv_delta_desc* d) {
     DeltaLayout l;
     if (delta_sizes(d) != FFTCONV_OK || !delta_layout(d, &l)) return 0;
-    return l.states + l.us;
+    return l.backward();
 }
 
 fftconv_status fftconv_delta_backward(const fftconv_delta_desc* d, const void* q, const void* k,
@@ -483,7 +489,7 @@ fftconv_status fftconv_delta_backward(const fftconv_delta_desc* d, const void* q
     CHECK(check_ptr(d_initial_state, state, false));
     CHECK(check_ptr(saved, l.saved()));
     if (saved_bytes < l.saved()) return FFTCONV_ERR_INVALID_ARG;
-    const size_t need = l.states + l.us;
+    const size_t need = l.backward();
     if (need && (!workspace || workspace_bytes < need)) return FFTCONV_ERR_WORKSPACE;
     if ((uintptr_t)workspace & 15) return FFTCONV_ERR_ALIGNMENT;
     in[5] = {saved, l.saved()};
@@ -498,6 +504,7 @@ fftconv_status fftconv_delta_backward(const fftconv_delta_desc* d, const void* q
     p.dfin = d_final_state;
     p.dstates = (float*)workspace;
     p.dys = (float*)((char*)workspace + l.states);
+    delta_place_segments(d, l, (char*)workspace + l.states + l.us, p.f);
     p.dq = dq;
     p.dk = dk;
     p.dv = dv;

@@ -114,6 +114,26 @@ def test_long_sequence_backward(dtype):
     check_backward(ins, cu, dtype, 32, 40)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 2100, 1, 1, 128, 24), (2, 1300, 1, 2, 24, 72)], ids=str)
+def test_cut_sequence_backward(shape, dtype):
+    ins = delta_inputs(23, *shape, dtype, decay=0.02)
+    assert is_cut(rule(shape[4], shape[5], dtype), gpu(*ins), None)
+    check_backward(ins, None, dtype, shape[4], shape[5])
+    check_backward(ins[:5] + (None,), None, dtype, shape[4], shape[5], with_final=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cut_packed_sequences_backward(dtype):
+    cu = torch.tensor([0, 0, 10, 3000])
+    ins = delta_inputs(24, 1, 3000, 1, 1, 16, 24, dtype, rows=3, decay=0.02)
+    check_backward(ins, cu, dtype, 16, 24)
+    cu = torch.tensor([0, 900, 3000])
+    ins = delta_inputs(25, 1, 3000, 1, 1, 16, 24, dtype, rows=2, decay=0.02)
+    assert is_cut(rule(16, 24, dtype), gpu(*ins), cu.cuda())
+    check_backward(ins, cu, dtype, 16, 24)
+
+
 # more workgroups of 64 columns than CUs, fewer of 128
 MANY = [(2, 130, 24, 72, 128, 128), (3, 70, 48, 48, 40, 128), (150, 65, 1, 1, 128, 104)]
 
