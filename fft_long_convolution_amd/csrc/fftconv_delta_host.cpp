@@ -197,11 +197,13 @@ size_t delta_slots(const fftconv_delta_desc* d) {
 
 // Chunks of a segment.  A sequence is a chain of chunks; where the heads and
 // columns leave CUs idle, sequences are cut into segments that are walked side
-// by side: once for their effects on the state, and, after a join of some 7 us a
-// segment, for the outputs.  The number of segments is the one of least time
-// under walk_us(); one where that is least.  (4 x 32768 x 4 x 128 bf16: 16
-// segments, 0.70 ms, uncut 2.1; 1 x 4096 x 8 x 128: 6, 0.12 ms, uncut 0.26;
-// 16 x 8192 x 6 x 128: uncut 0.65, in three 0.91.)
+// by side: once for their effects on the state, and, after a join, for the
+// outputs; the backward walk likewise.  The number of segments is the one of
+// least time by walk_us() and the steps of the join (2.5 us at D_k = 64, 7 at
+// 128), 1 where that is least.  bf16, forward: 4 x 32768 tokens of 4 heads of
+// 128, 16 segments, 0.69 ms, uncut 2.1; 1 x 4096 x 8: 6, 0.12 ms, uncut 0.26;
+// 16 x 8192 x 6: uncut 0.65, in three 0.91.  With the gradients, fp32, 2 x 1501
+// tokens of 4 heads of 64: 8 segments, 132 us, uncut some 230.
 size_t delta_seg_chunks(const fftconv_delta_desc* d) {
     const size_t nch = (d->T + kChunk - 1) / kChunk;
     const size_t rows = d->sequences ? d->sequences : d->B;
@@ -213,7 +215,10 @@ size_t delta_seg_chunks(const fftconv_delta_desc* d) {
     const double heads = (double)rows * d->Hv;
     const size_t v64 = (d->Dv + 63) / 64, v128 = (d->Dv + 127) / 128;
     const size_t k64 = (d->Dk + 63) / 64, k128 = (d->Dk + 127) / 128;
-    double best = L * walk_us(heads * v64, heads * v128, false, packed, nullptr);
+    // a chunk of fp32 against one of 16 bits; a step of the join
+    const double chunk = d->dtype == FFTCONV_F32 ? 1.35 : 1.0;
+    const double join = d->Dk <= 64 ? 2.5 : 7.0;
+    double best = chunk * L * walk_us(heads * v64, heads * v128, false, packed, nullptr);
     size_t per = whole;
     for (size_t n = 3; n <= 64 && n * 2 <= L; ++n) {
         const size_t p = (L + n - 1) / n;
@@ -222,7 +227,7 @@ size_t delta_seg_chunks(const fftconv_delta_desc* d) {
         const double effect = walk_us(heads * ((n - 1) * v64 + (n - 2) * k64),
                                       heads * ((n - 1) * v128 + (n - 2) * k128), true, packed,
                                       nullptr);
-        const double t = p * (full + effect) + 7.0 * (n - 2) + 12.0;
+        const double t = chunk * p * (full + effect) + join * (n - 2) + 12.0;
         if (t < best) {
             best = t;
             per = p;
