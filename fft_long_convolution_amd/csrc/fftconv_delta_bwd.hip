@@ -399,21 +399,23 @@ void delta_grads_kernel(DeltaGradParams gp) {
             for (int k = 0; k < NS; ++k) {
                 const int i = threadIdx.x + 256 * k, t = i / (KB * 64), in = i % (KB * 64);
                 const int ds = d0 + 16 * t < padded ? d0 + 16 * t : 0;
-                const du4* s = (const du4*)(S0 + (long long)ds * DK + in * 8);
-                const du4* d = (const du4*)(D + (long long)ds * DK + in * 8);
+                const int first = (in & ~63) * 2 + (in & 63);        // 16-byte piece
+                const du4* s = (const du4*)(S0 + (long long)ds * DK) + first;
+                const du4* d = (const du4*)(D + (long long)ds * DK) + first;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    x.s[k][j] = s[j];
-                    x.d[k][j] = d[j];
+                    x.s[k][j] = s[64 * j];
+                    x.d[k][j] = d[64 * j];
                 }
             }
             const int du = d0 + 16 * u_tile < padded ? d0 + 16 * u_tile : 0;
-            const du4* u = (const du4*)(U + (long long)du * kChunk + u_in * 8);
-            const du4* y = (const du4*)(Y + (long long)du * kChunk + u_in * 8);
+            const int first = (u_in & ~63) * 2 + (u_in & 63);
+            const du4* u = (const du4*)(U + (long long)du * kChunk) + first;
+            const du4* y = (const du4*)(Y + (long long)du * kChunk) + first;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                x.u[j] = u[j];
-                x.y[j] = y[j];
+                x.u[j] = u[64 * j];
+                x.y[j] = y[64 * j];
                 const int e = d0 + 16 * j + 4 * g < p.Dv ? d0 + 16 * j + 4 * g : 0;
                 x.o[j] = *(const piece*)(dO + e * kB);
                 x.v[j] = *(const piece*)(V + e * kB);

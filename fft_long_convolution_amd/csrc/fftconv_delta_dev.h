@@ -591,11 +591,13 @@ __device__ __forceinline__ void store_state(char* s, uint32_t bytes, uint32_t la
     }
 }
 // Saved matrices (states and their gradients, U, dY): rows x Dv of fp32 for a
-// chunk and head, rows a multiple of 32, columns padded to 16, and
-// behind them the largest magnitude of each column (and, with dY, of dO's).  Sixteen
-// columns together: block kb, place 16 g + (c ^ 4 g) holds rows
-// 32 kb + 8 g + i, i < 8, of column c: a lane's accumulators in two 16-byte
-// stores, and what RowTiles puts into LDS for transposed reads.
+// chunk and head, rows a multiple of 32, columns padded to 16, and behind them
+// the largest magnitude of each column (and, with dY, of dO's).  Sixteen
+// columns together: block kb, half j, place 16 g + (c ^ 4 g) holds rows
+// 32 kb + 8 g + 4 j + i, i < 4, of column c: a lane's accumulators in two
+// 16-byte stores, each of them 1 KiB in a row for the wave (with a lane's two
+// side by side the walks of 64 x 1024 tokens of 6 heads of 128 took 368 and 392
+// us, so 346 and 360), and what RowTiles puts into LDS for transposed reads.
 __host__ __device__ __forceinline__ long long saved_floats(int rows, int Dv) {
     const int cols = (Dv + 15) / 16 * 16;
     return (long long)(rows + 2) * cols;
@@ -606,12 +608,9 @@ __device__ __forceinline__ void save_columns(float* all, long long ci, int Dv, i
                                              float other = 0.f) {
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     float* base = all + ci * saved_floats(32 * KB, Dv);
-    dfloat4* d = (dfloat4*)(base + (long long)(col - c) * (32 * KB)) + (16 * g + (c ^ (4 * g))) * 2;
+    dfloat4* d = (dfloat4*)(base + (long long)(col - c) * (32 * KB)) + 16 * g + (c ^ (4 * g));
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        d[kb * 128] = x[2 * kb];
-        d[kb * 128 + 1] = x[2 * kb + 1];
-    }
+    for (int i = 0; i < 2 * KB; ++i) d[64 * i] = x[i];
     if (g == 0) {
         const int cols = (Dv + 15) / 16 * 16;
         float* m = base + (long long)cols * (32 * KB) + col;
