@@ -84,7 +84,9 @@ inline double walk_us(double units64, double units128, bool effect, bool packed,
     const double cus = 256.0;
     const auto time = [&](double units, double alone, double full) {
         const double load = units / cus;
-        const double rounds = load <= 1 ? 1 : packed ? 0.5 + 0.5 * load : (double)(long long)(load + 0.999999);
+        const double rounds = load <= 1 ? 1
+                              : packed  ? 0.5 + 0.5 * load
+                                        : (double)(long long)(load + 0.999999);
         return rounds * (alone + (full - alone) * (load < 1 ? load : 1));
     };
     const double four = effect ? time(units64, 2.5, 3.25) : time(units64, 3.4, 4.7);

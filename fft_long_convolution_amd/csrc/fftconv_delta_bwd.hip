@@ -31,7 +31,9 @@ struct RscanLds {
 // through K D, T^T dU and the two transposed products without an exchange.
 // FULL false: a segment's effect on D alone, from the gradient of the final
 // state (the last segment of a sequence) or from 0, and in columns of their own
-// the matrix D is multiplied with (from the identity, without dO).
+// the matrix D is multiplied with (from the identity, without dO).  Bound as
+// the forward walk is: 64 x 1024 tokens of 6 heads of 128 in bf16 take 360 us,
+// 16 chunks in two rounds of workgroups, 0.7 GB of D and dY written.
 template <int IO, int DK, int W, bool FULL>
 __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
@@ -337,7 +339,10 @@ __device__ __forceinline__ void unpack_pieces(const P (&x)[2], bool ok0, bool ok
 // d0 + 16 (i/4) + 4 g + i%4.  They and dO have one scale each.  The value heads
 // that share the key head follow one another, and their parts of dQ and dK are
 // summed in registers, in a fixed order; with one (GROUP false) R1 and R3 become
-// dQ and dK.
+// dQ and dK.  64 x 1024 tokens of 6 heads of 128 in bf16 take 510 to 530 us for
+// the 1.9 GB it reads (S0 and D, in fp32 for dg's sums, are 1.6 of them), 3.7
+// TB/s: its registers allow two workgroups a CU, which wait 40 % of the time,
+// the vector unit (the f16 terms) is busy 40 %, the matrix cores 15 %.
 template <int IO, int DK, bool GROUP>
 __global__ __launch_bounds__(256, GROUP || IO == IO_F32 ? 1 : 2)
 void delta_grads_kernel(DeltaGradParams gp) {

@@ -694,9 +694,10 @@ __device__ __forceinline__ double shifted(double x) {
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 // Sum of the log decays up to the lane's token, in units of log 2 (decay()
-// makes factors of them).  Sums are fp64, so e^(G_i - G_j) is right to fp32 however much the chunk has decayed before;
-// decays below -1e4 count as -1e4 (their factor is 0 in fp32 either way), so
-// a reset (g = -inf) does not meet itself as inf - inf.  NaN stays NaN.
+// makes factors of them).  Sums are fp64, so e^(G_i - G_j) is right to fp32
+// however much the chunk has decayed before; decays below -1e4 count as -1e4
+// (their factor is 0 in fp32 either way), so a reset (g = -inf) does not meet
+// itself as inf - inf.  NaN stays NaN.
 __device__ __forceinline__ double decay_sum(float g) {
     double s = g < -1e4f ? -1e4f : g;
     // within each group of 16, then the groups before

@@ -14,11 +14,11 @@
 //
 // The pass moves each element once in and once out and does some ten
 // operations on it, so HBM bounds it: 64 x 1024 tokens of 12 heads of 128 in
-// bf16, 403 MB, take 76 us (5.3 TB/s; a streaming copy reaches 6.0).  A lane holds 8 consecutive elements
-// (one 16-byte access at 16 bits, two at 32), the lanes of a head (D/8,
-// rounded up to a power of two) sum by shuffles, and a group of lanes walks
-// over heads of ONE token, so the token's cosines and sines are read once
-// and stay in registers.
+// bf16, 403 MB, take 76 us (5.3 TB/s; a streaming copy reaches 6.0).  A lane
+// holds 8 consecutive elements (one 16-byte access at 16 bits, two at 32), the
+// lanes of a head (D/8, rounded up to a power of two) sum by shuffles, and a
+// group of lanes walks over heads of ONE token, so the token's cosines and
+// sines are read once and stay in registers.
 #include "fftconv_delta.h"
 
 namespace fftconv {

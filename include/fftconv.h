@@ -456,8 +456,8 @@ fftconv_status fftconv_qknorm_forward(const fftconv_qknorm_desc *desc, const voi
                                       const float *sin, const long long *positions,
                                       void *q_out, void *k_out, void *stream);
 
-/* Bytes of the workspace of fftconv_qknorm_backward (0 where no weight
- * gradient is asked for does not matter: it is only used for those). */
+/* Bytes of the workspace of fftconv_qknorm_backward, which needs one where a
+ * weight's gradient is asked for (NULL otherwise). */
 size_t fftconv_qknorm_workspace_bytes(const fftconv_qknorm_desc *desc);
 
 /* Gradients of fftconv_qknorm_forward with respect to q, k (dq, dk,
@@ -493,7 +493,7 @@ typedef struct fftconv_delta_desc {
 /* The gated delta rule over sequences.  For each value head, from a state S
  * [Dk][Dv], every token does
  *     S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  o = scale S^T q.
- *  q, k [B][T][Hk][Dk], v [B][T][Hv][Dv]: strided, plan of the descriptor.
+ *  q, k [B][T][Hk][Dk], v [B][T][Hv][Dv]: strided as the descriptor says.
  *  g (log decay), beta (write strength): fp32 [B][T][Hv], contiguous.  g may
  *     be -inf (the state is dropped).  The rule is stable for beta |k|^2 <= 2
  *     and g <= 0: keys of norm one (FFTCONV_NORM_L2).
@@ -506,8 +506,12 @@ typedef struct fftconv_delta_desc {
  *  saved: fftconv_delta_saved_bytes(desc) bytes that fftconv_delta_backward
  *     will read (16-B aligned), or NULL in inference.
  *  workspace: fftconv_delta_workspace_bytes(desc) bytes.
- * States, gates and sums are fp32 or wider whatever the I/O type; fp32
- * operands of the matrix products are split so that 24 bits take part. */
+ * States, gates and sums are fp32 or wider whatever the I/O type.  fp32
+ * operands of the matrix products are split into two f16 terms, 22 bits, with a
+ * scale for each row or column; the queries' products with bf16 outputs take
+ * the leading term.  Long sequences of few heads are cut into segments, joined
+ * in another order of the same sums: results do not depend on anything but the
+ * descriptor and the inputs, and equal calls give equal bits. */
 fftconv_status fftconv_delta_forward(const fftconv_delta_desc *desc, const void *q,
                                      const void *k, const void *v, const float *g,
                                      const float *beta, const long long *cu_seqlens,
