@@ -67,8 +67,8 @@ hipError_t launch_delta_step(int io, const DeltaStepParams& p, hipStream_t s);
 constexpr int kChunk = 64;
 constexpr int kTriTiles = 6;               // 16 x 32 tiles of a 64 x 64 triangle
 // What a chunk and value head needs besides its tokens, in matrix-operand
-// order, one uint4 a lane: (I + A)^-1 in three bf16 terms, the decays (e^G,
-// e^(Gc-G), beta, e^Gc, 64 floats each), the decayed scores P.
+// order, one uint4 a lane: (I + A)^-1 in two f16 terms, the chunk's factors
+// (decays, beta, scales), the decayed scores P.
 int delta_pack_uint4(int io);              // of the forward pack
 int delta_back_pack_uint4();               // of its transposes
 
@@ -77,7 +77,7 @@ int delta_back_pack_uint4();               // of its transposes
 // measured at heads of 128 in bf16: alone on a card and with all 256 CUs taken.
 // A workgroup has a CU to itself, so more than 256 run in rounds; packed
 // sequences differ in length, and about half of a further round is hidden behind
-// the longest of them (46 sequences, 8 heads of 64, f16: 82 us with four waves
+// the longest of them (23 sequences, 8 heads of 64 x 128, f16: 82 us with four waves
 // and 368 workgroups, 97 with eight and 184).  *waves: the better of four and
 // eight.
 inline double walk_us(double units64, double units128, bool effect, bool packed, int* waves) {
@@ -116,8 +116,11 @@ struct DeltaParams {
     // like the slots of chunks, where seg_m is given
     long long segs;
     int seg_chunks;
-    float* seg_n;                    // [segs][Hv][Dk][Dv]
+    float* seg_n;                    // [segs][Hv][Dk][Dv]; pieces: [nseq] ...
     float* seg_m;                    // [segs][Hv][Dk][Dk]
+    // > 1: a walk's chains go in so many pieces (the segments), seg_n handed from
+    // one to the next, `rounds` launches of workgroups of `waves` chain waves
+    int pieces, rounds, round, waves;
     // for the backward, or null: each chunk's first state and U, [slots][Hv]
     // matrices in the layout of saved_floats()
     float* states;
@@ -126,6 +129,7 @@ struct DeltaParams {
 // Waves for the chain of a walk over p's segments.  effect: of the one that
 // makes their effects on the state, with columns for the matrices too.
 inline int walk_waves(const DeltaParams& p, bool effect) {
+    if (p.pieces > 1) return p.waves;
     const auto units = [&](int width) {
         return (double)p.segs * p.Hv *
                ((p.Dv + width - 1) / width + (effect ? (p.Dk + width - 1) / width : 0));
@@ -133,6 +137,13 @@ inline int walk_waves(const DeltaParams& p, bool effect) {
     int waves;
     walk_us(units(64), units(128), effect, p.cu != nullptr, &waves);
     return waves;
+}
+// Chains of a walk, and workgroups that take one of their pieces in each round.
+inline long long walk_chains(const DeltaParams& p, int waves) {
+    return p.nseq * p.Hv * ((p.Dv + 16 * waves - 1) / (16 * waves));
+}
+inline long long walk_machines(const DeltaParams& p, int waves) {
+    return (walk_chains(p, waves) * p.pieces + p.rounds - 1) / p.rounds;
 }
 
 struct DeltaGradParams {

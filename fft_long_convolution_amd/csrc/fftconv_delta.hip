@@ -424,9 +424,9 @@ enum ScanMode { kEffect, kOutputs, kSaving };
 // operands wait for one another, and what else a wave did would add to it (with
 // the loads in the chain's waves: 23 sequences of 9001 tokens in f16 103 us, so
 // 82; on eight waves, which hide more of it, 205 and 199).  With 256 CUs taken a chunk of bf16 at D_k = 128 takes 6.2 us on eight waves and 4.7 on
-// four: 64 x 1024 tokens of 6 heads of 128 are 384 workgroups of eight, two
-// rounds of 16 chunks, 199 us, with what the backward pass reads 346; the matrix
-// cores are busy 20 % of the time.
+// four: 64 x 1024 tokens of 6 heads of 128 are 384 chains of 16 chunks, three
+// launches of 256 workgroups and 8 chunks, 60 us each, with what the backward
+// pass reads 110; the matrix cores are busy 20 % of the time.
 template <int IO, int DK, int W, int MODE>
 __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaParams p) {
     constexpr bool FULL = MODE != kEffect;
@@ -436,18 +436,26 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
     extern __shared__ uint4 lds[];
     const int vcols = (p.Dv + kCols - 1) / kCols;
     const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
-    const unsigned units = (unsigned)p.segs * p.Hv * cols;
-    unsigned id = xcd_unit(blockIdx.x, units);
-    if (id >= units) return;
+    const bool pieces = FULL && p.pieces > 1;
+    int sn = 0;                                          // segment of the sequence
+    unsigned id;
+    if (pieces) {
+        if (!piece_of(p, (unsigned)p.nseq * p.Hv * cols, &id, &sn)) return;
+    } else {
+        const unsigned units = (unsigned)p.segs * p.Hv * cols;
+        id = xcd_unit(blockIdx.x, units);
+        if (id >= units) return;
+    }
     int cb = (int)(id % cols);
     id /= cols;
     const int h = (int)(id % p.Hv);
-    const long long seg = id / p.Hv;
-    const long long seq = seq_of(p, (unsigned)seg, p.seg_chunks);
+    id /= p.Hv;
+    const long long seq = pieces ? id : seq_of(p, id, p.seg_chunks);
     const Span sp = span_of(p, seq);
     const int chunks = (sp.len + kChunk - 1) / kChunk;
-    // segment of the sequence
-    const int sn = (int)((unsigned)seg - seg_of(p, sp, (unsigned)seq, p.seg_chunks));
+    const unsigned seg0 = seg_of(p, sp, (unsigned)seq, p.seg_chunks);
+    if (!pieces) sn = (int)(id - seg0);
+    const long long seg = (long long)seg0 + sn;
     const long long first_ = (long long)sn * p.seg_chunks;
     if (sn < 0 || (sn != 0 && first_ >= chunks)) return;   // no such segment
     const int first = (int)first_;
@@ -469,7 +477,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
     {
         const float* s = nullptr;
         if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col : nullptr;
-        else if (FULL) s = p.seg_n + ((seg - 1) * p.Hv + h) * state + col;
+        else if (FULL) s = p.seg_n + ((pieces ? seq : seg - 1) * p.Hv + h) * state + col;
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -678,7 +686,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
     }
     if (!cok) return;
     float* d = nullptr;
-    if (FULL) d = p.fin && last == chunks ? p.fin + (seq * p.Hv + h) * state : nullptr;
+    if (FULL && last == chunks) d = p.fin ? p.fin + (seq * p.Hv + h) * state : nullptr;
+    else if (FULL) d = pieces ? p.seg_n + (seq * p.Hv + h) * state : nullptr;
     else if (matrix) d = p.seg_m + (seg * p.Hv + h) * p.Dk * (long long)p.Dk;
     else d = p.seg_n + (seg * p.Hv + h) * state;
     if (d) store_state<ST>((char*)d, width * 4, (uint32_t)(8 * g * width + col) * 4, p.Dk, S);
@@ -799,9 +808,13 @@ hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
     const int width = 16 * W;
     const int cols = (p.Dv + width - 1) / width +
                      (MODE == kEffect ? (p.Dk + width - 1) / width : 0);
-    const long long units = p.segs * p.Hv * cols;
-    hipLaunchKernelGGL((delta_scan_kernel<IO, DK, W, MODE>), dim3((unsigned)xcd_blocks(units)),
-                       dim3(64 * (W + kLoaders)), bytes, s, p);
+    const bool pieces = MODE != kEffect && p.pieces > 1;
+    const long long units = pieces ? walk_machines(p, W) : p.segs * p.Hv * cols;
+    DeltaParams r = p;
+    do {
+        hipLaunchKernelGGL((delta_scan_kernel<IO, DK, W, MODE>), dim3((unsigned)xcd_blocks(units)),
+                           dim3(64 * (W + kLoaders)), bytes, s, r);
+    } while (pieces && ++r.round < r.rounds);
     return hipGetLastError();
 }
 

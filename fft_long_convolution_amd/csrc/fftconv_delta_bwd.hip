@@ -32,8 +32,8 @@ struct RscanLds {
 // FULL false: a segment's effect on D alone, from the gradient of the final
 // state (the last segment of a sequence) or from 0, and in columns of their own
 // the matrix D is multiplied with (from the identity, without dO).  Bound as
-// the forward walk is: 64 x 1024 tokens of 6 heads of 128 in bf16 take 360 us,
-// 16 chunks in two rounds of workgroups, 0.7 GB of D and dY written.
+// the forward walk is: 64 x 1024 tokens of 6 heads of 128 in bf16 take three
+// launches of 111 us, 0.7 GB of D and dY written.
 template <int IO, int DK, int W, bool FULL>
 __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
@@ -42,18 +42,27 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     extern __shared__ uint4 lds[];
     const int vcols = (p.Dv + kCols - 1) / kCols;
     const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
-    const unsigned units = (unsigned)p.segs * p.Hv * cols;
-    unsigned id = xcd_unit(blockIdx.x, units);
-    if (id >= units) return;
+    const bool pieces = FULL && p.pieces > 1;
+    int sn = 0;                                          // segment of the sequence
+    unsigned id;
+    if (pieces) {
+        if (!piece_of(p, (unsigned)p.nseq * p.Hv * cols, &id, &sn)) return;
+    } else {
+        const unsigned units = (unsigned)p.segs * p.Hv * cols;
+        id = xcd_unit(blockIdx.x, units);
+        if (id >= units) return;
+    }
     int cb = (int)(id % cols);
     id /= cols;
     const int h = (int)(id % p.Hv);
-    const long long seg = id / p.Hv;
-    const long long seq = seq_of(p, (unsigned)seg, p.seg_chunks);
+    id /= p.Hv;
+    const long long seq = pieces ? id : seq_of(p, id, p.seg_chunks);
     const Span sp = span_of(p, seq);
     const int chunks = (sp.len + kChunk - 1) / kChunk;
-    // segment of the sequence
-    const int sn = (int)((unsigned)seg - seg_of(p, sp, (unsigned)seq, p.seg_chunks));
+    const unsigned seg0 = seg_of(p, sp, (unsigned)seq, p.seg_chunks);
+    if (pieces) sn = p.pieces - 1 - sn;                  // from the end
+    else sn = (int)(id - seg0);
+    const long long seg = (long long)seg0 + sn;
     const long long first_ = (long long)sn * p.seg_chunks;
     if (sn < 0 || (sn != 0 && first_ >= chunks)) return;   // no such segment
     const int first = (int)first_;
@@ -75,7 +84,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     {
         const float* s = nullptr;
         if (last == chunks) s = gp.dfin ? gp.dfin + (seq * p.Hv + h) * state + col : nullptr;
-        else if (FULL) s = p.seg_n + ((seg + 1) * p.Hv + h) * state + col;
+        else if (FULL) s = p.seg_n + ((pieces ? seq : seg + 1) * p.Hv + h) * state + col;
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
@@ -281,7 +290,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     }
     if (!cok) return;
     float* d = nullptr;
-    if (FULL) d = gp.dinit && sn == 0 ? gp.dinit + (seq * p.Hv + h) * state : nullptr;
+    if (FULL && sn == 0) d = gp.dinit ? gp.dinit + (seq * p.Hv + h) * state : nullptr;
+    else if (FULL) d = pieces ? p.seg_n + (seq * p.Hv + h) * state : nullptr;
     else if (matrix) d = p.seg_m + (seg * p.Hv + h) * p.Dk * (long long)p.Dk;
     else d = p.seg_n + (seg * p.Hv + h) * state;
     if (d) store_state<ST>((char*)d, width * 4, (uint32_t)(8 * g * width + col) * 4, p.Dk, D);
@@ -757,9 +767,13 @@ hipError_t rscan_launch(const DeltaGradParams& p, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int width = 16 * W;
     const int cols = (p.f.Dv + width - 1) / width + (FULL ? 0 : (p.f.Dk + width - 1) / width);
-    const long long units = p.f.segs * p.f.Hv * cols;
-    hipLaunchKernelGGL((delta_rscan_kernel<IO, DK, W, FULL>), dim3((unsigned)xcd_blocks(units)),
-                       dim3(64 * (W + kLoaders)), bytes, s, p);
+    const bool pieces = FULL && p.f.pieces > 1;
+    const long long units = pieces ? walk_machines(p.f, W) : p.f.segs * p.f.Hv * cols;
+    DeltaGradParams r = p;
+    do {
+        hipLaunchKernelGGL((delta_rscan_kernel<IO, DK, W, FULL>), dim3((unsigned)xcd_blocks(units)),
+                           dim3(64 * (W + kLoaders)), bytes, s, r);
+    } while (pieces && ++r.f.round < r.f.rounds);
     return hipGetLastError();
 }
 template <int IO, int DK, bool FULL>

@@ -724,4 +724,24 @@ __device__ __forceinline__ unsigned xcd_unit(unsigned block, unsigned n) {
 }
 inline long long xcd_blocks(long long n) { return (n + 7) / 8 * 8; }
 
+// The piece of a chain that a workgroup takes in the present round.  All pieces
+// in a row, `pieces` a chain, are dealt to the machines (a workgroup of every
+// round) `rounds` at a time, so no two of a chain meet in one round; its first
+// piece is the one of its earliest round.  False: nothing to do.
+__device__ __forceinline__ bool piece_of(const DeltaParams& p, unsigned chains, unsigned* chain,
+                                         int* piece) {
+    const unsigned n = p.pieces, rounds = p.rounds, round = p.round;
+    const unsigned machines = (chains * n + rounds - 1) / rounds;
+    const unsigned m = xcd_unit(blockIdx.x, machines);
+    if (m >= machines) return false;
+    const unsigned at = m * rounds + round;
+    *chain = at / n;
+    if (*chain >= chains) return false;
+    // its rounds are start .. start + n - 1, modulo `rounds`
+    const unsigned start = *chain * n % rounds, end = start + n;
+    const unsigned early = end > rounds ? end - rounds : 0;
+    *piece = (int)(round < early ? round : early + round - start);
+    return true;
+}
+
 }  // namespace fftconv

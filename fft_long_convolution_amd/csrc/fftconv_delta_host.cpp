@@ -204,13 +204,25 @@ size_t delta_slots(const fftconv_delta_desc* d) {
 // 128, 16 segments, 0.69 ms, uncut 2.1; 1 x 4096 x 8: 6, 0.12 ms, uncut 0.26;
 // 16 x 8192 x 6: uncut 0.65, in three 0.91.  With the gradients, fp32, 2 x 1501
 // tokens of 4 heads of 64: 8 segments, 132 us, uncut some 230.
-size_t delta_seg_chunks(const fftconv_delta_desc* d) {
+//
+// Where the chains are more than the CUs, a last round of few would take as
+// long as a full one.  So equal chains are cut into pieces, which launches of
+// at most one workgroup a CU take round by round (piece_of() in the kernels).  A
+// round costs some 7 us beside its chunks.  Of calls, bf16 and heads of 128, in
+// pieces and whole: 64 x 1024 tokens of 6 heads, 384 chains in halves, 264 and
+// 276 us (with gradients 1169 and 1208); 33 x 4096 of 8, 264 chains, 0.73 and
+// 0.88 ms (3.20 and 3.64); 10 x 8192 of 32 in f16, 320 chains, 2.37 and 3.21
+// (8.8 and 10.9).
+struct Cut {
+    size_t per;             // chunks of a segment or piece
+    int pieces, rounds, waves;
+};
+Cut delta_cut(const fftconv_delta_desc* d) {
     const size_t nch = (d->T + kChunk - 1) / kChunk;
     const size_t rows = d->sequences ? d->sequences : d->B;
     const size_t chunks = d->sequences ? nch : d->B * nch;
-    const size_t whole = nch + 1;           // one segment a sequence
+    Cut cut = {nch + 1, 1, 1, 0};           // one segment a sequence
     const size_t L = rows ? chunks / rows : 0;      // of a sequence, on average
-    if (L < 8) return whole;
     const bool packed = d->sequences != 0;
     const double heads = (double)rows * d->Hv;
     const size_t v64 = (d->Dv + 63) / 64, v128 = (d->Dv + 127) / 128;
@@ -219,10 +231,9 @@ size_t delta_seg_chunks(const fftconv_delta_desc* d) {
     const double chunk = d->dtype == FFTCONV_F32 ? 1.35 : 1.0;
     const double join = d->Dk <= 64 ? 2.5 : 7.0;
     double best = chunk * L * walk_us(heads * v64, heads * v128, false, packed, nullptr);
-    size_t per = whole;
     for (size_t n = 3; n <= 64 && n * 2 <= L; ++n) {
         const size_t p = (L + n - 1) / n;
-        if ((L + p - 1) / p != n) continue;
+        if (L < 8 || (L + p - 1) / p != n) continue;
         const double full = walk_us(heads * n * v64, heads * n * v128, false, packed, nullptr);
         const double effect = walk_us(heads * ((n - 1) * v64 + (n - 2) * k64),
                                       heads * ((n - 1) * v128 + (n - 2) * k128), true, packed,
@@ -230,10 +241,26 @@ size_t delta_seg_chunks(const fftconv_delta_desc* d) {
         const double t = chunk * p * (full + effect) + join * (n - 2) + 12.0;
         if (t < best) {
             best = t;
-            per = p;
+            cut.per = p;
         }
     }
-    return per;
+    for (int waves = 4; waves <= 8 && !packed; waves += 4) {
+        const double chains = heads * (waves == 4 ? v64 : v128);
+        if (chains <= 256 || chains > 1e6) continue;
+        const double us = walk_us(waves == 4 ? 256 : 1e9, waves == 4 ? 1e9 : 256, false, false,
+                                  nullptr);
+        for (size_t n = 2; n <= 16 && n <= L; ++n) {
+            const size_t p = (L + n - 1) / n;
+            if ((L + p - 1) / p != n) continue;
+            const size_t rounds = ((size_t)chains * n + 255) / 256;
+            const double t = rounds * (chunk * p * us + 7.0);
+            if (t < best) {
+                best = t;
+                cut = {p, (int)n, (int)rounds, waves};
+            }
+        }
+    }
+    return cut;
 }
 size_t delta_segs(const fftconv_delta_desc* d, size_t per) {
     const size_t nch = (d->T + kChunk - 1) / kChunk;
@@ -251,7 +278,9 @@ struct DeltaLayout {
     size_t backward() const { return states + us + seg_n + seg_m; }
 };
 bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
-    size_t n, x, y, per = delta_seg_chunks(d), m;
+    size_t n, x, y, m;
+    const Cut c = delta_cut(d);
+    const size_t per = c.per;
     if (!product(delta_slots(d), d->Hv, 1, 1, &n) || n > kMaxGrid) return false;
     // saved matrices: rows for the largest magnitudes, columns padded to 16
     const size_t cols = (d->Dv + 15) / 16 * 16, rows = d->Dk <= 64 ? 64 : 128;
@@ -260,8 +289,10 @@ bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
     const size_t segs = delta_segs(d, per);
     if (!product(segs, d->Hv, (d->Dv + d->Dk + 15) / 16, 1, &m) || m > kMaxGrid) return false;
     l->pack = n * (size_t)delta_pack_uint4(d->dtype) * 16;
-    l->seg_n = cut ? segs * d->Hv * d->Dk * d->Dv * 4 : 0;
-    l->seg_m = cut ? segs * d->Hv * d->Dk * d->Dk * 4 : 0;
+    // pieces: one state a chain, which each of them takes over from the last
+    const size_t held = c.pieces > 1 ? (d->sequences ? d->sequences : d->B) : segs;
+    l->seg_n = cut ? held * d->Hv * d->Dk * d->Dv * 4 : 0;
+    l->seg_m = cut && c.pieces == 1 ? segs * d->Hv * d->Dk * d->Dk * 4 : 0;
     l->bpack = n * (size_t)delta_back_pack_uint4() * 16;
     l->states = x * 4;
     l->us = y * 4;
@@ -336,12 +367,14 @@ fftconv_status delta_inputs(const fftconv_delta_desc* d, const DeltaArgs& a, Del
 
 void delta_place_segments(const fftconv_delta_desc* d, const DeltaLayout& l, char* at,
                           DeltaParams& p) {
-    p.seg_chunks = (int)delta_seg_chunks(d);
-    p.segs = (long long)delta_segs(d, (size_t)p.seg_chunks);
-    if (l.seg_m) {
-        p.seg_n = (float*)at;
-        p.seg_m = (float*)(at + l.seg_n);
-    }
+    const Cut c = delta_cut(d);
+    p.seg_chunks = (int)c.per;
+    p.segs = (long long)delta_segs(d, c.per);
+    p.pieces = c.pieces;
+    p.rounds = c.rounds;
+    p.waves = c.waves;
+    if (l.seg_n) p.seg_n = (float*)at;
+    if (l.seg_m) p.seg_m = (float*)(at + l.seg_n);
 }
 void delta_place_saved(const DeltaLayout& l, void* saved, DeltaParams& p) {
     char* f = (char*)saved;

@@ -305,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void qknorm_bwd_kernel(QkNormParams p) {
                 a = sum_row<LPR>(a);
                 d = sum_row<LPR>(d);
                 const float r = 1.f / sqrtf(p.c * a + p.eps);
-                const float e = p.c * r * r * r * d;
+                const float e = p.c * (r * d) * r * r;   // r^3 alone may overflow
                 if (ok[j]) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {

@@ -154,6 +154,25 @@ def test_many_heads_backward(shape, dtype):
     check_backward(ins, None, dtype, shape[4], shape[5])
 
 
+# chains in pieces: more of them than CUs, several chunks long
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(3, 700, 96, 96, 16, 128), (5, 1030, 60, 60, 8, 24),
+                                   (2, 777, 60, 60, 72, 264)], ids=str)
+def test_chains_in_pieces(shape, dtype):
+    for init in (False, True):
+        ins = delta_inputs(sum(shape), *shape, dtype, init=init, decay=0.001)
+        assert is_cut(rule(shape[4], shape[5], dtype), gpu(*ins), None)
+        check_forward(ins, None, dtype, shape[4], shape[5])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(3, 800, 96, 96, 16, 24), (1, 700, 2, 300, 8, 104)], ids=str)
+def test_chains_in_pieces_backward(shape, dtype):
+    ins = delta_inputs(sum(shape), *shape, dtype, decay=0.001)
+    assert is_cut(rule(shape[4], shape[5], dtype), gpu(*ins), None)
+    check_backward(ins, None, dtype, shape[4], shape[5])
+
+
 def test_tensors_over_4_gib():
     # two batch rows 2^32 bytes apart, tokens and heads with gaps
     B, T, H, D = 2, 70, 2, 64
