@@ -234,9 +234,11 @@ struct PrepLds {
 // of a chunk at D_k = 128 in bf16.  It is latency, of barriers, LDS and the
 // substitution's 16 steps, that other workgroups of the CU only partly fill:
 // 64 x 1024 tokens of 6 heads of 128 in bf16, 6144 workgroups, take 111 us
-// (0.33 GB), with the transposes for the backward pass 130 (0.45 GB).
+// (0.33 GB), with the transposes for the backward pass 130 (0.45 GB).  (The
+// bound of two workgroups a CU keeps the compiler from accumulating in registers
+// apart, which cost it 290 moves in 1460 instructions.)
 template <int IO, int DK>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
+__global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
     typedef PrepLds<IO, DK> L;
     constexpr int NT = L::NT, KB = DK / 32, NO = Io<IO>::NO;
     const unsigned units = (unsigned)p.slots * p.Hv, u = xcd_unit(blockIdx.x, units);
@@ -395,15 +397,15 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaParams p) {
 // ------------------------------------------------- the walk over the chunks
 
 // LDS of the walk, in uint4.  Operands of the next chunk are put into a second
-// buffer while the present one is worked on, if they are of 16 bits; there is
-// no room for two of fp32's.
+// buffer while the present one is worked on, where the CU's 160 KB hold two
+// (fp32's at D_k = 128 do not fit, but for K alone).
 template <int IO, int DK, bool FULL>
 struct ScanLds {
     static constexpr int kRows = Io<IO>::NA * 4 * (DK / 32) * 64;
     static constexpr int kPackU4 = FULL ? pack_uint4<IO>() : kPm;
     static constexpr int kK = 0, kQ = kRows, kPack = kQ + (FULL ? kRows : 0);
     static constexpr int kSize = kPack + kPackU4;
-    static constexpr int kBufs = IO == IO_F32 ? 1 : 2;
+    static constexpr int kBufs = 2 * kSize * 16 <= kLdsBytes ? 2 : 1;
     static constexpr int kBytes = kBufs * kSize * 16;
 };
 

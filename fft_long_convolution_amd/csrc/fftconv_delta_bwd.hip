@@ -23,7 +23,7 @@ template <int IO, int DK>
 struct RscanLds {
     static constexpr int kRows = Io<IO>::NA * 4 * (DK / 32) * 64;     // uint4
     static constexpr int kK = 0, kQ = kRows, kPack = 2 * kRows, kSize = kPack + kBackPack;
-    static constexpr int kBufs = IO == IO_F32 ? 1 : 2;
+    static constexpr int kBufs = 2 * kSize * 16 <= kLdsBytes ? 2 : 1;
     static constexpr int kBytes = kBufs * kSize * 16;
 };
 
@@ -301,8 +301,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
 
 // LDS of delta_grads_kernel, in uint4: a slice (32 columns, two terms) of S0, D,
 // U and dY; after the last one, in its place, the chunk's keys and queries and
-// two 64 x 64 matrices.  Two workgroups fit a CU where keys and queries are of
-// 16 bits, and their waits and work overlap.
+// two 64 x 64 matrices.  Where two workgroups fit a CU, their waits and work
+// overlap.
 template <int IO, int DK>
 struct GradsLds {
     static constexpr int ST = DK / 16, KB = DK / 32;
@@ -339,6 +339,16 @@ __device__ __forceinline__ void unpack_pieces(const P (&x)[2], bool ok0, bool ok
     for (int i = 0; i < 8; ++i) y[i] = (i < 4 ? ok0 : ok1) ? y[i] : 0.f;
 }
 
+// Workgroups on a CU: two where 256 registers a lane hold what it needs, nearly.
+// 32 x 1024 tokens of 6 heads of 64 with two and with one: 3 key heads, bf16,
+// 15 registers spilled, 126 and 171 us; 6 key heads, fp32, none, 138 and 206.
+// fp32 with shared heads would spill 38: 179 and 200 us there, but 37 and 30
+// for 96 workgroups, which have a CU each.
+template <int IO, int DK, bool GROUP>
+constexpr int grads_per_cu() {
+    return DK > 64 ? (GROUP || IO == IO_F32 ? 1 : 2) : (GROUP && IO == IO_F32 ? 1 : 2);
+}
+
 // One workgroup of four waves per chunk and key head.  A wave owns 16 tokens as
 // the columns of its products, R^T = S0 dO^T and so on.  So a lane has one
 // token: what belongs to it (decays, row sums) is a scalar of the lane, and
@@ -354,7 +364,7 @@ __device__ __forceinline__ void unpack_pieces(const P (&x)[2], bool ok0, bool ok
 // TB/s: its registers allow two workgroups a CU, which wait 40 % of the time,
 // the vector unit (the f16 terms) is busy 40 %, the matrix cores 15 %.
 template <int IO, int DK, bool GROUP>
-__global__ __launch_bounds__(256, GROUP || IO == IO_F32 ? 1 : 2)
+__global__ __launch_bounds__(256, (grads_per_cu<IO, DK, GROUP>()))
 void delta_grads_kernel(DeltaGradParams gp) {
     typedef GradsLds<IO, DK> L;
     typedef SliceRegs<IO, DK> Regs;

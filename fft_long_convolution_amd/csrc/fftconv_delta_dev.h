@@ -663,6 +663,7 @@ __device__ __forceinline__ void row4(const uint4* rows, int m, int c, int el, fl
 
 // A chunk's pack, in uint4: T (two terms), the factors below, P (NO terms).
 // For the backward pass: T^T, factors, P^T (two terms).
+constexpr int kLdsBytes = 160 * 1024;              // of a CU
 constexpr int kTerm = kTriTiles * 64;             // one term of a triangle
 constexpr int kDec = 2 * kTerm, kDecU4 = 128, kPm = kDec + kDecU4;
 template <int IO>
