@@ -701,9 +701,10 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
 // segments go from the last on, all but the first).  The eight waves of a
 // workgroup take 16 columns each, as in the walk, and share M through LDS, the
 // next one's loads in flight.  States of a sequence's end go through every M, so
-// here both are in three bf16 terms, 24 bits.  A step reads 64 KB of M and 64 KB
-// of N at heads of 128, and one CU's loads bound it: 7 us a step, 105 us for 16
-// segments of 4 x 32768 tokens of 4 heads; 2.3 at D_k = 64.
+// here both are in three bf16 terms, 24 bits.  A step at heads of 128 brings 64 KB
+// of M and 64 KB of N through one CU, splits M and reads it from LDS eight times,
+// one after the other for the most part: 7 us a step, 105 us for 16 segments of 4
+// x 32768 tokens of 4 heads; 2.3 a step at D_k = 64.
 template <int DK>
 struct JoinLds {
     static constexpr int kHalves = DK / 64;             // 64 rows of M each
