@@ -69,8 +69,7 @@ constexpr int kTriTiles = 6;               // 16 x 32 tiles of a 64 x 64 triangl
 // What a chunk and value head needs besides its tokens, in matrix-operand
 // order, one uint4 a lane: (I + A)^-1 in two f16 terms, the chunk's factors
 // (decays, beta, scales), the decayed scores P.
-int delta_pack_uint4(int io);              // of the forward pack
-int delta_back_pack_uint4();               // of its transposes
+int delta_pack_uint4();                    // the pack of its transposes alike
 
 // Time of a walk for each chunk of its longest chain, in us, by the number of
 // workgroups that take 64 or 128 columns (four or eight waves for the chain),

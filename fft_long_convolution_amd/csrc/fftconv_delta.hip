@@ -183,10 +183,9 @@ __device__ float invert_unit_lower(const float (*a)[kLd], float (*t)[kLd]) {
     return big;
 }
 
-// Writes a lower triangle from LDS as N terms in operand order: tile (m, kb),
+// Writes a lower triangle from LDS as two terms in operand order: tile (m, kb),
 // lane (g, c), element i holds [tile_row(m, c)][32 kb + 8 g + i].  Rows are
 // multiplied with their scale.
-template <int N>
 __device__ __forceinline__ void store_tri(const float (*t)[kLd], const float* scale, uint4* dst) {
     for (int i = threadIdx.x; i < kTriTiles * 64; i += blockDim.x) {
         const int tile = i >> 6, l = i & 63;
@@ -196,10 +195,10 @@ __device__ __forceinline__ void store_tri(const float (*t)[kLd], const float* sc
         const float* s = &t[row][32 * kb + 8 * (l >> 4)];
         const float4 a = *(const float4*)s, b = *(const float4*)(s + 4);
         const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint4 w[N];
-        split8h<N>(x, scale[row], w);
+        uint4 w[2];
+        split8h<2>(x, scale[row], w);
 #pragma unroll
-        for (int j = 0; j < N; ++j) dst[j * kTerm + i] = w[j];
+        for (int j = 0; j < 2; ++j) dst[j * kTerm + i] = w[j];
     }
 }
 // The same triangle's transpose, an upper one: tile (m, kb), kb >= m / 2.
@@ -240,7 +239,7 @@ struct PrepLds {
 template <int IO, int DK>
 __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
     typedef PrepLds<IO, DK> L;
-    constexpr int NT = L::NT, KB = DK / 32, NO = Io<IO>::NO;
+    constexpr int NT = L::NT, KB = DK / 32;
     const unsigned units = (unsigned)p.slots * p.Hv, u = xcd_unit(blockIdx.x, units);
     if (u >= units) return;
     const unsigned slot = u / p.Hv;
@@ -342,8 +341,8 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
         if (c == 0) rowp[row] = s.to;
     }
     __syncthreads();
-    uint4* pack = p.pack + id * pack_uint4<IO>();
-    uint4* back = p.bpack ? p.bpack + id * kBackPack : nullptr;
+    uint4* pack = p.pack + id * kPack;
+    uint4* back = p.bpack ? p.bpack + id * kPack : nullptr;
     if (wave == 0) {
         const Scale one = {1.f, 1.f};
         const Scale sk = IO == IO_F16 ? one : scale_to(__uint_as_float(big[0][lane]));
@@ -368,7 +367,7 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             ((float*)(pack + kDec))[kBackP + tile_row(wave, 4 * g4 + r)] = back_row[r];
-    store_tri<NO>(P, rowp, pack + kPm);
+    store_tri(P, rowp, pack + kPm);
     if (back) {
         __syncthreads();
         store_tri_transposed(P, colp, back + kPm);
@@ -390,7 +389,7 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
         }
     }
     __syncthreads();
-    store_tri<2>(P, rowp, pack);
+    store_tri(P, rowp, pack);
     if (back) store_tri_transposed(P, rowp, back);
 }
 
@@ -402,9 +401,9 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
 template <int IO, int DK, bool FULL>
 struct ScanLds {
     static constexpr int kRows = Io<IO>::NA * 4 * (DK / 32) * 64;
-    static constexpr int kPackU4 = FULL ? pack_uint4<IO>() : kPm;
-    static constexpr int kK = 0, kQ = kRows, kPack = kQ + (FULL ? kRows : 0);
-    static constexpr int kSize = kPack + kPackU4;
+    static constexpr int kPackU4 = FULL ? kPack : kPm;
+    static constexpr int kK = 0, kQ = kRows, kTri = kQ + (FULL ? kRows : 0);
+    static constexpr int kSize = kTri + kPackU4;
     static constexpr int kBufs = 2 * kSize * 16 <= kLdsBytes ? 2 : 1;
     static constexpr int kBytes = kBufs * kSize * 16;
 };
@@ -433,7 +432,7 @@ template <int IO, int DK, int W, int MODE>
 __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaParams p) {
     constexpr bool FULL = MODE != kEffect;
     typedef ScanLds<IO, DK, FULL> L;
-    constexpr int NA = Io<IO>::NA, NO = Io<IO>::NO, KB = DK / 32, ST = DK / 16;
+    constexpr int NA = Io<IO>::NA, KB = DK / 32, ST = DK / 16;
     constexpr int kCols = 16 * W, kB = Io<IO>::kB;
     extern __shared__ uint4 lds[];
     const int vcols = (p.Dv + kCols - 1) / kCols;
@@ -496,8 +495,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
                                     (long long)p.Hv * p.Dv);
     const uint32_t vlane = (uint32_t)(8 * g) * (uint32_t)tv.bytes + colv * kB;
     const uint32_t olane = (uint32_t)(8 * g) * (uint32_t)to.bytes + col * kB;
-    const uint4* pack = p.pack + (sp.slot0 * p.Hv + h) * pack_uint4<IO>();
-    const long long pack_step = (long long)p.Hv * pack_uint4<IO>();
+    const uint4* pack = p.pack + (sp.slot0 * p.Hv + h) * kPack;
+    const long long pack_step = (long long)p.Hv * kPack;
 
     if (__builtin_amdgcn_readfirstlane(wave) >= W) {
         RowTiles<IO, DK, kLoaders> rk, rq;
@@ -513,7 +512,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
         const auto store = [&](uint4* d) __attribute__((always_inline)) {
             rk.store(d + L::kK);
             if (FULL) rq.store(d + L::kQ);
-            rp.store(d + L::kPack);
+            rp.store(d + L::kTri);
         };
         if (first < last) {
             load(first);
@@ -549,8 +548,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
         const int n = sp.len - ch * kChunk;
         const int ahead = ch + 1 < last ? ch + 1 : ch;
         const uint4* now = lds + buf * L::kSize;
-        const float* fac = (const float*)(now + L::kPack + kDec);
-        const uint4* tri = now + L::kPack;
+        const float* fac = (const float*)(now + L::kTri + kDec);
+        const uint4* tri = now + L::kTri;
         const float big_s = max_column(S);
         const Scale ss = scale_to(big_s);
         if (MODE == kSaving && cok) save_columns<KB>(p.states, ci, p.Dv, col, S, big_s);
@@ -571,7 +570,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
             uint4 st[2];
             split_acc<2>(S[2 * kb], S[2 * kb + 1], ss.to, st);
             mma_tiles(a, st, X);
-            if (FULL) mma_tiles(q, leading<NO>(st), O);
+            if (FULL) mma_tiles(q, st, O);
         }
         // X = beta o (V - e^G o K S);  O = scale e^G o Q S
 #pragma unroll
@@ -624,15 +623,15 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
             for (int m = 0; m < 4; ++m) PU[m] = dfloat4{0, 0, 0, 0};
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                uint4 ut[NO];
-                split_acc<NO>(U[2 * kb], U[2 * kb + 1], su.to, ut);
+                uint4 ut[2];
+                split_acc<2>(U[2 * kb], U[2 * kb + 1], su.to, ut);
 #pragma unroll
                 for (int m0 = 2 * kb; m0 < 4; m0 += 2) {
-                    uint4 a[2][NO];
+                    uint4 a[2][2];
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int i = 0; i < NO; ++i)
+                        for (int i = 0; i < 2; ++i)
                             a[m][i] = tri[kPm + i * kTerm + tri_tile(m0 + m, kb) * 64 + lane];
                     mma_tiles(a, ut, *(dfloat4 (*)[2])&PU[m0]);
                 }
@@ -860,11 +859,7 @@ hipError_t prep_io(const DeltaParams& p, hipStream_t s) {
 
 }  // namespace
 
-int delta_pack_uint4(int io) {
-    return io == IO_F32 ? pack_uint4<IO_F32>()
-           : io == IO_F16 ? pack_uint4<IO_F16>() : pack_uint4<IO_BF16>();
-}
-int delta_back_pack_uint4() { return kBackPack; }
+int delta_pack_uint4() { return kPack; }
 
 hipError_t launch_delta_step(int io, const DeltaStepParams& p, hipStream_t s) {
     switch (io) {

@@ -22,7 +22,7 @@ namespace {
 template <int IO, int DK>
 struct RscanLds {
     static constexpr int kRows = Io<IO>::NA * 4 * (DK / 32) * 64;     // uint4
-    static constexpr int kK = 0, kQ = kRows, kPack = 2 * kRows, kSize = kPack + kBackPack;
+    static constexpr int kK = 0, kQ = kRows, kTri = 2 * kRows, kSize = kTri + kPack;
     static constexpr int kBufs = 2 * kSize * 16 <= kLdsBytes ? 2 : 1;
     static constexpr int kBytes = kBufs * kSize * 16;
 };
@@ -100,11 +100,11 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     const Tokens to = tokens_of<IO>(gp.dout, ofirst, (long long)p.Hv * p.Dv);
     const Tokens tv = tokens_of<IO>(gp.dv, ofirst, (long long)p.Hv * p.Dv);
     const uint32_t olane = (uint32_t)(8 * g) * (uint32_t)to.bytes + colv * kB;
-    const uint4* pack = p.bpack + (sp.slot0 * p.Hv + h) * kBackPack;
-    const long long pack_step = (long long)p.Hv * kBackPack;
+    const uint4* pack = p.bpack + (sp.slot0 * p.Hv + h) * kPack;
+    const long long pack_step = (long long)p.Hv * kPack;
     if (__builtin_amdgcn_readfirstlane(wave) >= W) {
         RowTiles<IO, DK, kLoaders> rk, rq;
-        Block<kBackPack / 64, kLoaders> rp;
+        Block<kPack / 64, kLoaders> rp;
         const auto load = [&](int ch) __attribute__((always_inline)) {
             const int n = sp.len - ch * kChunk;
             const uint4* next_pack = pack + ch * pack_step;
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
         const auto store = [&](uint4* d) __attribute__((always_inline)) {
             rk.store(d + L::kK);
             rq.store(d + L::kQ);
-            rp.store(d + L::kPack);
+            rp.store(d + L::kTri);
         };
         if (first < last) {
             load(last - 1);
@@ -151,8 +151,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     for (int ch = last - 1; ch >= first; --ch) {
         const long long ci = (sp.slot0 + ch) * p.Hv + h;
         const uint4* now = lds + buf * L::kSize;
-        const float* fac = (const float*)(now + L::kPack + kDec);
-        const uint4* tri = now + L::kPack;
+        const float* fac = (const float*)(now + L::kTri + kDec);
+        const uint4* tri = now + L::kTri;
         dfloat4 dO[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) dO[m] = dN[m];
@@ -369,7 +369,7 @@ void delta_grads_kernel(DeltaGradParams gp) {
     typedef GradsLds<IO, DK> L;
     typedef SliceRegs<IO, DK> Regs;
     const DeltaParams& p = gp.f;
-    constexpr int NA = Io<IO>::NA, NO = Io<IO>::NO, KB = DK / 32, ST = L::ST, kB = Io<IO>::kB;
+    constexpr int NA = Io<IO>::NA, KB = DK / 32, ST = L::ST, kB = Io<IO>::kB;
     constexpr int NS = Regs::NS, GT = GROUP ? ST : 1;
     extern __shared__ uint4 lds[];
     __shared__ double G[kChunk];
@@ -395,7 +395,7 @@ void delta_grads_kernel(DeltaGradParams gp) {
     float (*F)[kLd] = (float (*)[kLd])(lds + L::kF);     // [i][j]: (E + E^T)_ij / rk_j
     const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2], p.ks[1]);
     const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2], p.qs[1]);
-    const float* fac = (const float*)(p.bpack + (slot * p.Hv + hk * p.group) * kBackPack + kDec);
+    const float* fac = (const float*)(p.bpack + (slot * p.Hv + hk * p.group) * kPack + kDec);
 
     dfloat4 dQ[GT], dK[GT];
 #pragma unroll
@@ -719,12 +719,12 @@ void delta_grads_kernel(DeltaGradParams gp) {
         }
         const Scale sw = scale_to(max_column(Dp)), st = scale_to(max_column(wt)),
                     sf = scale_to(max_column(ft));
-        uint4 wb[2][NO], tb_[2][NO], fb[2][NO];
+        uint4 wb[2][2], tb_[2][2], fb[2][2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            split_acc<NO>(Dp[2 * tb], Dp[2 * tb + 1], sw.to, wb[tb]);
-            split_acc<NO>(wt[2 * tb], wt[2 * tb + 1], st.to, tb_[tb]);
-            split_acc<NO>(ft[2 * tb], ft[2 * tb + 1], sf.to, fb[tb]);
+            split_acc<2>(Dp[2 * tb], Dp[2 * tb + 1], sw.to, wb[tb]);
+            split_acc<2>(wt[2 * tb], wt[2 * tb + 1], st.to, tb_[tb]);
+            split_acc<2>(ft[2 * tb], ft[2 * tb + 1], sf.to, fb[tb]);
         }
 #pragma unroll
         for (int t = 0; t < ST; ++t) {

@@ -33,12 +33,13 @@ typedef float dfloat4 __attribute__((ext_vector_type(4)));
 // of HIP's, a struct, end up in scratch memory here.
 typedef uint32_t du4 __attribute__((ext_vector_type(4)));
 
-// Terms: NA of an operand of the I/O type (16-bit values are exact in one),
-// NO of P, S and U where only outputs follow.  One f16 term, off by 2^-12, is
-// enough for a bf16 output, rounded by 2^-9; the others take both.
+// Terms: NA of an operand of the I/O type, whose 16-bit values are exact in one.
+// All others take two, also where only outputs of 16 bits follow: an output is
+// a sum whose terms may cancel, so an operand's rounding has to be small
+// beside the output's after they did.
 template <int IO>
 struct Io {
-    static constexpr int NA = IO == IO_F32 ? 2 : 1, NO = IO == IO_BF16 ? 1 : 2;
+    static constexpr int NA = IO == IO_F32 ? 2 : 1;
     static constexpr int kB = IO == IO_F32 ? 4 : 2;
 };
 
@@ -259,11 +260,6 @@ __device__ __forceinline__ dfloat4 mma_prod(const uint4 (&a)[NA], const uint4 (&
             if (j >= 0 && j < NB) c = mma_h(a[i], b[j], c);
         }
     return c;
-}
-// the first N of the terms
-template <int N>
-__device__ __forceinline__ const uint4 (&leading(const uint4 (&t)[2]))[N] {
-    return *(const uint4 (*)[N])&t;
 }
 
 // A power of two and its inverse.  Both are normal numbers for every largest
@@ -661,14 +657,12 @@ __device__ __forceinline__ void row4(const uint4* rows, int m, int c, int el, fl
     }
 }
 
-// A chunk's pack, in uint4: T (two terms), the factors below, P (NO terms).
-// For the backward pass: T^T, factors, P^T (two terms).
+// A chunk's pack, in uint4: T (two terms), the factors below, P (two terms).
+// For the backward pass: T^T, factors, P^T.
 constexpr int kLdsBytes = 160 * 1024;              // of a CU
 constexpr int kTerm = kTriTiles * 64;             // one term of a triangle
 constexpr int kDec = 2 * kTerm, kDecU4 = 128, kPm = kDec + kDecU4;
-template <int IO>
-constexpr int pack_uint4() { return kPm + Io<IO>::NO * kTerm; }
-constexpr int kBackPack = kPm + 2 * kTerm;
+constexpr int kPack = kPm + 2 * kTerm;
 // Factors of the chunk's tokens, 64 floats each.  With rk, rq the scales of
 // the rows of K and Q and G, beta as in the formulas:
 enum Factor {

@@ -288,12 +288,12 @@ bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
     const bool cut = per <= (d->T + kChunk - 1) / kChunk;
     const size_t segs = delta_segs(d, per);
     if (!product(segs, d->Hv, (d->Dv + d->Dk + 15) / 16, 1, &m) || m > kMaxGrid) return false;
-    l->pack = n * (size_t)delta_pack_uint4(d->dtype) * 16;
+    l->pack = n * (size_t)delta_pack_uint4() * 16;
     // pieces: one state a chain, which each of them takes over from the last
     const size_t held = c.pieces > 1 ? (d->sequences ? d->sequences : d->B) : segs;
     l->seg_n = cut ? held * d->Hv * d->Dk * d->Dv * 4 : 0;
     l->seg_m = cut && c.pieces == 1 ? segs * d->Hv * d->Dk * d->Dk * 4 : 0;
-    l->bpack = n * (size_t)delta_back_pack_uint4() * 16;
+    l->bpack = n * (size_t)delta_pack_uint4() * 16;
     l->states = x * 4;
     l->us = y * 4;
     return true;

@@ -508,10 +508,12 @@ typedef struct fftconv_delta_desc {
  *  workspace: fftconv_delta_workspace_bytes(desc) bytes.
  * States, gates and sums are fp32 or wider whatever the I/O type.  fp32
  * operands of the matrix products are split into two f16 terms, 22 bits, with a
- * scale for each row or column; the queries' products with bf16 outputs take
- * the leading term.  Long sequences of few heads are cut into segments, joined
- * in another order of the same sums: results do not depend on anything but the
- * descriptor and the inputs, and equal calls give equal bits. */
+ * scale for each row or column (in the gradients of a chunk, for each state
+ * and each matrix of its tokens: a value 2^-16 of the largest has all its
+ * bits); outputs are rounded to their type once.  Long sequences of few heads are
+ * cut into segments, joined in another order of the same sums: results do not
+ * depend on anything but the descriptor and the inputs, and equal calls give
+ * equal bits. */
 fftconv_status fftconv_delta_forward(const fftconv_delta_desc *desc, const void *q,
                                      const void *k, const void *v, const float *g,
                                      const float *beta, const long long *cu_seqlens,
