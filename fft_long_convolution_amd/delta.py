@@ -136,7 +136,14 @@ class _Op:
         """The call's tensors in a layout the library takes, its descriptor
         and what else follows from the sizes: from `kind` (a method that
         checks and describes) where no such call was seen before.  Misaligned
-        tensors are copied."""
+        tensors are copied first: a copy has strides of its own, and the
+        descriptor holds those of the tensor that goes in."""
+        ptrs = [0 if t is None else t.data_ptr() for t in ts]
+        for i, x in enumerate(ptrs):
+            if x & 15 and (x & 7 or ts[i].dtype != torch.int64):
+                ts = list(ts)
+                ts[i] = ts[i].clone(memory_format=torch.contiguous_format)
+                ptrs[i] = ts[i].data_ptr()
         key = (kind, self._settings, _layout(ts))
         found = self._known.get(key)
         if found is None:
@@ -145,12 +152,7 @@ class _Op:
                 self._known.clear()
             # tensors that had to be copied have another layout now
             self._known[(kind, self._settings, _layout(ts))] = found
-        ptrs = [0 if t is None else t.data_ptr() for t in ts]
-        for i, x in enumerate(ptrs):
-            if x & 15 and (x & 7 or ts[i].dtype != torch.int64):
-                ts = list(ts)
-                ts[i] = ts[i].clone()
-                ptrs[i] = ts[i].data_ptr()
+            ptrs = [0 if t is None else t.data_ptr() for t in ts]
         return found, ts, ptrs
 
     def _first(self, q, dims):
