@@ -440,7 +440,10 @@ fftconv_status fftconv_qknorm_backward(const fftconv_qknorm_desc* d, const void*
     const Range out[] = {{dq, qn}, {dk, kn}, {dq_weight, d->D * 4}, {dk_weight, d->D * 4},
                          {workspace, need}};
     if (!outputs_clear(out, more)) return FFTCONV_ERR_INVALID_ARG;
-    if (!(qn + kn) && !need) return FFTCONV_OK;
+    if (!(qn + kn)) {
+        if (!need) return FFTCONV_OK;
+        p.tokens = 0;      // no heads: the weights' gradients are 0, no token is read
+    }
     p.dqo = dq_out;
     p.dko = dk_out;
     p.dq = dq;

@@ -196,3 +196,20 @@ def test_refusals():
     with pytest.raises(FFTConvError) as e:
         QKNorm(12).forward(y, y)
     assert e.value.status == 2
+
+
+def test_backward_without_heads_reads_no_token():
+    # the weights' gradients are sums over no heads; positions and tables may be missing
+    import ctypes
+    from fft_long_convolution_amd import delta
+    for B, T in ((3, 5), (0, 5)):
+        d = delta.QKNormDesc(2, B, T, 0, 0, 64, 32, 0, 0, 1e-6, 100, delta._LL3(0, 64, 64),
+                             delta._LL3(0, 64, 64))
+        ref, L = ctypes.byref(d), delta.lib()
+        ws = torch.empty(L.fftconv_qknorm_workspace_bytes(ref), dtype=torch.uint8, device="cuda")
+        dw = torch.full((2, 64), 7.0, device="cuda")
+        status = L.fftconv_qknorm_backward(ref, *[None] * 11, dw[0].data_ptr(), dw[1].data_ptr(),
+                                           ws.data_ptr(), ws.numel(),
+                                           torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        assert torch.equal(dw, torch.zeros_like(dw))
