@@ -258,10 +258,14 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
     __shared__ double G[kChunk];
     __shared__ float bet[kChunk], rowp[kChunk], colp[kChunk];
     __shared__ uint32_t big[4][kChunk];      // largest of K, Q, columns of P, T
+    __shared__ float spoil[kChunk];          // NaN for a token with a score that is not finite
+    __shared__ int spoilt;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g4 = lane >> 4, rslot = 16 * g4 + (c ^ (4 * g4));
     const int hk = h / p.group;
     big[wave][lane] = 0;
+    if (wave == 1) spoil[lane] = 0.f;
+    if (threadIdx.x == 0) spoilt = 0;
     RowTiles<IO, DK, 4> rk, rq;
     rk.load(tokens_of<IO>(p.k, sp.b * p.ks[0] + tok * p.ks[1] + hk * p.ks[2], p.ks[1]), 0, n, p.Dk);
     rq.load(tokens_of<IO>(p.q, sp.b * p.qs[0] + tok * p.qs[1] + hk * p.qs[2], p.qs[1]), 0, n, p.Dk);
@@ -319,7 +323,15 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
                 const int row = tile_row(wave, 4 * g4 + r);
                 const float gam = row >= col ? decay(G[row] - G[col]) : 0.f;
                 const float pv = row >= col ? p.scale * gam * qk[j][r] : 0.f;
-                A[row][col] = row > col ? bet[row] * gam * kk[j][r] : 0.f;
+                float av = row > col ? bet[row] * gam * kk[j][r] : 0.f;
+                if (!finite(av)) {
+                    // The inverse would spread it over its zeros, to tokens
+                    // before this one.  The token itself is lost, by its beta.
+                    av = 0.f;
+                    spoil[row] = __uint_as_float(0x7fc00000u);
+                    spoilt = 1;
+                }
+                A[row][col] = av;
                 P[row][col] = pv;
                 qk[j][r] = fabsf(pv);
                 big_p = fmaxf(big_p, qk[j][r]);
@@ -356,7 +368,7 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
                 f[kDecayK + lane] = eg * sk.back;
                 f[kDecayQ + lane] = p.scale * eg * sq.back;
                 f[kEndK + lane] = ee * sk.back;
-                f[kBeta + lane] = bet[lane];
+                f[kBeta + lane] = bet[lane] + spoil[lane];
                 f[kScaleK + lane] = sk.to;
                 f[kScaleQ + lane] = sq.to;
                 if (lane == 0) f[kDecayAll] = decay(last);
@@ -385,7 +397,8 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
         if (threadIdx.x < 64) rowp[threadIdx.x] = s.to;
         if (threadIdx.x == 0) {
             ((float*)(pack + kDec))[kBackT] = s.back;
-            if (back) ((float*)(back + kDec))[kBackT] = s.back;
+            // backward a lost token's gradients are those of all before it
+            if (back) ((float*)(back + kDec))[kBackT] = spoilt ? __uint_as_float(0x7fc00000u) : s.back;
         }
     }
     __syncthreads();
@@ -415,56 +428,21 @@ struct ScanLds {
 // state; kSaving: and what the backward pass reads.
 enum ScanMode { kEffect, kOutputs, kSaving };
 
-// A wave owns 16 columns of the state: its accumulators hold S (Dk x 16), and
-// every product of the chunk, K S, T X, P U, K^T U, takes the last one's
-// accumulators as its B operand, so the chain of a chunk has no exchange and
-// no barrier of its own.  The W waves of a workgroup share the operands that
-// do not depend on the state (K, Q, T, P) through LDS, K^T being K read
-// transposed; four further waves bring the next chunk's, in step by a barrier a
-// chunk.  The chain is latency: a step's vector work, its products and their
-// operands wait for one another, and what else a wave did would add to it (with
-// the loads in the chain's waves: 23 sequences of 9001 tokens in f16 103 us, so
-// 82; on eight waves, which hide more of it, 205 and 199).  With 256 CUs taken a chunk of bf16 at D_k = 128 takes 6.2 us on eight waves and 4.7 on
-// four: 64 x 1024 tokens of 6 heads of 128 are 384 chains of 16 chunks, three
-// launches of 256 workgroups and 8 chunks, 60 us each, with what the backward
-// pass reads 110; the matrix cores are busy 20 % of the time.
-template <int IO, int DK, int W, int MODE>
-__global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaParams p) {
+// A workgroup's walk over the chunks of one segment.  CAREFUL: tokens are kept from
+// values that are not finite in the ones behind them.  Such a value meets the
+// zeros of T and P on its way through a chunk and takes tokens before it along;
+// it also stays in the state, so the plain walk needs no test in its steps.  True,
+// and nothing stored of the state, where one of the workgroup's states ends so.
+template <int IO, int DK, int W, int MODE, bool CAREFUL>
+__device__ __forceinline__ bool delta_walk(const DeltaParams& p, const Span& sp, long long seq,
+                                           long long seg, int sn, int h, int cb, bool matrix,
+                                           bool pieces, uint4* lds) {
     constexpr bool FULL = MODE != kEffect;
     typedef ScanLds<IO, DK, FULL> L;
     constexpr int NA = Io<IO>::NA, KB = DK / 32, ST = DK / 16;
     constexpr int kCols = 16 * W, kB = Io<IO>::kB;
-    extern __shared__ uint4 lds[];
-    const int vcols = (p.Dv + kCols - 1) / kCols;
-    const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
-    const bool pieces = FULL && p.pieces > 1;
-    int sn = 0;                                          // segment of the sequence
-    unsigned id;
-    if (pieces) {
-        if (!piece_of(p, (unsigned)p.nseq * p.Hv * cols, &id, &sn)) return;
-    } else {
-        const unsigned units = (unsigned)p.segs * p.Hv * cols;
-        id = xcd_unit(blockIdx.x, units);
-        if (id >= units) return;
-    }
-    int cb = (int)(id % cols);
-    id /= cols;
-    const int h = (int)(id % p.Hv);
-    id /= p.Hv;
-    const long long seq = pieces ? id : seq_of(p, id, p.seg_chunks);
-    const Span sp = span_of(p, seq);
-    const int chunks = (sp.len + kChunk - 1) / kChunk;
-    const unsigned seg0 = seg_of(p, sp, (unsigned)seq, p.seg_chunks);
-    if (!pieces) sn = (int)(id - seg0);
-    const long long seg = (long long)seg0 + sn;
-    const long long first_ = (long long)sn * p.seg_chunks;
-    if (sn < 0 || (sn != 0 && first_ >= chunks)) return;   // no such segment
-    const int first = (int)first_;
+    const int chunks = (sp.len + kChunk - 1) / kChunk, first = sn * p.seg_chunks;
     const int last = chunks - first > p.seg_chunks ? first + p.seg_chunks : chunks;
-    if (!FULL && (last == chunks || (sn == 0 && cb >= vcols))) return;
-    const bool matrix = !FULL && cb >= vcols;
-    if (matrix) cb -= vcols;
-
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = lane & 15, g = lane >> 4;
     const int slot = 16 * g + (c ^ (4 * g));             // of a row operand
@@ -474,20 +452,6 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
     const int colv = cok ? col : 0;                      // to read from
     const int hk = h / p.group;
     const long long state = p.Dk * (long long)p.Dv;
-    dfloat4 S[ST];
-    {
-        const float* s = nullptr;
-        if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col : nullptr;
-        else if (FULL) s = p.seg_n + ((pieces ? seq : seg - 1) * p.Hv + h) * state + col;
-#pragma unroll
-        for (int t = 0; t < ST; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = tile_row(t, 4 * g + r);
-                S[t][r] = matrix ? (row == col ? 1.f : 0.f)
-                                 : (s && cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f);
-            }
-    }
     const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2], p.ks[1]);
     const Tokens tq = tokens_of<IO>(p.q, sp.b * p.qs[0] + sp.t0 * p.qs[1] + hk * p.qs[2], p.qs[1]);
     const Tokens tv = tokens_of<IO>(p.v, sp.b * p.vs[0] + sp.t0 * p.vs[1] + h * p.vs[2], p.vs[1]);
@@ -531,9 +495,23 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
                 __syncthreads();
             }
         }
-        return;
+        return FULL && !CAREFUL && __syncthreads_or(0);
     }
 
+    dfloat4 S[ST];
+    {
+        const float* s = nullptr;
+        if (sn == 0) s = p.init ? p.init + (seq * p.Hv + h) * state + col : nullptr;
+        else if (FULL) s = p.seg_n + ((pieces ? seq : seg - 1) * p.Hv + h) * state + col;
+#pragma unroll
+        for (int t = 0; t < ST; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = tile_row(t, 4 * g + r);
+                S[t][r] = matrix ? (row == col ? 1.f : 0.f)
+                                 : (s && cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f);
+            }
+    }
     dfloat4 v[4];
     const auto load_v = [&](int ch) __attribute__((always_inline)) {
         if (!matrix) load_column<IO>(tv, ch * kChunk, vlane, sp.len - ch * kChunk, v);
@@ -588,8 +566,34 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
             }
         }
         load_v(ahead);
+        // Tokens of the lane's column from the first value that is not finite
+        // on: their outputs and the state become NaN, and x 0, for what follows
+        // multiplies it with the zeros of T and P.
+        const auto lose = [&](dfloat4 (&x)[4]) __attribute__((always_inline)) {
+            const float nan = __uint_as_float(0x7fc00000u);
+            int at = kChunk;
+#pragma unroll
+            for (int m = 3; m >= 0; --m)
+#pragma unroll
+                for (int r = 3; r >= 0; --r)
+                    if (!finite(x[m][r])) at = tile_row(m, 4 * g + r);
+            at = min(at, __shfl_xor(at, 16));
+            at = min(at, __shfl_xor(at, 32));
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (tile_row(m, 4 * g + r) >= at) {
+                        x[m][r] = 0.f;
+                        O[m][r] = nan;
+                    }
+            if (at < kChunk)
+#pragma unroll
+                for (int t = 0; t < ST; ++t) S[t] = dfloat4{nan, nan, nan, nan};
+        };
         // U = T X
         dfloat4 U[4];
+        if (CAREFUL) lose(X);
         const Scale sx = scale_to(max_column(X));
 #pragma unroll
         for (int m = 0; m < 4; ++m) U[m] = dfloat4{0, 0, 0, 0};
@@ -614,8 +618,12 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
             for (int m = 0; m < 4; ++m) U[m] *= back;
         }
         if (FULL) {
+            if (CAREFUL) lose(U);
             const float big_u = max_column(U);
-            if (MODE == kSaving && cok) save_columns<2>(p.us, ci, p.Dv, col, U, big_u);
+            // (an infinite largest value: a chunk with lost tokens has no gradients)
+            if (MODE == kSaving && cok)
+                save_columns<2>(p.us, ci, p.Dv, col, U,
+                                CAREFUL && S[0][0] != S[0][0] ? INFINITY : big_u);
             // O += P U
             const Scale su = scale_to(big_u);
             dfloat4 PU[4];
@@ -685,13 +693,69 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
         if (L::kBufs == 2) buf ^= 1;
         else __syncthreads();
     }
-    if (!cok) return;
+    if (FULL && !CAREFUL && __syncthreads_or(first < last && !finite(S[0][0]))) return true;
+    if (!cok) return false;
     float* d = nullptr;
     if (FULL && last == chunks) d = p.fin ? p.fin + (seq * p.Hv + h) * state : nullptr;
     else if (FULL) d = pieces ? p.seg_n + (seq * p.Hv + h) * state : nullptr;
     else if (matrix) d = p.seg_m + (seg * p.Hv + h) * p.Dk * (long long)p.Dk;
     else d = p.seg_n + (seg * p.Hv + h) * state;
     if (d) store_state<ST>((char*)d, width * 4, (uint32_t)(8 * g * width + col) * 4, p.Dk, S);
+    return false;
+}
+
+// A wave owns 16 columns of the state: its accumulators hold S (Dk x 16), and
+// every product of the chunk, K S, T X, P U, K^T U, takes the last one's
+// accumulators as its B operand, so the chain of a chunk has no exchange and
+// no barrier of its own.  The W waves of a workgroup share the operands that
+// do not depend on the state (K, Q, T, P) through LDS, K^T being K read
+// transposed; four further waves bring the next chunk's, in step by a barrier a
+// chunk.  The chain is latency: a step's vector work, its products and their
+// operands wait for one another, and what else a wave did would add to it (with
+// the loads in the chain's waves: 23 sequences of 9001 tokens in f16 103 us, so
+// 82; on eight waves, which hide more of it, 205 and 199).  With 256 CUs taken a chunk of bf16 at D_k = 128 takes 6.2 us on eight waves and 4.7 on
+// four: 64 x 1024 tokens of 6 heads of 128 are 384 chains of 16 chunks, three
+// launches of 256 workgroups and 8 chunks, 60 us each, with what the backward
+// pass reads 110; the matrix cores are busy 20 % of the time.
+template <int IO, int DK, int W, int MODE>
+__global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaParams p) {
+    constexpr bool FULL = MODE != kEffect;
+    constexpr int kCols = 16 * W;
+    extern __shared__ uint4 lds[];
+    const int vcols = (p.Dv + kCols - 1) / kCols;
+    const int cols = vcols + (FULL ? 0 : (p.Dk + kCols - 1) / kCols);
+    const bool pieces = FULL && p.pieces > 1;
+    int sn = 0;                                          // segment of the sequence
+    unsigned id;
+    if (pieces) {
+        if (!piece_of(p, (unsigned)p.nseq * p.Hv * cols, &id, &sn)) return;
+    } else {
+        const unsigned units = (unsigned)p.segs * p.Hv * cols;
+        id = xcd_unit(blockIdx.x, units);
+        if (id >= units) return;
+    }
+    int cb = (int)(id % cols);
+    id /= cols;
+    const int h = (int)(id % p.Hv);
+    id /= p.Hv;
+    const long long seq = pieces ? id : seq_of(p, id, p.seg_chunks);
+    const Span sp = span_of(p, seq);
+    const int chunks = (sp.len + kChunk - 1) / kChunk;
+    const unsigned seg0 = seg_of(p, sp, (unsigned)seq, p.seg_chunks);
+    if (!pieces) sn = (int)(id - seg0);
+    const long long seg = (long long)seg0 + sn;
+    const long long first_ = (long long)sn * p.seg_chunks;
+    if (sn < 0 || (sn != 0 && first_ >= chunks)) return;   // no such segment
+    const int first = (int)first_;
+    const int last = chunks - first > p.seg_chunks ? first + p.seg_chunks : chunks;
+    if (!FULL && (last == chunks || (sn == 0 && cb >= vcols))) return;
+    const bool matrix = !FULL && cb >= vcols;
+    if (matrix) cb -= vcols;
+
+    const bool lost =
+        delta_walk<IO, DK, W, MODE, false>(p, sp, seq, seg, sn, h, cb, matrix, pieces, lds);
+    if constexpr (FULL)
+        if (lost) delta_walk<IO, DK, W, MODE, true>(p, sp, seq, seg, sn, h, cb, false, pieces, lds);
 }
 
 // Joins the segments of a sequence: with N the last state of a segment from 0

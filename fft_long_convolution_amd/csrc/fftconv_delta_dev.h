@@ -262,14 +262,15 @@ __device__ __forceinline__ dfloat4 mma_prod(const uint4 (&a)[NA], const uint4 (&
     return c;
 }
 
-// A power of two and its inverse.  Both are normal numbers for every largest
-// value, 0, infinity and NaN (which stays what it is) among them.
+// A power of two and its inverse, both normal numbers.  Where the largest value
+// is not finite the others would vanish beside it, so the inverse is NaN: what
+// such a row or column is part of never looks like a result.
 struct Scale { float to, back; };
 __device__ __forceinline__ Scale scale_to(float largest) {
     int e = (int)(__float_as_uint(largest) >> 23) & 255;
-    e = e < 28 ? 28 : e > 240 ? 240 : e;
+    e = e < 28 ? 28 : e;
     return {__uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23),
-            __uint_as_float((uint32_t)(e - 14) << 23)};
+            e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(e - 14) << 23)};
 }
 // Reductions in the vector unit; a shuffle through LDS would take some 100
 // cycles a step.  All-reduce over the 16 lanes of a group, by rotations:
@@ -298,23 +299,29 @@ __device__ __forceinline__ float sum_groups(float a) {
                                                     false);
     return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
+// The larger magnitude; NaN where one of them is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    return __builtin_elementwise_maximum(a, b);
+}
+__device__ __forceinline__ bool finite(float a) { return fabsf(a) <= 3.402823466e38f; }
 // the larger value of the lane and of the other groups of 16 at its place
 __device__ __forceinline__ float max_groups(float a) {
     const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(a), false,
                                                     false);
-    a = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    a = max_nan(__uint_as_float(x[0]), __uint_as_float(x[1]));
     const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(a), false,
                                                     false);
-    return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+    return max_nan(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
-// largest magnitude in the lane's column of N tiles
+// largest magnitude in the lane's column of N tiles, NaN if one is there
 template <int N>
 __device__ __forceinline__ float max_column(const dfloat4 (&x)[N]) {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; r += 2) a = fmaxf(fmaxf(a, fabsf(x[i][r])), fabsf(x[i][r + 1]));
+        for (int r = 0; r < 4; r += 2)
+            a = max_nan(max_nan(a, fabsf(x[i][r])), fabsf(x[i][r + 1]));
     return max_groups(a);
 }
 

@@ -513,7 +513,11 @@ typedef struct fftconv_delta_desc {
  * bits); outputs are rounded to their type once.  Long sequences of few heads are
  * cut into segments, joined in another order of the same sums: results do not
  * depend on anything but the descriptor and the inputs, and equal calls give
- * equal bits. */
+ * equal bits.
+ *  A NaN or infinity reaches what it reaches in the rule: from k, g or beta its
+ * token's outputs, the later ones of the sequence and the state; from v the
+ * same in its column; from q its token's outputs.  They are not finite then
+ * (NaN also where the rule gives an infinity); all others are as without it. */
 fftconv_status fftconv_delta_forward(const fftconv_delta_desc *desc, const void *q,
                                      const void *k, const void *v, const float *g,
                                      const float *beta, const long long *cu_seqlens,
@@ -531,7 +535,9 @@ size_t fftconv_delta_saved_bytes(const fftconv_delta_desc *desc);
  *  dq, dk [B][T][Hk][Dk] (summed over the value heads that share the head,
  *     in a fixed order), dv [B][T][Hv][Dv], dg, dbeta fp32 [B][T][Hv];
  *     d_initial_state: as initial_state, or NULL to skip it.
- *  workspace: fftconv_delta_backward_workspace_bytes(desc) bytes. */
+ *  workspace: fftconv_delta_backward_workspace_bytes(desc) bytes.
+ *  Gradients that a NaN or infinity reaches are not finite, and those of the other
+ * tokens of its 64 (counted from the sequence's first) need not be. */
 fftconv_status fftconv_delta_backward(const fftconv_delta_desc *desc, const void *q,
                                       const void *k, const void *v, const float *g,
                                       const float *beta, const long long *cu_seqlens,
