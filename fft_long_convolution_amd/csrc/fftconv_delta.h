@@ -100,6 +100,7 @@ struct DeltaParams {
     long long T;
     long long qs[3], ks[3], vs[3];   // element strides (batch, token, head)
     const long long* cu;             // [nseq + 1] or null
+    int clear;                       // o of tokens that no sequence holds
     long long nseq, nch, slots;
     const void* q;
     const void* k;

@@ -245,8 +245,15 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaParams p) {
     const unsigned slot = u / p.Hv;
     const int h = (int)(u - slot * p.Hv);
     const long long id = u;
-    const Span sp = span_of(p, seq_of(p, slot, 1));
+    const unsigned seq = seq_of(p, slot, 1);
+    const Span sp = span_of(p, seq);
     const long long at = ((long long)slot - sp.slot0) * kChunk;
+    if (p.clear)
+        unheld_tokens(p, sp, seq, slot, [&](long long token, int rows) {
+            constexpr int kB = Io<IO>::kB;
+            clear_rows((char*)p.o + (token * p.Hv + h) * p.Dv * kB, (long long)p.Hv * p.Dv * kB,
+                       rows, p.Dv * kB);
+        });
     if (at < 0 || at >= sp.len) return;      // a slot between two sequences
     const int n = (int)(sp.len - at < kChunk ? sp.len - at : kChunk);
     const long long tok = sp.t0 + at;

@@ -380,8 +380,22 @@ void delta_grads_kernel(DeltaGradParams gp) {
     if (id >= units) return;
     const long long slot = id / p.Hk;
     const int hk = (int)(id - (unsigned)slot * p.Hk);
-    const Span sp = span_of(p, seq_of(p, (unsigned)slot, 1));
+    const unsigned seq = seq_of(p, (unsigned)slot, 1);
+    const Span sp = span_of(p, seq);
     const long long at = (slot - sp.slot0) * kChunk;
+    unheld_tokens(p, sp, seq, (unsigned)slot, [&](long long token, int rows) {
+        const long long k = (token * p.Hk + hk) * p.Dk * kB, kstep = (long long)p.Hk * p.Dk * kB;
+        clear_rows((char*)gp.dq + k, kstep, rows, p.Dk * kB);
+        clear_rows((char*)gp.dk + k, kstep, rows, p.Dk * kB);
+        const long long first = token * p.Hv + hk * p.group;
+        clear_rows((char*)gp.dv + first * p.Dv * kB, (long long)p.Hv * p.Dv * kB, rows,
+                   p.group * p.Dv * kB);
+        for (int i = threadIdx.x; i < rows * p.group; i += blockDim.x) {
+            const long long gi = first + (long long)(i / p.group) * p.Hv + i % p.group;
+            gp.dg[gi] = 0.f;
+            gp.dbeta[gi] = 0.f;
+        }
+    });
     if (at < 0 || at >= sp.len) return;
     const int n = (int)(sp.len - at < kChunk ? sp.len - at : kChunk);
     const long long tok = sp.t0 + at;

@@ -106,6 +106,30 @@ __device__ __forceinline__ unsigned seq_of(const DeltaParams& p, unsigned seg, u
     return lo;
 }
 
+// Tokens of a packed row that no sequence holds, for the workgroups of slots: those
+// before the first bound go to the slots up to the first sequence's, those
+// behind the last to the slots that its chunks leave.  do_rows(token, n).
+template <typename F>
+__device__ __forceinline__ void unheld_tokens(const DeltaParams& p, const Span& sp, unsigned seq,
+                                              unsigned slot, F do_rows) {
+    if (!p.cu) return;
+    if (seq == 0 && slot <= sp.slot0) {
+        const long long from = (long long)slot * kChunk;
+        if (from < sp.t0) do_rows(from, (int)(sp.t0 - from < kChunk ? sp.t0 - from : kChunk));
+    }
+    const long long left = slot - sp.slot0 - (sp.len + kChunk - 1) / kChunk;
+    if (seq + 1 == p.nseq && left >= 0) {
+        const long long from = sp.t0 + sp.len + left * kChunk;
+        if (from < p.T) do_rows(from, (int)(p.T - from < kChunk ? p.T - from : kChunk));
+    }
+}
+// rows of `bytes` (a multiple of 16) set to 0, `step` bytes apart, by the workgroup
+__device__ __forceinline__ void clear_rows(void* first, long long step, int rows, int bytes) {
+    const int per = bytes / 16;
+    for (int i = threadIdx.x; i < rows * per; i += blockDim.x)
+        *(uint4*)((char*)first + i / per * step + i % per * 16) = make_uint4(0, 0, 0, 0);
+}
+
 template <int IO>
 __device__ __forceinline__ float io_load(const void* p, long long i) {
     if constexpr (IO == IO_F32) return ((const float*)p)[i];

@@ -492,6 +492,7 @@ fftconv_status fftconv_delta_forward(const fftconv_delta_desc* d, const void* q,
     p.o = o;
     p.fin = final_state;
     p.pack = (uint4*)workspace;
+    p.clear = d->clear_unheld != 0;
     if (keep) delta_place_saved(l, saved, p);
     delta_place_segments(d, l, (char*)workspace + l.pack, p);
     hipStream_t s = (hipStream_t)stream;

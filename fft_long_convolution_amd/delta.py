@@ -42,7 +42,7 @@ class DeltaDesc(ctypes.Structure):
                 ("Hk", ctypes.c_size_t), ("Hv", ctypes.c_size_t), ("Dk", ctypes.c_size_t),
                 ("Dv", ctypes.c_size_t), ("sequences", ctypes.c_size_t),
                 ("scale", ctypes.c_float), ("q_stride", _LL3), ("k_stride", _LL3),
-                ("v_stride", _LL3)]
+                ("v_stride", _LL3), ("clear_unheld", ctypes.c_int)]
 
 
 _ready = None
@@ -327,18 +327,20 @@ class GatedDelta(_Op):
             initial_state = initial_state.contiguous()
         q, k, v = (_strided(x if x.stride(1) < 1 << 24 else x.contiguous(), self._step)
                    for x in (q, k, v))
-        desc = DeltaDesc(DTYPES[self.dtype], B, T, Hk, Hv, self.D_k, self.D_v, n, self.scale,
-                         _LL3(*q.stride()[:3]), _LL3(*k.stride()[:3]), _LL3(*v.stride()[:3]))
-        ref = ctypes.byref(desc)
+        # for a given o, and for a new one
+        ref, new = (ctypes.byref(DeltaDesc(
+            DTYPES[self.dtype], B, T, Hk, Hv, self.D_k, self.D_v, n, self.scale,
+            _LL3(*q.stride()[:3]), _LL3(*k.stride()[:3]), _LL3(*v.stride()[:3]), x))
+            for x in (0, 1))
         L = self._lib
         sizes = (L.fftconv_delta_workspace_bytes(ref), L.fftconv_delta_saved_bytes(ref),
                  L.fftconv_delta_backward_workspace_bytes(ref))
-        return ((dev, ref, state, sizes),
+        return ((dev, (ref, new), state, sizes),
                 (q, k, v, g.contiguous(), beta.contiguous(), cu_seqlens, initial_state))
 
     def _forward(self, ins, out, final_state, saved, train, workspace, stream):
-        (dev, ref, state, sizes), ins, ptrs = self._checked("_describe", ins)
-        v = ins[2]
+        (dev, refs, state, sizes), ins, ptrs = self._checked("_describe", ins)
+        v, ref = ins[2], refs[out is None]
         out = _like(v) if out is None else _given(out, "out", v.shape, self._dt, dev)
         if final_state is None:
             final_state = torch.empty(state, dtype=torch.float32, device=dev)
@@ -357,7 +359,9 @@ class GatedDelta(_Op):
                 final_state=None, workspace=None, stream=None):
         """Outputs [B, T, Hv, D_v] and final states [rows, Hv, D_k, D_v].
         cu_seqlens: int64 [n + 1] with the bounds of n sequences packed in the
-        one batch row (they may be empty); rows = n then, B otherwise."""
+        one batch row (they may be empty); rows = n then, B otherwise.  Tokens
+        before the first bound and behind the last belong to no sequence: their
+        outputs are 0, or what a given `out` holds."""
         return self._forward((q, k, v, g, beta, cu_seqlens, initial_state), out, final_state,
                              None, False, workspace, stream)[:2]
 
@@ -373,8 +377,9 @@ class GatedDelta(_Op):
         """Gradients of forward_train, for the same inputs and what it saved:
         d_out = dL/do, d_final_state = dL/d(final state) (None: 0).  Returns
         (dq, dk, dv, dg, dbeta, d_initial_state); the last is None where there
-        is no initial_state."""
-        (dev, ref, state, sizes), ins, ptrs = self._checked(
+        is no initial_state.  Tokens that no packed sequence holds have
+        gradients of 0."""
+        (dev, (ref, _), state, sizes), ins, ptrs = self._checked(
             "_describe", (q, k, v, g, beta, cu_seqlens, initial_state))
         _check(d_out, "d_out", ins[2].shape, self._dt, dev)
         d_out = _dense(d_out)

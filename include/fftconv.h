@@ -488,6 +488,9 @@ typedef struct fftconv_delta_desc {
     long long q_stride[3];    /* batch, token, head; token strides (and      */
     long long k_stride[3];    /* Hv Dv) below 2^24                           */
     long long v_stride[3];
+    int clear_unheld;         /* packed sequences: tokens before the first and
+                                 behind the last bound have o = 0 (else o
+                                 keeps there what it holds)                 */
 } fftconv_delta_desc;
 
 /* The gated delta rule over sequences.  For each value head, from a state S
@@ -501,7 +504,8 @@ typedef struct fftconv_delta_desc {
  *     (sequences may be empty); NULL when sequences = 0.  Bounds outside
  *     [0, T] or out of order are clamped on the device.
  *  initial_state: fp32 [rows][Hv][Dk][Dv], rows = sequences or B; NULL for 0.
- *  o [B][T][Hv][Dv].  Tokens that no sequence holds are not written.
+ *  o [B][T][Hv][Dv].  Tokens that no sequence holds are not written, or 0
+ *     where the descriptor asks for that.
  *  final_state: fp32, as initial_state; NULL to skip it.
  *  saved: fftconv_delta_saved_bytes(desc) bytes that fftconv_delta_backward
  *     will read (16-B aligned), or NULL in inference.
@@ -535,6 +539,7 @@ size_t fftconv_delta_saved_bytes(const fftconv_delta_desc *desc);
  *  dq, dk [B][T][Hk][Dk] (summed over the value heads that share the head,
  *     in a fixed order), dv [B][T][Hv][Dv], dg, dbeta fp32 [B][T][Hv];
  *     d_initial_state: as initial_state, or NULL to skip it.
+ *  Tokens before the first and behind the last of cu_seqlens have gradients of 0.
  *  workspace: fftconv_delta_backward_workspace_bytes(desc) bytes.
  *  Gradients that a NaN or infinity reaches are not finite, and those of the other
  * tokens of its 64 (counted from the sequence's first) need not be. */
