@@ -100,6 +100,7 @@ struct DeltaParams {
     long long T;
     long long qs[3], ks[3], vs[3];   // element strides (batch, token, head)
     const long long* cu;             // [nseq + 1] or null
+    bool packed;                     // cu is given
     int clear;                       // o of tokens that no sequence holds
     long long nseq, nch, slots;
     const void* q;
@@ -126,24 +127,32 @@ struct DeltaParams {
     float* states;
     float* us;
 };
-// Waves for the chain of a walk over p's segments.  effect: of the one that
-// makes their effects on the state, with columns for the matrices too.
-inline int walk_waves(const DeltaParams& p, bool effect) {
-    if (p.pieces > 1) return p.waves;
-    const auto units = [&](int width) {
-        return (double)p.segs * p.Hv *
-               ((p.Dv + width - 1) / width + (effect ? (p.Dk + width - 1) / width : 0));
-    };
+constexpr int kLoaders = 4;   // waves of a walk that bring the operands
+// A walk's launch: waves for the chain and workgroups.  effect: of the walk that
+// makes the segments' effects on the state, with columns for the matrices too.
+struct WalkGrid {
     int waves;
-    walk_us(units(64), units(128), effect, p.cu != nullptr, &waves);
-    return waves;
-}
-// Chains of a walk, and workgroups that take one of their pieces in each round.
-inline long long walk_chains(const DeltaParams& p, int waves) {
-    return p.nseq * p.Hv * ((p.Dv + 16 * waves - 1) / (16 * waves));
-}
-inline long long walk_machines(const DeltaParams& p, int waves) {
-    return (walk_chains(p, waves) * p.pieces + p.rounds - 1) / p.rounds;
+    long long units;
+    int threads() const { return 64 * (waves + kLoaders); }
+    // dealt to the XCDs in eights; the threads of a launch are a 32-bit number
+    long long blocks() const { return (units + 7) / 8 * 8; }
+    bool fits() const { return blocks() * threads() <= 0xffffffffll; }
+};
+inline WalkGrid walk_grid(const DeltaParams& p, bool effect) {
+    const auto columns = [&](int width) {
+        return (p.Dv + width - 1) / width + (effect ? (p.Dk + width - 1) / width : 0);
+    };
+    WalkGrid w;
+    if (p.pieces > 1 && !effect) {
+        // workgroups that take one of the chains' pieces in each round
+        w.waves = p.waves;
+        w.units = (p.nseq * p.Hv * columns(16 * w.waves) * p.pieces + p.rounds - 1) / p.rounds;
+        return w;
+    }
+    const double chains = (double)p.segs * p.Hv;
+    walk_us(chains * columns(64), chains * columns(128), effect, p.packed, &w.waves);
+    w.units = p.segs * p.Hv * columns(16 * w.waves);
+    return w;
 }
 
 struct DeltaGradParams {

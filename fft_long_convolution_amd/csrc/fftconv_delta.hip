@@ -873,28 +873,24 @@ hipError_t step_io(const DeltaStepParams& p, hipStream_t s) {
 }
 
 template <int IO, int DK, int W, int MODE>
-hipError_t scan_launch(const DeltaParams& p, hipStream_t s) {
+hipError_t scan_launch(const DeltaParams& p, const WalkGrid& w, hipStream_t s) {
     const int bytes = ScanLds<IO, DK, MODE != kEffect>::kBytes;
     const hipError_t e = hipFuncSetAttribute((const void*)delta_scan_kernel<IO, DK, W, MODE>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int width = 16 * W;
-    const int cols = (p.Dv + width - 1) / width +
-                     (MODE == kEffect ? (p.Dk + width - 1) / width : 0);
-    const bool pieces = MODE != kEffect && p.pieces > 1;
-    const long long units = pieces ? walk_machines(p, W) : p.segs * p.Hv * cols;
     DeltaParams r = p;
     do {
-        hipLaunchKernelGGL((delta_scan_kernel<IO, DK, W, MODE>), dim3((unsigned)xcd_blocks(units)),
-                           dim3(64 * (W + kLoaders)), bytes, s, r);
-    } while (pieces && ++r.round < r.rounds);
+        hipLaunchKernelGGL((delta_scan_kernel<IO, DK, W, MODE>), dim3((unsigned)w.blocks()),
+                           dim3(w.threads()), bytes, s, r);
+    } while (MODE != kEffect && p.pieces > 1 && ++r.round < r.rounds);
     return hipGetLastError();
 }
 
 template <int IO, int DK, int MODE>
 hipError_t scan_mode(const DeltaParams& p, hipStream_t s) {
-    return walk_waves(p, MODE == kEffect) == 4 ? scan_launch<IO, DK, 4, MODE>(p, s)
-                                               : scan_launch<IO, DK, 8, MODE>(p, s);
+    const WalkGrid w = walk_grid(p, MODE == kEffect);
+    return w.waves == 4 ? scan_launch<IO, DK, 4, MODE>(p, w, s)
+                        : scan_launch<IO, DK, 8, MODE>(p, w, s);
 }
 template <int IO, int DK>
 hipError_t scan_io(const DeltaParams& p, hipStream_t s) {

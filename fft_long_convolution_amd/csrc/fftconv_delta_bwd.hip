@@ -784,26 +784,23 @@ void delta_grads_kernel(DeltaGradParams gp) {
 }
 
 template <int IO, int DK, int W, bool FULL>
-hipError_t rscan_launch(const DeltaGradParams& p, hipStream_t s) {
+hipError_t rscan_launch(const DeltaGradParams& p, const WalkGrid& w, hipStream_t s) {
     const int bytes = RscanLds<IO, DK>::kBytes;
     const hipError_t e = hipFuncSetAttribute((const void*)delta_rscan_kernel<IO, DK, W, FULL>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int width = 16 * W;
-    const int cols = (p.f.Dv + width - 1) / width + (FULL ? 0 : (p.f.Dk + width - 1) / width);
-    const bool pieces = FULL && p.f.pieces > 1;
-    const long long units = pieces ? walk_machines(p.f, W) : p.f.segs * p.f.Hv * cols;
     DeltaGradParams r = p;
     do {
-        hipLaunchKernelGGL((delta_rscan_kernel<IO, DK, W, FULL>), dim3((unsigned)xcd_blocks(units)),
-                           dim3(64 * (W + kLoaders)), bytes, s, r);
-    } while (pieces && ++r.f.round < r.f.rounds);
+        hipLaunchKernelGGL((delta_rscan_kernel<IO, DK, W, FULL>), dim3((unsigned)w.blocks()),
+                           dim3(w.threads()), bytes, s, r);
+    } while (FULL && p.f.pieces > 1 && ++r.f.round < r.f.rounds);
     return hipGetLastError();
 }
 template <int IO, int DK, bool FULL>
 hipError_t rscan_mode(const DeltaGradParams& p, hipStream_t s) {
-    return walk_waves(p.f, !FULL) == 4 ? rscan_launch<IO, DK, 4, FULL>(p, s)
-                                       : rscan_launch<IO, DK, 8, FULL>(p, s);
+    const WalkGrid w = walk_grid(p.f, !FULL);
+    return w.waves == 4 ? rscan_launch<IO, DK, 4, FULL>(p, w, s)
+                        : rscan_launch<IO, DK, 8, FULL>(p, w, s);
 }
 template <int IO, int DK>
 hipError_t rscan_io(const DeltaGradParams& p, hipStream_t s) {

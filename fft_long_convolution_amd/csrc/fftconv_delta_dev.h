@@ -708,7 +708,6 @@ enum Factor {
     kBackT = 449,     // inverse scale of T
 };
 
-constexpr int kLoaders = 4;   // waves of a walk that bring the operands
 constexpr int kLd = 68;   // floats between rows of the 64 x 64 matrices in LDS
 
 // x of the lane that is so many places before in the group of 16, or 0

@@ -270,6 +270,7 @@ size_t delta_segs(const fftconv_delta_desc* d, size_t per) {
 
 // Bytes of the buffers of a call, each a multiple of 16.
 struct DeltaLayout {
+    Cut cut;
     size_t pack, seg_n, seg_m;      // forward workspace
     size_t bpack, states, us;       // saved
     size_t workspace() const { return pack + seg_n + seg_m; }
@@ -277,10 +278,24 @@ struct DeltaLayout {
     // dstates, dys and the segments
     size_t backward() const { return states + us + seg_n + seg_m; }
 };
+// What the walks' launches follow from.
+void delta_geometry(const fftconv_delta_desc* d, const Cut& c, DeltaParams& p) {
+    p.Dk = (int)d->Dk;
+    p.Dv = (int)d->Dv;
+    p.Hv = (int)d->Hv;
+    p.packed = d->sequences != 0;
+    p.nseq = (long long)(d->sequences ? d->sequences : d->B);
+    p.seg_chunks = (int)c.per;
+    p.segs = (long long)delta_segs(d, c.per);
+    p.pieces = c.pieces;
+    p.rounds = c.rounds;
+    p.waves = c.waves;
+}
 bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
     size_t n, x, y, m;
     const Cut c = delta_cut(d);
     const size_t per = c.per;
+    l->cut = c;
     if (!product(delta_slots(d), d->Hv, 1, 1, &n) || n > kMaxGrid) return false;
     // saved matrices: rows for the largest magnitudes, columns padded to 16
     const size_t cols = (d->Dv + 15) / 16 * 16, rows = d->Dk <= 64 ? 64 : 128;
@@ -296,7 +311,9 @@ bool delta_layout(const fftconv_delta_desc* d, DeltaLayout* l) {
     l->bpack = n * (size_t)delta_pack_uint4() * 16;
     l->states = x * 4;
     l->us = y * 4;
-    return true;
+    DeltaParams p = DeltaParams();
+    delta_geometry(d, c, p);
+    return walk_grid(p, false).fits() && (!l->seg_m || walk_grid(p, true).fits());
 }
 
 struct DeltaArgs {
@@ -367,12 +384,7 @@ fftconv_status delta_inputs(const fftconv_delta_desc* d, const DeltaArgs& a, Del
 
 void delta_place_segments(const fftconv_delta_desc* d, const DeltaLayout& l, char* at,
                           DeltaParams& p) {
-    const Cut c = delta_cut(d);
-    p.seg_chunks = (int)c.per;
-    p.segs = (long long)delta_segs(d, c.per);
-    p.pieces = c.pieces;
-    p.rounds = c.rounds;
-    p.waves = c.waves;
+    delta_geometry(d, l.cut, p);
     if (l.seg_n) p.seg_n = (float*)at;
     if (l.seg_m) p.seg_m = (float*)(at + l.seg_n);
 }

@@ -248,3 +248,13 @@ def test_missing_library_fails_loudly(monkeypatch):
     for make in (lambda: delta.QKNorm(64), lambda: delta.GatedDelta(64, 64)):
         with pytest.raises(RuntimeError, match="not built"):
             make()
+
+
+def test_more_chains_than_a_launch_takes():
+    # 512 threads and more for each chain, fewer than 2^32 in all: refused before
+    # anything is launched, not by the launch of the walk
+    for B in (8388609, 9000000, 16 << 20):
+        d = delta_desc(B=B, T=1, Hk=1, Hv=1, Dk=8, Dv=8)
+        assert sizes(d) == (0, 0, 0)
+        assert forward(d, ws_bytes=1 << 50, saved_bytes=1 << 50) == UNSUPPORTED
+    assert min(sizes(delta_desc(B=8388000, T=1, Hk=1, Hv=1, Dk=8, Dv=8))) > 0
