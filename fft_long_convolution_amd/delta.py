@@ -127,10 +127,15 @@ class _Op:
     def __init__(self, dtype):
         if dtype not in DTYPES:
             raise ValueError("dtype must be one of %s" % list(DTYPES))
-        self.dtype = dtype
+        self._dtype = dtype
         self._dt = TORCH_DTYPES[dtype]
         self._step = 4 if dtype == "f32" else 8
         self._lib = lib()
+
+    @property
+    def dtype(self):
+        """Fixed: what else follows from it is made once."""
+        return self._dtype
 
     def _checked(self, kind, ts):
         """The call's tensors in a layout the library takes, its descriptor
@@ -214,7 +219,10 @@ class QKNorm(_Op):
             raise ValueError("norm must be one of %s" % list(NORMS))
         self.D, self.rotary_dim, self.norm = D, rotary_dim, norm
         self.eps, self.interleaved = eps, interleaved
-        self._settings = (D, rotary_dim, norm, eps, interleaved, dtype)
+
+    @property
+    def _settings(self):
+        return self.D, self.rotary_dim, self.norm, self.eps, self.interleaved, self.dtype
 
     def _describe(self, q, k, q_weight, k_weight, cos, sin, positions):
         dev = self._first(q, 4)
@@ -301,7 +309,10 @@ class GatedDelta(_Op):
         super().__init__(dtype)
         self.D_k, self.D_v = D_k, D_v
         self.scale = D_k ** -0.5 if scale is None else float(scale)
-        self._settings = (D_k, D_v, dtype, self.scale)
+
+    @property
+    def _settings(self):
+        return self.D_k, self.D_v, self.dtype, self.scale
 
     def _describe(self, q, k, v, g, beta, cu_seqlens, initial_state):
         dev = self._first(q, 4)

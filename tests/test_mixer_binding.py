@@ -79,3 +79,31 @@ def test_descriptor_has_the_strides_of_the_tensors_passed(calls, name, twice):
     q, k, v = projection(2, 5, (6, 6, 6), 128, 4, 8)
     for x, y in zip(copied, (q, k, v) if not name.startswith("norm") else (q, k)):
         assert torch.equal(x, y if x.dim() == 4 else y[:, 0])
+
+
+def test_settings_changed_after_the_first_call(calls):
+    # descriptors are kept by the settings they were made with: neither the
+    # changed operator nor another of the old settings gets the wrong one
+    q, k, v = projection(1, 4, (2, 2, 2), 64, 0, 0)
+    g = torch.zeros(1, 4, 2)
+    for change_first in (False, True):
+        a, b = delta.GatedDelta(64, 64), delta.GatedDelta(64, 64)
+        if not change_first:
+            a.forward(q, k, v, g, g)
+        a.scale = 3.0
+        a.forward(q, k, v, g, g)
+        assert calls[-1][1].scale == 3.0
+        b.forward(q, k, v, g, g)
+        assert calls[-1][1].scale == 0.125
+        delta._Op._known.clear()
+        a, b = delta.QKNorm(64, eps=1e-6), delta.QKNorm(64, eps=1e-6)
+        if not change_first:
+            a.forward(q, k)
+        a.eps, a.norm = 0.5, "l2"
+        a.forward(q, k)
+        assert calls[-1][1].eps == 0.5 and calls[-1][1].norm == delta.NORMS["l2"]
+        b.forward(q, k)
+        assert abs(calls[-1][1].eps - 1e-6) < 1e-12 and calls[-1][1].norm == 0
+        delta._Op._known.clear()
+    with pytest.raises(AttributeError):
+        delta.GatedDelta(64, 64).dtype = "f16"
