@@ -1,6 +1,6 @@
 """A block of a hybrid model: a long convolution over the channels, then a
-layer of the gated delta rule, trained on one sequence and served from its
-state.
+layer of the gated delta rule, trained on whole sequences and served token by
+token: the rule from its state, the convolution from the tokens seen so far.
 
     python examples/hybrid_block.py [--train-steps 200] [--new-tokens 32]
 
@@ -10,7 +10,7 @@ The block runs the library's operators as a program would:
   GatedDelta.forward_train    the sequence, and what its gradients need
   GatedDelta.backward, QKNorm.backward, FFTConv.backward
   GatedDelta.forward          a prompt, packed with others, to its state
-  GatedDelta.step             then one token at a time against the pool
+  GatedDelta.step, FFTConv    then one token at a time
 It is trained to give what a second block with other random weights gives on
 a synthetic batch.
 """
@@ -121,21 +121,58 @@ class HybridBlock(torch.nn.Module):
 
     @torch.no_grad()
     def prefill(self, x, bounds):
-        """Prompts packed in one row x [1, T, width] (after the convolution),
-        bounds int64 [n + 1]: outputs, and the state of each."""
-        q, k, v, g, beta = self.heads_of(x)
-        start = torch.repeat_interleave(bounds[:-1], bounds.diff())
-        q, k = self.rotated(q, k, (torch.arange(x.shape[1], device=x.device) - start)[None])
+        """Prompts packed in one row x [1, T, width], bounds int64 [n + 1]:
+        outputs, and of each its tokens [n, N, width] and its state."""
+        lengths = bounds.diff()
+        row = torch.repeat_interleave(torch.arange(len(lengths), device=x.device), lengths)
+        position = torch.arange(x.shape[1], device=x.device) - bounds[row]
+        seen = x.new_zeros(len(lengths), self.conv.N, self.width)
+        seen[row, position] = x[0]
+        q, k, v, g, beta = self.heads_of(self.mix(seen)[row, position][None])
+        q, k = self.rotated(q, k, position[None])
         o, state = self.rule.forward(q, k, v, g, beta, cu_seqlens=bounds)
-        return self.out(o.flatten(2)), state
+        return self.out(o.flatten(2)), seen, state
 
     @torch.no_grad()
-    def decode(self, x, state, slots, positions):
-        """One token x [n, width] for each request: its state is state[slot]."""
-        q, k, v, g, beta = self.heads_of(x)
+    def decode(self, x, seen, state, slots, positions):
+        """The next token x [n, width] of each request, whose earlier ones are
+        seen[slot] and whose state is state[slot]; both take it in.  The
+        convolution is causal, so what stands behind the token does not
+        matter; it is taken over the whole length here."""
+        seen[slots, positions] = x
+        rows = torch.arange(len(slots), device=x.device)
+        q, k, v, g, beta = self.heads_of(self.mix(seen[slots])[rows, positions])
         q, k = self.rotated(q[:, None], k[:, None], positions[:, None])
         o = self.rule.step(q[:, 0], k[:, 0], v, g, beta, state, slots=slots)
         return self.out(o.flatten(1))
+
+
+def serve(block, x, lengths, new_tokens):
+    """Prompts x[b, :lengths[b]], then new_tokens of each one at a time:
+    pairs of what serving and what the training pass over the whole x gives."""
+    whole = block(x)
+    bounds = torch.tensor([0, *lengths], device=x.device).cumsum(0)
+    y, seen, state = block.prefill(torch.cat([x[b, :n] for b, n in enumerate(lengths)])[None],
+                                   bounds)
+    pairs = [(y[0, bounds[b]:bounds[b + 1]], whole[b, :n]) for b, n in enumerate(lengths)]
+    # requests live in pools, among others
+    slots = torch.arange(len(lengths), device=x.device) * 3 + 2
+    seen_pool = seen.new_zeros(3 * len(lengths) + 2, *seen.shape[1:])
+    state_pool = state.new_zeros(3 * len(lengths) + 2, *state.shape[1:])
+    seen_pool[slots], state_pool[slots] = seen, state
+    at = torch.tensor(lengths, device=x.device)
+    rows = torch.arange(len(lengths), device=x.device)
+    for _ in range(new_tokens):
+        y = block.decode(x[rows, at], seen_pool, state_pool, slots, at)
+        pairs.append((y, whole[rows, at]))
+        at = at + 1
+    return pairs
+
+
+def worst_error(pairs):
+    """The largest error of a pair, relative to the norm of all tokens."""
+    whole = sum(w.float().norm().item() ** 2 for _, w in pairs) ** 0.5
+    return max((y - w).float().norm().item() for y, w in pairs) / whole
 
 
 def main(width=128, heads=2, N=256, batch=4, train_steps=200, new_tokens=32, log=print):
@@ -161,24 +198,7 @@ def main(width=128, heads=2, N=256, batch=4, train_steps=200, new_tokens=32, log
     # give what the training pass gives over the whole sequences
     with torch.no_grad():
         x = torch.randn(2, N, width, device="cuda").to(kind)
-        whole = block(x)
-        mixed = block.mix(x)
-        lengths = (N - new_tokens, N - new_tokens - 37)
-        bounds = torch.tensor([0, lengths[0], sum(lengths)], device="cuda")
-        packed = torch.cat([mixed[b, :n] for b, n in enumerate(lengths)])[None]
-        y, state = block.prefill(packed, bounds)
-        pool = torch.zeros(8, *state.shape[1:], device="cuda")
-        slots = torch.tensor([5, 2], device="cuda")
-        pool[slots] = state
-        worst = max((y[0, :lengths[0]] - whole[0, :lengths[0]]).float().norm().item(),
-                    (y[0, lengths[0]:] - whole[1, :lengths[1]]).float().norm().item())
-        at = torch.tensor(lengths, device="cuda")
-        rows = torch.arange(2, device="cuda")
-        for _ in range(new_tokens):
-            y = block.decode(mixed[rows, at], pool, slots, at)
-            worst = max(worst, (y - whole[rows, at]).float().norm().item())
-            at = at + 1
-        error = worst / whole.float().norm().item()
+        error = worst_error(serve(block, x, (N - new_tokens, N - new_tokens - 37), new_tokens))
     log("prefill and %d decoded tokens against the training pass: %.2e" % (new_tokens, error))
     return losses, error
 
