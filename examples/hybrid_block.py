@@ -170,9 +170,8 @@ def serve(block, x, lengths, new_tokens):
 
 
 def worst_error(pairs):
-    """The largest error of a pair, relative to the norm of all tokens."""
-    whole = sum(w.float().norm().item() ** 2 for _, w in pairs) ** 0.5
-    return max((y - w).float().norm().item() for y, w in pairs) / whole
+    """The largest error of a pair, relative to the norm of the same tokens."""
+    return max(((y - w).float().norm() / w.float().norm()).item() for y, w in pairs)
 
 
 def main(width=128, heads=2, N=256, batch=4, train_steps=200, new_tokens=32, log=print):
