@@ -352,9 +352,6 @@ __device__ __forceinline__ float max_column(const dfloat4 (&x)[N]) {
 // Loads under a condition read the tensor's first elements where it does not
 // hold and drop them: a load inside a branch would have to arrive before the
 // branch ends, one latency after the other.
-__device__ __forceinline__ uint4 keep(bool ok, uint4 x) {
-    return make_uint4(ok ? x.x : 0, ok ? x.y : 0, ok ? x.z : 0, ok ? x.w : 0);
-}
 template <int IO>
 __device__ __forceinline__ float io_load_if(const void* p, long long i, bool ok) {
     const float x = io_load<IO>(p, ok ? i : 0);
@@ -382,18 +379,6 @@ __device__ __forceinline__ void unpack8(const du4* r, float (&x)[8]) {
             }
         }
     }
-}
-// eight consecutive elements
-template <int IO>
-__device__ __forceinline__ void load8(const void* p, long long i, bool ok, float (&x)[8]) {
-    constexpr int kB = IO == IO_F32 ? 4 : 2;
-    const du4* s = (const du4*)((const char*)p + (ok ? i : 0) * kB);
-    du4 r[2];
-    r[0] = s[0];
-    if (IO == IO_F32) r[1] = s[1];
-    unpack8<IO>(r, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = ok ? x[j] : 0.f;
 }
 // The tokens of one head: a base for the whole workgroup and byte offsets of
 // the lanes below 2^32 (the host keeps token strides below 2^24 elements), so
