@@ -456,7 +456,7 @@ __device__ __forceinline__ bool delta_walk(const DeltaParams& p, const Span& sp,
     const int col = cb * kCols + wave * 16 + c;
     const int width = matrix ? p.Dk : p.Dv;
     const bool cok = col < width;
-    const int colv = cok ? col : 0;                      // to read from
+    const int colv = cok && !matrix ? col : 0;           // to read from
     const int hk = h / p.group;
     const long long state = p.Dk * (long long)p.Dv;
     const Tokens tk = tokens_of<IO>(p.k, sp.b * p.ks[0] + sp.t0 * p.ks[1] + hk * p.ks[2], p.ks[1]);
@@ -519,13 +519,8 @@ __device__ __forceinline__ bool delta_walk(const DeltaParams& p, const Span& sp,
                                  : (s && cok && row < p.Dk ? s[(long long)row * p.Dv] : 0.f);
             }
     }
-    dfloat4 v[4];
-    const auto load_v = [&](int ch) __attribute__((always_inline)) {
-        if (!matrix) load_column<IO>(tv, ch * kChunk, vlane, sp.len - ch * kChunk, v);
-    };
-#pragma unroll
-    for (int m = 0; m < 4; ++m) v[m] = dfloat4{0, 0, 0, 0};
-    if (first < last) load_v(first);
+    Column<IO> v;
+    if (first < last) v.load(tv, first * kChunk, vlane, sp.len - first * kChunk);
     __syncthreads();
     int buf = 0;
     for (int ch = first; ch < last; ++ch) {
@@ -568,11 +563,11 @@ __device__ __forceinline__ bool delta_walk(const DeltaParams& p, const Span& sp,
             const float fv[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                X[m][r] = bv[r] * fmaf(-(ev[r] * ss.back), X[m][r], v[m][r]);
+                X[m][r] = bv[r] * fmaf(-(ev[r] * ss.back), X[m][r], matrix ? 0.f : v.get(m, r));
                 if (FULL) O[m][r] = (fv[r] * ss.back) * O[m][r];
             }
         }
-        load_v(ahead);
+        v.load(tv, ahead * kChunk, vlane, sp.len - ahead * kChunk);
         // Tokens of the lane's column from the first value that is not finite
         // on: their outputs and the state become NaN, and x 0, for what follows
         // multiplies it with the zeros of T and P.

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     const int col = cb * kCols + wave * 16 + c;
     const int width = matrix ? p.Dk : p.Dv;
     const bool cok = col < width;
-    const int colv = cok ? col : 0;                      // to read from
+    const int colv = cok && !matrix ? col : 0;           // to read from
     const int hk = h / p.group;
     const long long state = p.Dk * (long long)p.Dv;
     dfloat4 D[ST];
@@ -139,13 +139,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
     }
     // dO of the next chunk.  The tokens from n on that repeat the last one
     // meet columns of P^T and rows of Q that are 0.
-    dfloat4 dN[4];
-    const auto load_do = [&](int ch) __attribute__((always_inline)) {
-        if (!matrix) load_column<IO>(to, ch * kChunk, olane, sp.len - ch * kChunk, dN);
-    };
-#pragma unroll
-    for (int m = 0; m < 4; ++m) dN[m] = dfloat4{0, 0, 0, 0};
-    if (first < last) load_do(last - 1);
+    Column<IO> next;
+    if (first < last) next.load(to, (last - 1) * kChunk, olane, sp.len - (last - 1) * kChunk);
     __syncthreads();
     int buf = 0;
     for (int ch = last - 1; ch >= first; --ch) {
@@ -155,7 +150,9 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
         const uint4* tri = now + L::kTri;
         dfloat4 dO[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) dO[m] = dN[m];
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dO[m][r] = matrix ? 0.f : next.get(m, r);
         const int ahead = ch > first ? ch - 1 : first;
         const float big_d = max_column(D);
         if (FULL && cok) save_columns<KB>(gp.dstates, ci, p.Dv, col, D, big_d);
@@ -251,7 +248,7 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaG
             }
         }
         const float ec = fac[kDecayAll];
-        load_do(ahead);
+        next.load(to, ahead * kChunk, olane, sp.len - ahead * kChunk);
         const Scale sy = scale_to(max_column(dY)), sq = scale_to(max_column(dO));
         uint4 yt[2][2], ot[2][2];
 #pragma unroll

@@ -537,31 +537,33 @@ struct Block {
     }
 };
 // Elements [8 g + tile_base(m) + r] of one column of 64 tokens, as a lane's
-// accumulators have them; `lane`: byte offset of the column and the group's
-// first token.  Tokens from n on read the last one: nothing that is made of
-// them is kept.
+// accumulators have them.  The bits as loaded, made numbers where they are used:
+// loads that are in flight for a chunk may meet neither an instruction nor the end
+// of a branch.
 template <int IO>
-__device__ __forceinline__ void load_column(const Tokens& x, long long token, uint32_t lane, int n,
-                                            dfloat4 (&v)[4]) {
-    const char* s = x.at(token);
-    if (n >= kChunk) {
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                v[m][r] = io_load<IO>(s + (tile_base(m) + r) * x.bytes + lane, 0);
-    } else {
-        const int g = (threadIdx.x >> 4) & 3;
-        const uint32_t col = lane - 8 * g * (uint32_t)x.bytes;
+struct Column {
+    uint32_t raw[4][4];
+    // lane: byte offset of the column and the group's first token.  Tokens from n
+    // on read the last one: nothing that is made of them is kept.
+    __device__ __forceinline__ void load(const Tokens& x, long long token, uint32_t lane, int n) {
+        const char* s = x.at(token);
+        const int g = (threadIdx.x >> 4) & 3, left = n - 8 * g;
+        const uint32_t bytes = (uint32_t)x.bytes, last = lane + (uint32_t)(left - 1) * bytes;
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = 8 * g + tile_base(m) + r;
-                v[m][r] = io_load<IO>(s + (row < n ? row : n - 1) * (uint32_t)x.bytes + col, 0);
+                const uint32_t at = tile_base(m) + r < left ? lane + (tile_base(m) + r) * bytes : last;
+                if constexpr (IO == IO_F32) raw[m][r] = *(const uint32_t*)(s + at);
+                else raw[m][r] = *(const uint16_t*)(s + at);
             }
     }
-}
+    __device__ __forceinline__ float get(int m, int r) const {
+        if constexpr (IO == IO_F32) return __uint_as_float(raw[m][r]);
+        else if constexpr (IO == IO_BF16) return __uint_as_float(raw[m][r] << 16);
+        else return (float)__builtin_bit_cast(_Float16, (uint16_t)raw[m][r]);
+    }
+};
 template <int IO>
 __device__ __forceinline__ void store_column(char* s, long long bytes, uint32_t lane, int n,
                                              const dfloat4 (&v)[4]) {
