@@ -402,19 +402,24 @@ hipError_t bwd_nt(const QkNormParams& p, hipStream_t s) {
 }
 
 // Whether q and k are so large that little of them is still in a cache (256 MB
-// in all, which the pass fills four or five times over) when they are read
-// again.  Past the caches, 200 MB: forward 82 -> 76 us, 268 MB: backward 173 ->
-// 152 us; but 23 MB: backward 22.5 -> 25 us.
-bool streams(int io, const QkNormParams& p) {
-    return p.tokens * (p.Hq + p.Hk) * p.D * (io == IO_F32 ? 4 : 2) > (64ll << 20);
+// in all) when they are read again.  16 bits, 12 heads of 128, through the caches
+// and past them: 128 MB forward 47 and 54 us, backward 87 and 81; 192 MB 80 and 75,
+// 122 and 114; 256 MB 102 and 96, 161 and 152; 64 MB 29 and 32, 46 and 47.  fp32 is
+// slower past them at every size (192 MB: 82 and 87, 122 and 130).
+bool streams(const QkNormParams& p) {
+    return p.tokens * (p.Hq + p.Hk) * p.D * 2 > (160ll << 20);
 }
 template <int IO>
 hipError_t fwd_io(const QkNormParams& p, hipStream_t s) {
-    return streams(IO, p) ? fwd_nt<IO, true>(p, s) : fwd_nt<IO, false>(p, s);
+    if constexpr (IO != IO_F32)
+        if (streams(p)) return fwd_nt<IO, true>(p, s);
+    return fwd_nt<IO, false>(p, s);
 }
 template <int IO>
 hipError_t bwd_io(const QkNormParams& p, hipStream_t s) {
-    return streams(IO, p) ? bwd_nt<IO, true>(p, s) : bwd_nt<IO, false>(p, s);
+    if constexpr (IO != IO_F32)
+        if (streams(p)) return bwd_nt<IO, true>(p, s);
+    return bwd_nt<IO, false>(p, s);
 }
 
 }  // namespace
