@@ -72,13 +72,24 @@ constexpr int kTriTiles = 6;               // 16 x 32 tiles of a 64 x 64 triangl
 int delta_pack_uint4();                    // the pack of its transposes alike
 
 // Time of a walk for each chunk of its longest chain, in us, by the number of
-// workgroups that take 64 or 128 columns (four or eight waves for the chain),
-// measured at heads of 128 in bf16: alone on a card and with all 256 CUs taken.
-// A workgroup has a CU to itself, so more than 256 run in rounds; packed
-// sequences differ in length, and about half of a further round is hidden behind
-// the longest of them (23 sequences, 8 heads of 64 x 128, f16: 82 us with four waves
-// and 368 workgroups, 97 with eight and 184).  *waves: the better of four and
-// eight.
+// workgroups that take 64 or 128 columns (four or eight waves for the chain):
+// alone on a card and with all 256 CUs taken, for heads of 128 at 16 bits (measured
+// 3.0 and 4.5 with four, 4.9 and 6.9 with eight; f16 within 6 %).  Heads of 64 take
+// 0.75 to 0.85 of it and fp32 1.4 to 1.65, with four and eight alike, so they
+// choose alike.  A workgroup has a CU to itself, so more than 256 run in rounds;
+// packed sequences differ in length, and about half of a further round is hidden
+// behind the longest of them.  *waves: the better of four and eight.
+//
+// Held against 45 measured calls, 13 of equal and 32 of packed sequences (half of
+// them of lengths as of chance), 1 to 100 rows, heads of 64 to 128 x 64 to 256, all
+// types: what this and delta_cut() choose is within 5 % of the best of whole and
+// cut walks on average, 22 % at most.  The most by a length that the host does not
+// know.  Four or eight waves: 23 sequences of 9001 tokens, 8 heads of 64 x 128, f16,
+// 98 us with four (chosen) and 112 with eight, of equal lengths 76 and 63; 30 of
+// 12000, 12 heads of 128, bf16, 178 and 202 (chosen), of equal ones 135 and 142; 38 of
+// 16000, 6 heads of 128 x 256, 226 and 199 (chosen), 149 and 130.  Segments: 10 of
+// 16000, 2 heads of 128, in 5 chunks (chosen) 152 us and in 12, 129; 5 of 4000, 3 of 96,
+// fp32, in 3 (chosen) 128 and in 4, 106.
 inline double walk_us(double units64, double units128, bool effect, bool packed, int* waves) {
     const double cus = 256.0;
     const auto time = [&](double units, double alone, double full) {

@@ -213,3 +213,26 @@ def test_backward_without_heads_reads_no_token():
                                            torch.cuda.current_stream().cuda_stream)
         assert status == 0
         assert torch.equal(dw, torch.zeros_like(dw))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_large_tensors_have_the_bits_of_their_parts(dtype):
+    # past the caches: loads and stores of another kind, the same sums
+    from fft_long_convolution_amd.delta import QKNorm
+    T = 120001
+    q = torch.randn(1, T, 5, 128, device="cuda").to(DT[dtype])
+    k = torch.randn(1, T, 1, 128, device="cuda").to(DT[dtype])
+    assert (q.numel() + k.numel()) * 2 > 160 << 20
+    angle = torch.rand(64, 32, device="cuda")
+    w = 1 + torch.rand(128, device="cuda")
+    pos = torch.randint(0, 64, (1, T), device="cuda")
+    op = QKNorm(128, rotary_dim=64, dtype=dtype)
+    whole = op.forward(q, k, w, w, angle.cos(), angle.sin(), pos)
+    grads = op.backward(q, k, whole[0], whole[1], w, w, angle.cos(), angle.sin(), pos)
+    for a, z in ((0, 60000), (60000, T)):
+        part = [x[:, a:z] for x in (q, k)]
+        y = op.forward(*part, w, w, angle.cos(), angle.sin(), pos[:, a:z])
+        d = op.backward(*part, whole[0][:, a:z], whole[1][:, a:z], w, w, angle.cos(),
+                        angle.sin(), pos[:, a:z])
+        for x, p in zip((*whole, *grads[:2]), (*y, *d[:2])):
+            assert torch.equal(x[:, a:z], p)
