@@ -73,10 +73,10 @@ int delta_pack_uint4();                    // the pack of its transposes alike
 
 // Time of a walk for each chunk of its longest chain, in us, by the number of
 // workgroups that take 64 or 128 columns (four or eight waves for the chain):
-// alone on a card and with all 256 CUs taken, for heads of 128 at 16 bits (measured
-// 3.0 and 4.5 with four, 4.9 and 6.9 with eight; f16 within 6 %).  Heads of 64 take
-// 0.75 to 0.85 of it and fp32 1.4 to 1.65, with four and eight alike, so they
-// choose alike.  A workgroup has a CU to itself, so more than 256 run in rounds;
+// alone on a card and with all 256 CUs taken, for heads of 128 at 16 bits.  (The
+// outputs' are 3.0 and 4.5 with four and 4.9 and 6.9 with eight now, f16 within 6 %;
+// effects 2.2 and 2.5, 3.1 and 4.0.)  Heads of 64 take 0.75 to 0.85 of it and fp32
+// 1.4 to 1.65, with four and eight alike, so they choose alike.  A workgroup has a CU to itself, so more than 256 run in rounds;
 // packed sequences differ in length, and about half of a further round is hidden
 // behind the longest of them.  *waves: the better of four and eight.
 //

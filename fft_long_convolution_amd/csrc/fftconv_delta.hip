@@ -229,11 +229,12 @@ struct PrepLds {
 // One workgroup of four waves per chunk and value head: a wave makes 16 rows of
 // K K^T and Q K^T (16-bit operands exact, fp32 in three bf16 terms), the decays
 // turn them into A and P, then T is made from A in LDS.  Writes T, P and the
-// chunk's factors as the walk takes them, 20 KB for the 32 KB of keys and queries
-// of a chunk at D_k = 128 in bf16.  It is latency, of barriers, LDS and the
-// substitution's 16 steps, that other workgroups of the CU only partly fill:
-// 64 x 1024 tokens of 6 heads of 128 in bf16, 6144 workgroups, take 111 us
-// (0.33 GB), with the transposes for the backward pass 130 (0.45 GB).  (The
+// chunk's factors as the walk takes them, 27 KB for the 32 KB of keys and queries
+// of a chunk at D_k = 128 in bf16.  It is latency, of barriers, LDS (31 % of its
+// cycles bank conflicts) and the substitution's 16 steps, that other workgroups of
+// the CU only partly fill: 64 x 1024 tokens of 6 heads of 128 in bf16, 6144
+// workgroups, take 100 to 110 us (0.36 GB), with the transposes for the backward
+// pass 125 to 145 (0.53 GB).  (The
 // bound of two workgroups a CU keeps the compiler from accumulating in registers
 // apart, which cost it 290 moves in 1460 instructions.)
 template <int IO, int DK>
@@ -715,10 +716,12 @@ __device__ __forceinline__ bool delta_walk(const DeltaParams& p, const Span& sp,
 // chunk.  The chain is latency: a step's vector work, its products and their
 // operands wait for one another, and what else a wave did would add to it (with
 // the loads in the chain's waves: 23 sequences of 9001 tokens in f16 103 us, so
-// 82; on eight waves, which hide more of it, 205 and 199).  With 256 CUs taken a chunk of bf16 at D_k = 128 takes 6.2 us on eight waves and 4.7 on
+// 82 when both were tried; on eight waves, which hide more of it, 205 and 199).  With
+// 256 CUs taken a chunk of bf16 at D_k = 128 takes 6.9 us on eight waves and 4.5 on
 // four: 64 x 1024 tokens of 6 heads of 128 are 384 chains of 16 chunks, three
-// launches of 256 workgroups and 8 chunks, 60 us each, with what the backward
-// pass reads 110; the matrix cores are busy 20 % of the time.
+// launches of 256 workgroups and 8 chunks, 63 to 69 us each, with what the backward
+// pass reads 88 to 100.  The vector unit (scales and terms) is busy 46 % of the
+// time, the matrix cores 21 %, and 30 % of the LDS cycles are bank conflicts.
 template <int IO, int DK, int W, int MODE>
 __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaParams p) {
     constexpr bool FULL = MODE != kEffect;
@@ -768,8 +771,8 @@ __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_scan_kernel(DeltaPa
 // next one's loads in flight.  States of a sequence's end go through every M, so
 // here both are in three bf16 terms, 24 bits.  A step at heads of 128 brings 64 KB
 // of M and 64 KB of N through one CU, splits M and reads it from LDS eight times,
-// one after the other for the most part: 7 us a step, 105 us for 16 segments of 4
-// x 32768 tokens of 4 heads; 2.3 a step at D_k = 64.
+// one after the other for the most part: 6 to 7 us a step, 95 to 104 us for 16
+// segments of 4 x 32768 tokens of 4 heads; 2.2 a step at D_k = 64.
 template <int DK>
 struct JoinLds {
     static constexpr int kHalves = DK / 64;             // 64 rows of M each

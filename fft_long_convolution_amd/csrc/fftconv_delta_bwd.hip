@@ -33,7 +33,7 @@ struct RscanLds {
 // state (the last segment of a sequence) or from 0, and in columns of their own
 // the matrix D is multiplied with (from the identity, without dO).  Bound as
 // the forward walk is: 64 x 1024 tokens of 6 heads of 128 in bf16 take three
-// launches of 111 us, 0.7 GB of D and dY written.
+// launches of 92 to 98 us, 0.7 GB of D, dY and dV written.
 template <int IO, int DK, int W, bool FULL>
 __global__ __launch_bounds__(64 * (W + kLoaders)) void delta_rscan_kernel(DeltaGradParams gp) {
     typedef RscanLds<IO, DK> L;
@@ -337,10 +337,11 @@ __device__ __forceinline__ void unpack_pieces(const P (&x)[2], bool ok0, bool ok
 }
 
 // Workgroups on a CU: two where 256 registers a lane hold what it needs, nearly.
-// 32 x 1024 tokens of 6 heads of 64 with two and with one: 3 key heads, bf16,
-// 15 registers spilled, 126 and 171 us; 6 key heads, fp32, none, 138 and 206.
-// fp32 with shared heads would spill 38: 179 and 200 us there, but 37 and 30
-// for 96 workgroups, which have a CU each.
+// Backward calls with two and with one: 32 x 1024 tokens of 6 heads of 64, 3 key
+// heads, bf16 (8 registers spilled) 190 and 240 us, 6 key heads, fp32 (none) 231 and
+// 296; 64 x 1024 of 6 heads of 128, bf16 (4 spilled) 754 and 937, with 3 key heads
+// (117 spilled) 947 and 900.  fp32 with shared heads of 64 (33 spilled): 259 and 280
+// at 768 workgroups, but 84 and 78 at 96, which have a CU each.
 template <int IO, int DK, bool GROUP>
 constexpr int grads_per_cu() {
     return DK > 64 ? (GROUP || IO == IO_F32 ? 1 : 2) : (GROUP && IO == IO_F32 ? 1 : 2);
@@ -356,10 +357,11 @@ constexpr int grads_per_cu() {
 // d0 + 16 (i/4) + 4 g + i%4.  They and dO have one scale each.  The value heads
 // that share the key head follow one another, and their parts of dQ and dK are
 // summed in registers, in a fixed order; with one (GROUP false) R1 and R3 become
-// dQ and dK.  64 x 1024 tokens of 6 heads of 128 in bf16 take 510 to 530 us for
-// the 1.9 GB it reads (S0 and D, in fp32 for dg's sums, are 1.6 of them), 3.7
-// TB/s: its registers allow two workgroups a CU, which wait 40 % of the time,
-// the vector unit (the f16 terms) is busy 40 %, the matrix cores 15 %.
+// dQ and dK.  64 x 1024 tokens of 6 heads of 128 in bf16 take 510 to 560 us for
+// the 1.6 GB it reads (S0 and D, in fp32 for dg's sums, are 0.8 of them, U and dY
+// 0.4) and the 0.2 it writes, 3.2 to 3.5 TB/s: its registers allow two workgroups a
+// CU, which wait 38 % of the time; the vector unit (the f16 terms) is busy 38 %, the
+// matrix cores 15 %, and 41 % of the LDS cycles are bank conflicts.
 template <int IO, int DK, bool GROUP>
 __global__ __launch_bounds__(256, (grads_per_cu<IO, DK, GROUP>()))
 void delta_grads_kernel(DeltaGradParams gp) {

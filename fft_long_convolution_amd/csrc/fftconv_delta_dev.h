@@ -611,7 +611,8 @@ __device__ __forceinline__ void store_state(char* s, uint32_t bytes, uint32_t la
 // 32 kb + 8 g + 4 j + i, i < 4, of column c: a lane's accumulators in two
 // 16-byte stores, each of them 1 KiB in a row for the wave (with a lane's two
 // side by side the walks of 64 x 1024 tokens of 6 heads of 128 took 368 and 392
-// us, so 346 and 360), and what RowTiles puts into LDS for transposed reads.
+// us, so 346 and 360 when both were tried), and what RowTiles puts into LDS for
+// transposed reads.
 __host__ __device__ __forceinline__ long long saved_floats(int rows, int Dv) {
     const int cols = (Dv + 15) / 16 * 16;
     return (long long)(rows + 2) * cols;

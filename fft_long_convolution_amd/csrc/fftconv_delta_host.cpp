@@ -201,18 +201,18 @@ size_t delta_slots(const fftconv_delta_desc* d) {
 // outputs; the backward walk likewise.  The number of segments is the one of
 // least time by walk_us() and the steps of the join (2.5 us at D_k = 64, 7 at
 // 128), 1 where that is least.  bf16, forward: 4 x 32768 tokens of 4 heads of
-// 128, 16 segments, 0.69 ms, uncut 2.1; 1 x 4096 x 8: 6, 0.12 ms, uncut 0.26;
-// 16 x 8192 x 6: uncut 0.65, in three 0.91.  With the gradients, fp32, 2 x 1501
-// tokens of 4 heads of 64: 8 segments, 132 us, uncut some 230.
+// 128, 16 segments, 0.73 ms, uncut 1.75; 1 x 4096 x 8: 8, 0.12 ms, uncut 0.22;
+// 16 x 8192 x 6: uncut 0.63, in three 1.06.  With the gradients, fp32, 2 x 1501
+// tokens of 4 heads of 64: 8 segments, 137 us, uncut 229.
 //
 // Where the chains are more than the CUs, a last round of few would take as
 // long as a full one.  So equal chains are cut into pieces, which launches of
 // at most one workgroup a CU take round by round (piece_of() in the kernels).  A
 // round costs some 7 us beside its chunks.  Of calls, bf16 and heads of 128, in
-// pieces and whole: 64 x 1024 tokens of 6 heads, 384 chains in halves, 264 and
-// 276 us (with gradients 1169 and 1208); 33 x 4096 of 8, 264 chains, 0.73 and
-// 0.88 ms (3.20 and 3.64); 10 x 8192 of 32 in f16, 320 chains, 2.37 and 3.21
-// (8.8 and 10.9).
+// pieces and whole: 64 x 1024 tokens of 6 heads, 384 chains in halves, 309 and
+// 322 us (with gradients 1188 and 1198); 33 x 4096 of 8, 264 chains, 0.84 and
+// 1.01 ms (3.24 and 3.61); 10 x 8192 of 32 in f16, 320 chains, 1.69 and 2.01
+// (7.3 and 8.3).
 struct Cut {
     size_t per;             // chunks of a segment or piece
     int pieces, rounds, waves;
