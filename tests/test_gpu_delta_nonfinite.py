@@ -117,3 +117,38 @@ def test_no_gradient_looks_like_a_result(dtype, which, value):
             rest = [j for j in range(T) if j // 64 != t // 64]
             if which in (Q, V):
                 assert torch.equal(there[0, rest], fin[0, rest]), i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(3, 200, 96, 96, 16, 24), (2, 130, 24, 72, 128, 128)], ids=str)
+def test_other_heads_of_many(shape, dtype):
+    # chains in pieces, and eight waves of 128 columns: all chains but one have
+    # the bits of the call without NaN, that one's tokens before it their values
+    b, t, h = 1, 101, 5
+    ins = gpu(*delta_inputs(sum(shape), *shape, dtype))
+    op = rule(shape[4], shape[5], dtype)
+    d = torch.randn(ins[2].shape, device="cuda").to(ins[2].dtype)
+
+    def run(v):
+        a = (*ins[:2], v, *ins[3:5])
+        o, S = op.forward(*a, initial_state=ins[5])
+        o2, S2, saved = op.forward_train(*a, initial_state=ins[5])
+        return [o, o2, S, S2], op.backward(*a, d, saved, d_final_state=S, initial_state=ins[5])
+
+    (clean, _), bad = run(ins[2]), ins[2].clone()
+    bad[b, t, h, 3] = math.nan
+    got, grads = run(bad)
+    for x, y in zip(got[:2], clean[:2]):
+        lost = torch.zeros(x.shape, dtype=torch.bool, device="cuda")
+        lost[b, t:, h, 3] = True
+        assert torch.equal(torch.isnan(x), lost)
+        e = (x[b, :t, h, 3].double() - y[b, :t, h, 3].double()).norm()
+        assert e <= TOL[dtype] * y[b, :t, h, 3].double().norm()
+        lost[b, :, h, 3] = True
+        assert torch.equal(x[~lost], y[~lost])
+    for x, y in zip(got[2:], clean[2:]):
+        lost = torch.zeros(x.shape, dtype=torch.bool, device="cuda")
+        lost[b, h, :, 3] = True
+        assert torch.equal(torch.isnan(x), lost) and torch.equal(x[~lost], y[~lost])
+    assert not torch.isfinite(grads[0][b, t, h // (shape[3] // shape[2])]).any()
+    assert torch.isfinite(grads[2][0]).all()
