@@ -338,10 +338,10 @@ __device__ __forceinline__ void unpack_pieces(const P (&x)[2], bool ok0, bool ok
 
 // Workgroups on a CU: two where 256 registers a lane hold what it needs, nearly.
 // Backward calls with two and with one: 32 x 1024 tokens of 6 heads of 64, 3 key
-// heads, bf16 (8 registers spilled) 190 and 240 us, 6 key heads, fp32 (none) 231 and
-// 296; 64 x 1024 of 6 heads of 128, bf16 (4 spilled) 754 and 937, with 3 key heads
-// (117 spilled) 947 and 900.  fp32 with shared heads of 64 (33 spilled): 259 and 280
-// at 768 workgroups, but 84 and 78 at 96, which have a CU each.
+// heads, bf16 (20 registers spilled) 206 and 237 us, 6 key heads, fp32 (none) 232 and
+// 297; 64 x 1024 of 6 heads of 128, bf16 (6 spilled) 764 and 930, with 3 key heads
+// (134 spilled) 1020 and 885.  fp32 with shared heads of 64 (46 spilled): 271 and 280
+// at 768 workgroups, but 85 and 78 at 96, which have a CU each.
 template <int IO, int DK, bool GROUP>
 constexpr int grads_per_cu() {
     return DK > 64 ? (GROUP || IO == IO_F32 ? 1 : 2) : (GROUP && IO == IO_F32 ? 1 : 2);
@@ -372,9 +372,10 @@ void delta_grads_kernel(DeltaGradParams gp) {
     constexpr int NS = Regs::NS, GT = GROUP ? ST : 1;
     extern __shared__ uint4 lds[];
     __shared__ double G[kChunk];
-    __shared__ float bet[kChunk], colsum[4][kChunk], rowG[kChunk], rowB[kChunk];
+    __shared__ double colsum[4][kChunk], rowG[kChunk], red3[4];
+    __shared__ float bet[kChunk], rowB[kChunk];
     __shared__ float backK[kChunk], backQ[kChunk];
-    __shared__ float red[4], red3[4], big[5];
+    __shared__ float red[4], big[5];
     const unsigned units = (unsigned)p.slots * p.Hk, id = xcd_unit(blockIdx.x, units);
     if (id >= units) return;
     const long long slot = id / p.Hk;
@@ -630,8 +631,13 @@ void delta_grads_kernel(DeltaGradParams gp) {
         s1 *= bq;
         s2 *= bk;
         s3 *= bk;
-        // the 64 x 64 part: the lane's token is i, tile j's row 4 g + r is j
-        float sg = 0.f, sb = yv;
+        // The 64 x 64 part: the lane's token is i, tile j's row 4 g + r is j.
+        // dg is dG summed from the end, where a term of tokens i and j counts
+        // for the g between them alone: in all others it stands in a row and in
+        // a column, and has to leave nothing.  So these sums are of 64 bits; in
+        // 32 dg was off by 1e-7 of the terms, all of it where e^g is as small.
+        double sg = 0.;
+        float sb = yv;
         {
             dfloat4 kk[4], qk[4];
 #pragma unroll
@@ -661,51 +667,52 @@ void delta_grads_kernel(DeltaGradParams gp) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int j0 = tile_row(j, 4 * g);
-                float cs[4];
+                float t[4];
                 const dfloat4 bj = *(const dfloat4*)&backK[j0];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    float w = 0.f, f = 0.f, t = 0.f;
+                    float w = 0.f, f = 0.f;
+                    t[r] = 0.f;
                     if (j < jtiles && mine >= j0 + r) {
                         const float gam = decay(Gi - G[j0 + r]);
                         const float kij = kk[j][r] * (bk * bj[r]);
                         w = gam * (fp * Dp[j][r]);
                         const float x = mine > j0 + r ? gam * (fy * Dy[j][r]) : 0.f;
                         f = -b * x;
-                        t = w * (qk[j][r] * (bq * bj[r])) + f * kij;
-                        sg += t;
+                        t[r] = w * (qk[j][r] * (bq * bj[r])) + f * kij;
+                        sg += t[r];
                         sb -= x * kij;
                         F[mine][j0 + r] = f * bj[r];
                         if (mine > j0 + r) F[j0 + r][mine] = f * bk;
                     }
                     Dp[j][r] = w * bj[r];        // the lane's row of W
                     Wt[j0 + r][mine] = w * bq;
-                    cs[r] = t;
                 }
-                // sums over the wave's tokens
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    cs[r] = sum16(cs[r]);
-                    if (c == 0) colsum[wave][j0 + r] = cs[r];
-                }
+                // over the wave's tokens
+                const double cs = sum16_of4(t);
+                if ((c & 3) == 0) colsum[wave][j0 + (c >> 2)] = cs;
             }
         }
-        const float rg = sum_groups(sg + s1 - b * s2 - s3), rb = sum_groups(sb - s2);
-        s3 = sum_groups(s3);
+        const double s3_all = sum_groups((double)s3);
+        const double rg = sum_groups(sg + (s1 - b * s2)) - s3_all;
+        const float rb = sum_groups(sb - s2);
         if (g == 0) {
             rowG[mine] = rg;
             rowB[mine] = rb;
         }
         // the chunk's last decay
-        s3 = sum16(s3);
+        double s3_wave = s3_all + moved<0x128>(s3_all);
+        s3_wave += moved<0x141>(s3_wave);
+        s3_wave += moved<0xb1>(s3_wave);
+        s3_wave += moved<0x4e>(s3_wave);
         if (lane == 0) {
             red[wave] = sd;
-            red3[wave] = s3;
+            red3[wave] = s3_wave;
         }
         __syncthreads();
         if (wave == 0) {
-            double x = (double)rowG[lane] - (colsum[0][lane] + colsum[1][lane] + colsum[2][lane] +
-                                             colsum[3][lane]);
+            double x = rowG[lane] -
+                       (colsum[0][lane] + colsum[1][lane] + colsum[2][lane] + colsum[3][lane]);
             if (lane == 63)
                 x += (red3[0] + red3[1] + red3[2] + red3[3]) +
                      decay(last) * (red[0] + red[1] + red[2] + red[3]);

@@ -323,6 +323,34 @@ __device__ __forceinline__ float sum_groups(float a) {
                                                     false);
     return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
+// Sums in 64 bits.
+template <int DPP>
+__device__ __forceinline__ float moved(float a) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(a), DPP, 15, 15, true));
+}
+template <int DPP>
+__device__ __forceinline__ double moved(double a) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, a);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((uint32_t)u, DPP, 15, 15, true);
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((uint32_t)(u >> 32), DPP, 15, 15, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Of four values over the 16 lanes of a group: lane c gets the sum of t[c / 4].  Half
+// of them go to the lanes half a group away, then half of the rest.
+__device__ __forceinline__ double sum16_of4(const float (&t)[4]) {
+    const int c = threadIdx.x & 15;
+    const bool up = c & 8, odd = c & 4;
+    const float s0 = up ? t[0] : t[2], s1 = up ? t[1] : t[3];
+    const double a = (double)(up ? t[2] : t[0]) + moved<0x128>(s0);
+    const double b = (double)(up ? t[3] : t[1]) + moved<0x128>(s1);
+    double x = (odd ? b : a) + moved<0x141>(odd ? a : b);     // the mirrored eight
+    x += moved<0xb1>(x);                                       // and its four lanes
+    return x + moved<0x4e>(x);
+}
+__device__ __forceinline__ double sum_groups(double a) {
+    a += __shfl_xor(a, 32);
+    return a + __shfl_xor(a, 16);
+}
 // The larger magnitude; NaN where one of them is (fmaxf would drop it).
 __device__ __forceinline__ float max_nan(float a, float b) {
     return __builtin_elementwise_maximum(a, b);

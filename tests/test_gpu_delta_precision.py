@@ -108,3 +108,27 @@ def test_fp32_terms_of_tokens_of_all_sizes():
     want, = torch.autograd.grad((want * do.double()).sum(), leaf[:1])
     e = (dq - want) / size[:, None, None]
     assert e.norm() <= TOL["f32"] * (want / size[:, None, None]).norm()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decay_gradients_of_each_head(dtype):
+    # g around -rate: dg is e^g times something of order one, head by head.  The
+    # factors e^(G_i - G_j) are off by the rounding of their exponents, 23 / 2^24
+    # of themselves where e^-16 is the largest: within what fp32 outputs may be off.
+    rates = torch.tensor([0.01, 1.0, 4.0, 8.0, 16.0])
+    T, H, D = 150, len(rates), 64
+    q, k, v, g, beta, S = delta_inputs(51, 1, T, H, H, D, D, dtype)
+    g = -rates * (0.9 + 0.2 * torch.rand(1, T, H, generator=torch.Generator().manual_seed(2)))
+    gen = torch.Generator().manual_seed(3)
+    do = torch.randn(v.shape, generator=gen).to(v.dtype)
+    dS = torch.randn(S.shape, generator=gen)
+    op, a = rule(D, D, dtype), gpu(q, k, v, g, beta, S)
+    _, _, saved = op.forward_train(*a[:5], initial_state=a[5])
+    dg = op.backward(*a[:5], do.cuda(), saved, d_final_state=dS.cuda(), initial_state=a[5])[3]
+    leaf = double(q, k, v, g, beta, S)
+    leaf[3].requires_grad_()
+    o, F = delta(*leaf, None, D ** -0.5)
+    want, = torch.autograd.grad((o * do.double()).sum() + (F * dS.double()).sum(), leaf[3:4])
+    for h in range(H):
+        e = (dg[0, :, h].cpu().double() - want[0, :, h]).norm() / want[0, :, h].norm()
+        assert e <= TOL["f32"], (rates[h].item(), e.item())
