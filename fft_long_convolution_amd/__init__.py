@@ -11,18 +11,23 @@ ctypes binding over it that uses PyTorch only for device memory and streams.
 :mod:`fft_long_convolution_amd.delta` binds the token mixers that hybrid
 models put beside long convolutions: norms of queries and keys with the
 position rotation, and the gated delta rule.
+:mod:`fft_long_convolution_amd.decay` binds linear attention with a decay for
+each head and layer norm.
 Importing this package loads nothing; the library is opened on first use.
 """
 import importlib
 
-__all__ = ["FFTConv", "GatedDelta", "QKNorm", "delta", "fftconv", "inputs"]
+__all__ = ["DecayAttention", "FFTConv", "GatedDelta", "LayerNorm", "QKNorm", "decay", "delta",
+           "fftconv", "inputs"]
 
 
 def __getattr__(name):
-    if name in ("delta", "fftconv", "inputs"):
+    if name in ("decay", "delta", "fftconv", "inputs"):
         return importlib.import_module(__name__ + "." + name)
     if name == "FFTConv":
         return importlib.import_module(__name__ + ".fftconv").FFTConv
     if name in ("GatedDelta", "QKNorm"):
         return getattr(importlib.import_module(__name__ + ".delta"), name)
+    if name in ("DecayAttention", "LayerNorm"):
+        return getattr(importlib.import_module(__name__ + ".decay"), name)
     raise AttributeError(name)

@@ -22,7 +22,11 @@ SOURCES = [os.path.join(HERE, "csrc", "fftconv_host.cpp"),
            os.path.join(HERE, "csrc", "fftconv_delta_host.cpp"),
            os.path.join(HERE, "csrc", "fftconv_qknorm.hip"),
            os.path.join(HERE, "csrc", "fftconv_delta.hip"),
-           os.path.join(HERE, "csrc", "fftconv_delta_bwd.hip")]
+           os.path.join(HERE, "csrc", "fftconv_delta_bwd.hip"),
+           os.path.join(HERE, "csrc", "fftconv_decay_host.cpp"),
+           os.path.join(HERE, "csrc", "fftconv_layernorm.hip"),
+           os.path.join(HERE, "csrc", "fftconv_decay.hip"),
+           os.path.join(HERE, "csrc", "fftconv_decay_bwd.hip")]
 # per-source extra flags: the inner multi-pass kernel schedules best with the
 # max-ILP strategy (measured; the other kernels are slower with it)
 EXTRA = {"fftconv_inner.hip": ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]}

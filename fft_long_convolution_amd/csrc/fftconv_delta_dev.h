@@ -734,13 +734,8 @@ __device__ __forceinline__ double shifted(double x) {
     const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(u >> 32), DPP, 15, 15, true);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// Sum of the log decays up to the lane's token, in units of log 2 (decay()
-// makes factors of them).  Sums are fp64, so e^(G_i - G_j) is right to fp32
-// however much the chunk has decayed before; decays below -1e4 count as -1e4
-// (their factor is 0 in fp32 either way), so a reset (g = -inf) does not meet
-// itself as inf - inf.  NaN stays NaN.
-__device__ __forceinline__ double decay_sum(float g) {
-    double s = g < -1e4f ? -1e4f : g;
+// sum of the values of the lanes up to this one
+__device__ __forceinline__ double prefix_sum(double s) {
     // within each group of 16, then the groups before
     s += shifted<0x111>(s);
     s += shifted<0x112>(s);
@@ -751,7 +746,15 @@ __device__ __forceinline__ double decay_sum(float g) {
     if (lane >= 16) s += a;
     if (lane >= 32) s += b;
     if (lane >= 48) s += c;
-    return s * 1.4426950408889634074;
+    return s;
+}
+// Sum of the log decays up to the lane's token, in units of log 2 (decay()
+// makes factors of them).  Sums are fp64, so e^(G_i - G_j) is right to fp32
+// however much the chunk has decayed before; decays below -1e4 count as -1e4
+// (their factor is 0 in fp32 either way), so a reset (g = -inf) does not meet
+// itself as inf - inf.  NaN stays NaN.
+__device__ __forceinline__ double decay_sum(float g) {
+    return prefix_sum(g < -1e4f ? -1e4f : g) * 1.4426950408889634074;
 }
 __device__ __forceinline__ float decay(double g) { return __builtin_amdgcn_exp2f((float)g); }
 

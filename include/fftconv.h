@@ -403,9 +403,10 @@ fftconv_status fftconv_backward(fftconv_plan_t plan, const void *u,
 /* ------------------------------------------------------------------------
  * Token mixers beside the long convolution.  Hybrid models put layers of the
  * gated delta rule (a linear recurrence over a matrix-valued state for each
- * head) next to long-convolution layers; the calls below are that rule over
- * whole sequences and for single tokens, and the norms and position rotation
- * of its queries and keys.  They need no plan: a descriptor holds the sizes.
+ * head) or of linear attention with decays next to long-convolution layers; the
+ * calls below are these over whole sequences and for single tokens, the norms
+ * and position rotation of their queries and keys, and the layer norm of the
+ * tokens before them.  They need no plan: a descriptor holds the sizes.
  *
  * Conventions beyond those at the head of this file:
  *  - Strides are in elements; the last dimension is contiguous.  Strides are
@@ -564,6 +565,123 @@ fftconv_status fftconv_delta_step(const fftconv_delta_desc *desc, const void *q,
                                   const void *k, const void *v, const float *g,
                                   const float *beta, float *state, size_t pool,
                                   const long long *slots, void *o, void *stream);
+
+/* Sizes of the calls of linear attention with a decay for each head. */
+typedef struct fftconv_decay_desc {
+    fftconv_dtype dtype;      /* of q, k, v, o and their gradients          */
+    size_t B, T;              /* batch rows and tokens of a row             */
+    size_t Hk, Hv;            /* heads of q and k, and of v: Hv a multiple of
+                                 Hk; value head h reads head h / (Hv/Hk)    */
+    size_t Dk, Dv;            /* head sizes, multiples of 8; Dk <= 256, and
+                                 Dv <= 1024 (backward: 256)                 */
+    size_t sequences;         /* 0: each batch row is a sequence.  n > 0: B
+                                 = 1 and the row packs n sequences whose
+                                 bounds are in cu_seqlens                   */
+    float scale;              /* of the outputs, e.g. Dk^(-1/2)             */
+    int fixed_decay;          /* g (and dg) is [Hv]: one log decay a head   */
+    long long q_stride[3];    /* batch, token, head; token strides (and      */
+    long long k_stride[3];    /* Hv Dv, Hv Dk) below 2^24                    */
+    long long v_stride[3];
+    int clear_unheld;         /* packed sequences: tokens before the first and
+                                 behind the last bound have o = 0 (else o
+                                 keeps there what it holds)                 */
+} fftconv_decay_desc;
+
+/* Linear attention with a decay for each head, over sequences.  For each value
+ * head, from a state S [Dk][Dv], every token does
+ *     S <- e^g S + k v^T;  o = scale S^T q.
+ *  q, k [B][T][Hk][Dk], v [B][T][Hv][Dv]: strided as the descriptor says.
+ *  g (log decay): fp32 [B][T][Hv], contiguous, or [Hv] where the decay is fixed.
+ *     It may be -inf (the state is dropped) and positive, as far as states and
+ *     decays between two tokens stay finite.
+ *  cu_seqlens: device, int64 [sequences + 1], ascending from 0 to T
+ *     (sequences may be empty); NULL when sequences = 0.  Bounds outside
+ *     [0, T] or out of order are clamped on the device.
+ *  initial_state: fp32 [rows][Hv][Dk][Dv], rows = sequences or B; NULL for 0.
+ *  o [B][T][Hv][Dv].  Tokens that no sequence holds are not written, or 0
+ *     where the descriptor asks for that.
+ *  final_state: fp32, as initial_state; NULL to skip it.
+ *  workspace: fftconv_decay_workspace_bytes(desc) bytes.
+ * States, decays and sums are fp32 or wider whatever the I/O type; operands of the
+ * 16-bit matrix products that are not of the I/O type are split into two or three
+ * terms (22 to 26 bits in states, 17 in what meets 16-bit outputs only); outputs are
+ * rounded to their type once.  Long sequences of few heads are cut into segments:
+ * equal calls give equal bits.
+ *  A NaN or infinity reaches what it reaches in the formulas: from k or g its
+ * token's outputs, the later ones of the sequence and the state (from k in its
+ * row); from v the same in its column; from q its token's outputs.  They are not
+ * finite then (NaN also where the formula gives an infinity); all others are as
+ * without it. */
+fftconv_status fftconv_decay_forward(const fftconv_decay_desc *desc, const void *q,
+                                     const void *k, const void *v, const float *g,
+                                     const long long *cu_seqlens, const float *initial_state,
+                                     void *o, float *final_state, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+size_t fftconv_decay_workspace_bytes(const fftconv_decay_desc *desc);
+
+/* Gradients of fftconv_decay_forward, which saves nothing for them.
+ *  q .. initial_state: as given to the forward call.
+ *  d_o [B][T][Hv][Dv], contiguous; d_final_state: as final_state, or NULL
+ *     for 0.
+ *  dq, dk [B][T][Hk][Dk] (summed over the value heads that share the head,
+ *     in a fixed order), dv [B][T][Hv][Dv]; dg fp32 [B][T][Hv], or [Hv] where
+ *     the decay is fixed; d_initial_state: as initial_state, or NULL to skip it.
+ *  Tokens before the first and behind the last of cu_seqlens have gradients of 0.
+ *  workspace: fftconv_decay_backward_workspace_bytes(desc) bytes.
+ *  Gradients that a NaN or infinity reaches are not finite, and those of the other
+ * tokens of its 64 (counted from the sequence's first) need not be. */
+fftconv_status fftconv_decay_backward(const fftconv_decay_desc *desc, const void *q,
+                                      const void *k, const void *v, const float *g,
+                                      const long long *cu_seqlens, const float *initial_state,
+                                      const void *d_o, const float *d_final_state, void *dq,
+                                      void *dk, void *dv, float *dg, float *d_initial_state,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+size_t fftconv_decay_backward_workspace_bytes(const fftconv_decay_desc *desc);
+
+/* One token for each of desc->B requests (T must be 1) against a pool of
+ * states that is updated in place.
+ *  q, k, v, g: as above with T = 1.
+ *  state: fp32 [pool][Hv][Dk][Dv]; slots: device, int64 [B], the state of
+ *     each request (NULL: request i has state i).  A request whose slot is
+ *     outside [0, pool), such as -1 for padding, changes no state and its o
+ *     is 0.  Two requests of a call must not share a slot.
+ *  o [B][Hv][Dv]. */
+fftconv_status fftconv_decay_step(const fftconv_decay_desc *desc, const void *q, const void *k,
+                                  const void *v, const float *g, float *state, size_t pool,
+                                  const long long *slots, void *o, void *stream);
+
+/* Sizes of fftconv_layernorm_forward / _backward. */
+typedef struct fftconv_layernorm_desc {
+    fftconv_dtype dtype;      /* of x, y and their gradients                */
+    size_t rows, D;           /* D <= 16384                                 */
+    float eps;
+    long long x_stride;       /* elements between rows of x, any number from D
+                                 on (one row: unused)                       */
+} fftconv_layernorm_desc;
+
+/* Layer norm of token rows:
+ *     y = weight (x - m) / sqrt(s + eps) + bias,
+ * m the mean of the row's D elements and s the mean of (x - m)^2.
+ *  weight, bias: device, fp32 [D], each NULL for 1 and 0.
+ *  x [rows][D], strided; y [rows][D], contiguous.
+ * Arithmetic is fp32 with one rounding to the output's type.  Rows of which D and
+ * x_stride keep 16-byte alignment move in pieces of 16 bytes, others element by
+ * element. */
+fftconv_status fftconv_layernorm_forward(const fftconv_layernorm_desc *desc, const void *x,
+                                         const float *weight, const float *bias, void *y,
+                                         void *stream);
+
+/* Bytes of the workspace of fftconv_layernorm_backward, which needs one where
+ * dweight or dbias is asked for (NULL otherwise). */
+size_t fftconv_layernorm_workspace_bytes(const fftconv_layernorm_desc *desc);
+
+/* Gradients of fftconv_layernorm_forward from dy (contiguous): dx (contiguous),
+ * dweight and dbias (fp32 [D], each NULL to skip it).  The sums over the rows run
+ * in a fixed order: equal inputs give equal bits. */
+fftconv_status fftconv_layernorm_backward(const fftconv_layernorm_desc *desc, const void *x,
+                                          const float *weight, const void *dy, void *dx,
+                                          float *dweight, float *dbias, void *workspace,
+                                          size_t workspace_bytes, void *stream);
 
 /* Static, human-readable text for a status code. */
 const char *fftconv_status_string(fftconv_status status);
