@@ -40,7 +40,8 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
                                                      const Factors<C>& F, float scale, int wave,
                                                      float (*part)[C]) {
     constexpr int KT = C / 16;
-    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int lane = fresh_lane(), g = lane >> 4, c = lane & 15;
+    const RowReader<IO, DA, 16> rows(lane);
     if (NW > KT && wave >= KT) return;
 #pragma unroll
     for (int j = 0; j < (KT + NW - 1) / NW; ++j) {
@@ -50,14 +51,15 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
         for (int kt = 0; kt < KT; ++kt) vd[kt] = kq[kt] = dfloat4{0, 0, 0, 0};
 #pragma unroll
         for (int kb = 0; kb < DA / 32; ++kb) {
-            const Frag<IO> b = row_frag<IO, DA>(V, 16 * qt + c, 32 * kb + 8 * g);
-            const Frag<IO> b2 = row_frag<IO, DA>(K, 16 * qt + c, 32 * kb + 8 * g);
+            const Frag<IO> b = rows.get(V, 16 * qt, 32 * kb);
+            const Frag<IO> b2 = rows.get(K, 16 * qt, 32 * kb);
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
                 if (kt >= qt) {
-                    vd[kt] = mma16<IO>(row_frag<IO, DA>(DO, 16 * kt + c, 32 * kb + 8 * g), b, vd[kt]);
-                    kq[kt] = mma16<IO>(row_frag<IO, DA>(Q, 16 * kt + c, 32 * kb + 8 * g), b2, kq[kt]);
+                    vd[kt] = mma16<IO>(rows.get(DO, 16 * kt, 32 * kb), b, vd[kt]);
+                    kq[kt] = mma16<IO>(rows.get(Q, 16 * kt, 32 * kb), b2, kq[kt]);
                 }
+            __builtin_amdgcn_sched_barrier(0);
         }
         const int i = 16 * qt + c, iw = F.whole[i];
         const float ir = F.rest[i];
@@ -106,7 +108,7 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             if (kt < (qt & ~1)) continue;
-            put_scores<IO, C>(P, qt, kt, to, vd[kt]);
+            put_scores<IO, C>(P, lane, qt, kt, to, vd[kt]);
         }
     }
 }
@@ -203,10 +205,13 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
         dfloat16 acc[C / 32];
         if (keys) {
             make_scores_and_sums<IO, DA, C, RW>(V, DO, K, Q, P, back[1], fac, f.scale, wave, part);
+            __builtin_amdgcn_sched_barrier(0);
             state_product<IO, DA, C, IO == IO_BF16 ? 2 : Kind<IO>::NS>(V, X, fac, acc);
         } else {
             make_scores<IO, DA, C, RW, true>(K, Q, P, back[0], fac, f.scale, wave);
+            __builtin_amdgcn_sched_barrier(0);
             state_product<IO, DA, C, Kind<IO>::NS>(K, X, fac, acc);
+            __builtin_amdgcn_sched_barrier(0);
             row_dots<IO, DA, C>(V, mine < DA ? mine : 0, acc, dots[wave]);
         }
         __syncthreads();
@@ -230,13 +235,14 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
         }
         Frag<IO> val[C / 16];
         const int from = mine < DA ? mine : 0;
+        const ColReader<IO, DA, false> vcols(fresh_lane());
 #pragma unroll
-        for (int kb = 0; kb < C / 16; ++kb)
-            val[kb] = col_frag<IO, DA, false>(keys ? Q : DO, 16 * kb, from);
+        for (int kb = 0; kb < C / 16; ++kb) val[kb] = vcols.get(keys ? Q : DO, 16 * kb, from);
         scores_product<IO, C, true>(P, back[keys], val, fac.unbounded, acc);
-        store_rows<IO, C>(keys ? (wide ? p.dk_heads : p.dk) : p.dv,
-                          ((token0 + at) * f.Hv + h) * cols + col, (long long)f.Hv * cols, wide, ok,
-                          n, acc);
+        const long long row = (long long)f.Hv * cols * (wide ? 4 : kB);
+        store_rows<IO, C>((char*)(keys ? (wide ? p.dk_heads : p.dk) : p.dv) + (token0 + at) * row,
+                          row, h * cols + col, wide, ok, n, acc);
+        __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(keys ? DO : Q, val, fac, X);
         if (tid < 64 && more) factors(F[(i + 1) & 1], g, C);
         __syncthreads();

@@ -98,14 +98,23 @@ __device__ __forceinline__ uint32_t swirl(uint32_t t) {
     if constexpr (PIECES == 8) return ((t >> 3) & 1) | ((t >> 1) & 2) | ((t << 1) & 4);
     else return ((t >> 3) & 1) | ((t >> 1) & 2) | ((t & 1) << 2) | ((t & 2) << 2);
 }
+// Bases are of a lane; which of its pieces is read is then an exclusive or with a
+// constant, which token an immediate offset: swirl() is linear and sees four bits.
 template <int IO, int D>
 struct Rows {
-    static constexpr int kB = Kind<IO>::kB, kPieces = D * kB / 16;
+    static constexpr int kB = Kind<IO>::kB, kPieces = D * kB / 16, kRow = D * kB;
     // byte offset of piece u of a token
     static __device__ __forceinline__ uint32_t at(uint32_t token, uint32_t u) {
-        return token * (D * kB) + ((u ^ swirl<kPieces>(token)) << 4);
+        return token * kRow + ((u ^ swirl<kPieces>(token)) << 4);
     }
 };
+// The lane, unknown to the compiler: what follows from it is made where it is
+// used instead of being kept in registers over the whole walk.
+__device__ __forceinline__ int fresh_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
 
 // Eight consecutive elements or k, as an operand.
 template <int IO>
@@ -122,54 +131,74 @@ __device__ __forceinline__ void unpack_frag(const Frag<IO>& f, float (&x)[8]) {
         unpack8<IO>(&f.v, x);
     }
 }
-// elements e .. e + 7 (e a multiple of eight) of a token
-template <int IO, int D>
-__device__ __forceinline__ Frag<IO> row_frag(const char* m, int token, int e) {
-    Frag<IO> f;
-    if constexpr (IO == IO_F32) {
-        f.a = *(const dfloat4*)(m + Rows<IO, D>::at(token, e / 4));
-        f.b = *(const dfloat4*)(m + Rows<IO, D>::at(token, e / 4 + 1));
-    } else {
-        f.v = *(const du4*)(m + Rows<IO, D>::at(token, e / 8));
+// Rows as operands with k along the elements: lane (g, c), of lanes in groups of G,
+// has token t0 + c at elements e0 + 8g + i, i < 8; t0 a multiple of 16, e0 of 16.
+template <int IO, int D, int G>
+struct RowReader {
+    uint32_t base;
+    __device__ __forceinline__ explicit RowReader(int lane)
+        : base(Rows<IO, D>::at(lane & (G - 1), (lane / G) * (IO == IO_F32 ? 2 : 1))) {}
+    __device__ __forceinline__ Frag<IO> get(const char* m, int t0, int e0) const {
+        Frag<IO> f;
+        if constexpr (IO == IO_F32) {
+            const char* s = m + t0 * Rows<IO, D>::kRow;
+            f.a = *(const dfloat4*)(s + (base ^ (uint32_t)(e0 << 2)));
+            f.b = *(const dfloat4*)(s + (base ^ (uint32_t)(e0 << 2 | 16)));
+        } else {
+            f.v = *(const du4*)(m + t0 * Rows<IO, D>::kRow + (base ^ (uint32_t)(e0 << 1)));
+        }
+        return f;
     }
-    return f;
-}
-// Lane (g, c): tokens t0 + 8g + i, i < 8, at element e0 + c, or, STATE, at the
-// element that row c of a tile of the state stands for.
+};
+// Rows as operands with k along the tokens: lane (g, c) has tokens t0 + 8g + i, i < 8,
+// at element e0 + c, or, STATE, at the element that row c of a tile of the state
+// stands for; t0 a multiple of 16, e0 of 32.
 template <int IO, int D, bool STATE>
-__device__ __forceinline__ Frag<IO> col_frag(const char* m, int t0, int e0) {
-    const int lane = threadIdx.x & 63;
-    Frag<IO> f;
-    if constexpr (IO == IO_F32) {
-        const int c = lane & 31;
-        const int e = e0 + (STATE ? (c & 19) | ((c & 8) >> 1) | ((c & 4) << 1) : c);
-        const int t = t0 + 8 * (lane >> 5);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = *(const float*)(m + Rows<IO, D>::at(t + i, e >> 2) + 4 * (e & 3));
-            if (i < 4) f.a[i & 3] = x; else f.b[i & 3] = x;
+struct ColReader {
+    typedef Rows<IO, D> R;
+    uint32_t base;
+    __device__ __forceinline__ explicit ColReader(int lane) {
+        if constexpr (IO == IO_F32) {
+            const int c = lane & 31;
+            const int e = STATE ? (c & 19) | ((c & 8) >> 1) | ((c & 4) << 1) : c;
+            base = R::at(8 * (lane >> 5), e >> 2) + 4 * (e & 3);
+        } else {
+            // each read takes, from 16 lanes, four tokens by four pieces of four
+            // elements, and gives lane j the four tokens' element j of the pieces in
+            // the lanes' order: the state's order swaps the middle two
+            const int j = lane & 15;
+            int piece = j & 3;
+            if (STATE) piece = (piece >> 1) | ((piece & 1) << 1);
+            base = R::at(8 * (lane >> 5) + (j >> 2), 2 * ((lane >> 4) & 1) + (piece >> 1)) +
+                   8 * (piece & 1);
         }
-    } else {
-        // each read takes, from 16 lanes, four tokens by four pieces of four
-        // elements, and gives lane j the four tokens' element j of the pieces in
-        // the lanes' order: the state's order swaps the middle two
-        typedef short s4 __attribute__((ext_vector_type(4)));
-        const int j = lane & 15, t = t0 + 8 * (lane >> 5) + (j >> 2);
-        int piece = j & 3;
-        if (STATE) piece = (piece >> 1) | ((piece & 1) << 1);
-        const int u = (e0 >> 3) + 2 * ((lane >> 4) & 1) + (piece >> 1);
-        uint2 r[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const char* s = m + Rows<IO, D>::at(t + 4 * half, u) + 8 * (piece & 1);
-            r[half] = __builtin_bit_cast(
-                uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                           (__attribute__((address_space(3))) s4*)s));
-        }
-        f.v = du4{r[0].x, r[0].y, r[1].x, r[1].y};
     }
-    return f;
-}
+    __device__ __forceinline__ Frag<IO> get(const char* m, int t0, int e0) const {
+        const char* s = m + t0 * R::kRow;
+        Frag<IO> f;
+        if constexpr (IO == IO_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = *(const float*)(
+                    s + i * R::kRow + (base ^ (uint32_t)(e0 << 2) ^ (swirl<R::kPieces>(i) << 4)));
+                if (i < 4) f.a[i & 3] = x; else f.b[i & 3] = x;
+            }
+        } else {
+            typedef short s4 __attribute__((ext_vector_type(4)));
+            uint2 r[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const char* x = s + 4 * half * R::kRow +
+                                (base ^ (uint32_t)(e0 << 1) ^ (swirl<R::kPieces>(4 * half) << 4));
+                r[half] = __builtin_bit_cast(
+                    uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                               (__attribute__((address_space(3))) s4*)x));
+            }
+            f.v = du4{r[0].x, r[0].y, r[1].x, r[1].y};
+        }
+        return f;
+    }
+};
 
 // C tokens of rows on their way from memory to LDS, by N threads (tid < N):
 // tokens from n on and pieces from the row's end on are 0.
@@ -178,30 +207,27 @@ struct Moving {
     static constexpr int kPieces = Rows<IO, D>::kPieces, kMine = C * kPieces / N;
     static_assert(C * kPieces % N == 0, "threads share the pieces evenly");
     du4 r[kMine];
+    static constexpr int kStep = N / kPieces;           // tokens between a thread's pieces
+    static_assert(N % kPieces == 0, "a thread keeps its piece");
     __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int pieces,
                                          int tid) {
         const char* p = x.at(token);
         const uint32_t stride = (uint32_t)x.bytes;
+        const int u = tid % kPieces, left = u < pieces ? n - tid / kPieces : 0;
+        const uint32_t mine = (uint32_t)(tid / kPieces) * stride + 16u * u;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-            const int i = j * N + tid, t = i / kPieces, u = i % kPieces;
-            const bool ok = t < n && u < pieces;
-            r[j] = *(const du4*)(p + (ok ? t * stride + 16u * u : 0u));
-        }
+        for (int j = 0; j < kMine; ++j)
+            r[j] = *(const du4*)(p + (j * kStep < left ? mine + j * kStep * stride : 0u));
         if (n >= C && pieces == kPieces) return;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-            const int i = j * N + tid, t = i / kPieces, u = i % kPieces;
+        for (int j = 0; j < kMine; ++j)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) r[j][w] = t < n && u < pieces ? r[j][w] : 0;
-        }
+            for (int w = 0; w < 4; ++w) r[j][w] = j * kStep < left ? r[j][w] : 0;
     }
     __device__ __forceinline__ void store(char* m, int tid) const {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-            const int i = j * N + tid;
-            *(du4*)(m + Rows<IO, D>::at(i / kPieces, i % kPieces)) = r[j];
-        }
+        for (int j = 0; j < kMine; ++j)
+            *(du4*)(m + Rows<IO, D>::at(j * kStep + tid / kPieces, tid % kPieces)) = r[j];
     }
     // whether an element is infinite or NaN
     __device__ __forceinline__ bool unbounded() const {
@@ -358,17 +384,17 @@ template <int IO, int C>
 struct Scores {
     static constexpr int kBlock = 64 * (IO == IO_F32 ? 32 : 16), kBlocks = (C / 32) * (C / 16);
     static constexpr int kTerm = kBlock * kBlocks, kBytes = kTerm * Kind<IO>::NP;
-    static __device__ __forceinline__ Frag<IO> get(const char* P, int term, int m, int kb) {
-        return *(const Frag<IO>*)(P + term * kTerm +
-                                  ((m * (C / 16) + kb) * 64 + (threadIdx.x & 63)) *
-                                      (int)sizeof(Frag<IO>));
+    static __device__ __forceinline__ Frag<IO> get(const char* P, int lane, int term, int m, int kb) {
+        return *(const Frag<IO>*)(P + term * kTerm + (m * (C / 16) + kb) * kBlock +
+                                  lane * (int)sizeof(Frag<IO>));
     }
 };
 // The lane's rows 16 kt + 4 g + r of B, r < 4, for its row 16 qt + c of A.
 template <int IO, int C>
-__device__ __forceinline__ void put_scores(char* P, int qt, int kt, float to, dfloat4 p) {
+__device__ __forceinline__ void put_scores(char* P, int lane, int qt, int kt, float to,
+                                           dfloat4 p) {
     constexpr int NP = Kind<IO>::NP;
-    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int g = lane >> 4, c = lane & 15;
     const int place = ((qt >> 1) * (C / 16) + kt) * 64 + (g >> 1) * 32 + 16 * (qt & 1) + c;
     if constexpr (IO == IO_F32) {
         *(dfloat4*)(P + place * 32 + (g & 1) * 16) = p;
@@ -386,7 +412,8 @@ template <int IO, int DA, int C, int NW, bool REV>
 __device__ __forceinline__ void make_scores(const char* A, const char* B, char* P, float* back,
                                             const Factors<C>& F, float scale, int wave) {
     constexpr int KT = C / 16;
-    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int lane = fresh_lane(), g = lane >> 4, c = lane & 15;
+    const RowReader<IO, DA, 16> rows(lane);
     if (NW > KT && wave >= KT) return;
 #pragma unroll
     for (int j = 0; j < (KT + NW - 1) / NW; ++j) {
@@ -396,12 +423,12 @@ __device__ __forceinline__ void make_scores(const char* A, const char* B, char* 
         for (int kt = 0; kt < KT; ++kt) acc[kt] = dfloat4{0, 0, 0, 0};
 #pragma unroll
         for (int kb = 0; kb < DA / 32; ++kb) {
-            const Frag<IO> b = row_frag<IO, DA>(A, 16 * qt + c, 32 * kb + 8 * g);
+            const Frag<IO> b = rows.get(A, 16 * qt, 32 * kb);
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
                 if (REV ? kt >= qt : kt <= qt)
-                    acc[kt] = mma16<IO>(row_frag<IO, DA>(B, 16 * kt + c, 32 * kb + 8 * g), b,
-                                        acc[kt]);
+                    acc[kt] = mma16<IO>(rows.get(B, 16 * kt, 32 * kb), b, acc[kt]);
+            __builtin_amdgcn_sched_barrier(0);
         }
         const int i = 16 * qt + c, iw = F.whole[i];
         const float ir = F.rest[i];
@@ -432,7 +459,7 @@ __device__ __forceinline__ void make_scores(const char* A, const char* B, char* 
         // with the zeros beside the diagonal within a block of 32
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
-            if (REV ? kt >= (qt & ~1) : kt <= (qt | 1)) put_scores<IO, C>(P, qt, kt, to, acc[kt]);
+            if (REV ? kt >= (qt & ~1) : kt <= (qt | 1)) put_scores<IO, C>(P, lane, qt, kt, to, acc[kt]);
     }
 }
 
@@ -489,7 +516,8 @@ struct State {
 template <int IO, int DA, int C, int NS>
 __device__ __forceinline__ void state_product(const char* A, const State<DA>& S, const Factors<C>& F,
                                               dfloat16 (&acc)[C / 32]) {
-    const int lane = threadIdx.x & 63, g = lane >> 5, c = lane & 31;
+    const int lane = fresh_lane(), g = lane >> 5;
+    const RowReader<IO, DA, 32> rows(lane);
     float back = 1.f, to = 1.f;
     if constexpr (IO == IO_F16) {
         const Scale sc = scale_to(S.largest());
@@ -512,11 +540,12 @@ __device__ __forceinline__ void state_product(const char* A, const State<DA>& S,
             Frag<IO> a[C / 32];
 #pragma unroll
             for (int m = 0; m < C / 32; ++m)
-                a[m] = row_frag<IO, DA>(A, 32 * m + c, 32 * i + 16 * x + 8 * g);
+                a[m] = rows.get(A, 32 * m, 32 * i + 16 * x);
 #pragma unroll
             for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
                 for (int m = 0; m < C / 32; ++m) acc[m] = mma32<IO>(a[m], b[n], acc[m]);
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
     for (int m = 0; m < C / 32; ++m)
@@ -538,7 +567,7 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
                                                const Frag<IO> (&values)[C / 16], bool unbounded,
                                                dfloat16 (&acc)[C / 32]) {
     constexpr int NP = Kind<IO>::NP, KB = C / 16;
-    const int g = (threadIdx.x & 63) >> 5;
+    const int lane = fresh_lane(), g = lane >> 5;
     Frag<IO> v[KB];
     int bad = REV ? -1 : C;            // the first (last) such token of the column
 #pragma unroll
@@ -572,7 +601,7 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
         for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
             for (int kb = REV ? 2 * m : 0; kb < (REV ? KB : 2 * m + 2); ++kb)
-                s = mma32<IO>(Scores<IO, C>::get(P, n, m, kb), v[kb], s);
+                s = mma32<IO>(Scores<IO, C>::get(P, lane, n, m, kb), v[kb], s);
         if constexpr (IO == IO_F16) {
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -594,71 +623,89 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
     }
 }
 
+// eight values of the tokens t .. t + 7 times their w
+template <int IO, int C>
+__device__ __forceinline__ void weighted(const Frag<IO>& v, const Factors<C>& F, int t, float (&x)[8]) {
+    unpack_frag<IO>(v, x);
+    const float4 a = *(const float4*)&F.w[t], b = *(const float4*)&F.w[t + 4];
+    x[0] *= a.x; x[1] *= a.y; x[2] *= a.z; x[3] *= a.w;
+    x[4] *= b.x; x[5] *= b.y; x[6] *= b.z; x[7] *= b.w;
+}
 // S <- e^Dc S + B^T (w o V)
 template <int IO, int DA, int C>
 __device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&values)[C / 16],
                                              const Factors<C>& F, State<DA>& S) {
     constexpr int NS = Kind<IO>::NS, KB = C / 16;
-    const int g = (threadIdx.x & 63) >> 5;
+    const int lane = fresh_lane(), g = lane >> 5;
+    const ColReader<IO, DA, true> cols(lane);
     float all = F.all, to = 1.f, back = 1.f;
-    float x[KB][8];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        unpack_frag<IO>(values[kb], x[kb]);
-        const float4 a = *(const float4*)&F.w[16 * kb + 8 * g];
-        const float4 b = *(const float4*)&F.w[16 * kb + 8 * g + 4];
-        const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[kb][i] *= w[i];
-    }
     if constexpr (IO == IO_F16) {
         // the column's scale; values of less than 2^-24 of the state do not
         // reach it, and so do not ask for a larger one
         float largest = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < KB; ++kb) {
+            float x[8];
+            weighted<IO, C>(values[kb], F, 16 * kb + 8 * g, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) largest = fmaxf(largest, fabsf(x[kb][i]));
+            for (int i = 0; i < 8; ++i) largest = fmaxf(largest, fabsf(x[i]));
+        }
         largest = max_halves(largest);
         const Scale sc = scale_to(fmaxf(finite(largest) ? largest : 0.f, S.largest() * all * 0x1p-24f));
         to = sc.to;
         back = sc.back;
         all *= to;
     }
-    Frag<IO> v[KB][NS];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) terms<IO, NS>(x[kb], to, v[kb]);
-#pragma unroll
-    for (int i = 0; i < DA / 32; ++i) {
+    for (int i = 0; i < DA / 32; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) S.t[i][r] *= all;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            const Frag<IO> a = col_frag<IO, DA, true>(B, 16 * kb, 32 * i);
+    for (int kb = 0; kb < KB; ++kb) {
+        float x[8];
+        Frag<IO> v[NS];
+        weighted<IO, C>(values[kb], F, 16 * kb + 8 * g, x);
+        terms<IO, NS>(x, to, v);
+        Frag<IO> a[DA / 32];
 #pragma unroll
-            for (int n = NS - 1; n >= 0; --n) S.t[i] = mma32<IO>(a, v[kb][n], S.t[i]);
-        }
-        if constexpr (IO == IO_F16)
+        for (int i = 0; i < DA / 32; ++i) a[i] = cols.get(B, 16 * kb, 32 * i);
+#pragma unroll
+        for (int n = NS - 1; n >= 0; --n)
+#pragma unroll
+            for (int i = 0; i < DA / 32; ++i) S.t[i] = mma32<IO>(a[i], v[n], S.t[i]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (IO == IO_F16)
+#pragma unroll
+        for (int i = 0; i < DA / 32; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) S.t[i][r] *= back;
-    }
 }
 
-// the tile's rows to memory, those below n: type IO, or fp32 where wide
+// The rows below n to memory, `row` bytes apart: of type IO, or fp32 where wide.
 template <int IO, int C>
-__device__ __forceinline__ void store_rows(void* out, long long first, long long stride, bool wide,
-                                           bool ok, int n, const dfloat16 (&acc)[C / 32]) {
-    const int g = (threadIdx.x & 63) >> 5;
+__device__ __forceinline__ void store_rows(char* out, long long row, int col, bool wide, bool ok,
+                                           int n, const dfloat16 (&acc)[C / 32]) {
+    const int g = fresh_lane() >> 5;
+    if (!ok) return;
+    const uint32_t mine = (uint32_t)(4 * g) * (uint32_t)row + (uint32_t)col * (wide ? 4 : Kind<IO>::kB);
+    const int left = n - 4 * g;
+    const auto put = [&](bool whole, bool wide) {
 #pragma unroll
-    for (int m = 0; m < C / 32; ++m)
+        for (int m = 0; m < C / 32; ++m)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int t = 32 * m + 8 * (r >> 2) + 4 * g + (r & 3);
-            if (ok && t < n) {
-                if (wide) ((float*)out)[first + t * stride] = acc[m][r];
-                else io_store<IO>(out, first + t * stride, acc[m][r]);
+            for (int r = 0; r < 16; ++r) {
+                const int t = 32 * m + 8 * (r >> 2) + (r & 3);
+                char* to = out + t * row + mine;
+                if (whole || t < left) {
+                    if (wide) *(float*)to = acc[m][r];
+                    else io_store<IO>(to, 0, acc[m][r]);
+                }
             }
-        }
+    };
+    if (wide) put(n >= C, true);
+    else if (n >= C) put(true, false);
+    else put(false, false);
 }
 
 // Sums over the 16 lanes of a group: lane c gets that of t[c / 4].
@@ -681,9 +728,10 @@ __device__ __forceinline__ float sum_pair(float a) {
 template <int IO, int D, int C>
 __device__ __forceinline__ void row_dots(const char* X, int first, const dfloat16 (&acc)[C / 32],
                                          float* dots) {
-    const int lane = threadIdx.x & 63, g = lane >> 5, c = lane & 31;
+    typedef Rows<IO, D> R;
+    const int lane = fresh_lane(), g = lane >> 5, e = first + (lane & 31);
     constexpr int kPer = 16 / Kind<IO>::kB;
-    const int piece = (first + c) / kPer, in = (first + c) % kPer;
+    const uint32_t base = R::at(4 * g, e / kPer) + e % kPer * Kind<IO>::kB;
 #pragma unroll
     for (int m = 0; m < C / 32; ++m)
 #pragma unroll
@@ -692,7 +740,8 @@ __device__ __forceinline__ void row_dots(const char* X, int first, const dfloat1
 #pragma unroll
             for (int b = 0; b < 4; ++b)
                 x[b] = acc[m][4 * a + b] *
-                       io_load<IO>(X + Rows<IO, D>::at(32 * m + 8 * a + 4 * g + b, piece), in);
+                       io_load<IO>(X + (32 * m + 8 * a + b) * R::kRow +
+                                       (base ^ (swirl<R::kPieces>(8 * a + b) << 4)), 0);
             const float d = sum_pair(sums16_of4(x));
             if ((lane & 19) == 0) dots[32 * m + 8 * a + 4 * g + ((lane & 15) >> 2)] = d;
         }

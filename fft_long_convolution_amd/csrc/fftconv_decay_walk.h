@@ -141,7 +141,9 @@ __global__ __launch_bounds__(64 * W, DA > 128 ? 1 : 2) void decay_walk_kernel(De
         dfloat16 acc[C / 32];
         if (OUT) {
             make_scores<IO, DA, C, W, false>(A, B, P, back, f, p.ss, wave);
+            __builtin_amdgcn_sched_barrier(0);
             state_product<IO, DA, C, IO == IO_BF16 && !DOT ? 2 : Kind<IO>::NS>(A, S, f, acc);
+            __builtin_amdgcn_sched_barrier(0);
             if (DOT) row_dots<IO, 32 * W, C>(lds + L::kAtX, 32 * wave, acc, dots[wave]);
             __syncthreads();
         }
@@ -157,13 +159,16 @@ __global__ __launch_bounds__(64 * W, DA > 128 ? 1 : 2) void decay_walk_kernel(De
                 p.before[((long long)slice * p.Hv + h) * p.tokens + s.b * p.sp.T + s.t0 + at + t] = (float)d;
         }
         Frag<IO> vf[C / 16];
+        const ColReader<IO, 32 * W, false> vcols(fresh_lane());
 #pragma unroll
-        for (int kb = 0; kb < C / 16; ++kb) vf[kb] = col_frag<IO, 32 * W, false>(V, 16 * kb, 32 * wave);
+        for (int kb = 0; kb < C / 16; ++kb) vf[kb] = vcols.get(V, 16 * kb, 32 * wave);
         if (OUT) {
             scores_product<IO, C, false>(P, back, vf, f.unbounded, acc);
-            store_rows<IO, C>(p.out, ((s.b * p.sp.T + s.t0 + at) * p.Hv + h) * p.cols + col,
-                              (long long)p.Hv * p.cols, p.wide, ok, n, acc);
+            const long long row = (long long)p.Hv * p.cols * (p.wide ? 4 : kB);
+            store_rows<IO, C>((char*)p.out + (s.b * p.sp.T + s.t0 + at) * row, row,
+                              h * p.cols + col, p.wide, ok, n, acc);
         }
+        __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(B, vf, f, S);
         if (wave == 0 && more) factors(F[(ch + 1) & 1], g, m);
         __syncthreads();
