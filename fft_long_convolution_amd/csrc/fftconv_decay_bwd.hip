@@ -54,22 +54,18 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
             const Frag<IO> b = rows.get(V, 16 * qt, 32 * kb);
             const Frag<IO> b2 = rows.get(K, 16 * qt, 32 * kb);
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-                if (kt >= qt) {
-                    vd[kt] = mma16<IO>(rows.get(DO, 16 * kt, 32 * kb), b, vd[kt]);
-                    kq[kt] = mma16<IO>(rows.get(Q, 16 * kt, 32 * kb), b2, kq[kt]);
-                }
+            for (int kt = 0; kt < KT; ++kt) {
+                vd[kt] = mma16<IO>(rows.get(DO, 16 * kt, 32 * kb), b, vd[kt]);
+                kq[kt] = mma16<IO>(rows.get(Q, 16 * kt, 32 * kb), b2, kq[kt]);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
+        products_done();
         const int i = 16 * qt + c, iw = F.whole[i];
         const float ir = F.rest[i];
         float largest = 0.f, carry = 0.f;
 #pragma unroll
         for (int kt = KT - 1; kt >= 0; --kt) {
-            if (kt < qt) {
-                if (c == 0) *(float4*)&part[qt][16 * kt + 4 * g] = make_float4(0, 0, 0, 0);
-                continue;
-            }
             const int s0 = 16 * kt + 4 * g;
             const int4 sw = *(const int4*)&F.whole[s0];
             const float4 sr = *(const float4*)&F.rest[s0];
@@ -106,10 +102,7 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
             if (g == 0) back[i] = sc.back;
         }
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            if (kt < (qt & ~1)) continue;
-            put_scores<IO, C>(P, lane, qt, kt, to, vd[kt]);
-        }
+        for (int kt = 0; kt < KT; ++kt) put_scores<IO, C>(P, lane, qt, kt, to, vd[kt]);
     }
 }
 
@@ -128,8 +121,9 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
     const unsigned seg = u / slices / f.Hv;
     DecaySpan s;
     if (!segment_of(f.sp, seg, s)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6 & (RW - 1);
-    const bool keys = __builtin_amdgcn_readfirstlane(tid >> 6) >= RW;      // the role
+    const int tid = threadIdx.x, lane = tid & 63, place = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = place & (RW - 1);
+    const bool keys = place >= RW;      // the role
     const int first = slice * 32 * RW, mine = first + 32 * wave, col = mine + (lane & 31);
     const int cols = keys ? f.Dk : f.Dv, rows = keys ? f.Dv : f.Dk;
     const bool ok = col < cols, wide = keys && p.dk_heads;
@@ -174,7 +168,11 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
         mv.load(v, at, n, vp, tid);
         md.load(d, at, n, vp, tid);
     };
-    const auto put = [&](Factors<C>& F) {
+    const auto put = [&](Factors<C>& F, int n) {
+        mq.clear(n, kp, tid);
+        mk.clear(n, kp, tid);
+        mv.clear(n, vp, tid);
+        md.clear(n, vp, tid);
         mq.store(Q, tid);
         mk.store(K, tid);
         mv.store(V, tid);
@@ -190,7 +188,7 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
         fetch(at, n);
         if (tid < 64) factors(F[0], log_decay(at, n), n);
         __syncthreads();
-        put(F[0]);
+        put(F[0], n);
         __syncthreads();
     }
     for (int i = 0; i < chunks; ++i) {
@@ -239,14 +237,19 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
 #pragma unroll
         for (int kb = 0; kb < C / 16; ++kb) val[kb] = vcols.get(keys ? Q : DO, 16 * kb, from);
         scores_product<IO, C, true>(P, back[keys], val, fac.unbounded, acc);
-        const long long row = (long long)f.Hv * cols * (wide ? 4 : kB);
-        store_rows<IO, C>((char*)(keys ? (wide ? p.dk_heads : p.dk) : p.dv) + (token0 + at) * row,
-                          row, h * cols + col, wide, ok, n, acc);
+        __builtin_amdgcn_sched_barrier(0);
+        // K's and V's tiles are done with
+        const int ob = wide ? 4 : kB;
+        const long long row = (long long)f.Hv * cols * ob;
+        store_rows<IO, DA, C>(keys ? V : K, from, acc,
+                              (char*)(keys ? (wide ? (void*)p.dk_heads : p.dk) : p.dv) +
+                                  (token0 + at) * row + (long long)(h * cols + mine) * ob,
+                              row, (cols - mine) * ob / 16, wide, n);
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(keys ? DO : Q, val, fac, X);
         if (tid < 64 && more) factors(F[(i + 1) & 1], g, C);
         __syncthreads();
-        if (more) put(F[(i + 1) & 1]);
+        if (more) put(F[(i + 1) & 1], C);
         __syncthreads();
     }
     if (!keys && s.index == 0 && p.dinit)

@@ -80,6 +80,12 @@ __device__ __forceinline__ bool segment_of(const DecaySpans& p, unsigned seg, De
         s.t0 = 0;
         s.len = (int)p.T;
     }
+    // the same for all lanes: kept in scalar registers
+    s.seq = __builtin_amdgcn_readfirstlane(s.seq);
+    s.index = __builtin_amdgcn_readfirstlane(s.index);
+    s.len = __builtin_amdgcn_readfirstlane(s.len);
+    s.b = __builtin_amdgcn_readfirstlane((uint32_t)s.b);
+    s.t0 = __builtin_amdgcn_readfirstlane((uint32_t)s.t0);
     const long long from = (long long)s.index * L;
     if (from >= s.len && s.index) return false;
     s.from = (int)from;
@@ -131,6 +137,11 @@ __device__ __forceinline__ void unpack_frag(const Frag<IO>& f, float (&x)[8]) {
         unpack8<IO>(&f.v, x);
     }
 }
+__device__ __forceinline__ int fresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // Rows as operands with k along the elements: lane (g, c), of lanes in groups of G,
 // has token t0 + c at elements e0 + 8g + i, i < 8; t0 a multiple of 16, e0 of 16.
 template <int IO, int D, int G>
@@ -209,22 +220,30 @@ struct Moving {
     du4 r[kMine];
     static constexpr int kStep = N / kPieces;           // tokens between a thread's pieces
     static_assert(N % kPieces == 0, "a thread keeps its piece");
+    // Loads in flight may meet neither an instruction nor the end of a branch: those
+    // of what is not there read the first piece, and are dropped by clear().
     __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int pieces,
                                          int tid) {
         const char* p = x.at(token);
         const uint32_t stride = (uint32_t)x.bytes;
+        tid = fresh(tid);
         const int u = tid % kPieces, left = u < pieces ? n - tid / kPieces : 0;
         const uint32_t mine = (uint32_t)(tid / kPieces) * stride + 16u * u;
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
             r[j] = *(const du4*)(p + (j * kStep < left ? mine + j * kStep * stride : 0u));
-        if (n >= C && pieces == kPieces) return;
+    }
+    __device__ __forceinline__ void clear(int n, int pieces, int tid) {
+        if (n >= C && pieces >= kPieces) return;
+        tid = fresh(tid);
+        const int left = tid % kPieces < pieces ? n - tid / kPieces : 0;
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
 #pragma unroll
             for (int w = 0; w < 4; ++w) r[j][w] = j * kStep < left ? r[j][w] : 0;
     }
     __device__ __forceinline__ void store(char* m, int tid) const {
+        tid = fresh(tid);
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
             *(du4*)(m + Rows<IO, D>::at(j * kStep + tid / kPieces, tid % kPieces)) = r[j];
@@ -280,6 +299,15 @@ __device__ __forceinline__ dfloat16 mma32(const Frag<IO>& a, const Frag<IO>& b, 
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(dbf8, a.v),
                                                        __builtin_bit_cast(dbf8, b.v), c, 0, 0, 0);
     }
+}
+// After a run of matrix instructions: time for the last of them to write its result.
+// The compiler puts the waits that are needed before what reads it in the same
+// block, but a block that a branch leads to may begin with such a read: one did (an
+// accumulator's copy right behind the branch), and got the old value.
+__device__ __forceinline__ void products_done() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 7");
+    __builtin_amdgcn_sched_barrier(0);
 }
 // x[8] times s (f16; a power of two) as N terms
 template <int IO, int N>
@@ -426,16 +454,15 @@ __device__ __forceinline__ void make_scores(const char* A, const char* B, char* 
             const Frag<IO> b = rows.get(A, 16 * qt, 32 * kb);
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
-                if (REV ? kt >= qt : kt <= qt)
-                    acc[kt] = mma16<IO>(rows.get(B, 16 * kt, 32 * kb), b, acc[kt]);
+                acc[kt] = mma16<IO>(rows.get(B, 16 * kt, 32 * kb), b, acc[kt]);
             __builtin_amdgcn_sched_barrier(0);
         }
+        products_done();
         const int i = 16 * qt + c, iw = F.whole[i];
         const float ir = F.rest[i];
         float largest = 0.f;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-            if (!(REV ? kt >= qt : kt <= qt)) continue;
             const int s0 = 16 * kt + 4 * g;
             const int4 sw = *(const int4*)&F.whole[s0];
             const float4 sr = *(const float4*)&F.rest[s0];
@@ -456,10 +483,8 @@ __device__ __forceinline__ void make_scores(const char* A, const char* B, char* 
             to = sc.to;
             if (g == 0) back[i] = sc.back;
         }
-        // with the zeros beside the diagonal within a block of 32
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-            if (REV ? kt >= (qt & ~1) : kt <= (qt | 1)) put_scores<IO, C>(P, lane, qt, kt, to, acc[kt]);
+        for (int kt = 0; kt < KT; ++kt) put_scores<IO, C>(P, lane, qt, kt, to, acc[kt]);
     }
 }
 
@@ -547,6 +572,7 @@ __device__ __forceinline__ void state_product(const char* A, const State<DA>& S,
                 for (int m = 0; m < C / 32; ++m) acc[m] = mma32<IO>(a[m], b[n], acc[m]);
             __builtin_amdgcn_sched_barrier(0);
         }
+    products_done();
 #pragma unroll
     for (int m = 0; m < C / 32; ++m)
 #pragma unroll
@@ -559,37 +585,12 @@ __device__ __forceinline__ void state_product(const char* A, const State<DA>& S,
         }
 }
 
-// acc += P V: v holds the columns of V, block kb the tokens 16 kb ...  A value that
-// is infinite or NaN is left out, as it would meet the zeros of P, and the
-// column's rows that see it become NaN.
+// acc += P V: v holds the columns of V, block kb the tokens 16 kb ...
 template <int IO, int C, bool REV>
-__device__ __forceinline__ void scores_product(const char* P, const float* back,
-                                               const Frag<IO> (&values)[C / 16], bool unbounded,
-                                               dfloat16 (&acc)[C / 32]) {
+__device__ __forceinline__ void add_scores(const char* P, const float* back, int lane,
+                                           const Frag<IO> (&v)[C / 16], dfloat16 (&acc)[C / 32]) {
     constexpr int NP = Kind<IO>::NP, KB = C / 16;
-    const int lane = fresh_lane(), g = lane >> 5;
-    Frag<IO> v[KB];
-    int bad = REV ? -1 : C;            // the first (last) such token of the column
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) v[kb] = values[kb];
-    if (unbounded) {
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            float x[8];
-            unpack_frag<IO>(v[kb], x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!finite(x[i])) {
-                    const int t = 16 * kb + 8 * g + i;
-                    bad = REV ? max(bad, t) : min(bad, t);
-                    x[i] = 0.f;
-                }
-            Frag<IO> t[1];
-            terms<IO, 1>(x, 1.f, t);       // exact: they are of the type
-            v[kb] = t[0];
-        }
-        bad = REV ? max_halves(bad) : min_halves(bad);
-    }
+    const int g = lane >> 5;
 #pragma unroll
     for (int m = 0; m < C / 32; ++m) {
         dfloat16 s;
@@ -602,6 +603,7 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
 #pragma unroll
             for (int kb = REV ? 2 * m : 0; kb < (REV ? KB : 2 * m + 2); ++kb)
                 s = mma32<IO>(Scores<IO, C>::get(P, lane, n, m, kb), v[kb], s);
+        products_done();
         if constexpr (IO == IO_F16) {
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -614,13 +616,46 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
         } else {
             acc[m] = s;
         }
-        if (unbounded)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int t = 32 * m + 8 * (r >> 2) + 4 * g + (r & 3);
-                if (REV ? t <= bad : t >= bad) acc[m][r] = __uint_as_float(0x7fc00000u);
-            }
     }
+}
+// The same where V may hold a value that is infinite or NaN: it is left out, as it
+// would meet the zeros of P, and the column's rows that see it become NaN.
+template <int IO, int C, bool REV>
+__device__ __forceinline__ void scores_product(const char* P, const float* back,
+                                               const Frag<IO> (&values)[C / 16], bool unbounded,
+                                               dfloat16 (&acc)[C / 32]) {
+    constexpr int KB = C / 16;
+    const int lane = fresh_lane(), g = lane >> 5;
+    if (!unbounded) {
+        add_scores<IO, C, REV>(P, back, lane, values, acc);
+        return;
+    }
+    Frag<IO> v[KB];
+    int bad = REV ? -1 : C;            // the first (last) such token of the column
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+        float x[8];
+        unpack_frag<IO>(values[kb], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!finite(x[i])) {
+                const int t = 16 * kb + 8 * g + i;
+                bad = REV ? max(bad, t) : min(bad, t);
+                x[i] = 0.f;
+            }
+        Frag<IO> t[1];
+        terms<IO, 1>(x, 1.f, t);       // exact: they are of the type
+        v[kb] = t[0];
+    }
+    bad = REV ? max_halves(bad) : min_halves(bad);
+    add_scores<IO, C, REV>(P, back, lane, v, acc);
+#pragma unroll
+    for (int m = 0; m < C / 32; ++m)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int t = 32 * m + 8 * (r >> 2) + 4 * g + (r & 3);
+            if (REV ? t <= bad : t >= bad) acc[m][r] = __uint_as_float(0x7fc00000u);
+        }
 }
 
 // eight values of the tokens t .. t + 7 times their w
@@ -675,6 +710,7 @@ __device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&val
             for (int i = 0; i < DA / 32; ++i) S.t[i] = mma32<IO>(a[i], v[n], S.t[i]);
         __builtin_amdgcn_sched_barrier(0);
     }
+    products_done();
     if constexpr (IO == IO_F16)
 #pragma unroll
         for (int i = 0; i < DA / 32; ++i)
@@ -682,30 +718,57 @@ __device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&val
             for (int r = 0; r < 16; ++r) S.t[i][r] *= back;
 }
 
-// The rows below n to memory, `row` bytes apart: of type IO, or fp32 where wide.
-template <int IO, int C>
-__device__ __forceinline__ void store_rows(char* out, long long row, int col, bool wide, bool ok,
-                                           int n, const dfloat16 (&acc)[C / 32]) {
-    const int g = fresh_lane() >> 5;
-    if (!ok) return;
-    const uint32_t mine = (uint32_t)(4 * g) * (uint32_t)row + (uint32_t)col * (wide ? 4 : Kind<IO>::kB);
-    const int left = n - 4 * g;
-    const auto put = [&](bool whole, bool wide) {
+// The wave's 32 columns of the rows below n to memory, `row` bytes apart, through the
+// places of its columns in a tile that nobody else uses (columns first .. first + 32):
+// stores of 16 bytes, four or eight lanes a row, where the accumulators would give
+// 32 of two.  pieces: 16-byte pieces that there are.  wide: fp32 whatever the type.
+template <int IO, int D, int C>
+__device__ __forceinline__ void store_rows(char* tile, int first, const dfloat16 (&acc)[C / 32],
+                                           char* out, long long row, int pieces, bool wide, int n) {
+    typedef Rows<IO, D> R;
+    constexpr int kB = R::kB, kPer = 16 / kB;
+    const int lane = fresh_lane(), g = lane >> 5, c = lane & 31;
+    const auto drain = [&](int t0, int tokens, int per, auto place) {
+        asm volatile("" ::: "memory");
+        const int u = lane % per, left = u < pieces ? n - t0 - lane / per : 0;
+        char* to = out + t0 * row;
+        const uint32_t mine = (uint32_t)(lane / per) * (uint32_t)row + 16u * u;
+#pragma unroll
+        for (int j = 0; j < tokens * per / 64; ++j) {
+            const int t = j * (64 / per);
+            const du4 x = *(const du4*)(tile + place(t + lane / per, u));
+            if (t < left) *(du4*)(to + t * row + mine) = x;
+        }
+        asm volatile("" ::: "memory");
+    };
+    if (IO == IO_F32 || !wide) {
+        const uint32_t base = R::at(4 * g, (first + c) / kPer) + (first + c) % kPer * kB;
 #pragma unroll
         for (int m = 0; m < C / 32; ++m)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int t = 32 * m + 8 * (r >> 2) + (r & 3);
-                char* to = out + t * row + mine;
-                if (whole || t < left) {
-                    if (wide) *(float*)to = acc[m][r];
-                    else io_store<IO>(to, 0, acc[m][r]);
-                }
+                const int t = 8 * (r >> 2) + (r & 3);
+                io_store<IO>(tile + (32 * m + t) * R::kRow + (base ^ (swirl<R::kPieces>(t) << 4)), 0,
+                             acc[m][r]);
             }
-    };
-    if (wide) put(n >= C, true);
-    else if (n >= C) put(true, false);
-    else put(false, false);
+        drain(0, C, 32 / kPer, [&](int t, int u) { return R::at(t, first / kPer + u); });
+    } else {
+        // half of the tokens at a time: a row's upper 16 columns C/2 rows on
+        const uint32_t base = R::at(4 * g + (c >> 4) * (C / 2), first / kPer + ((c >> 2) & 3)) +
+                              4 * (c & 3);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int f = half * C / 4; f < (half + 1) * C / 4; ++f) {
+                const int t = (32 * (f >> 4) + 8 * ((f & 15) >> 2) + (f & 3)) % (C / 2);
+                *(float*)(tile + t * R::kRow + (base ^ (swirl<R::kPieces>(t) << 4))) =
+                    acc[f >> 4][f & 15];
+            }
+            drain(half * (C / 2), C / 2, 8, [&](int t, int u) {
+                return R::at(t + (u >> 2) * (C / 2), first / kPer + (u & 3));
+            });
+        }
+    }
 }
 
 // Sums over the 16 lanes of a group: lane c gets that of t[c / 4].

@@ -47,7 +47,7 @@ struct WalkLds {
 };
 
 template <int IO, int DA, int C, int W, int MODE>
-__global__ __launch_bounds__(64 * W, DA > 128 ? 1 : 2) void decay_walk_kernel(DecayWalk p) {
+__global__ __launch_bounds__(64 * W, DA > 128 || (DA == 128 && W == 2) ? 1 : 2) void decay_walk_kernel(DecayWalk p) {
     typedef WalkLds<IO, DA, C, W, MODE> L;
     constexpr int N = 64 * W, kB = Kind<IO>::kB;
     constexpr bool OUT = L::kOut, REV = MODE == kEffectsBack, DOT = MODE == kQueries;
@@ -59,13 +59,13 @@ __global__ __launch_bounds__(64 * W, DA > 128 ? 1 : 2) void decay_walk_kernel(De
     if (!segment_of(p.sp, seg, s)) return;
     if (MODE == kEffects && s.last) return;
     if (MODE == kEffectsBack && s.index == 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int first = slice * 32 * W, col = first + 32 * wave + (lane & 31);
     const bool ok = col < p.cols;
     const int here = p.cols - first < 32 * W ? p.cols - first : 32 * W;
     if (OUT && p.clear && s.index == 0 && p.sp.cu) {
         // tokens before the first sequence and behind the last
-        clear_unheld(p.sp, s, p.out, p.wide ? 4 : kB, p.Hv, p.cols, h, first, here);
+        clear_unheld(p.sp, s, p.out, DOT && p.wide ? 4 : kB, p.Hv, p.cols, h, first, here);
     }
     const long long size = (long long)p.rows * p.cols;
     State<DA> S;
@@ -107,7 +107,11 @@ __global__ __launch_bounds__(64 * W, DA > 128 ? 1 : 2) void decay_walk_kernel(De
         mv.load(vs, at, n, vpieces, tid);
         if (DOT) mx.load(x, at, n, vpieces, tid);
     };
-    const auto put = [&](Factors<C>& f) {
+    const auto put = [&](Factors<C>& f, int n) {
+        if (OUT) ma.clear(n, pieces, tid);
+        mb.clear(n, pieces, tid);
+        mv.clear(n, vpieces, tid);
+        if (DOT) mx.clear(n, vpieces, tid);
         if (OUT) ma.store(A, tid);
         mb.store(B, tid);
         mv.store(V, tid);
@@ -125,7 +129,7 @@ __global__ __launch_bounds__(64 * W, DA > 128 ? 1 : 2) void decay_walk_kernel(De
         fetch(at, n);
         if (wave == 0) factors(F[0], log_decay(at, n), n);
         __syncthreads();
-        put(F[0]);
+        put(F[0], n);
         __syncthreads();
     }
     for (int ch = 0; ch < chunks; ++ch) {
@@ -164,15 +168,20 @@ __global__ __launch_bounds__(64 * W, DA > 128 ? 1 : 2) void decay_walk_kernel(De
         for (int kb = 0; kb < C / 16; ++kb) vf[kb] = vcols.get(V, 16 * kb, 32 * wave);
         if (OUT) {
             scores_product<IO, C, false>(P, back, vf, f.unbounded, acc);
-            const long long row = (long long)p.Hv * p.cols * (p.wide ? 4 : kB);
-            store_rows<IO, C>((char*)p.out + (s.b * p.sp.T + s.t0 + at) * row, row,
-                              h * p.cols + col, p.wide, ok, n, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            const bool wide = DOT && p.wide;
+            const int ob = wide ? 4 : kB;
+            const long long row = (long long)p.Hv * p.cols * ob;
+            store_rows<IO, 32 * W, C>(
+                V, 32 * wave, acc,
+                (char*)p.out + (s.b * p.sp.T + s.t0 + at) * row + (long long)(h * p.cols + first + 32 * wave) * ob,
+                row, (here - 32 * wave) * ob / 16, wide, n);
         }
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(B, vf, f, S);
         if (wave == 0 && more) factors(F[(ch + 1) & 1], g, m);
         __syncthreads();
-        if (more) put(F[(ch + 1) & 1]);
+        if (more) put(F[(ch + 1) & 1], m);
         __syncthreads();
     }
     if (OUT) {
