@@ -100,14 +100,23 @@ struct DecayGradParams {
     // dg_t is the sum over pairs s < t <= u of what u's output owes to s.  before:
     // s before the chunk, u in it; behind: s in it, u in it or behind; both [parts
     // of the columns][Hv][B T].  ends: <d final state, final state> in parts;
-    // chunks: by all tokens of a chunk what is behind it, and its e^Dc, [parts of
-    // the columns][slots][Hv], a packed sequence's slots from cu / chunk + its
-    // number on.
+    // before_all, chunks: by all tokens of a chunk what is before it, and what is
+    // behind and the chunk's e^Dc, [parts of the columns][slots][Hv], a packed
+    // sequence's slots from cu / chunk + its number on.  What all tokens of a chunk
+    // share is in 64 bits: a fixed decay's dg sums it over all of them.
     float* before;
     float* behind;
-    float* ends;
-    float2* chunks;
+    double* ends;
+    double* before_all;
+    double2* chunks;
     long long slots;
+    // every anchor_every chunks of a sequence from the first on: the state before the
+    // chunk (as accumulators of its transpose, [anchors][Hv][16 columns of Dk][tiles
+    // of Dv][lane]), and e^Dc times its product with the gradient of the chunk's last
+    int anchor_every;
+    float* anchors;
+    double* anchor_dg;               // [parts of the columns of Dk][anchors][Hv]
+    long long anchor_count;
     double* sums;                    // dg of the parts of the tokens (fixed decays)
     float* dq_heads;                 // [B][T][Hv][Dk], or null where Hv = Hk
     float* dk_heads;
@@ -118,6 +127,18 @@ struct DecayGradParams {
     float* dinit;                    // [nseq][Hv][Dk][Dv] or null
 };
 hipError_t launch_decay_bwd(int io, const DecayGradParams& p, hipStream_t s);
+// Chunks between anchors.  A decay for each token: every fourth, 16 KB of states
+// written and read for each 64 tokens of a head of 128.  A fixed decay's dg sums what
+// all tokens of a chunk share, and its error with it: every chunk.
+inline int decay_anchor_every(bool fixed) { return fixed ? 1 : 4; }
+// Anchors in all; a packed sequence's start at cu / (so many chunks) + its number.
+inline size_t decay_anchors(size_t T, size_t nseq, bool packed, size_t n) {
+    return packed ? T / n + nseq : nseq * ((T + n - 1) / n);
+}
+// accumulators of an anchor, in floats
+inline size_t decay_anchor_floats(int Dk, int Dv) {
+    return (size_t)(Dk + 15) / 16 * ((size_t)(Dv + 31) / 32) * 512;
+}
 // Workgroups of the last pass over dg take so many chunks of a sequence.
 constexpr int kDgChunks = 64;
 inline size_t decay_dg_units(size_t T, size_t nseq, bool packed, int chunk) {

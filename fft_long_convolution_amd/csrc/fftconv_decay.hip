@@ -136,8 +136,7 @@ __global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, l
         const dfloat4 effect = *x;
         *x = S;
         if (!last) {
-            const Power d = power_of(seg_g[i]);
-            const float a = exp2_of(d.whole, d.rest);
+            const float a = exact_exp2(seg_g[i]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[r] = a * S[r] + effect[r];
         }

@@ -16,8 +16,12 @@
 //   s in it, u behind:            sum over s < t of k_s . (dk_s's part with X)
 //   both in it:                   sums of W over rectangles
 //   s before, u behind:           A = e^Dc <X, S0>, the same for the whole chunk
-// A follows from the next chunk's: A + (s in it, u behind) by all tokens = A' + (s
-// before, u in the next) by all of its, 0 where e^Dc leaves nothing in fp32.
+// The walk of dq leaves S0 of every fourth chunk for A.  Between them A follows from
+// the next chunk's A': A + (s in it, u behind) by all tokens = A' + (s before, u in the
+// next) by all of its; it is taken as 0 where e^Dc is below 2^-22, which the terms'
+// own errors reach.  A fixed decay's dg sums A over all tokens, so its errors too: it
+// has S0 of every chunk.  (With chains to the sequence's end dg of 2 x 1501 tokens of
+// one decay a head was off by 1.4e-5, in fours by up to 4e-6.)
 #include "fftconv_decay_walk.h"
 
 namespace fftconv {
@@ -26,58 +30,59 @@ namespace {
 template <int IO, int DA>
 struct Back {
     static constexpr int C = IO == IO_F32 || DA > 128 ? 32 : 64;
-    static constexpr int RW = DA <= 64 ? 2 : 4;          // waves of a role
+    static constexpr int RW = DA <= 64 ? 4 : 8;          // waves of a role
     static constexpr int kTile = C * DA * Kind<IO>::kB;
     static constexpr int kP = Scores<IO, C>::kBytes;
     static constexpr int kBytes = 4 * kTile + 2 * kP;
 };
 
 // Scores of dk (rows of v against do) as make_scores() makes them, and the sums over
-// rectangles of W: part[qt][t] for the sixteen s of the wave.
+// rectangles of W: sums[unit][t] for the sixteen s and the u of the unit.
 template <int IO, int DA, int C, int NW>
 __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* DO, const char* K,
                                                      const char* Q, char* P, float* back,
                                                      const Factors<C>& F, float scale, int wave,
-                                                     float (*part)[C]) {
-    constexpr int KT = C / 16;
+                                                     float (*sums)[C]) {
+    typedef Scores<IO, C> L;
     const int lane = fresh_lane(), g = lane >> 4, c = lane & 15;
-    const RowReader<IO, DA, 16> rows(lane);
-    if (NW > KT && wave >= KT) return;
+    const RowReader<IO, DA> rows(lane);
 #pragma unroll
-    for (int j = 0; j < (KT + NW - 1) / NW; ++j) {
-        const int qt = wave + NW * j;
-        dfloat4 vd[KT], kq[KT];
+    for (int j = 0; j < (L::kUnits + NW - 1) / NW; ++j) {
+        const int unit = wave + NW * j, qt = unit % L::M, part = unit / L::M, k0 = part * L::kTiles;
+        if (NW > L::kUnits && unit >= L::kUnits) continue;
+        if (k0 + L::kTiles - 1 < (qt & ~1)) {
+            if (lane < C) sums[unit][lane] = 0.f;
+            continue;
+        }
+        dfloat4 vd[L::kTiles], kq[L::kTiles];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) vd[kt] = kq[kt] = dfloat4{0, 0, 0, 0};
+        for (int x = 0; x < L::kTiles; ++x) vd[x] = kq[x] = dfloat4{0, 0, 0, 0};
 #pragma unroll
         for (int kb = 0; kb < DA / 32; ++kb) {
-            const Frag<IO> b = rows.get(V, 16 * qt, 32 * kb);
-            const Frag<IO> b2 = rows.get(K, 16 * qt, 32 * kb);
+            constexpr int kTile = 16 * Rows<IO, DA>::kRow;
+            const Frag<IO> b = rows.get(V + qt * kTile, 0, 32 * kb);
+            const Frag<IO> b2 = rows.get(K + qt * kTile, 0, 32 * kb);
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                vd[kt] = mma16<IO>(rows.get(DO, 16 * kt, 32 * kb), b, vd[kt]);
-                kq[kt] = mma16<IO>(rows.get(Q, 16 * kt, 32 * kb), b2, kq[kt]);
+            for (int x = 0; x < L::kTiles; ++x) {
+                vd[x] = mma16<IO>(rows.get(DO + k0 * kTile, 16 * x, 32 * kb), b, vd[x]);
+                kq[x] = mma16<IO>(rows.get(Q + k0 * kTile, 16 * x, 32 * kb), b2, kq[x]);
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
         products_done();
-        const int i = 16 * qt + c, iw = F.whole[i];
-        const float ir = F.rest[i];
+        const int i = 16 * qt + c, whole = F.whole[i];
+        const float rest = F.rest[i];
         float largest = 0.f, carry = 0.f;
 #pragma unroll
-        for (int kt = KT - 1; kt >= 0; --kt) {
-            const int s0 = 16 * kt + 4 * g;
-            const int4 sw = *(const int4*)&F.whole[s0];
-            const float4 sr = *(const float4*)&F.rest[s0];
-            const int w[4] = {sw.x, sw.y, sw.z, sw.w};
-            const float r[4] = {sr.x, sr.y, sr.z, sr.w};
-            float y[4];
+        for (int x = L::kTiles - 1; x >= 0; --x) {
+            const int s0 = 16 * (k0 + x) + 4 * g;
+            float gam[4], y[4];
+            decays_between<C, true>(F, s0, whole, rest, gam);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = scale * exp2_of(w[e] - iw, r[e] - ir) * vd[kt][e];
-                vd[kt][e] = s0 + e >= i ? x : 0.f;
-                y[e] = s0 + e > i ? x * kq[kt][e] : 0.f;
-                if (IO == IO_F16) largest = fmaxf(largest, fabsf(vd[kt][e]));
+                const float p = scale * gam[e] * vd[x][e];
+                vd[x][e] = s0 + e >= i ? p : 0.f;
+                y[e] = s0 + e > i ? p * kq[x][e] : 0.f;
+                if (IO == IO_F16) largest = fmaxf(largest, fabsf(vd[x][e]));
             }
             // of the tokens u from t on
             y[2] += y[3];
@@ -93,16 +98,22 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = s0 + e > i ? y[e] + behind : 0.f;
             const float sum = sums16_of4(y);
-            if ((c & 3) == 0) part[qt][s0 + (c >> 2)] = sum;
+            if ((c & 3) == 0) sums[unit][s0 + (c >> 2)] = sum;
         }
-        float to = 1.f;
-        if constexpr (IO == IO_F16) {
-            const Scale sc = scale_to(fmaxf(max_groups(largest), 0x1p-40f));
-            to = sc.to;
-            if (g == 0) back[i] = sc.back;
-        }
+        // t before and behind the unit's u
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) put_scores<IO, C>(P, lane, qt, kt, to, vd[kt]);
+        for (int kt = 0; kt < L::M; ++kt) {
+            if (kt >= k0 && kt < k0 + L::kTiles) continue;
+            const int s0 = 16 * kt + 4 * g;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = kt < k0 && s0 + e > i ? carry : 0.f;
+            const float sum = sums16_of4(y);
+            if ((c & 3) == 0) sums[unit][s0 + (c >> 2)] = sum;
+        }
+        const float to = L::scale(largest, back, lane, qt, part);
+#pragma unroll
+        for (int x = 0; x < L::kTiles; ++x) L::put(P, lane, qt, k0 + x, to, vd[x]);
     }
 }
 
@@ -110,10 +121,10 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
 // chunks backward in time, with the gradient X of the state, columns of Dv in the
 // first role's waves (dv) and, transposed, columns of Dk in the second's (dk).
 template <int IO, int DA>
-__global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(DecayGradParams p,
-                                                                             int slices) {
+__global__ __launch_bounds__((DA <= 64 ? 512 : 1024), 4) void decay_back_kernel(DecayGradParams p,
+                                                                               int slices) {
     typedef Back<IO, DA> L;
-    constexpr int C = L::C, RW = L::RW, N = 128 * RW, kB = Kind<IO>::kB;
+    constexpr int C = L::C, RW = L::RW, N = 128 * RW, kB = Kind<IO>::kB, kCols = 16 * RW;
     const DecayParams& f = p.f;
     const unsigned units = (unsigned)(f.sp.segs * f.Hv * slices), u = xcd_unit(blockIdx.x, units);
     if (u >= units) return;
@@ -124,14 +135,14 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
     const int tid = threadIdx.x, lane = tid & 63, place = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wave = place & (RW - 1);
     const bool keys = place >= RW;      // the role
-    const int first = slice * 32 * RW, mine = first + 32 * wave, col = mine + (lane & 31);
+    const int first = slice * kCols, mine = first + 16 * wave, col = mine + (lane & 15);
     const int cols = keys ? f.Dk : f.Dv, rows = keys ? f.Dv : f.Dk;
-    const bool ok = col < cols, wide = keys && p.dk_heads;
+    const bool ok = col < cols, wide = p.dk_heads != nullptr;
+    // what there is of the slice's columns
+    const int nk = min(f.Dk - first, kCols), nv = min(f.Dv - first, kCols);
     if (s.index == 0 && f.sp.cu) {
-        const int nk = min(f.Dk - first, 32 * RW), nv = min(f.Dv - first, 32 * RW);
         if (nk > 0)
-            clear_unheld(f.sp, s, p.dk_heads ? p.dk_heads : p.dk, p.dk_heads ? 4 : kB, f.Hv, f.Dk, h,
-                         first, nk);
+            clear_unheld(f.sp, s, wide ? p.dk_heads : p.dk, wide ? 4 : kB, f.Hv, f.Dk, h, first, nk);
         if (nv > 0) clear_unheld(f.sp, s, p.dv, kB, f.Hv, f.Dv, h, first, nv);
     }
     const long long size = (long long)f.Dk * f.Dv;
@@ -147,28 +158,44 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
     char* const V = lds + 2 * L::kTile;
     char* const DO = lds + 3 * L::kTile;
     char* const P = lds + 4 * L::kTile + (keys ? L::kP : 0);
-    __shared__ __attribute__((aligned(16))) Factors<C> F[2];
-    __shared__ __attribute__((aligned(16))) float back[2][C];
-    __shared__ __attribute__((aligned(16))) float part[C / 16][C];
+    __shared__ __attribute__((aligned(16))) Factors<C> F[8];
+    __shared__ __attribute__((aligned(16))) float back[2][C / 32 * C];
+    __shared__ float sums[Scores<IO, C>::kUnits][C];
     __shared__ float dots[RW][C];
+    __shared__ int unbounded[2];
+    __shared__ double products[RW];
     const int chunks = (s.to - s.from + C - 1) / C;
     const Tokens q = rows_of<IO>(f.q, s, h), k = rows_of<IO>(f.k, s, h), v = rows_of<IO>(f.v, s, h),
                  d = rows_of<IO>(p.d_o, s, h);
+    const long long anchor_floats = (long long)((f.Dk + 15) / 16) * ((f.Dv + 31) / 32) * 512;
     const int kp = f.Dk * kB / 16, vp = f.Dv * kB / 16;
     const float* gates = f.fixed ? f.g + h : f.g + (s.b * f.sp.T + s.t0) * f.Hv + h;
-    const auto log_decay = [&](int at, int n) {
-        return f.fixed ? gates[0] : gates[(long long)(at + (lane < n ? lane : n - 1)) * f.Hv];
-    };
     const long long token0 = s.b * f.sp.T + s.t0;
     const long long slot0 = f.sp.cu ? s.t0 / C + s.seq : s.b * ((f.sp.T + C - 1) / C);
+    // the first token of the walk's chunk i, and its tokens
+    const auto start = [&](int i) { return s.from + (chunks - 1 - i) * C; };
+    const auto count = [&](int i) { return min(C, s.to - start(i)); };
+    const auto log_decays = [&](int i) {
+        const int n = place < 4 && i + place < chunks ? count(i + place) : 0;
+        if (n <= 0) return 0.f;
+        if (f.fixed) return gates[0];
+        return gates[(long long)(start(i + place) + min(lane, n - 1)) * f.Hv];
+    };
+    const auto factors = [&](int i, float g) {
+        if (place >= 4 || i + place >= chunks) return;
+        put_factors<C, true>(F[(i + place) & 7], decays_to<C>(g, f.fixed, count(i + place)), 1.f,
+                             f.scale);
+    };
     Moving<IO, DA, C, N> mq, mk, mv, md;
-    const auto fetch = [&](int at, int n) {
+    const auto fetch = [&](int i) {
+        const int at = start(i), n = count(i);
         mq.load(q, at, n, kp, tid);
         mk.load(k, at, n, kp, tid);
         mv.load(v, at, n, vp, tid);
         md.load(d, at, n, vp, tid);
     };
-    const auto put = [&](Factors<C>& F, int n) {
+    const auto put = [&](int i) {
+        const int n = count(i);
         mq.clear(n, kp, tid);
         mk.clear(n, kp, tid);
         mv.clear(n, vp, tid);
@@ -177,32 +204,47 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
         mk.store(K, tid);
         mv.store(V, tid);
         md.store(DO, tid);
-        if (mq.unbounded() || md.unbounded()) F.unbounded = 1;
+        if (mq.unbounded() || md.unbounded()) unbounded[i & 1] = 1;
     };
-    const auto factors = [&](Factors<C>& F, float g, int n) {
-        put_factors<C, true>(F, decays_to<C>(g, f.fixed, n), 1.f, f.scale);
-        if (lane == 0) F.unbounded = 0;
-    };
+    const int kb = wide ? 4 : kB;
+    const long long krow = (long long)f.Hv * f.Dk * kb, vrow = (long long)f.Hv * f.Dv * kB;
+    char* const dk = (char*)(wide ? (void*)p.dk_heads : p.dk) + token0 * krow +
+                     (long long)(h * f.Dk + first) * kb;
+    char* const dv = (char*)p.dv + token0 * vrow + (long long)(h * f.Dv + first) * kB;
     if (chunks) {
-        const int at = s.from + (chunks - 1) * C, n = s.to - at;
-        fetch(at, n);
-        if (tid < 64) factors(F[0], log_decay(at, n), n);
+        fetch(0);
+        factors(0, log_decays(0));
+        if (tid < 2) unbounded[tid] = 0;
         __syncthreads();
-        put(F[0], n);
+        put(0);
         __syncthreads();
     }
+    const int tile = mine < DA ? wave + first / 16 : 0;        // columns that are in the tiles
     for (int i = 0; i < chunks; ++i) {
-        const Factors<C>& fac = F[i & 1];
-        const int ch = chunks - 1 - i, at = s.from + ch * C, n = s.to - at < C ? s.to - at : C;
-        const bool more = ch > 0;
+        const Factors<C>& fac = F[i & 7];
+        const int at = start(i), n = count(i);
+        const bool more = i + 1 < chunks;
         float g = 0.f;
-        if (more) {
-            fetch(at - C, C);
-            if (tid < 64) g = log_decay(at - C, C);
+        const bool anchor = at / C % p.anchor_every == 0;
+        if (anchor && keys) {
+            double x = 0;
+            if (mine < f.Dk) {
+                const int tiles = 2 * ((f.Dv + 31) / 32);
+                x = X.times_tiles(p.anchors +
+                                      (anchor_of(f.sp, s, C, p.anchor_every, at / C) * f.Hv + h) *
+                                          anchor_floats +
+                                      (long long)(mine / 16) * tiles * 256,
+                                  tiles);
+            }
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+            if (lane == 0) products[wave] = x;
         }
-        dfloat16 acc[C / 32];
+        if (more) fetch(i + 1);
+        if ((i & 3) == 0) g = log_decays(i + 4);
+        dfloat4 acc[C / 16];
         if (keys) {
-            make_scores_and_sums<IO, DA, C, RW>(V, DO, K, Q, P, back[1], fac, f.scale, wave, part);
+            make_scores_and_sums<IO, DA, C, RW>(V, DO, K, Q, P, back[1], fac, f.scale, wave, sums);
             __builtin_amdgcn_sched_barrier(0);
             state_product<IO, DA, C, IO == IO_BF16 ? 2 : Kind<IO>::NS>(V, X, fac, acc);
         } else {
@@ -210,17 +252,17 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
             __builtin_amdgcn_sched_barrier(0);
             state_product<IO, DA, C, Kind<IO>::NS>(K, X, fac, acc);
             __builtin_amdgcn_sched_barrier(0);
-            row_dots<IO, DA, C>(V, mine < DA ? mine : 0, acc, dots[wave]);
+            row_dots<IO, DA, C>(V, 16 * tile, acc, dots[wave]);
         }
         __syncthreads();
-        if (tid < 64 && first < f.Dv) {
+        if (place == RW - 1 && nv > 0) {
             // s in the chunk before t
             double x = 0, r = 0;
             if (lane < C) {
 #pragma unroll
                 for (int w = 0; w < RW; ++w) x += dots[w][lane];
 #pragma unroll
-                for (int w = 0; w < C / 16; ++w) r += part[w][lane];
+                for (int w = 0; w < Scores<IO, C>::kUnits; ++w) r += sums[w][lane];
             }
             const double to = prefix_sum(x), all = __shfl(to, 63);
             double before = __shfl_up(to, 1);
@@ -229,31 +271,41 @@ __global__ __launch_bounds__((DA <= 64 ? 256 : 512), 1) void decay_back_kernel(D
                 p.behind[((long long)slice * f.Hv + h) * p.B * f.sp.T + token0 + at + lane] =
                     (float)(before + (slice == 0 ? r : 0));
             if (lane == 0)
-                p.chunks[(slice * p.slots + slot0 + at / C) * f.Hv + h] = make_float2((float)all, fac.all);
+                p.chunks[(slice * p.slots + slot0 + at / C) * f.Hv + h] = make_double2(all, fac.all);
         }
-        Frag<IO> val[C / 16];
-        const int from = mine < DA ? mine : 0;
+        if (anchor && tid == 0 && nk > 0) {
+            double x = 0;
+#pragma unroll
+            for (int w = 0; w < RW; ++w) x += products[w];
+            p.anchor_dg[(slice * p.anchor_count + anchor_of(f.sp, s, C, p.anchor_every, at / C)) *
+                            f.Hv + h] = fac.all * x;
+        }
+        Frag<IO> val[C / 32];
         const ColReader<IO, DA, false> vcols(fresh_lane());
 #pragma unroll
-        for (int kb = 0; kb < C / 16; ++kb) val[kb] = vcols.get(keys ? Q : DO, 16 * kb, from);
-        scores_product<IO, C, true>(P, back[keys], val, fac.unbounded, acc);
+        for (int j = 0; j < C / 32; ++j)
+            val[j] = vcols.get(keys ? Q : DO, 32 * j, tile);
+        scores_product<IO, C, true>(P, back[keys], val, unbounded[i & 1], acc);
         __builtin_amdgcn_sched_barrier(0);
         // K's and V's tiles are done with
-        const int ob = wide ? 4 : kB;
-        const long long row = (long long)f.Hv * cols * ob;
-        store_rows<IO, DA, C>(keys ? V : K, from, acc,
-                              (char*)(keys ? (wide ? (void*)p.dk_heads : p.dk) : p.dv) +
-                                  (token0 + at) * row + (long long)(h * cols + mine) * ob,
-                              row, (cols - mine) * ob / 16, wide, n);
+        if (keys && wide) rows_to_memory<C>(dk + at * krow + 64 * wave, krow, ok, n, acc);
+        else if (mine < DA) rows_to_tile<IO, DA, C>(keys ? V : K, mine, acc);
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(keys ? DO : Q, val, fac, X);
-        if (tid < 64 && more) factors(F[(i + 1) & 1], g, C);
+        if ((i & 3) == 0) factors(i + 4, g);
+        if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
-        if (more) put(F[(i + 1) & 1], C);
+        Moving<IO, DA, C, N> outk, outv;
+        outv.take(K, tid);
+        outk.take(V, tid);
+        if (more) put(i + 1);
+        const int p0 = first * kB / 16;
+        outv.write(dv + at * vrow, vrow, n, p0, p0 + nv * kB / 16, tid);
+        if (!wide) outk.write(dk + at * krow, krow, n, p0, p0 + nk * kB / 16, tid);
         __syncthreads();
     }
     if (!keys && s.index == 0 && p.dinit)
-        X.store(p.dinit + (s.seq * (long long)f.Hv + h) * size + col * cs, rs, ok, rows);
+        X.store(p.dinit + (s.seq * (long long)f.Hv + h) * size + at_col, rs, ok, rows);
 }
 
 // dg from its parts, kDgChunks chunks of C tokens a workgroup.
@@ -262,7 +314,7 @@ __global__ __launch_bounds__(256) void decay_dg_kernel(DecayGradParams p, DecayS
     const DecayParams& f = p.f;
     const int h = (int)(blockIdx.x % f.Hv), lane = threadIdx.x & 63;
     const unsigned part = blockIdx.x / f.Hv;
-    __shared__ float A[kDgChunks];
+    __shared__ double A[kDgChunks];
     __shared__ double sums[4];
     DecaySpan s;
     double sum = 0;
@@ -277,23 +329,29 @@ __global__ __launch_bounds__(256) void decay_dg_kernel(DecayGradParams p, DecayS
             for (int top = (nc - 1) / kDgChunks * kDgChunks; top >= mine; top -= kDgChunks) {
                 const int c = top + kDgChunks - 1 - lane;      // lanes: from the last on
                 double b = 0;
-                int keep = 1;
+                int keep = 1, chain = 1;        // chain: by way of the next chunk
                 if (c < nc) {
-                    for (int i = 0; i < vs; ++i) {
-                        // a slice's sum is its part of the chunk's
-                        const float2 x = p.chunks[(i * p.slots + slot0 + c) * f.Hv + h];
-                        b -= x.x;
-                        keep = x.y >= 0x1p-24f;
-                    }
-                    if (c + 1 < nc) {
+                    if (c % p.anchor_every == 0) {
+                        chain = 0;
+                        const long long a = anchor_of(sp, s, C, p.anchor_every, c);
                         for (int i = 0; i < ks; ++i)
-                            b += p.before[((long long)i * f.Hv + h) * tokens + token0 +
-                                          (long long)(c + 1) * C];
+                            b += p.anchor_dg[(i * p.anchor_count + a) * f.Hv + h];
                     } else {
-                        for (int i = 0; i < ends; ++i)
-                            b += p.ends[(s.seq * (long long)f.Hv + h) * ends + i];
+                        for (int i = 0; i < vs; ++i) {
+                            const double2 x = p.chunks[(i * p.slots + slot0 + c) * f.Hv + h];
+                            b -= x.x;
+                            keep = x.y >= 0x1p-22;
+                        }
+                        if (c + 1 < nc) {
+                            for (int i = 0; i < ks; ++i)
+                                b += p.before_all[(i * p.slots + slot0 + c + 1) * f.Hv + h];
+                        } else {
+                            for (int i = 0; i < ends; ++i)
+                                b += p.ends[(s.seq * (long long)f.Hv + h) * ends + i];
+                        }
+                        if (!keep) b = 0;
                     }
-                    if (!keep) b = 0;
+                    keep &= chain;
                 }
                 // the lane's chunk on top of the later ones': A = keep A' + b
                 for (int m = 1; m < 64; m <<= 1) {
@@ -306,17 +364,17 @@ __global__ __launch_bounds__(256) void decay_dg_kernel(DecayGradParams p, DecayS
                 }
                 if (keep) b += next;
                 next = __shfl(b, 63);
-                if (top == mine) A[kDgChunks - 1 - lane] = (float)b;
+                if (top == mine) A[kDgChunks - 1 - lane] = b;
             }
         }
         __syncthreads();
         for (int t = s.from + threadIdx.x; t < s.to; t += 256) {
             const long long at = token0 + t;
-            float x = A[(t - s.from) / C], y = 0;
-            for (int i = 0; i < ks; ++i) y += p.before[((long long)i * f.Hv + h) * tokens + at];
-            for (int i = 0; i < vs; ++i) y += p.behind[((long long)i * f.Hv + h) * tokens + at];
-            if (f.fixed) sum += (double)x + (double)y;
-            else p.dg[at * f.Hv + h] = x + y;
+            double x = A[(t - s.from) / C];
+            for (int i = 0; i < ks; ++i) x += p.before[((long long)i * f.Hv + h) * tokens + at];
+            for (int i = 0; i < vs; ++i) x += p.behind[((long long)i * f.Hv + h) * tokens + at];
+            if (f.fixed) sum += x;
+            else p.dg[at * f.Hv + h] = (float)x;
         }
         if (!f.fixed && sp.cu && s.index == 0) {
             const long long end = s.t0 + s.len;
@@ -367,7 +425,7 @@ hipError_t back_launch(const DecayGradParams& p, hipStream_t s) {
                                              hipFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (e != hipSuccess) return e;
     const int widest = p.f.Dk > p.f.Dv ? p.f.Dk : p.f.Dv;
-    const int slices = (widest + 32 * L::RW - 1) / (32 * L::RW);
+    const int slices = (widest + 16 * L::RW - 1) / (16 * L::RW);
     hipLaunchKernelGGL(kernel, dim3((unsigned)xcd_blocks(p.f.sp.segs * p.f.Hv * slices)),
                        dim3(128 * L::RW), L::kBytes, s, p, slices);
     return hipGetLastError();
@@ -421,6 +479,11 @@ hipError_t bwd_io(const DecayGradParams& p, hipStream_t s) {
     w.wide = p.dq_heads != nullptr;
     w.clear = 1;
     w.before = p.before;
+    w.before_all = p.before_all;
+    w.slots = p.slots;
+    w.anchor_every = p.anchor_every;
+    w.anchors = p.anchors;
+    w.anchor_floats = (long long)decay_anchor_floats(f.Dk, f.Dv);
     w.dfin = p.dfin;
     w.ends = p.ends;
     const int widest = f.Dk > f.Dv ? f.Dk : f.Dv;
@@ -438,7 +501,7 @@ hipError_t bwd_io(const DecayGradParams& p, hipStream_t s) {
     sp.per = sp.cu ? 1 : (int)(sp.T ? (sp.T + sp.seg_tokens - 1) / sp.seg_tokens : 1);
     if (sp.segs)
         hipLaunchKernelGGL(decay_dg_kernel, dim3((unsigned)(sp.segs * f.Hv)), dim3(256), 0, s, p, sp,
-                           C, ks, vs, 4 * ks);
+                           C, ks, vs, 8 * ks);
     if (f.fixed)
         hipLaunchKernelGGL(decay_dg_sum_kernel, dim3(f.Hv), dim3(256), 0, s, p.sums, sp.segs, f.Hv,
                            p.dg);

@@ -3,7 +3,7 @@
 // of a chunk that the forward and the backward walks share.
 //
 // A walk takes a sequence's chunks of C tokens one after the other with a state
-// S (DA x columns) in the accumulators of its waves, 32 columns a wave.  With rows
+// S (DA x columns) in the accumulators of its waves, 16 columns a wave.  With rows
 // A, B of DA elements and rows V of the columns, and D_t the sum of the log decays
 // from the chunk's first token to t:
 //   out = f o (A S) + P V,   P_ts = Gam_ts A_t.B_s
@@ -13,26 +13,24 @@
 //
 // Matrix products.  16-bit rows are exact operands.  An fp32 operand is written
 // in terms of that type, each the rounding of what the ones before leave: of
-// bf16 three for states (26 bits) and two for scores (17 bits: they meet outputs of 8),
+// bf16 three for states (26 bits) and two for what meets outputs of 8 bits only (17),
 // with fp32's range; of f16 two (22 bits), with a power of two for each column
-// (states, weighted values) or row (scores) that takes the largest to 2^14.
+// (states, weighted values) or row of 32 scores that takes the largest to 2^14.
 // fp32 rows go to the fp32 matrix instructions as they are, which have 1/16 of
 // the rate, and so have all operands 24 bits.
 //
-// Operand order.  The 32 x 32 instructions take 16 k at a time: lane (g = l/32, c
-// = l%32) gives A[row c][k = 8g + i], B[k = 8g + i][col c], i < 8, and has D[row
-// 8a + 4g + b][col c] in register 4a + b.  Row 8a + 4g + b of a 32-row tile of
-// the state stands for element 16 (a/2) + 8g + 4 (a%2) + b, so that a lane's
-// accumulators are the eight k that it gives as B of the next product.  fp32:
-// the same places, eight instructions of two k.
+// Operand order.  The 16 x 16 instructions take 32 k at a time: lane (g = l/16, c
+// = l%16) gives A[row c][k = 8g + i], B[k = 8g + i][col c], i < 8, and has D[row
+// 4g + r][col c], r < 4.  Row 4g + r of a 16-row tile i of the state stands for
+// element 32 (i/2) + 8g + 4 (i%2) + r, so that a lane's accumulators of two tiles
+// are the eight k that it gives as B of the next product.  fp32: the same places,
+// eight instructions of four k.
 #pragma once
 
 #include "fftconv_decay.h"
 #include "fftconv_delta_dev.h"
 
 namespace fftconv {
-
-typedef float dfloat16 __attribute__((ext_vector_type(16)));
 
 template <int IO>
 struct Kind {
@@ -142,13 +140,13 @@ __device__ __forceinline__ int fresh(int x) {
     return x;
 }
 
-// Rows as operands with k along the elements: lane (g, c), of lanes in groups of G,
-// has token t0 + c at elements e0 + 8g + i, i < 8; t0 a multiple of 16, e0 of 16.
-template <int IO, int D, int G>
+// Rows as operands with k along the elements: lane (g, c) has token t0 + c at
+// elements e0 + 8g + i, i < 8; t0 a multiple of 16, e0 of 32.
+template <int IO, int D>
 struct RowReader {
     uint32_t base;
     __device__ __forceinline__ explicit RowReader(int lane)
-        : base(Rows<IO, D>::at(lane & (G - 1), (lane / G) * (IO == IO_F32 ? 2 : 1))) {}
+        : base(Rows<IO, D>::at(lane & 15, (lane >> 4) * (IO == IO_F32 ? 2 : 1))) {}
     __device__ __forceinline__ Frag<IO> get(const char* m, int t0, int e0) const {
         Frag<IO> f;
         if constexpr (IO == IO_F32) {
@@ -162,46 +160,44 @@ struct RowReader {
     }
 };
 // Rows as operands with k along the tokens: lane (g, c) has tokens t0 + 8g + i, i < 8,
-// at element e0 + c, or, STATE, at the element that row c of a tile of the state
-// stands for; t0 a multiple of 16, e0 of 32.
+// at element 16 i + c, or, STATE, at the element that row c of tile i of the state
+// stands for; t0 a multiple of 32.
 template <int IO, int D, bool STATE>
 struct ColReader {
     typedef Rows<IO, D> R;
     uint32_t base;
     __device__ __forceinline__ explicit ColReader(int lane) {
+        const int g = lane >> 4, j = lane & 15;
         if constexpr (IO == IO_F32) {
-            const int c = lane & 31;
-            const int e = STATE ? (c & 19) | ((c & 8) >> 1) | ((c & 4) << 1) : c;
-            base = R::at(8 * (lane >> 5), e >> 2) + 4 * (e & 3);
+            base = R::at(8 * g, STATE ? 2 * (j >> 2) : j >> 2) + 4 * (j & 3);
         } else {
             // each read takes, from 16 lanes, four tokens by four pieces of four
             // elements, and gives lane j the four tokens' element j of the pieces in
-            // the lanes' order: the state's order swaps the middle two
-            const int j = lane & 15;
-            int piece = j & 3;
-            if (STATE) piece = (piece >> 1) | ((piece & 1) << 1);
-            base = R::at(8 * (lane >> 5) + (j >> 2), 2 * ((lane >> 4) & 1) + (piece >> 1)) +
-                   8 * (piece & 1);
+            // the lanes' order
+            base = STATE ? R::at(8 * g + (j >> 2), j & 3)
+                         : R::at(8 * g + (j >> 2), (j & 3) >> 1) + 8 * (j & 1);
         }
     }
-    __device__ __forceinline__ Frag<IO> get(const char* m, int t0, int e0) const {
+    __device__ __forceinline__ Frag<IO> get(const char* m, int t0, int i) const {
+        const uint32_t at = base ^ (uint32_t)(STATE ? 32 * (i >> 1) * R::kB : 16 * i * R::kB);
         const char* s = m + t0 * R::kRow;
         Frag<IO> f;
         if constexpr (IO == IO_F32) {
+            const uint32_t half = STATE ? 16 * (i & 1) : 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int k = 0; k < 8; ++k) {
                 const float x = *(const float*)(
-                    s + i * R::kRow + (base ^ (uint32_t)(e0 << 2) ^ (swirl<R::kPieces>(i) << 4)));
-                if (i < 4) f.a[i & 3] = x; else f.b[i & 3] = x;
+                    s + k * R::kRow + (at ^ half ^ (swirl<R::kPieces>(k) << 4)));
+                if (k < 4) f.a[k & 3] = x; else f.b[k & 3] = x;
             }
         } else {
             typedef short s4 __attribute__((ext_vector_type(4)));
             uint2 r[2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const char* x = s + 4 * half * R::kRow +
-                                (base ^ (uint32_t)(e0 << 1) ^ (swirl<R::kPieces>(4 * half) << 4));
-                r[half] = __builtin_bit_cast(
+            for (int k = 0; k < 2; ++k) {
+                const char* x = s + 4 * k * R::kRow + (STATE ? 8 * (i & 1) : 0) +
+                                (at ^ (swirl<R::kPieces>(4 * k) << 4));
+                r[k] = __builtin_bit_cast(
                     uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                (__attribute__((address_space(3))) s4*)x));
             }
@@ -211,15 +207,19 @@ struct ColReader {
     }
 };
 
-// C tokens of rows on their way from memory to LDS, by N threads (tid < N):
-// tokens from n on and pieces from the row's end on are 0.
+// C tokens of rows on their way from memory to LDS (or back), by N threads (tid < N),
+// each of which keeps to its pieces: tokens from n on and pieces from the row's end
+// on are 0.
 template <int IO, int D, int C, int N>
 struct Moving {
-    static constexpr int kPieces = Rows<IO, D>::kPieces, kMine = C * kPieces / N;
-    static_assert(C * kPieces % N == 0, "threads share the pieces evenly");
+    static constexpr int kPieces = Rows<IO, D>::kPieces, kAll = C * kPieces;
+    static constexpr int kMine = (kAll + N - 1) / N, kStep = N / kPieces;
+    static_assert(N % kPieces == 0 && (kAll % N == 0 || kAll < N), "threads share evenly");
     du4 r[kMine];
-    static constexpr int kStep = N / kPieces;           // tokens between a thread's pieces
-    static_assert(N % kPieces == 0, "a thread keeps its piece");
+    static __device__ __forceinline__ bool idle(int tid) { return kAll < N && tid >= kAll; }
+    static __device__ __forceinline__ uint32_t place(int j, int tid) {
+        return Rows<IO, D>::at(j * kStep + tid / kPieces, tid % kPieces);
+    }
     // Loads in flight may meet neither an instruction nor the end of a branch: those
     // of what is not there read the first piece, and are dropped by clear().
     __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int pieces,
@@ -244,9 +244,25 @@ struct Moving {
     }
     __device__ __forceinline__ void store(char* m, int tid) const {
         tid = fresh(tid);
+        if (idle(tid)) return;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) *(du4*)(m + place(j, tid)) = r[j];
+    }
+    __device__ __forceinline__ void take(const char* m, int tid) {
+        tid = fresh(tid);
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) r[j] = *(const du4*)(m + (idle(tid) ? 0 : place(j, tid)));
+    }
+    // pieces from .. to - 1 of the tokens below n, `row` bytes apart, piece `from` first
+    __device__ __forceinline__ void write(char* out, long long row, int n, int from, int to,
+                                          int tid) const {
+        tid = fresh(tid);
+        if (idle(tid)) return;
+        const int u = tid % kPieces, left = u >= from && u < to ? n - tid / kPieces : 0;
+        const uint32_t mine = (uint32_t)(tid / kPieces) * (uint32_t)row + 16u * (u - from);
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
-            *(du4*)(m + Rows<IO, D>::at(j * kStep + tid / kPieces, tid % kPieces)) = r[j];
+            if (j * kStep < left) *(du4*)(out + j * kStep * row + mine) = r[j];
     }
     // whether an element is infinite or NaN
     __device__ __forceinline__ bool unbounded() const {
@@ -281,22 +297,6 @@ __device__ __forceinline__ dfloat4 mma16(const Frag<IO>& a, const Frag<IO>& b, d
                                                       __builtin_bit_cast(dh8, b.v), c, 0, 0, 0);
     } else {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(dbf8, a.v),
-                                                       __builtin_bit_cast(dbf8, b.v), c, 0, 0, 0);
-    }
-}
-template <int IO>
-__device__ __forceinline__ dfloat16 mma32(const Frag<IO>& a, const Frag<IO>& b, dfloat16 c) {
-    if constexpr (IO == IO_F32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.a[i], b.a[i], c, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.b[i], b.b[i], c, 0, 0, 0);
-        return c;
-    } else if constexpr (IO == IO_F16) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(dh8, a.v),
-                                                      __builtin_bit_cast(dh8, b.v), c, 0, 0, 0);
-    } else {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(dbf8, a.v),
                                                        __builtin_bit_cast(dbf8, b.v), c, 0, 0, 0);
     }
 }
@@ -341,19 +341,14 @@ __device__ __forceinline__ void terms(const float (&x)[8], float s, Frag<IO> (&t
     }
 }
 
-// the larger of the lane's value and that of the other half of the wave
-__device__ __forceinline__ float max_halves(float a) {
-    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(a), false,
-                                                    false);
-    return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+// the larger (smaller) of the lane's value and those of the other groups at its place
+__device__ __forceinline__ int max_all(int a) {
+    a = max(a, __shfl_xor(a, 32));
+    return max(a, __shfl_xor(a, 16));
 }
-__device__ __forceinline__ int min_halves(int a) {
-    const auto x = __builtin_amdgcn_permlane32_swap((uint32_t)a, (uint32_t)a, false, false);
-    return min((int)x[0], (int)x[1]);
-}
-__device__ __forceinline__ int max_halves(int a) {
-    const auto x = __builtin_amdgcn_permlane32_swap((uint32_t)a, (uint32_t)a, false, false);
-    return max((int)x[0], (int)x[1]);
+__device__ __forceinline__ int min_all(int a) {
+    a = min(a, __shfl_xor(a, 32));
+    return min(a, __shfl_xor(a, 16));
 }
 
 // -------------------------------------------------------- factors of a chunk
@@ -365,8 +360,7 @@ struct Factors {
     int whole[C];
     float rest[C];
     float f[C], w[C];        // of the rows of the state's product, of the values
-    float all;               // e^Dc
-    int unbounded;           // an infinite or NaN value in the chunk
+    float all, none[3];      // e^Dc
 };
 struct Power { int whole; float rest; };
 __device__ __forceinline__ Power power_of(double x) {
@@ -375,6 +369,20 @@ __device__ __forceinline__ Power power_of(double x) {
 }
 __device__ __forceinline__ float exp2_of(int whole, float rest) {
     return __builtin_ldexpf(__builtin_amdgcn_exp2f(rest), whole);
+}
+// 2^x rounded to fp32 once: of a chunk's factors, which all elements of a row and the
+// whole state share, so that their errors do not average out.  Taylor terms of
+// 2^rest = e^(rest log 2) up to (0.35)^11 / 11! = 2e-13.
+__device__ __forceinline__ float exact_exp2(double x) {
+    const double n = __builtin_rint(x), y = (x - n) * 0.6931471805599453;
+    double e = 1.0 / 3628800;
+#pragma unroll
+    for (int i = 9; i >= 0; --i) {
+        constexpr double inverse[10] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720,
+                                        1.0 / 5040, 1.0 / 40320, 1.0 / 362880};
+        e = __builtin_fma(e, y, inverse[i]);
+    }
+    return __builtin_ldexpf((float)e, (int)n);
 }
 // By the 64 lanes of one wave: D of the lane's token (n tokens, those behind have the
 // last one's), in units of log 2.  g: the token's log decay (0 behind the last).
@@ -392,8 +400,8 @@ template <int C, bool REV>
 __device__ __forceinline__ void put_factors(Factors<C>& F, double D, float sf, float sw) {
     const int lane = threadIdx.x & 63;
     const double all = __shfl(D, C - 1);
-    const Power p = power_of(D), r = power_of(all - D);
-    const float to = exp2_of(p.whole, p.rest), from = exp2_of(r.whole, r.rest);
+    const Power p = power_of(D);
+    const float to = exact_exp2(D), from = exact_exp2(all - D);
     if (lane < C) {
         F.whole[lane] = p.whole;
         F.rest[lane] = p.rest;
@@ -405,114 +413,129 @@ __device__ __forceinline__ void put_factors(Factors<C>& F, double D, float sf, f
 
 // ------------------------------------------------------- the steps of a chunk
 
-// Scores P (rows A against rows B) by NW waves, as operands of 32 rows x 16 k: block
-// (m, kb) of term i at ((i * C/32 + m) * C/16 + kb) * 64 + lane.  f16: rows scaled, back
-// holds the inverse scales.
+// Scores P (rows A against rows B) as operands of 16 rows x 32 k: block (m, kb) of
+// term i at ((i * C/16 + m) * C/32 + kb) * 64 + lane.  f16: 32 scores of a row have
+// a scale, back[kb][row] holds its inverse.  A wave makes kTiles blocks of 16 x 16 of
+// a row tile together.
 template <int IO, int C>
 struct Scores {
-    static constexpr int kBlock = 64 * (IO == IO_F32 ? 32 : 16), kBlocks = (C / 32) * (C / 16);
-    static constexpr int kTerm = kBlock * kBlocks, kBytes = kTerm * Kind<IO>::NP;
+    static constexpr int kBlock = 64 * (int)sizeof(Frag<IO>), M = C / 16, KB = C / 32;
+    static constexpr int kTerm = kBlock * M * KB, kBytes = kTerm * Kind<IO>::NP;
+    static constexpr int kTiles = C == 64 || IO == IO_F16 ? 2 : 1;
+    static constexpr int kParts = M / kTiles, kUnits = M * kParts;
     static __device__ __forceinline__ Frag<IO> get(const char* P, int lane, int term, int m, int kb) {
-        return *(const Frag<IO>*)(P + term * kTerm + (m * (C / 16) + kb) * kBlock +
+        return *(const Frag<IO>*)(P + term * kTerm + (m * KB + kb) * kBlock +
                                   lane * (int)sizeof(Frag<IO>));
     }
-};
-// The lane's rows 16 kt + 4 g + r of B, r < 4, for its row 16 qt + c of A.
-template <int IO, int C>
-__device__ __forceinline__ void put_scores(char* P, int lane, int qt, int kt, float to,
-                                           dfloat4 p) {
-    constexpr int NP = Kind<IO>::NP;
-    const int g = lane >> 4, c = lane & 15;
-    const int place = ((qt >> 1) * (C / 16) + kt) * 64 + (g >> 1) * 32 + 16 * (qt & 1) + c;
-    if constexpr (IO == IO_F32) {
-        *(dfloat4*)(P + place * 32 + (g & 1) * 16) = p;
-    } else {
-        const float x[8] = {p[0], p[1], p[2], p[3], 0, 0, 0, 0};
-        Frag<IO> t[NP];
-        terms<IO, NP>(x, to, t);
+    // the lane's rows 16 kt + 4 g + r of B, r < 4, for its row 16 qt + c of A
+    static __device__ __forceinline__ void put(char* P, int lane, int qt, int kt, float to, dfloat4 p) {
+        const int g = lane >> 4, c = lane & 15;
+        const int place = (qt * KB + (kt >> 1)) * 64 + (2 * (kt & 1) + (g >> 1)) * 16 + c;
+        if constexpr (IO == IO_F32) {
+            *(dfloat4*)(P + place * 32 + (g & 1) * 16) = p;
+        } else {
+            const float x[8] = {p[0], p[1], p[2], p[3], 0, 0, 0, 0};
+            Frag<IO> t[Kind<IO>::NP];
+            terms<IO, Kind<IO>::NP>(x, to, t);
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-            *(uint2*)(P + n * Scores<IO, C>::kTerm + place * 16 + (g & 1) * 8) =
-                make_uint2(t[n].v[0], t[n].v[1]);
+            for (int n = 0; n < Kind<IO>::NP; ++n)
+                *(uint2*)(P + n * kTerm + place * 16 + (g & 1) * 8) = make_uint2(t[n].v[0], t[n].v[1]);
+        }
     }
+    // the scale of a row, from the largest of the lane's scores of it: at most 2^54, as
+    // scores below 2^-40 do not reach an f16 output
+    static __device__ __forceinline__ float scale(float largest, float* back, int lane, int qt, int part) {
+        if constexpr (IO == IO_F16) {
+            const Scale sc = scale_to(fmaxf(max_groups(largest), 0x1p-40f));
+            if (lane < 16) back[part * C + 16 * qt + lane] = sc.back;
+            return sc.to;
+        }
+        return 1.f;
+    }
+};
+// Decays between the lane's token (whole, rest) and tokens s0 .. s0 + 3.
+template <int C, bool REV>
+__device__ __forceinline__ void decays_between(const Factors<C>& F, int s0, int whole, float rest,
+                                               float (&gam)[4]) {
+    const int4 sw = *(const int4*)&F.whole[s0];
+    const float4 sr = *(const float4*)&F.rest[s0];
+    const int w[4] = {sw.x, sw.y, sw.z, sw.w};
+    const float r[4] = {sr.x, sr.y, sr.z, sr.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        gam[e] = REV ? exp2_of(w[e] - whole, r[e] - rest) : exp2_of(whole - w[e], rest - r[e]);
 }
 template <int IO, int DA, int C, int NW, bool REV>
 __device__ __forceinline__ void make_scores(const char* A, const char* B, char* P, float* back,
                                             const Factors<C>& F, float scale, int wave) {
-    constexpr int KT = C / 16;
+    typedef Scores<IO, C> L;
     const int lane = fresh_lane(), g = lane >> 4, c = lane & 15;
-    const RowReader<IO, DA, 16> rows(lane);
-    if (NW > KT && wave >= KT) return;
+    const RowReader<IO, DA> rows(lane);
 #pragma unroll
-    for (int j = 0; j < (KT + NW - 1) / NW; ++j) {
-        const int qt = wave + NW * j;
-        dfloat4 acc[KT];
+    for (int j = 0; j < (L::kUnits + NW - 1) / NW; ++j) {
+        const int unit = wave + NW * j, qt = unit % L::M, part = unit / L::M, k0 = part * L::kTiles;
+        // blocks of 32 k that meet no 1 of the triangle are not read
+        if ((NW > L::kUnits && unit >= L::kUnits) ||
+            (REV ? k0 + L::kTiles - 1 < (qt & ~1) : k0 > (qt | 1)))
+            continue;
+        dfloat4 acc[L::kTiles];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) acc[kt] = dfloat4{0, 0, 0, 0};
+        for (int x = 0; x < L::kTiles; ++x) acc[x] = dfloat4{0, 0, 0, 0};
 #pragma unroll
         for (int kb = 0; kb < DA / 32; ++kb) {
-            const Frag<IO> b = rows.get(A, 16 * qt, 32 * kb);
+            const Frag<IO> b = rows.get(A + qt * 16 * Rows<IO, DA>::kRow, 0, 32 * kb);
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-                acc[kt] = mma16<IO>(rows.get(B, 16 * kt, 32 * kb), b, acc[kt]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int x = 0; x < L::kTiles; ++x)
+                acc[x] = mma16<IO>(rows.get(B + k0 * 16 * Rows<IO, DA>::kRow, 16 * x, 32 * kb), b, acc[x]);
         }
         products_done();
-        const int i = 16 * qt + c, iw = F.whole[i];
-        const float ir = F.rest[i];
+        const int i = 16 * qt + c, whole = F.whole[i];
+        const float rest = F.rest[i];
         float largest = 0.f;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            const int s0 = 16 * kt + 4 * g;
-            const int4 sw = *(const int4*)&F.whole[s0];
-            const float4 sr = *(const float4*)&F.rest[s0];
-            const int w[4] = {sw.x, sw.y, sw.z, sw.w};
-            const float r[4] = {sr.x, sr.y, sr.z, sr.w};
+        for (int x = 0; x < L::kTiles; ++x) {
+            const int s0 = 16 * (k0 + x) + 4 * g;
+            float gam[4];
+            decays_between<C, REV>(F, s0, whole, rest, gam);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float gam = REV ? exp2_of(w[e] - iw, r[e] - ir) : exp2_of(iw - w[e], ir - r[e]);
-                const bool on = REV ? s0 + e >= i : s0 + e <= i;
-                acc[kt][e] = on ? scale * gam * acc[kt][e] : 0.f;
-                if (IO == IO_F16) largest = fmaxf(largest, fabsf(acc[kt][e]));
+                const float p = scale * gam[e] * acc[x][e];
+                acc[x][e] = (REV ? s0 + e >= i : s0 + e <= i) ? p : 0.f;
+                if (IO == IO_F16) largest = fmaxf(largest, fabsf(acc[x][e]));
             }
         }
-        float to = 1.f;
-        if constexpr (IO == IO_F16) {
-            // at most 2^54: scores below 2^-40 do not reach an f16 output
-            const Scale sc = scale_to(fmaxf(max_groups(largest), 0x1p-40f));
-            to = sc.to;
-            if (g == 0) back[i] = sc.back;
-        }
+        const float to = L::scale(largest, back, lane, qt, part);
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) put_scores<IO, C>(P, lane, qt, kt, to, acc[kt]);
+        for (int x = 0; x < L::kTiles; ++x) L::put(P, lane, qt, k0 + x, to, acc[x]);
     }
 }
 
-// The lane's columns of the state: tiles of 32 elements.
+// The lane's column of the state: tiles of 16 elements.
 template <int DA>
 struct State {
-    dfloat16 t[DA / 32];
+    static constexpr int N = DA / 16;
+    dfloat4 t[N];
     // largest magnitude of the column that is finite
     __device__ __forceinline__ float largest() const {
         float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < DA / 32; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) a = fmaxf(a, fabsf(t[i][r]));
-        a = max_halves(a);
+            for (int r = 0; r < 4; ++r) a = fmaxf(a, fabsf(t[i][r]));
+        a = max_groups(a);
         return finite(a) ? a : 0.f;
     }
-    // element of register r of tile i for the lane's half g
+    // element of register r of tile i for the lane's group g
     static __device__ __forceinline__ int element(int i, int r, int g) {
-        return 32 * i + 16 * (r >> 3) + 8 * g + (r & 7);
+        return 32 * (i >> 1) + 8 * g + 4 * (i & 1) + r;
     }
-    // base[element * rs + column * cs], elements below rows, where ok
+    // base[element * rs], elements below rows, where ok
     __device__ __forceinline__ void load(const float* base, long long rs, bool ok, int rows) {
-        const int g = (threadIdx.x & 63) >> 5;
+        const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-        for (int i = 0; i < DA / 32; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < 4; ++r) {
                 const int e = element(i, r, g);
                 const bool here = ok && e < rows;
                 const float x = base[here ? e * rs : 0];
@@ -520,29 +543,54 @@ struct State {
             }
     }
     __device__ __forceinline__ void store(float* base, long long rs, bool ok, int rows) const {
-        const int g = (threadIdx.x & 63) >> 5;
+        const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-        for (int i = 0; i < DA / 32; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
+            for (int r = 0; r < 4; ++r) {
                 const int e = element(i, r, g);
                 if (ok && e < rows) base[e * rs] = t[i][r];
             }
     }
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int i = 0; i < DA / 32; ++i)
+        for (int i = 0; i < N; ++i) t[i] = dfloat4{0, 0, 0, 0};
+    }
+    // as it is, `tiles` of its tiles
+    __device__ __forceinline__ void store_tiles(float* to, int tiles) const {
+        dfloat4* d = (dfloat4*)to + fresh_lane();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) t[i][r] = 0.f;
+        for (int i = 0; i < N; ++i)
+            if (i < tiles) d[64 * i] = t[i];
+    }
+    // sum of the products with tiles so stored, of the lane
+    __device__ __forceinline__ float times_tiles(const float* from, int tiles) const {
+        const dfloat4* d = (const dfloat4*)from + fresh_lane();
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < tiles) {
+                const dfloat4 x = d[64 * i];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a += t[i][r] * x[r];
+            }
+        return a;
     }
 };
+// The anchor before a sequence's chunk number `chunk` (a multiple of `every`), of C tokens
+__device__ __forceinline__ long long anchor_of(const DecaySpans& p, const DecaySpan& s, int C,
+                                               int every, int chunk) {
+    const int n = every * C;
+    return (p.cu ? s.t0 / n + s.seq : s.b * ((p.T + n - 1) / n)) + chunk / every;
+}
 
-// acc[m] = f o (rows A times S) for the 32-row tiles m
+// acc[m] = f o (rows A times S) for the row tiles m
 template <int IO, int DA, int C, int NS>
 __device__ __forceinline__ void state_product(const char* A, const State<DA>& S, const Factors<C>& F,
-                                              dfloat16 (&acc)[C / 32]) {
-    const int lane = fresh_lane(), g = lane >> 5;
-    const RowReader<IO, DA, 32> rows(lane);
+                                              dfloat4 (&acc)[C / 16]) {
+    constexpr int M = C / 16;
+    const int lane = fresh_lane(), g = lane >> 4;
+    const RowReader<IO, DA> rows(lane);
     float back = 1.f, to = 1.f;
     if constexpr (IO == IO_F16) {
         const Scale sc = scale_to(S.largest());
@@ -550,71 +598,71 @@ __device__ __forceinline__ void state_product(const char* A, const State<DA>& S,
         back = sc.back;
     }
 #pragma unroll
-    for (int m = 0; m < C / 32; ++m)
+    for (int m = 0; m < M; ++m) acc[m] = dfloat4{0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[m][r] = 0.f;
+    for (int kb = 0; kb < DA / 32; ++kb) {
+        Frag<IO> a[M], b[NS];
 #pragma unroll
-    for (int i = 0; i < DA / 32; ++i)
+        for (int m = 0; m < M; ++m) a[m] = rows.get(A, 16 * m, 32 * kb);
+        const float s[8] = {S.t[2 * kb][0], S.t[2 * kb][1], S.t[2 * kb][2], S.t[2 * kb][3],
+                            S.t[2 * kb + 1][0], S.t[2 * kb + 1][1], S.t[2 * kb + 1][2],
+                            S.t[2 * kb + 1][3]};
+        terms<IO, NS>(s, to, b);
+        if constexpr (IO == IO_F32) {
+            // a chain of additions for each block of k: fewer roundings in a row
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float s[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) s[r] = S.t[i][8 * x + r];
-            Frag<IO> b[NS];
-            terms<IO, NS>(s, to, b);
-            Frag<IO> a[C / 32];
-#pragma unroll
-            for (int m = 0; m < C / 32; ++m)
-                a[m] = rows.get(A, 32 * m, 32 * i + 16 * x);
+            for (int m = 0; m < M; ++m)
+                acc[m] += mma16<IO>(a[m], b[0], dfloat4{0, 0, 0, 0});
+        } else {
 #pragma unroll
             for (int n = NS - 1; n >= 0; --n)
 #pragma unroll
-                for (int m = 0; m < C / 32; ++m) acc[m] = mma32<IO>(a[m], b[n], acc[m]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int m = 0; m < M; ++m) acc[m] = mma16<IO>(a[m], b[n], acc[m]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+    }
     products_done();
 #pragma unroll
-    for (int m = 0; m < C / 32; ++m)
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const float4 f = *(const float4*)&F.f[32 * m + 8 * a + 4 * g];
-            acc[m][4 * a] *= f.x * back;
-            acc[m][4 * a + 1] *= f.y * back;
-            acc[m][4 * a + 2] *= f.z * back;
-            acc[m][4 * a + 3] *= f.w * back;
-        }
+    for (int m = 0; m < M; ++m) {
+        const float4 f = *(const float4*)&F.f[16 * m + 4 * g];
+        acc[m][0] *= f.x * back;
+        acc[m][1] *= f.y * back;
+        acc[m][2] *= f.z * back;
+        acc[m][3] *= f.w * back;
+    }
 }
 
-// acc += P V: v holds the columns of V, block kb the tokens 16 kb ...
+// acc += P V: v holds the column of V, block kb the tokens 32 kb ...
 template <int IO, int C, bool REV>
 __device__ __forceinline__ void add_scores(const char* P, const float* back, int lane,
-                                           const Frag<IO> (&v)[C / 16], dfloat16 (&acc)[C / 32]) {
-    constexpr int NP = Kind<IO>::NP, KB = C / 16;
-    const int g = lane >> 5;
+                                           const Frag<IO> (&v)[C / 32], dfloat4 (&acc)[C / 16]) {
+    typedef Scores<IO, C> L;
+    constexpr int NP = Kind<IO>::NP;
 #pragma unroll
-    for (int m = 0; m < C / 32; ++m) {
-        dfloat16 s;
-        if constexpr (IO == IO_F16)
+    for (int kb = 0; kb < L::KB; ++kb) {
+        dfloat4 s[L::M];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) s[r] = 0.f;
-        else s = acc[m];
+        for (int m = 0; m < L::M; ++m)
+            s[m] = IO == IO_F16 ? dfloat4{0, 0, 0, 0} : acc[m];
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
-            for (int kb = REV ? 2 * m : 0; kb < (REV ? KB : 2 * m + 2); ++kb)
-                s = mma32<IO>(Scores<IO, C>::get(P, lane, n, m, kb), v[kb], s);
+            for (int m = 0; m < L::M; ++m)
+                if (REV ? kb >= m / 2 : kb <= m / 2)
+                    s[m] = mma16<IO>(L::get(P, lane, n, m, kb), v[kb], s[m]);
         products_done();
-        if constexpr (IO == IO_F16) {
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const float4 f = *(const float4*)&back[32 * m + 8 * a + 4 * g];
-                acc[m][4 * a] += s[4 * a] * f.x;
-                acc[m][4 * a + 1] += s[4 * a + 1] * f.y;
-                acc[m][4 * a + 2] += s[4 * a + 2] * f.z;
-                acc[m][4 * a + 3] += s[4 * a + 3] * f.w;
+        for (int m = 0; m < L::M; ++m) {
+            if constexpr (IO == IO_F16) {
+                if (!(REV ? kb >= m / 2 : kb <= m / 2)) continue;
+                const float4 f = *(const float4*)&back[kb * C + 16 * m + 4 * (lane >> 4)];
+                acc[m][0] += s[m][0] * f.x;
+                acc[m][1] += s[m][1] * f.y;
+                acc[m][2] += s[m][2] * f.z;
+                acc[m][3] += s[m][3] * f.w;
+            } else {
+                acc[m] = s[m];
             }
-        } else {
-            acc[m] = s;
         }
     }
 }
@@ -622,24 +670,23 @@ __device__ __forceinline__ void add_scores(const char* P, const float* back, int
 // would meet the zeros of P, and the column's rows that see it become NaN.
 template <int IO, int C, bool REV>
 __device__ __forceinline__ void scores_product(const char* P, const float* back,
-                                               const Frag<IO> (&values)[C / 16], bool unbounded,
-                                               dfloat16 (&acc)[C / 32]) {
-    constexpr int KB = C / 16;
-    const int lane = fresh_lane(), g = lane >> 5;
+                                               const Frag<IO> (&values)[C / 32], bool unbounded,
+                                               dfloat4 (&acc)[C / 16]) {
+    const int lane = fresh_lane(), g = lane >> 4;
     if (!unbounded) {
         add_scores<IO, C, REV>(P, back, lane, values, acc);
         return;
     }
-    Frag<IO> v[KB];
+    Frag<IO> v[C / 32];
     int bad = REV ? -1 : C;            // the first (last) such token of the column
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
+    for (int kb = 0; kb < C / 32; ++kb) {
         float x[8];
         unpack_frag<IO>(values[kb], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (!finite(x[i])) {
-                const int t = 16 * kb + 8 * g + i;
+                const int t = 32 * kb + 8 * g + i;
                 bad = REV ? max(bad, t) : min(bad, t);
                 x[i] = 0.f;
             }
@@ -647,13 +694,13 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
         terms<IO, 1>(x, 1.f, t);       // exact: they are of the type
         v[kb] = t[0];
     }
-    bad = REV ? max_halves(bad) : min_halves(bad);
+    bad = REV ? max_all(bad) : min_all(bad);
     add_scores<IO, C, REV>(P, back, lane, v, acc);
 #pragma unroll
-    for (int m = 0; m < C / 32; ++m)
+    for (int m = 0; m < C / 16; ++m)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int t = 32 * m + 8 * (r >> 2) + 4 * g + (r & 3);
+        for (int r = 0; r < 4; ++r) {
+            const int t = 16 * m + 4 * g + r;
             if (REV ? t <= bad : t >= bad) acc[m][r] = __uint_as_float(0x7fc00000u);
         }
 }
@@ -666,109 +713,89 @@ __device__ __forceinline__ void weighted(const Frag<IO>& v, const Factors<C>& F,
     x[0] *= a.x; x[1] *= a.y; x[2] *= a.z; x[3] *= a.w;
     x[4] *= b.x; x[5] *= b.y; x[6] *= b.z; x[7] *= b.w;
 }
-// S <- e^Dc S + B^T (w o V)
+// S <- e^Dc S + B^T (w o V).  The chunk's part is summed by itself: one rounding of the
+// state a chunk.
 template <int IO, int DA, int C>
-__device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&values)[C / 16],
+__device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&values)[C / 32],
                                              const Factors<C>& F, State<DA>& S) {
-    constexpr int NS = Kind<IO>::NS, KB = C / 16;
-    const int lane = fresh_lane(), g = lane >> 5;
+    constexpr int NS = Kind<IO>::NS, KB = C / 32, G = 4;
+    const int lane = fresh_lane(), g = lane >> 4;
     const ColReader<IO, DA, true> cols(lane);
-    float all = F.all, to = 1.f, back = 1.f;
+    const float all = F.all;
+    float to = 1.f, back = 1.f;
     if constexpr (IO == IO_F16) {
-        // the column's scale; values of less than 2^-24 of the state do not
-        // reach it, and so do not ask for a larger one
         float largest = 0.f;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             float x[8];
-            weighted<IO, C>(values[kb], F, 16 * kb + 8 * g, x);
+            weighted<IO, C>(values[kb], F, 32 * kb + 8 * g, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) largest = fmaxf(largest, fabsf(x[i]));
         }
-        largest = max_halves(largest);
-        const Scale sc = scale_to(fmaxf(finite(largest) ? largest : 0.f, S.largest() * all * 0x1p-24f));
+        largest = max_groups(largest);
+        const Scale sc = scale_to(finite(largest) ? largest : 0.f);
         to = sc.to;
         back = sc.back;
-        all *= to;
     }
-#pragma unroll
-    for (int i = 0; i < DA / 32; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S.t[i][r] *= all;
+    Frag<IO> v[KB][NS];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
         float x[8];
-        Frag<IO> v[NS];
-        weighted<IO, C>(values[kb], F, 16 * kb + 8 * g, x);
-        terms<IO, NS>(x, to, v);
-        Frag<IO> a[DA / 32];
+        weighted<IO, C>(values[kb], F, 32 * kb + 8 * g, x);
+        terms<IO, NS>(x, to, v[kb]);
+    }
 #pragma unroll
-        for (int i = 0; i < DA / 32; ++i) a[i] = cols.get(B, 16 * kb, 32 * i);
+    for (int i = 0; i < State<DA>::N; i += G) {
+        dfloat4 part[G];
 #pragma unroll
-        for (int n = NS - 1; n >= 0; --n)
+        for (int j = 0; j < G; ++j) part[j] = dfloat4{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < DA / 32; ++i) S.t[i] = mma32<IO>(a[i], v[n], S.t[i]);
+        for (int kb = 0; kb < KB; ++kb) {
+            Frag<IO> a[G];
+#pragma unroll
+            for (int j = 0; j < G; ++j) a[j] = cols.get(B, 32 * kb, i + j);
+#pragma unroll
+            for (int n = NS - 1; n >= 0; --n)
+#pragma unroll
+                for (int j = 0; j < G; ++j) part[j] = mma16<IO>(a[j], v[kb][n], part[j]);
+        }
+        products_done();
+#pragma unroll
+        for (int j = 0; j < G; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S.t[i + j][r] = IO == IO_F16 ? fmaf(all, S.t[i + j][r], back * part[j][r])
+                                             : fmaf(all, S.t[i + j][r], part[j][r]);
         __builtin_amdgcn_sched_barrier(0);
     }
-    products_done();
-    if constexpr (IO == IO_F16)
-#pragma unroll
-        for (int i = 0; i < DA / 32; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) S.t[i][r] *= back;
 }
 
-// The wave's 32 columns of the rows below n to memory, `row` bytes apart, through the
-// places of its columns in a tile that nobody else uses (columns first .. first + 32):
-// stores of 16 bytes, four or eight lanes a row, where the accumulators would give
-// 32 of two.  pieces: 16-byte pieces that there are.  wide: fp32 whatever the type.
+// The wave's 16 columns of the rows to a tile's columns first ..., in the I/O type, for
+// threads that then take whole pieces of it.
 template <int IO, int D, int C>
-__device__ __forceinline__ void store_rows(char* tile, int first, const dfloat16 (&acc)[C / 32],
-                                           char* out, long long row, int pieces, bool wide, int n) {
+__device__ __forceinline__ void rows_to_tile(char* tile, int first, const dfloat4 (&acc)[C / 16]) {
     typedef Rows<IO, D> R;
-    constexpr int kB = R::kB, kPer = 16 / kB;
-    const int lane = fresh_lane(), g = lane >> 5, c = lane & 31;
-    const auto drain = [&](int t0, int tokens, int per, auto place) {
-        asm volatile("" ::: "memory");
-        const int u = lane % per, left = u < pieces ? n - t0 - lane / per : 0;
-        char* to = out + t0 * row;
-        const uint32_t mine = (uint32_t)(lane / per) * (uint32_t)row + 16u * u;
+    constexpr int kPer = 16 / R::kB;
+    const int lane = fresh_lane(), e = first + (lane & 15);
+    const uint32_t base = R::at(4 * (lane >> 4), e / kPer) + e % kPer * R::kB;
 #pragma unroll
-        for (int j = 0; j < tokens * per / 64; ++j) {
-            const int t = j * (64 / per);
-            const du4 x = *(const du4*)(tile + place(t + lane / per, u));
-            if (t < left) *(du4*)(to + t * row + mine) = x;
-        }
-        asm volatile("" ::: "memory");
-    };
-    if (IO == IO_F32 || !wide) {
-        const uint32_t base = R::at(4 * g, (first + c) / kPer) + (first + c) % kPer * kB;
+    for (int m = 0; m < C / 16; ++m)
 #pragma unroll
-        for (int m = 0; m < C / 32; ++m)
+        for (int r = 0; r < 4; ++r)
+            io_store<IO>(tile + (16 * m + r) * R::kRow + (base ^ (swirl<R::kPieces>(r) << 4)), 0,
+                         acc[m][r]);
+}
+// The rows below n to fp32 memory, `row` bytes apart.
+template <int C>
+__device__ __forceinline__ void rows_to_memory(char* out, long long row, bool ok, int n,
+                                               const dfloat4 (&acc)[C / 16]) {
+    const int lane = fresh_lane(), left = ok ? n - 4 * (lane >> 4) : 0;
+    const uint32_t mine = (uint32_t)(4 * (lane >> 4)) * (uint32_t)row + 4u * (lane & 15);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int t = 8 * (r >> 2) + (r & 3);
-                io_store<IO>(tile + (32 * m + t) * R::kRow + (base ^ (swirl<R::kPieces>(t) << 4)), 0,
-                             acc[m][r]);
-            }
-        drain(0, C, 32 / kPer, [&](int t, int u) { return R::at(t, first / kPer + u); });
-    } else {
-        // half of the tokens at a time: a row's upper 16 columns C/2 rows on
-        const uint32_t base = R::at(4 * g + (c >> 4) * (C / 2), first / kPer + ((c >> 2) & 3)) +
-                              4 * (c & 3);
+    for (int m = 0; m < C / 16; ++m)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int f = half * C / 4; f < (half + 1) * C / 4; ++f) {
-                const int t = (32 * (f >> 4) + 8 * ((f & 15) >> 2) + (f & 3)) % (C / 2);
-                *(float*)(tile + t * R::kRow + (base ^ (swirl<R::kPieces>(t) << 4))) =
-                    acc[f >> 4][f & 15];
-            }
-            drain(half * (C / 2), C / 2, 8, [&](int t, int u) {
-                return R::at(t + (u >> 2) * (C / 2), first / kPer + (u & 3));
-            });
-        }
-    }
+        for (int r = 0; r < 4; ++r)
+            if (16 * m + r < left) *(float*)(out + (16 * m + r) * row + mine) = acc[m][r];
 }
 
 // Sums over the 16 lanes of a group: lane c gets that of t[c / 4].
@@ -781,34 +808,26 @@ __device__ __forceinline__ float sums16_of4(const float (&t)[4]) {
     x += moved<0xb1>(x);
     return x + moved<0x4e>(x);
 }
-// sum of the lane's value and its neighbour group's of 16 in the half of the wave
-__device__ __forceinline__ float sum_pair(float a) {
-    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(a), false,
-                                                    false);
-    return __uint_as_float(y[0]) + __uint_as_float(y[1]);
-}
-// dots[t] = sum over the wave's 32 columns of acc and the rows X at column first
+// dots[t] = sum over the wave's 16 columns of acc and the rows X at column first
 template <int IO, int D, int C>
-__device__ __forceinline__ void row_dots(const char* X, int first, const dfloat16 (&acc)[C / 32],
+__device__ __forceinline__ void row_dots(const char* X, int first, const dfloat4 (&acc)[C / 16],
                                          float* dots) {
     typedef Rows<IO, D> R;
-    const int lane = fresh_lane(), g = lane >> 5, e = first + (lane & 31);
-    constexpr int kPer = 16 / Kind<IO>::kB;
-    const uint32_t base = R::at(4 * g, e / kPer) + e % kPer * Kind<IO>::kB;
+    constexpr int kPer = 16 / R::kB;
+    const int lane = fresh_lane(), g = lane >> 4, e = first + (lane & 15);
+    const uint32_t base = R::at(4 * g, e / kPer) + e % kPer * R::kB;
 #pragma unroll
-    for (int m = 0; m < C / 32; ++m)
+    for (int m = 0; m < C / 16; ++m) {
+        float x[4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            float x[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                x[b] = acc[m][4 * a + b] *
-                       io_load<IO>(X + (32 * m + 8 * a + b) * R::kRow +
-                                       (base ^ (swirl<R::kPieces>(8 * a + b) << 4)), 0);
-            const float d = sum_pair(sums16_of4(x));
-            if ((lane & 19) == 0) dots[32 * m + 8 * a + 4 * g + ((lane & 15) >> 2)] = d;
-        }
+        for (int r = 0; r < 4; ++r)
+            x[r] = acc[m][r] * io_load<IO>(X + (16 * m + r) * R::kRow +
+                                               (base ^ (swirl<R::kPieces>(r) << 4)), 0);
+        const float d = sums16_of4(x);
+        if ((lane & 3) == 0) dots[16 * m + 4 * g + ((lane & 15) >> 2)] = d;
+    }
 }
+
 // Columns first .. first + n of the tokens that no sequence holds become 0, by the
 // workgroups of the first and the last sequence's first segments.
 __device__ __forceinline__ void clear_unheld(const DecaySpans& p, const DecaySpan& s, void* out,

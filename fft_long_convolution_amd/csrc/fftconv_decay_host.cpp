@@ -77,10 +77,11 @@ struct DecayLayout {
     size_t seg, seg_g;            // bytes
     // backward: parts of dg by columns of dk and of dv, of the last states, of
     // chunks, of workgroups; dq and dk of the value heads where they share heads
-    size_t before, behind, ends, chunks, sums, shared, slots;
+    size_t before, behind, ends, before_all, chunks, anchors, anchor_dg, sums, shared, slots, anchor_count;
     size_t forward() const { return seg + seg_g; }
     size_t backward() const {
-        return 2 * seg + seg_g + before + behind + ends + chunks + sums + 2 * shared;
+        return 2 * seg + seg_g + before + behind + ends + before_all + chunks + anchors + anchor_dg +
+               sums + 2 * shared;
     }
 };
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -103,8 +104,14 @@ bool decay_layout(const fftconv_decay_desc* d, DecayLayout* l) {
     l->slots = d->sequences ? d->T / C + d->sequences : d->B * ((d->T + C - 1) / C);
     l->before = up16(k128 * d->Hv * tokens * 4);
     l->behind = up16(v128 * d->Hv * tokens * 4);
-    l->ends = up16(rows * d->Hv * k128 * 4 * 4);
-    l->chunks = up16(v128 * l->slots * d->Hv * 8);
+    l->ends = up16(rows * d->Hv * k128 * 8 * 8);
+    l->before_all = up16(k128 * l->slots * d->Hv * 8);
+    l->chunks = up16(v128 * l->slots * d->Hv * 16);
+    const size_t anchors = decay_anchors(d->T, rows, d->sequences != 0,
+                                         C * decay_anchor_every(d->fixed_decay != 0));
+    l->anchors = anchors * d->Hv * decay_anchor_floats((int)d->Dk, (int)d->Dv) * 4;
+    l->anchor_dg = up16(k128 * anchors * d->Hv * 8);
+    l->anchor_count = anchors;
     l->sums = d->fixed_decay ? up16(decay_dg_units(d->T, rows, d->sequences != 0, (int)C) * d->Hv * 8) : 0;
     l->shared = d->Hv > d->Hk ? up16(tokens * d->Hv * d->Dk * 4) : 0;
     return true;
@@ -319,9 +326,14 @@ fftconv_status fftconv_decay_backward(const fftconv_decay_desc* d, const void* q
     }
     p.before = (float*)take(l.before);
     p.behind = (float*)take(l.behind);
-    p.ends = (float*)take(l.ends);
-    p.chunks = (float2*)take(l.chunks);
+    p.ends = (double*)take(l.ends);
+    p.before_all = (double*)take(l.before_all);
+    p.chunks = (double2*)take(l.chunks);
     p.slots = (long long)l.slots;
+    p.anchor_every = decay_anchor_every(p.f.fixed);
+    p.anchors = (float*)take(l.anchors);
+    p.anchor_dg = (double*)take(l.anchor_dg);
+    p.anchor_count = (long long)l.anchor_count;
     if (l.sums) p.sums = (double*)take(l.sums);
     if (l.shared) {
         p.dq_heads = (float*)take(l.shared);

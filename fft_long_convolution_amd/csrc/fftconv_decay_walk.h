@@ -30,7 +30,12 @@ struct DecayWalk {
     float* before;                   // [slices][Hv][B T]
     long long tokens;                // B T
     const float* dfin;
-    float* ends;                     // [nseq][Hv][4 slices]
+    double* before_all;              // [slices][slots][Hv]
+    long long slots;
+    double* ends;                    // [nseq][Hv][8 slices]
+    int anchor_every;
+    float* anchors;
+    long long anchor_floats;         // of a head's anchor
 };
 
 enum WalkMode { kOutputs, kEffects, kEffectsBack, kQueries };
@@ -39,17 +44,26 @@ template <int IO, int DA, int C, int W, int MODE>
 struct WalkLds {
     static constexpr int kB = Kind<IO>::kB;
     static constexpr bool kOut = MODE == kOutputs || MODE == kQueries;
-    static constexpr int kA = kOut ? C * DA * kB : 0, kBm = C * DA * kB, kV = C * 32 * W * kB;
+    static constexpr int kA = kOut ? C * DA * kB : 0, kBm = C * DA * kB, kV = C * 16 * W * kB;
     static constexpr int kP = kOut ? Scores<IO, C>::kBytes : 0;
     static constexpr int kX = MODE == kQueries ? kV : 0;
     static constexpr int kAtB = kA, kAtV = kAtB + kBm, kAtP = kAtV + kV, kAtX = kAtP + kP;
     static constexpr int kBytes = kAtX + kX;
 };
 
+// Waves of a SIMD that a workgroup of W waves leaves registers for: two workgroups a CU
+// (at 16 bits and heads of 128 each has 73 KB of its LDS), one for larger heads.
+template <int DA, int W>
+constexpr int kWalkWaves = (DA > 128 ? 1 : 2) * W / 4;
+
+// A workgroup takes 16 W columns of a segment of one head.  A chunk goes in two
+// halves: scores and the state's product (with A and B), then what has V in it; the
+// rows of the next chunk are on their way in registers all the time, and go to LDS
+// when the chunk is done, where its outputs, brought to V's place, come out.
 template <int IO, int DA, int C, int W, int MODE>
-__global__ __launch_bounds__(64 * W, DA > 128 || (DA == 128 && W == 2) ? 1 : 2) void decay_walk_kernel(DecayWalk p) {
+__global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel(DecayWalk p) {
     typedef WalkLds<IO, DA, C, W, MODE> L;
-    constexpr int N = 64 * W, kB = Kind<IO>::kB;
+    constexpr int N = 64 * W, kB = Kind<IO>::kB, kCols = 16 * W;
     constexpr bool OUT = L::kOut, REV = MODE == kEffectsBack, DOT = MODE == kQueries;
     const unsigned units = (unsigned)(p.sp.segs * p.Hv * p.slices), u = xcd_unit(blockIdx.x, units);
     if (u >= units) return;
@@ -60,54 +74,70 @@ __global__ __launch_bounds__(64 * W, DA > 128 || (DA == 128 && W == 2) ? 1 : 2) 
     if (MODE == kEffects && s.last) return;
     if (MODE == kEffectsBack && s.index == 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int first = slice * 32 * W, col = first + 32 * wave + (lane & 31);
-    const bool ok = col < p.cols;
-    const int here = p.cols - first < 32 * W ? p.cols - first : 32 * W;
+    const int first = slice * kCols, col = first + 16 * wave + (lane & 15);
+    const bool ok = col < p.cols, wide = DOT && p.wide;
+    const int here = p.cols - first < kCols ? p.cols - first : kCols;
     if (OUT && p.clear && s.index == 0 && p.sp.cu) {
         // tokens before the first sequence and behind the last
-        clear_unheld(p.sp, s, p.out, DOT && p.wide ? 4 : kB, p.Hv, p.cols, h, first, here);
+        clear_unheld(p.sp, s, p.out, wide ? 4 : kB, p.Hv, p.cols, h, first, here);
     }
-    const long long size = (long long)p.rows * p.cols;
+    const long long size = (long long)p.rows * p.cols, at_col = ok ? col * p.cs : 0;
     State<DA> S;
     S.clear();
     if (OUT) {
-        if (p.seg) S.load(p.seg + (seg * (long long)p.Hv + h) * size + (ok ? col * p.cs : 0), p.rs, ok, p.rows);
+        if (p.seg) S.load(p.seg + (seg * (long long)p.Hv + h) * size + at_col, p.rs, ok, p.rows);
         else if (p.init)
-            S.load(p.init + (s.seq * (long long)p.Hv + h) * size + (ok ? col * p.cs : 0), p.rs, ok, p.rows);
+            S.load(p.init + (s.seq * (long long)p.Hv + h) * size + at_col, p.rs, ok, p.rows);
     }
 
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    char* A = lds;
-    char* B = lds + L::kAtB;
-    char* V = lds + L::kAtV;
-    char* P = lds + L::kAtP;
-    __shared__ __attribute__((aligned(16))) Factors<C> F[2];
-    __shared__ __attribute__((aligned(16))) float back[C];
+    char* const A = lds;
+    char* const B = lds + L::kAtB;
+    char* const V = lds + L::kAtV;
+    char* const P = lds + L::kAtP;
+    __shared__ __attribute__((aligned(16))) Factors<C> F[8];
+    __shared__ __attribute__((aligned(16))) float back[C / 32 * C];
+    __shared__ float dots[DOT ? W : 1][DOT ? C : 1];
+    __shared__ int unbounded[2];
+    __shared__ double sums[4];
     const int chunks = (s.to - s.from + C - 1) / C;
     const Tokens a = rows_of<IO>(p.a, s, h), b = rows_of<IO>(p.b, s, h), v = rows_of<IO>(p.v, s, h);
     const int pieces = p.rows * kB / 16, vpieces = here * kB / 16;
-    const long long vcol = (long long)first * kB;
-    const Tokens vs = {v.base + vcol, v.bytes};
-    const float* gates = p.fixed ? p.g + h : p.g + (s.b * p.sp.T + s.t0) * p.Hv + h;
-    const auto log_decay = [&](int at, int n) {
-        return p.fixed ? gates[0] : gates[(long long)(at + (lane < n ? lane : n - 1)) * p.Hv];
-    };
-    double sum = 0;
-    Moving<IO, DA, C, N> ma, mb;
-    Moving<IO, 32 * W, C, N> mv, mx;
+    const Tokens vs = {v.base + first * kB, v.bytes};
     Tokens x = vs;
     if (DOT) {
         x = rows_of<IO>(p.x, s, h);
-        x.base += vcol;
+        x.base += first * kB;
     }
-    __shared__ float dots[DOT ? W : 1][DOT ? C : 1];
-    const auto fetch = [&](int at, int n) {
+    const float* gates = p.fixed ? p.g + h : p.g + (s.b * p.sp.T + s.t0) * p.Hv + h;
+    // tokens of the chunk number i of the walk, its first one
+    const auto count = [&](int i) { return min(C, s.to - s.from - i * C); };
+    double sum = 0;
+    // of chunks i .. i + 3, by the first four waves
+    const auto log_decays = [&](int i) {
+        const int n = wave < 4 ? count(i + wave) : 0;
+        if (n <= 0) return 0.f;
+        if (p.fixed) return gates[0];
+        return gates[(long long)(s.from + (i + wave) * C + min(lane, n - 1)) * p.Hv];
+    };
+    const auto factors = [&](int i, float g) {
+        const int n = wave < 4 ? count(i + wave) : 0;
+        if (n <= 0) return;
+        const double D = decays_to<C>(g, p.fixed, n);
+        put_factors<C, REV>(F[(i + wave) & 7], D, p.sf, p.sw);
+        if (!OUT) sum += __shfl(D, C - 1);
+    };
+    Moving<IO, DA, C, N> ma, mb;
+    Moving<IO, kCols, C, N> mv, mx, mo;
+    const auto fetch = [&](int i) {
+        const int at = s.from + i * C, n = count(i);
         if (OUT) ma.load(a, at, n, pieces, tid);
         mb.load(b, at, n, pieces, tid);
         mv.load(vs, at, n, vpieces, tid);
         if (DOT) mx.load(x, at, n, vpieces, tid);
     };
-    const auto put = [&](Factors<C>& f, int n) {
+    const auto put = [&](int i) {
+        const int n = count(i);
         if (OUT) ma.clear(n, pieces, tid);
         mb.clear(n, pieces, tid);
         mv.clear(n, vpieces, tid);
@@ -116,42 +146,47 @@ __global__ __launch_bounds__(64 * W, DA > 128 || (DA == 128 && W == 2) ? 1 : 2) 
         mb.store(B, tid);
         mv.store(V, tid);
         if (DOT) mx.store(lds + L::kAtX, tid);
-        if (OUT && mv.unbounded()) f.unbounded = 1;
+        if (OUT && mv.unbounded()) unbounded[i & 1] = 1;
     };
-    const auto factors = [&](Factors<C>& f, float g, int n) {
-        const double D = decays_to<C>(g, p.fixed, n);
-        put_factors<C, REV>(f, D, p.sf, p.sw);
-        sum += __shfl(D, C - 1);
-        if (lane == 0) f.unbounded = 0;
-    };
+    const int ob = wide ? 4 : kB;
+    const long long row = (long long)p.Hv * p.cols * ob;
+    char* const out = (char*)p.out + (s.b * p.sp.T + s.t0 + s.from) * row +
+                      (long long)(h * p.cols + first) * ob;
     if (chunks) {
-        const int at = s.from, n = s.to - at < C ? s.to - at : C;
-        fetch(at, n);
-        if (wave == 0) factors(F[0], log_decay(at, n), n);
+        fetch(0);
+        factors(0, log_decays(0));
+        if (tid < 2) unbounded[tid] = 0;
         __syncthreads();
-        put(F[0], n);
+        put(0);
         __syncthreads();
     }
-    for (int ch = 0; ch < chunks; ++ch) {
-        const Factors<C>& f = F[ch & 1];
-        const int at = s.from + ch * C, n = s.to - at < C ? s.to - at : C;
-        const bool more = ch + 1 < chunks;
-        const int next = more ? at + C : at, m = s.to - next < C ? s.to - next : C;
+    for (int i = 0; i < chunks; ++i) {
+        const Factors<C>& f = F[i & 7];
+        const bool more = i + 1 < chunks;
         float g = 0.f;
-        if (more) {
-            fetch(next, m);
-            if (wave == 0) g = log_decay(next, m);
+        if (DOT) {
+            const int chunk = s.from / C + i;
+            if (chunk % p.anchor_every == 0 && first + 16 * wave < p.cols) {
+                const int tiles = 2 * ((p.rows + 31) / 32);
+                S.store_tiles(p.anchors +
+                                  (anchor_of(p.sp, s, C, p.anchor_every, chunk) * p.Hv + h) *
+                                      p.anchor_floats +
+                                  (long long)(first / 16 + wave) * tiles * 256,
+                              tiles);
+            }
         }
-        dfloat16 acc[C / 32];
+        if (more) fetch(i + 1);
+        if ((i & 3) == 0) g = log_decays(i + 4);
+        dfloat4 acc[C / 16];
         if (OUT) {
             make_scores<IO, DA, C, W, false>(A, B, P, back, f, p.ss, wave);
             __builtin_amdgcn_sched_barrier(0);
             state_product<IO, DA, C, IO == IO_BF16 && !DOT ? 2 : Kind<IO>::NS>(A, S, f, acc);
             __builtin_amdgcn_sched_barrier(0);
-            if (DOT) row_dots<IO, 32 * W, C>(lds + L::kAtX, 32 * wave, acc, dots[wave]);
+            if (DOT) row_dots<IO, kCols, C>(lds + L::kAtX, 16 * wave, acc, dots[wave]);
             __syncthreads();
         }
-        if (DOT && wave == 0) {
+        if (DOT && wave == W - 1) {
             // from the chunk's last token on
             double d = 0;
             if (lane < C)
@@ -159,55 +194,63 @@ __global__ __launch_bounds__(64 * W, DA > 128 || (DA == 128 && W == 2) ? 1 : 2) 
                 for (int w = 0; w < W; ++w) d += dots[w][C - 1 - lane];
             d = prefix_sum(d);
             const int t = C - 1 - lane;
-            if (t >= 0 && t < n)
-                p.before[((long long)slice * p.Hv + h) * p.tokens + s.b * p.sp.T + s.t0 + at + t] = (float)d;
+            if (t == 0) {
+                const long long slot0 = p.sp.cu ? s.t0 / C + s.seq : s.b * ((p.sp.T + C - 1) / C);
+                p.before_all[(slice * p.slots + slot0 + s.from / C + i) * p.Hv + h] = d;
+            }
+            if (t >= 0 && t < count(i))
+                p.before[((long long)slice * p.Hv + h) * p.tokens + s.b * p.sp.T + s.t0 + s.from +
+                         i * C + t] = (float)d;
         }
-        Frag<IO> vf[C / 16];
-        const ColReader<IO, 32 * W, false> vcols(fresh_lane());
+        Frag<IO> vf[C / 32];
+        const ColReader<IO, kCols, false> vcols(fresh_lane());
 #pragma unroll
-        for (int kb = 0; kb < C / 16; ++kb) vf[kb] = vcols.get(V, 16 * kb, 32 * wave);
+        for (int kb = 0; kb < C / 32; ++kb) vf[kb] = vcols.get(V, 32 * kb, wave);
         if (OUT) {
-            scores_product<IO, C, false>(P, back, vf, f.unbounded, acc);
+            scores_product<IO, C, false>(P, back, vf, unbounded[i & 1], acc);
             __builtin_amdgcn_sched_barrier(0);
-            const bool wide = DOT && p.wide;
-            const int ob = wide ? 4 : kB;
-            const long long row = (long long)p.Hv * p.cols * ob;
-            store_rows<IO, 32 * W, C>(
-                V, 32 * wave, acc,
-                (char*)p.out + (s.b * p.sp.T + s.t0 + at) * row + (long long)(h * p.cols + first + 32 * wave) * ob,
-                row, (here - 32 * wave) * ob / 16, wide, n);
+            if (wide) rows_to_memory<C>(out + i * C * row + 64 * wave, row, ok, count(i), acc);
+            else rows_to_tile<IO, kCols, C>(V, 16 * wave, acc);
         }
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(B, vf, f, S);
-        if (wave == 0 && more) factors(F[(ch + 1) & 1], g, m);
+        if ((i & 3) == 0) factors(i + 4, g);
+        if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
-        if (more) put(F[(ch + 1) & 1], m);
+        if (OUT && !wide) mo.take(V, tid);
+        if (more) put(i + 1);
+        if (OUT && !wide) mo.write(out + i * C * row, row, count(i), 0, vpieces, tid);
         __syncthreads();
     }
     if (OUT) {
         if (s.last && p.fin)
-            S.store(p.fin + (s.seq * (long long)p.Hv + h) * size + col * p.cs, p.rs, ok, p.rows);
+            S.store(p.fin + (s.seq * (long long)p.Hv + h) * size + at_col, p.rs, ok, p.rows);
         if (DOT && s.last) {
             double d = 0;
             if (p.dfin) {
-                const float* df = p.dfin + (s.seq * (long long)p.Hv + h) * size + col * p.cs;
+                const float* df = p.dfin + (s.seq * (long long)p.Hv + h) * size + at_col;
 #pragma unroll
-                for (int i = 0; i < DA / 32; ++i)
+                for (int i = 0; i < State<DA>::N; ++i)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int e = State<DA>::element(i, r, lane >> 5);
+                    for (int r = 0; r < 4; ++r) {
+                        const int e = State<DA>::element(i, r, lane >> 4);
                         if (ok && e < p.rows) d += (double)df[e * p.rs] * S.t[i][r];
                     }
             }
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) d += __shfl_xor(d, m);
-            if (lane < 4 / W)
-                p.ends[(s.seq * (long long)p.Hv + h) * 4 * p.slices + 4 * slice + wave + W * lane] =
-                    lane ? 0.f : (float)d;
+            if (lane < 8 / W)
+                p.ends[(s.seq * (long long)p.Hv + h) * 8 * p.slices + 8 * slice + wave + W * lane] =
+                    lane ? 0 : d;
         }
     } else {
-        S.store(p.seg + (seg * (long long)p.Hv + h) * size + col * p.cs, p.rs, ok, p.rows);
-        if (slice == 0 && tid == 0) p.seg_g[seg * (long long)p.Hv + h] = sum;
+        S.store(p.seg + (seg * (long long)p.Hv + h) * size + at_col, p.rs, ok, p.rows);
+        if (slice == 0) {
+            if (lane == 0 && wave < 4) sums[wave] = sum;
+            __syncthreads();
+            if (tid == 0)
+                p.seg_g[seg * (long long)p.Hv + h] = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        }
     }
 }
 
@@ -219,7 +262,7 @@ hipError_t decay_walk_launch(const DecayWalk& p, hipStream_t s) {
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     DecayWalk w = p;
-    w.slices = (p.cols + 32 * W - 1) / (32 * W);
+    w.slices = (p.cols + 16 * W - 1) / (16 * W);
     const long long units = p.sp.segs * p.Hv * w.slices;
     hipLaunchKernelGGL(kernel, dim3((unsigned)xcd_blocks(units)), dim3(64 * W), bytes, s, w);
     return hipGetLastError();
@@ -229,10 +272,10 @@ hipError_t decay_walk_cols(const DecayWalk& p, hipStream_t s) {
     constexpr int C = IO == IO_F32 || DA > 128 ? 32 : 64;
     // the chunks of the gradients' other walk, which has wide rows then
     if constexpr (MODE == kQueries && C == 64)
-        if (p.cols > 128) return decay_walk_launch<IO, DA, 32, 4, MODE>(p, s);
-    // two waves where four would have nothing to do
-    return p.cols <= 64 ? decay_walk_launch<IO, DA, C, 2, MODE>(p, s)
-                        : decay_walk_launch<IO, DA, C, 4, MODE>(p, s);
+        if (p.cols > 128) return decay_walk_launch<IO, DA, 32, 8, MODE>(p, s);
+    // four waves where eight would have nothing to do
+    return p.cols <= 64 ? decay_walk_launch<IO, DA, C, 4, MODE>(p, s)
+                        : decay_walk_launch<IO, DA, C, 8, MODE>(p, s);
 }
 template <int IO, int MODE>
 hipError_t decay_walk_io(const DecayWalk& p, hipStream_t s) {
