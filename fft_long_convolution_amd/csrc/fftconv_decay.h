@@ -49,9 +49,8 @@ struct DecayStepParams {
 };
 hipError_t launch_decay_step(int io, const DecayStepParams& p, hipStream_t s);
 
-// Tokens of a chunk: 64, and 32 where the chunk's rows in LDS would leave a CU
-// one workgroup (fp32, heads of more than 128).
-inline int decay_chunk(int io, int widest) { return io == IO_F32 || widest > 128 ? 32 : 64; }
+constexpr int kDecayChunk = 32;      // tokens
+constexpr int kDecayCols = 64;       // columns of a head that a workgroup takes
 constexpr int kSegAlign = 64;        // segments are cut at multiples of it
 
 // A token matrix, [B][T][H][D] with strides in elements; value head h reads
@@ -127,10 +126,10 @@ struct DecayGradParams {
     float* dinit;                    // [nseq][Hv][Dk][Dv] or null
 };
 hipError_t launch_decay_bwd(int io, const DecayGradParams& p, hipStream_t s);
-// Chunks between anchors.  A decay for each token: every fourth, 16 KB of states
-// written and read for each 64 tokens of a head of 128.  A fixed decay's dg sums what
-// all tokens of a chunk share, and its error with it: every chunk.
-inline int decay_anchor_every(bool fixed) { return fixed ? 1 : 4; }
+// Chunks between anchors.  A decay for each token: every eighth, 8 KB of states
+// written and read for each chunk of a head of 128.  A fixed decay's dg sums what
+// all tokens of a chunk share, and its error with it: every second.
+inline int decay_anchor_every(bool fixed) { return fixed ? 2 : 8; }
 // Anchors in all; a packed sequence's start at cu / (so many chunks) + its number.
 inline size_t decay_anchors(size_t T, size_t nseq, bool packed, size_t n) {
     return packed ? T / n + nseq : nseq * ((T + n - 1) / n);
@@ -141,8 +140,8 @@ inline size_t decay_anchor_floats(int Dk, int Dv) {
 }
 // Workgroups of the last pass over dg take so many chunks of a sequence.
 constexpr int kDgChunks = 64;
-inline size_t decay_dg_units(size_t T, size_t nseq, bool packed, int chunk) {
-    const size_t n = (size_t)kDgChunks * chunk;
+inline size_t decay_dg_units(size_t T, size_t nseq, bool packed) {
+    const size_t n = (size_t)kDgChunks * kDecayChunk;
     return packed ? T / n + nseq : nseq * (T ? (T + n - 1) / n : 1);
 }
 

@@ -16,12 +16,12 @@
 //   s in it, u behind:            sum over s < t of k_s . (dk_s's part with X)
 //   both in it:                   sums of W over rectangles
 //   s before, u behind:           A = e^Dc <X, S0>, the same for the whole chunk
-// The walk of dq leaves S0 of every fourth chunk for A.  Between them A follows from
+// The walk of dq leaves S0 of every eighth chunk for A.  Between them A follows from
 // the next chunk's A': A + (s in it, u behind) by all tokens = A' + (s before, u in the
 // next) by all of its; it is taken as 0 where e^Dc is below 2^-22, which the terms'
 // own errors reach.  A fixed decay's dg sums A over all tokens, so its errors too: it
-// has S0 of every chunk.  (With chains to the sequence's end dg of 2 x 1501 tokens of
-// one decay a head was off by 1.4e-5, in fours by up to 4e-6.)
+// has S0 of every second.  (With chains to the sequence's end dg of 2 x 1501 tokens of
+// one decay a head was off by 1.4e-5.)
 #include "fftconv_decay_walk.h"
 
 namespace fftconv {
@@ -29,8 +29,8 @@ namespace {
 
 template <int IO, int DA>
 struct Back {
-    static constexpr int C = IO == IO_F32 || DA > 128 ? 32 : 64;
-    static constexpr int RW = DA <= 64 ? 4 : 8;          // waves of a role
+    static constexpr int C = kDecayChunk;
+    static constexpr int RW = 4;                         // waves of a role
     static constexpr int kTile = C * DA * Kind<IO>::kB;
     static constexpr int kP = Scores<IO, C>::kBytes;
     static constexpr int kBytes = 4 * kTile + 2 * kP;
@@ -121,7 +121,7 @@ __device__ __forceinline__ void make_scores_and_sums(const char* V, const char* 
 // chunks backward in time, with the gradient X of the state, columns of Dv in the
 // first role's waves (dv) and, transposed, columns of Dk in the second's (dk).
 template <int IO, int DA>
-__global__ __launch_bounds__((DA <= 64 ? 512 : 1024), 4) void decay_back_kernel(DecayGradParams p,
+__global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(DecayGradParams p,
                                                                                int slices) {
     typedef Back<IO, DA> L;
     constexpr int C = L::C, RW = L::RW, N = 128 * RW, kB = Kind<IO>::kB, kCols = 16 * RW;
@@ -186,37 +186,53 @@ __global__ __launch_bounds__((DA <= 64 ? 512 : 1024), 4) void decay_back_kernel(
         put_factors<C, true>(F[(i + place) & 7], decays_to<C>(g, f.fixed, count(i + place)), 1.f,
                              f.scale);
     };
-    Moving<IO, DA, C, N> mq, mk, mv, md;
-    const auto fetch = [&](int i) {
-        const int at = start(i), n = count(i);
-        mq.load(q, at, n, kp, tid);
-        mk.load(k, at, n, kp, tid);
-        mv.load(v, at, n, vp, tid);
-        md.load(d, at, n, vp, tid);
+    typedef Moving<IO, DA, C, N> Move;
+    Move mq, mk, mv, md;
+    const int last = s.from + (chunks - 1) * C;
+    Source sq = Move::source(q, last, tid), sk = Move::source(k, last, tid),
+           sv = Move::source(v, last, tid), sd = Move::source(d, last, tid);
+    const uint32_t piece = Move::place(tid);
+    // n: tokens of the chunk
+    const auto fetch = [&](int n) {
+        const int lk = Move::left(tid, n, kp), lv = Move::left(tid, n, vp);
+        mq.load(sq, lk);
+        mk.load(sk, lk);
+        mv.load(sv, lv);
+        md.load(sd, lv);
+        sq.p -= C * (long long)sq.stride;
+        sk.p -= C * (long long)sk.stride;
+        sv.p -= C * (long long)sv.stride;
+        sd.p -= C * (long long)sd.stride;
     };
-    const auto put = [&](int i) {
-        const int n = count(i);
-        mq.clear(n, kp, tid);
-        mk.clear(n, kp, tid);
-        mv.clear(n, vp, tid);
-        md.clear(n, vp, tid);
-        mq.store(Q, tid);
-        mk.store(K, tid);
-        mv.store(V, tid);
-        md.store(DO, tid);
-        if (mq.unbounded() || md.unbounded()) unbounded[i & 1] = 1;
+    const auto put = [&](int n, int* bad) {
+        if (n < C || kp < Move::kPieces || vp < Move::kPieces) {
+            const int lk = Move::left(tid, n, kp), lv = Move::left(tid, n, vp);
+            mq.clear(lk);
+            mk.clear(lk);
+            mv.clear(lv);
+            md.clear(lv);
+        }
+        mq.store(Q, piece, tid);
+        mk.store(K, piece, tid);
+        mv.store(V, piece, tid);
+        md.store(DO, piece, tid);
+        if (mq.unbounded() || md.unbounded()) *bad = 1;
     };
-    const int kb = wide ? 4 : kB;
+    const int kb = wide ? 4 : kB, p0 = first * kB / 16;
     const long long krow = (long long)f.Hv * f.Dk * kb, vrow = (long long)f.Hv * f.Dv * kB;
     char* const dk = (char*)(wide ? (void*)p.dk_heads : p.dk) + token0 * krow +
                      (long long)(h * f.Dk + first) * kb;
     char* const dv = (char*)p.dv + token0 * vrow + (long long)(h * f.Dv + first) * kB;
+    // the thread's piece among the slice's columns
+    const int at_piece = tid % Move::kPieces - p0, t0 = tid / Move::kPieces;
+    float g = 0.f;
     if (chunks) {
-        fetch(0);
+        fetch(count(0));
         factors(0, log_decays(0));
+        g = log_decays(4);
         if (tid < 2) unbounded[tid] = 0;
         __syncthreads();
-        put(0);
+        put(count(0), &unbounded[0]);
         __syncthreads();
     }
     const int tile = mine < DA ? wave + first / 16 : 0;        // columns that are in the tiles
@@ -224,7 +240,10 @@ __global__ __launch_bounds__((DA <= 64 ? 512 : 1024), 4) void decay_back_kernel(
         const Factors<C>& fac = F[i & 7];
         const int at = start(i), n = count(i);
         const bool more = i + 1 < chunks;
-        float g = 0.f;
+        if ((i & 3) == 0) {
+            factors(i + 4, g);
+            g = log_decays(i + 8);
+        }
         const bool anchor = at / C % p.anchor_every == 0;
         if (anchor && keys) {
             double x = 0;
@@ -240,8 +259,7 @@ __global__ __launch_bounds__((DA <= 64 ? 512 : 1024), 4) void decay_back_kernel(
             for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
             if (lane == 0) products[wave] = x;
         }
-        if (more) fetch(i + 1);
-        if ((i & 3) == 0) g = log_decays(i + 4);
+        if (more) fetch(C);
         dfloat4 acc[C / 16];
         if (keys) {
             make_scores_and_sums<IO, DA, C, RW>(V, DO, K, Q, P, back[1], fac, f.scale, wave, sums);
@@ -292,25 +310,28 @@ __global__ __launch_bounds__((DA <= 64 ? 512 : 1024), 4) void decay_back_kernel(
         else if (mine < DA) rows_to_tile<IO, DA, C>(keys ? V : K, mine, acc);
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(keys ? DO : Q, val, fac, X);
-        if ((i & 3) == 0) factors(i + 4, g);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
-        Moving<IO, DA, C, N> outk, outv;
-        outv.take(K, tid);
-        outk.take(V, tid);
-        if (more) put(i + 1);
-        const int p0 = first * kB / 16;
-        outv.write(dv + at * vrow, vrow, n, p0, p0 + nv * kB / 16, tid);
-        if (!wide) outk.write(dk + at * krow, krow, n, p0, p0 + nk * kB / 16, tid);
+        Move rows_k, rows_v;
+        rows_v.take(K, piece, tid);
+        rows_k.take(V, piece, tid);
+        if (more) put(C, &unbounded[(i + 1) & 1]);
+        const int here = at_piece >= 0 ? n - t0 : 0;
+        rows_v.write(dv + at * vrow, (uint32_t)(t0 * vrow) + 16u * at_piece, vrow,
+                     at_piece < nv * kB / 16 ? here : 0, tid);
+        if (!wide)
+            rows_k.write(dk + at * krow, (uint32_t)(t0 * krow) + 16u * at_piece, krow,
+                         at_piece < nk * kB / 16 ? here : 0, tid);
         __syncthreads();
     }
     if (!keys && s.index == 0 && p.dinit)
         X.store(p.dinit + (s.seq * (long long)f.Hv + h) * size + at_col, rs, ok, rows);
 }
 
-// dg from its parts, kDgChunks chunks of C tokens a workgroup.
-__global__ __launch_bounds__(256) void decay_dg_kernel(DecayGradParams p, DecaySpans sp, int C,
-                                                       int ks, int vs, int ends) {
+// dg from its parts, kDgChunks chunks a workgroup.  Parts by columns: ks of Dk, vs of Dv.
+__global__ __launch_bounds__(256) void decay_dg_kernel(DecayGradParams p, DecaySpans sp, int ks,
+                                                       int vs) {
+    constexpr int C = kDecayChunk;
     const DecayParams& f = p.f;
     const int h = (int)(blockIdx.x % f.Hv), lane = threadIdx.x & 63;
     const unsigned part = blockIdx.x / f.Hv;
@@ -346,8 +367,8 @@ __global__ __launch_bounds__(256) void decay_dg_kernel(DecayGradParams p, DecayS
                             for (int i = 0; i < ks; ++i)
                                 b += p.before_all[(i * p.slots + slot0 + c + 1) * f.Hv + h];
                         } else {
-                            for (int i = 0; i < ends; ++i)
-                                b += p.ends[(s.seq * (long long)f.Hv + h) * ends + i];
+                            for (int i = 0; i < 4 * ks; ++i)
+                                b += p.ends[(s.seq * (long long)f.Hv + h) * 4 * ks + i];
                         }
                         if (!keep) b = 0;
                     }
@@ -494,14 +515,14 @@ hipError_t bwd_io(const DecayGradParams& p, hipStream_t s) {
                             : back_launch<IO, 256>(p, s);
         if (e != hipSuccess) return e;
     }
-    const int C = decay_chunk(IO, widest), ks = (f.Dk + 127) / 128, vs = (f.Dv + 127) / 128;
+    const int ks = (f.Dk + kDecayCols - 1) / kDecayCols, vs = (f.Dv + kDecayCols - 1) / kDecayCols;
     DecaySpans sp = f.sp;
-    sp.seg_tokens = kDgChunks * C;
-    sp.segs = (long long)decay_dg_units(sp.T, sp.nseq, sp.cu != nullptr, C);
+    sp.seg_tokens = kDgChunks * kDecayChunk;
+    sp.segs = (long long)decay_dg_units(sp.T, sp.nseq, sp.cu != nullptr);
     sp.per = sp.cu ? 1 : (int)(sp.T ? (sp.T + sp.seg_tokens - 1) / sp.seg_tokens : 1);
     if (sp.segs)
         hipLaunchKernelGGL(decay_dg_kernel, dim3((unsigned)(sp.segs * f.Hv)), dim3(256), 0, s, p, sp,
-                           C, ks, vs, 8 * ks);
+                           ks, vs);
     if (f.fixed)
         hipLaunchKernelGGL(decay_dg_sum_kernel, dim3(f.Hv), dim3(256), 0, s, p.sums, sp.segs, f.Hv,
                            p.dg);

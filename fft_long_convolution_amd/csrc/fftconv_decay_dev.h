@@ -207,9 +207,14 @@ struct ColReader {
     }
 };
 
-// C tokens of rows on their way from memory to LDS (or back), by N threads (tid < N),
-// each of which keeps to its pieces: tokens from n on and pieces from the row's end
-// on are 0.
+// Rows of one head on their way: the walk's present ones (a uniform address) and the
+// thread's part of them.
+struct Source {
+    const char* p;
+    uint32_t stride, mine;
+};
+// C tokens of rows on their way from memory to LDS (or back), by N threads, each of
+// which keeps to its pieces: tokens from n on and pieces from the row's end on are 0.
 template <int IO, int D, int C, int N>
 struct Moving {
     static constexpr int kPieces = Rows<IO, D>::kPieces, kAll = C * kPieces;
@@ -217,68 +222,70 @@ struct Moving {
     static_assert(N % kPieces == 0 && (kAll % N == 0 || kAll < N), "threads share evenly");
     du4 r[kMine];
     static __device__ __forceinline__ bool idle(int tid) { return kAll < N && tid >= kAll; }
-    static __device__ __forceinline__ uint32_t place(int j, int tid) {
-        return Rows<IO, D>::at(j * kStep + tid / kPieces, tid % kPieces);
+    // of the thread's first piece, in a tile
+    static __device__ __forceinline__ uint32_t place(int tid) {
+        return Rows<IO, D>::at(tid / kPieces, tid % kPieces);
+    }
+    static __device__ __forceinline__ uint32_t next(uint32_t place, int j) {
+        return (place ^ (swirl<kPieces>(j * kStep) << 4)) + j * kStep * Rows<IO, D>::kRow;
+    }
+    // tokens of the thread's, counted from its first one
+    static __device__ __forceinline__ int left(int tid, int n, int pieces) {
+        return tid % kPieces < pieces ? n - tid / kPieces : 0;
+    }
+    static __device__ __forceinline__ Source source(const Tokens& x, long long token, int tid) {
+        return {x.at(token), (uint32_t)x.bytes,
+                (uint32_t)(tid / kPieces) * (uint32_t)x.bytes + 16u * (tid % kPieces)};
     }
     // Loads in flight may meet neither an instruction nor the end of a branch: those
     // of what is not there read the first piece, and are dropped by clear().
-    __device__ __forceinline__ void load(const Tokens& x, long long token, int n, int pieces,
-                                         int tid) {
-        const char* p = x.at(token);
-        const uint32_t stride = (uint32_t)x.bytes;
-        tid = fresh(tid);
-        const int u = tid % kPieces, left = u < pieces ? n - tid / kPieces : 0;
-        const uint32_t mine = (uint32_t)(tid / kPieces) * stride + 16u * u;
+    __device__ __forceinline__ void load(const Source& s, int left) {
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
-            r[j] = *(const du4*)(p + (j * kStep < left ? mine + j * kStep * stride : 0u));
+            r[j] = *(const du4*)(s.p + (j * kStep < left ? s.mine + j * kStep * s.stride : 0u));
     }
-    __device__ __forceinline__ void clear(int n, int pieces, int tid) {
-        if (n >= C && pieces >= kPieces) return;
-        tid = fresh(tid);
-        const int left = tid % kPieces < pieces ? n - tid / kPieces : 0;
+    __device__ __forceinline__ void clear(int left) {
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
 #pragma unroll
             for (int w = 0; w < 4; ++w) r[j][w] = j * kStep < left ? r[j][w] : 0;
     }
-    __device__ __forceinline__ void store(char* m, int tid) const {
-        tid = fresh(tid);
+    __device__ __forceinline__ void store(char* m, uint32_t place, int tid) const {
         if (idle(tid)) return;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) *(du4*)(m + place(j, tid)) = r[j];
+        for (int j = 0; j < kMine; ++j) *(du4*)(m + next(place, j)) = r[j];
     }
-    __device__ __forceinline__ void take(const char* m, int tid) {
-        tid = fresh(tid);
+    __device__ __forceinline__ void take(const char* m, uint32_t place, int tid) {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) r[j] = *(const du4*)(m + (idle(tid) ? 0 : place(j, tid)));
+        for (int j = 0; j < kMine; ++j) r[j] = *(const du4*)(m + (idle(tid) ? 0 : next(place, j)));
     }
-    // pieces from .. to - 1 of the tokens below n, `row` bytes apart, piece `from` first
-    __device__ __forceinline__ void write(char* out, long long row, int n, int from, int to,
+    // to rows `row` bytes apart, the thread's first piece at mine
+    __device__ __forceinline__ void write(char* out, uint32_t mine, long long row, int left,
                                           int tid) const {
-        tid = fresh(tid);
         if (idle(tid)) return;
-        const int u = tid % kPieces, left = u >= from && u < to ? n - tid / kPieces : 0;
-        const uint32_t mine = (uint32_t)(tid / kPieces) * (uint32_t)row + 16u * (u - from);
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
             if (j * kStep < left) *(du4*)(out + j * kStep * row + mine) = r[j];
     }
     // whether an element is infinite or NaN
     __device__ __forceinline__ bool unbounded() const {
-        uint32_t most = 0;
+        if constexpr (IO == IO_F32) {
+            uint32_t most = 0;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j)
+            for (int j = 0; j < kMine; ++j)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t u = r[j][w];
-                if constexpr (IO == IO_F32) {
-                    most = max(most, u & 0x7fffffffu);
-                } else {
-                    most = max(most, max((u & 0x7fffu) << 16, u & 0x7fff0000u));
-                }
-            }
-        return most >= (IO == IO_F16 ? 0x7c000000u : 0x7f800000u);
+                for (int w = 0; w < 4; ++w) most = max(most, r[j][w] & 0x7fffffffu);
+            return most >= 0x7f800000u;
+        } else {
+            typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+            u2 most = {0, 0};
+#pragma unroll
+            for (int j = 0; j < kMine; ++j)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    most = __builtin_elementwise_max(most, __builtin_bit_cast(u2, r[j][w] & 0x7fff7fffu));
+            return max(most.x, most.y) >= (IO == IO_F16 ? 0x7c00 : 0x7f80);
+        }
     }
 };
 
@@ -329,7 +336,8 @@ __device__ __forceinline__ void terms(const float (&x)[8], float s, Frag<IO> (&t
                 } else {
                     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
                     const b2 h = {(__bf16)a, (__bf16)b};
-                    const uint32_t u = __builtin_bit_cast(uint32_t, h);
+                    uint32_t u = __builtin_bit_cast(uint32_t, h);
+                    asm("" : "+v"(u));       // one conversion of two values
                     t[n].v[i] = u;
                     if (n + 1 < N) {
                         a -= __uint_as_float(u << 16);
@@ -371,18 +379,21 @@ __device__ __forceinline__ float exp2_of(int whole, float rest) {
     return __builtin_ldexpf(__builtin_amdgcn_exp2f(rest), whole);
 }
 // 2^x rounded to fp32 once: of a chunk's factors, which all elements of a row and the
-// whole state share, so that their errors do not average out.  Taylor terms of
-// 2^rest = e^(rest log 2) up to (0.35)^11 / 11! = 2e-13.
+// whole state share, so that their errors do not average out.  With y = rest log 2,
+// at most 0.35: 1 + y in 64 bits and the Taylor terms from y^2 / 2 on, below 0.07, in
+// 32 (off by 2^-28), up to y^9 / 9! (2e-10).
 __device__ __forceinline__ float exact_exp2(double x) {
     const double n = __builtin_rint(x), y = (x - n) * 0.6931471805599453;
-    double e = 1.0 / 3628800;
-#pragma unroll
-    for (int i = 9; i >= 0; --i) {
-        constexpr double inverse[10] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720,
-                                        1.0 / 5040, 1.0 / 40320, 1.0 / 362880};
-        e = __builtin_fma(e, y, inverse[i]);
-    }
-    return __builtin_ldexpf((float)e, (int)n);
+    const float z = (float)y;
+    float e = 1.f / 362880;
+    e = fmaf(e, z, 1.f / 40320);
+    e = fmaf(e, z, 1.f / 5040);
+    e = fmaf(e, z, 1.f / 720);
+    e = fmaf(e, z, 1.f / 120);
+    e = fmaf(e, z, 1.f / 24);
+    e = fmaf(e, z, 1.f / 6);
+    e = fmaf(e, z, 0.5f);
+    return __builtin_ldexpf((float)(1.0 + (y + (double)(e * z * z))), (int)n);
 }
 // By the 64 lanes of one wave: D of the lane's token (n tokens, those behind have the
 // last one's), in units of log 2.  g: the token's log decay (0 behind the last).
@@ -632,14 +643,43 @@ __device__ __forceinline__ void state_product(const char* A, const State<DA>& S,
     }
 }
 
-// acc += P V: v holds the column of V, block kb the tokens 32 kb ...
+// The values with 0 for those that are infinite or NaN; bad: the first (REV: last) of
+// their tokens, t the first of the eight.
+template <int IO, bool REV>
+__device__ __forceinline__ Frag<IO> bounded(const Frag<IO>& v, int t, int& bad) {
+    Frag<IO> x = v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bool ok;
+        if constexpr (IO == IO_F32) {
+            float& e = i < 4 ? ((float*)&x.a)[i & 3] : ((float*)&x.b)[i & 3];
+            ok = finite(e);
+            e = ok ? e : 0.f;
+        } else {
+            constexpr uint32_t top = IO == IO_F16 ? 0x7c00u : 0x7f80u;
+            const int shift = 16 * (i & 1);
+            ok = (x.v[i >> 1] >> shift & top) != top;
+            if (!ok) x.v[i >> 1] &= 0xffff0000u >> shift;
+        }
+        if (!ok) bad = REV ? max(bad, t + i) : min(bad, t + i);
+    }
+    return x;
+}
+// acc += P V: values holds the column of V, block kb the tokens 32 kb ...  unbounded: one
+// of V's values is infinite or NaN.  Those are left out, as they would meet the
+// zeros of P, and the column's rows that see one become NaN.
 template <int IO, int C, bool REV>
-__device__ __forceinline__ void add_scores(const char* P, const float* back, int lane,
-                                           const Frag<IO> (&v)[C / 32], dfloat4 (&acc)[C / 16]) {
+__device__ __forceinline__ void scores_product(const char* P, const float* back,
+                                               const Frag<IO> (&values)[C / 32], bool unbounded,
+                                               dfloat4 (&acc)[C / 16]) {
     typedef Scores<IO, C> L;
     constexpr int NP = Kind<IO>::NP;
+    const int lane = fresh_lane(), g = lane >> 4;
+    int bad = REV ? -1 : C;
 #pragma unroll
     for (int kb = 0; kb < L::KB; ++kb) {
+        Frag<IO> v = values[kb];
+        if (unbounded) v = bounded<IO, REV>(v, 32 * kb + 8 * g, bad);
         dfloat4 s[L::M];
 #pragma unroll
         for (int m = 0; m < L::M; ++m)
@@ -649,13 +689,13 @@ __device__ __forceinline__ void add_scores(const char* P, const float* back, int
 #pragma unroll
             for (int m = 0; m < L::M; ++m)
                 if (REV ? kb >= m / 2 : kb <= m / 2)
-                    s[m] = mma16<IO>(L::get(P, lane, n, m, kb), v[kb], s[m]);
+                    s[m] = mma16<IO>(L::get(P, lane, n, m, kb), v, s[m]);
         products_done();
 #pragma unroll
         for (int m = 0; m < L::M; ++m) {
             if constexpr (IO == IO_F16) {
                 if (!(REV ? kb >= m / 2 : kb <= m / 2)) continue;
-                const float4 f = *(const float4*)&back[kb * C + 16 * m + 4 * (lane >> 4)];
+                const float4 f = *(const float4*)&back[kb * C + 16 * m + 4 * g];
                 acc[m][0] += s[m][0] * f.x;
                 acc[m][1] += s[m][1] * f.y;
                 acc[m][2] += s[m][2] * f.z;
@@ -665,37 +705,8 @@ __device__ __forceinline__ void add_scores(const char* P, const float* back, int
             }
         }
     }
-}
-// The same where V may hold a value that is infinite or NaN: it is left out, as it
-// would meet the zeros of P, and the column's rows that see it become NaN.
-template <int IO, int C, bool REV>
-__device__ __forceinline__ void scores_product(const char* P, const float* back,
-                                               const Frag<IO> (&values)[C / 32], bool unbounded,
-                                               dfloat4 (&acc)[C / 16]) {
-    const int lane = fresh_lane(), g = lane >> 4;
-    if (!unbounded) {
-        add_scores<IO, C, REV>(P, back, lane, values, acc);
-        return;
-    }
-    Frag<IO> v[C / 32];
-    int bad = REV ? -1 : C;            // the first (last) such token of the column
-#pragma unroll
-    for (int kb = 0; kb < C / 32; ++kb) {
-        float x[8];
-        unpack_frag<IO>(values[kb], x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!finite(x[i])) {
-                const int t = 32 * kb + 8 * g + i;
-                bad = REV ? max(bad, t) : min(bad, t);
-                x[i] = 0.f;
-            }
-        Frag<IO> t[1];
-        terms<IO, 1>(x, 1.f, t);       // exact: they are of the type
-        v[kb] = t[0];
-    }
+    if (!unbounded) return;
     bad = REV ? max_all(bad) : min_all(bad);
-    add_scores<IO, C, REV>(P, back, lane, v, acc);
 #pragma unroll
     for (int m = 0; m < C / 16; ++m)
 #pragma unroll
@@ -718,7 +729,7 @@ __device__ __forceinline__ void weighted(const Frag<IO>& v, const Factors<C>& F,
 template <int IO, int DA, int C>
 __device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&values)[C / 32],
                                              const Factors<C>& F, State<DA>& S) {
-    constexpr int NS = Kind<IO>::NS, KB = C / 32, G = 4;
+    constexpr int NS = Kind<IO>::NS, KB = C / 32, G = 2;
     const int lane = fresh_lane(), g = lane >> 4;
     const ColReader<IO, DA, true> cols(lane);
     const float all = F.all;

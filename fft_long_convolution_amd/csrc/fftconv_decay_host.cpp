@@ -67,9 +67,39 @@ fftconv_status decay_sizes(const fftconv_decay_desc* d) {
     return FFTCONV_OK;
 }
 
-// Tokens of a segment.
+// Tokens of a segment.  A sequence is a chain of chunks; where the heads and columns
+// leave CUs idle, sequences are cut into segments that are walked side by side: once
+// for their effects on the state, and, after a join, for the outputs.  The length is
+// the one of least time by the model below, a whole sequence where that is least.
 size_t decay_segment(const fftconv_decay_desc* d) {
-    return (d->T + kSegAlign) / kSegAlign * kSegAlign;       // one segment a sequence
+    const size_t blocks = (d->T + kSegAlign - 1) / kSegAlign;
+    const size_t whole = (blocks + 1) * kSegAlign;
+    const size_t rows = d->sequences ? d->sequences : d->B;
+    if (!rows || !blocks) return whole;
+    const double heads = (double)rows * d->Hv * ((d->Dv + kDecayCols - 1) / kDecayCols);
+    // us of a block of two chunks: alone on a CU, and what each further one adds
+    const double wide = (d->dtype == FFTCONV_F32 ? 2.0 : 1.0) * (d->Dk > 128 ? 2.0 : d->Dk > 64 ? 1.0 : 0.7);
+    const auto walk = [&](double units) {
+        return wide * (5.0 + 1.8 * (units > 256 ? units / 256 - 1 : 0));
+    };
+    const auto effects = [&](double units) {
+        return wide * (2.4 + 0.8 * (units > 256 ? units / 256 - 1 : 0));
+    };
+    // packed sequences: some are longer than the average
+    const double mean = (double)blocks / (d->sequences ? rows : 1);
+    const double longest = d->sequences ? (mean * 3 < blocks ? mean * 3 : (double)blocks) : mean;
+    double best = longest * walk(heads);
+    size_t most = whole;
+    for (size_t per = 1; per < blocks && per < longest; per = per < 16 ? per + 1 : per * 5 / 4) {
+        const double n = longest / per, all = heads * (mean / per < 1 ? 1 : mean / per);
+        if (n > 256) continue;
+        const double t = per * (walk(all) + effects(all)) + 10.0 + 0.6 * n;
+        if (t < best) {
+            best = t;
+            most = per * kSegAlign;
+        }
+    }
+    return most;
 }
 
 struct DecayLayout {
@@ -98,21 +128,21 @@ bool decay_layout(const fftconv_decay_desc* d, DecayLayout* l) {
     l->seg = cut ? l->segs * d->Hv * d->Dk * d->Dv * 4 : 0;
     l->seg_g = cut ? up16(l->segs * d->Hv * 8) : 0;
     const size_t tokens = d->B * d->T, rows = d->sequences ? d->sequences : d->B;
-    const size_t widest = d->Dk > d->Dv ? d->Dk : d->Dv;
-    const size_t C = (size_t)decay_chunk(d->dtype, (int)widest);
-    const size_t k128 = (d->Dk + 127) / 128, v128 = (d->Dv + 127) / 128;
+    const size_t C = kDecayChunk;
+    // parts by columns, of Dk and of Dv
+    const size_t ks = (d->Dk + kDecayCols - 1) / kDecayCols, vs = (d->Dv + kDecayCols - 1) / kDecayCols;
     l->slots = d->sequences ? d->T / C + d->sequences : d->B * ((d->T + C - 1) / C);
-    l->before = up16(k128 * d->Hv * tokens * 4);
-    l->behind = up16(v128 * d->Hv * tokens * 4);
-    l->ends = up16(rows * d->Hv * k128 * 8 * 8);
-    l->before_all = up16(k128 * l->slots * d->Hv * 8);
-    l->chunks = up16(v128 * l->slots * d->Hv * 16);
+    l->before = up16(ks * d->Hv * tokens * 4);
+    l->behind = up16(vs * d->Hv * tokens * 4);
+    l->ends = up16(rows * d->Hv * ks * 4 * 8);
+    l->before_all = up16(ks * l->slots * d->Hv * 8);
+    l->chunks = up16(vs * l->slots * d->Hv * 16);
     const size_t anchors = decay_anchors(d->T, rows, d->sequences != 0,
                                          C * decay_anchor_every(d->fixed_decay != 0));
     l->anchors = anchors * d->Hv * decay_anchor_floats((int)d->Dk, (int)d->Dv) * 4;
-    l->anchor_dg = up16(k128 * anchors * d->Hv * 8);
+    l->anchor_dg = up16(ks * anchors * d->Hv * 8);
     l->anchor_count = anchors;
-    l->sums = d->fixed_decay ? up16(decay_dg_units(d->T, rows, d->sequences != 0, (int)C) * d->Hv * 8) : 0;
+    l->sums = d->fixed_decay ? up16(decay_dg_units(d->T, rows, d->sequences != 0) * d->Hv * 8) : 0;
     l->shared = d->Hv > d->Hk ? up16(tokens * d->Hv * d->Dk * 4) : 0;
     return true;
 }

@@ -32,7 +32,7 @@ struct DecayWalk {
     const float* dfin;
     double* before_all;              // [slices][slots][Hv]
     long long slots;
-    double* ends;                    // [nseq][Hv][8 slices]
+    double* ends;                    // [nseq][Hv][slices][4]
     int anchor_every;
     float* anchors;
     long long anchor_floats;         // of a head's anchor
@@ -51,17 +51,16 @@ struct WalkLds {
     static constexpr int kBytes = kAtX + kX;
 };
 
-// Waves of a SIMD that a workgroup of W waves leaves registers for: two workgroups a CU
-// (at 16 bits and heads of 128 each has 73 KB of its LDS), one for larger heads.
-template <int DA, int W>
-constexpr int kWalkWaves = (DA > 128 ? 1 : 2) * W / 4;
+// Waves of a SIMD that the walk leaves registers for.
+template <int IO, int DA, int MODE>
+constexpr int kWalkWaves = DA > 128 ? 2 : IO == IO_F32 && DA > 64 ? 3 : 4;
 
 // A workgroup takes 16 W columns of a segment of one head.  A chunk goes in two
 // halves: scores and the state's product (with A and B), then what has V in it; the
 // rows of the next chunk are on their way in registers all the time, and go to LDS
 // when the chunk is done, where its outputs, brought to V's place, come out.
 template <int IO, int DA, int C, int W, int MODE>
-__global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel(DecayWalk p) {
+__global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk_kernel(DecayWalk p) {
     typedef WalkLds<IO, DA, C, W, MODE> L;
     constexpr int N = 64 * W, kB = Kind<IO>::kB, kCols = 16 * W;
     constexpr bool OUT = L::kOut, REV = MODE == kEffectsBack, DOT = MODE == kQueries;
@@ -110,15 +109,16 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel
         x.base += first * kB;
     }
     const float* gates = p.fixed ? p.g + h : p.g + (s.b * p.sp.T + s.t0) * p.Hv + h;
-    // tokens of the chunk number i of the walk, its first one
-    const auto count = [&](int i) { return min(C, s.to - s.from - i * C); };
+    // the first token of chunk number i of the walk in the segment, and its tokens
+    const auto start = [&](int i) { return (REV ? chunks - 1 - i : i) * C; };
+    const auto count = [&](int i) { return i < chunks ? min(C, s.to - s.from - start(i)) : 0; };
     double sum = 0;
     // of chunks i .. i + 3, by the first four waves
     const auto log_decays = [&](int i) {
         const int n = wave < 4 ? count(i + wave) : 0;
         if (n <= 0) return 0.f;
         if (p.fixed) return gates[0];
-        return gates[(long long)(s.from + (i + wave) * C + min(lane, n - 1)) * p.Hv];
+        return gates[(long long)(s.from + start(i + wave) + min(lane, n - 1)) * p.Hv];
     };
     const auto factors = [&](int i, float g) {
         const int n = wave < 4 ? count(i + wave) : 0;
@@ -127,43 +127,64 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel
         put_factors<C, REV>(F[(i + wave) & 7], D, p.sf, p.sw);
         if (!OUT) sum += __shfl(D, C - 1);
     };
-    Moving<IO, DA, C, N> ma, mb;
-    Moving<IO, kCols, C, N> mv, mx, mo;
-    const auto fetch = [&](int i) {
-        const int at = s.from + i * C, n = count(i);
-        if (OUT) ma.load(a, at, n, pieces, tid);
-        mb.load(b, at, n, pieces, tid);
-        mv.load(vs, at, n, vpieces, tid);
-        if (DOT) mx.load(x, at, n, vpieces, tid);
+    typedef Moving<IO, DA, C, N> MoveA;
+    typedef Moving<IO, kCols, C, N> MoveV;
+    MoveA ma, mb;
+    MoveV mv, mx, mo;
+    const long long token = s.from + (chunks ? start(0) : 0);
+    Source sa = MoveA::source(a, token, tid), sb = MoveA::source(b, token, tid),
+           sv = MoveV::source(vs, token, tid), sx = MoveV::source(x, token, tid);
+    const uint32_t pa = MoveA::place(tid), pv = MoveV::place(tid);
+    const bool aligned = pieces >= MoveA::kPieces && vpieces >= MoveV::kPieces;
+    // n: tokens of the chunk
+    const auto fetch = [&](int n) {
+        const int la = MoveA::left(tid, n, pieces), lv = MoveV::left(tid, n, vpieces);
+        if (OUT) ma.load(sa, la);
+        mb.load(sb, la);
+        mv.load(sv, lv);
+        if (DOT) mx.load(sx, lv);
+        constexpr long long kOn = REV ? -C : C;
+        sa.p += kOn * sa.stride;
+        sb.p += kOn * sb.stride;
+        sv.p += kOn * sv.stride;
+        if (DOT) sx.p += kOn * sx.stride;
     };
-    const auto put = [&](int i) {
-        const int n = count(i);
-        if (OUT) ma.clear(n, pieces, tid);
-        mb.clear(n, pieces, tid);
-        mv.clear(n, vpieces, tid);
-        if (DOT) mx.clear(n, vpieces, tid);
-        if (OUT) ma.store(A, tid);
-        mb.store(B, tid);
-        mv.store(V, tid);
-        if (DOT) mx.store(lds + L::kAtX, tid);
-        if (OUT && mv.unbounded()) unbounded[i & 1] = 1;
+    const auto put = [&](int n, int* bad) {
+        if (n < C || !aligned) {
+            const int la = MoveA::left(tid, n, pieces), lv = MoveV::left(tid, n, vpieces);
+            if (OUT) ma.clear(la);
+            mb.clear(la);
+            mv.clear(lv);
+            if (DOT) mx.clear(lv);
+        }
+        if (OUT) ma.store(A, pa, tid);
+        mb.store(B, pa, tid);
+        mv.store(V, pv, tid);
+        if (DOT) mx.store(lds + L::kAtX, pv, tid);
+        if (OUT && mv.unbounded()) *bad = 1;
     };
     const int ob = wide ? 4 : kB;
     const long long row = (long long)p.Hv * p.cols * ob;
-    char* const out = (char*)p.out + (s.b * p.sp.T + s.t0 + s.from) * row +
-                      (long long)(h * p.cols + first) * ob;
+    char* out = (char*)p.out + (s.b * p.sp.T + s.t0 + s.from) * row +
+                (long long)(h * p.cols + first) * ob;
+    const uint32_t omine = tid / MoveV::kPieces * (uint32_t)row + 16u * (tid % MoveV::kPieces);
+    float g = 0.f;
     if (chunks) {
-        fetch(0);
+        fetch(count(0));
         factors(0, log_decays(0));
+        g = log_decays(4);
         if (tid < 2) unbounded[tid] = 0;
         __syncthreads();
-        put(0);
+        put(count(0), &unbounded[0]);
         __syncthreads();
     }
     for (int i = 0; i < chunks; ++i) {
         const Factors<C>& f = F[i & 7];
-        const bool more = i + 1 < chunks;
-        float g = 0.f;
+        const int n = count(i), ahead = count(i + 1);
+        if ((i & 3) == 0) {
+            factors(i + 4, g);
+            g = log_decays(i + 8);
+        }
         if (DOT) {
             const int chunk = s.from / C + i;
             if (chunk % p.anchor_every == 0 && first + 16 * wave < p.cols) {
@@ -175,8 +196,7 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel
                               tiles);
             }
         }
-        if (more) fetch(i + 1);
-        if ((i & 3) == 0) g = log_decays(i + 4);
+        if (ahead) fetch(ahead);
         dfloat4 acc[C / 16];
         if (OUT) {
             make_scores<IO, DA, C, W, false>(A, B, P, back, f, p.ss, wave);
@@ -198,7 +218,7 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel
                 const long long slot0 = p.sp.cu ? s.t0 / C + s.seq : s.b * ((p.sp.T + C - 1) / C);
                 p.before_all[(slice * p.slots + slot0 + s.from / C + i) * p.Hv + h] = d;
             }
-            if (t >= 0 && t < count(i))
+            if (t >= 0 && t < n)
                 p.before[((long long)slice * p.Hv + h) * p.tokens + s.b * p.sp.T + s.t0 + s.from +
                          i * C + t] = (float)d;
         }
@@ -209,17 +229,17 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel
         if (OUT) {
             scores_product<IO, C, false>(P, back, vf, unbounded[i & 1], acc);
             __builtin_amdgcn_sched_barrier(0);
-            if (wide) rows_to_memory<C>(out + i * C * row + 64 * wave, row, ok, count(i), acc);
+            if (wide) rows_to_memory<C>(out + 64 * wave, row, ok, n, acc);
             else rows_to_tile<IO, kCols, C>(V, 16 * wave, acc);
         }
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C>(B, vf, f, S);
-        if ((i & 3) == 0) factors(i + 4, g);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
-        if (OUT && !wide) mo.take(V, tid);
-        if (more) put(i + 1);
-        if (OUT && !wide) mo.write(out + i * C * row, row, count(i), 0, vpieces, tid);
+        if (OUT && !wide) mo.take(V, pv, tid);
+        if (ahead) put(ahead, &unbounded[(i + 1) & 1]);
+        if (OUT && !wide) mo.write(out, omine, row, MoveV::left(tid, n, vpieces), tid);
+        out += C * row;
         __syncthreads();
     }
     if (OUT) {
@@ -239,9 +259,8 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<DA, W>)) void decay_walk_kernel
             }
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) d += __shfl_xor(d, m);
-            if (lane < 8 / W)
-                p.ends[(s.seq * (long long)p.Hv + h) * 8 * p.slices + 8 * slice + wave + W * lane] =
-                    lane ? 0 : d;
+            if (lane == 0)
+                p.ends[((s.seq * (long long)p.Hv + h) * p.slices + slice) * W + wave] = d;
         }
     } else {
         S.store(p.seg + (seg * (long long)p.Hv + h) * size + at_col, p.rs, ok, p.rows);
@@ -267,21 +286,11 @@ hipError_t decay_walk_launch(const DecayWalk& p, hipStream_t s) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)xcd_blocks(units)), dim3(64 * W), bytes, s, w);
     return hipGetLastError();
 }
-template <int IO, int DA, int MODE>
-hipError_t decay_walk_cols(const DecayWalk& p, hipStream_t s) {
-    constexpr int C = IO == IO_F32 || DA > 128 ? 32 : 64;
-    // the chunks of the gradients' other walk, which has wide rows then
-    if constexpr (MODE == kQueries && C == 64)
-        if (p.cols > 128) return decay_walk_launch<IO, DA, 32, 8, MODE>(p, s);
-    // four waves where eight would have nothing to do
-    return p.cols <= 64 ? decay_walk_launch<IO, DA, C, 4, MODE>(p, s)
-                        : decay_walk_launch<IO, DA, C, 8, MODE>(p, s);
-}
 template <int IO, int MODE>
 hipError_t decay_walk_io(const DecayWalk& p, hipStream_t s) {
-    return p.rows <= 64    ? decay_walk_cols<IO, 64, MODE>(p, s)
-           : p.rows <= 128 ? decay_walk_cols<IO, 128, MODE>(p, s)
-                           : decay_walk_cols<IO, 256, MODE>(p, s);
+    return p.rows <= 64    ? decay_walk_launch<IO, 64, kDecayChunk, 4, MODE>(p, s)
+           : p.rows <= 128 ? decay_walk_launch<IO, 128, kDecayChunk, 4, MODE>(p, s)
+                           : decay_walk_launch<IO, 256, kDecayChunk, 4, MODE>(p, s);
 }
 
 }  // namespace fftconv
