@@ -129,16 +129,29 @@ __global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, l
     }
     dfloat4 S = {0, 0, 0, 0};
     if (init) S = *(const dfloat4*)(init + (seq * Hv + h) * size + 4 * e);
-    for (long long j = 0; j < n; ++j) {
-        const long long i = (first + (back ? n - 1 - j : j)) * Hv + h;
-        dfloat4* x = (dfloat4*)(seg + i * size + 4 * e);
-        const bool last = j + 1 == n;
-        const dfloat4 effect = *x;
-        *x = S;
-        if (!last) {
-            const float a = exact_exp2(seg_g[i]);
+    // eight segments' effects on their way at once
+    constexpr int kAhead = 8;
+    for (long long j0 = 0; j0 < n; j0 += kAhead) {
+        dfloat4 effect[kAhead];
+        double g[kAhead];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[r] = a * S[r] + effect[r];
+        for (int j = 0; j < kAhead; ++j) {
+            // (the last one's is not made, and not used)
+            const long long at = j0 + j < n ? j0 + j : n - 1;
+            const long long i = (first + (back ? n - 1 - at : at)) * Hv + h;
+            effect[j] = *(const dfloat4*)(seg + i * size + 4 * e);
+            g[j] = seg_g[i];
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (j0 + j >= n) break;
+            const long long i = (first + (back ? n - 1 - j0 - j : j0 + j)) * Hv + h;
+            *(dfloat4*)(seg + i * size + 4 * e) = S;
+            if (j0 + j + 1 < n) {
+                const float a = exact_exp2(g[j]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[r] = fmaf(a, S[r], effect[j][r]);
+            }
         }
     }
 }

@@ -39,13 +39,13 @@ struct Back {
 // Scores of dk (rows of v against do) as make_scores() makes them, and the sums over
 // rectangles of W: sums[unit][t] for the sixteen s and the u of the unit.
 template <int IO, int DA, int C, int NW>
-__device__ __forceinline__ void make_scores_and_sums(const char* V, const char* DO, const char* K,
+__device__ __forceinline__ void make_scores_and_sums(const RowReader<IO, DA>& rows, int lane,
+                                                     const char* V, const char* DO, const char* K,
                                                      const char* Q, char* P, float* back,
                                                      const Factors<C>& F, float scale, int wave,
                                                      float (*sums)[C]) {
     typedef Scores<IO, C> L;
-    const int lane = fresh_lane(), g = lane >> 4, c = lane & 15;
-    const RowReader<IO, DA> rows(lane);
+    const int g = lane >> 4, c = lane & 15;
 #pragma unroll
     for (int j = 0; j < (L::kUnits + NW - 1) / NW; ++j) {
         const int unit = wave + NW * j, qt = unit % L::M, part = unit / L::M, k0 = part * L::kTiles;
@@ -236,9 +236,11 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
         __syncthreads();
     }
     const int tile = mine < DA ? wave + first / 16 : 0;        // columns that are in the tiles
+    Places<IO, DA, DA> places(lane, 16 * tile);
     for (int i = 0; i < chunks; ++i) {
         const Factors<C>& fac = F[i & 7];
         const int at = start(i), n = count(i);
+        places.fresh();
         const bool more = i + 1 < chunks;
         if ((i & 3) == 0) {
             factors(i + 4, g);
@@ -262,15 +264,18 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
         if (more) fetch(C);
         dfloat4 acc[C / 16];
         if (keys) {
-            make_scores_and_sums<IO, DA, C, RW>(V, DO, K, Q, P, back[1], fac, f.scale, wave, sums);
+            make_scores_and_sums<IO, DA, C, RW>(places.rows, places.lane, V, DO, K, Q, P, back[1], fac,
+                                                f.scale, wave, sums);
             __builtin_amdgcn_sched_barrier(0);
-            state_product<IO, DA, C, IO == IO_BF16 ? 2 : Kind<IO>::NS>(V, X, fac, acc);
+            state_product<IO, DA, C, IO == IO_BF16 ? 2 : Kind<IO>::NS>(places.rows, places.lane, V, X,
+                                                                       fac, acc);
         } else {
-            make_scores<IO, DA, C, RW, true>(K, Q, P, back[0], fac, f.scale, wave);
+            make_scores<IO, DA, C, RW, true>(places.rows, places.lane, K, Q, P, back[0], fac, f.scale,
+                                             wave);
             __builtin_amdgcn_sched_barrier(0);
-            state_product<IO, DA, C, Kind<IO>::NS>(K, X, fac, acc);
+            state_product<IO, DA, C, Kind<IO>::NS>(places.rows, places.lane, K, X, fac, acc);
             __builtin_amdgcn_sched_barrier(0);
-            row_dots<IO, DA, C>(V, 16 * tile, acc, dots[wave]);
+            row_dots<IO, DA, C>(places.cells, places.lane, V, acc, dots[wave]);
         }
         __syncthreads();
         if (place == RW - 1 && nv > 0) {
@@ -299,17 +304,15 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
                             f.Hv + h] = fac.all * x;
         }
         Frag<IO> val[C / 32];
-        const ColReader<IO, DA, false> vcols(fresh_lane());
 #pragma unroll
-        for (int j = 0; j < C / 32; ++j)
-            val[j] = vcols.get(keys ? Q : DO, 32 * j, tile);
-        scores_product<IO, C, true>(P, back[keys], val, unbounded[i & 1], acc);
+        for (int j = 0; j < C / 32; ++j) val[j] = places.values.get(keys ? Q : DO, 32 * j, tile);
+        scores_product<IO, C, true>(P, back[keys], places.lane, val, unbounded[i & 1], acc);
         __builtin_amdgcn_sched_barrier(0);
         // K's and V's tiles are done with
-        if (keys && wide) rows_to_memory<C>(dk + at * krow + 64 * wave, krow, ok, n, acc);
-        else if (mine < DA) rows_to_tile<IO, DA, C>(keys ? V : K, mine, acc);
+        if (keys && wide) rows_to_memory<C>(places.lane, dk + at * krow + 64 * wave, krow, ok, n, acc);
+        else if (mine < DA) rows_to_tile<IO, DA, C>(places.cells, keys ? V : K, acc);
         __builtin_amdgcn_sched_barrier(0);
-        update_state<IO, DA, C>(keys ? DO : Q, val, fac, X);
+        update_state<IO, DA, C>(places.elements, places.lane, keys ? DO : Q, val, fac, X);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
         Move rows_k, rows_v;

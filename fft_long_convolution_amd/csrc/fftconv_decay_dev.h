@@ -112,13 +112,9 @@ struct Rows {
         return token * kRow + ((u ^ swirl<kPieces>(token)) << 4);
     }
 };
-// The lane, unknown to the compiler: what follows from it is made where it is
-// used instead of being kept in registers over the whole walk.
-__device__ __forceinline__ int fresh_lane() {
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    return lane;
-}
+// x, unknown to the compiler from here on: what follows from a lane's base is made
+// where it is used instead of being kept in registers over the whole walk.
+__device__ __forceinline__ void forget(uint32_t& x) { asm volatile("" : "+v"(x)); }
 
 // Eight consecutive elements or k, as an operand.
 template <int IO>
@@ -135,11 +131,6 @@ __device__ __forceinline__ void unpack_frag(const Frag<IO>& f, float (&x)[8]) {
         unpack8<IO>(&f.v, x);
     }
 }
-__device__ __forceinline__ int fresh(int x) {
-    asm volatile("" : "+v"(x));
-    return x;
-}
-
 // Rows as operands with k along the elements: lane (g, c) has token t0 + c at
 // elements e0 + 8g + i, i < 8; t0 a multiple of 16, e0 of 32.
 template <int IO, int D>
@@ -204,6 +195,40 @@ struct ColReader {
             f.v = du4{r[0].x, r[0].y, r[1].x, r[1].y};
         }
         return f;
+    }
+};
+
+// Single elements of a tile in accumulator order: lane (g, c) has token t0 + 4g + r, r < 4,
+// at column first + c; t0 a multiple of 16.
+template <int IO, int D>
+struct CellPlaces {
+    typedef Rows<IO, D> R;
+    uint32_t base;
+    __device__ __forceinline__ CellPlaces(int lane, int first) {
+        constexpr int kPer = 16 / R::kB;
+        const int e = first + (lane & 15);
+        base = R::at(4 * (lane >> 4), e / kPer) + e % kPer * R::kB;
+    }
+    __device__ __forceinline__ uint32_t at(int t0, int r) const {
+        return (t0 + r) * R::kRow + (base ^ (swirl<R::kPieces>(r) << 4));
+    }
+};
+// The bases of a lane.  Columns of the values are `first` and so on in tiles of DV.
+template <int IO, int DA, int DV>
+struct Places {
+    RowReader<IO, DA> rows;
+    ColReader<IO, DA, true> elements;
+    ColReader<IO, DV, false> values;
+    CellPlaces<IO, DV> cells;
+    uint32_t lane;
+    __device__ __forceinline__ Places(int lane, int first)
+        : rows(lane), elements(lane), values(lane), cells(lane, first), lane(lane) {}
+    __device__ __forceinline__ void fresh() {
+        forget(rows.base);
+        forget(elements.base);
+        forget(values.base);
+        forget(cells.base);
+        forget(lane);
     }
 };
 
@@ -477,11 +502,11 @@ __device__ __forceinline__ void decays_between(const Factors<C>& F, int s0, int 
         gam[e] = REV ? exp2_of(w[e] - whole, r[e] - rest) : exp2_of(whole - w[e], rest - r[e]);
 }
 template <int IO, int DA, int C, int NW, bool REV>
-__device__ __forceinline__ void make_scores(const char* A, const char* B, char* P, float* back,
+__device__ __forceinline__ void make_scores(const RowReader<IO, DA>& rows, int lane, const char* A,
+                                            const char* B, char* P, float* back,
                                             const Factors<C>& F, float scale, int wave) {
     typedef Scores<IO, C> L;
-    const int lane = fresh_lane(), g = lane >> 4, c = lane & 15;
-    const RowReader<IO, DA> rows(lane);
+    const int g = lane >> 4, c = lane & 15;
 #pragma unroll
     for (int j = 0; j < (L::kUnits + NW - 1) / NW; ++j) {
         const int unit = wave + NW * j, qt = unit % L::M, part = unit / L::M, k0 = part * L::kTiles;
@@ -569,14 +594,14 @@ struct State {
     }
     // as it is, `tiles` of its tiles
     __device__ __forceinline__ void store_tiles(float* to, int tiles) const {
-        dfloat4* d = (dfloat4*)to + fresh_lane();
+        dfloat4* d = (dfloat4*)to + (threadIdx.x & 63);
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (i < tiles) d[64 * i] = t[i];
     }
     // sum of the products with tiles so stored, of the lane
     __device__ __forceinline__ float times_tiles(const float* from, int tiles) const {
-        const dfloat4* d = (const dfloat4*)from + fresh_lane();
+        const dfloat4* d = (const dfloat4*)from + (threadIdx.x & 63);
         float a = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -597,11 +622,11 @@ __device__ __forceinline__ long long anchor_of(const DecaySpans& p, const DecayS
 
 // acc[m] = f o (rows A times S) for the row tiles m
 template <int IO, int DA, int C, int NS>
-__device__ __forceinline__ void state_product(const char* A, const State<DA>& S, const Factors<C>& F,
+__device__ __forceinline__ void state_product(const RowReader<IO, DA>& rows, int lane, const char* A,
+                                              const State<DA>& S, const Factors<C>& F,
                                               dfloat4 (&acc)[C / 16]) {
     constexpr int M = C / 16;
-    const int lane = fresh_lane(), g = lane >> 4;
-    const RowReader<IO, DA> rows(lane);
+    const int g = lane >> 4;
     float back = 1.f, to = 1.f;
     if constexpr (IO == IO_F16) {
         const Scale sc = scale_to(S.largest());
@@ -632,7 +657,6 @@ __device__ __forceinline__ void state_product(const char* A, const State<DA>& S,
         }
         __builtin_amdgcn_sched_barrier(0);
     }
-    products_done();
 #pragma unroll
     for (int m = 0; m < M; ++m) {
         const float4 f = *(const float4*)&F.f[16 * m + 4 * g];
@@ -669,12 +693,12 @@ __device__ __forceinline__ Frag<IO> bounded(const Frag<IO>& v, int t, int& bad) 
 // of V's values is infinite or NaN.  Those are left out, as they would meet the
 // zeros of P, and the column's rows that see one become NaN.
 template <int IO, int C, bool REV>
-__device__ __forceinline__ void scores_product(const char* P, const float* back,
+__device__ __forceinline__ void scores_product(const char* P, const float* back, int lane,
                                                const Frag<IO> (&values)[C / 32], bool unbounded,
                                                dfloat4 (&acc)[C / 16]) {
     typedef Scores<IO, C> L;
     constexpr int NP = Kind<IO>::NP;
-    const int lane = fresh_lane(), g = lane >> 4;
+    const int g = lane >> 4;
     int bad = REV ? -1 : C;
 #pragma unroll
     for (int kb = 0; kb < L::KB; ++kb) {
@@ -727,11 +751,11 @@ __device__ __forceinline__ void weighted(const Frag<IO>& v, const Factors<C>& F,
 // S <- e^Dc S + B^T (w o V).  The chunk's part is summed by itself: one rounding of the
 // state a chunk.
 template <int IO, int DA, int C>
-__device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&values)[C / 32],
+__device__ __forceinline__ void update_state(const ColReader<IO, DA, true>& cols, int lane,
+                                             const char* B, const Frag<IO> (&values)[C / 32],
                                              const Factors<C>& F, State<DA>& S) {
-    constexpr int NS = Kind<IO>::NS, KB = C / 32, G = 2;
-    const int lane = fresh_lane(), g = lane >> 4;
-    const ColReader<IO, DA, true> cols(lane);
+    constexpr int NS = Kind<IO>::NS, KB = C / 32, G = 4;
+    const int g = lane >> 4;
     const float all = F.all;
     float to = 1.f, back = 1.f;
     if constexpr (IO == IO_F16) {
@@ -770,7 +794,6 @@ __device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&val
 #pragma unroll
                 for (int j = 0; j < G; ++j) part[j] = mma16<IO>(a[j], v[kb][n], part[j]);
         }
-        products_done();
 #pragma unroll
         for (int j = 0; j < G; ++j)
 #pragma unroll
@@ -781,26 +804,21 @@ __device__ __forceinline__ void update_state(const char* B, const Frag<IO> (&val
     }
 }
 
-// The wave's 16 columns of the rows to a tile's columns first ..., in the I/O type, for
+// The wave's 16 columns of the rows to their places in a tile, in the I/O type, for
 // threads that then take whole pieces of it.
 template <int IO, int D, int C>
-__device__ __forceinline__ void rows_to_tile(char* tile, int first, const dfloat4 (&acc)[C / 16]) {
-    typedef Rows<IO, D> R;
-    constexpr int kPer = 16 / R::kB;
-    const int lane = fresh_lane(), e = first + (lane & 15);
-    const uint32_t base = R::at(4 * (lane >> 4), e / kPer) + e % kPer * R::kB;
+__device__ __forceinline__ void rows_to_tile(const CellPlaces<IO, D>& cells, char* tile,
+                                             const dfloat4 (&acc)[C / 16]) {
 #pragma unroll
     for (int m = 0; m < C / 16; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            io_store<IO>(tile + (16 * m + r) * R::kRow + (base ^ (swirl<R::kPieces>(r) << 4)), 0,
-                         acc[m][r]);
+        for (int r = 0; r < 4; ++r) io_store<IO>(tile + cells.at(16 * m, r), 0, acc[m][r]);
 }
 // The rows below n to fp32 memory, `row` bytes apart.
 template <int C>
-__device__ __forceinline__ void rows_to_memory(char* out, long long row, bool ok, int n,
+__device__ __forceinline__ void rows_to_memory(int lane, char* out, long long row, bool ok, int n,
                                                const dfloat4 (&acc)[C / 16]) {
-    const int lane = fresh_lane(), left = ok ? n - 4 * (lane >> 4) : 0;
+    const int left = ok ? n - 4 * (lane >> 4) : 0;
     const uint32_t mine = (uint32_t)(4 * (lane >> 4)) * (uint32_t)row + 4u * (lane & 15);
 #pragma unroll
     for (int m = 0; m < C / 16; ++m)
@@ -819,23 +837,17 @@ __device__ __forceinline__ float sums16_of4(const float (&t)[4]) {
     x += moved<0xb1>(x);
     return x + moved<0x4e>(x);
 }
-// dots[t] = sum over the wave's 16 columns of acc and the rows X at column first
+// dots[t] = sum over the wave's 16 columns of acc and the rows X there
 template <int IO, int D, int C>
-__device__ __forceinline__ void row_dots(const char* X, int first, const dfloat4 (&acc)[C / 16],
-                                         float* dots) {
-    typedef Rows<IO, D> R;
-    constexpr int kPer = 16 / R::kB;
-    const int lane = fresh_lane(), g = lane >> 4, e = first + (lane & 15);
-    const uint32_t base = R::at(4 * g, e / kPer) + e % kPer * R::kB;
+__device__ __forceinline__ void row_dots(const CellPlaces<IO, D>& cells, int lane, const char* X,
+                                         const dfloat4 (&acc)[C / 16], float* dots) {
 #pragma unroll
     for (int m = 0; m < C / 16; ++m) {
         float x[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            x[r] = acc[m][r] * io_load<IO>(X + (16 * m + r) * R::kRow +
-                                               (base ^ (swirl<R::kPieces>(r) << 4)), 0);
+        for (int r = 0; r < 4; ++r) x[r] = acc[m][r] * io_load<IO>(X + cells.at(16 * m, r), 0);
         const float d = sums16_of4(x);
-        if ((lane & 3) == 0) dots[16 * m + 4 * g + ((lane & 15) >> 2)] = d;
+        if ((lane & 3) == 0) dots[16 * m + 4 * (lane >> 4) + ((lane & 15) >> 2)] = d;
     }
 }
 

@@ -53,7 +53,7 @@ struct WalkLds {
 
 // Waves of a SIMD that the walk leaves registers for.
 template <int IO, int DA, int MODE>
-constexpr int kWalkWaves = DA > 128 ? 2 : IO == IO_F32 && DA > 64 ? 3 : 4;
+constexpr int kWalkWaves = DA > 128 ? 2 : DA > 64 ? 3 : 4;
 
 // A workgroup takes 16 W columns of a segment of one head.  A chunk goes in two
 // halves: scores and the state's product (with A and B), then what has V in it; the
@@ -168,6 +168,7 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk
     char* out = (char*)p.out + (s.b * p.sp.T + s.t0 + s.from) * row +
                 (long long)(h * p.cols + first) * ob;
     const uint32_t omine = tid / MoveV::kPieces * (uint32_t)row + 16u * (tid % MoveV::kPieces);
+    Places<IO, DA, kCols> at(lane, 16 * wave);
     float g = 0.f;
     if (chunks) {
         fetch(count(0));
@@ -181,6 +182,7 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk
     for (int i = 0; i < chunks; ++i) {
         const Factors<C>& f = F[i & 7];
         const int n = count(i), ahead = count(i + 1);
+        at.fresh();
         if ((i & 3) == 0) {
             factors(i + 4, g);
             g = log_decays(i + 8);
@@ -199,11 +201,12 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk
         if (ahead) fetch(ahead);
         dfloat4 acc[C / 16];
         if (OUT) {
-            make_scores<IO, DA, C, W, false>(A, B, P, back, f, p.ss, wave);
+            make_scores<IO, DA, C, W, false>(at.rows, at.lane, A, B, P, back, f, p.ss, wave);
             __builtin_amdgcn_sched_barrier(0);
-            state_product<IO, DA, C, IO == IO_BF16 && !DOT ? 2 : Kind<IO>::NS>(A, S, f, acc);
+            state_product<IO, DA, C, IO == IO_BF16 && !DOT ? 2 : Kind<IO>::NS>(at.rows, at.lane, A, S,
+                                                                              f, acc);
             __builtin_amdgcn_sched_barrier(0);
-            if (DOT) row_dots<IO, kCols, C>(lds + L::kAtX, 16 * wave, acc, dots[wave]);
+            if (DOT) row_dots<IO, kCols, C>(at.cells, at.lane, lds + L::kAtX, acc, dots[wave]);
             __syncthreads();
         }
         if (DOT && wave == W - 1) {
@@ -223,17 +226,16 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk
                          i * C + t] = (float)d;
         }
         Frag<IO> vf[C / 32];
-        const ColReader<IO, kCols, false> vcols(fresh_lane());
 #pragma unroll
-        for (int kb = 0; kb < C / 32; ++kb) vf[kb] = vcols.get(V, 32 * kb, wave);
+        for (int kb = 0; kb < C / 32; ++kb) vf[kb] = at.values.get(V, 32 * kb, wave);
         if (OUT) {
-            scores_product<IO, C, false>(P, back, vf, unbounded[i & 1], acc);
+            scores_product<IO, C, false>(P, back, at.lane, vf, unbounded[i & 1], acc);
             __builtin_amdgcn_sched_barrier(0);
-            if (wide) rows_to_memory<C>(out + 64 * wave, row, ok, n, acc);
-            else rows_to_tile<IO, kCols, C>(V, 16 * wave, acc);
+            if (wide) rows_to_memory<C>(at.lane, out + 64 * wave, row, ok, n, acc);
+            else rows_to_tile<IO, kCols, C>(at.cells, V, acc);
         }
         __builtin_amdgcn_sched_barrier(0);
-        update_state<IO, DA, C>(B, vf, f, S);
+        update_state<IO, DA, C>(at.elements, at.lane, B, vf, f, S);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
         if (OUT && !wide) mo.take(V, pv, tid);
