@@ -109,10 +109,11 @@ struct DecayGradParams {
     double* before_all;
     double2* chunks;
     long long slots;
-    // every anchor_every chunks of a sequence from the first on: the state before the
+    // every 1 << anchor_shift chunks of a sequence from the first on: the state before the
     // chunk (as accumulators of its transpose, [anchors][Hv][16 columns of Dk][tiles
     // of Dv][lane]), and e^Dc times its product with the gradient of the chunk's last
-    int anchor_every;
+    int anchor_shift;
+    long long anchor_floats;         // of a head's anchor
     float* anchors;
     double* anchor_dg;               // [parts of the columns of Dk][anchors][Hv]
     long long anchor_count;
@@ -129,7 +130,7 @@ hipError_t launch_decay_bwd(int io, const DecayGradParams& p, hipStream_t s);
 // Chunks between anchors.  A decay for each token: every eighth, 8 KB of states
 // written and read for each chunk of a head of 128.  A fixed decay's dg sums what
 // all tokens of a chunk share, and its error with it: every second.
-inline int decay_anchor_every(bool fixed) { return fixed ? 2 : 8; }
+inline int decay_anchor_shift(bool fixed) { return fixed ? 1 : 3; }
 // Anchors in all; a packed sequence's start at cu / (so many chunks) + its number.
 inline size_t decay_anchors(size_t T, size_t nseq, bool packed, size_t n) {
     return packed ? T / n + nseq : nseq * ((T + n - 1) / n);

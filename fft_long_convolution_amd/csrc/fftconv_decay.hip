@@ -112,46 +112,41 @@ hipError_t fwd_io(const DecayParams& p, hipStream_t s) {
 // ------------------------------------------------------------------- segments
 
 // The segments' effects on the state become their first states: a thread takes
-// four elements of one sequence's state.  back: from the last segment to the first.
+// an element of one sequence's state.  back: from the last segment to the first.
 __global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, long long size,
                                                          const float* init, float* seg,
                                                          const double* seg_g, bool back) {
-    const long long per = (size / 4 + 255) / 256;
+    const long long per = (size + 255) / 256;
     const long long block = blockIdx.x / per, e = (blockIdx.x - block * per) * 256 + threadIdx.x;
     const unsigned h = (unsigned)(block % Hv);
     const long long seq = block / Hv;
-    if (4 * e >= size) return;
+    if (e >= size) return;
     long long first = seq * p.per, n = p.per;
     if (p.cu) {
         const long long a = bound_of(p, seq), z = bound_of(p, seq + 1);
         first = a / p.seg_tokens + seq;
         n = z > a ? (z - a + p.seg_tokens - 1) / p.seg_tokens : 1;
     }
-    dfloat4 S = {0, 0, 0, 0};
-    if (init) S = *(const dfloat4*)(init + (seq * Hv + h) * size + 4 * e);
-    // eight segments' effects on their way at once
-    constexpr int kAhead = 8;
+    float S = init ? init[(seq * Hv + h) * size + e] : 0.f;
+    // sixteen segments' effects on their way at once
+    constexpr int kAhead = 16;
     for (long long j0 = 0; j0 < n; j0 += kAhead) {
-        dfloat4 effect[kAhead];
+        float effect[kAhead];
         double g[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             // (the last one's is not made, and not used)
             const long long at = j0 + j < n ? j0 + j : n - 1;
             const long long i = (first + (back ? n - 1 - at : at)) * Hv + h;
-            effect[j] = *(const dfloat4*)(seg + i * size + 4 * e);
+            effect[j] = seg[i * size + e];
             g[j] = seg_g[i];
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             if (j0 + j >= n) break;
             const long long i = (first + (back ? n - 1 - j0 - j : j0 + j)) * Hv + h;
-            *(dfloat4*)(seg + i * size + 4 * e) = S;
-            if (j0 + j + 1 < n) {
-                const float a = exact_exp2(g[j]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[r] = fmaf(a, S[r], effect[j][r]);
-            }
+            seg[i * size + e] = S;
+            if (j0 + j + 1 < n) S = fmaf(exact_exp2(g[j]), S, effect[j]);
         }
     }
 }
@@ -159,7 +154,7 @@ __global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, l
 }  // namespace
 
 hipError_t launch_decay_join(const DecayParams& p, const float* init, bool back, hipStream_t s) {
-    const long long size = (long long)p.Dk * p.Dv, per = (size / 4 + 255) / 256;
+    const long long size = (long long)p.Dk * p.Dv, per = (size + 255) / 256;
     hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)(p.sp.nseq * p.Hv * per)), dim3(256), 0, s,
                        p.sp, p.Hv, size, init, p.seg, p.seg_g, back);
     return hipGetLastError();

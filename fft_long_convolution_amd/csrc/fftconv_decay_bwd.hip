@@ -121,7 +121,7 @@ __device__ __forceinline__ void make_scores_and_sums(const RowReader<IO, DA>& ro
 // chunks backward in time, with the gradient X of the state, columns of Dv in the
 // first role's waves (dv) and, transposed, columns of Dk in the second's (dk).
 template <int IO, int DA>
-__global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(DecayGradParams p,
+__global__ __launch_bounds__(512, (DA > 128 || (IO == IO_F32 && DA > 64) ? 2 : 4)) void decay_back_kernel(DecayGradParams p,
                                                                                int slices) {
     typedef Back<IO, DA> L;
     constexpr int C = L::C, RW = L::RW, N = 128 * RW, kB = Kind<IO>::kB, kCols = 16 * RW;
@@ -167,7 +167,6 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
     const int chunks = (s.to - s.from + C - 1) / C;
     const Tokens q = rows_of<IO>(f.q, s, h), k = rows_of<IO>(f.k, s, h), v = rows_of<IO>(f.v, s, h),
                  d = rows_of<IO>(p.d_o, s, h);
-    const long long anchor_floats = (long long)((f.Dk + 15) / 16) * ((f.Dv + 31) / 32) * 512;
     const int kp = f.Dk * kB / 16, vp = f.Dv * kB / 16;
     const float* gates = f.fixed ? f.g + h : f.g + (s.b * f.sp.T + s.t0) * f.Hv + h;
     const long long token0 = s.b * f.sp.T + s.t0;
@@ -219,12 +218,10 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
         if (mq.unbounded() || md.unbounded()) *bad = 1;
     };
     const int kb = wide ? 4 : kB, p0 = first * kB / 16;
-    const long long krow = (long long)f.Hv * f.Dk * kb, vrow = (long long)f.Hv * f.Dv * kB;
-    char* const dk = (char*)(wide ? (void*)p.dk_heads : p.dk) + token0 * krow +
-                     (long long)(h * f.Dk + first) * kb;
-    char* const dv = (char*)p.dv + token0 * vrow + (long long)(h * f.Dv + first) * kB;
-    // the thread's piece among the slice's columns
-    const int at_piece = tid % Move::kPieces - p0, t0 = tid / Move::kPieces;
+    const uint32_t krow = (uint32_t)(f.Hv * f.Dk * kb), vrow = (uint32_t)(f.Hv * f.Dv * kB);
+    char* dk = (char*)(wide ? (void*)p.dk_heads : p.dk) + (token0 + last) * krow +
+               (long long)(h * f.Dk + first) * kb;
+    char* dv = (char*)p.dv + (token0 + last) * vrow + (long long)(h * f.Dv + first) * kB;
     float g = 0.f;
     if (chunks) {
         fetch(count(0));
@@ -246,14 +243,14 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
             factors(i + 4, g);
             g = log_decays(i + 8);
         }
-        const bool anchor = at / C % p.anchor_every == 0;
+        const bool anchor = (at / C & ((1 << p.anchor_shift) - 1)) == 0;
         if (anchor && keys) {
             double x = 0;
             if (mine < f.Dk) {
                 const int tiles = 2 * ((f.Dv + 31) / 32);
                 x = X.times_tiles(p.anchors +
-                                      (anchor_of(f.sp, s, C, p.anchor_every, at / C) * f.Hv + h) *
-                                          anchor_floats +
+                                      (anchor_of(f.sp, s, C, p.anchor_shift, at / C) * f.Hv + h) *
+                                          p.anchor_floats +
                                       (long long)(mine / 16) * tiles * 256,
                                   tiles);
             }
@@ -300,7 +297,7 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
             double x = 0;
 #pragma unroll
             for (int w = 0; w < RW; ++w) x += products[w];
-            p.anchor_dg[(slice * p.anchor_count + anchor_of(f.sp, s, C, p.anchor_every, at / C)) *
+            p.anchor_dg[(slice * p.anchor_count + anchor_of(f.sp, s, C, p.anchor_shift, at / C)) *
                             f.Hv + h] = fac.all * x;
         }
         Frag<IO> val[C / 32];
@@ -309,22 +306,24 @@ __global__ __launch_bounds__(512, (DA <= 128 ? 4 : 2)) void decay_back_kernel(De
         scores_product<IO, C, true>(P, back[keys], places.lane, val, unbounded[i & 1], acc);
         __builtin_amdgcn_sched_barrier(0);
         // K's and V's tiles are done with
-        if (keys && wide) rows_to_memory<C>(places.lane, dk + at * krow + 64 * wave, krow, ok, n, acc);
+        if (keys && wide) rows_to_memory<C>(places.lane, dk + 64 * wave, krow, ok, n, acc);
         else if (mine < DA) rows_to_tile<IO, DA, C>(places.cells, keys ? V : K, acc);
         __builtin_amdgcn_sched_barrier(0);
-        update_state<IO, DA, C>(places.elements, places.lane, keys ? DO : Q, val, fac, X);
+        update_state<IO, DA, C, 2>(places.elements, places.lane, keys ? DO : Q, val, fac, X);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
         Move rows_k, rows_v;
         rows_v.take(K, piece, tid);
         rows_k.take(V, piece, tid);
         if (more) put(C, &unbounded[(i + 1) & 1]);
-        const int here = at_piece >= 0 ? n - t0 : 0;
-        rows_v.write(dv + at * vrow, (uint32_t)(t0 * vrow) + 16u * at_piece, vrow,
-                     at_piece < nv * kB / 16 ? here : 0, tid);
-        if (!wide)
-            rows_k.write(dk + at * krow, (uint32_t)(t0 * krow) + 16u * at_piece, krow,
-                         at_piece < nk * kB / 16 ? here : 0, tid);
+        // the thread's piece among the slice's columns
+        const int id = fresh_thread(), at_piece = id % Move::kPieces - p0, t0 = id / Move::kPieces;
+        const bool mine_k = at_piece >= 0 && at_piece < nk * kB / 16,
+                   mine_v = at_piece >= 0 && at_piece < nv * kB / 16;
+        rows_v.write(dv, (uint32_t)t0 * vrow + 16u * at_piece, vrow, mine_v ? n - t0 : 0, tid);
+        if (!wide) rows_k.write(dk, (uint32_t)t0 * krow + 16u * at_piece, krow, mine_k ? n - t0 : 0, tid);
+        dk -= C * (long long)krow;
+        dv -= C * (long long)vrow;
         __syncthreads();
     }
     if (!keys && s.index == 0 && p.dinit)
@@ -355,9 +354,9 @@ __global__ __launch_bounds__(256) void decay_dg_kernel(DecayGradParams p, DecayS
                 double b = 0;
                 int keep = 1, chain = 1;        // chain: by way of the next chunk
                 if (c < nc) {
-                    if (c % p.anchor_every == 0) {
+                    if ((c & ((1 << p.anchor_shift) - 1)) == 0) {
                         chain = 0;
-                        const long long a = anchor_of(sp, s, C, p.anchor_every, c);
+                        const long long a = anchor_of(sp, s, C, p.anchor_shift, c);
                         for (int i = 0; i < ks; ++i)
                             b += p.anchor_dg[(i * p.anchor_count + a) * f.Hv + h];
                     } else {
@@ -449,7 +448,7 @@ hipError_t back_launch(const DecayGradParams& p, hipStream_t s) {
                                              hipFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (e != hipSuccess) return e;
     const int widest = p.f.Dk > p.f.Dv ? p.f.Dk : p.f.Dv;
-    const int slices = (widest + 16 * L::RW - 1) / (16 * L::RW);
+    const int slices = (widest + kDecayCols - 1) / kDecayCols;
     hipLaunchKernelGGL(kernel, dim3((unsigned)xcd_blocks(p.f.sp.segs * p.f.Hv * slices)),
                        dim3(128 * L::RW), L::kBytes, s, p, slices);
     return hipGetLastError();
@@ -505,9 +504,9 @@ hipError_t bwd_io(const DecayGradParams& p, hipStream_t s) {
     w.before = p.before;
     w.before_all = p.before_all;
     w.slots = p.slots;
-    w.anchor_every = p.anchor_every;
+    w.anchor_shift = p.anchor_shift;
     w.anchors = p.anchors;
-    w.anchor_floats = (long long)decay_anchor_floats(f.Dk, f.Dv);
+    w.anchor_floats = p.anchor_floats;
     w.dfin = p.dfin;
     w.ends = p.ends;
     const int widest = f.Dk > f.Dv ? f.Dk : f.Dv;

@@ -115,6 +115,11 @@ struct Rows {
 // x, unknown to the compiler from here on: what follows from a lane's base is made
 // where it is used instead of being kept in registers over the whole walk.
 __device__ __forceinline__ void forget(uint32_t& x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ int fresh_thread() {
+    uint32_t x = threadIdx.x;
+    forget(x);
+    return (int)x;
+}
 
 // Eight consecutive elements or k, as an operand.
 template <int IO>
@@ -220,7 +225,7 @@ struct Places {
     ColReader<IO, DA, true> elements;
     ColReader<IO, DV, false> values;
     CellPlaces<IO, DV> cells;
-    uint32_t lane;
+    int lane;
     __device__ __forceinline__ Places(int lane, int first)
         : rows(lane), elements(lane), values(lane), cells(lane, first), lane(lane) {}
     __device__ __forceinline__ void fresh() {
@@ -228,7 +233,7 @@ struct Places {
         forget(elements.base);
         forget(values.base);
         forget(cells.base);
-        forget(lane);
+        lane = fresh_thread() & 63;
     }
 };
 
@@ -285,12 +290,12 @@ struct Moving {
         for (int j = 0; j < kMine; ++j) r[j] = *(const du4*)(m + (idle(tid) ? 0 : next(place, j)));
     }
     // to rows `row` bytes apart, the thread's first piece at mine
-    __device__ __forceinline__ void write(char* out, uint32_t mine, long long row, int left,
+    __device__ __forceinline__ void write(char* out, uint32_t mine, uint32_t row, int left,
                                           int tid) const {
         if (idle(tid)) return;
 #pragma unroll
         for (int j = 0; j < kMine; ++j)
-            if (j * kStep < left) *(du4*)(out + j * kStep * row + mine) = r[j];
+            if (j * kStep < left) *(du4*)(out + (j * kStep * row + mine)) = r[j];
     }
     // whether an element is infinite or NaN
     __device__ __forceinline__ bool unbounded() const {
@@ -613,11 +618,11 @@ struct State {
         return a;
     }
 };
-// The anchor before a sequence's chunk number `chunk` (a multiple of `every`), of C tokens
+// The anchor before a sequence's chunk number `chunk` of C tokens (a multiple of 1 << shift)
 __device__ __forceinline__ long long anchor_of(const DecaySpans& p, const DecaySpan& s, int C,
-                                               int every, int chunk) {
-    const int n = every * C;
-    return (p.cu ? s.t0 / n + s.seq : s.b * ((p.T + n - 1) / n)) + chunk / every;
+                                               int shift, int chunk) {
+    const long long n = (long long)C << shift;
+    return (p.cu ? s.t0 / n + s.seq : s.b * ((p.T + n - 1) / n)) + (chunk >> shift);
 }
 
 // acc[m] = f o (rows A times S) for the row tiles m
@@ -749,12 +754,12 @@ __device__ __forceinline__ void weighted(const Frag<IO>& v, const Factors<C>& F,
     x[4] *= b.x; x[5] *= b.y; x[6] *= b.z; x[7] *= b.w;
 }
 // S <- e^Dc S + B^T (w o V).  The chunk's part is summed by itself: one rounding of the
-// state a chunk.
-template <int IO, int DA, int C>
+// state a chunk.  G: tiles at a time.
+template <int IO, int DA, int C, int G>
 __device__ __forceinline__ void update_state(const ColReader<IO, DA, true>& cols, int lane,
                                              const char* B, const Frag<IO> (&values)[C / 32],
                                              const Factors<C>& F, State<DA>& S) {
-    constexpr int NS = Kind<IO>::NS, KB = C / 32, G = 4;
+    constexpr int NS = Kind<IO>::NS, KB = C / 32;
     const int g = lane >> 4;
     const float all = F.all;
     float to = 1.f, back = 1.f;
@@ -816,15 +821,15 @@ __device__ __forceinline__ void rows_to_tile(const CellPlaces<IO, D>& cells, cha
 }
 // The rows below n to fp32 memory, `row` bytes apart.
 template <int C>
-__device__ __forceinline__ void rows_to_memory(int lane, char* out, long long row, bool ok, int n,
+__device__ __forceinline__ void rows_to_memory(int lane, char* out, uint32_t row, bool ok, int n,
                                                const dfloat4 (&acc)[C / 16]) {
     const int left = ok ? n - 4 * (lane >> 4) : 0;
-    const uint32_t mine = (uint32_t)(4 * (lane >> 4)) * (uint32_t)row + 4u * (lane & 15);
+    const uint32_t mine = (uint32_t)(4 * (lane >> 4)) * row + 4u * (lane & 15);
 #pragma unroll
     for (int m = 0; m < C / 16; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            if (16 * m + r < left) *(float*)(out + (16 * m + r) * row + mine) = acc[m][r];
+            if (16 * m + r < left) *(float*)(out + ((16 * m + r) * row + mine)) = acc[m][r];
 }
 
 // Sums over the 16 lanes of a group: lane c gets that of t[c / 4].

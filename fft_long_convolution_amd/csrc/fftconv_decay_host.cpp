@@ -76,7 +76,8 @@ size_t decay_segment(const fftconv_decay_desc* d) {
     const size_t whole = (blocks + 1) * kSegAlign;
     const size_t rows = d->sequences ? d->sequences : d->B;
     if (!rows || !blocks) return whole;
-    const double heads = (double)rows * d->Hv * ((d->Dv + kDecayCols - 1) / kDecayCols);
+    const double vs = (double)((d->Dv + kDecayCols - 1) / kDecayCols);
+    const double heads = (double)rows * d->Hv * vs;
     // us of a block of two chunks: alone on a CU, and what each further one adds
     const double wide = (d->dtype == FFTCONV_F32 ? 2.0 : 1.0) * (d->Dk > 128 ? 2.0 : d->Dk > 64 ? 1.0 : 0.7);
     const auto walk = [&](double units) {
@@ -93,7 +94,9 @@ size_t decay_segment(const fftconv_decay_desc* d) {
     for (size_t per = 1; per < blocks && per < longest; per = per < 16 ? per + 1 : per * 5 / 4) {
         const double n = longest / per, all = heads * (mean / per < 1 ? 1 : mean / per);
         if (n > 256) continue;
-        const double t = per * (walk(all) + effects(all)) + 10.0 + 0.6 * n;
+        // the join, and states made, joined and read at 5 bytes a ps
+        const double states = heads / vs * (mean / per) * d->Dk * d->Dv * 16 / 5e6;
+        const double t = per * (walk(all) + effects(all)) + 10.0 + 0.3 * n + states;
         if (t < best) {
             best = t;
             most = per * kSegAlign;
@@ -138,7 +141,7 @@ bool decay_layout(const fftconv_decay_desc* d, DecayLayout* l) {
     l->before_all = up16(ks * l->slots * d->Hv * 8);
     l->chunks = up16(vs * l->slots * d->Hv * 16);
     const size_t anchors = decay_anchors(d->T, rows, d->sequences != 0,
-                                         C * decay_anchor_every(d->fixed_decay != 0));
+                                         C << decay_anchor_shift(d->fixed_decay != 0));
     l->anchors = anchors * d->Hv * decay_anchor_floats((int)d->Dk, (int)d->Dv) * 4;
     l->anchor_dg = up16(ks * anchors * d->Hv * 8);
     l->anchor_count = anchors;
@@ -360,7 +363,8 @@ fftconv_status fftconv_decay_backward(const fftconv_decay_desc* d, const void* q
     p.before_all = (double*)take(l.before_all);
     p.chunks = (double2*)take(l.chunks);
     p.slots = (long long)l.slots;
-    p.anchor_every = decay_anchor_every(p.f.fixed);
+    p.anchor_shift = decay_anchor_shift(p.f.fixed);
+    p.anchor_floats = (long long)decay_anchor_floats(p.f.Dk, p.f.Dv);
     p.anchors = (float*)take(l.anchors);
     p.anchor_dg = (double*)take(l.anchor_dg);
     p.anchor_count = (long long)l.anchor_count;

@@ -33,7 +33,7 @@ struct DecayWalk {
     double* before_all;              // [slices][slots][Hv]
     long long slots;
     double* ends;                    // [nseq][Hv][slices][4]
-    int anchor_every;
+    int anchor_shift;
     float* anchors;
     long long anchor_floats;         // of a head's anchor
 };
@@ -53,7 +53,7 @@ struct WalkLds {
 
 // Waves of a SIMD that the walk leaves registers for.
 template <int IO, int DA, int MODE>
-constexpr int kWalkWaves = DA > 128 ? 2 : DA > 64 ? 3 : 4;
+constexpr int kWalkWaves = DA > 128 ? 2 : DA > 64 ? (IO == IO_F32 ? 2 : 3) : 4;
 
 // A workgroup takes 16 W columns of a segment of one head.  A chunk goes in two
 // halves: scores and the state's product (with A and B), then what has V in it; the
@@ -164,10 +164,10 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk
         if (OUT && mv.unbounded()) *bad = 1;
     };
     const int ob = wide ? 4 : kB;
-    const long long row = (long long)p.Hv * p.cols * ob;
+    const uint32_t row = (uint32_t)(p.Hv * p.cols * ob);
     char* out = (char*)p.out + (s.b * p.sp.T + s.t0 + s.from) * row +
                 (long long)(h * p.cols + first) * ob;
-    const uint32_t omine = tid / MoveV::kPieces * (uint32_t)row + 16u * (tid % MoveV::kPieces);
+    const uint32_t omine = tid / MoveV::kPieces * row + 16u * (tid % MoveV::kPieces);
     Places<IO, DA, kCols> at(lane, 16 * wave);
     float g = 0.f;
     if (chunks) {
@@ -189,10 +189,10 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk
         }
         if (DOT) {
             const int chunk = s.from / C + i;
-            if (chunk % p.anchor_every == 0 && first + 16 * wave < p.cols) {
+            if ((chunk & ((1 << p.anchor_shift) - 1)) == 0 && first + 16 * wave < p.cols) {
                 const int tiles = 2 * ((p.rows + 31) / 32);
                 S.store_tiles(p.anchors +
-                                  (anchor_of(p.sp, s, C, p.anchor_every, chunk) * p.Hv + h) *
+                                  (anchor_of(p.sp, s, C, p.anchor_shift, chunk) * p.Hv + h) *
                                       p.anchor_floats +
                                   (long long)(first / 16 + wave) * tiles * 256,
                               tiles);
@@ -235,13 +235,13 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk
             else rows_to_tile<IO, kCols, C>(at.cells, V, acc);
         }
         __builtin_amdgcn_sched_barrier(0);
-        update_state<IO, DA, C>(at.elements, at.lane, B, vf, f, S);
+        update_state<IO, DA, C, 4>(at.elements, at.lane, B, vf, f, S);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
         if (OUT && !wide) mo.take(V, pv, tid);
         if (ahead) put(ahead, &unbounded[(i + 1) & 1]);
         if (OUT && !wide) mo.write(out, omine, row, MoveV::left(tid, n, vpieces), tid);
-        out += C * row;
+        out += C * (long long)row;
         __syncthreads();
     }
     if (OUT) {
