@@ -9,6 +9,12 @@
 // type.  A row stays in registers between its sums: s is of differences
 // already taken, and m and r are not kept for the backward pass, which has the
 // row in hand anyway.
+//
+// Each element moves once in and once out (backward twice in) with some ten operations:
+// HBM bounds both passes.  64 x 1024 rows of 768 in bf16, 201 MB, take 35 us (5.8 TB/s;
+// a streaming copy reaches 5.9), 16 x 8192 of 768 in f16 forward and backward, 1.0 GB,
+// 193 us (5.2).  A lane of a row's group holds its pieces of eight elements from the load
+// to the store; the sums go by shuffles, of rows of more than 2048 through LDS.
 #include "fftconv_decay.h"
 #include "fftconv_delta_dev.h"
 
@@ -24,9 +30,17 @@ template <int LPR, bool WIDE>
 __device__ __forceinline__ int place(int v, int c) {
     return WIDE ? 8 * (v * LPR + c) : 8 * v * LPR + c;
 }
+// A piece as loaded.
+template <int IO, bool WIDE>
+struct Piece {
+    static constexpr int kWords = WIDE ? (IO == IO_F32 ? 2 : 1) : 8;
+    du4 wide[WIDE ? kWords : 1];
+    float each[WIDE ? 1 : 8];
+};
+// A piece that is used at once: what is not there is 0.
 template <int IO, int LPR, bool WIDE>
-__device__ __forceinline__ void load_piece(const void* p, long long at, int v, int c, int D,
-                                           bool have, float (&x)[8]) {
+__device__ __forceinline__ void load_now(const void* p, long long at, int v, int c, int D, bool have,
+                                         float (&x)[8]) {
     const int e = place<LPR, WIDE>(v, c);
     if constexpr (WIDE) {
         const bool ok = have && e < D;
@@ -47,14 +61,59 @@ __device__ __forceinline__ void load_piece(const void* p, long long at, int v, i
         }
     }
 }
+// One that stays in flight: what is not there reads the row's first elements, as it may
+// meet no branch's end, and is dropped by unpack_piece().
+template <int IO, int LPR, bool WIDE>
+__device__ __forceinline__ void load_piece(const void* p, long long at, int v, int c, int D,
+                                           Piece<IO, WIDE>& x) {
+    const int e = place<LPR, WIDE>(v, c);
+    if constexpr (WIDE) {
+        constexpr int kB = IO == IO_F32 ? 4 : 2;
+#pragma unroll
+        for (int j = 0; j < Piece<IO, WIDE>::kWords; ++j)
+            x.wide[j] = *(const du4*)((const char*)p + (at + (e < D ? e : 0)) * kB + 16 * j);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.each[i] = io_load<IO>(p, at + (e + i * LPR < D ? e + i * LPR : 0));
+    }
+}
+template <int IO, int LPR, bool WIDE>
+__device__ __forceinline__ void unpack_piece(const Piece<IO, WIDE>& p, int v, int c, int D, bool have,
+                                             float (&x)[8]) {
+    const int e = place<LPR, WIDE>(v, c);
+    if constexpr (WIDE) unpack8<IO>(p.wide, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool ok = have && (WIDE ? e : e + i * LPR) < D;
+        x[i] = ok ? (WIDE ? x[i] : p.each[i]) : 0.f;
+    }
+}
+// past: by the caches
 template <int IO, int LPR, bool WIDE>
 __device__ __forceinline__ void store_piece(void* p, long long at, int v, int c, int D,
-                                            const float (&x)[8]) {
+                                            const float (&x)[8], bool past = false) {
     const int e = place<LPR, WIDE>(v, c);
     if constexpr (WIDE) {
         if (e >= D) return;
-        store4<IO>(p, at + e, dfloat4{x[0], x[1], x[2], x[3]});
-        store4<IO>(p, at + e + 4, dfloat4{x[4], x[5], x[6], x[7]});
+        if constexpr (IO == IO_F32) {
+            store4<IO>(p, at + e, dfloat4{x[0], x[1], x[2], x[3]});
+            store4<IO>(p, at + e + 4, dfloat4{x[4], x[5], x[6], x[7]});
+        } else {
+            du4 u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (IO == IO_BF16) {
+                    const __bf16 h[2] = {(__bf16)x[2 * j], (__bf16)x[2 * j + 1]};
+                    u[j] = __builtin_bit_cast(uint32_t, h);
+                } else {
+                    const dh2 h = {(_Float16)x[2 * j], (_Float16)x[2 * j + 1]};
+                    u[j] = __builtin_bit_cast(uint32_t, h);
+                }
+            }
+            du4* const to = (du4*)((char*)p + (at + e) * 2);
+            if (past) __builtin_nontemporal_store(u, to);
+            else *to = u;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -130,7 +189,7 @@ __device__ __forceinline__ void load_weights(const float* w, int c, int D, float
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         if (w) {
-            load_piece<IO_F32, LPR, WIDE>(w, 0, v, c, D, true, x[v]);
+            load_now<IO_F32, LPR, WIDE>(w, 0, v, c, D, true, x[v]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[v][i] = other;
@@ -147,7 +206,7 @@ __global__ __launch_bounds__(kGroupThreads<LPR>) void layernorm_fwd_kernel(Layer
     float x[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        load_piece<IO, LPR, WIDE>(p.x, (have ? row : 0) * p.stride, v, c, p.D, have, x[v]);
+        load_now<IO, LPR, WIDE>(p.x, (have ? row : 0) * p.stride, v, c, p.D, have, x[v]);
     float w[V][8], b[V][8];
     load_weights<LPR, V, WIDE>(p.w, c, p.D, 1.f, w);
     load_weights<LPR, V, WIDE>(p.b, c, p.D, 0.f, b);
@@ -157,7 +216,7 @@ __global__ __launch_bounds__(kGroupThreads<LPR>) void layernorm_fwd_kernel(Layer
     for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[v][i] = x[v][i] * r * w[v][i] + b[v][i];
-        store_piece<IO, LPR, WIDE>(p.y, row * p.D, v, c, p.D, x[v]);
+        store_piece<IO, LPR, WIDE>(p.y, row * p.D, v, c, p.D, x[v], p.past);
     }
 }
 
@@ -173,16 +232,34 @@ __global__ __launch_bounds__(kGroupThreads<LPR>) void layernorm_bwd_kernel(Layer
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) gw[v][i] = gb[v][i] = 0.f;
-    for (long long row0 = (long long)blockIdx.x * kGroups; row0 < p.rows;
-         row0 += (long long)gridDim.x * kGroups) {
+    // the next row is on its way while this one is worked on, where that is few registers
+    constexpr bool kAhead = WIDE && IO != IO_F32;
+    Piece<IO, WIDE> rx[V], rd[V];
+    const long long step = (long long)gridDim.x * kGroups;
+    const auto fetch = [&](long long row) {
+        row = row < p.rows ? row : 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            load_piece<IO, LPR, WIDE>(p.x, row * p.stride, v, c, p.D, rx[v]);
+            load_piece<IO, LPR, WIDE>(p.dy, row * p.D, v, c, p.D, rd[v]);
+        }
+    };
+    if (kAhead && p.rows) fetch((long long)blockIdx.x * kGroups + group);
+    for (long long row0 = (long long)blockIdx.x * kGroups; row0 < p.rows; row0 += step) {
         const long long row = row0 + group;
         const bool have = row < p.rows;
         float x[V][8], d[V][8];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            load_piece<IO, LPR, WIDE>(p.x, (have ? row : 0) * p.stride, v, c, p.D, have, x[v]);
-            load_piece<IO, LPR, WIDE>(p.dy, (have ? row : 0) * p.D, v, c, p.D, have, d[v]);
+            if constexpr (kAhead) {
+                unpack_piece<IO, LPR, WIDE>(rx[v], v, c, p.D, have, x[v]);
+                unpack_piece<IO, LPR, WIDE>(rd[v], v, c, p.D, have, d[v]);
+            } else {
+                load_now<IO, LPR, WIDE>(p.x, (have ? row : 0) * p.stride, v, c, p.D, have, x[v]);
+                load_now<IO, LPR, WIDE>(p.dy, (have ? row : 0) * p.D, v, c, p.D, have, d[v]);
+            }
         }
+        if (kAhead) fetch(row + step);
         const float r = normal<LPR, V, WIDE>(p, c, x, lds);
         float h = 0.f, hn = 0.f;
 #pragma unroll
@@ -207,7 +284,7 @@ __global__ __launch_bounds__(kGroupThreads<LPR>) void layernorm_bwd_kernel(Layer
         for (int v = 0; v < V; ++v) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[v][i] = r * (d[v][i] - h - x[v][i] * hn);
-            store_piece<IO, LPR, WIDE>(p.dx, row * p.D, v, c, p.D, x[v]);
+            store_piece<IO, LPR, WIDE>(p.dx, row * p.D, v, c, p.D, x[v], p.past);
         }
     }
     if (!p.part) return;
@@ -267,9 +344,11 @@ __global__ __launch_bounds__(256) void layernorm_sum_kernel(LayerNormParams p) {
     if (d) d[i < p.D ? i : i - p.D] = a;
 }
 
-int lanes_of(int D) {
-    const int pieces = (D + 7) / 8;
-    return pieces <= 64 ? 16 : pieces <= 128 ? 32 : pieces <= 256 ? 64 : pieces <= 1024 ? 256 : 512;
+// Lanes of a row: up to four pieces a lane forward; backward, where a lane holds sums,
+// weights and two rows too, up to two as far as that goes.
+int lanes_of(int D, bool back) {
+    const int n = (D + 7) / 8 * (back ? 2 : 1);
+    return n <= 64 ? 16 : n <= 128 ? 32 : n <= 256 ? 64 : n <= 1024 ? 256 : 512;
 }
 
 template <int IO, int LPR, int V, bool WIDE>
@@ -294,7 +373,7 @@ hipError_t pieces(const LayerNormParams& p, bool back, hipStream_t s) {
 }
 template <int IO, bool WIDE>
 hipError_t lanes(const LayerNormParams& p, bool back, hipStream_t s) {
-    switch (lanes_of(p.D)) {
+    switch (lanes_of(p.D, back)) {
     case 16: return pieces<IO, 16, WIDE>(p, back, s);
     case 32: return pieces<IO, 32, WIDE>(p, back, s);
     case 64: return pieces<IO, 64, WIDE>(p, back, s);
@@ -302,7 +381,11 @@ hipError_t lanes(const LayerNormParams& p, bool back, hipStream_t s) {
     default: return pieces<IO, 512, WIDE>(p, back, s);
     }
 }
-hipError_t any(int io, const LayerNormParams& p, bool back, hipStream_t s) {
+// Outputs of 160 MB and more do not stay in the caches (256 MB in all) until they are
+// read again, and past them they leave the input there: 16 x 8192 rows of 768 in f16,
+// 201 MB each, forward and backward 193 us, through the caches 200.
+hipError_t any(int io, LayerNormParams p, bool back, hipStream_t s) {
+    p.past = p.rows * p.D * 2 >= (160ll << 20);
     switch (io) {
     case IO_F32: return p.wide ? lanes<IO_F32, true>(p, back, s) : lanes<IO_F32, false>(p, back, s);
     case IO_F16: return p.wide ? lanes<IO_F16, true>(p, back, s) : lanes<IO_F16, false>(p, back, s);
@@ -312,9 +395,10 @@ hipError_t any(int io, const LayerNormParams& p, bool back, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups of the backward pass: they keep their sums to the end.
+// Workgroups of the backward pass: they keep their sums to the end, so about as many as
+// run at once (three on each of the 256 CUs at three pieces a lane).
 int layernorm_bwd_blocks(long long rows, int D) {
-    const int lpr = lanes_of(D), groups = lpr > 256 ? 1 : 256 / lpr;
+    const int lpr = lanes_of(D, true), groups = lpr > 256 ? 1 : 256 / lpr;
     const long long n = (rows + groups - 1) / groups;
     return (int)(n < 1 ? 1 : n > 768 ? 768 : n);
 }
