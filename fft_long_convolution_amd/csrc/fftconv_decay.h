@@ -16,6 +16,7 @@ struct LayerNormParams {
     float eps;
     long long stride;         // elements between rows of x
     bool wide;                // rows in 16-byte pieces: sizes and strides allow it
+    bool past;                // outputs past the caches
     const void* x;
     const float* w;           // [D] or null
     const float* b;

@@ -128,27 +128,26 @@ __global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, l
         n = z > a ? (z - a + p.seg_tokens - 1) / p.seg_tokens : 1;
     }
     float S = init ? init[(seq * Hv + h) * size + e] : 0.f;
-    // sixteen segments' effects on their way at once
-    constexpr int kAhead = 16;
-    for (long long j0 = 0; j0 < n; j0 += kAhead) {
+    const auto at = [&](long long j) { return (first + (back ? n - 1 - j : j)) * Hv + h; };
+    // eight segments' effects on their way at once; the last one's is not made
+    constexpr int kAhead = 8;
+    for (long long j0 = 0; j0 + 1 < n; j0 += kAhead) {
         float effect[kAhead];
         double g[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            // (the last one's is not made, and not used)
-            const long long at = j0 + j < n ? j0 + j : n - 1;
-            const long long i = (first + (back ? n - 1 - at : at)) * Hv + h;
+            const long long i = at(j0 + j + 1 < n ? j0 + j : n - 2);
             effect[j] = seg[i * size + e];
             g[j] = seg_g[i];
         }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (j0 + j >= n) break;
-            const long long i = (first + (back ? n - 1 - j0 - j : j0 + j)) * Hv + h;
-            seg[i * size + e] = S;
-            if (j0 + j + 1 < n) S = fmaf(exact_exp2(g[j]), S, effect[j]);
-        }
+        for (int j = 0; j < kAhead; ++j)
+            if (j0 + j + 1 < n) {
+                seg[at(j0 + j) * size + e] = S;
+                S = fmaf(exact_exp2(g[j]), S, effect[j]);
+            }
     }
+    seg[at(n - 1) * size + e] = S;
 }
 
 }  // namespace

@@ -261,8 +261,13 @@ __global__ __launch_bounds__(512, (DA > 128 || (IO == IO_F32 && DA > 64) ? 2 : 4
         if (more) fetch(C);
         dfloat4 acc[C / 16];
         if (keys) {
-            make_scores_and_sums<IO, DA, C, RW>(places.rows, places.lane, V, DO, K, Q, P, back[1], fac,
-                                                f.scale, wave, sums);
+            // the sums once for a head
+            if (slice == 0)
+                make_scores_and_sums<IO, DA, C, RW>(places.rows, places.lane, V, DO, K, Q, P, back[1],
+                                                    fac, f.scale, wave, sums);
+            else
+                make_scores<IO, DA, C, RW, true>(places.rows, places.lane, V, DO, P, back[1], fac,
+                                                 f.scale, wave);
             __builtin_amdgcn_sched_barrier(0);
             state_product<IO, DA, C, IO == IO_BF16 ? 2 : Kind<IO>::NS>(places.rows, places.lane, V, X,
                                                                        fac, acc);
@@ -281,15 +286,16 @@ __global__ __launch_bounds__(512, (DA > 128 || (IO == IO_F32 && DA > 64) ? 2 : 4
             if (lane < C) {
 #pragma unroll
                 for (int w = 0; w < RW; ++w) x += dots[w][lane];
+                if (slice == 0)
 #pragma unroll
-                for (int w = 0; w < Scores<IO, C>::kUnits; ++w) r += sums[w][lane];
+                    for (int w = 0; w < Scores<IO, C>::kUnits; ++w) r += sums[w][lane];
             }
             const double to = prefix_sum(x), all = __shfl(to, 63);
             double before = __shfl_up(to, 1);
             if (lane == 0) before = 0;
             if (lane < n)
                 p.behind[((long long)slice * f.Hv + h) * p.B * f.sp.T + token0 + at + lane] =
-                    (float)(before + (slice == 0 ? r : 0));
+                    (float)(before + r);
             if (lane == 0)
                 p.chunks[(slice * p.slots + slot0 + at / C) * f.Hv + h] = make_double2(all, fac.all);
         }

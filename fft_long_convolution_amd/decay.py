@@ -79,7 +79,7 @@ class LayerNorm(_Op):
 
     def _rows(self, x, name):
         """x [..., D] as [rows, D]."""
-        if x.dim() < 1 or x.shape[-1] != self.D:
+        if x.dim() < 1 or x.shape[-1] != self.D or self.D < 1:
             raise ValueError("%s must be [..., %d]" % (name, self.D))
         return x if x.dim() == 2 else x.reshape(x.numel() // self.D, self.D)
 
