@@ -596,7 +596,8 @@ typedef struct fftconv_decay_desc {
  *     decays between two tokens stay finite.
  *  cu_seqlens: device, int64 [sequences + 1], ascending from 0 to T
  *     (sequences may be empty); NULL when sequences = 0.  Bounds outside
- *     [0, T] or out of order are clamped on the device.
+ *     [0, T] are clamped on the device; where bounds are out of order nothing
+ *     outside the tensors is touched, and there are no defined results.
  *  initial_state: fp32 [rows][Hv][Dk][Dv], rows = sequences or B; NULL for 0.
  *  o [B][T][Hv][Dv].  Tokens that no sequence holds are not written, or 0
  *     where the descriptor asks for that.
@@ -628,8 +629,8 @@ size_t fftconv_decay_workspace_bytes(const fftconv_decay_desc *desc);
  *     the decay is fixed; d_initial_state: as initial_state, or NULL to skip it.
  *  Tokens before the first and behind the last of cu_seqlens have gradients of 0.
  *  workspace: fftconv_decay_backward_workspace_bytes(desc) bytes.
- *  Gradients that a NaN or infinity reaches are not finite, and those of the other
- * tokens of its 64 (counted from the sequence's first) need not be. */
+ *  Gradients that a NaN or infinity reaches are not finite, and the others of its
+ * sequence and heads need not be. */
 fftconv_status fftconv_decay_backward(const fftconv_decay_desc *desc, const void *q,
                                       const void *k, const void *v, const float *g,
                                       const long long *cu_seqlens, const float *initial_state,
