@@ -59,7 +59,7 @@ constexpr int kSegAlign = 64;        // segments are cut at multiples of it
 struct DecayRows {
     const void* p;
     long long st[3];                 // batch, token, head
-    int group, D;
+    int group;
 };
 // Sequences, and their segments of seg_tokens tokens (a multiple of
 // kSegAlign).  Equal lengths: sequence i is batch row i, its segments are

@@ -82,6 +82,8 @@ size_t decay_segment(const fftconv_decay_desc* d) {
     const size_t whole = (blocks + 1) * kSegAlign;
     const size_t rows = d->sequences ? d->sequences : d->B;
     if (!rows || !blocks) return whole;
+    // workgroups of the join
+    if (rows * d->Hv * ((d->Dk * d->Dv + 255) / 256) > kMaxGrid) return whole;
     const double vs = (double)((d->Dv + kDecayCols - 1) / kDecayCols);
     const double heads = (double)rows * d->Hv * vs;
     // us of 64 tokens in a walk of so many workgroups: the latency of one, or what the
@@ -101,6 +103,9 @@ size_t decay_segment(const fftconv_decay_desc* d) {
         const double n = (double)(size_t)(longest / per + 0.999);
         const double all = heads * (d->sequences ? mean / per + 0.5 : n);
         if (n > 256) continue;
+        // those of the walks
+        const size_t segs = d->sequences ? blocks / per + rows : rows * ((blocks + per - 1) / per);
+        if (segs * d->Hv * 32 > kMaxGrid) continue;
         // two more launches, the join's steps, states made, joined and read at 5 TB/s
         const double states = all / vs * d->Dk * d->Dv * 16 / 5e6;
         const double t = per * (time(all, 4.3, 2.75) + time(all, 2.3, 1.45)) + 14.0 + 0.3 * n + states;
@@ -207,9 +212,9 @@ fftconv_status decay_inputs(const fftconv_decay_desc* d, const DecayArgs& a, con
     p.fixed = d->fixed_decay != 0;
     p.clear = d->clear_unheld != 0;
     const int group = (int)(d->Hv / d->Hk);
-    p.q = {a.q, {d->q_stride[0], d->q_stride[1], d->q_stride[2]}, group, p.Dk};
-    p.k = {a.k, {d->k_stride[0], d->k_stride[1], d->k_stride[2]}, group, p.Dk};
-    p.v = {a.v, {d->v_stride[0], d->v_stride[1], d->v_stride[2]}, 1, p.Dv};
+    p.q = {a.q, {d->q_stride[0], d->q_stride[1], d->q_stride[2]}, group};
+    p.k = {a.k, {d->k_stride[0], d->k_stride[1], d->k_stride[2]}, group};
+    p.v = {a.v, {d->v_stride[0], d->v_stride[1], d->v_stride[2]}, 1};
     p.g = a.g;
     p.init = a.init;
     return FFTCONV_OK;
@@ -346,7 +351,7 @@ fftconv_status fftconv_decay_backward(const fftconv_decay_desc* d, const void* q
     p.B = (long long)d->B;
     p.d_o = {d_o,
              {(long long)(d->T * d->Hv * d->Dv), (long long)(d->Hv * d->Dv), (long long)d->Dv},
-             1, (int)d->Dv};
+             1};
     p.dfin = d_final_state;
     p.dq = dq;
     p.dk = dk;

@@ -52,15 +52,21 @@ struct WalkLds {
 };
 
 // Waves of a SIMD that the walk leaves registers for.
-template <int IO, int DA, int MODE>
+template <int IO, int DA>
 constexpr int kWalkWaves = DA > 128 ? 2 : DA > 64 ? (IO == IO_F32 ? 2 : 3) : 4;
 
 // A workgroup takes 16 W columns of a segment of one head.  A chunk goes in two
 // halves: scores and the state's product (with A and B), then what has V in it; the
 // rows of the next chunk are on their way in registers all the time, and go to LDS
 // when the chunk is done, where its outputs, brought to V's place, come out.
+//
+// 64 x 1024 tokens of 6 heads of 128 in bf16 take 132 us, 428 MB or 3.2 TB/s.  Vector
+// instructions bound it: some 480 of them (terms of the state, factors, addresses)
+// for 48 matrix instructions of a wave and chunk.  Chunks of 64 tokens on tiles of 32 x 32
+// took 154 us, eight waves of 16 columns no less; with chunks of 32 the scores outside the
+// triangle are few and three workgroups share a CU.
 template <int IO, int DA, int C, int W, int MODE>
-__global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA, MODE>)) void decay_walk_kernel(DecayWalk p) {
+__global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA>)) void decay_walk_kernel(DecayWalk p) {
     typedef WalkLds<IO, DA, C, W, MODE> L;
     constexpr int N = 64 * W, kB = Kind<IO>::kB, kCols = 16 * W;
     constexpr bool OUT = L::kOut, REV = MODE == kEffectsBack, DOT = MODE == kQueries;

@@ -13,7 +13,7 @@
 // Each element moves once in and once out (backward twice in) with some ten operations:
 // HBM bounds both passes.  64 x 1024 rows of 768 in bf16, 201 MB, take 35 us (5.8 TB/s;
 // a streaming copy reaches 5.9), 16 x 8192 of 768 in f16 forward and backward, 1.0 GB,
-// 193 us (5.2).  A lane of a row's group holds its pieces of eight elements from the load
+// 198 us (5.1).  A lane of a row's group holds its pieces of eight elements from the load
 // to the store; the sums go by shuffles, of rows of more than 2048 through LDS.
 #include "fftconv_decay.h"
 #include "fftconv_delta_dev.h"
@@ -357,8 +357,16 @@ hipError_t launch(const LayerNormParams& p, bool back, hipStream_t s) {
     if (back) {
         hipLaunchKernelGGL((layernorm_bwd_kernel<IO, LPR, V, WIDE>), dim3(p.blocks), dim3(N), 0, s, p);
     } else {
-        const dim3 grid((unsigned)((p.rows + kGroups - 1) / kGroups));
-        hipLaunchKernelGGL((layernorm_fwd_kernel<IO, LPR, V, WIDE>), grid, dim3(N), 0, s, p);
+        // a launch takes fewer than 2^32 threads
+        constexpr long long most = 0xffffffffll / N * kGroups, kB = IO == IO_F32 ? 4 : 2;
+        LayerNormParams part = p;
+        for (long long left = p.rows; left > 0; left -= most) {
+            part.rows = left < most ? left : most;
+            const dim3 grid((unsigned)((part.rows + kGroups - 1) / kGroups));
+            hipLaunchKernelGGL((layernorm_fwd_kernel<IO, LPR, V, WIDE>), grid, dim3(N), 0, s, part);
+            part.x = (const char*)part.x + most * p.stride * kB;
+            part.y = (char*)part.y + most * p.D * kB;
+        }
     }
     return hipGetLastError();
 }
@@ -383,7 +391,7 @@ hipError_t lanes(const LayerNormParams& p, bool back, hipStream_t s) {
 }
 // Outputs of 160 MB and more do not stay in the caches (256 MB in all) until they are
 // read again, and past them they leave the input there: 16 x 8192 rows of 768 in f16,
-// 201 MB each, forward and backward 193 us, through the caches 200.
+// 201 MB each, forward and backward 193 us, through the caches 200 (in turn).
 hipError_t any(int io, LayerNormParams p, bool back, hipStream_t s) {
     p.past = p.rows * p.D * 2 >= (160ll << 20);
     switch (io) {

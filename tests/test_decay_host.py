@@ -286,3 +286,14 @@ def test_missing_library_fails_loudly(monkeypatch):
     for make in (lambda: decay.LayerNorm(64), lambda: decay.DecayAttention(64, 64)):
         with pytest.raises(RuntimeError, match="not built"):
             make()
+
+
+def test_more_segments_than_a_launch_takes():
+    # sequences that could be cut are walked whole where the segments, or the threads
+    # that join them, would be more than one launch takes
+    for kw in (dict(T=8000 * 192, sequences=8000, Hk=64, Hv=64, Dk=8, Dv=8),
+               dict(T=8000 * 192, sequences=8000, Hk=64, Hv=64, Dk=128, Dv=128),
+               dict(T=7000 * 300, sequences=7000, Hk=64, Hv=64, Dk=128, Dv=128)):
+        d = desc(B=1, **kw)
+        assert sizes(d)[0] == 0 and sizes(d)[1] > 0
+        assert call(d, ws_bytes=0, ws=None, q=None) == INVALID       # not UNSUPPORTED

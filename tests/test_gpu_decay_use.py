@@ -404,3 +404,14 @@ def test_layer_norm_past_4_gib():
     assert torch.equal(y, norm(D, "bf16").forward(z, w, w))
     assert all(torch.equal(a, b) for a, b in zip(norm(D, "bf16").backward(x, z, w, w),
                                                  norm(D, "bf16").backward(z, z, w, w)))
+
+
+def test_more_rows_than_a_launch_takes():
+    """16 rows a workgroup of 256 threads: 2^28 rows are 2^32 threads."""
+    base = torch.randn(1 << 14, 8, device="cuda").bfloat16()
+    n, w = (1 << 14) + 1, torch.ones(8, device="cuda")
+    x = base.repeat(n, 1)
+    y = norm(8, "bf16").forward(x, w, w).view(n, 1 << 14, 8)
+    want = norm(8, "bf16").forward(base, w, w)
+    for i in (0, 1, n // 2, n - 2, n - 1):
+        assert torch.equal(y[i], want)
