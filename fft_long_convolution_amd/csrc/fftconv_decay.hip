@@ -113,54 +113,69 @@ hipError_t fwd_io(const DecayParams& p, hipStream_t s) {
 
 // ------------------------------------------------------------------- segments
 
-// The segments' effects on the state become their first states: a thread takes
-// an element of one sequence's state.  back: from the last segment to the first.
-// A chain of loads: with one effect on its way 16 segments took as long as the walk of
-// a few chunks (4 x 32768 tokens of 4 heads 288 us in all), with eight 280.
-__global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, long long size,
+// The segments' effects on the state become their first states: a thread takes V
+// elements of one sequence's state.  back: from the last segment to the first.
+// A chain of loads, so eight segments' effects are on their way at once (the last
+// segment's is not made); sixteen were no faster.
+template <int V>
+__global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, unsigned size,
                                                          const float* init, float* seg,
                                                          const double* seg_g, bool back) {
-    const long long per = (size + 255) / 256;
-    const long long block = blockIdx.x / per, e = (blockIdx.x - block * per) * 256 + threadIdx.x;
-    const unsigned h = (unsigned)(block % Hv);
-    const long long seq = block / Hv;
+    typedef float Part __attribute__((ext_vector_type(V)));
+    const unsigned per = (size + 256 * V - 1) / (256 * V), block = blockIdx.x / per;
+    const unsigned e = ((blockIdx.x - block * per) * 256 + threadIdx.x) * V;
+    const unsigned seq = block / (unsigned)Hv, h = block - seq * Hv;
     if (e >= size) return;
-    long long first = seq * p.per, n = p.per;
+    long long first = (long long)seq * p.per;
+    int n = p.per;
     if (p.cu) {
-        const long long a = bound_of(p, seq), z = bound_of(p, seq + 1);
-        first = a / p.seg_tokens + seq;
-        n = z > a ? (z - a + p.seg_tokens - 1) / p.seg_tokens : 1;
+        const unsigned a = (unsigned)bound_of(p, seq), z = (unsigned)bound_of(p, seq + 1);
+        first = a / (unsigned)p.seg_tokens + seq;
+        n = z > a ? (int)((z - a + p.seg_tokens - 1) / (unsigned)p.seg_tokens) : 1;
     }
-    float S = init ? init[(seq * Hv + h) * size + e] : 0.f;
-    const auto at = [&](long long j) { return (first + (back ? n - 1 - j : j)) * Hv + h; };
-    // eight segments' effects on their way at once; the last one's is not made
+    const auto part = [&](const float* x, long long i) { return *(const Part*)(x + i * size + e); };
+    Part S;
+#pragma unroll
+    for (int v = 0; v < V; ++v) S[v] = 0.f;
+    if (init) S = part(init, (long long)seq * Hv + h);
+    const auto at = [&](int j) { return (first + (back ? n - 1 - j : j)) * Hv + h; };
     constexpr int kAhead = 8;
-    for (long long j0 = 0; j0 + 1 < n; j0 += kAhead) {
-        float effect[kAhead];
+    for (int j0 = 0; j0 + 1 < n; j0 += kAhead) {
+        Part effect[kAhead];
         double g[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const long long i = at(j0 + j + 1 < n ? j0 + j : n - 2);
-            effect[j] = seg[i * size + e];
+            effect[j] = part(seg, i);
             g[j] = seg_g[i];
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
             if (j0 + j + 1 < n) {
-                seg[at(j0 + j) * size + e] = S;
-                S = fmaf(exact_exp2(g[j]), S, effect[j]);
+                *(Part*)(seg + at(j0 + j) * size + e) = S;
+                const float a = exact_exp2(g[j]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) S[v] = fmaf(a, S[v], effect[j][v]);
             }
     }
-    seg[at(n - 1) * size + e] = S;
+    *(Part*)(seg + at(n - 1) * size + e) = S;
+}
+template <int V>
+hipError_t join_launch(const DecayParams& p, const float* init, bool back, hipStream_t s) {
+    const unsigned size = (unsigned)(p.Dk * p.Dv), per = (size + 256 * V - 1) / (256 * V);
+    hipLaunchKernelGGL((decay_join_kernel<V>), dim3((unsigned)(p.sp.nseq * p.Hv * per)),
+                       dim3(256), 0, s, p.sp, p.Hv, size, init, p.seg, p.seg_g, back);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_decay_join(const DecayParams& p, const float* init, bool back, hipStream_t s) {
-    const long long size = (long long)p.Dk * p.Dv, per = (size + 255) / 256;
-    hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)(p.sp.nseq * p.Hv * per)), dim3(256), 0, s,
-                       p.sp, p.Hv, size, init, p.seg, p.seg_g, back);
-    return hipGetLastError();
+    // Four elements a thread where that leaves a workgroup for each CU.  With one and with
+    // four: 5888 workgroups of single elements 18.0 and 8.3 us, 1024 (4 x 32768 tokens of 4
+    // heads of 128) 12.8 and 9.2, 128 (2 x 1501 of 4 heads of 64) 7.2 and 8.1.
+    const long long blocks = p.sp.nseq * p.Hv * ((p.Dk * p.Dv + 255) / 256);
+    return blocks >= 1024 ? join_launch<4>(p, init, back, s) : join_launch<1>(p, init, back, s);
 }
 
 hipError_t launch_decay_fwd(int io, const DecayParams& p, hipStream_t s) {

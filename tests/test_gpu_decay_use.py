@@ -415,3 +415,24 @@ def test_more_rows_than_a_launch_takes():
     want = norm(8, "bf16").forward(base, w, w)
     for i in (0, 1, n // 2, n - 2, n - 1):
         assert torch.equal(y[i], want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_states_are_joined(dtype):
+    """Cut sequences of so many states that a thread joins several elements: each row
+    as it is by itself (other segments, so other roundings)."""
+    B, T, H, D = 20, 1000, 2, 128
+    assert B * H * D * D // 256 > 2048
+    q, k, v, g, S = gpu(*decay_inputs(8, B, T, H, H, D, D, dtype, rate=0.02))
+    op = attend(D, D, dtype)
+    assert op._lib.fftconv_decay_workspace_bytes(op._describe(q, k, v, g, None, None)[0][1][0]) > 0
+    do = torch.randn(v.shape, device="cuda").to(DT[dtype])
+    got = [*op.forward(q, k, v, g, initial_state=S),
+           *op.backward(q, k, v, g, do, d_final_state=S, initial_state=S)]
+    for i in (0, 7, B - 1):
+        r = [x[i:i + 1] for x in (q, k, v, g, S, do)]
+        want = [*op.forward(*r[:4], initial_state=r[4]),
+                *op.backward(*r[:4], r[5], d_final_state=r[4], initial_state=r[4])]
+        for name, x, y in zip(("o", "state", *NAMES), got, want):
+            t = "f32" if name == "state" else kind(name, dtype)
+            assert rel(x[i:i + 1], y.cpu().double()) <= 2 * TOL[t], name
