@@ -73,11 +73,10 @@ fftconv_status decay_sizes(const fftconv_decay_desc* d) {
 // the one of least time by the model below, a whole sequence where that is least.
 //
 // Measured, bf16 and heads of 128, whole, as chosen and the best of ten lengths from 64
-// tokens on: 4 x 32768 tokens of 4 heads 2209, 289 and 279 us; 16 x 8192 of 6, 550, 377
-// and 377; 1 x 4096 of 8, 274, 48 and 47; 16 x 1024 of 6, 74, 74 (whole) and 74; with
-// gradients 8 x 2048 of 4, 638, 239 and 239.  23 packed
-// sequences of 9001 tokens, 8 heads of 64 x 128 in f16, 102, 71 and 70
-// (62 as chosen since the join takes four elements a thread).
+// tokens on: 4 x 32768 tokens of 4 heads 2209, 280 and 280 us; 16 x 8192 of 6, 549, 374
+// and 372; 1 x 4096 of 8, 271, 47 and 46; 16 x 1024 of 6, 75, 75 (whole) and 66; with
+// gradients 8 x 2048 of 4, 635, 234 and 226.  23 packed sequences of 9001 tokens, 8 heads
+// of 64 x 128 in f16, 102, 63 and 59.
 size_t decay_segment(const fftconv_decay_desc* d) {
     const size_t blocks = (d->T + kSegAlign - 1) / kSegAlign;
     const size_t whole = (blocks + 1) * kSegAlign;
