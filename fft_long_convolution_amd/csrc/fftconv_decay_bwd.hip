@@ -275,13 +275,12 @@ __global__ __launch_bounds__(512, (DA > 128 || (IO == IO_F32 && DA > 64) ? 2 : 4
                 make_scores<IO, DA, C, RW, true>(places.rows, places.lane, V, DO, P, back[1], fac,
                                                  f.scale, wave);
             __builtin_amdgcn_sched_barrier(0);
-            state_product<IO, DA, C, IO == IO_BF16 ? 2 : Kind<IO>::NS>(places.rows, places.lane, V, X,
-                                                                       fac, acc);
+            state_product<IO, DA, C>(places.rows, places.lane, V, X, fac, acc);
         } else {
             make_scores<IO, DA, C, RW, true>(places.rows, places.lane, K, Q, P, back[0], fac, f.scale,
                                              wave);
             __builtin_amdgcn_sched_barrier(0);
-            state_product<IO, DA, C, Kind<IO>::NS>(places.rows, places.lane, K, X, fac, acc);
+            state_product<IO, DA, C>(places.rows, places.lane, K, X, fac, acc);
             __builtin_amdgcn_sched_barrier(0);
             row_dots<IO, DA, C>(places.cells, places.lane, V, acc, dots[wave]);
         }

@@ -11,11 +11,12 @@
 // forward in time f = e^D, w = e^(Dc-D), Gam_ts = e^(D_t-D_s) for s <= t; backward
 // f = e^(Dc-D), w = e^D, Gam_ts = e^(D_s-D_t) for s >= t (and constant factors).
 //
-// Matrix products.  16-bit rows are exact operands.  An fp32 operand is written
-// in terms of that type, each the rounding of what the ones before leave: of
-// bf16 three for states (26 bits) and two for what meets outputs of 8 bits only (17),
-// with fp32's range; of f16 two (22 bits), with a power of two for each column
-// (states, weighted values) or row of 32 scores that takes the largest to 2^14.
+// Matrix products.  16-bit rows are exact operands.  An fp32 operand (states, scores,
+// weighted values) is written in terms of that type, each the rounding of what the ones
+// before leave: of bf16 three (26 bits), with fp32's range; of f16 two (22 bits), with a
+// power of two for each column (states, weighted values) or row of 32 scores that takes
+// the largest to 2^14.  So the rounding of an output is the only one to fewer bits, also
+// where most of a sum cancels.
 // fp32 rows go to the fp32 matrix instructions as they are, which have 1/16 of
 // the rate, and so have all operands 24 bits.
 //
@@ -35,8 +36,7 @@ namespace fftconv {
 template <int IO>
 struct Kind {
     static constexpr int kB = IO == IO_F32 ? 4 : 2;
-    static constexpr int NS = IO == IO_BF16 ? 3 : IO == IO_F16 ? 2 : 1;   // terms of a state
-    static constexpr int NP = IO == IO_F32 ? 1 : 2;                       // of scores
+    static constexpr int NT = IO == IO_BF16 ? 3 : IO == IO_F16 ? 2 : 1;   // terms of an operand
 };
 
 // ------------------------------------------------------------------- spans
@@ -461,7 +461,7 @@ __device__ __forceinline__ void put_factors(Factors<C>& F, double D, float sf, f
 template <int IO, int C>
 struct Scores {
     static constexpr int kBlock = 64 * (int)sizeof(Frag<IO>), M = C / 16, KB = C / 32;
-    static constexpr int kTerm = kBlock * M * KB, kBytes = kTerm * Kind<IO>::NP;
+    static constexpr int kTerm = kBlock * M * KB, kBytes = kTerm * Kind<IO>::NT;
     static constexpr int kTiles = C == 64 || IO == IO_F16 ? 2 : 1;
     static constexpr int kParts = M / kTiles, kUnits = M * kParts;
     static __device__ __forceinline__ Frag<IO> get(const char* P, int lane, int term, int m, int kb) {
@@ -476,10 +476,10 @@ struct Scores {
             *(dfloat4*)(P + place * 32 + (g & 1) * 16) = p;
         } else {
             const float x[8] = {p[0], p[1], p[2], p[3], 0, 0, 0, 0};
-            Frag<IO> t[Kind<IO>::NP];
-            terms<IO, Kind<IO>::NP>(x, to, t);
+            Frag<IO> t[Kind<IO>::NT];
+            terms<IO, Kind<IO>::NT>(x, to, t);
 #pragma unroll
-            for (int n = 0; n < Kind<IO>::NP; ++n)
+            for (int n = 0; n < Kind<IO>::NT; ++n)
                 *(uint2*)(P + n * kTerm + place * 16 + (g & 1) * 8) = make_uint2(t[n].v[0], t[n].v[1]);
         }
     }
@@ -626,11 +626,11 @@ __device__ __forceinline__ long long anchor_of(const DecaySpans& p, const DecayS
 }
 
 // acc[m] = f o (rows A times S) for the row tiles m
-template <int IO, int DA, int C, int NS>
+template <int IO, int DA, int C>
 __device__ __forceinline__ void state_product(const RowReader<IO, DA>& rows, int lane, const char* A,
                                               const State<DA>& S, const Factors<C>& F,
                                               dfloat4 (&acc)[C / 16]) {
-    constexpr int M = C / 16;
+    constexpr int M = C / 16, N = Kind<IO>::NT;
     const int g = lane >> 4;
     float back = 1.f, to = 1.f;
     if constexpr (IO == IO_F16) {
@@ -642,13 +642,13 @@ __device__ __forceinline__ void state_product(const RowReader<IO, DA>& rows, int
     for (int m = 0; m < M; ++m) acc[m] = dfloat4{0, 0, 0, 0};
 #pragma unroll
     for (int kb = 0; kb < DA / 32; ++kb) {
-        Frag<IO> a[M], b[NS];
+        Frag<IO> a[M], b[N];
 #pragma unroll
         for (int m = 0; m < M; ++m) a[m] = rows.get(A, 16 * m, 32 * kb);
         const float s[8] = {S.t[2 * kb][0], S.t[2 * kb][1], S.t[2 * kb][2], S.t[2 * kb][3],
                             S.t[2 * kb + 1][0], S.t[2 * kb + 1][1], S.t[2 * kb + 1][2],
                             S.t[2 * kb + 1][3]};
-        terms<IO, NS>(s, to, b);
+        terms<IO, N>(s, to, b);
         if constexpr (IO == IO_F32) {
             // a chain of additions for each block of k: fewer roundings in a row
 #pragma unroll
@@ -656,7 +656,7 @@ __device__ __forceinline__ void state_product(const RowReader<IO, DA>& rows, int
                 acc[m] += mma16<IO>(a[m], b[0], dfloat4{0, 0, 0, 0});
         } else {
 #pragma unroll
-            for (int n = NS - 1; n >= 0; --n)
+            for (int n = N - 1; n >= 0; --n)
 #pragma unroll
                 for (int m = 0; m < M; ++m) acc[m] = mma16<IO>(a[m], b[n], acc[m]);
         }
@@ -702,7 +702,7 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
                                                const Frag<IO> (&values)[C / 32], bool unbounded,
                                                dfloat4 (&acc)[C / 16]) {
     typedef Scores<IO, C> L;
-    constexpr int NP = Kind<IO>::NP;
+    constexpr int N = Kind<IO>::NT;
     const int g = lane >> 4;
     int bad = REV ? -1 : C;
 #pragma unroll
@@ -714,7 +714,7 @@ __device__ __forceinline__ void scores_product(const char* P, const float* back,
         for (int m = 0; m < L::M; ++m)
             s[m] = IO == IO_F16 ? dfloat4{0, 0, 0, 0} : acc[m];
 #pragma unroll
-        for (int n = NP - 1; n >= 0; --n)
+        for (int n = N - 1; n >= 0; --n)
 #pragma unroll
             for (int m = 0; m < L::M; ++m)
                 if (REV ? kb >= m / 2 : kb <= m / 2)
@@ -759,7 +759,7 @@ template <int IO, int DA, int C, int G>
 __device__ __forceinline__ void update_state(const ColReader<IO, DA, true>& cols, int lane,
                                              const char* B, const Frag<IO> (&values)[C / 32],
                                              const Factors<C>& F, State<DA>& S) {
-    constexpr int NS = Kind<IO>::NS, KB = C / 32;
+    constexpr int N = Kind<IO>::NT, KB = C / 32;
     const int g = lane >> 4;
     const float all = F.all;
     float to = 1.f, back = 1.f;
@@ -777,12 +777,12 @@ __device__ __forceinline__ void update_state(const ColReader<IO, DA, true>& cols
         to = sc.to;
         back = sc.back;
     }
-    Frag<IO> v[KB][NS];
+    Frag<IO> v[KB][N];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
         float x[8];
         weighted<IO, C>(values[kb], F, 32 * kb + 8 * g, x);
-        terms<IO, NS>(x, to, v[kb]);
+        terms<IO, N>(x, to, v[kb]);
     }
 #pragma unroll
     for (int i = 0; i < State<DA>::N; i += G) {
@@ -795,7 +795,7 @@ __device__ __forceinline__ void update_state(const ColReader<IO, DA, true>& cols
 #pragma unroll
             for (int j = 0; j < G; ++j) a[j] = cols.get(B, 32 * kb, i + j);
 #pragma unroll
-            for (int n = NS - 1; n >= 0; --n)
+            for (int n = N - 1; n >= 0; --n)
 #pragma unroll
                 for (int j = 0; j < G; ++j) part[j] = mma16<IO>(a[j], v[kb][n], part[j]);
         }

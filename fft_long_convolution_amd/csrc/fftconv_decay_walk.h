@@ -60,7 +60,7 @@ constexpr int kWalkWaves = DA > 128 ? 2 : DA > 64 ? (IO == IO_F32 ? 2 : 3) : 4;
 // rows of the next chunk are on their way in registers all the time, and go to LDS
 // when the chunk is done, where its outputs, brought to V's place, come out.
 //
-// 64 x 1024 tokens of 6 heads of 128 in bf16 take 132 us, 428 MB or 3.2 TB/s.  Vector
+// 64 x 1024 tokens of 6 heads of 128 in bf16 take 148 us, 428 MB or 2.9 TB/s.  Vector
 // instructions bound it: some 480 of them (terms of the state, factors, addresses)
 // for 48 matrix instructions of a wave and chunk.  Chunks of 64 tokens on tiles of 32 x 32
 // took 154 us, eight waves of 16 columns no less; with chunks of 32 the scores outside the
@@ -209,8 +209,7 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA>)) void decay_walk_kerne
         if (OUT) {
             make_scores<IO, DA, C, W, false>(at.rows, at.lane, A, B, P, back, f, p.ss, wave);
             __builtin_amdgcn_sched_barrier(0);
-            state_product<IO, DA, C, IO == IO_BF16 && !DOT ? 2 : Kind<IO>::NS>(at.rows, at.lane, A, S,
-                                                                              f, acc);
+            state_product<IO, DA, C>(at.rows, at.lane, A, S, f, acc);
             __builtin_amdgcn_sched_barrier(0);
             if (DOT) row_dots<IO, kCols, C>(at.cells, at.lane, lds + L::kAtX, acc, dots[wave]);
             __syncthreads();

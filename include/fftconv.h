@@ -604,9 +604,9 @@ typedef struct fftconv_decay_desc {
  *  final_state: fp32, as initial_state; NULL to skip it.
  *  workspace: fftconv_decay_workspace_bytes(desc) bytes.
  * States, decays and sums are fp32 or wider whatever the I/O type; operands of the
- * 16-bit matrix products that are not of the I/O type are split into two or three
- * terms (22 to 26 bits in states, 17 in what meets 16-bit outputs only); outputs are
- * rounded to their type once.  Long sequences of few heads are cut into segments:
+ * 16-bit matrix products that are not of the I/O type (states, scores) are split into
+ * three bf16 terms, 26 bits, or two f16 terms, 22 bits, with a scale for each column or
+ * row; outputs are rounded to their type once.  Long sequences of few heads are cut into segments:
  * equal calls give equal bits.
  *  A NaN or infinity reaches what it reaches in the formulas: from k or g its
  * token's outputs, the later ones of the sequence and the state (from k in its
