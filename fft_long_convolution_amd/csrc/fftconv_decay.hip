@@ -153,9 +153,12 @@ __global__ __launch_bounds__(256) void decay_join_kernel(DecaySpans p, int Hv, u
         for (int j = 0; j < kAhead; ++j)
             if (j0 + j + 1 < n) {
                 *(Part*)(seg + at(j0 + j) * size + e) = S;
-                const float a = exact_exp2(g[j]);
+                // the rounding of a, the same for equal segments, goes with it
+                float left;
+                const float a = exact_exp2(g[j], left);
 #pragma unroll
-                for (int v = 0; v < V; ++v) S[v] = fmaf(a, S[v], effect[j][v]);
+                for (int v = 0; v < V; ++v)
+                    S[v] = fmaf(a, S[v], fmaf(a * left, S[v], effect[j][v]));
             }
     }
     *(Part*)(seg + at(n - 1) * size + e) = S;

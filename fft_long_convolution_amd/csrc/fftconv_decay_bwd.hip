@@ -228,6 +228,7 @@ __global__ __launch_bounds__(512, (DA > 128 || (IO == IO_F32 && DA > 64) ? 2 : 4
     char* dk = (char*)(wide ? (void*)p.dk_heads : p.dk) + (token0 + last) * krow +
                (long long)(h * f.Dk + first) * kb;
     char* dv = (char*)p.dv + (token0 + last) * vrow + (long long)(h * f.Dv + first) * kB;
+    Drift drift;
     float g = 0.f;
     if (chunks) {
         fetch(count(0));
@@ -321,6 +322,7 @@ __global__ __launch_bounds__(512, (DA > 128 || (IO == IO_F32 && DA > 64) ? 2 : 4
         else if (mine < DA) rows_to_tile<IO, DA, C>(places.cells, keys ? V : K, acc);
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C, 2>(places.elements, places.lane, keys ? DO : Q, val, fac, X);
+        drift.after(fac.err, i, !more, X);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
         Move rows_k, rows_v;

@@ -398,7 +398,8 @@ struct Factors {
     int whole[C];
     float rest[C];
     float f[C], w[C];        // of the rows of the state's product, of the values
-    float all, none[3];      // e^Dc
+    float all, err;          // e^Dc, and what its rounding left of it, in parts of it
+    float none[2];
 };
 struct Power { int whole; float rest; };
 __device__ __forceinline__ Power power_of(double x) {
@@ -412,7 +413,8 @@ __device__ __forceinline__ float exp2_of(int whole, float rest) {
 // whole state share, so that their errors do not average out.  With y = rest log 2,
 // at most 0.35: 1 + y in 64 bits and the Taylor terms from y^2 / 2 on, below 0.07, in
 // 32 (off by 2^-28), up to y^9 / 9! (2e-10).
-__device__ __forceinline__ float exact_exp2(double x) {
+// left: the exact value is (1 + left) times the result.
+__device__ __forceinline__ float exact_exp2(double x, float& left) {
     const double n = __builtin_rint(x), y = (x - n) * 0.6931471805599453;
     const float z = (float)y;
     float e = 1.f / 362880;
@@ -423,7 +425,14 @@ __device__ __forceinline__ float exact_exp2(double x) {
     e = fmaf(e, z, 1.f / 24);
     e = fmaf(e, z, 1.f / 6);
     e = fmaf(e, z, 0.5f);
-    return __builtin_ldexpf((float)(1.0 + (y + (double)(e * z * z))), (int)n);
+    const double exact = 1.0 + (y + (double)(e * z * z));
+    const float near = (float)exact;
+    left = (float)(exact - near) / near;
+    return __builtin_ldexpf(near, (int)n);
+}
+__device__ __forceinline__ float exact_exp2(double x) {
+    float left;
+    return exact_exp2(x, left);
 }
 // By the 64 lanes of one wave: D of the lane's token (n tokens, those behind have the
 // last one's), in units of log 2.  g: the token's log decay (0 behind the last).
@@ -442,13 +451,17 @@ __device__ __forceinline__ void put_factors(Factors<C>& F, double D, float sf, f
     const int lane = threadIdx.x & 63;
     const double all = __shfl(D, C - 1);
     const Power p = power_of(D);
-    const float to = exact_exp2(D), from = exact_exp2(all - D);
+    float left;
+    const float to = exact_exp2(D, left), from = exact_exp2(all - D);
     if (lane < C) {
         F.whole[lane] = p.whole;
         F.rest[lane] = p.rest;
         F.f[lane] = sf * (REV ? from : to);
         F.w[lane] = sw * (REV ? to : from);
-        if (lane == C - 1) F.all = to;
+        if (lane == C - 1) {
+            F.all = to;
+            F.err = left;
+        }
     }
 }
 
@@ -596,6 +609,13 @@ struct State {
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < N; ++i) t[i] = dfloat4{0, 0, 0, 0};
+    }
+    // times 1 + x
+    __device__ __forceinline__ void correct(float x) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[i][r] = fmaf(x, t[i][r], t[i][r]);
     }
     // as it is, `tiles` of its tiles
     __device__ __forceinline__ void store_tiles(float* to, int tiles) const {
@@ -753,6 +773,21 @@ __device__ __forceinline__ void weighted(const Frag<IO>& v, const Factors<C>& F,
     x[0] *= a.x; x[1] *= a.y; x[2] *= a.z; x[3] *= a.w;
     x[4] *= b.x; x[5] *= b.y; x[6] *= b.z; x[7] *= b.w;
 }
+// What the roundings of e^Dc left of a state, in parts of it.  With equal decays that
+// is the same number chunk after chunk, up to 2^-25: over the 1024 chunks of a slow
+// decay 3e-5 of the state, where its own roundings, either way, come to 1e-6.  So it is
+// summed and given back every eighth chunk (2^-22 at most by then), which costs an
+// eighth of a vector instruction for each element and chunk.
+struct Drift {
+    float sum = 0.f;
+    template <int DA>
+    __device__ __forceinline__ void after(float err, int chunk, bool last, State<DA>& S) {
+        sum += err;
+        if ((chunk & 7) != 7 && !last) return;
+        S.correct(sum);
+        sum = 0.f;
+    }
+};
 // S <- e^Dc S + B^T (w o V).  The chunk's part is summed by itself: one rounding of the
 // state a chunk.  G: tiles at a time.
 template <int IO, int DA, int C, int G>

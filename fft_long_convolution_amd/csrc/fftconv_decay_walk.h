@@ -175,6 +175,7 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA>)) void decay_walk_kerne
                 (long long)(h * p.cols + first) * ob;
     const uint32_t omine = tid / MoveV::kPieces * row + 16u * (tid % MoveV::kPieces);
     Places<IO, DA, kCols> at(lane, 16 * wave);
+    Drift drift;
     float g = 0.f;
     if (chunks) {
         fetch(count(0));
@@ -241,6 +242,7 @@ __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA>)) void decay_walk_kerne
         }
         __builtin_amdgcn_sched_barrier(0);
         update_state<IO, DA, C, 4>(at.elements, at.lane, B, vf, f, S);
+        drift.after(f.err, i, ahead == 0, S);
         if (tid == 0) unbounded[(i + 1) & 1] = 0;
         __syncthreads();
         if (OUT && !wide) mo.take(V, pv, tid);
