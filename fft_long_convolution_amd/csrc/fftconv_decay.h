@@ -140,7 +140,8 @@ inline size_t decay_anchors(size_t T, size_t nseq, bool packed, size_t n) {
 inline size_t decay_anchor_floats(int Dk, int Dv) {
     return (size_t)(Dk + 15) / 16 * ((size_t)(Dv + 31) / 32) * 512;
 }
-// Workgroups of the last pass over dg take so many chunks of a sequence.
+// Workgroups of the last pass over dg take so many chunks of a sequence, a multiple of
+// those between anchors: none looks further than the chunk behind its own.
 constexpr int kDgChunks = 64;
 inline size_t decay_dg_units(size_t T, size_t nseq, bool packed) {
     const size_t n = (size_t)kDgChunks * kDecayChunk;
