@@ -121,11 +121,14 @@ __device__ __forceinline__ void make_scores_and_sums(const RowReader<IO, DA>& ro
 // chunks backward in time, with the gradient X of the state, columns of Dv in the
 // first role's waves (dv) and, transposed, columns of Dk in the second's (dk).
 //
-// 64 x 1024 tokens of 6 heads of 128 in bf16 take 366 us (of 650 for the forward pass and
-// all gradients; the walk of dq 191, dg 16).  Vector instructions bound it as they do the
-// forward walk.  Both products in one role of four waves need 64 more state registers:
-// 454 us with two waves a SIMD, 1000 with registers spilled; the chains in three rounds
-// of half their length 381.
+// 64 x 1024 tokens of 6 heads of 128 in bf16 take 405 us in a trace (the walk of dq 204,
+// dg 16, outputs 161; a call of the forward pass and all gradients takes 700 without one).
+// Vector instructions take 58 % of the cycles, matrix instructions 22 %, and waves wait 46 %
+// of their time for the chunk's barriers, LDS and loads (the walk of dq: 55, 22 and 41 %).
+// With two terms of the state for dk and of scores it took 366; at that time both
+// products in one role of four waves, which need 64 more state registers, took 454 with
+// two waves a SIMD and 1000 with registers spilled, the chains in three rounds of half
+// their length 381.
 template <int IO, int DA>
 __global__ __launch_bounds__(512, (DA > 128 || (IO == IO_F32 && DA > 64) ? 2 : 4)) void decay_back_kernel(DecayGradParams p,
                                                                                int slices) {

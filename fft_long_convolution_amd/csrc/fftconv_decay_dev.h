@@ -96,7 +96,11 @@ __device__ __forceinline__ bool segment_of(const DecaySpans& p, unsigned seg, De
 
 // Which 16-byte piece of a token's row holds piece u: u ^ swirl(token).  Sixteen
 // tokens at one piece (row reads) and four tokens by 32 bytes of two neighbouring
-// 16-element groups (transposed reads) each meet all banks.
+// 16-element groups (transposed reads of the values) each meet all banks.  Single cells of
+// 16 columns of 16-bit rows do not: tokens 8 apart exchange two neighbouring pieces, so
+// four tokens meet each bank twice; nor do the transposed reads of the state's elements,
+// which take the same half of all pieces.  A third of the walks' LDS cycles are such
+// conflicts.
 template <int PIECES>
 __device__ __forceinline__ uint32_t swirl(uint32_t t) {
     if constexpr (PIECES == 8) return ((t >> 3) & 1) | ((t >> 1) & 2) | ((t << 1) & 4);

@@ -73,10 +73,12 @@ fftconv_status decay_sizes(const fftconv_decay_desc* d) {
 // the one of least time by the model below, a whole sequence where that is least.
 //
 // Measured, bf16 and heads of 128, whole, as chosen and the best of ten lengths from 64
-// tokens on: 4 x 32768 tokens of 4 heads 2209, 280 and 280 us; 16 x 8192 of 6, 549, 374
-// and 372; 1 x 4096 of 8, 271, 47 and 46; 16 x 1024 of 6, 75, 75 (whole) and 66; with
-// gradients 8 x 2048 of 4, 635, 234 and 226.  23 packed sequences of 9001 tokens, 8 heads
-// of 64 x 128 in f16, 102, 63 and 59.
+// tokens on: 4 x 32768 tokens of 4 heads 2545, 310 and 292 us; 16 x 8192 of 6, 623, 406
+// and 405; 1 x 4096 of 8, 310, 49 and 50; 16 x 1024 of 6, 84, 84 (whole) and 71; with
+// gradients 8 x 2048 of 4, 687, 243 and 238.  23 packed sequences of 9001 tokens, 8 heads
+// of 64 x 128 in f16, 102, 65 and 61.  The device alone knows the bounds of packed
+// sequences: 16384 tokens in 40 of 6 heads, walked whole, take 57 us where they are of equal
+// length and 1254 where one holds nearly all (in segments of 256 tokens 100 and 135).
 size_t decay_segment(const fftconv_decay_desc* d) {
     const size_t blocks = (d->T + kSegAlign - 1) / kSegAlign;
     const size_t whole = (blocks + 1) * kSegAlign;

@@ -60,11 +60,14 @@ constexpr int kWalkWaves = DA > 128 ? 2 : DA > 64 ? (IO == IO_F32 ? 2 : 3) : 4;
 // rows of the next chunk are on their way in registers all the time, and go to LDS
 // when the chunk is done, where its outputs, brought to V's place, come out.
 //
-// 64 x 1024 tokens of 6 heads of 128 in bf16 take 148 us, 428 MB or 2.9 TB/s.  Vector
-// instructions bound it: some 480 of them (terms of the state, factors, addresses)
-// for 48 matrix instructions of a wave and chunk.  Chunks of 64 tokens on tiles of 32 x 32
-// took 154 us, eight waves of 16 columns no less; with chunks of 32 the scores outside the
-// triangle are few and three workgroups share a CU.
+// 64 x 1024 tokens of 6 heads of 128 in bf16 take 150 us, 428 MB or 2.9 TB/s.  By the
+// counters vector instructions take 59 % of the cycles (490 for 58 matrix instructions
+// of a wave and chunk: terms of the state, factors, addresses), matrix instructions 28 %,
+// and waves wait 31 % of their time, at the chunk's three barriers and for LDS: the tiles
+// are there once, so a chunk's rows go in when the one before is done.  With two bf16
+// terms of states and scores, 17 bits, it took 134.  Then chunks of 64 tokens on tiles of
+// 32 x 32 took 154, eight waves of 16 columns no less; with chunks of 32 the scores
+// outside the triangle are few and three workgroups share a CU.
 template <int IO, int DA, int C, int W, int MODE>
 __global__ __launch_bounds__(64 * W, (kWalkWaves<IO, DA>)) void decay_walk_kernel(DecayWalk p) {
     typedef WalkLds<IO, DA, C, W, MODE> L;

@@ -11,9 +11,9 @@
 // row in hand anyway.
 //
 // Each element moves once in and once out (backward twice in) with some ten operations:
-// HBM bounds both passes.  64 x 1024 rows of 768 in bf16, 201 MB, take 35 us (5.8 TB/s;
-// a streaming copy reaches 5.9), 16 x 8192 of 768 in f16 forward and backward, 1.0 GB,
-// 198 us (5.1).  A lane of a row's group holds its pieces of eight elements from the load
+// HBM bounds both passes.  64 x 1024 rows of 768 in bf16, 201 MB, take 31 us and a call 38
+// (6.5 and 5.2 TB/s: part of so many bytes stays in the 256 MB of caches; a streaming copy of
+// 2 GB reaches 5.9), 16 x 8192 of 768 in f16 forward and backward, 1.0 GB, 198 us (5.1).  A lane of a row's group holds its pieces of eight elements from the load
 // to the store; the sums go by shuffles, of rows of more than 2048 through LDS.
 #include "fftconv_decay.h"
 #include "fftconv_delta_dev.h"
@@ -404,7 +404,9 @@ hipError_t any(int io, LayerNormParams p, bool back, hipStream_t s) {
 }  // namespace
 
 // Workgroups of the backward pass: they keep their sums to the end, so about as many as
-// run at once (three on each of the 256 CUs at three pieces a lane).
+// run at once (at two pieces a lane, three of 256 threads on each of the 256 CUs).  With few
+// wide rows their sums are more than the rows: of 1000 x 8192 in bf16, 49 MB in and out,
+// they are 50 MB, written and read (45 us in all).
 int layernorm_bwd_blocks(long long rows, int D) {
     const int lpr = lanes_of(D, true), groups = lpr > 256 ? 1 : 256 / lpr;
     const long long n = (rows + groups - 1) / groups;
