@@ -12,9 +12,10 @@
 //
 // Each element moves once in and once out (backward twice in) with some ten operations:
 // HBM bounds both passes.  64 x 1024 rows of 768 in bf16, 201 MB, take 31 us and a call 38
-// (6.5 and 5.2 TB/s: part of so many bytes stays in the 256 MB of caches; a streaming copy of
-// 2 GB reaches 5.9), 16 x 8192 of 768 in f16 forward and backward, 1.0 GB, 198 us (5.1).  A lane of a row's group holds its pieces of eight elements from the load
-// to the store; the sums go by shuffles, of rows of more than 2048 through LDS.
+// (6.5 and 5.2 TB/s: part of so many bytes stays in the 256 MB of caches; a streaming copy
+// of 2 GB reaches 5.9), 16 x 8192 of 768 in f16 forward and backward, 1.0 GB, 198 us
+// (5.1).  A lane of a row's group holds its pieces of eight elements from the load to the
+// store; the sums go by shuffles, of rows of more than 2048 through LDS.
 #include "fftconv_decay.h"
 #include "fftconv_delta_dev.h"
 

@@ -606,8 +606,8 @@ typedef struct fftconv_decay_desc {
  * States, decays and sums are fp32 or wider whatever the I/O type; operands of the
  * 16-bit matrix products that are not of the I/O type (states, scores) are split into
  * three bf16 terms, 26 bits, or two f16 terms, 22 bits, with a scale for each column or
- * row; outputs are rounded to their type once.  Long sequences of few heads are cut into segments:
- * equal calls give equal bits.
+ * row; outputs are rounded to their type once.  Long sequences of few heads are cut into
+ * segments: equal calls give equal bits.
  *  A NaN or infinity reaches what it reaches in the formulas: from k or g its
  * token's outputs, the later ones of the sequence and the state (from k in its
  * row); from v the same in its column; from q its token's outputs.  They are not
